@@ -1,0 +1,129 @@
+/*
+ * mm_ops.h -- C ABI of the operators beside the fused MoE-FFN layer (mm.h), in the same library:
+ *
+ *   mm_residual_norm_*   the step between two blocks: the norm after a block, its gate, the scaled
+ *                        residual sum and the norm before the next block, forward and backward;
+ *   mm_router_*          top-k selection over expert logits, the routing weights and the loss
+ *                        statistics, forward and backward: what mm_forward takes as topk_ids and
+ *                        topk_weights;
+ *   mm_decode            the whole MoE layer for a few tokens (inference): router product,
+ *                        selection, experts and weighted sum in two launches, with bf16 expert
+ *                        weights or e4m3 ones that carry a scale per 128 x 128 block;
+ *   mm_quantize_blocks   bf16 weights to e4m3 and the scales of their blocks.
+ *
+ * The rules of mm.h hold here too: row-major contiguous device memory, every buffer (workspaces
+ * included) belongs to the caller, nothing is allocated, all work is enqueued on `stream` and
+ * nothing synchronises with the host. Host-side checks return an error before anything is
+ * enqueued; mm_last_error_detail and mm_status_string describe it. Host threads may call
+ * concurrently on different workspaces. Pointers are aligned to their element; 16-byte alignment
+ * where a function says so. Sums, statistics and products are held in 32 bits; every output is
+ * rounded once to its type. Results depend on the inputs and the device's SM count only.
+ */
+#ifndef MM_OPS_H_
+#define MM_OPS_H_
+
+#include "mm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum mm_dtype { MM_BF16 = 0, MM_FP32 = 1, MM_E4M3 = 2 } mm_dtype;
+
+/* Version of this header's functions and structs (mm_abi_version is mm.h's). */
+int mm_ops_version(void);
+
+/* ---- residual_norm ------------------------------------------------------------------------
+ *
+ *   p[t]  = f[t] * rsqrt(mean(f[t]^2) + eps) * post_weight       (p = f without a post weight)
+ *   r'[t] = residual_scale * r[t] + gate[t / (T / groups)] * p[t]         (gate = 1 without one)
+ *   n[t]  = r'[t] * rsqrt(mean(r'[t]^2) + eps) * pre_weight
+ *
+ * r (residual) and r' (residual_out) have the stream type, f (branch) and n (normed) the block
+ * type, the two weights and the gate the parameter type; a gradient has the type of what it is
+ * the gradient of. Type triples: stream bf16 or fp32, block no wider than the stream, parameters
+ * bf16 or fp32. A gate has `groups` rows of H, each for T / groups consecutive tokens (1: one
+ * gate per channel; T: one per token; 0: no gate).
+ * Sizes: T >= 0 (T = 0 does nothing forward and writes zero parameter gradients backward),
+ * 1 <= H <= 16384, T a multiple of groups. Rows whose length is a multiple of 16 bytes in every
+ * type, at 16-byte aligned addresses, move as 16-byte words; others element by element. */
+typedef struct mm_norm_desc {
+  int64_t T, H, groups;
+  int32_t stream_type, block_type, param_type; /* mm_dtype */
+  float residual_scale, eps;
+} mm_norm_desc;
+
+/* branch may be NULL (a norm before the first block: r' = residual_scale * r; no post weight or
+ * gate then). pre_weight and normed are both given or both NULL (after the last block: no norm
+ * before). residual_out may be NULL (r' not wanted) and may be `residual` itself. */
+mm_status mm_residual_norm_forward(const mm_norm_desc* d, const void* residual, const void* branch,
+                                   const void* post_weight, const void* pre_weight,
+                                   const void* gate, void* residual_out, void* normed,
+                                   void* stream);
+
+/* Bytes of workspace the backward needs (0: unsupported sizes). Needs no initialisation. */
+size_t mm_residual_norm_workspace_size(const mm_norm_desc* d);
+
+/* Gradients at the forward's residual_out (r', as stored) and branch, for the gradients of r' and
+ * n. Both norms' statistics are computed from these inputs. d_residual_out may be NULL (zero);
+ * d_normed is given exactly if pre_weight is. d_branch, d_post_weight, d_pre_weight and d_gate are
+ * given exactly if branch, post_weight, pre_weight and gate are. d_residual may be d_residual_out
+ * itself. The parameter gradients are sums over tokens in a fixed order. Workspace: 256-byte
+ * aligned. */
+mm_status mm_residual_norm_backward(const mm_norm_desc* d, const void* residual_out,
+                                    const void* branch, const void* post_weight,
+                                    const void* pre_weight, const void* gate,
+                                    const void* d_residual_out, const void* d_normed,
+                                    void* d_residual, void* d_branch, void* d_post_weight,
+                                    void* d_pre_weight, void* d_gate, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* ---- router -------------------------------------------------------------------------------
+ *
+ * Over logits z [T, E] (bf16 or fp32), per token:
+ *   key_e = z_e + bias_e (MM_SCORE_SOFTMAX), sigmoid(z_e) + bias_e (MM_SCORE_SIGMOID with a bias),
+ *           z_e (no bias); the K largest keys are selected, largest first, equal ones from the
+ *           lowest expert up. -0 equals 0; NaN ranks below -inf.
+ *   a_e   = exp(z_e - max z) or sigmoid(z_e);  A = sum_e a_e
+ *   weight of a selected expert j, without the bias:
+ *     normalize:   scale * a_j / sum of the selected a   (all 0 where that sum is 0: a token whose
+ *                  selected logits are all -inf)
+ *     otherwise:   scale * a_j / A (softmax; 0 where every logit is -inf) or scale * a_j (sigmoid)
+ *   prob_sum_e = sum_t a_te / A_t     (a row whose A is 0 adds nothing)
+ *   lse_t = log sum_e exp(z_te)       (-inf for a row of -inf)
+ * prob_sum and lse are the statistics of load-balancing and z losses; each may be NULL.
+ * topk_ids are distinct and in [0, E) for any input, so they are valid for mm_forward.
+ * Sizes: T >= 0, 1 <= E <= 1024, 1 <= K <= 16, K <= E. */
+#define MM_SCORE_SOFTMAX 0
+#define MM_SCORE_SIGMOID 1
+typedef struct mm_router_desc {
+  int64_t T;
+  int32_t E, K;
+  int32_t logits_type; /* MM_BF16 or MM_FP32 */
+  int32_t score;       /* MM_SCORE_* */
+  int32_t normalize;
+  float scale;
+} mm_router_desc;
+
+/* Bytes of workspace for a forward that writes prob_sum (0: unsupported sizes). */
+size_t mm_router_workspace_size(const mm_router_desc* d);
+
+/* bias fp32 [E] or NULL; topk_ids int32 [T, K], topk_weights fp32 [T, K]; prob_sum fp32 [E] or
+ * NULL (the workspace, 256-byte aligned, is needed only with it), lse fp32 [T] or NULL. */
+mm_status mm_router_forward(const mm_router_desc* d, const void* logits, const float* bias,
+                            int32_t* topk_ids, float* topk_weights, float* prob_sum, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* d_logits (the logits' type) from the gradients of topk_weights (fp32 [T, K]), prob_sum (fp32
+ * [E] or NULL) and lse (fp32 [T] or NULL). topk_ids are the forward's; an id outside [0, E)
+ * contributes nothing. The selection itself has no gradient. Masked (-inf) logits get a gradient
+ * of 0. */
+mm_status mm_router_backward(const mm_router_desc* d, const void* logits, const int32_t* topk_ids,
+                             const float* d_topk_weights, const float* d_prob_sum,
+                             const float* d_lse, void* d_logits, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MM_OPS_H_ */

@@ -13,6 +13,7 @@ import re
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmm.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mm.h")
+OPS_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mm_ops.h")
 
 MM_OK = 0
 MM_ERR_INVALID_ARG = 1
@@ -32,6 +33,11 @@ MM_FLAG_FORWARD_ONLY = 0x20
 MM_FLAG_SEPARATE_FORWARD_GEMMS = 0x40
 MM_FLAG_SINGLE_CTA_TILES = 0x100
 MM_NUM_STAGES = 17
+MM_BF16 = 0
+MM_FP32 = 1
+MM_E4M3 = 2
+MM_SCORE_SOFTMAX = 0
+MM_SCORE_SIGMOID = 1
 MM_TRACE_CTA = 0
 MM_TRACE_MAINLOOP = 1
 MM_TRACE_EPILOGUE = 2
@@ -64,6 +70,19 @@ class mm_shared_expert(ctypes.Structure):
 class mm_options(ctypes.Structure):
     _fields_ = [("shared", ctypes.POINTER(mm_shared_expert)),
                 ("tokens_per_expert", ctypes.c_void_p)]
+
+
+class mm_norm_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("stream_type", ctypes.c_int32), ("block_type", ctypes.c_int32),
+                ("param_type", ctypes.c_int32), ("residual_scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
+class mm_router_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("logits_type", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _P = ctypes.c_void_p
@@ -101,6 +120,14 @@ def _lib():
         "mm_stage_name": (ctypes.c_char_p, [ctypes.c_int]),
         "mm_route_noalloc": (st, [mm_dims, _P, _P, _P, _P, _P]),
         "mm_trace_set": (st, [_P, ctypes.c_size_t]),
+        # include/mm_ops.h (descriptors are passed by address)
+        "mm_ops_version": (ctypes.c_int, []),
+        "mm_residual_norm_forward": (st, [_P] * 9),
+        "mm_residual_norm_workspace_size": (ctypes.c_size_t, [_P]),
+        "mm_residual_norm_backward": (st, [_P] * 14 + [ctypes.c_size_t, _P]),
+        "mm_router_workspace_size": (ctypes.c_size_t, [_P]),
+        "mm_router_forward": (st, [_P] * 8 + [ctypes.c_size_t, _P]),
+        "mm_router_backward": (st, [_P] * 8),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -110,9 +137,9 @@ def _lib():
     return lib
 
 
-def header_symbols() -> list[str]:
-    """Function names declared in include/mm.h."""
-    text = open(HEADER_PATH).read()
+def header_symbols(path: str = HEADER_PATH) -> list[str]:
+    """Function names declared in include/mm.h (or in the header at `path`)."""
+    text = open(path).read()
     return sorted(set(re.findall(r"^[A-Za-z_][\w \*]*?\b(mm_\w+)\s*\(", text, re.M)))
 
 

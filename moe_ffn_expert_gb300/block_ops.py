@@ -1,0 +1,290 @@
+"""PyTorch entry points of the operators beside the fused MoE-FFN layer (include/mm_ops.h).
+
+Training and prompts:
+
+    n            = residual_norm(x, None, pre_weight=w)[1]      # the norm before a block
+    logits       = n @ router_weight.T                          # the router's product
+    ids, weights, prob_sum, lse = moe_router(logits, k, stats=True)
+    f            = hyper_mega_moe(n, ids, weights, up, down)    # torch_api
+    x, n         = residual_norm(x, f, post_weight=..., gate=..., pre_weight=...)
+
+`residual_norm` and `moe_router` are differentiable; the `*_forward` / `*_backward` functions are
+the calls they make. Argument marshalling only: shapes and types are checked, non-contiguous
+tensors are copied to contiguous ones, and everything else runs in libmm.so on the current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from functools import lru_cache
+
+import torch
+
+from . import _abi
+
+_TYPE = {torch.bfloat16: _abi.MM_BF16, torch.float32: _abi.MM_FP32}
+_SCORE = {"softmax": _abi.MM_SCORE_SOFTMAX, "sigmoid": _abi.MM_SCORE_SIGMOID}
+
+
+def _stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _contiguous(t):
+    return t if t is None or t.is_contiguous() else t.contiguous()
+
+
+def _type(name, t):
+    try:
+        return _TYPE[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {t.dtype}") from None
+
+
+def _on_gpu(op, first, *others):
+    if not first.is_cuda:
+        raise ValueError(f"{op} runs on a CUDA device only (no CPU path)")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{op}: all tensors must be on {first.device}")
+
+
+# ------------------------------------------------------------------------------- residual_norm
+
+@lru_cache(maxsize=256)
+def _norm_plan(T, H, groups, stream, block, param, scale, eps):
+    """(descriptor, its address, backward workspace bytes) of one problem."""
+    d = _abi.mm_norm_desc(T, H, groups, stream, block, param, scale, eps)
+    return d, ctypes.addressof(d), int(_abi._lib().mm_residual_norm_workspace_size(ctypes.byref(d)))
+
+
+def _norm_inputs(residual, branch, post_weight, pre_weight, gate, residual_scale, eps):
+    _on_gpu("residual_norm", residual, branch, post_weight, pre_weight, gate)
+    if residual.dim() != 2:
+        raise ValueError("expected residual[T,H]")
+    T, H = residual.shape
+    if branch is None:
+        if post_weight is not None or gate is not None:
+            raise ValueError("post_weight and gate belong to a branch")
+    elif branch.shape != residual.shape:
+        raise ValueError("expected branch[T,H] of residual's shape")
+    params = [t for t in (post_weight, pre_weight, gate) if t is not None]
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None and t.shape != (H,):
+            raise ValueError(f"expected {name}[H]")
+    groups = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.unsqueeze(0)
+        if gate.dim() != 2 or gate.shape[1] != H or gate.shape[0] < 1 or T % gate.shape[0]:
+            raise ValueError("expected gate[H] or gate[G,H] with T a multiple of G")
+        groups = gate.shape[0]
+    if any(p.dtype != params[0].dtype for p in params):
+        raise TypeError("post_weight, pre_weight and gate must have one dtype")
+    stream = _type("residual", residual)
+    block = _type("branch", branch) if branch is not None else stream
+    if block > stream:
+        raise TypeError("a bfloat16 residual needs a bfloat16 branch")
+    param = _type("parameters", params[0]) if params else stream
+    plan = _norm_plan(T, H, groups, stream, block, param, float(residual_scale), float(eps))
+    return plan, gate
+
+
+def residual_norm_forward(residual, branch=None, *, post_weight=None, pre_weight=None, gate=None,
+                          residual_scale=1.0, eps=1e-6, normed_dtype=None):
+    """(residual_out, normed): r' = residual_scale * r + gate * rmsnorm(branch, post_weight) and
+    rmsnorm(r', pre_weight) (None without a pre_weight). `gate` is [H] (per channel) or [G, H],
+    row g for the g-th T / G tokens. normed has the branch's type; without a branch
+    `normed_dtype` (the residual's if None)."""
+    plan, gate = _norm_inputs(residual, branch, post_weight, pre_weight, gate, residual_scale, eps)
+    ndt = residual.dtype if branch is None else branch.dtype
+    if branch is None and normed_dtype is not None and normed_dtype != ndt:
+        d = plan[0]
+        if _TYPE.get(normed_dtype, 2) > d.stream_type:
+            raise TypeError("normed_dtype must be no wider than the residual")
+        ndt = normed_dtype
+        plan = _norm_plan(d.T, d.H, d.groups, d.stream_type, _TYPE[ndt], d.param_type,
+                          float(residual_scale), float(eps))
+    residual, branch, gate = _contiguous(residual), _contiguous(branch), _contiguous(gate)
+    post_weight, pre_weight = _contiguous(post_weight), _contiguous(pre_weight)
+    out = torch.empty_like(residual)
+    normed = torch.empty(residual.shape, dtype=ndt, device=residual.device) \
+        if pre_weight is not None else None
+    _abi.check(_abi._lib().mm_residual_norm_forward(
+        plan[1], residual.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(pre_weight), _ptr(gate),
+        out.data_ptr(), _ptr(normed), _stream(residual)), "mm_residual_norm_forward")
+    return out, normed
+
+
+def residual_norm_backward(residual_out, branch, d_residual_out, d_normed, *, post_weight=None,
+                           pre_weight=None, gate=None, residual_scale=1.0, eps=1e-6):
+    """(d_residual, d_branch, d_post_weight, d_pre_weight, d_gate) at the forward's residual_out
+    and branch; None in the place of what was not given. d_residual_out may be None (zero);
+    d_normed is given exactly if pre_weight is."""
+    plan, g2 = _norm_inputs(residual_out, branch, post_weight, pre_weight, gate, residual_scale, eps)
+    if (d_normed is None) != (pre_weight is None):
+        raise ValueError("give d_normed exactly if pre_weight is given")
+    if d_residual_out is None and d_normed is None:
+        raise ValueError("give d_residual_out or d_normed")
+    d = plan[0]
+    if d_residual_out is not None and (d_residual_out.shape != residual_out.shape
+                                       or d_residual_out.dtype != residual_out.dtype):
+        raise ValueError("d_residual_out must have residual_out's shape and dtype")
+    if d_normed is not None:
+        if d_normed.shape != residual_out.shape:
+            raise ValueError("d_normed must have residual_out's shape")
+        block = _type("d_normed", d_normed)
+        if branch is None and block < d.stream_type:
+            plan = _norm_plan(d.T, d.H, d.groups, d.stream_type, block, d.param_type,
+                              float(residual_scale), float(eps))
+        elif block != d.block_type:
+            raise TypeError("d_normed must have the branch's dtype")
+    _on_gpu("residual_norm", residual_out, d_residual_out, d_normed)
+    residual_out, branch, g2 = _contiguous(residual_out), _contiguous(branch), _contiguous(g2)
+    d_residual_out, d_normed = _contiguous(d_residual_out), _contiguous(d_normed)
+    post_weight, pre_weight = _contiguous(post_weight), _contiguous(pre_weight)
+    like = torch.empty_like
+    dr = like(residual_out)
+    df = None if branch is None else like(branch)
+    dpost = None if post_weight is None else like(post_weight)
+    dpre = None if pre_weight is None else like(pre_weight)
+    dg = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    ws = torch.empty(plan[2], dtype=torch.uint8, device=residual_out.device)
+    _abi.check(_abi._lib().mm_residual_norm_backward(
+        plan[1], residual_out.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(pre_weight),
+        _ptr(g2), _ptr(d_residual_out), _ptr(d_normed), dr.data_ptr(), _ptr(df), _ptr(dpost),
+        _ptr(dpre), _ptr(dg), ws.data_ptr(), plan[2], _stream(residual_out)),
+        "mm_residual_norm_backward")
+    return dr, df, dpost, dpre, dg
+
+
+class ResidualNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, residual, branch, post_weight, pre_weight, gate, residual_scale, eps, ndt):
+        out, normed = residual_norm_forward(
+            residual, branch, post_weight=post_weight, pre_weight=pre_weight, gate=gate,
+            residual_scale=residual_scale, eps=eps, normed_dtype=ndt)
+        ctx.save_for_backward(out, branch, post_weight, pre_weight, gate)
+        ctx.scale, ctx.eps = residual_scale, eps
+        ctx.set_materialize_grads(False)
+        ctx.ndt = None if normed is None else normed.dtype
+        return out, normed
+
+    @staticmethod
+    def backward(ctx, d_out, d_normed):
+        out, branch, post_weight, pre_weight, gate = ctx.saved_tensors
+        if pre_weight is not None and d_normed is None:  # the normed output was not used
+            d_normed = torch.zeros(out.shape, dtype=ctx.ndt, device=out.device)
+        if d_out is None and d_normed is None:
+            return (None,) * 8
+        dr, df, dpost, dpre, dg = residual_norm_backward(
+            out, branch, d_out, d_normed, post_weight=post_weight, pre_weight=pre_weight,
+            gate=gate, residual_scale=ctx.scale, eps=ctx.eps)
+        return dr, df, dpost, dpre, dg, None, None, None
+
+
+def residual_norm(residual, branch=None, *, post_weight=None, pre_weight=None, gate=None,
+                  residual_scale=1.0, eps=1e-6, normed_dtype=None):
+    """residual_norm_forward with gradients for residual, branch, both weights and the gate."""
+    return ResidualNormFunction.apply(residual, branch, post_weight, pre_weight, gate,
+                                      residual_scale, eps, normed_dtype)
+
+
+# ------------------------------------------------------------------------------- router
+
+@lru_cache(maxsize=256)
+def _router_plan(T, E, K, logits_type, score, normalize, scale):
+    d = _abi.mm_router_desc(T, E, K, logits_type, _SCORE[score], int(normalize), scale)
+    return d, ctypes.addressof(d), int(_abi._lib().mm_router_workspace_size(ctypes.byref(d)))
+
+
+def _router_inputs(logits, k, score, normalize, scale):
+    if not logits.is_cuda:
+        raise ValueError("the router runs on a CUDA device only (no CPU path)")
+    if logits.dim() != 2:
+        raise ValueError("expected logits[T,E]")
+    if score not in _SCORE:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    T, E = logits.shape
+    if not 1 <= k <= E:
+        raise ValueError("expected 1 <= k <= E")
+    return _router_plan(T, E, int(k), _type("logits", logits), score, bool(normalize), float(scale))
+
+
+def router_forward(logits, k, *, bias=None, score="softmax", normalize=True, scale=1.0,
+                   stats=False):
+    """(topk_ids int32 [T,k], topk_weights fp32 [T,k], prob_sum fp32 [E], lse fp32 [T]); the last
+    two are None without `stats`. See mm_ops.h for the definitions. `bias` fp32 [E] takes part in
+    the selection only."""
+    plan = _router_inputs(logits, k, score, normalize, scale)
+    T, E = logits.shape
+    if bias is not None:
+        if bias.shape != (E,) or bias.dtype != torch.float32 or bias.device != logits.device:
+            raise ValueError("expected bias[E] in float32 on the logits' device")
+        bias = _contiguous(bias)
+    logits = _contiguous(logits)
+    dev = logits.device
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    prob_sum = lse = ws = None
+    if stats:
+        prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        ws = torch.empty(plan[2], dtype=torch.uint8, device=dev)
+    _abi.check(_abi._lib().mm_router_forward(
+        plan[1], logits.data_ptr(), _ptr(bias), ids.data_ptr(), weights.data_ptr(), _ptr(prob_sum),
+        _ptr(lse), _ptr(ws), plan[2] if stats else 0, _stream(logits)), "mm_router_forward")
+    return ids, weights, prob_sum, lse
+
+
+def router_backward(logits, topk_ids, d_weights, d_prob_sum=None, d_lse=None, *, score="softmax",
+                    normalize=True, scale=1.0):
+    """d_logits (the logits' type) from the gradients of topk_weights, prob_sum and lse."""
+    if topk_ids.dim() != 2 or topk_ids.dtype != torch.int32:
+        raise ValueError("expected topk_ids[T,k] in int32")
+    plan = _router_inputs(logits, topk_ids.shape[1], score, normalize, scale)
+    T, E = logits.shape
+    _on_gpu("the router", logits, topk_ids, d_weights, d_prob_sum, d_lse)
+    for name, t, shape in (("topk_ids", topk_ids, (T, topk_ids.shape[1])),
+                           ("d_weights", d_weights, tuple(topk_ids.shape)),
+                           ("d_prob_sum", d_prob_sum, (E,)), ("d_lse", d_lse, (T,))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"expected {name} of shape {shape}")
+        if t is not None and t is not topk_ids and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32")
+    logits, topk_ids, d_weights = _contiguous(logits), _contiguous(topk_ids), _contiguous(d_weights)
+    d_prob_sum, d_lse = _contiguous(d_prob_sum), _contiguous(d_lse)
+    dz = torch.empty_like(logits)
+    _abi.check(_abi._lib().mm_router_backward(
+        plan[1], logits.data_ptr(), topk_ids.data_ptr(), d_weights.data_ptr(), _ptr(d_prob_sum),
+        _ptr(d_lse), dz.data_ptr(), _stream(logits)), "mm_router_backward")
+    return dz
+
+
+class RouterFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, bias, score, normalize, scale, stats):
+        ids, weights, prob_sum, lse = router_forward(
+            logits, k, bias=bias, score=score, normalize=normalize, scale=scale, stats=stats)
+        ctx.save_for_backward(logits, ids)
+        ctx.how = dict(score=score, normalize=normalize, scale=scale)
+        ctx.mark_non_differentiable(ids)
+        ctx.set_materialize_grads(False)
+        return ids, weights, prob_sum, lse
+
+    @staticmethod
+    def backward(ctx, _, d_weights, d_prob_sum, d_lse):
+        logits, ids = ctx.saved_tensors
+        if d_weights is None and d_prob_sum is None and d_lse is None:
+            return (None,) * 7
+        if d_weights is None:
+            d_weights = torch.zeros(ids.shape, dtype=torch.float32, device=ids.device)
+        return (router_backward(logits, ids, d_weights, d_prob_sum, d_lse, **ctx.how),) + (None,) * 6
+
+
+def moe_router(logits, k, *, bias=None, score="softmax", normalize=True, scale=1.0, stats=False):
+    """router_forward with a gradient for the logits (through topk_weights, prob_sum and lse)."""
+    return RouterFunction.apply(logits, k, bias, score, normalize, scale, stats)

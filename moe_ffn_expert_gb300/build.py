@@ -15,8 +15,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmm.so")
-SOURCES = ["mm_api.cu", "mm_route.cu", "mm_gemm.cu", "mm_route_static.cu"]
-HEADERS = ["mm_device.cuh", "mm_layout.h", "mm_kernels.h"]
+SOURCES = ["mm_api.cu", "mm_route.cu", "mm_gemm.cu", "mm_route_static.cu", "mm_norm.cu",
+           "mm_router.cu"]
+HEADERS = ["mm_device.cuh", "mm_layout.h", "mm_kernels.h", "mm_rows.cuh", "mm_select.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,7 +34,7 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "mm.h"))
+    files += [os.path.join(ROOT, "include", h) for h in ("mm.h", "mm_ops.h")]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -115,22 +115,6 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 // Text of the last CUDA failure seen by a call of this thread (see mm_last_error_detail).
 thread_local char g_err[256] = "";
 
-mm_status cuda_fail(cudaError_t e, const char* what) {
-  // the previous detail (a note from a lower layer) is kept after this one, shortened to fit
-  char inner[160];
-  memcpy(inner, g_err, sizeof(inner) - 1);
-  inner[sizeof(inner) - 1] = 0;
-  snprintf(g_err, sizeof(g_err), "%.80s: %.60s (%.40s)%s%.60s", what, cudaGetErrorString(e),
-           cudaGetErrorName(e), inner[0] ? "; " : "", inner);
-  return MM_ERR_CUDA;
-}
-
-#define MM_TRY(expr)                                    \
-  do {                                                  \
-    cudaError_t _e = (expr);                            \
-    if (_e != cudaSuccess) return cuda_fail(_e, #expr); \
-  } while (0)
-
 // A second stream per device and host thread, for work that may overlap the caller's stream
 // inside one call, with the two events that fork it from and join it back to the caller's
 // stream. Created once per device and thread (non-blocking, highest priority, so its small grids
@@ -161,17 +145,26 @@ cudaError_t side_stream(SideStream** out) {
   return cudaSuccess;
 }
 
-// Makes the current device's primary context current on this thread. Tensor-map encoding is a
-// driver call that needs one, and a thread that has not launched anything yet (an autograd
-// worker thread, say) may not have it bound.
+}  // namespace
+
+mm_status cuda_fail(cudaError_t e, const char* what) {
+  // the previous detail (a note from a lower layer) is kept after this one, shortened to fit
+  char inner[160];
+  memcpy(inner, g_err, sizeof(inner) - 1);
+  inner[sizeof(inner) - 1] = 0;
+  snprintf(g_err, sizeof(g_err), "%.80s: %.60s (%.40s)%s%.60s", what, cudaGetErrorString(e),
+           cudaGetErrorName(e), inner[0] ? "; " : "", inner);
+  return MM_ERR_CUDA;
+}
+
+void clear_error() { g_err[0] = 0; }
+
 cudaError_t bind_context() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   return cudaSetDevice(dev);
 }
-
-}  // namespace
 
 TraceCtx trace_ctx() { return t_trace_cur; }
 static_assert(sizeof(mm_trace_record) == 32 && offsetof(mm_trace_record, unit) == 8 &&
@@ -335,7 +328,7 @@ static mm_status forward_empty(const Plan& p, const mm_shared_expert* se, const 
     return MM_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = reinterpret_cast<char*>(workspace);
-  g_err[0] = 0;
+  clear_error();
   MM_TRY(bind_context());
   MM_TRY(cudaMemsetAsync(ws + w.off_hdr, 0, HDR_WORDS * sizeof(int32_t), st));
   if (flags & MM_FLAG_FORWARD_ONLY)
@@ -369,7 +362,7 @@ static mm_status backward_empty(const Plan& p, const mm_shared_expert* se,
              !aligned(se->d_down_proj_weight, 16)))
     return MM_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  g_err[0] = 0;
+  clear_error();
   MM_TRY(bind_context());
   MM_TRY(launch_backward_check(w, reinterpret_cast<char*>(workspace), st));
   if (flags & MM_FLAG_ACCUMULATE_WEIGHT_GRADS) return MM_OK;  // adding zero changes nothing
@@ -408,7 +401,7 @@ static mm_status forward_impl(mm_dims d, const mm_shared_expert* se, const int32
     return MM_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = reinterpret_cast<char*>(workspace);
-  g_err[0] = 0;
+  clear_error();
   MM_TRY(bind_context());
 
   MM_TRY(cudaMemsetAsync(ws + w.off_hdr, 0, HDR_WORDS * sizeof(int32_t), st));
@@ -507,7 +500,7 @@ static mm_status backward_impl(mm_dims d, const mm_shared_expert* se, const void
     return MM_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = reinterpret_cast<char*>(workspace);
-  g_err[0] = 0;
+  clear_error();
   MM_TRY(bind_context());
 
   MM_TRY(timed(ST_GATHER_DY, st,

@@ -97,6 +97,35 @@ struct GemmCall {
 
 cudaError_t launch_gemm(const Workspace& w, char* ws, const GemmCall& c, cudaStream_t st);
 
+// MM_ERR_CUDA, with the failing step and the error kept for mm_last_error_detail (this thread).
+mm_status cuda_fail(cudaError_t e, const char* what);
+// Empties this thread's mm_last_error_detail (at the start of a call that may fail).
+void clear_error();
+
+#define MM_TRY(expr)                                            \
+  do {                                                          \
+    cudaError_t _e = (expr);                                    \
+    if (_e != cudaSuccess) return ::mm::cuda_fail(_e, #expr);   \
+  } while (0)
+
+// Makes the current device's primary context current on this thread. Tensor-map encoding is a
+// driver call that needs one, and a thread that has not launched anything yet (an autograd
+// worker thread, say) may not have it bound.
+cudaError_t bind_context();
+
+// ---- column sums of fp32 partial slices, in a fixed order (mm_router.cu)
+//   dst[y][c] = sum over p < parts of src[y][p][c], for each job; type: MM_BF16 or MM_FP32 outputs.
+struct SumJob {
+  const float* src;
+  void* dst;
+  int64_t parts, first;  // first: the output rows of the jobs before this one
+};
+struct SumArgs {
+  SumJob job[3];
+  int jobs, cols, type;
+};
+cudaError_t launch_column_sums(const SumArgs& a, int64_t rows, cudaStream_t st);
+
 // Records a description of a host-side failure for mm_last_error_detail (this thread).
 void note_error(const char* fmt, ...);
 

@@ -1,0 +1,385 @@
+// Router: top-k selection over expert logits, its weights and loss statistics, and its gradient
+// (definitions in mm_ops.h). One warp per token, E / 32 logits per lane in registers.
+//
+// In terms of logits the gradient is, with p = a / A, w^ the normalised weights of the selected
+// experts, c = scale and the upstream gradients dw, dP (prob_sum) and dL (lse):
+//   normalize, softmax:  dz_j += c w^_j (dw_j - sum_i dw_i w^_i)            j selected
+//   normalize, sigmoid:  the same times (1 - sigmoid z_j)
+//   softmax:             dz_j += c dw_j p_j,  dz_e -= p_e sum_j c dw_j p_j
+//   sigmoid:             dz_j += c dw_j a_j (1 - a_j)
+//   prob_sum:            dz_e += p_e (dP_e - sum_i dP_i p_i)   [sigmoid: times (1 - a_e)]
+//   lse:                 dz_e += dL exp(z_e - lse)
+//
+// A row is a few hundred bytes: the kernels are bound by launch and row latency at serving sizes,
+// and by the K rounds of the selection over many rows.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "mm_kernels.h"
+#include "mm_select.cuh"
+
+namespace mm {
+namespace {
+
+constexpr int kWarps = 8;  // rows in flight per block
+
+struct RouterArgs {
+  int64_t T;
+  int E, K, score, normalize;
+  float scale;
+  const void* logits;
+  const float* bias;
+  int32_t* ids;
+  float *weights, *lse, *prob_part;  // prob_part: [gridDim.x][E] partial sums or null
+  // backward
+  const int32_t* ids_in;
+  const float *dw, *dP, *dL;
+  void* dz;
+};
+
+__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+__device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
+
+template <int NV>
+__device__ __forceinline__ float row_max(const float (&z)[NV], int E, int lane) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (lane + 32 * j < E) m = fmaxf(m, z[j]);
+  m = warp_max(m);
+  return m == -INFINITY ? 0.f : m;  // a row of -inf: exp(z) is 0 without a shift
+}
+
+template <typename LT, int NV>
+__global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
+  __shared__ float part[kWarps][32];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, K = a.K;
+  const bool all = a.prob_part != nullptr || (a.score == MM_SCORE_SOFTMAX && !a.normalize);
+  float acc[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) acc[j] = 0.f;
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+    const LT* row = static_cast<const LT*>(a.logits) + t * E;
+    float z[NV];
+    uint32_t key[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = lane + 32 * j;
+      z[j] = e < E ? load_logit(row + e) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = lane + 32 * j;
+      key[j] = 0;
+      if (e >= E) continue;
+      float k = z[j];
+      if (a.bias != nullptr)
+        k = (a.score == MM_SCORE_SIGMOID ? sigmoid_accurate(k) : k) + a.bias[e];
+      key[j] = order_key(k);
+    }
+    float m = 0.f, A = 0.f;
+    if (all || a.lse != nullptr) m = row_max<NV>(z, E, lane);
+    if (all) {
+      float x[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        x[j] = lane + 32 * j >= E ? 0.f
+               : a.score == MM_SCORE_SIGMOID ? sigmoid_accurate(z[j]) : expf(z[j] - m);
+        A += x[j];
+      }
+      A = warp_sum(A);
+      if (a.prob_part != nullptr) {
+        const float inv = A == 0.f ? 0.f : 1.f / A;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) acc[j] += x[j] * inv;
+      }
+    }
+    if (a.lse != nullptr) {
+      float s = A;
+      if (!all || a.score == MM_SCORE_SIGMOID) {
+        s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (lane + 32 * j < E) s += expf(z[j] - m);
+        s = warp_sum(s);
+      }
+      if (lane == 0) a.lse[t] = m + logf(s);
+    }
+    const int id = select_topk<NV>(key, K, lane);
+    const float zs = lane < K ? load_logit(row + id) : 0.f;
+    const float w = selected_weight(zs, lane < K, a.score, a.normalize, a.scale, m, A);
+    if (lane < K) {
+      a.ids[t * K + lane] = id;
+      a.weights[t * K + lane] = w;
+    }
+  }
+  if (a.prob_part == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {  // the block's warps, in order
+    part[warp][lane] = acc[j];
+    __syncthreads();
+    if (warp == 0 && lane + 32 * j < E) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) s += part[i][lane];
+      a.prob_part[(int64_t)blockIdx.x * E + lane + 32 * j] = s;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename LT, int NV>
+__global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E, K = a.K;
+  const bool soft = a.score == MM_SCORE_SOFTMAX;
+  const bool all = a.dP != nullptr || (soft && !a.normalize);
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+    const LT* row = static_cast<const LT*>(a.logits) + t * E;
+    float z[NV], dz[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = lane + 32 * j;
+      z[j] = e < E ? load_logit(row + e) : 0.f;
+      dz[j] = 0.f;
+    }
+    const int id_in = lane < K ? a.ids_in[t * K + lane] : -1;
+    const bool has = id_in >= 0 && id_in < E;
+    const float dw = has ? a.scale * a.dw[t * K + lane] : 0.f;
+    const float zs = has ? load_logit(row + id_in) : 0.f;
+    float m = 0.f, A = 0.f, inv = 0.f;
+    if (all || a.dL != nullptr) m = row_max<NV>(z, E, lane);
+    float p[NV];
+    if (all) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        p[j] = lane + 32 * j >= E ? 0.f : soft ? expf(z[j] - m) : sigmoid_accurate(z[j]);
+        A += p[j];
+      }
+      A = warp_sum(A);
+      inv = A == 0.f ? 0.f : 1.f / A;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) p[j] *= inv;
+    }
+    // through the weights: `add` goes to the lane's selected expert, `common` p_e to every one
+    float add, common = 0.f;
+    if (a.normalize) {
+      const float w = selected_weight(zs, has, a.score, 1, 1.f, 0.f, 0.f);
+      add = w * (dw - warp_sum(dw * w));
+      if (!soft) add *= sigmoid_accurate(-zs);
+    } else if (soft) {
+      add = has ? dw * expf(zs - m) * inv : 0.f;
+      common -= warp_sum(add);
+    } else {
+      add = dw * sigmoid_accurate(zs) * sigmoid_accurate(-zs);
+    }
+    if (!has) add = 0.f;
+    if (all) {
+      float dot = 0.f, g[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        g[j] = a.dP != nullptr && lane + 32 * j < E ? a.dP[lane + 32 * j] : 0.f;
+        dot += g[j] * p[j];
+      }
+      dot = warp_sum(dot);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const float to_prob = p[j] * (g[j] - dot);
+        dz[j] = (soft ? to_prob : to_prob * sigmoid_accurate(-z[j])) + common * p[j];
+      }
+    }
+    if (a.dL != nullptr) {
+      float x[NV], s = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        x[j] = lane + 32 * j < E ? expf(z[j] - m) : 0.f;
+        s += x[j];
+      }
+      s = warp_sum(s);
+      const float f = s == 0.f ? 0.f : a.dL[t] / s;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) dz[j] += f * x[j];
+    }
+    for (int k = 0; k < K; ++k) {
+      const int e = __shfl_sync(0xFFFFFFFFu, has ? id_in : -1, k);
+      const float v = __shfl_sync(0xFFFFFFFFu, add, k);
+      if (e >= 0 && (e & 31) == lane) {
+        const int j0 = e >> 5;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (j == j0) dz[j] += v;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (lane + 32 * j < E) store_logit(static_cast<LT*>(a.dz) + t * E + lane + 32 * j, dz[j]);
+  }
+}
+
+// 32 columns per block, the parts dealt to 32 warps and added in a fixed order.
+__global__ void __launch_bounds__(1024) k_column_sums(SumArgs a) {
+  __shared__ float part[32][33];
+  pdl_wait();
+  int k = 0;
+#pragma unroll
+  for (int i = 1; i < 3; ++i)
+    if (i < a.jobs && (int64_t)blockIdx.y >= a.job[i].first) k = i;
+  const SumJob job = a.job[k];
+  const int64_t y = (int64_t)blockIdx.y - job.first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < a.cols)
+#pragma unroll 4
+    for (int64_t p = warp; p < job.parts; p += 32) s += job.src[(y * job.parts + p) * a.cols + c];
+  part[warp][lane] = s;
+  __syncthreads();
+  s = warp_sum(part[lane][warp]);  // column `warp` of this block
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < a.cols) {
+    const float v[1] = {s};
+    store_any<1>(job.dst, a.type, y * a.cols + col, v);
+  }
+}
+
+inline bool aligned_to(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+
+mm_status check_desc(const mm_router_desc* d) {
+  if (d == nullptr || d->T < 0 || d->E < 1 || d->K < 1 || d->K > d->E) return MM_ERR_INVALID_ARG;
+  if (d->logits_type != MM_BF16 && d->logits_type != MM_FP32) return MM_ERR_INVALID_ARG;
+  if (d->score != MM_SCORE_SOFTMAX && d->score != MM_SCORE_SIGMOID) return MM_ERR_INVALID_ARG;
+  if (d->E > 1024 || d->K > 16 || d->T >= ((int64_t)1 << 40)) return MM_ERR_UNSUPPORTED;
+  return MM_OK;
+}
+
+int64_t router_blocks(const mm_router_desc& d) {
+  return std::min<int64_t>((d.T + kWarps - 1) / kWarps, (int64_t)std::max(1, device_sm_count()) * 4);
+}
+
+RouterArgs router_args(const mm_router_desc& d) {
+  RouterArgs a{};
+  a.T = d.T;
+  a.E = d.E;
+  a.K = d.K;
+  a.score = d.score;
+  a.normalize = d.normalize;
+  a.scale = d.scale;
+  return a;
+}
+
+// Calls f with the number of logits per lane as a compile-time constant.
+template <typename F>
+cudaError_t for_width(int E, F&& f) {
+  if (E <= 32) return f(std::integral_constant<int, 1>());
+  if (E <= 64) return f(std::integral_constant<int, 2>());
+  if (E <= 128) return f(std::integral_constant<int, 4>());
+  if (E <= 256) return f(std::integral_constant<int, 8>());
+  if (E <= 512) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
+}
+
+}  // namespace
+
+cudaError_t launch_column_sums(const SumArgs& a, int64_t rows, cudaStream_t st) {
+  return launch_pdl(k_column_sums, dim3((unsigned)((a.cols + 31) / 32), (unsigned)rows),
+                    dim3(1024), 0, st, a);
+}
+
+}  // namespace mm
+
+using namespace mm;
+
+extern "C" {
+
+size_t mm_router_workspace_size(const mm_router_desc* d) {
+  if (check_desc(d) != MM_OK) return 0;
+  return std::max<size_t>(256, (size_t)router_blocks(*d) * d->E * sizeof(float));
+}
+
+mm_status mm_router_forward(const mm_router_desc* d, const void* logits, const float* bias,
+                            int32_t* topk_ids, float* topk_weights, float* prob_sum, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  mm_status s = check_desc(d);
+  if (s != MM_OK) return s;
+  if (!aligned_to(bias, 4) || !aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4) ||
+      !aligned_to(prob_sum, 4) || !aligned_to(lse, 4) ||
+      !aligned_to(logits, d->logits_type == MM_BF16 ? 2 : 4))
+    return MM_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (d->T == 0) {
+    clear_error();
+    if (prob_sum) MM_TRY(cudaMemsetAsync(prob_sum, 0, d->E * sizeof(float), st));
+    return MM_OK;
+  }
+  if (!logits || !topk_ids || !topk_weights) return MM_ERR_INVALID_ARG;
+  const int64_t blocks = router_blocks(*d);
+  if (prob_sum && (workspace == nullptr || !aligned_to(workspace, 256) ||
+                   workspace_bytes < (size_t)blocks * d->E * sizeof(float)))
+    return MM_ERR_WORKSPACE;
+  clear_error();
+  RouterArgs a = router_args(*d);
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.lse = lse;
+  a.prob_part = prob_sum ? static_cast<float*>(workspace) : nullptr;
+  MM_TRY(for_width(d->E, [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    return d->logits_type == MM_BF16
+               ? launch_pdl(k_router_fwd<__nv_bfloat16, NV>, dim3((unsigned)blocks),
+                            dim3(32 * kWarps), 0, st, a)
+               : launch_pdl(k_router_fwd<float, NV>, dim3((unsigned)blocks), dim3(32 * kWarps), 0,
+                            st, a);
+  }));
+  if (prob_sum) {
+    SumArgs sa{};
+    sa.cols = d->E;
+    sa.type = MM_FP32;
+    sa.jobs = 1;
+    sa.job[0] = SumJob{a.prob_part, prob_sum, blocks, 0};
+    MM_TRY(launch_column_sums(sa, 1, st));
+  }
+  return MM_OK;
+}
+
+mm_status mm_router_backward(const mm_router_desc* d, const void* logits, const int32_t* topk_ids,
+                             const float* d_topk_weights, const float* d_prob_sum,
+                             const float* d_lse, void* d_logits, void* stream) {
+  mm_status s = check_desc(d);
+  if (s != MM_OK) return s;
+  const size_t es = d->logits_type == MM_BF16 ? 2 : 4;
+  if (!aligned_to(logits, es) || !aligned_to(d_logits, es) || !aligned_to(topk_ids, 4) ||
+      !aligned_to(d_topk_weights, 4) || !aligned_to(d_prob_sum, 4) || !aligned_to(d_lse, 4))
+    return MM_ERR_INVALID_ARG;
+  if (d->T == 0) return MM_OK;
+  if (!logits || !topk_ids || !d_topk_weights || !d_logits) return MM_ERR_INVALID_ARG;
+  clear_error();
+  RouterArgs a = router_args(*d);
+  a.logits = logits;
+  a.ids_in = topk_ids;
+  a.dw = d_topk_weights;
+  a.dP = d_prob_sum;
+  a.dL = d_lse;
+  a.dz = d_logits;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t blocks = router_blocks(*d);
+  MM_TRY(for_width(d->E, [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    return d->logits_type == MM_BF16
+               ? launch_pdl(k_router_bwd<__nv_bfloat16, NV>, dim3((unsigned)blocks),
+                            dim3(32 * kWarps), 0, st, a)
+               : launch_pdl(k_router_bwd<float, NV>, dim3((unsigned)blocks), dim3(32 * kWarps), 0,
+                            st, a);
+  }));
+  return MM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,81 @@
+// Device helpers of the row-wise operators (residual_norm, router): typed loads and stores of
+// W consecutive elements as 32-bit floats, and sums over a block.
+#pragma once
+
+#include "mm_device.cuh"
+
+namespace mm {
+
+// W consecutive elements at p as floats. W = 8: p is 16-byte aligned.
+template <int W>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[W]) {
+  if constexpr (W == 8) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(u[i]);
+      v[2 * i + 1] = bf16_hi(u[i]);
+    }
+  } else {
+    static_assert(W == 1, "widths 8 and 1");
+    v[0] = __bfloat162float(p[0]);
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[W]) {
+  if constexpr (W == 8) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0];
+    const float4 b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    static_assert(W == 1, "widths 8 and 1");
+    v[0] = p[0];
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[W]) {
+  if constexpr (W == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  else
+    p[0] = __float2bfloat16_rn(v[0]);
+}
+
+template <int W>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[W]) {
+  if constexpr (W == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    p[0] = v[0];
+  }
+}
+
+// The same for a type known at run time (MM_BF16 or MM_FP32); element offset `at`.
+template <int W>
+__device__ __forceinline__ void load_any(const void* p, int type, int64_t at, float (&v)[W]) {
+  if (type == MM_BF16)
+    load_vec<W>(static_cast<const __nv_bfloat16*>(p) + at, v);
+  else
+    load_vec<W>(static_cast<const float*>(p) + at, v);
+}
+
+template <int W>
+__device__ __forceinline__ void store_any(void* p, int type, int64_t at, const float (&v)[W]) {
+  if (type == MM_BF16)
+    store_vec<W>(static_cast<__nv_bfloat16*>(p) + at, v);
+  else
+    store_vec<W>(static_cast<float*>(p) + at, v);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+}  // namespace mm
