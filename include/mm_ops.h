@@ -122,6 +122,57 @@ mm_status mm_router_backward(const mm_router_desc* d, const void* logits, const 
                              const float* d_topk_weights, const float* d_prob_sum,
                              const float* d_lse, void* d_logits, void* stream);
 
+/* ---- decode -------------------------------------------------------------------------------
+ *
+ * The whole MoE layer for T <= 64 tokens with T * K <= 1024, inference only, in two launches:
+ *   logits = x router^T (fp32), selection and weights as the router above (or the caller's ids
+ *   and weights), y_t = sum_k w_tk o_tk + o_shared_t with o = (silu(x Wg) * (x Wu)) Wd, the
+ *   products w * h rounded to bf16 once, everything else in 32 bits, y rounded once.
+ * Every selected expert's weights are read once per 32 of its tokens.
+ *
+ * weight_type MM_BF16: up bf16 [E, H, 2I], down bf16 [E, I, H] as in mm.h; H, I, shared_I multiples
+ * of 8. MM_E4M3: the same shapes in e4m3 with fp32 scales of their 128 x 128 blocks,
+ * up_scale [E, ceil(H/128), ceil(2I/128)], down_scale [E, ceil(I/128), ceil(H/128)] (rows and
+ * columns counted over the whole matrix, so a block may hold the last gate and the first up
+ * columns); a weight's value is its e4m3 number times its block's scale. H and both I multiples
+ * of 16. The shared expert's matrices have the experts' type, E = 1.
+ * Sizes: H, I, shared_I <= 65536, E <= 1024, K <= 16. */
+typedef struct mm_decode_desc {
+  mm_dims dims;
+  int64_t shared_I; /* 0: no shared expert */
+  int32_t weight_type;
+  int32_t router_type; /* MM_BF16 or MM_FP32: the router weight's type */
+  int32_t score, normalize;
+  float scale;
+} mm_decode_desc;
+
+typedef struct mm_decode_weights {
+  const void *up, *down;                     /* 16-byte aligned */
+  const float *up_scale, *down_scale;        /* MM_E4M3 only */
+  const void *shared_up, *shared_down;       /* with shared_I > 0 */
+  const float *shared_up_scale, *shared_down_scale;
+  const void* router;                        /* [E, H], 16-byte aligned; NULL: the caller routes */
+  const float* router_bias;                  /* fp32 [E] or NULL */
+} mm_decode_weights;
+
+/* Bytes of workspace (0: unsupported). Needs no initialisation; one call at a time may use it. */
+size_t mm_decode_workspace_size(const mm_decode_desc* d);
+
+/* x, y bf16 [T, H], 16-byte aligned. With a router, topk_ids and topk_weights are outputs (either
+ * may be NULL: not wanted); without one they are inputs, int32 and fp32 [T, K]; an id outside
+ * [0, E) records MM_ERR_BAD_EXPERT_ID in the workspace's status word (mm_get_status) and y is not
+ * written. Device waits are bounded and record MM_ERR_TIMEOUT the same way. */
+mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const void* x,
+                    int32_t* topk_ids, float* topk_weights, void* y, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* bf16 matrices w [n, R, C] to e4m3 q [n, R, C] and the scales [n, ceil(R/128), ceil(C/128)] of
+ * their 128 x 128 blocks: scale = max |w| / 448 (1 for a block of zeros), q = w / scale rounded to
+ * nearest even and saturated; a block with an infinity or a NaN gets a NaN scale. C a multiple of
+ * 8, w 16-byte and q 8-byte aligned. */
+mm_status mm_quantize_blocks(int64_t n, int64_t R, int64_t C, const void* w, void* q, float* scale,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

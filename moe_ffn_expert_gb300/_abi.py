@@ -85,6 +85,18 @@ class mm_router_desc(ctypes.Structure):
                 ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class mm_decode_desc(ctypes.Structure):
+    _fields_ = [("dims", mm_dims), ("shared_I", ctypes.c_int64), ("weight_type", ctypes.c_int32),
+                ("router_type", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class mm_decode_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "up", "down", "up_scale", "down_scale", "shared_up", "shared_down", "shared_up_scale",
+        "shared_down_scale", "router", "router_bias")]
+
+
 _P = ctypes.c_void_p
 _LIB = None
 
@@ -128,6 +140,9 @@ def _lib():
         "mm_router_workspace_size": (ctypes.c_size_t, [_P]),
         "mm_router_forward": (st, [_P] * 8 + [ctypes.c_size_t, _P]),
         "mm_router_backward": (st, [_P] * 8),
+        "mm_decode_workspace_size": (ctypes.c_size_t, [_P]),
+        "mm_decode": (st, [_P] * 7 + [ctypes.c_size_t, _P]),
+        "mm_quantize_blocks": (st, [ctypes.c_int64] * 3 + [_P] * 4),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -8,6 +8,11 @@ Training and prompts:
     f            = hyper_mega_moe(n, ids, weights, up, down)    # torch_api
     x, n         = residual_norm(x, f, post_weight=..., gate=..., pre_weight=...)
 
+A few tokens at a time (inference):
+
+    layer = MoEDecoder(up, down, k=8, router_weight=router_weight)   # once per layer
+    f     = layer(n)                                                 # router, experts, sum
+
 `residual_norm` and `moe_router` are differentiable; the `*_forward` / `*_backward` functions are
 the calls they make. Argument marshalling only: shapes and types are checked, non-contiguous
 tensors are copied to contiguous ones, and everything else runs in libmm.so on the current stream.
@@ -288,3 +293,148 @@ class RouterFunction(torch.autograd.Function):
 def moe_router(logits, k, *, bias=None, score="softmax", normalize=True, scale=1.0, stats=False):
     """router_forward with a gradient for the logits (through topk_weights, prob_sum and lse)."""
     return RouterFunction.apply(logits, k, bias, score, normalize, scale, stats)
+
+
+# ------------------------------------------------------------------------------- decode
+
+def quantize_expert_weights(w):
+    """(q float8_e4m3fn of w's shape, scale fp32 [..., ceil(R/128), ceil(C/128)]) of bf16 matrices
+    w [..., R, C]: one scale per 128 x 128 block (mm_quantize_blocks)."""
+    if w.dim() < 2 or w.dtype != torch.bfloat16 or not w.is_cuda:
+        raise ValueError("expected bfloat16 matrices [..., R, C] on a CUDA device")
+    w = w.contiguous()
+    *lead, R, C = w.shape
+    n = w.numel() // (R * C) if R * C else 0
+    q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+    scale = torch.empty((*lead, -(-R // 128), -(-C // 128)), dtype=torch.float32, device=w.device)
+    _abi.check(_abi._lib().mm_quantize_blocks(n, R, C, w.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                              _stream(w)), "mm_quantize_blocks")
+    return q, scale
+
+
+class MoEDecoder:
+    """The whole MoE layer for up to `max_tokens` (<= 64) tokens a call, inference only: keeps the
+    weights, their description and a workspace between calls.
+
+    up_proj_weight [E,H,2I], down_proj_weight [E,I,H]: bf16, or float8_e4m3fn with up_scale /
+    down_scale (quantize_expert_weights). With router_weight [E,H] (bf16 or fp32) a call takes the
+    tokens alone and selects k experts as moe_router does (router_bias fp32 [E], score, normalize,
+    scale); without one it takes topk_ids and topk_weights [T,k]. `shared`: (up [H,2Is],
+    down [Is,H]) of a shared expert, and their two scales for 8-bit weights (or None, None).
+
+    Calls run on the current stream and use the one workspace: one decoder serves one stream."""
+
+    def __init__(self, up_proj_weight, down_proj_weight, *, k, up_scale=None, down_scale=None,
+                 router_weight=None, router_bias=None, score="softmax", normalize=True, scale=1.0,
+                 shared=None, max_tokens=64):
+        up, down = up_proj_weight, down_proj_weight
+        if up.dim() != 3 or down.dim() != 3:
+            raise ValueError("expected up_proj_weight[E,H,2I] and down_proj_weight[E,I,H]")
+        E, H, I2 = up.shape
+        I = I2 // 2
+        if I2 % 2 or down.shape != (E, I, H):
+            raise ValueError("expected up_proj_weight[E,H,2I] and down_proj_weight[E,I,H]")
+        if up.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or down.dtype != up.dtype:
+            raise TypeError("expert weights must be bfloat16 or float8_e4m3fn")
+        fp8 = up.dtype == torch.float8_e4m3fn
+        if score not in _SCORE:
+            raise ValueError("score must be 'softmax' or 'sigmoid'")
+        shared = tuple(shared) + (None,) * (4 - len(shared)) if shared is not None else (None,) * 4
+        s_up, s_down, s_us, s_ds = shared
+        Is = 0
+        if (s_up is None) != (s_down is None):
+            raise ValueError("give both shared-expert weights or neither")
+        if s_up is not None:
+            Is = s_down.shape[0]
+            if s_up.shape != (H, 2 * Is) or s_down.shape != (Is, H):
+                raise ValueError("expected shared weights [H,2Is] and [Is,H]")
+            if s_up.dtype != up.dtype or s_down.dtype != up.dtype:
+                raise TypeError("shared-expert weights must have the experts' type")
+
+        def blocks(n):
+            return -(-n // 128)
+
+        for name, t, shape in (("up_scale", up_scale, (E, blocks(H), blocks(I2))),
+                               ("down_scale", down_scale, (E, blocks(I), blocks(H))),
+                               ("shared up scale", s_us, (blocks(H), blocks(2 * Is))),
+                               ("shared down scale", s_ds, (blocks(Is), blocks(H)))):
+            wanted = fp8 and (Is > 0 or not name.startswith("shared"))
+            if (t is not None) != wanted:
+                raise ValueError(f"{name} goes with float8_e4m3fn weights, and only with them")
+            if t is not None and (t.shape != shape or t.dtype != torch.float32):
+                raise ValueError(f"expected {name} of shape {shape} in float32")
+        if router_weight is not None and router_weight.shape != (E, H):
+            raise ValueError("expected router_weight[E,H]")
+        if router_bias is not None and (router_weight is None or router_bias.shape != (E,)
+                                        or router_bias.dtype != torch.float32):
+            raise ValueError("expected router_bias[E] in float32, with a router_weight")
+        if not 1 <= k <= E:
+            raise ValueError("expected 1 <= k <= E")
+        kept = [up, down, up_scale, down_scale, s_up, s_down, s_us, s_ds, router_weight, router_bias]
+        _on_gpu("MoEDecoder", *kept)
+        kept = [_contiguous(t) for t in kept]
+        self._kept = kept
+        self._weights = _abi.mm_decode_weights(*[_ptr(t) for t in kept])
+        self._weights_at = ctypes.addressof(self._weights)
+        self.routes = router_weight is not None
+        self.k, self.H, self.device, self.max_tokens = int(k), H, up.device, int(max_tokens)
+        rt = _type("router_weight", router_weight) if self.routes else _abi.MM_BF16
+        self._fields = (Is, _abi.MM_E4M3 if fp8 else _abi.MM_BF16, rt, _SCORE[score], int(normalize),
+                        float(scale))
+        self._dims = (H, I, E)
+        self._descs = {}
+        nbytes = self._desc(self.max_tokens)[1]
+        if nbytes == 0:
+            raise ValueError(f"unsupported sizes max_tokens={max_tokens} H={H} I={I} E={E} k={k} Is={Is}")
+        self._ws = torch.empty(nbytes, dtype=torch.uint8, device=up.device)
+
+    def _desc(self, T):
+        """(address of the descriptor of a call with T tokens, its workspace bytes)."""
+        got = self._descs.get(T)
+        if got is None:
+            H, I, E = self._dims
+            d = _abi.mm_decode_desc(_abi.dims(T, H, I, E, self.k), *self._fields)
+            at = ctypes.addressof(d)
+            got = self._descs[T] = (at, int(_abi._lib().mm_decode_workspace_size(at)), d)
+        return got
+
+    def _call(self, x, ids, weights):
+        if x.dim() != 2 or x.shape[1] != self.H or x.dtype != torch.bfloat16 or x.device != self.device:
+            raise ValueError(f"expected x[T,{self.H}] in bfloat16 on {self.device}")
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens in a decoder for {self.max_tokens}")
+        x = _contiguous(x)
+        y = torch.empty_like(x)
+        _abi.check(_abi._lib().mm_decode(
+            self._desc(T)[0], self._weights_at, x.data_ptr(), _ptr(ids), _ptr(weights), y.data_ptr(),
+            self._ws.data_ptr(), self._ws.numel(), _stream(x)), "mm_decode")
+        return y
+
+    def __call__(self, x, topk_ids=None, topk_weights=None):
+        """y [T,H] bf16 for x [T,H] bf16."""
+        if self.routes:
+            if topk_ids is not None or topk_weights is not None:
+                raise ValueError("this decoder routes by itself (it has a router_weight)")
+            return self._call(x, None, None)
+        if topk_ids is None or topk_weights is None:
+            raise ValueError("a decoder without a router_weight needs topk_ids and topk_weights")
+        if topk_ids.shape != (x.shape[0], self.k) or topk_weights.shape != topk_ids.shape:
+            raise ValueError(f"expected topk_ids and topk_weights [T,{self.k}]")
+        if topk_ids.dtype not in (torch.int32, torch.int64):
+            raise TypeError("topk_ids must be int32 or int64")
+        ids = _contiguous(topk_ids.to(torch.int32))
+        return self._call(x, ids, _contiguous(topk_weights.to(torch.float32)))
+
+    def with_routing(self, x):
+        """(y, topk_ids int32 [T,k], topk_weights fp32 [T,k]) of a decoder that routes."""
+        if not self.routes:
+            raise ValueError("this decoder has no router_weight")
+        ids = torch.empty((x.shape[0], self.k), dtype=torch.int32, device=self.device)
+        weights = torch.empty((x.shape[0], self.k), dtype=torch.float32, device=self.device)
+        return self._call(x, ids, weights), ids, weights
+
+    def status(self) -> int:
+        """Waits for the current stream and returns the last call's status (MM_OK,
+        MM_ERR_BAD_EXPERT_ID or MM_ERR_TIMEOUT)."""
+        return _abi.mm_get_status(self._ws.data_ptr(), _stream(self._ws))

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmm.so")
 SOURCES = ["mm_api.cu", "mm_route.cu", "mm_gemm.cu", "mm_route_static.cu", "mm_norm.cu",
-           "mm_router.cu"]
+           "mm_router.cu", "mm_decode.cu"]
 HEADERS = ["mm_device.cuh", "mm_layout.h", "mm_kernels.h", "mm_rows.cuh", "mm_select.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

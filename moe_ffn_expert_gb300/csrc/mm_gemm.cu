@@ -1419,35 +1419,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Tensor map; dims/box innermost first; strides in bytes (rank-1). bf16 with the 128-byte
-// swizzle unless stated.
-bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-              const uint64_t* strides, const uint32_t* box,
-              CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-  auto fn = encode_fn();
-  if (!fn) {
-    note_error("cuTensorMapEncodeTiled unavailable");
-    return false;
-  }
-  cuuint64_t d[3], s[2];
-  cuuint32_t b[3], es[3] = {1, 1, 1};
-  for (int i = 0; i < rank; ++i) {
-    d[i] = dims[i];
-    b[i] = box[i];
-  }
-  for (int i = 0; i < rank - 1; ++i) s[i] = strides[i];
-  const CUresult r = fn(m, dtype, (cuuint32_t)rank, const_cast<void*>(base), d, s, b, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    note_error("tensor map encode failed (CUresult %d): rank %d dims %llu %llu %llu box %u %u %u",
-               (int)r, rank, (unsigned long long)d[0], (unsigned long long)(rank > 1 ? d[1] : 0),
-               (unsigned long long)(rank > 2 ? d[2] : 0), b[0], rank > 1 ? b[1] : 0u,
-               rank > 2 ? b[2] : 0u);
-  return r == CUDA_SUCCESS;
-}
-
 bool map_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, uint32_t box_cols,
               uint32_t box_rows) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
@@ -1800,6 +1771,32 @@ cudaError_t run(const Workspace& w, char* ws, const GemmCall& c, cudaStream_t st
 }  // namespace
 
 int device_sm_count() { return sm_count(); }
+
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box,
+              CUtensorMapDataType dtype, CUtensorMapSwizzle swz) {
+  auto fn = encode_fn();
+  if (!fn) {
+    note_error("cuTensorMapEncodeTiled unavailable");
+    return false;
+  }
+  cuuint64_t d[3], s[2];
+  cuuint32_t b[3], es[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+  }
+  for (int i = 0; i < rank - 1; ++i) s[i] = strides[i];
+  const CUresult r = fn(m, dtype, (cuuint32_t)rank, const_cast<void*>(base), d, s, b, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    note_error("tensor map encode failed (CUresult %d): rank %d dims %llu %llu %llu box %u %u %u",
+               (int)r, rank, (unsigned long long)d[0], (unsigned long long)(rank > 1 ? d[1] : 0),
+               (unsigned long long)(rank > 2 ? d[2] : 0), b[0], rank > 1 ? b[1] : 0u,
+               rank > 2 ? b[2] : 0u);
+  return r == CUDA_SUCCESS;
+}
 
 cudaError_t launch_gemm(const Workspace& w, char* ws, const GemmCall& c, cudaStream_t st) {
   const int pair = c.paired;

@@ -1,6 +1,7 @@
 // Host launchers of the library's kernels (each enqueues exactly one kernel on `stream`).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -125,6 +126,13 @@ struct SumArgs {
   int jobs, cols, type;
 };
 cudaError_t launch_column_sums(const SumArgs& a, int64_t rows, cudaStream_t st);
+
+// Tensor map of a rank-2 or -3 tensor; dims and box innermost first, strides in bytes (rank - 1).
+// False (with the reason noted) if it cannot be encoded.
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box,
+              CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B);
 
 // Records a description of a host-side failure for mm_last_error_detail (this thread).
 void note_error(const char* fmt, ...);

@@ -110,3 +110,39 @@ def test_router_host_checks():
     assert lib.mm_router_workspace_size(ref(d)) >= 256
     assert lib.mm_router_backward(ref(d), 16, None, 16, None, None, 16, None) == _abi.MM_ERR_INVALID_ARG
     assert lib.mm_router_backward(ref(desc(T=0)), None, None, None, None, None, None, None) == _abi.MM_OK
+
+
+def test_decode_host_checks():
+    lib = _abi._lib()
+    bad, unsup, wsz = _abi.MM_ERR_INVALID_ARG, _abi.MM_ERR_UNSUPPORTED, _abi.MM_ERR_WORKSPACE
+
+    def desc(T=4, H=64, I=32, E=8, K=2, Is=0, wt=0, rt=0, score=0):
+        return _abi.mm_decode_desc(_abi.dims(T, H, I, E, K), Is, wt, rt, score, 1, 1.0)
+
+    def weights(up=16, down=16, us=0, ds=0, su=0, sd=0, sus=0, sds=0, r=16, b=0):
+        return _abi.mm_decode_weights(*[p or None for p in (up, down, us, ds, su, sd, sus, sds, r, b)])
+
+    def call(d, w, x=16, ids=16, tw=16, y=16, ws=256, size=1 << 30):
+        return lib.mm_decode(ref(d), ref(w), x, ids, tw, y, ws, size, None)
+
+    for d in (desc(T=-1), desc(H=0), desc(I=0), desc(E=0), desc(K=0), desc(Is=-8), desc(wt=1), desc(rt=2), desc(score=3)):
+        assert call(d, weights()) == bad and lib.mm_decode_workspace_size(ref(d)) == 0
+    for d in (desc(T=65), desc(K=17), desc(T=64, K=17), desc(E=1025), desc(H=60), desc(I=36), desc(Is=4), desc(H=65544),
+              desc(wt=2, H=72), desc(wt=2, I=40)):
+        assert call(d, weights()) == unsup and lib.mm_decode_workspace_size(ref(d)) == 0
+    d = desc()
+    n = lib.mm_decode_workspace_size(ref(d))
+    assert n > 0
+    assert call(d, weights(), size=n - 1) == wsz and call(d, weights(), ws=128) == wsz and call(d, weights(), ws=None) == wsz
+    for w in (weights(up=0), weights(down=24), weights(us=16, ds=16), weights(su=16, sd=16), weights(r=8), weights(b=2),
+              weights(r=0, b=16)):
+        assert call(d, w) == bad
+    assert call(d, weights(), x=None) == bad and call(d, weights(), y=24) == bad and call(d, weights(), ids=18) == bad
+    assert call(d, weights(r=0), ids=None) == bad                      # no router: the ids are inputs
+    assert call(desc(E=1, K=2), weights()) == bad                      # more experts wanted than there are
+    assert call(desc(wt=2), weights()) == bad                          # 8-bit weights without scales
+    assert call(desc(Is=32), weights()) == bad                         # a shared expert without weights
+    assert lib.mm_quantize_blocks(-1, 8, 8, 16, 16, 16, None) == bad
+    assert lib.mm_quantize_blocks(1, 8, 12, 16, 16, 16, None) == unsup
+    assert lib.mm_quantize_blocks(1, 8, 8, 24, 16, 16, None) == bad
+    assert lib.mm_quantize_blocks(0, 8, 8, None, None, None, None) == _abi.MM_OK
