@@ -17,10 +17,17 @@
 // works through its units in the order it claimed them, so what a unit waits for is always held
 // by a CTA that is running or done: no wait depends on how many CTAs are resident.
 //
-// The products run as mma.sync m16n8k16 with the weights as the 16-row operand (its transpose
-// comes with ldmatrix.trans from the row-major tiles that TMA brings) and up to 8 tokens per
-// instruction: one to 32 rows of an expert cost no padding to 128 rows and no accumulator in
-// tensor memory, and the tensor cores are idle for most of the time either way.
+// The products run on tcgen05.mma with the weights as the M = 128 operand, straight from the
+// row-major tiles that TMA brings (MN-major descriptors), and the chunk's rows as N: 16 or 32
+// columns of the accumulator instead of 128 rows of padding. No thread touches a weight.
+//
+// e4m3 weights meet 16-bit activations: tensor cores take either both in 8 bits or both in 16.
+// A bf16 number is the exact sum of two e4m3 numbers, x s = hi + lo / 16 (4 significant bits
+// each, s a power of two per row that keeps the row's largest value below 256; what lies 2^-22
+// below that is rounded), so both halves of every row are columns of N and the accumulator's two
+// columns are added: twice the columns, no conversion of the weights, which outnumber the rows'
+// elements many times. The products of 128 x 128 blocks are scaled in 32 bits as they leave the
+// tensor memory. h is split the same way, with a scale per row and 64 columns.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -40,17 +47,18 @@ constexpr int kChunk = 32;        // rows of one expert per unit
 constexpr int kCols = 128;        // weight columns per unit
 constexpr int kTokens = 8;        // tokens per combine unit
 constexpr int kMaxSplit = 4;      // parts of I per GEMM2 column tile
-constexpr int kConsumers = 8;     // warps; 4 column groups x 2 halves of a stage's k
-constexpr int kThreads = 32 * (kConsumers + 2);
 constexpr int kTileBytes = 16384; // one stage of weights: 64 x 128 bf16 or 128 x 128 e4m3
-constexpr int kQueue = 4;
+constexpr int kThreads = 384;     // weight loads, row loads, MMA, tensor memory; 2 x 4 epilogue
+constexpr int kFirstEpilogue = 4;
+constexpr int kQueue = 8;         // units claimed ahead
+constexpr int kSlots = 8;         // accumulators of 64 columns in tensor memory, half per epilogue set
+constexpr int kRing = kSlots / 2;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <bool FP8>
 struct Cfg {
-  static constexpr int KB = FP8 ? 128 : 64;           // k per stage
-  static constexpr int PITCH = KB * 2 + 16;           // bytes per row of the token operand
-  static constexpr int B_BYTES = kChunk * PITCH;
+  static constexpr int KB = FP8 ? 128 : 64;                 // k per stage: 128 bytes of a row
+  static constexpr int B_BYTES = (FP8 ? 2 : 1) * kChunk * 128;
   static constexpr int STAGES = FP8 ? 7 : 8;
 };
 
@@ -58,8 +66,9 @@ struct Cfg {
 enum { W_STATUS = 0, W_NEXT = 1, W_READY1 = 64 };
 
 struct DecodeArgs {
-  CUtensorMap up, down, s_up, s_down;
-  const __nv_bfloat16* x;
+  CUtensorMap up, down, s_up, s_down;  // weights, boxes of 64 columns
+  CUtensorMap x;                       // token rows (e4m3: hi rows, then lo rows), one per box
+  CUtensorMap h_rows, s_h_rows;        // rows of h (the same), 8 per box
   const float *up_scale, *down_scale, *s_up_scale, *s_down_scale;
   const float* logits;    // with a router
   const float* bias;
@@ -68,25 +77,31 @@ struct DecodeArgs {
   __nv_bfloat16* y;
   int* hdr;
   int *ready1, *ready2;
-  __nv_bfloat16 *h, *s_h;  // [S, I], [T, Is]
+  void *h, *s_h;           // bf16 [S, I], [T, Is]; e4m3: [2, S, I], [2, T, Is]
+  const float* x_scale;    // e4m3: [T], [S, ceil(I / 64)], [T, ceil(Is / 64)]
+  float *h_scale, *s_h_scale;
   float *o, *s_o;          // [split][S, H], [split][T, H]
   int T, H, I, E, K, S, Is, score, normalize, route;
   float scale;
 };
 
-// Everything of a CTA that is derived from the routing.
+// What a CTA keeps of the routing.
 struct Tables {
+  float w[kMaxSlots];          // weight of a sorted row
   int16_t tok[kMaxSlots];      // token of a sorted row
   int16_t row[kMaxSlots];      // sorted row of a slot
-  float w[kMaxSlots];          // weight of a sorted row
-  float slot_w[kMaxSlots];     // weight of a slot
-  int16_t id[kMaxSlots];       // expert of a slot
   uint16_t chunk_row[kMaxSlots];
   uint16_t chunk_e[kMaxSlots];
-  uint32_t count[kMaxE];       // slots | chunks << 16, then the exclusive sums
-  uint16_t next[kMaxE];        // rows placed so far
   uint8_t chunk_n[kMaxSlots];
   int chunks, bad;
+};
+
+// What only building the tables needs (in the stage ring's memory).
+struct Building {
+  float slot_w[kMaxSlots];     // weight of a slot
+  int16_t id[kMaxSlots];       // expert of a slot
+  uint32_t count[kMaxE];       // slots | chunks << 16, then the exclusive sums
+  uint16_t next[kMaxE];        // rows placed so far
 };
 
 struct Unit {
@@ -99,45 +114,22 @@ struct Work {
   int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, t2s, total;
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+// x = (hi + lo / 16) / s for |x s| < 256.
+__device__ __forceinline__ void split_e4m3(float xs, uint8_t& hi, uint8_t& lo) {
+  hi = __nv_cvt_float_to_fp8(xs, __NV_SATFINITE, __NV_E4M3);
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(hi, __NV_E4M3);
+  const float back = __half2float(*reinterpret_cast<const __half*>(&h));
+  lo = __nv_cvt_float_to_fp8((xs - back) * 16.f, __NV_SATFINITE, __NV_E4M3);
 }
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-// d += a b for a 16 x 16 tile of weights (transposed) and 8 tokens.
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Two e4m3 numbers (low and high byte) as bf16: exact (3 mantissa bits, exponents -9..8), NaN stays.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_bf16(f.x, f.y);
+// The power of two that brings a largest magnitude into [128, 256) and its inverse. `amax` that is
+// not finite: the inverse is NaN, so that whatever the row's products are multiplied with it is.
+__device__ __forceinline__ float split_scale(float amax, float* inverse) {
+  int e = (int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127;
+  const bool bad = e == 128;
+  e = max(e, -100);  // zero and tiny rows
+  *inverse = bad ? __int_as_float(0x7FC00000) : __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+  return bad ? 0.f : __uint_as_float((uint32_t)(7 - e + 127) << 23);
 }
 
 // ---------------------------------------------------------------------------------- k_logits
@@ -149,7 +141,50 @@ struct LogitArgs {
   int* zero;  // words to clear
   int zero_n;
   int T, H, E;
+  int logit_blocks;  // then, for e4m3 weights, one block per token
+  uint8_t* x8;       // [2, T, H]
+  float* x_scale;    // [T]
 };
+
+// Row t of x as e4m3 hi and lo parts.
+__device__ void split_row(const LogitArgs& a, int t, float* red) {
+  const int tid = threadIdx.x;
+  const __nv_bfloat16* row = a.x + (int64_t)t * a.H;
+  float m = 0.f;
+  bool nan = false;
+  for (int c = tid * 8; c < a.H; c += 256 * 8) {
+    float v[8];
+    load_vec<8>(row + c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      nan |= v[k] != v[k];
+      m = fmaxf(m, fabsf(v[k]));
+    }
+  }
+  m = warp_max(m);
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  nan = __syncthreads_or(nan);
+  m = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+  float inv;
+  const float s = split_scale(nan ? INFINITY : m, &inv);
+  if (tid == 0) a.x_scale[t] = inv;
+  uint8_t* hi = a.x8 + (int64_t)t * a.H;
+  uint8_t* lo = a.x8 + (int64_t)(a.T + t) * a.H;
+  for (int c = tid * 8; c < a.H; c += 256 * 8) {
+    float v[8];
+    load_vec<8>(row + c, v);
+    uint8_t h[8], l[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) split_e4m3(v[k] * s, h[k], l[k]);
+    auto word = [](const uint8_t* b) {
+      return (uint32_t)b[0] | (uint32_t)b[1] << 8 | (uint32_t)b[2] << 16 | (uint32_t)b[3] << 24;
+    };
+    *reinterpret_cast<uint2*>(hi + c) = make_uint2(word(h), word(h + 4));
+    *reinterpret_cast<uint2*>(lo + c) = make_uint2(word(l), word(l + 4));
+  }
+}
 
 // 4 experts x 4 tokens per block, H dealt to the 8 warps; the 16 sums of a warp's lanes are
 // reduced by halving exchanges, the warps' sums in order.
@@ -159,10 +194,13 @@ __global__ void __launch_bounds__(256) k_logits(LogitArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
-  for (int i = block * 256 + tid; i < a.zero_n; i += blocks * 256) a.zero[i] = 0;
-  if (a.router == nullptr) return;
-  const int e0 = blockIdx.x * 4, t0 = blockIdx.y * 4;
+  for (int i = (int)blockIdx.x * 256 + tid; i < a.zero_n; i += (int)gridDim.x * 256) a.zero[i] = 0;
+  if ((int)blockIdx.x >= a.logit_blocks) {
+    if (a.x8 != nullptr) split_row(a, (int)blockIdx.x - a.logit_blocks, &part[0][0]);
+    return;
+  }
+  const int eb = (a.E + 3) / 4;
+  const int e0 = (int)blockIdx.x % eb * 4, t0 = (int)blockIdx.x / eb * 4;
   float acc[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
@@ -195,14 +233,13 @@ __global__ void __launch_bounds__(256) k_logits(LogitArgs a) {
 // ---------------------------------------------------------------------------------- k_experts
 
 template <int NV>
-__device__ void select_row(const DecodeArgs& a, Tables& tb, int t, int lane) {
-  const float* row = a.logits + (int64_t)t * a.E;
+__device__ void select_row(const DecodeArgs& a, Building& bd, const float* row, int t, int lane) {
   uint32_t key[NV];
   float z[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = lane + 32 * j;
-    z[j] = e < a.E ? __ldcg(row + e) : 0.f;
+    z[j] = e < a.E ? row[e] : 0.f;
   }
   float m = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -224,11 +261,11 @@ __device__ void select_row(const DecodeArgs& a, Tables& tb, int t, int lane) {
     sum = warp_sum(sum);
   }
   const int id = select_topk<NV>(key, a.K, lane);
-  const float zs = lane < a.K ? __ldcg(row + id) : 0.f;
+  const float zs = lane < a.K ? row[id] : 0.f;
   const float w = selected_weight(zs, lane < a.K, a.score, a.normalize, a.scale, m, sum);
   if (lane < a.K) {
-    tb.id[t * a.K + lane] = (int16_t)id;
-    tb.slot_w[t * a.K + lane] = w;
+    bd.id[t * a.K + lane] = (int16_t)id;
+    bd.slot_w[t * a.K + lane] = w;
     if (blockIdx.x == 0) {
       if (a.ids != nullptr) a.ids[t * a.K + lane] = id;
       if (a.weights != nullptr) a.weights[t * a.K + lane] = w;
@@ -238,34 +275,48 @@ __device__ void select_row(const DecodeArgs& a, Tables& tb, int t, int lane) {
 
 // Routing tables of the CTA: the slots sorted by expert (stable), cut into chunks. The same in
 // every CTA. False if a caller's id is out of range.
-__device__ bool build_tables(const DecodeArgs& a, Tables& tb) {
+__device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int ring_bytes) {
+  Building& bd = *reinterpret_cast<Building*>(ring);
+  float* ls = reinterpret_cast<float*>(ring + sizeof(Building));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e < a.E; e += kThreads) tb.count[e] = 0, tb.next[e] = 0;
+  for (int e = tid; e < a.E; e += kThreads) bd.count[e] = 0, bd.next[e] = 0;
   if (tid == 0) tb.bad = 0;
-  __syncthreads();
   if (a.route) {
-    for (int t = warp; t < a.T; t += kThreads / 32) {
-      if (a.E <= 32) select_row<1>(a, tb, t, lane);
-      else if (a.E <= 64) select_row<2>(a, tb, t, lane);
-      else if (a.E <= 128) select_row<4>(a, tb, t, lane);
-      else if (a.E <= 256) select_row<8>(a, tb, t, lane);
-      else if (a.E <= 512) select_row<16>(a, tb, t, lane);
-      else select_row<32>(a, tb, t, lane);
+    // all logits at once where they fit (T E <= 31 K), so that a row's selection starts from
+    // shared memory
+    const int n = a.T * a.E;
+    const bool fits = (size_t)n * 4 + sizeof(Building) <= (size_t)ring_bytes;
+    if (fits) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kThreads) ls[i] = __ldcg(a.logits + i);
+      __syncthreads();
     }
+    const float* rows = fits ? ls : a.logits;
+    for (int t = warp; t < a.T; t += kThreads / 32) {
+      const float* row = rows + t * a.E;
+      if (a.E <= 32) select_row<1>(a, bd, row, t, lane);
+      else if (a.E <= 64) select_row<2>(a, bd, row, t, lane);
+      else if (a.E <= 128) select_row<4>(a, bd, row, t, lane);
+      else if (a.E <= 256) select_row<8>(a, bd, row, t, lane);
+      else if (a.E <= 512) select_row<16>(a, bd, row, t, lane);
+      else select_row<32>(a, bd, row, t, lane);
+    }
+    __syncthreads();
   } else {
+    __syncthreads();
     for (int s = tid; s < a.S; s += kThreads) {
       const int e = a.ids[s];
       if (e < 0 || e >= a.E) tb.bad = 1;
-      tb.id[s] = (int16_t)e;
-      tb.slot_w[s] = a.weights[s];
+      bd.id[s] = (int16_t)e;
+      bd.slot_w[s] = a.weights[s];
+    }
+    __syncthreads();
+    if (tb.bad) {
+      if (tid == 0) set_status(a.hdr + W_STATUS, MM_ERR_BAD_EXPERT_ID);
+      return false;
     }
   }
-  __syncthreads();
-  if (tb.bad) {
-    if (tid == 0) set_status(a.hdr + W_STATUS, MM_ERR_BAD_EXPERT_ID);
-    return false;
-  }
-  for (int s = tid; s < a.S; s += kThreads) atomicAdd(&tb.count[tb.id[s]], 1u);
+  for (int s = tid; s < a.S; s += kThreads) atomicAdd(&bd.count[bd.id[s]], 1u);
   __syncthreads();
   if (warp == 0) {
     // exclusive sums of slots (low half) and chunks (high half) over the experts; a lane takes
@@ -273,8 +324,8 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb) {
     const int per = (a.E + 31) / 32, e0 = lane * per, e1 = min(a.E, e0 + per);
     uint32_t sum = 0;
     for (int e = e0; e < e1; ++e) {
-      const uint32_t n = tb.count[e];
-      tb.count[e] = sum;
+      const uint32_t n = bd.count[e];
+      bd.count[e] = sum;
       sum += n | ((n + kChunk - 1) / kChunk) << 16;
     }
     uint32_t before = sum;
@@ -285,35 +336,37 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb) {
     }
     if (lane == 31) tb.chunks = (int)(before >> 16);
     before -= sum;
-    for (int e = e0; e < e1; ++e) tb.count[e] += before;
+    for (int e = e0; e < e1; ++e) bd.count[e] += before;
     __syncwarp();
     // slots in order, 32 at a time: a slot's place among its expert's is what came before
     for (int s0 = 0; s0 < a.S; s0 += 32) {
       const int s = s0 + lane;
-      const int e = s < a.S ? tb.id[s] : -1 - lane;
+      const int e = s < a.S ? bd.id[s] : -1 - lane;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
       if (s < a.S) {
-        const int rank = tb.next[e] + __popc(same & ((1u << lane) - 1u));
-        const int r = (int)(tb.count[e] & 0xFFFFu) + rank;
+        const int rank = bd.next[e] + __popc(same & ((1u << lane) - 1u));
+        const int r = (int)(bd.count[e] & 0xFFFFu) + rank;
         tb.row[s] = (int16_t)r;
         tb.tok[r] = (int16_t)(s / a.K);
-        tb.w[r] = tb.slot_w[s];
+        tb.w[r] = bd.slot_w[s];
         if (rank % kChunk == 0) {  // first row of a chunk
-          const int c = (int)(tb.count[e] >> 16) + rank / kChunk;
+          const int c = (int)(bd.count[e] >> 16) + rank / kChunk;
           tb.chunk_row[c] = (uint16_t)r;
           tb.chunk_e[c] = (uint16_t)e;
         }
       }
       __syncwarp();
-      if (s < a.S && (same >> lane) == 1u) tb.next[e] += (uint16_t)__popc(same);
+      if (s < a.S && (same >> lane) == 1u) bd.next[e] += (uint16_t)__popc(same);
       __syncwarp();
     }
   }
   __syncthreads();
   for (int c = tid; c < tb.chunks; c += kThreads) {
-    const int e = tb.chunk_e[c], first = (int)(tb.count[e] & 0xFFFFu);
-    tb.chunk_n[c] = (uint8_t)min(kChunk, first + (int)tb.next[e] - (int)tb.chunk_row[c]);
+    const int e = tb.chunk_e[c], first = (int)(bd.count[e] & 0xFFFFu);
+    tb.chunk_n[c] = (uint8_t)min(kChunk, first + (int)bd.next[e] - (int)tb.chunk_row[c]);
   }
+  // the ring is TMA's from here on
+  fence_proxy_async_smem();
   __syncthreads();
   return true;
 }
@@ -397,51 +450,89 @@ __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, c
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<FP8>;
-  constexpr int KB = C::KB, STAGES = C::STAGES, PITCH = C::PITCH;
+  constexpr int KB = C::KB, STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
-  __shared__ uint64_t bars[3 * STAGES + 2 * kQueue + 8];
+  __shared__ uint64_t bars[3 * STAGES + 2 * kQueue + 2 * kSlots + 4 + 1];
   __shared__ int queue[kQueue];
+  __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // weights of all stages (1024-byte aligned for the swizzle), token rows, the sums of the second
-  // k half's warps
+  // the stages' weights and rows (1024-byte aligned for the swizzle), then [row][128 columns] of
+  // a GEMM1 unit for each epilogue set
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const aligned = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t rows_at = base + STAGES * kTileBytes;
-  float* const halves = reinterpret_cast<float*>(aligned + STAGES * (kTileBytes + C::B_BYTES));
+  float* const exchange = reinterpret_cast<float*>(aligned + STAGES * (kTileBytes + C::B_BYTES));
   const uint32_t bar0 = smem_u32(bars);
   auto full_w = [&](int s) { return bar0 + 8u * s; };
   auto full_b = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
   auto q_full = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };
   auto q_empty = [&](int s) { return bar0 + 8u * (3 * STAGES + kQueue + s); };
-  auto half_full = [&](int c) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + c); };
-  auto half_empty = [&](int c) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + 4 + c); };
+  auto acc_full = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + s); };
+  auto acc_empty = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + kSlots + s); };
+  auto x_full = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + 2 * kSlots + s); };
+  auto x_empty = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + 2 * kSlots + 2 + s); };
+  const uint32_t mma_done = bar0 + 8u * (3 * STAGES + 2 * kQueue + 2 * kSlots + 4);
   if (tid == 0) {
-    for (int c = 0; c < 4; ++c) {
-      mbar_init(half_full(c), 1);
-      mbar_init(half_empty(c), 1);
-    }
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_w(s), 1);
       mbar_init(full_b(s), 1);
-      mbar_init(empty(s), kConsumers);
+      mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kQueue; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), kConsumers + 1);
+      mbar_init(q_empty(s), 2 + 8);  // row loads, MMA, epilogue warps
     }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(acc_full(s), 1);
+      mbar_init(acc_empty(s), 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(x_full(s), 4);
+      mbar_init(x_empty(s), 4);
+    }
+    mbar_init(mma_done, 1);
     mbar_fence_init();
     tma_prefetch_desc(&a.up);
     tma_prefetch_desc(&a.down);
+    tma_prefetch_desc(&a.x);
+    tma_prefetch_desc(&a.h_rows);
   }
   pdl_wait();
-  if (!build_tables(a, tb)) return;  // (its barriers also publish the initialised mbarriers)
+  if (!build_tables(a, tb, aligned, STAGES * (kTileBytes + C::B_BYTES))) return;
+  if (warp == 3) {
+    tmem_alloc(smem_u32(&tmem_slot), kSlots * 64);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
   const Work work = make_work<FP8>(a, tb.chunks);
   // a wait that runs out ends its role; the roles that depend on it run out in turn
   auto give_up = [&] { set_status(a.hdr + W_STATUS, MM_ERR_TIMEOUT); };
+  // next unit of the queue (-1: no more, -2: gave up); one lane per warp counts the read
+  auto take = [&](int qi) {
+    const int qs = qi % kQueue;
+    if (!mbar_wait(q_full(qs), (qi / kQueue) & 1, kTimeoutNs)) {
+      if (lane == 0) give_up();
+      return -2;
+    }
+    return queue[qs];
+  };
+  // accumulators of a unit: one for bf16; e4m3: one per scale, 128 rows of up, 64 of down
+  auto slots_of = [&](const Unit& u) {
+    if (!FP8) return 1;
+    if (u.kind == 0) return u.kb1 - u.kb0;
+    const int I = u.shared ? a.Is : a.I;
+    return min(2 * u.kb1, (I + 63) / 64) - 2 * u.kb0;
+  };
+  auto columns_of = [&](const Unit& u) {  // N of the products
+    return FP8 ? 2 * ((u.n + 7) & ~7) : (u.n + 15) & ~15;
+  };
 
-  if (warp == kConsumers) {
+  if (warp == 0) {
     // ------------------------------------------------ claims units and loads their weights
     if (lane == 0) {
       int u = blockIdx.x, it = 0;
@@ -459,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         u = gridDim.x + atomicAdd(a.hdr + W_NEXT, 1);
         const CUtensorMap* map = un.kind == 0 ? (un.shared ? &a.s_up : &a.up)
                                               : (un.shared ? &a.s_down : &a.down);
-        const int I = un.shared ? a.Is : a.I;
+        const int c0 = un.tile * (un.kind == 0 ? 64 : kCols);
+        const int c1 = un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + 64;
         for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
           const int s = it % STAGES;
           if (!mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, kTimeoutNs)) {
@@ -469,44 +561,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           }
           const uint32_t dst = base + s * kTileBytes;
           mbar_arrive_expect_tx(full_w(s), kTileBytes);
-          if (un.kind == 0) {
-            tma_load_3d(dst, map, full_w(s), un.tile * 64, kb * KB, un.e);
-            tma_load_3d(dst + kTileBytes / 2, map, full_w(s), I + un.tile * 64, kb * KB, un.e);
-          } else if (FP8) {
-            tma_load_3d(dst, map, full_w(s), un.tile * kCols, kb * KB, un.e);
-          } else {
-            tma_load_3d(dst, map, full_w(s), un.tile * kCols, kb * KB, un.e);
-            tma_load_3d(dst + kTileBytes / 2, map, full_w(s), un.tile * kCols + 64, kb * KB, un.e);
-          }
+          tma_load_3d(dst, map, full_w(s), c0, kb * KB, un.e);
+          tma_load_3d(dst + kTileBytes / 2, map, full_w(s), c1, kb * KB, un.e);
         }
       }
       // no CTA leaves with a copy into its shared memory in flight
       for (int j = max(0, it - STAGES); j < it; ++j)
         mbar_wait(full_w(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
     }
-  } else if (warp == kConsumers + 1) {
-    // ------------------------------------------------ loads the token rows
+  } else if (warp == 1) {
+    // ------------------------------------------------ loads the rows
     int it = 0;
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
-      const int qs = qi % kQueue;
-      if (!mbar_wait(q_full(qs), (qi / kQueue) & 1, kTimeoutNs)) {
-        if (lane == 0) give_up();
-        break;
-      }
-      const int u = queue[qs];
+      const int u = take(qi);
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_empty(qs));
+      if (u == -2) break;
+      if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
       if (u < 0) break;
       const Unit un = unit_at(a, tb, work, u);
       if (un.kind == 2) continue;
-      const int I = un.shared ? a.Is : a.I, width = un.kind == 0 ? a.H : I;
-      const __nv_bfloat16* src = a.x;
+      const CUtensorMap* map = un.kind == 0 ? &a.x : un.shared ? &a.s_h_rows : &a.h_rows;
+      // lanes of the first half load the rows (e4m3: their hi parts), those of the second the lo
+      // parts; x: 4 rows by number per lane, h: 8 consecutive rows
+      const int part = lane >> 4, j = lane & 15;
+      const int n8 = (un.n + 7) & ~7, groups = un.kind == 0 ? (un.n + 3) / 4 : n8 / 8;
+      const bool loads = (FP8 || part == 0) && j < groups;
+      const int lo = part * (un.kind == 0 || un.shared ? a.T : a.S);  // first row of the lo parts
+      int r[4] = {0, 0, 0, 0};
       if (un.kind == 0) {
-        if (lane < un.n)
-          src += (int64_t)(un.shared ? un.row0 + lane : tb.tok[un.row0 + lane]) * a.H;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = un.row0 + min(4 * j + i, un.n - 1);
+          r[i] = lo + (un.shared ? row : tb.tok[row]);
+        }
       } else {
-        // this chunk's rows: every consumer warp of the first k half counts once per unit
+        // the chunk's rows of h: every epilogue warp counts once per GEMM1 unit
         const int target = 4 * (un.shared ? work.nt1s : work.nt1);
         int there = 1;
         if (lane == 0) there = wait_counter(a.ready1 + un.ready, target, kTimeoutNs);
@@ -515,8 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           break;
         }
         fence_proxy_async_global();
-        src = (un.shared ? a.s_h : a.h) + (int64_t)(un.row0 + lane) * I;
+        r[0] = lo + un.row0 + 8 * j;
       }
+      const uint32_t bytes = (FP8 ? 2 : 1) * groups * (un.kind == 0 ? 512 : 1024);
+      const uint32_t to = (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
         const int s = it % STAGES;
         if (!mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, kTimeoutNs)) {
@@ -524,32 +616,97 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           ok = false;
           break;
         }
-        const uint32_t bytes = (uint32_t)min(KB, width - kb * KB) * 2u;
-        if (lane == 0) mbar_arrive_expect_tx(full_b(s), bytes * un.n);
+        if (lane == 0) mbar_arrive_expect_tx(full_b(s), bytes);
         __syncwarp();
-        if (lane < un.n)
-          bulk_load(rows_at + s * C::B_BYTES + lane * PITCH, src + kb * KB, bytes, full_b(s));
+        if (loads) {
+          const uint32_t dst = rows_at + s * C::B_BYTES + to;
+          if (un.kind == 0)
+            tma_gather4(dst, map, full_b(s), kb * KB, r[0], r[1], r[2], r[3]);
+          else
+            tma_load_2d(dst, map, full_b(s), kb * KB, r[0]);
+        }
       }
     }
     for (int j = max(0, it - STAGES); j < it; ++j)
       mbar_wait(full_b(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
-  } else {
-    // ------------------------------------------------ products, sums and stores
-    const int cg = warp & 3, kh = warp >> 2;
-    const int bi = lane >> 3, br = lane & 7, g = lane >> 2, q = lane & 3;
-    int it = 0, uses = 0;
+  } else if (warp == 2) {
+    // ------------------------------------------------ issues the products
+    if (lane == 0) {
+      int it = 0, used[2] = {0, 0};  // accumulators so far in each set's ring
+      bool ok = true;
+      for (int qi = 0; ok; ++qi) {
+        const int u = take(qi);
+        if (u == -2) break;
+        mbar_arrive(q_empty(qi % kQueue));
+        if (u < 0) break;
+        const Unit un = unit_at(a, tb, work, u);
+        if (un.kind == 2) continue;
+        const int set = qi & 1;
+        int acc = used[set];
+        const int n = columns_of(un), end = acc + slots_of(un);
+        const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
+        bool fresh = true;  // the next product starts an accumulator
+        for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
+          const int s = it % STAGES, ph = (it / STAGES) & 1;
+          if (!mbar_wait(full_w(s), ph, kTimeoutNs) || !mbar_wait(full_b(s), ph, kTimeoutNs)) {
+            give_up();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t wt = base + s * kTileBytes, bt = rows_at + s * C::B_BYTES;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {  // 16 (bf16) or 32 (e4m3) rows of weights
+            if (acc >= end) break;          // e4m3: past the last 64 rows of h
+            const int slot = set * kRing + acc % kRing;
+            if (fresh && !mbar_wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1, kTimeoutNs)) {
+              give_up();
+              ok = false;
+              break;
+            }
+            if (fresh) tc_fence_after();
+            const uint32_t d = tmem + slot * 64;
+            if constexpr (FP8)
+              umma_e4m3(d, sdesc_sw64(wt + ks * 2048, kTileBytes / 2, 512),
+                        sdesc_sw128(bt + ks * 32, 16, 1024), idesc, fresh ? 0u : 1u);
+            else
+              umma_bf16(d, sdesc_sw128(wt + ks * 2048, kTileBytes / 2, 1024),
+                        sdesc_sw128(bt + ks * 32, 16, 1024), idesc, fresh ? 0u : 1u);
+            fresh = false;
+            // e4m3: an accumulator ends with its block of one scale
+            if (FP8 && (ks == 3 || (ks == 1 && un.kind == 1))) {
+              umma_commit(acc_full(slot));
+              ++acc;
+              fresh = true;
+            }
+          }
+          if (!ok) break;
+          umma_commit(empty(s));
+        }
+        if (!FP8 && ok) {
+          umma_commit(acc_full(set * kRing + acc % kRing));
+          ++acc;
+        }
+        used[set] = acc;
+      }
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0, kTimeoutNs);
+    }
+  } else if (warp >= kFirstEpilogue) {
+    // ------------------------------------------------ accumulators to h, partial rows and y
+    const int set = (warp - kFirstEpilogue) >> 2, q = warp & 3;  // q: the warp's quarter of the lanes
+    const int col = q * 32 + lane;  // of the unit's 128
+    float* const ex = exchange + set * kChunk * kCols;
+    int acc = 0, uses = 0;
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
-      const int qs = qi % kQueue;
-      if (!mbar_wait(q_full(qs), (qi / kQueue) & 1, kTimeoutNs)) {
-        if (lane == 0) give_up();
-        break;
-      }
-      const int u = queue[qs];
+      const int u = take(qi);
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_empty(qs));
+      if (u == -2) break;
+      if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
       if (u < 0) break;
       const Unit un = unit_at(a, tb, work, u);
+      if ((qi & 1) != set) continue;  // the sets take units in turn, each with its own accumulators
       if (un.kind == 2) {
         const int target = 4 * (work.nc * work.split + work.ncs * work.splits);
         int there = 1;
@@ -558,13 +715,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           if (lane == 0) give_up();
           break;
         }
-        const int t = un.row0 + warp, c = un.tile * kCols + lane * 4;
-        if (warp < un.n && c < a.H) {
+        const int c = un.tile * kCols + lane * 4;
+        for (int i = q; i < un.n; i += 4) {
+          const int t = un.row0 + i;
+          if (c >= a.H) continue;
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
           auto add = [&](const float* p) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
           };
+#pragma unroll 8
           for (int k = 0; k < a.K; ++k)
             for (int p = 0; p < work.split; ++p)
               add(a.o + ((int64_t)p * a.S + tb.row[t * a.K + k]) * a.H + c);
@@ -575,225 +735,170 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         continue;
       }
-      const int nt = (un.n + 7) >> 3;
-      const int I = un.shared ? a.Is : a.I, width = un.kind == 0 ? a.H : I;
-      float acc[2][4][4];
+      const int nslots = slots_of(un);
+      const int n8 = (un.n + 7) & ~7;
+      const int I = un.shared ? a.Is : a.I, nt64 = (I + 63) / 64;
+      float v[kChunk];
+      if constexpr (!FP8) {
+        const int s = set * kRing + acc % kRing;
+        if (!mbar_wait(acc_full(s), (acc / kRing) & 1, kTimeoutNs)) {
+          if (lane == 0) give_up();
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int j = 0; j < kChunk / 8; ++j) {
+          if (8 * j >= n8) continue;
+          uint32_t r[8];
+          tmem_ld_32x8(d + 8 * j, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int i = 0; i < 8; ++i) v[8 * j + i] = __uint_as_float(r[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(s));
+        ++acc;
+      } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
-      // e4m3: the scales of this warp's two column groups, one k block per lane
-      const float *sc0 = nullptr, *sc1 = nullptr;
-      int sc_stride = 0;
-      float scale0 = 0.f, scale1 = 0.f;
-      if constexpr (FP8) {
+        for (int i = 0; i < kChunk; ++i) v[i] = 0.f;
+        // this column's weight scales, one per 128 rows; GEMM2: the rows' scales, one per 64
+        const int c = un.kind == 0 ? (q < 2 ? un.tile * 64 + col : I + un.tile * 64 + col - 64)
+                                   : un.tile * kCols + col;
+        const int cols = un.kind == 0 ? 2 * I : a.H, nb = (cols + 127) / 128;
         const float* sc = un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
                                        : (un.shared ? a.s_down_scale : a.down_scale);
-        const int cols = un.kind == 0 ? 2 * I : a.H, nb = (cols + 127) / 128;
-        sc_stride = nb;
-        sc += (int64_t)un.e * ((width + 127) / 128) * nb;
-        const int c0 = un.kind == 0 ? un.tile * 64 + cg * 16 : un.tile * kCols + cg * 32;
-        const int c1 = un.kind == 0 ? I + c0 : c0 + 16;
-        sc0 = sc + min(c0 / 128, nb - 1);
-        sc1 = sc + min(c1 / 128, nb - 1);
+        const int row_blocks = ((un.kind == 0 ? a.H : I) + 127) / 128;
+        sc += (int64_t)un.e * row_blocks * nb + min(c / 128, nb - 1);
+        const float* hs = (un.shared ? a.s_h_scale : a.h_scale) +
+                          (int64_t)(un.row0 + min(lane, un.n - 1)) * nt64 + 2 * un.kb0;
+        const int per = un.kind == 0 ? 0 : 1;  // slots per 128 rows: 1 or 2
+        if (un.kind == 1) {  // the scales of h come with its rows
+          const int target = 4 * (un.shared ? work.nt1s : work.nt1);
+          int there = 1;
+          if (lane == 0) there = wait_counter(a.ready1 + un.ready, target, kTimeoutNs);
+          if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
+            if (lane == 0) give_up();
+            break;
+          }
+        }
+        float ws_next = __ldg(sc + (int64_t)un.kb0 * nb);
+        float hs_next = un.kind == 1 ? __ldcg(hs) : 1.f;
+        for (int i = 0; i < nslots; ++i, ++acc) {
+          const float ws = ws_next, hscale = hs_next;
+          if (i + 1 < nslots) {
+            ws_next = __ldg(sc + (int64_t)(un.kb0 + ((i + 1) >> per)) * nb);
+            if (un.kind == 1) hs_next = __ldcg(hs + i + 1);
+          }
+          const int s = set * kRing + acc % kRing;
+          if (!mbar_wait(acc_full(s), (acc / kRing) & 1, kTimeoutNs)) {
+            if (lane == 0) give_up();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+          for (int j = 0; j < kChunk / 8; ++j) {
+            if (8 * j >= n8) continue;
+            uint32_t hi[8], lo[8];
+            tmem_ld_32x8(d + 8 * j, hi);
+            tmem_ld_32x8(d + n8 + 8 * j, lo);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float p = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k]));
+              const float f = un.kind == 1 ? ws * __shfl_sync(0xFFFFFFFFu, hscale, 8 * j + k) : ws;
+              v[8 * j + k] = fmaf(f, p, v[8 * j + k]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty(s));
+        }
+        if (!ok) break;
+        if (un.kind == 0) {  // the tokens' scales
+          const float xs = lane < un.n
+                               ? a.x_scale[un.shared ? un.row0 + lane : tb.tok[un.row0 + lane]] : 0.f;
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i)
+            if (i < n8) v[i] *= __shfl_sync(0xFFFFFFFFu, xs, i);
+        }
       }
-      for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
-        const int s = it % STAGES, ph = (it / STAGES) & 1;
-        if constexpr (FP8) {
-          if (((kb - un.kb0) & 31) == 0 && kb + lane < un.kb1) {
-            scale0 = sc0[(int64_t)(kb + lane) * sc_stride];
-            scale1 = sc1[(int64_t)(kb + lane) * sc_stride];
-          }
-        }
-        if (!mbar_wait(full_w(s), ph, kTimeoutNs) || !mbar_wait(full_b(s), ph, kTimeoutNs)) {
-          if (lane == 0) give_up();
-          ok = false;
-          break;
-        }
-        const uint32_t wt = base + s * kTileBytes, bt = rows_at + s * C::B_BYTES;
-        const int kvalid = min(KB, width - kb * KB);  // a multiple of 8
-        if constexpr (!FP8) {
-          const int k0 = kh * 32;
-          if (k0 < kvalid) {
-            uint32_t b[4][4];
+      if (un.kind == 1) {
+        float* o = un.shared ? a.s_o + (int64_t)un.split * a.T * a.H
+                             : a.o + (int64_t)un.split * a.S * a.H;
+        const int c = un.tile * kCols + col;
+        if (c < a.H) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j >= nt) continue;
-              ldsm4(bt + (j * 8 + br) * PITCH + (k0 + bi * 8) * 2, b[j]);
-              // past the rows' end shared memory holds anything; the weights there are zero
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (k0 + 8 * i >= kvalid) b[j][i] = 0;
-            }
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              const int kr = k0 + ks * 16 + (bi >> 1) * 8 + br;
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                const int box = un.kind == 0 ? (bi & 1) : (cg >> 1);
-                const int c16 = un.kind == 0 ? cg * 2 + m : (cg & 1) * 4 + m * 2 + (bi & 1);
-                uint32_t r[4];
-                ldsm4_trans(wt + box * (kTileBytes / 2) + kr * 128 + ((c16 ^ (kr & 7)) << 4), r);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (j < nt) mma16816(acc[m][j], r[0], r[1], r[2], r[3], b[j][2 * ks], b[j][2 * ks + 1]);
-              }
-            }
-          }
-        } else {
-          float part[2][4][4];
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) part[m][j][i] = 0.f;
-#pragma unroll
-          for (int k32 = 0; k32 < 2; ++k32) {
-            const int k0 = kh * 64 + k32 * 32;
-            if (k0 >= kvalid) continue;
-            uint32_t b[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j >= nt) continue;
-              ldsm4(bt + (j * 8 + br) * PITCH + (k0 + bi * 8) * 2, b[j]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (k0 + 8 * i >= kvalid) b[j][i] = 0;
-            }
-            const int kr = k0 + bi * 8 + br;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              uint32_t r[4];
-              if (un.kind == 0)
-                ldsm4_trans(wt + m * (kTileBytes / 2) + kr * 64 + ((cg ^ ((kr >> 1) & 3)) << 4), r);
-              else
-                ldsm4_trans(wt + kr * 128 + (((cg * 2 + m) ^ (kr & 7)) << 4), r);
-              // r[i]: bytes (column 2g, 2g + 1) at k = 8 i + 2q, then at the next k
-              uint32_t lo[4], hi[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t v = __byte_perm(r[i], 0, 0x3120);
-                lo[i] = e4m3x2_to_bf16x2(v);
-                hi[i] = e4m3x2_to_bf16x2(v >> 16);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (j >= nt) continue;
-                mma16816(part[m][j], lo[0], hi[0], lo[1], hi[1], b[j][0], b[j][1]);
-                mma16816(part[m][j], lo[2], hi[2], lo[3], hi[3], b[j][2], b[j][3]);
-              }
-            }
-          }
-          const float f0 = __shfl_sync(0xFFFFFFFFu, scale0, (kb - un.kb0) & 31);
-          const float f1 = __shfl_sync(0xFFFFFFFFu, scale1, (kb - un.kb0) & 31);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              acc[0][j][i] = fmaf(f0, part[0][j][i], acc[0][j][i]);
-              acc[1][j][i] = fmaf(f1, part[1][j][i], acc[1][j][i]);
-            }
+          for (int i = 0; i < kChunk; ++i)
+            if (i < un.n) o[(int64_t)(un.row0 + i) * a.H + c] = v[i];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty(s));
-      }
-      if (!ok) break;
-      // the two k halves of a column group meet: the second hands its sums over
-      float* const mine = halves + cg * 32 * 32 + lane;
-      if (kh == 1) {
-        if (!mbar_wait(half_empty(cg), (uses & 1) ^ 1, kTimeoutNs)) {
-          if (lane == 0) give_up();
-          break;
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mine[((m * 4 + j) * 4 + i) * 32] = acc[m][j][i];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(half_full(cg));
-        ++uses;
+        if (lane == 0) red_add_release_gpu(a.ready2 + un.tile, 1);
         continue;
       }
-      if (!mbar_wait(half_full(cg), uses & 1, kTimeoutNs)) {
+      // GEMM1: columns 0..63 are gate, 64..127 up of the same 64; the set's warps meet in shared
+      // memory and take the rows in turn, two columns per lane
+      if (!mbar_wait(x_empty(set), (uses & 1) ^ 1, kTimeoutNs)) {
         if (lane == 0) give_up();
         break;
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][j][i] += mine[((m * 4 + j) * 4 + i) * 32];
+      for (int i = 0; i < kChunk; ++i)
+        if (i < un.n) ex[i * kCols + col] = v[i];
       __syncwarp();
-      if (lane == 0) mbar_arrive(half_empty(cg));
-      ++uses;
-      if (un.kind == 0) {
-        __nv_bfloat16* h = (un.shared ? a.s_h : a.h);
-        const int c0 = un.tile * 64 + cg * 16;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= nt) continue;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int n = j * 8 + 2 * q + i;
-            if (n >= un.n) continue;
-            const int row = un.row0 + n;
-            const float w = un.shared ? 1.f : tb.w[row];
-            auto swiglu = [&](float gate, float up) { return w * (gate * sigmoidf_(gate) * up); };
-            __nv_bfloat16* dst = h + (int64_t)row * I;
-            if constexpr (FP8) {
-              const int c = c0 + 2 * g;
-              if (c < I)
-                *reinterpret_cast<uint32_t*>(dst + c) =
-                    pack_bf16(swiglu(acc[0][j][i], acc[1][j][i]),
-                              swiglu(acc[0][j][2 + i], acc[1][j][2 + i]));
-            } else {
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                const int c = c0 + 8 * m + g;
-                if (c < I) dst[c] = __float2bfloat16_rn(swiglu(acc[m][j][i], acc[m][j][2 + i]));
-              }
-            }
-          }
-        }
-        fence_proxy_async_global();
-        __syncwarp();
-        if (lane == 0) red_add_release_gpu(a.ready1 + un.ready, 1);
-      } else {
-        float* o = un.shared ? a.s_o + (int64_t)un.split * a.T * a.H
-                             : a.o + (int64_t)un.split * a.S * a.H;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= nt) continue;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int n = j * 8 + 2 * q + i;
-            if (n >= un.n) continue;
-            float* dst = o + (int64_t)(un.row0 + n) * a.H;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const int c = un.tile * kCols + cg * 32 + m * 16 + (FP8 ? 2 * g : g);
-              if constexpr (FP8) {
-                if (c < a.H)
-                  *reinterpret_cast<float2*>(dst + c) = make_float2(acc[m][j][i], acc[m][j][2 + i]);
-              } else {
-                if (c < a.H) dst[c] = acc[m][j][i];
-                if (c + 8 < a.H) dst[c + 8] = acc[m][j][2 + i];
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) red_add_release_gpu(a.ready2 + un.tile, 1);
+      if (lane == 0) mbar_arrive(x_full(set));
+      if (!mbar_wait(x_full(set), uses & 1, kTimeoutNs)) {
+        if (lane == 0) give_up();
+        break;
       }
+      const int c = un.tile * 64 + 2 * lane;
+      for (int i = q; i < un.n; i += 4) {
+        const int row = un.row0 + i;
+        const float w = un.shared ? 1.f : tb.w[row];
+        const float2 g = *reinterpret_cast<const float2*>(ex + i * kCols + 2 * lane);
+        const float2 l = *reinterpret_cast<const float2*>(ex + i * kCols + 64 + 2 * lane);
+        float h0 = w * (g.x * sigmoidf_(g.x) * l.x), h1 = w * (g.y * sigmoidf_(g.y) * l.y);
+        if constexpr (FP8) {
+          if (c >= I) h0 = h1 = 0.f;
+          float m = fmaxf(fabsf(h0), fabsf(h1));
+          if (h0 != h0 || h1 != h1) m = INFINITY;
+          float inv;
+          const float s = split_scale(warp_max(m), &inv);
+          uint8_t hi0, lo0, hi1, lo1;
+          split_e4m3(h0 * s, hi0, lo0);
+          split_e4m3(h1 * s, hi1, lo1);
+          uint8_t* dst = static_cast<uint8_t*>(un.shared ? a.s_h : a.h) + (int64_t)row * I + c;
+          if (c < I) {
+            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(hi0 | hi1 << 8);
+            *reinterpret_cast<uint16_t*>(dst + (int64_t)(un.shared ? a.T : a.S) * I) =
+                (uint16_t)(lo0 | lo1 << 8);
+          }
+          if (lane == 0)
+            (un.shared ? a.s_h_scale : a.h_scale)[(int64_t)row * nt64 + un.tile] = inv;
+        } else {
+          if (c < I)
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(un.shared ? a.s_h : a.h) +
+                                         (int64_t)row * I + c) = pack_bf16(h0, h1);
+        }
+      }
+      fence_proxy_async_global();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(x_empty(set));
+        red_add_release_gpu(a.ready1 + un.ready, 1);
+      }
+      ++uses;
     }
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kSlots * 64);
   }
 }
 
@@ -851,7 +956,7 @@ inline bool aligned_to(const void* p, size_t a) {
 }
 
 struct Layout {
-  size_t off_ready2, off_logits, off_h, off_sh, off_o, off_so, total;
+  size_t off_ready2, off_logits, off_x8, off_xs, off_h, off_sh, off_hs, off_shs, off_o, off_so, total;
   int zero_words;
 };
 
@@ -885,6 +990,11 @@ Layout layout(const mm_decode_desc& d) {
   l.off_ready2 = take((size_t)((m.H + kCols - 1) / kCols) * 4);
   l.zero_words = (int)(off / 4);
   l.off_logits = take((size_t)(m.T * m.E) * 4);
+  const bool fp8 = d.weight_type == MM_E4M3;
+  l.off_x8 = take(fp8 ? (size_t)m.T * m.H * 2 : 0);
+  l.off_xs = take(fp8 ? (size_t)m.T * 4 : 0);
+  l.off_hs = take(fp8 ? S * ((m.I + 63) / 64) * 4 : 0);
+  l.off_shs = take(fp8 ? (size_t)m.T * ((d.shared_I + 63) / 64) * 4 : 0);
   l.off_h = take(S * m.I * 2);
   l.off_sh = take((size_t)m.T * d.shared_I * 2);
   l.off_o = take((size_t)kMaxSplit * S * m.H * 4);
@@ -893,20 +1003,31 @@ Layout layout(const mm_decode_desc& d) {
   return l;
 }
 
-bool weight_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t n, bool fp8,
-                uint32_t box_cols, uint32_t box_rows) {
+bool weight_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t n,
+                bool fp8) {
   const uint64_t es = fp8 ? 1 : 2;
   const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)n};
   const uint64_t strides[2] = {(uint64_t)cols * es, (uint64_t)cols * rows * es};
-  const uint32_t box[3] = {box_cols, box_rows, 1};
+  const uint32_t box[3] = {64, fp8 ? 128u : 64u, 1};
   return make_map(m, base, 3, dims, strides, box,
                   fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                  box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                  fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Rows of 128-byte boxes: bf16 or e4m3 [rows, cols].
+bool row_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, bool fp8,
+             uint32_t box_rows) {
+  const uint64_t es = fp8 ? 1 : 2;
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t strides[1] = {(uint64_t)cols * es};
+  const uint32_t box[2] = {(uint32_t)(128 / es), box_rows};
+  return make_map(m, base, 2, dims, strides, box,
+                  fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
 template <bool FP8>
 constexpr size_t dynamic_smem() {
-  return 1024 + Cfg<FP8>::STAGES * (kTileBytes + Cfg<FP8>::B_BYTES) + 4 * 32 * 32 * 4;
+  return 1024 + Cfg<FP8>::STAGES * (kTileBytes + Cfg<FP8>::B_BYTES) + 2 * kChunk * kCols * 4;
 }
 
 template <bool FP8>
@@ -983,14 +1104,17 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   la.H = (int)m.H;
   la.E = (int)m.E;
   DecodeArgs a{};
-  const uint32_t rows = fp8 ? 128 : 64, down_cols = fp8 ? 128 : 64;
-  bool maps = weight_map(&a.up, w->up, 2 * m.I, m.H, m.E, fp8, 64, rows) &&
-              weight_map(&a.down, w->down, m.H, m.I, m.E, fp8, down_cols, rows);
+  char* const x_rows = fp8 ? ws + l.off_x8 : static_cast<char*>(const_cast<void*>(x));
+  const int64_t parts = fp8 ? 2 : 1;  // hi and lo
+  bool maps = weight_map(&a.up, w->up, 2 * m.I, m.H, m.E, fp8) &&
+              weight_map(&a.down, w->down, m.H, m.I, m.E, fp8) &&
+              row_map(&a.x, x_rows, m.H, parts * m.T, fp8, 1) &&
+              row_map(&a.h_rows, ws + l.off_h, m.I, parts * m.T * m.K, fp8, 8);
   if (shared)
-    maps = maps && weight_map(&a.s_up, w->shared_up, 2 * d->shared_I, m.H, 1, fp8, 64, rows) &&
-           weight_map(&a.s_down, w->shared_down, m.H, d->shared_I, 1, fp8, down_cols, rows);
+    maps = maps && weight_map(&a.s_up, w->shared_up, 2 * d->shared_I, m.H, 1, fp8) &&
+           weight_map(&a.s_down, w->shared_down, m.H, d->shared_I, 1, fp8) &&
+           row_map(&a.s_h_rows, ws + l.off_sh, d->shared_I, parts * m.T, fp8, 8);
   if (!maps) return cuda_fail(cudaErrorInvalidValue, "decode tensor maps");
-  a.x = la.x;
   a.up_scale = w->up_scale;
   a.down_scale = w->down_scale;
   a.s_up_scale = w->shared_up_scale;
@@ -1003,8 +1127,11 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   a.hdr = la.zero;
   a.ready1 = la.zero + W_READY1;
   a.ready2 = reinterpret_cast<int*>(ws + l.off_ready2);
-  a.h = reinterpret_cast<__nv_bfloat16*>(ws + l.off_h);
-  a.s_h = reinterpret_cast<__nv_bfloat16*>(ws + l.off_sh);
+  a.h = ws + l.off_h;
+  a.s_h = ws + l.off_sh;
+  a.x_scale = reinterpret_cast<float*>(ws + l.off_xs);
+  a.h_scale = reinterpret_cast<float*>(ws + l.off_hs);
+  a.s_h_scale = reinterpret_cast<float*>(ws + l.off_shs);
   a.o = reinterpret_cast<float*>(ws + l.off_o);
   a.s_o = reinterpret_cast<float*>(ws + l.off_so);
   a.T = la.T;
@@ -1018,7 +1145,12 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   a.normalize = d->normalize;
   a.scale = d->scale;
   a.route = w->router != nullptr;
-  const dim3 grid = a.route ? dim3((unsigned)((a.E + 3) / 4), (unsigned)((a.T + 3) / 4)) : dim3(1);
+  la.logit_blocks = a.route ? (a.E + 3) / 4 * ((a.T + 3) / 4) : 0;
+  if (fp8) {
+    la.x8 = reinterpret_cast<uint8_t*>(ws + l.off_x8);
+    la.x_scale = reinterpret_cast<float*>(ws + l.off_xs);
+  }
+  const dim3 grid((unsigned)std::max(1, la.logit_blocks + (fp8 ? a.T : 0)));
   if (d->router_type == MM_BF16)
     MM_TRY(launch_pdl(k_logits<__nv_bfloat16>, grid, dim3(256), 0, st, la));
   else
