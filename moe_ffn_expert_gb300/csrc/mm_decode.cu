@@ -114,6 +114,9 @@ struct Work {
   int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, t2s, total;
 };
 
+// A value that all lanes share, in the form the compiler knows to be shared.
+__device__ __forceinline__ int uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
+
 // x = (hi + lo / 16) / s for |x s| < 256.
 __device__ __forceinline__ void split_e4m3(float xs, uint8_t& hi, uint8_t& lo) {
   hi = __nv_cvt_float_to_fp8(xs, __NV_SATFINITE, __NV_E4M3);
@@ -238,13 +241,13 @@ __device__ void select_row(const DecodeArgs& a, Building& bd, const float* row, 
   float z[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e = lane + 32 * j;
+    const int e = lane * NV + j;
     z[j] = e < a.E ? row[e] : 0.f;
   }
   float m = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e = lane + 32 * j;
+    const int e = lane * NV + j;
     key[j] = 0;
     if (e >= a.E) continue;
     float k = z[j];
@@ -257,7 +260,7 @@ __device__ void select_row(const DecodeArgs& a, Building& bd, const float* row, 
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (lane + 32 * j < a.E) sum += expf(z[j] - m);
+      if (lane * NV + j < a.E) sum += expf(z[j] - m);
     sum = warp_sum(sum);
   }
   const int id = select_topk<NV>(key, a.K, lane);
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   constexpr int KB = C::KB, STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
-  __shared__ uint64_t bars[3 * STAGES + 2 * kQueue + 2 * kSlots + 4 + 1];
+  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 2 * kSlots + 4 + 1];
   __shared__ int queue[kQueue];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -464,20 +467,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   const uint32_t rows_at = base + STAGES * kTileBytes;
   float* const exchange = reinterpret_cast<float*>(aligned + STAGES * (kTileBytes + C::B_BYTES));
   const uint32_t bar0 = smem_u32(bars);
-  auto full_w = [&](int s) { return bar0 + 8u * s; };
-  auto full_b = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
-  auto q_full = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };
-  auto q_empty = [&](int s) { return bar0 + 8u * (3 * STAGES + kQueue + s); };
-  auto acc_full = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + s); };
-  auto acc_empty = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + kSlots + s); };
-  auto x_full = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + 2 * kSlots + s); };
-  auto x_empty = [&](int s) { return bar0 + 8u * (3 * STAGES + 2 * kQueue + 2 * kSlots + 2 + s); };
-  const uint32_t mma_done = bar0 + 8u * (3 * STAGES + 2 * kQueue + 2 * kSlots + 4);
+  constexpr int Q = 2 * STAGES, ACC = Q + 2 * kQueue, X = ACC + 2 * kSlots;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto q_full = [&](int s) { return bar0 + 8u * (Q + s); };
+  auto q_empty = [&](int s) { return bar0 + 8u * (Q + kQueue + s); };
+  auto acc_full = [&](int s) { return bar0 + 8u * (ACC + s); };
+  auto acc_empty = [&](int s) { return bar0 + 8u * (ACC + kSlots + s); };
+  auto x_full = [&](int s) { return bar0 + 8u * (X + s); };
+  auto x_empty = [&](int s) { return bar0 + 8u * (X + 2 + s); };
+  const uint32_t mma_done = bar0 + 8u * (X + 4);
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_w(s), 1);
-      mbar_init(full_b(s), 1);
+      mbar_init(full(s), 2);  // the weights' and the rows' producers
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < kQueue; ++s) {
@@ -534,44 +536,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
 
   if (warp == 0) {
     // ------------------------------------------------ claims units and loads their weights
-    if (lane == 0) {
-      int u = blockIdx.x, it = 0;
-      bool ok = true;
-      for (int qi = 0; ok; ++qi) {
-        const int qs = qi % kQueue;
-        if (!mbar_wait(q_empty(qs), ((qi / kQueue) & 1) ^ 1, kTimeoutNs)) {
-          give_up();
-          break;
-        }
+    int u = blockIdx.x, it = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int qi = 0; ok; ++qi) {
+      const int qs = qi % kQueue;
+      if (!mbar_wait(q_empty(qs), ((qi / kQueue) & 1) ^ 1, kTimeoutNs)) {
+        if (lane == 0) give_up();
+        break;
+      }
+      if (lane == 0) {
         queue[qs] = u < work.total ? u : -1;
         mbar_arrive(q_full(qs));
-        if (u >= work.total) break;
-        const Unit un = unit_at(a, tb, work, u);
-        u = gridDim.x + atomicAdd(a.hdr + W_NEXT, 1);
-        const CUtensorMap* map = un.kind == 0 ? (un.shared ? &a.s_up : &a.up)
-                                              : (un.shared ? &a.s_down : &a.down);
-        const int c0 = un.tile * (un.kind == 0 ? 64 : kCols);
-        const int c1 = un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + 64;
-        for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, kTimeoutNs)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          const uint32_t dst = base + s * kTileBytes;
-          mbar_arrive_expect_tx(full_w(s), kTileBytes);
-          tma_load_3d(dst, map, full_w(s), c0, kb * KB, un.e);
-          tma_load_3d(dst + kTileBytes / 2, map, full_w(s), c1, kb * KB, un.e);
-        }
       }
-      // no CTA leaves with a copy into its shared memory in flight
-      for (int j = max(0, it - STAGES); j < it; ++j)
-        mbar_wait(full_w(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
+      if (u >= work.total) break;
+      const Unit un = unit_at(a, tb, work, u);
+      int next = 0;
+      if (lane == 0) next = atomicAdd(a.hdr + W_NEXT, 1);  // needed when this unit is issued
+      const CUtensorMap* map = un.kind == 0 ? (un.shared ? &a.s_up : &a.up)
+                                            : (un.shared ? &a.s_down : &a.down);
+      const int e = uniform(un.e), kb1 = uniform(un.kb1);
+      const int c0 = uniform(un.tile * (un.kind == 0 ? 64 : kCols));
+      const int c1 = uniform(un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + 64);
+      for (int kb = uniform(un.kb0); kb < kb1; ++kb, ++it) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty(s), ph ^ 1, kTimeoutNs))) {
+          if (lane == 0) give_up();
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t dst = base + s * kTileBytes, bar = full(s);
+          mbar_arrive_expect_tx(bar, kTileBytes);
+          tma_load_3d(dst, map, bar, c0, kb * KB, e);
+          tma_load_3d(dst + kTileBytes / 2, map, bar, c1, kb * KB, e);
+        }
+        __syncwarp();
+        if (++s == STAGES) s = 0, ph ^= 1;
+      }
+      u = gridDim.x + __shfl_sync(0xFFFFFFFFu, next, 0);
     }
+    // no CTA leaves with a copy into its shared memory in flight
+    for (int j = max(0, it - STAGES); j < it; ++j)
+      mbar_wait(full(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
   } else if (warp == 1) {
     // ------------------------------------------------ loads the rows
-    int it = 0;
+    int it = 0, s = 0;
+    uint32_t ph = 0;
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
       const int u = take(qi);
@@ -610,88 +620,126 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const uint32_t bytes = (FP8 ? 2 : 1) * groups * (un.kind == 0 ? 512 : 1024);
       const uint32_t to = (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
-        const int s = it % STAGES;
-        if (!mbar_wait(empty(s), ((it / STAGES) & 1) ^ 1, kTimeoutNs)) {
+        if (!mbar_wait(empty(s), ph ^ 1, kTimeoutNs)) {
           if (lane == 0) give_up();
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(full_b(s), bytes);
+        if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
         __syncwarp();
         if (loads) {
           const uint32_t dst = rows_at + s * C::B_BYTES + to;
           if (un.kind == 0)
-            tma_gather4(dst, map, full_b(s), kb * KB, r[0], r[1], r[2], r[3]);
+            tma_gather4(dst, map, full(s), kb * KB, r[0], r[1], r[2], r[3]);
           else
-            tma_load_2d(dst, map, full_b(s), kb * KB, r[0]);
+            tma_load_2d(dst, map, full(s), kb * KB, r[0]);
         }
+        __syncwarp();
+        if (++s == STAGES) s = 0, ph ^= 1;
       }
     }
     for (int j = max(0, it - STAGES); j < it; ++j)
-      mbar_wait(full_b(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
+      mbar_wait(full(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
   } else if (warp == 2) {
     // ------------------------------------------------ issues the products
-    if (lane == 0) {
-      int it = 0, used[2] = {0, 0};  // accumulators so far in each set's ring
-      bool ok = true;
-      for (int qi = 0; ok; ++qi) {
-        const int u = take(qi);
-        if (u == -2) break;
-        mbar_arrive(q_empty(qi % kQueue));
-        if (u < 0) break;
-        const Unit un = unit_at(a, tb, work, u);
-        if (un.kind == 2) continue;
-        const int set = qi & 1;
-        int acc = used[set];
-        const int n = columns_of(un), end = acc + slots_of(un);
-        const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
-        bool fresh = true;  // the next product starts an accumulator
-        for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
-          const int s = it % STAGES, ph = (it / STAGES) & 1;
-          if (!mbar_wait(full_w(s), ph, kTimeoutNs) || !mbar_wait(full_b(s), ph, kTimeoutNs)) {
-            give_up();
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t wt = base + s * kTileBytes, bt = rows_at + s * C::B_BYTES;
+    // The warp stays in step, an elected lane issues, and what an issue takes is known to be the
+    // same in all lanes: operands that are not pass through a move to a uniform register each, and
+    // with descriptors built per product in a branch of one lane an issue took 165 cycles instead
+    // of 41, longer than its weights take to arrive.
+    const uint64_t wdesc = FP8 ? sdesc_sw64(base, kTileBytes / 2, 512)
+                               : sdesc_sw128(base, kTileBytes / 2, 1024);
+    const uint64_t bdesc = sdesc_sw128(rows_at, 16, 1024);
+    int s = 0, used[2] = {0, 0};  // stage; accumulators so far in each set's ring
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int qi = 0; ok; ++qi) {
+      const int u = uniform(take(qi));
+      if (u == -2) break;
+      if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
+      if (u < 0) break;
+      const Unit un = unit_at(a, tb, work, u);
+      if (u >= work.t2s) continue;  // combine
+      const int set = qi & 1, blocks = uniform(un.kb1 - un.kb0), slots = uniform(slots_of(un));
+      const uint32_t n = (uint32_t)uniform(columns_of(un));
+      const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
+      int acc = set ? used[1] : used[0];
+      const int end = acc + slots;
+      auto wait = [&](uint32_t bar, uint32_t phase) {
+        if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, kTimeoutNs))) return;
+        if (lane == 0) give_up();
+        ok = false;
+      };
+      // products ks0 .. ks1 - 1 of stage s into the accumulator at d
+      auto products = [&](uint32_t d, int ks0, int ks1, bool fresh) {
+        const uint64_t wd = wdesc + (uint32_t)s * (kTileBytes / 16);
+        const uint64_t bd = bdesc + (uint32_t)s * (C::B_BYTES / 16);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {  // 16 (bf16) or 32 (e4m3) rows of weights
-            if (acc >= end) break;          // e4m3: past the last 64 rows of h
-            const int slot = set * kRing + acc % kRing;
-            if (fresh && !mbar_wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1, kTimeoutNs)) {
-              give_up();
-              ok = false;
-              break;
-            }
-            if (fresh) tc_fence_after();
-            const uint32_t d = tmem + slot * 64;
-            if constexpr (FP8)
-              umma_e4m3(d, sdesc_sw64(wt + ks * 2048, kTileBytes / 2, 512),
-                        sdesc_sw128(bt + ks * 32, 16, 1024), idesc, fresh ? 0u : 1u);
-            else
-              umma_bf16(d, sdesc_sw128(wt + ks * 2048, kTileBytes / 2, 1024),
-                        sdesc_sw128(bt + ks * 32, 16, 1024), idesc, fresh ? 0u : 1u);
-            fresh = false;
-            // e4m3: an accumulator ends with its block of one scale
-            if (FP8 && (ks == 3 || (ks == 1 && un.kind == 1))) {
-              umma_commit(acc_full(slot));
-              ++acc;
-              fresh = true;
-            }
-          }
+        for (int ks = 0; ks < 4; ++ks) {
+          if (ks < ks0 || ks >= ks1) continue;
+          const uint32_t accumulate = fresh && ks == ks0 ? 0u : 1u;
+          if constexpr (FP8)
+            umma_e4m3(d, wd + ks * (2048 / 16), bd + ks * 2, idesc, accumulate);
+          else
+            umma_bf16(d, wd + ks * (2048 / 16), bd + ks * 2, idesc, accumulate);
+        }
+      };
+      if constexpr (!FP8) {
+        const int slot = set * kRing + acc % kRing;
+        const uint32_t d = tmem + slot * 64;
+        wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1);
+        for (int i = 0; i < blocks && ok; ++i) {
+          wait(full(s), ph);
           if (!ok) break;
-          umma_commit(empty(s));
+          tc_fence_after();
+          if (elect_one()) {
+            products(d, 0, 4, i == 0);
+            umma_commit(empty(s));
+            if (i + 1 == blocks) umma_commit(acc_full(slot));
+          }
+          __syncwarp();
+          if (++s == STAGES) s = 0, ph ^= 1;
         }
-        if (!FP8 && ok) {
-          umma_commit(acc_full(set * kRing + acc % kRing));
+        ++acc;
+      } else {
+        // an accumulator per scale: 128 rows of up, 64 rows of down
+        const bool up = u < work.t1s;
+        for (int i = 0; i < blocks && ok; ++i) {
+          const int slot = set * kRing + acc % kRing;
+          wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1);
+          if (ok) wait(full(s), ph);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (up)
+              products(tmem + slot * 64, 0, 4, true);
+            else
+              products(tmem + slot * 64, 0, 2, true);
+            umma_commit(acc_full(slot));
+          }
+          __syncwarp();
           ++acc;
+          if (!up && acc < end) {  // (the last 128 rows of h may be 64)
+            const int slot2 = set * kRing + acc % kRing;
+            wait(acc_empty(slot2), ((acc / kRing) & 1) ^ 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              products(tmem + slot2 * 64, 2, 4, true);
+              umma_commit(acc_full(slot2));
+            }
+            __syncwarp();
+            ++acc;
+          }
+          if (elect_one()) umma_commit(empty(s));
+          __syncwarp();
+          if (++s == STAGES) s = 0, ph ^= 1;
         }
-        used[set] = acc;
       }
-      umma_commit(mma_done);
-      mbar_wait(mma_done, 0, kTimeoutNs);
+      if (set) used[1] = acc; else used[0] = acc;
     }
+    if (elect_one()) umma_commit(mma_done);
+    __syncwarp();
+    mbar_wait(mma_done, 0, kTimeoutNs);
   } else if (warp >= kFirstEpilogue) {
     // ------------------------------------------------ accumulators to h, partial rows and y
     const int set = (warp - kFirstEpilogue) >> 2, q = warp & 3;  // q: the warp's quarter of the lanes
@@ -763,17 +811,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       } else {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) v[i] = 0.f;
-        // this column's weight scales, one per 128 rows; GEMM2: the rows' scales, one per 64
-        const int c = un.kind == 0 ? (q < 2 ? un.tile * 64 + col : I + un.tile * 64 + col - 64)
-                                   : un.tile * kCols + col;
+        // This warp's columns lie in one or two blocks of 128 (its first and last column's); lane
+        // i holds their scales of the i-th of 32 row blocks, so that the accumulators of a unit
+        // never wait for a scale from HBM. GEMM2: lane n holds row n's scales of h, one per 64.
+        const int q0 = un.kind == 0 ? (q < 2 ? un.tile * 64 + q * 32 : I + un.tile * 64 + q * 32 - 64)
+                                    : un.tile * kCols + q * 32;
         const int cols = un.kind == 0 ? 2 * I : a.H, nb = (cols + 127) / 128;
         const float* sc = un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
                                        : (un.shared ? a.s_down_scale : a.down_scale);
         const int row_blocks = ((un.kind == 0 ? a.H : I) + 127) / 128;
-        sc += (int64_t)un.e * row_blocks * nb + min(c / 128, nb - 1);
+        sc += (int64_t)un.e * row_blocks * nb;
+        const int b0 = min(q0 / 128, nb - 1), b1 = min((q0 + 31) / 128, nb - 1);
+        const bool second = (q0 + lane) / 128 > q0 / 128;  // this lane's column is in the latter
         const float* hs = (un.shared ? a.s_h_scale : a.h_scale) +
                           (int64_t)(un.row0 + min(lane, un.n - 1)) * nt64 + 2 * un.kb0;
-        const int per = un.kind == 0 ? 0 : 1;  // slots per 128 rows: 1 or 2
+        const int per = un.kind == 0 ? 0 : 1;  // 2^per accumulators per 128 rows
+        float sc0 = 0.f, sc1 = 0.f, hv[4] = {1.f, 1.f, 1.f, 1.f};
+        auto load_scales = [&](int kb) {
+          if (kb + lane < un.kb1) {
+            sc0 = __ldg(sc + (int64_t)(kb + lane) * nb + b0);
+            sc1 = __ldg(sc + (int64_t)(kb + lane) * nb + b1);
+          }
+        };
+        load_scales(un.kb0);
         if (un.kind == 1) {  // the scales of h come with its rows
           const int target = 4 * (un.shared ? work.nt1s : work.nt1);
           int there = 1;
@@ -782,40 +842,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             if (lane == 0) give_up();
             break;
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < nslots) hv[i] = __ldcg(hs + i);
         }
-        float ws_next = __ldg(sc + (int64_t)un.kb0 * nb);
-        float hs_next = un.kind == 1 ? __ldcg(hs) : 1.f;
-        for (int i = 0; i < nslots; ++i, ++acc) {
-          const float ws = ws_next, hscale = hs_next;
-          if (i + 1 < nslots) {
-            ws_next = __ldg(sc + (int64_t)(un.kb0 + ((i + 1) >> per)) * nb);
-            if (un.kind == 1) hs_next = __ldcg(hs + i + 1);
-          }
-          const int s = set * kRing + acc % kRing;
-          if (!mbar_wait(acc_full(s), (acc / kRing) & 1, kTimeoutNs)) {
-            if (lane == 0) give_up();
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
+        for (int i0 = 0; i0 < nslots && ok; i0 += 4) {
 #pragma unroll
-          for (int j = 0; j < kChunk / 8; ++j) {
-            if (8 * j >= n8) continue;
-            uint32_t hi[8], lo[8];
-            tmem_ld_32x8(d + 8 * j, hi);
-            tmem_ld_32x8(d + n8 + 8 * j, lo);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float p = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k]));
-              const float f = un.kind == 1 ? ws * __shfl_sync(0xFFFFFFFFu, hscale, 8 * j + k) : ws;
-              v[8 * j + k] = fmaf(f, p, v[8 * j + k]);
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int i = i0 + k4;
+            if (i >= nslots) break;
+            const int blk = i >> per;
+            if (i == (blk << per) && blk > 0 && (blk & 31) == 0) load_scales(un.kb0 + blk);
+            const float w0 = __shfl_sync(0xFFFFFFFFu, sc0, blk & 31);
+            const float w1 = __shfl_sync(0xFFFFFFFFu, sc1, blk & 31);
+            const float ws = second ? w1 : w0, hscale = hv[k4];
+            if (un.kind == 1 && i + 4 < nslots) hv[k4] = __ldcg(hs + i + 4);
+            const int s = set * kRing + acc % kRing;
+            if (!mbar_wait(acc_full(s), (acc / kRing) & 1, kTimeoutNs)) {
+              if (lane == 0) give_up();
+              ok = false;
+              break;
             }
+            tc_fence_after();
+            const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+            for (int j = 0; j < kChunk / 8; ++j) {
+              if (8 * j >= n8) continue;
+              uint32_t hi[8], lo[8];
+              tmem_ld_32x8(d + 8 * j, hi);
+              tmem_ld_32x8(d + n8 + 8 * j, lo);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float p = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k]));
+                const float f = un.kind == 1 ? ws * __shfl_sync(0xFFFFFFFFu, hscale, 8 * j + k) : ws;
+                v[8 * j + k] = fmaf(f, p, v[8 * j + k]);
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty(s));
+            ++acc;
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty(s));
         }
         if (!ok) break;
         if (un.kind == 0) {  // the tokens' scales

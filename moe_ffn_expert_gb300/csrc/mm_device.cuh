@@ -148,6 +148,15 @@ __device__ __forceinline__ bool wait_counter(const int* p, int target, uint64_t 
   }
 }
 
+// True in one lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------ clusters of two CTAs
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

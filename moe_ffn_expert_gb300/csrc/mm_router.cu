@@ -48,7 +48,7 @@ __device__ __forceinline__ float row_max(const float (&z)[NV], int E, int lane) 
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (lane + 32 * j < E) m = fmaxf(m, z[j]);
+    if (lane * NV + j < E) m = fmaxf(m, z[j]);
   m = warp_max(m);
   return m == -INFINITY ? 0.f : m;  // a row of -inf: exp(z) is 0 without a shift
 }
@@ -69,12 +69,12 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
     uint32_t key[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = lane + 32 * j;
+      const int e = lane * NV + j;
       z[j] = e < E ? load_logit(row + e) : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = lane + 32 * j;
+      const int e = lane * NV + j;
       key[j] = 0;
       if (e >= E) continue;
       float k = z[j];
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
       float x[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        x[j] = lane + 32 * j >= E ? 0.f
+        x[j] = lane * NV + j >= E ? 0.f
                : a.score == MM_SCORE_SIGMOID ? sigmoid_accurate(z[j]) : expf(z[j] - m);
         A += x[j];
       }
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
         s = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-          if (lane + 32 * j < E) s += expf(z[j] - m);
+          if (lane * NV + j < E) s += expf(z[j] - m);
         s = warp_sum(s);
       }
       if (lane == 0) a.lse[t] = m + logf(s);
@@ -123,11 +123,11 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
   for (int j = 0; j < NV; ++j) {  // the block's warps, in order
     part[warp][lane] = acc[j];
     __syncthreads();
-    if (warp == 0 && lane + 32 * j < E) {
+    if (warp == 0 && lane * NV + j < E) {
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) s += part[i][lane];
-      a.prob_part[(int64_t)blockIdx.x * E + lane + 32 * j] = s;
+      a.prob_part[(int64_t)blockIdx.x * E + lane * NV + j] = s;
     }
     __syncthreads();
   }
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
     float z[NV], dz[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int e = lane + 32 * j;
+      const int e = lane * NV + j;
       z[j] = e < E ? load_logit(row + e) : 0.f;
       dz[j] = 0.f;
     }
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
     if (all) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        p[j] = lane + 32 * j >= E ? 0.f : soft ? expf(z[j] - m) : sigmoid_accurate(z[j]);
+        p[j] = lane * NV + j >= E ? 0.f : soft ? expf(z[j] - m) : sigmoid_accurate(z[j]);
         A += p[j];
       }
       A = warp_sum(A);
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
       float dot = 0.f, g[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        g[j] = a.dP != nullptr && lane + 32 * j < E ? a.dP[lane + 32 * j] : 0.f;
+        g[j] = a.dP != nullptr && lane * NV + j < E ? a.dP[lane * NV + j] : 0.f;
         dot += g[j] * p[j];
       }
       dot = warp_sum(dot);
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
       float x[NV], s = 0.f;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        x[j] = lane + 32 * j < E ? expf(z[j] - m) : 0.f;
+        x[j] = lane * NV + j < E ? expf(z[j] - m) : 0.f;
         s += x[j];
       }
       s = warp_sum(s);
@@ -209,16 +209,13 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
     for (int k = 0; k < K; ++k) {
       const int e = __shfl_sync(0xFFFFFFFFu, has ? id_in : -1, k);
       const float v = __shfl_sync(0xFFFFFFFFu, add, k);
-      if (e >= 0 && (e & 31) == lane) {
-        const int j0 = e >> 5;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (j == j0) dz[j] += v;
-      }
+      for (int j = 0; j < NV; ++j)
+        if (e == lane * NV + j) dz[j] += v;
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (lane + 32 * j < E) store_logit(static_cast<LT*>(a.dz) + t * E + lane + 32 * j, dz[j]);
+      if (lane * NV + j < E) store_logit(static_cast<LT*>(a.dz) + t * E + lane * NV + j, dz[j]);
   }
 }
 
