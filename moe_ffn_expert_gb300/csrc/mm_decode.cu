@@ -117,6 +117,29 @@ struct Work {
 // A value that all lanes share, in the form the compiler knows to be shared.
 __device__ __forceinline__ int uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
 
+// A ring's stage barriers as one warp in step walks them. The next stage is asked for before the
+// current one's work is issued, so that the answer's latency passes behind it: ~100 cycles of a
+// stage's ~350.
+template <int STAGES>
+struct Walk {
+  uint32_t bar0, phase;  // first barrier; parity to wait for
+  int s = 0;
+  bool ready = false;
+  __device__ __forceinline__ Walk(uint32_t bar, uint32_t first) : bar0(bar), phase(first) {}
+  // Stage s is there (true in every lane), or the wait ran out.
+  __device__ __forceinline__ bool wait() {
+    if (__all_sync(0xFFFFFFFFu, ready)) return true;
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar0 + 8u * s, phase, kTimeoutNs));
+  }
+  __device__ __forceinline__ void ask_next() {
+    const bool wrap = s + 1 == STAGES;
+    ready = mbar_test_wait(bar0 + 8u * (wrap ? 0 : s + 1), wrap ? phase ^ 1u : phase);
+  }
+  __device__ __forceinline__ void next() {
+    if (++s == STAGES) s = 0, phase ^= 1u;
+  }
+};
+
 // x = (hi + lo / 16) / s for |x s| < 256.
 __device__ __forceinline__ void split_e4m3(float xs, uint8_t& hi, uint8_t& lo) {
   hi = __nv_cvt_float_to_fp8(xs, __NV_SATFINITE, __NV_E4M3);
@@ -536,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
 
   if (warp == 0) {
     // ------------------------------------------------ claims units and loads their weights
-    int u = blockIdx.x, it = 0, s = 0;
-    uint32_t ph = 0;
+    int u = blockIdx.x, it = 0;
+    Walk<STAGES> ring(empty(0), 1);
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
       const int qs = qi % kQueue;
@@ -559,19 +582,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const int c0 = uniform(un.tile * (un.kind == 0 ? 64 : kCols));
       const int c1 = uniform(un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + 64);
       for (int kb = uniform(un.kb0); kb < kb1; ++kb, ++it) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty(s), ph ^ 1, kTimeoutNs))) {
+        if (!ring.wait()) {
           if (lane == 0) give_up();
           ok = false;
           break;
         }
+        ring.ask_next();
         if (elect_one()) {
-          const uint32_t dst = base + s * kTileBytes, bar = full(s);
+          const uint32_t dst = base + ring.s * kTileBytes, bar = full(ring.s);
           mbar_arrive_expect_tx(bar, kTileBytes);
           tma_load_3d(dst, map, bar, c0, kb * KB, e);
           tma_load_3d(dst + kTileBytes / 2, map, bar, c1, kb * KB, e);
         }
         __syncwarp();
-        if (++s == STAGES) s = 0, ph ^= 1;
+        ring.next();
       }
       u = gridDim.x + __shfl_sync(0xFFFFFFFFu, next, 0);
     }
@@ -580,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       mbar_wait(full(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
   } else if (warp == 1) {
     // ------------------------------------------------ loads the rows
-    int it = 0, s = 0;
-    uint32_t ph = 0;
+    int it = 0;
+    Walk<STAGES> ring(empty(0), 1);
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
       const int u = take(qi);
@@ -620,11 +644,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const uint32_t bytes = (FP8 ? 2 : 1) * groups * (un.kind == 0 ? 512 : 1024);
       const uint32_t to = (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
-        if (!mbar_wait(empty(s), ph ^ 1, kTimeoutNs)) {
+        if (!ring.wait()) {
           if (lane == 0) give_up();
           ok = false;
           break;
         }
+        ring.ask_next();
+        const int s = ring.s;
         if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
         __syncwarp();
         if (loads) {
@@ -635,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             tma_load_2d(dst, map, full(s), kb * KB, r[0]);
         }
         __syncwarp();
-        if (++s == STAGES) s = 0, ph ^= 1;
+        ring.next();
       }
     }
     for (int j = max(0, it - STAGES); j < it; ++j)
@@ -649,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     const uint64_t wdesc = FP8 ? sdesc_sw64(base, kTileBytes / 2, 512)
                                : sdesc_sw128(base, kTileBytes / 2, 1024);
     const uint64_t bdesc = sdesc_sw128(rows_at, 16, 1024);
-    int s = 0, used[2] = {0, 0};  // stage; accumulators so far in each set's ring
-    uint32_t ph = 0;
+    Walk<STAGES> ring(full(0), 0);
+    int used[2] = {0, 0};  // accumulators so far in each set's ring
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
       const int u = uniform(take(qi));
@@ -669,10 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) give_up();
         ok = false;
       };
-      // products ks0 .. ks1 - 1 of stage s into the accumulator at d
+      // products ks0 .. ks1 - 1 of the ring's stage into the accumulator at d
       auto products = [&](uint32_t d, int ks0, int ks1, bool fresh) {
-        const uint64_t wd = wdesc + (uint32_t)s * (kTileBytes / 16);
-        const uint64_t bd = bdesc + (uint32_t)s * (C::B_BYTES / 16);
+        const uint64_t wd = wdesc + (uint32_t)ring.s * (kTileBytes / 16);
+        const uint64_t bd = bdesc + (uint32_t)ring.s * (C::B_BYTES / 16);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           if (ks < ks0 || ks >= ks1) continue;
@@ -688,16 +714,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         const uint32_t d = tmem + slot * 64;
         wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1);
         for (int i = 0; i < blocks && ok; ++i) {
-          wait(full(s), ph);
-          if (!ok) break;
+          if (!ring.wait()) {
+            if (lane == 0) give_up();
+            ok = false;
+            break;
+          }
+          ring.ask_next();
           tc_fence_after();
           if (elect_one()) {
             products(d, 0, 4, i == 0);
-            umma_commit(empty(s));
+            umma_commit(empty(ring.s));
             if (i + 1 == blocks) umma_commit(acc_full(slot));
           }
           __syncwarp();
-          if (++s == STAGES) s = 0, ph ^= 1;
+          ring.next();
         }
         ++acc;
       } else {
@@ -706,8 +736,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         for (int i = 0; i < blocks && ok; ++i) {
           const int slot = set * kRing + acc % kRing;
           wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1);
-          if (ok) wait(full(s), ph);
           if (!ok) break;
+          if (!ring.wait()) {
+            if (lane == 0) give_up();
+            ok = false;
+            break;
+          }
+          ring.ask_next();
           tc_fence_after();
           if (elect_one()) {
             if (up)
@@ -730,9 +765,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             __syncwarp();
             ++acc;
           }
-          if (elect_one()) umma_commit(empty(s));
+          if (elect_one()) umma_commit(empty(ring.s));
           __syncwarp();
-          if (++s == STAGES) s = 0, ph ^= 1;
+          ring.next();
         }
       }
       if (set) used[1] = acc; else used[0] = acc;
