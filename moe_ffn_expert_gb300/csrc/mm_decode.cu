@@ -574,8 +574,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       }
       if (u >= work.total) break;
       const Unit un = unit_at(a, tb, work, u);
-      int next = 0;
-      if (lane == 0) next = atomicAdd(a.hdr + W_NEXT, 1);  // needed when this unit is issued
       const CUtensorMap* map = un.kind == 0 ? (un.shared ? &a.s_up : &a.up)
                                             : (un.shared ? &a.s_down : &a.down);
       const int e = uniform(un.e), kb1 = uniform(un.kb1);
@@ -597,6 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         __syncwarp();
         ring.next();
       }
+      // The next unit is claimed only when this one's loads are issued: the ring still holds work
+      // for longer than the claim takes, and a CTA stuck in front of a chunk that is not ready
+      // does not sit on units that others could take.
+      int next = 0;
+      if (lane == 0) next = atomicAdd(a.hdr + W_NEXT, 1);
       u = gridDim.x + __shfl_sync(0xFFFFFFFFu, next, 0);
     }
     // no CTA leaves with a copy into its shared memory in flight
@@ -802,17 +805,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         for (int i = q; i < un.n; i += 4) {
           const int t = un.row0 + i;
           if (c >= a.H) continue;
+          // rows in slot order, a slot's parts in order; 8 loads in flight
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          auto add = [&](const float* p) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-          };
-#pragma unroll 8
-          for (int k = 0; k < a.K; ++k)
-            for (int p = 0; p < work.split; ++p)
-              add(a.o + ((int64_t)p * a.S + tb.row[t * a.K + k]) * a.H + c);
-          if (work.ncs > 0)
-            for (int p = 0; p < work.splits; ++p) add(a.s_o + ((int64_t)p * a.T + t) * a.H + c);
+          const int routed = a.K * work.split, all = routed + (work.ncs > 0 ? work.splits : 0);
+          for (int i0 = 0; i0 < all; i0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const int j = i0 + r;
+              v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (j >= all) continue;
+              const int k = j / work.split;
+              const float* p =
+                  j < routed ? a.o + ((int64_t)(j - k * work.split) * a.S + tb.row[t * a.K + k]) * a.H
+                             : a.s_o + ((int64_t)(j - routed) * a.T + t) * a.H;
+              v[r] = __ldcg(reinterpret_cast<const float4*>(p + c));
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
+          }
           *reinterpret_cast<uint2*>(a.y + (int64_t)t * a.H + c) =
               make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
         }
