@@ -9,13 +9,17 @@
 //             caller's ids) in shared memory, then takes work units from one global counter:
 //     GEMM1   (chunk of up to 32 rows of one expert, 64 gate + 64 up columns): w * silu(g) * u
 //     GEMM2   (chunk, 128 output columns, part of I): fp32 partial rows
-//     combine (8 tokens, 128 columns): the sum of a token's partial rows, in slot order
+//   and when they are out, sums the partial rows of (token, 128 columns) tasks in slot order, dealt
+//   evenly to the warps of the grid.
 //
-// A GEMM2 unit needs its chunk's GEMM1 units, a combine unit its columns' GEMM2 units: counters
-// in the workspace, waited for at the last moment and only for the small operand, so the weight
-// loads of the next units run ahead through the wait. Units are claimed in that order, and a CTA
-// works through its units in the order it claimed them, so what a unit waits for is always held
-// by a CTA that is running or done: no wait depends on how many CTAs are resident.
+// A GEMM2 unit needs its chunk's GEMM1 units, a sum its columns' GEMM2 units: counters in the
+// workspace, waited for at the last moment and only for the small operand, so the weight loads of
+// the next units run ahead through the wait. Units are claimed in that order, and a CTA works
+// through its units in the order it claimed them, so what a unit waits for is always held by a CTA
+// that is running or done: no wait depends on how many CTAs are resident.
+//
+// From 13 tokens on, the selection runs as a launch of the router's kernel between the two: a CTA
+// that selects for 64 tokens itself takes 13 us, one per warp for up to 12 tokens 2.6.
 //
 // The products run on tcgen05.mma with the weights as the M = 128 operand, straight from the
 // row-major tiles that TMA brings (MN-major descriptors), and the chunk's rows as N: 16 or 32
@@ -43,9 +47,9 @@ namespace mm {
 namespace {
 
 constexpr int kMaxT = 64, kMaxSlots = 1024, kMaxE = 1024;
+constexpr int kMaxRouted = 12;    // tokens whose selection every CTA repeats, one per warp
 constexpr int kChunk = 32;        // rows of one expert per unit
 constexpr int kCols = 128;        // weight columns per unit
-constexpr int kTokens = 8;        // tokens per combine unit
 constexpr int kMaxSplit = 4;      // parts of I per GEMM2 column tile
 constexpr int kTileBytes = 16384; // one stage of weights: 64 x 128 bf16 or 128 x 128 e4m3
 constexpr int kThreads = 384;     // weight loads, row loads, MMA, tensor memory; 2 x 4 epilogue
@@ -100,18 +104,20 @@ struct Tables {
 struct Building {
   float slot_w[kMaxSlots];     // weight of a slot
   int16_t id[kMaxSlots];       // expert of a slot
+  uint8_t rank[kMaxSlots];     // slots of the same expert before it in its batch of 32
   uint32_t count[kMaxE];       // slots | chunks << 16, then the exclusive sums
-  uint16_t next[kMaxE];        // rows placed so far
+  // then uint16_t [batches][E]: an expert's slots per batch, then those of the batches before; and
+  // with a router fp32 [T][E] logits
 };
 
 struct Unit {
-  int kind;  // 0 GEMM1, 1 GEMM2, 2 combine
+  int kind;  // 0 GEMM1, 1 GEMM2
   int shared, row0, n, e, tile, kb0, kb1, split, ready;
 };
 
 // Work units in claiming order.
 struct Work {
-  int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, t2s, total;
+  int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, total;
 };
 
 // A value that all lanes share, in the form the compiler knows to be shared.
@@ -301,25 +307,20 @@ __device__ void select_row(const DecodeArgs& a, Building& bd, const float* row, 
 
 // Routing tables of the CTA: the slots sorted by expert (stable), cut into chunks. The same in
 // every CTA. False if a caller's id is out of range.
-__device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int ring_bytes) {
+__device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
   Building& bd = *reinterpret_cast<Building*>(ring);
-  float* ls = reinterpret_cast<float*>(ring + sizeof(Building));
+  uint16_t* before_batch = reinterpret_cast<uint16_t*>(ring + sizeof(Building));
+  float* ls = reinterpret_cast<float*>(ring + sizeof(Building));  // (used before it)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e < a.E; e += kThreads) bd.count[e] = 0, bd.next[e] = 0;
   if (tid == 0) tb.bad = 0;
   if (a.route) {
-    // all logits at once where they fit (T E <= 31 K), so that a row's selection starts from
-    // shared memory
+    // a row's selection starts from shared memory (kMaxRouted rows of at most 1024 fit)
     const int n = a.T * a.E;
-    const bool fits = (size_t)n * 4 + sizeof(Building) <= (size_t)ring_bytes;
-    if (fits) {
 #pragma unroll 4
-      for (int i = tid; i < n; i += kThreads) ls[i] = __ldcg(a.logits + i);
-      __syncthreads();
-    }
-    const float* rows = fits ? ls : a.logits;
+    for (int i = tid; i < n; i += kThreads) ls[i] = __ldcg(a.logits + i);
+    __syncthreads();
     for (int t = warp; t < a.T; t += kThreads / 32) {
-      const float* row = rows + t * a.E;
+      const float* row = ls + t * a.E;
       if (a.E <= 32) select_row<1>(a, bd, row, t, lane);
       else if (a.E <= 64) select_row<2>(a, bd, row, t, lane);
       else if (a.E <= 128) select_row<4>(a, bd, row, t, lane);
@@ -342,18 +343,39 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int
       return false;
     }
   }
-  for (int s = tid; s < a.S; s += kThreads) atomicAdd(&bd.count[bd.id[s]], 1u);
+  // A slot's row is the first row of its expert, plus the expert's slots in the batches before,
+  // plus those before it in its batch: all batches at once, then all experts, then all slots.
+  // (One warp walking the slots took 6 us for 512.)
+  const int batches = (a.S + 31) / 32;
+  for (int i = tid; i < batches * a.E; i += kThreads) before_batch[i] = 0;
+  __syncthreads();
+  for (int b = warp; b < batches; b += kThreads / 32) {
+    const int s = b * 32 + lane;
+    const int e = s < a.S ? bd.id[s] : -1 - lane;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    if (s < a.S) {
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      bd.rank[s] = (uint8_t)rank;
+      if (rank == 0) before_batch[b * a.E + e] = (uint16_t)__popc(same);
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < a.E; e += kThreads) {
+    uint32_t n = 0;
+    for (int b = 0; b < batches; ++b) {
+      const uint32_t here = before_batch[b * a.E + e];
+      before_batch[b * a.E + e] = (uint16_t)n;
+      n += here;
+    }
+    bd.count[e] = n | ((n + kChunk - 1) / kChunk) << 16;
+  }
   __syncthreads();
   if (warp == 0) {
     // exclusive sums of slots (low half) and chunks (high half) over the experts; a lane takes
     // consecutive experts
     const int per = (a.E + 31) / 32, e0 = lane * per, e1 = min(a.E, e0 + per);
     uint32_t sum = 0;
-    for (int e = e0; e < e1; ++e) {
-      const uint32_t n = bd.count[e];
-      bd.count[e] = sum;
-      sum += n | ((n + kChunk - 1) / kChunk) << 16;
-    }
+    for (int e = e0; e < e1; ++e) sum += bd.count[e];
     uint32_t before = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -362,34 +384,26 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int
     }
     if (lane == 31) tb.chunks = (int)(before >> 16);
     before -= sum;
-    for (int e = e0; e < e1; ++e) bd.count[e] += before;
-    __syncwarp();
-    // slots in order, 32 at a time: a slot's place among its expert's is what came before
-    for (int s0 = 0; s0 < a.S; s0 += 32) {
-      const int s = s0 + lane;
-      const int e = s < a.S ? bd.id[s] : -1 - lane;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-      if (s < a.S) {
-        const int rank = bd.next[e] + __popc(same & ((1u << lane) - 1u));
-        const int r = (int)(bd.count[e] & 0xFFFFu) + rank;
-        tb.row[s] = (int16_t)r;
-        tb.tok[r] = (int16_t)(s / a.K);
-        tb.w[r] = bd.slot_w[s];
-        if (rank % kChunk == 0) {  // first row of a chunk
-          const int c = (int)(bd.count[e] >> 16) + rank / kChunk;
-          tb.chunk_row[c] = (uint16_t)r;
-          tb.chunk_e[c] = (uint16_t)e;
-        }
+    for (int e = e0; e < e1; ++e) {
+      const uint32_t n = bd.count[e];
+      bd.count[e] = before;
+      const int first = (int)(before & 0xFFFFu), rows = (int)(n & 0xFFFFu);
+      for (int c = 0; c < (int)(n >> 16); ++c) {
+        const int at = (int)(before >> 16) + c;
+        tb.chunk_row[at] = (uint16_t)(first + c * kChunk);
+        tb.chunk_e[at] = (uint16_t)e;
+        tb.chunk_n[at] = (uint8_t)min(kChunk, rows - c * kChunk);
       }
-      __syncwarp();
-      if (s < a.S && (same >> lane) == 1u) bd.next[e] += (uint16_t)__popc(same);
-      __syncwarp();
+      before += n;
     }
   }
   __syncthreads();
-  for (int c = tid; c < tb.chunks; c += kThreads) {
-    const int e = tb.chunk_e[c], first = (int)(bd.count[e] & 0xFFFFu);
-    tb.chunk_n[c] = (uint8_t)min(kChunk, first + (int)bd.next[e] - (int)tb.chunk_row[c]);
+  for (int s = tid; s < a.S; s += kThreads) {
+    const int e = bd.id[s];
+    const int r = (int)(bd.count[e] & 0xFFFFu) + before_batch[(s >> 5) * a.E + e] + bd.rank[s];
+    tb.row[s] = (int16_t)r;
+    tb.tok[r] = (int16_t)(s / a.K);
+    tb.w[r] = bd.slot_w[s];
   }
   // the ring is TMA's from here on
   fence_proxy_async_smem();
@@ -417,8 +431,7 @@ __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
   w.t1 = w.nc * w.nt1;
   w.t1s = w.t1 + w.ncs * w.nt1s;
   w.t2 = w.t1s + w.nc * w.nt2 * w.split;
-  w.t2s = w.t2 + w.ncs * w.nt2 * w.splits;
-  w.total = w.t2s + w.nt2 * ((a.T + kTokens - 1) / kTokens);
+  w.total = w.t2 + w.ncs * w.nt2 * w.splits;
   return w;
 }
 
@@ -436,7 +449,7 @@ __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, c
     r.tile = v - c * nt;
     r.kb0 = 0;
     r.kb1 = w.kb_h;
-  } else if (u < w.t2s) {
+  } else {
     r.kind = 1;
     r.shared = u >= w.t2;
     const int v = u - (r.shared ? w.t2 : w.t1s), sp = r.shared ? w.splits : w.split;
@@ -447,17 +460,6 @@ __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, c
     r.split = rest - r.tile * sp;
     r.kb0 = kb * r.split / sp;
     r.kb1 = kb * (r.split + 1) / sp;
-  } else {
-    r.kind = 2;
-    const int v = u - w.t2s;
-    c = v / w.nt2;
-    r.tile = v - c * w.nt2;
-    r.row0 = c * kTokens;
-    r.n = min(kTokens, a.T - r.row0);
-    r.e = 0;
-    r.kb0 = r.kb1 = 0;
-    r.ready = 0;
-    return r;
   }
   if (r.shared) {
     r.row0 = c * kChunk;
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   constexpr int KB = C::KB, STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
-  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 2 * kSlots + 4 + 1];
+  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 2 * kSlots + 6 + 1];
   __shared__ int queue[kQueue];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -499,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   auto acc_empty = [&](int s) { return bar0 + 8u * (ACC + kSlots + s); };
   auto x_full = [&](int s) { return bar0 + 8u * (X + s); };
   auto x_empty = [&](int s) { return bar0 + 8u * (X + 2 + s); };
-  const uint32_t mma_done = bar0 + 8u * (X + 4);
+  auto handed = [&](int s) { return bar0 + 8u * (X + 4 + s); };
+  const uint32_t mma_done = bar0 + 8u * (X + 6);
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 2);  // the weights' and the rows' producers
@@ -516,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     for (int s = 0; s < 2; ++s) {
       mbar_init(x_full(s), 4);
       mbar_init(x_empty(s), 4);
+      mbar_init(handed(s), 4);
     }
     mbar_init(mma_done, 1);
     mbar_fence_init();
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     tma_prefetch_desc(&a.h_rows);
   }
   pdl_wait();
-  if (!build_tables(a, tb, aligned, STAGES * (kTileBytes + C::B_BYTES))) return;
+  if (!build_tables(a, tb, aligned)) return;
   if (warp == 3) {
     tmem_alloc(smem_u32(&tmem_slot), kSlots * 64);
     tmem_relinquish();
@@ -617,7 +621,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
       if (u < 0) break;
       const Unit un = unit_at(a, tb, work, u);
-      if (un.kind == 2) continue;
       const CUtensorMap* map = un.kind == 0 ? &a.x : un.shared ? &a.s_h_rows : &a.h_rows;
       // lanes of the first half load the rows (e4m3: their hi parts), those of the second the lo
       // parts; x: 4 rows by number per lane, h: 8 consecutive rows
@@ -687,12 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
       if (u < 0) break;
       const Unit un = unit_at(a, tb, work, u);
-      if (u >= work.t2s) continue;  // combine
-      const int set = qi & 1, blocks = uniform(un.kb1 - un.kb0), slots = uniform(slots_of(un));
+      const int blocks = uniform(un.kb1 - un.kb0);
       const uint32_t n = (uint32_t)uniform(columns_of(un));
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
-      int acc = set ? used[1] : used[0];
-      const int end = acc + slots;
       auto wait = [&](uint32_t bar, uint32_t phase) {
         if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, kTimeoutNs))) return;
         if (lane == 0) give_up();
@@ -713,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
       };
       if constexpr (!FP8) {
+        const int set = qi & 1, acc = set ? used[1]++ : used[0]++;
         const int slot = set * kRing + acc % kRing;
         const uint32_t d = tmem + slot * 64;
         wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1);
@@ -732,14 +733,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           __syncwarp();
           ring.next();
         }
-        ++acc;
       } else {
-        // an accumulator per scale: 128 rows of up, 64 rows of down
+        // an accumulator per scale, 128 rows of up or 64 of down, for the two sets in turn
         const bool up = u < work.t1s;
+        int to = qi & 1, left = uniform(slots_of(un));
+        auto accumulate = [&](int ks0, int ks1) {  // the next accumulator: these products
+          const int n_used = to ? used[1] : used[0];
+          const int slot = to * kRing + n_used % kRing;
+          wait(acc_empty(slot), ((n_used / kRing) & 1) ^ 1);
+          if (!ok) return;
+          tc_fence_after();
+          if (elect_one()) {
+            products(tmem + slot * 64, ks0, ks1, true);
+            umma_commit(acc_full(slot));
+          }
+          __syncwarp();
+          if (to) ++used[1]; else ++used[0];
+          to ^= 1;
+          --left;
+        };
         for (int i = 0; i < blocks && ok; ++i) {
-          const int slot = set * kRing + acc % kRing;
-          wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1);
-          if (!ok) break;
           if (!ring.wait()) {
             if (lane == 0) give_up();
             ok = false;
@@ -747,98 +760,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           }
           ring.ask_next();
           tc_fence_after();
-          if (elect_one()) {
-            if (up)
-              products(tmem + slot * 64, 0, 4, true);
-            else
-              products(tmem + slot * 64, 0, 2, true);
-            umma_commit(acc_full(slot));
+          if (up) {
+            accumulate(0, 4);
+          } else {
+            accumulate(0, 2);
+            if (ok && left > 0) accumulate(2, 4);  // (the last 128 rows of h may be 64)
           }
-          __syncwarp();
-          ++acc;
-          if (!up && acc < end) {  // (the last 128 rows of h may be 64)
-            const int slot2 = set * kRing + acc % kRing;
-            wait(acc_empty(slot2), ((acc / kRing) & 1) ^ 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              products(tmem + slot2 * 64, 2, 4, true);
-              umma_commit(acc_full(slot2));
-            }
-            __syncwarp();
-            ++acc;
-          }
+          if (!ok) break;
           if (elect_one()) umma_commit(empty(ring.s));
           __syncwarp();
           ring.next();
         }
       }
-      if (set) used[1] = acc; else used[0] = acc;
     }
     if (elect_one()) umma_commit(mma_done);
     __syncwarp();
     mbar_wait(mma_done, 0, kTimeoutNs);
   } else if (warp >= kFirstEpilogue) {
     // ------------------------------------------------ accumulators to h, partial rows and y
+    // Two sets of four warps. bf16: they take the units in turn. e4m3: both work on every unit,
+    // each on every second accumulator; the unit's owner (in turn) adds the other's sums.
     const int set = (warp - kFirstEpilogue) >> 2, q = warp & 3;  // q: the warp's quarter of the lanes
     const int col = q * 32 + lane;  // of the unit's 128
-    float* const ex = exchange + set * kChunk * kCols;
-    int acc = 0, uses = 0;
+    int acc = 0;                    // accumulators taken from this set's ring
+    int x_uses[2] = {0, 0};         // uses of each set's exchange buffer
+    int up_units = 0;               // GEMM1 units that this set finished
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
       const int u = take(qi);
       __syncwarp();
-      if (u == -2) break;
+      if (u == -2) {
+        ok = false;
+        break;
+      }
       if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
       if (u < 0) break;
+      const int owner = qi & 1;
+      if (!FP8 && owner != set) continue;
       const Unit un = unit_at(a, tb, work, u);
-      if ((qi & 1) != set) continue;  // the sets take units in turn, each with its own accumulators
-      if (un.kind == 2) {
-        const int target = 4 * (work.nc * work.split + work.ncs * work.splits);
-        int there = 1;
-        if (lane == 0) there = wait_counter(a.ready2 + un.tile, target, kTimeoutNs);
-        if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
-          if (lane == 0) give_up();
-          break;
-        }
-        const int c = un.tile * kCols + lane * 4;
-        for (int i = q; i < un.n; i += 4) {
-          const int t = un.row0 + i;
-          if (c >= a.H) continue;
-          // rows in slot order, a slot's parts in order; 8 loads in flight
-          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int routed = a.K * work.split, all = routed + (work.ncs > 0 ? work.splits : 0);
-          for (int i0 = 0; i0 < all; i0 += 8) {
-            float4 v[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const int j = i0 + r;
-              v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (j >= all) continue;
-              const int k = j / work.split;
-              const float* p =
-                  j < routed ? a.o + ((int64_t)(j - k * work.split) * a.S + tb.row[t * a.K + k]) * a.H
-                             : a.s_o + ((int64_t)(j - routed) * a.T + t) * a.H;
-              v[r] = __ldcg(reinterpret_cast<const float4*>(p + c));
-            }
-#pragma unroll
-            for (int r = 0; r < 8; ++r) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
-          }
-          *reinterpret_cast<uint2*>(a.y + (int64_t)t * a.H + c) =
-              make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-        }
-        continue;
-      }
-      const int nslots = slots_of(un);
+      float* const ex = exchange + owner * kChunk * kCols;
       const int n8 = (un.n + 7) & ~7;
       const int I = un.shared ? a.Is : a.I, nt64 = (I + 63) / 64;
+      auto wait = [&](uint32_t bar, uint32_t phase) {
+        if (mbar_wait(bar, phase, kTimeoutNs)) return true;
+        if (lane == 0) give_up();
+        ok = false;
+        return false;
+      };
       float v[kChunk];
       if constexpr (!FP8) {
         const int s = set * kRing + acc % kRing;
-        if (!mbar_wait(acc_full(s), (acc / kRing) & 1, kTimeoutNs)) {
-          if (lane == 0) give_up();
-          break;
-        }
+        if (!wait(acc_full(s), (acc / kRing) & 1)) break;
         tc_fence_after();
         const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
 #pragma unroll
@@ -869,46 +841,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         sc += (int64_t)un.e * row_blocks * nb;
         const int b0 = min(q0 / 128, nb - 1), b1 = min((q0 + 31) / 128, nb - 1);
         const bool second = (q0 + lane) / 128 > q0 / 128;  // this lane's column is in the latter
-        const float* hs = (un.shared ? a.s_h_scale : a.h_scale) +
-                          (int64_t)(un.row0 + min(lane, un.n - 1)) * nt64 + 2 * un.kb0;
         const int per = un.kind == 0 ? 0 : 1;  // 2^per accumulators per 128 rows
+        const int first = set ^ owner, slots = (slots_of(un) - first + 1) >> 1;  // this set's
+        const float* hs = (un.shared ? a.s_h_scale : a.h_scale) +
+                          (int64_t)(un.row0 + min(lane, un.n - 1)) * nt64 + 2 * un.kb0 + first;
         float sc0 = 0.f, sc1 = 0.f, hv[4] = {1.f, 1.f, 1.f, 1.f};
-        auto load_scales = [&](int kb) {
-          if (kb + lane < un.kb1) {
-            sc0 = __ldg(sc + (int64_t)(kb + lane) * nb + b0);
-            sc1 = __ldg(sc + (int64_t)(kb + lane) * nb + b1);
+        int group = 0;  // of 32 row blocks
+        auto load_scales = [&] {
+          const int kb = un.kb0 + 32 * group + lane;
+          if (kb < un.kb1) {
+            sc0 = __ldg(sc + (int64_t)kb * nb + b0);
+            sc1 = __ldg(sc + (int64_t)kb * nb + b1);
           }
         };
-        load_scales(un.kb0);
+        load_scales();
         if (un.kind == 1) {  // the scales of h come with its rows
           const int target = 4 * (un.shared ? work.nt1s : work.nt1);
           int there = 1;
           if (lane == 0) there = wait_counter(a.ready1 + un.ready, target, kTimeoutNs);
           if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
             if (lane == 0) give_up();
+            ok = false;
             break;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i < nslots) hv[i] = __ldcg(hs + i);
+            if (i < slots) hv[i] = __ldcg(hs + 2 * i);
         }
-        for (int i0 = 0; i0 < nslots && ok; i0 += 4) {
+        for (int i0 = 0; i0 < slots && ok; i0 += 4) {
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
             const int i = i0 + k4;
-            if (i >= nslots) break;
-            const int blk = i >> per;
-            if (i == (blk << per) && blk > 0 && (blk & 31) == 0) load_scales(un.kb0 + blk);
+            if (i >= slots) break;
+            const int blk = (2 * i + first) >> per;
+            if (blk >> 5 != group) {
+              group = blk >> 5;
+              load_scales();
+            }
             const float w0 = __shfl_sync(0xFFFFFFFFu, sc0, blk & 31);
             const float w1 = __shfl_sync(0xFFFFFFFFu, sc1, blk & 31);
             const float ws = second ? w1 : w0, hscale = hv[k4];
-            if (un.kind == 1 && i + 4 < nslots) hv[k4] = __ldcg(hs + i + 4);
+            if (un.kind == 1 && i + 4 < slots) hv[k4] = __ldcg(hs + 2 * (i + 4));
             const int s = set * kRing + acc % kRing;
-            if (!mbar_wait(acc_full(s), (acc / kRing) & 1, kTimeoutNs)) {
-              if (lane == 0) give_up();
-              ok = false;
-              break;
-            }
+            if (!wait(acc_full(s), (acc / kRing) & 1)) break;
             tc_fence_after();
             const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
 #pragma unroll
@@ -932,6 +907,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           }
         }
         if (!ok) break;
+        const int use = owner ? x_uses[1]++ : x_uses[0]++;
+        if (set != owner) {  // hand the sums over
+          if (!wait(x_empty(owner), (use & 1) ^ 1)) break;
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i)
+            if (i < un.n) ex[i * kCols + col] = v[i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(handed(owner));
+          continue;
+        }
+        if (!wait(handed(owner), use & 1)) break;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+          if (i < un.n) v[i] += ex[i * kCols + col];
         if (un.kind == 0) {  // the tokens' scales
           const float xs = lane < un.n
                                ? a.x_scale[un.shared ? un.row0 + lane : tb.tok[un.row0 + lane]] : 0.f;
@@ -950,24 +939,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             if (i < un.n) o[(int64_t)(un.row0 + i) * a.H + c] = v[i];
         }
         __syncwarp();
-        if (lane == 0) red_add_release_gpu(a.ready2 + un.tile, 1);
+        if (lane == 0) {
+          if (FP8) mbar_arrive(x_empty(owner));
+          red_add_release_gpu(a.ready2 + un.tile, 1);
+        }
         continue;
       }
       // GEMM1: columns 0..63 are gate, 64..127 up of the same 64; the set's warps meet in shared
       // memory and take the rows in turn, two columns per lane
-      if (!mbar_wait(x_empty(set), (uses & 1) ^ 1, kTimeoutNs)) {
-        if (lane == 0) give_up();
-        break;
+      if (!FP8) {
+        const int use = owner ? x_uses[1]++ : x_uses[0]++;
+        if (!wait(x_empty(owner), (use & 1) ^ 1)) break;
       }
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
         if (i < un.n) ex[i * kCols + col] = v[i];
       __syncwarp();
-      if (lane == 0) mbar_arrive(x_full(set));
-      if (!mbar_wait(x_full(set), uses & 1, kTimeoutNs)) {
-        if (lane == 0) give_up();
-        break;
-      }
+      if (lane == 0) mbar_arrive(x_full(owner));
+      if (!wait(x_full(owner), up_units & 1)) break;
+      ++up_units;
       const int c = un.tile * 64 + 2 * lane;
       for (int i = q; i < un.n; i += 4) {
         const int row = un.row0 + i;
@@ -1001,10 +991,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       fence_proxy_async_global();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(x_empty(set));
+        mbar_arrive(x_empty(owner));
         red_add_release_gpu(a.ready1 + un.ready, 1);
       }
-      ++uses;
+    }
+    // ------------------------------------------------ sums of the partial rows
+    const int target = 4 * (work.nc * work.split + work.ncs * work.splits);
+    const int routed = a.K * work.split, all = routed + (work.ncs > 0 ? work.splits : 0);
+    for (int task = (warp - kFirstEpilogue) * (int)gridDim.x + (int)blockIdx.x;
+         ok && task < a.T * work.nt2; task += 8 * (int)gridDim.x) {
+      const int t = task / work.nt2, tile = task - t * work.nt2, c = tile * kCols + lane * 4;
+      int there = 1;
+      if (lane == 0) there = wait_counter(a.ready2 + tile, target, kTimeoutNs);
+      if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
+        if (lane == 0) give_up();
+        break;
+      }
+      if (c >= a.H) continue;
+      // rows in slot order, a slot's parts in order; 8 loads in flight
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < all; i0 += 8) {
+        float4 r8[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int j = i0 + r;
+          r8[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j >= all) continue;
+          const int k = j / work.split;
+          const float* p =
+              j < routed ? a.o + ((int64_t)(j - k * work.split) * a.S + tb.row[t * a.K + k]) * a.H
+                         : a.s_o + ((int64_t)(j - routed) * a.T + t) * a.H;
+          r8[r] = __ldcg(reinterpret_cast<const float4*>(p + c));
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          s.x += r8[r].x, s.y += r8[r].y, s.z += r8[r].z, s.w += r8[r].w;
+      }
+      *reinterpret_cast<uint2*>(a.y + (int64_t)t * a.H + c) =
+          make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
     }
   }
   tc_fence_before();
@@ -1070,7 +1094,7 @@ inline bool aligned_to(const void* p, size_t a) {
 }
 
 struct Layout {
-  size_t off_ready2, off_logits, off_x8, off_xs, off_h, off_sh, off_hs, off_shs, off_o, off_so, total;
+  size_t off_ready2, off_logits, off_ids, off_weights, off_x8, off_xs, off_h, off_sh, off_hs, off_shs, off_o, off_so, total;
   int zero_words;
 };
 
@@ -1104,6 +1128,8 @@ Layout layout(const mm_decode_desc& d) {
   l.off_ready2 = take((size_t)((m.H + kCols - 1) / kCols) * 4);
   l.zero_words = (int)(off / 4);
   l.off_logits = take((size_t)(m.T * m.E) * 4);
+  l.off_ids = take(S * 4);
+  l.off_weights = take(S * 4);
   const bool fp8 = d.weight_type == MM_E4M3;
   l.off_x8 = take(fp8 ? (size_t)m.T * m.H * 2 : 0);
   l.off_xs = take(fp8 ? (size_t)m.T * 4 : 0);
@@ -1269,6 +1295,16 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
     MM_TRY(launch_pdl(k_logits<__nv_bfloat16>, grid, dim3(256), 0, st, la));
   else
     MM_TRY(launch_pdl(k_logits<float>, grid, dim3(256), 0, st, la));
+  if (a.route && m.T > kMaxRouted) {
+    int32_t* ids = topk_ids ? topk_ids : reinterpret_cast<int32_t*>(ws + l.off_ids);
+    float* weights = topk_weights ? topk_weights : reinterpret_cast<float*>(ws + l.off_weights);
+    const mm_router_desc rd{m.T, (int32_t)m.E, (int32_t)m.K, MM_FP32, d->score, d->normalize,
+                            d->scale};
+    MM_TRY(launch_router(rd, la.logits, w->router_bias, ids, weights, st));
+    a.route = 0;
+    a.ids = ids;
+    a.weights = weights;
+  }
   const int sms = std::max(1, device_sm_count());
   if (fp8)
     MM_TRY(launch_experts<true>(a, sms, st));

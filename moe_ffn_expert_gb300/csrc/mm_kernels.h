@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/mm_ops.h"
 #include "mm_layout.h"
 
 namespace mm {
@@ -126,6 +127,10 @@ struct SumArgs {
   int jobs, cols, type;
 };
 cudaError_t launch_column_sums(const SumArgs& a, int64_t rows, cudaStream_t st);
+
+// The router's selection and weights over fp32 logits (mm_router.cu).
+cudaError_t launch_router(const mm_router_desc& d, const float* logits, const float* bias,
+                          int32_t* ids, float* weights, cudaStream_t st);
 
 // Tensor map of a rank-2 or -3 tensor; dims and box innermost first, strides in bytes (rank - 1).
 // False (with the reason noted) if it cannot be encoded.

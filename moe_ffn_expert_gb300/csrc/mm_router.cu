@@ -57,6 +57,7 @@ template <typename LT, int NV>
 __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
   __shared__ float part[kWarps][32];
   pdl_wait();
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, K = a.K;
   const bool all = a.prob_part != nullptr || (a.score == MM_SCORE_SOFTMAX && !a.normalize);
@@ -282,7 +283,27 @@ cudaError_t for_width(int E, F&& f) {
   return f(std::integral_constant<int, 32>());
 }
 
+cudaError_t launch_fwd(const mm_router_desc& d, const RouterArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)router_blocks(d)), block(32 * kWarps);
+  return for_width(d.E, [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    return d.logits_type == MM_BF16
+               ? launch_pdl(k_router_fwd<__nv_bfloat16, NV>, grid, block, 0, st, a)
+               : launch_pdl(k_router_fwd<float, NV>, grid, block, 0, st, a);
+  });
+}
+
 }  // namespace
+
+cudaError_t launch_router(const mm_router_desc& d, const float* logits, const float* bias,
+                          int32_t* ids, float* weights, cudaStream_t st) {
+  RouterArgs a = router_args(d);
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  return launch_fwd(d, a, st);
+}
 
 cudaError_t launch_column_sums(const SumArgs& a, int64_t rows, cudaStream_t st) {
   return launch_pdl(k_column_sums, dim3((unsigned)((a.cols + 31) / 32), (unsigned)rows),
@@ -328,14 +349,7 @@ mm_status mm_router_forward(const mm_router_desc* d, const void* logits, const f
   a.weights = topk_weights;
   a.lse = lse;
   a.prob_part = prob_sum ? static_cast<float*>(workspace) : nullptr;
-  MM_TRY(for_width(d->E, [&](auto nv) {
-    constexpr int NV = decltype(nv)::value;
-    return d->logits_type == MM_BF16
-               ? launch_pdl(k_router_fwd<__nv_bfloat16, NV>, dim3((unsigned)blocks),
-                            dim3(32 * kWarps), 0, st, a)
-               : launch_pdl(k_router_fwd<float, NV>, dim3((unsigned)blocks), dim3(32 * kWarps), 0,
-                            st, a);
-  }));
+  MM_TRY(launch_fwd(*d, a, st));
   if (prob_sum) {
     SumArgs sa{};
     sa.cols = d->E;
