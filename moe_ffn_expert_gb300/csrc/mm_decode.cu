@@ -55,8 +55,6 @@ constexpr int kTileBytes = 16384; // one stage of weights: 64 x 128 bf16 or 128 
 constexpr int kThreads = 384;     // weight loads, row loads, MMA, tensor memory; 2 x 4 epilogue
 constexpr int kFirstEpilogue = 4;
 constexpr int kQueue = 8;         // units claimed ahead
-constexpr int kSlots = 8;         // accumulators of 64 columns in tensor memory, half per epilogue set
-constexpr int kRing = kSlots / 2;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <bool FP8>
@@ -64,6 +62,10 @@ struct Cfg {
   static constexpr int KB = FP8 ? 128 : 64;                 // k per stage: 128 bytes of a row
   static constexpr int B_BYTES = (FP8 ? 2 : 1) * kChunk * 128;
   static constexpr int STAGES = FP8 ? 7 : 8;
+  // accumulators in tensor memory, half of them per epilogue set: 32 columns for a bf16 unit; for
+  // a stage of e4m3 weights 64 (hi and lo parts of 32 rows), twice with the two scales of h
+  static constexpr int SLOT_COLS = FP8 ? 128 : 64;
+  static constexpr int RING = 512 / SLOT_COLS / 2;
 };
 
 // int32 words at the start of the workspace (zeroed by k_logits)
@@ -110,8 +112,10 @@ struct Building {
   // with a router fp32 [T][E] logits
 };
 
+// A work unit as its claimer describes it to the CTA's other warps (one place computes it: code
+// that runs once costs more to fetch than to execute).
 struct Unit {
-  int kind;  // 0 GEMM1, 1 GEMM2
+  int kind;  // 0 GEMM1, 1 GEMM2, -1 no more units
   int shared, row0, n, e, tile, kb0, kb1, split, ready;
 };
 
@@ -343,6 +347,38 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
       return false;
     }
   }
+  if (a.S <= 32) {  // one warp, one slot per lane; experts in the order of their first slots
+    if (warp == 0) {
+      const int e = lane < a.S ? bd.id[lane] : -1 - lane;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+      const int leader = __ffs(same) - 1, n = __popc(same);
+      const bool leads = leader == lane && lane < a.S;
+      const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+      int sum = leads ? n : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const int first = __shfl_sync(0xFFFFFFFFu, sum - (leads ? n : 0), leader);
+      if (lane < a.S) {
+        const int r = first + __popc(same & ((1u << lane) - 1u));
+        tb.row[lane] = (int16_t)r;
+        tb.tok[r] = (int16_t)(lane / a.K);
+        tb.w[r] = bd.slot_w[lane];
+        if (leads) {
+          const int c = __popc(leaders & ((1u << lane) - 1u));
+          tb.chunk_row[c] = (uint16_t)r;
+          tb.chunk_e[c] = (uint16_t)e;
+          tb.chunk_n[c] = (uint8_t)n;
+        }
+      }
+      if (lane == 0) tb.chunks = __popc(leaders);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    return true;
+  }
   // A slot's row is the first row of its expert, plus the expert's slots in the batches before,
   // plus those before it in its batch: all batches at once, then all experts, then all slots.
   // (One warp walking the slots took 6 us for 512.)
@@ -438,6 +474,8 @@ __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
 __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, const Work& w,
                                         int u) {
   Unit r;
+  r.kind = -1;
+  if (u >= w.total) return r;
   r.shared = 0;
   r.split = 0;
   int c;
@@ -478,27 +516,27 @@ __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, c
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__ DecodeArgs a) {
   using C = Cfg<FP8>;
-  constexpr int KB = C::KB, STAGES = C::STAGES;
+  constexpr int KB = C::KB, STAGES = C::STAGES, RING = C::RING;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
-  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 2 * kSlots + 6 + 1];
-  __shared__ int queue[kQueue];
+  __shared__ Unit queue[kQueue];
+  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 4 * RING + 6 + 1];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the stages' weights and rows (1024-byte aligned for the swizzle), then [row][128 columns] of
-  // a GEMM1 unit for each epilogue set
+  // a unit for each epilogue set
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const aligned = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t rows_at = base + STAGES * kTileBytes;
   float* const exchange = reinterpret_cast<float*>(aligned + STAGES * (kTileBytes + C::B_BYTES));
   const uint32_t bar0 = smem_u32(bars);
-  constexpr int Q = 2 * STAGES, ACC = Q + 2 * kQueue, X = ACC + 2 * kSlots;
+  constexpr int Q = 2 * STAGES, ACC = Q + 2 * kQueue, X = ACC + 4 * RING;
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto q_full = [&](int s) { return bar0 + 8u * (Q + s); };
   auto q_empty = [&](int s) { return bar0 + 8u * (Q + kQueue + s); };
-  auto acc_full = [&](int s) { return bar0 + 8u * (ACC + s); };
-  auto acc_empty = [&](int s) { return bar0 + 8u * (ACC + kSlots + s); };
+  auto acc_full = [&](int set, int s) { return bar0 + 8u * (ACC + set * RING + s); };
+  auto acc_empty = [&](int set, int s) { return bar0 + 8u * (ACC + (2 + set) * RING + s); };
   auto x_full = [&](int s) { return bar0 + 8u * (X + s); };
   auto x_empty = [&](int s) { return bar0 + 8u * (X + 2 + s); };
   auto handed = [&](int s) { return bar0 + 8u * (X + 4 + s); };
@@ -512,9 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 2 + 8);  // row loads, MMA, epilogue warps
     }
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(acc_full(s), 1);
-      mbar_init(acc_empty(s), 4);
+    for (int s = 0; s < 2 * RING; ++s) {
+      mbar_init(acc_full(0, s), 1);
+      mbar_init(acc_empty(0, s), 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(x_full(s), 4);
@@ -528,40 +566,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     tma_prefetch_desc(&a.x);
     tma_prefetch_desc(&a.h_rows);
   }
-  pdl_wait();
-  if (!build_tables(a, tb, aligned)) return;
   if (warp == 3) {
-    tmem_alloc(smem_u32(&tmem_slot), kSlots * 64);
+    tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  pdl_wait();
+  const bool good = build_tables(a, tb, aligned);  // (its barriers publish the mbarriers and tmem_slot)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const Work work = make_work<FP8>(a, tb.chunks);
   // a wait that runs out ends its role; the roles that depend on it run out in turn
   auto give_up = [&] { set_status(a.hdr + W_STATUS, MM_ERR_TIMEOUT); };
-  // next unit of the queue (-1: no more, -2: gave up); one lane per warp counts the read
-  auto take = [&](int qi) {
-    const int qs = qi % kQueue;
-    if (!mbar_wait(q_full(qs), (qi / kQueue) & 1, kTimeoutNs)) {
-      if (lane == 0) give_up();
-      return -2;
-    }
-    return queue[qs];
+  // entry qi of the queue (null: the wait ran out), every lane
+  auto take = [&](int qi) -> const Unit* {
+    if (mbar_wait(q_full(qi % kQueue), (qi / kQueue) & 1, kTimeoutNs)) return &queue[qi % kQueue];
+    if (lane == 0) give_up();
+    return nullptr;
   };
-  // accumulators of a unit: one for bf16; e4m3: one per scale, 128 rows of up, 64 of down
-  auto slots_of = [&](const Unit& u) {
-    if (!FP8) return 1;
-    if (u.kind == 0) return u.kb1 - u.kb0;
-    const int I = u.shared ? a.Is : a.I;
-    return min(2 * u.kb1, (I + 63) / 64) - 2 * u.kb0;
-  };
-  auto columns_of = [&](const Unit& u) {  // N of the products
-    return FP8 ? 2 * ((u.n + 7) & ~7) : (u.n + 15) & ~15;
+  // the warp has read its entry
+  auto taken = [&](int qi) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
   };
 
-  if (warp == 0) {
+  if (!good) {
+    // a caller's id is out of range: nothing to do
+  } else if (warp == 0) {
     // ------------------------------------------------ claims units and loads their weights
     int u = blockIdx.x, it = 0;
     Walk<STAGES> ring(empty(0), 1);
@@ -572,12 +603,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) give_up();
         break;
       }
+      const Unit un = unit_at(a, tb, work, u);
       if (lane == 0) {
-        queue[qs] = u < work.total ? u : -1;
+        queue[qs] = un;
         mbar_arrive(q_full(qs));
       }
-      if (u >= work.total) break;
-      const Unit un = unit_at(a, tb, work, u);
+      if (un.kind < 0) break;
       const CUtensorMap* map = un.kind == 0 ? (un.shared ? &a.s_up : &a.up)
                                             : (un.shared ? &a.s_down : &a.down);
       const int e = uniform(un.e), kb1 = uniform(un.kb1);
@@ -615,12 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     Walk<STAGES> ring(empty(0), 1);
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
-      const int u = take(qi);
-      __syncwarp();
-      if (u == -2) break;
-      if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
-      if (u < 0) break;
-      const Unit un = unit_at(a, tb, work, u);
+      const Unit* const entry = take(qi);
+      if (entry == nullptr) break;
+      const Unit un = *entry;
+      taken(qi);
+      if (un.kind < 0) break;
       const CUtensorMap* map = un.kind == 0 ? &a.x : un.shared ? &a.s_h_rows : &a.h_rows;
       // lanes of the first half load the rows (e4m3: their hi parts), those of the second the lo
       // parts; x: 4 rows by number per lane, h: 8 consecutive rows
@@ -648,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         r[0] = lo + un.row0 + 8 * j;
       }
       const uint32_t bytes = (FP8 ? 2 : 1) * groups * (un.kind == 0 ? 512 : 1024);
-      const uint32_t to = (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
+      const uint32_t to = rows_at + (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
         if (!ring.wait()) {
           if (lane == 0) give_up();
@@ -656,15 +686,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           break;
         }
         ring.ask_next();
-        const int s = ring.s;
-        if (lane == 0) mbar_arrive_expect_tx(full(s), bytes);
+        if (lane == 0) mbar_arrive_expect_tx(full(ring.s), bytes);
         __syncwarp();
         if (loads) {
-          const uint32_t dst = rows_at + s * C::B_BYTES + to;
+          const uint32_t dst = to + ring.s * C::B_BYTES;
           if (un.kind == 0)
-            tma_gather4(dst, map, full(s), kb * KB, r[0], r[1], r[2], r[3]);
+            tma_gather4(dst, map, full(ring.s), kb * KB, r[0], r[1], r[2], r[3]);
           else
-            tma_load_2d(dst, map, full(s), kb * KB, r[0]);
+            tma_load_2d(dst, map, full(ring.s), kb * KB, r[0]);
         }
         __syncwarp();
         ring.next();
@@ -682,96 +711,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                                : sdesc_sw128(base, kTileBytes / 2, 1024);
     const uint64_t bdesc = sdesc_sw128(rows_at, 16, 1024);
     Walk<STAGES> ring(full(0), 0);
-    int used[2] = {0, 0};  // accumulators so far in each set's ring
+    Walk<RING> accs[2] = {Walk<RING>(acc_empty(0, 0), 1), Walk<RING>(acc_empty(1, 0), 1)};
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
-      const int u = uniform(take(qi));
-      if (u == -2) break;
-      if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
-      if (u < 0) break;
-      const Unit un = unit_at(a, tb, work, u);
-      const int blocks = uniform(un.kb1 - un.kb0);
-      const uint32_t n = (uint32_t)uniform(columns_of(un));
+      const Unit* const entry = take(qi);
+      if (!__all_sync(0xFFFFFFFFu, entry != nullptr)) break;
+      const int kind = uniform(entry->kind), blocks = uniform(entry->kb1 - entry->kb0);
+      const int rows = uniform(entry->n), kb0 = uniform(entry->kb0), shared = uniform(entry->shared);
+      taken(qi);
+      if (kind < 0) break;
+      // N: the chunk's rows (e4m3: their hi parts, then their lo parts)
+      const uint32_t n = FP8 ? 2 * ((rows + 7) & ~7) : (rows + 15) & ~15;
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
-      auto wait = [&](uint32_t bar, uint32_t phase) {
-        if (__all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, kTimeoutNs))) return;
+      int set = qi & 1;
+      uint32_t d = 0;
+      auto next_slot = [&] {  // the next accumulator of `set`, free
+        Walk<RING>& w = set ? accs[1] : accs[0];
+        if (w.wait()) {
+          d = tmem + (set * RING + w.s) * C::SLOT_COLS;
+          tc_fence_after();
+          return true;
+        }
         if (lane == 0) give_up();
-        ok = false;
+        return ok = false;
       };
-      // products ks0 .. ks1 - 1 of the ring's stage into the accumulator at d
-      auto products = [&](uint32_t d, int ks0, int ks1, bool fresh) {
-        const uint64_t wd = wdesc + (uint32_t)ring.s * (kTileBytes / 16);
-        const uint64_t bd = bdesc + (uint32_t)ring.s * (C::B_BYTES / 16);
+      auto slot_done = [&] {
+        Walk<RING>& w = set ? accs[1] : accs[0];
+        w.ask_next();
+        w.next();
+      };
+      if (!FP8 && !next_slot()) break;
+      for (int i = 0; i < blocks; ++i) {
+        if (FP8 && !next_slot()) break;
+        if (!ring.wait()) {
+          if (lane == 0) give_up();
+          ok = false;
+          break;
+        }
+        ring.ask_next();
+        tc_fence_after();
+        // e4m3, GEMM2: 64 rows of weights per scale of h (the last block may have 64 rows only)
+        const bool halves = FP8 && kind == 1;
+        const bool upper = !halves || (kb0 + i) * 128 + 64 < (shared ? a.Is : a.I);
+        if (elect_one()) {
+          const uint64_t wd = wdesc + (uint32_t)ring.s * (kTileBytes / 16);
+          const uint64_t bd = bdesc + (uint32_t)ring.s * (C::B_BYTES / 16);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          if (ks < ks0 || ks >= ks1) continue;
-          const uint32_t accumulate = fresh && ks == ks0 ? 0u : 1u;
-          if constexpr (FP8)
-            umma_e4m3(d, wd + ks * (2048 / 16), bd + ks * 2, idesc, accumulate);
-          else
-            umma_bf16(d, wd + ks * (2048 / 16), bd + ks * 2, idesc, accumulate);
+          for (int ks = 0; ks < 4; ++ks) {  // 16 (bf16) or 32 (e4m3) rows of weights
+            if (ks == 2 && !upper) break;
+            const uint64_t wk = wd + ks * (2048 / 16), bk = bd + ks * 2;
+            if constexpr (FP8)
+              umma_e4m3(halves && ks >= 2 ? d + 64 : d, wk, bk, idesc,
+                        ks == 0 || (halves && ks == 2) ? 0u : 1u);
+            else
+              umma_bf16(d, wk, bk, idesc, i == 0 && ks == 0 ? 0u : 1u);
+          }
+          umma_commit(empty(ring.s));
+          if (FP8 || i + 1 == blocks) umma_commit(acc_full(set, (set ? accs[1] : accs[0]).s));
         }
-      };
-      if constexpr (!FP8) {
-        const int set = qi & 1, acc = set ? used[1]++ : used[0]++;
-        const int slot = set * kRing + acc % kRing;
-        const uint32_t d = tmem + slot * 64;
-        wait(acc_empty(slot), ((acc / kRing) & 1) ^ 1);
-        for (int i = 0; i < blocks && ok; ++i) {
-          if (!ring.wait()) {
-            if (lane == 0) give_up();
-            ok = false;
-            break;
-          }
-          ring.ask_next();
-          tc_fence_after();
-          if (elect_one()) {
-            products(d, 0, 4, i == 0);
-            umma_commit(empty(ring.s));
-            if (i + 1 == blocks) umma_commit(acc_full(slot));
-          }
-          __syncwarp();
-          ring.next();
-        }
-      } else {
-        // an accumulator per scale, 128 rows of up or 64 of down, for the two sets in turn
-        const bool up = u < work.t1s;
-        int to = qi & 1, left = uniform(slots_of(un));
-        auto accumulate = [&](int ks0, int ks1) {  // the next accumulator: these products
-          const int n_used = to ? used[1] : used[0];
-          const int slot = to * kRing + n_used % kRing;
-          wait(acc_empty(slot), ((n_used / kRing) & 1) ^ 1);
-          if (!ok) return;
-          tc_fence_after();
-          if (elect_one()) {
-            products(tmem + slot * 64, ks0, ks1, true);
-            umma_commit(acc_full(slot));
-          }
-          __syncwarp();
-          if (to) ++used[1]; else ++used[0];
-          to ^= 1;
-          --left;
-        };
-        for (int i = 0; i < blocks && ok; ++i) {
-          if (!ring.wait()) {
-            if (lane == 0) give_up();
-            ok = false;
-            break;
-          }
-          ring.ask_next();
-          tc_fence_after();
-          if (up) {
-            accumulate(0, 4);
-          } else {
-            accumulate(0, 2);
-            if (ok && left > 0) accumulate(2, 4);  // (the last 128 rows of h may be 64)
-          }
-          if (!ok) break;
-          if (elect_one()) umma_commit(empty(ring.s));
-          __syncwarp();
-          ring.next();
+        __syncwarp();
+        ring.next();
+        if (FP8) {
+          slot_done();
+          set ^= 1;
         }
       }
+      if (!FP8 && ok) slot_done();
     }
     if (elect_one()) umma_commit(mma_done);
     __syncwarp();
@@ -782,56 +787,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     // each on every second accumulator; the unit's owner (in turn) adds the other's sums.
     const int set = (warp - kFirstEpilogue) >> 2, q = warp & 3;  // q: the warp's quarter of the lanes
     const int col = q * 32 + lane;  // of the unit's 128
+    const uint32_t tmem_q = tmem + set * RING * C::SLOT_COLS + ((uint32_t)(q * 32) << 16);
     int acc = 0;                    // accumulators taken from this set's ring
     int x_uses[2] = {0, 0};         // uses of each set's exchange buffer
     int up_units = 0;               // GEMM1 units that this set finished
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
-      const int u = take(qi);
-      __syncwarp();
-      if (u == -2) {
+      const Unit* const entry = take(qi);
+      if (entry == nullptr) {
         ok = false;
         break;
       }
-      if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
-      if (u < 0) break;
+      const Unit un = *entry;
+      taken(qi);
+      if (un.kind < 0) break;
       const int owner = qi & 1;
       if (!FP8 && owner != set) continue;
-      const Unit un = unit_at(a, tb, work, u);
-      float* const ex = exchange + owner * kChunk * kCols;
+      float* const ex = exchange + owner * kChunk * kCols + col;
       const int n8 = (un.n + 7) & ~7;
       const int I = un.shared ? a.Is : a.I, nt64 = (I + 63) / 64;
       auto wait = [&](uint32_t bar, uint32_t phase) {
         if (mbar_wait(bar, phase, kTimeoutNs)) return true;
         if (lane == 0) give_up();
-        ok = false;
-        return false;
+        return ok = false;
       };
-      float v[kChunk];
+      // this thread's column of rows j .. j + 7: GEMM1 to the exchange, GEMM2 to the partial rows
+      const int c2 = un.tile * kCols + col;
+      float* const o = (un.shared ? a.s_o + (int64_t)un.split * a.T * a.H
+                                  : a.o + (int64_t)un.split * a.S * a.H) +
+                       (int64_t)un.row0 * a.H + c2;
+      auto emit = [&](const float* v, int j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (j + i >= un.n) continue;
+          if (un.kind == 0)
+            ex[(j + i) * kCols] = v[i];
+          else if (c2 < a.H)
+            o[(int64_t)(j + i) * a.H] = v[i];
+        }
+      };
       if constexpr (!FP8) {
-        const int s = set * kRing + acc % kRing;
-        if (!wait(acc_full(s), (acc / kRing) & 1)) break;
+        if (un.kind == 0) {
+          const int use = owner ? x_uses[1]++ : x_uses[0]++;
+          if (!wait(x_empty(owner), (use & 1) ^ 1)) break;
+        }
+        if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) break;
         tc_fence_after();
-        const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
-#pragma unroll
-        for (int j = 0; j < kChunk / 8; ++j) {
-          if (8 * j >= n8) continue;
+        const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
+#pragma unroll 1
+        for (int j = 0; j < n8; j += 8) {
           uint32_t r[8];
-          tmem_ld_32x8(d + 8 * j, r);
+          tmem_ld_32x8(d + j, r);
           tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[8 * j + i] = __uint_as_float(r[i]);
+          emit(reinterpret_cast<const float*>(r), j);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty(s));
+        if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
         ++acc;
       } else {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) v[i] = 0.f;
         // This warp's columns lie in one or two blocks of 128 (its first and last column's); lane
         // i holds their scales of the i-th of 32 row blocks, so that the accumulators of a unit
-        // never wait for a scale from HBM. GEMM2: lane n holds row n's scales of h, one per 64.
+        // never wait for a scale from HBM. GEMM2: lane n holds row n's two scales of h.
         const int q0 = un.kind == 0 ? (q < 2 ? un.tile * 64 + q * 32 : I + un.tile * 64 + q * 32 - 64)
                                     : un.tile * kCols + q * 32;
         const int cols = un.kind == 0 ? 2 * I : a.H, nb = (cols + 127) / 128;
@@ -841,20 +858,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         sc += (int64_t)un.e * row_blocks * nb;
         const int b0 = min(q0 / 128, nb - 1), b1 = min((q0 + 31) / 128, nb - 1);
         const bool second = (q0 + lane) / 128 > q0 / 128;  // this lane's column is in the latter
-        const int per = un.kind == 0 ? 0 : 1;  // 2^per accumulators per 128 rows
-        const int first = set ^ owner, slots = (slots_of(un) - first + 1) >> 1;  // this set's
+        const int first = un.kb0 + (set ^ owner);          // this set's blocks: first, first + 2, ...
         const float* hs = (un.shared ? a.s_h_scale : a.h_scale) +
-                          (int64_t)(un.row0 + min(lane, un.n - 1)) * nt64 + 2 * un.kb0 + first;
-        float sc0 = 0.f, sc1 = 0.f, hv[4] = {1.f, 1.f, 1.f, 1.f};
-        int group = 0;  // of 32 row blocks
-        auto load_scales = [&] {
-          const int kb = un.kb0 + 32 * group + lane;
-          if (kb < un.kb1) {
-            sc0 = __ldg(sc + (int64_t)kb * nb + b0);
-            sc1 = __ldg(sc + (int64_t)kb * nb + b1);
-          }
-        };
-        load_scales();
+                          (int64_t)(un.row0 + min(lane, un.n - 1)) * nt64;
+        float sc0 = 0.f, sc1 = 0.f, hs0 = 1.f, hs1 = 1.f, hs0_next = 1.f, hs1_next = 1.f;
         if (un.kind == 1) {  // the scales of h come with its rows
           const int target = 4 * (un.shared ? work.nt1s : work.nt1);
           int there = 1;
@@ -864,80 +871,85 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             ok = false;
             break;
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < slots) hv[i] = __ldcg(hs + 2 * i);
         }
-        for (int i0 = 0; i0 < slots && ok; i0 += 4) {
+        auto load_hs = [&](int kb) {
+          if (un.kind == 0 || kb >= un.kb1) return;
+          hs0_next = __ldcg(hs + 2 * kb);
+          if (2 * kb + 1 < nt64) hs1_next = __ldcg(hs + 2 * kb + 1);
+        };
+        load_hs(first);
+        // G groups of 8 rows
+        auto unit = [&](auto groups) {
+          constexpr int G = decltype(groups)::value;
+          float v[8 * G];
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const int i = i0 + k4;
-            if (i >= slots) break;
-            const int blk = (2 * i + first) >> per;
-            if (blk >> 5 != group) {
-              group = blk >> 5;
-              load_scales();
+          for (int i = 0; i < 8 * G; ++i) v[i] = 0.f;
+          int loaded = -1;  // group of 32 row blocks whose scales the lanes hold
+#pragma unroll 1
+          for (int kb = first; kb < un.kb1; kb += 2, ++acc) {
+            const int blk = kb - un.kb0;
+            if (blk >> 5 != loaded) {
+              loaded = blk >> 5;
+              const int at = un.kb0 + 32 * loaded + lane;
+              if (at < un.kb1) {
+                sc0 = __ldg(sc + (int64_t)at * nb + b0);
+                sc1 = __ldg(sc + (int64_t)at * nb + b1);
+              }
             }
+            hs0 = hs0_next;
+            hs1 = hs1_next;
+            load_hs(kb + 2);
             const float w0 = __shfl_sync(0xFFFFFFFFu, sc0, blk & 31);
             const float w1 = __shfl_sync(0xFFFFFFFFu, sc1, blk & 31);
-            const float ws = second ? w1 : w0, hscale = hv[k4];
-            if (un.kind == 1 && i + 4 < slots) hv[k4] = __ldcg(hs + 2 * (i + 4));
-            const int s = set * kRing + acc % kRing;
-            if (!wait(acc_full(s), (acc / kRing) & 1)) break;
+            const float ws = second ? w1 : w0;
+            if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
             tc_fence_after();
-            const uint32_t d = tmem + s * 64 + ((uint32_t)(q * 32) << 16);
+            const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
+            const int halves = un.kind == 0 ? 1 : min(2, nt64 - 2 * kb);
+#pragma unroll 1
+            for (int half = 0; half < halves; ++half) {
+              uint32_t hi[8 * G], lo[8 * G];
 #pragma unroll
-            for (int j = 0; j < kChunk / 8; ++j) {
-              if (8 * j >= n8) continue;
-              uint32_t hi[8], lo[8];
-              tmem_ld_32x8(d + 8 * j, hi);
-              tmem_ld_32x8(d + n8 + 8 * j, lo);
+              for (int j = 0; j < G; ++j) {
+                tmem_ld_32x8(d + half * 64 + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(hi + 8 * j));
+                tmem_ld_32x8(d + half * 64 + 8 * (G + j),
+                             *reinterpret_cast<uint32_t(*)[8]>(lo + 8 * j));
+              }
               tmem_ld_wait();
+              const float h = half ? hs1 : hs0;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float p = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k]));
-                const float f = un.kind == 1 ? ws * __shfl_sync(0xFFFFFFFFu, hscale, 8 * j + k) : ws;
-                v[8 * j + k] = fmaf(f, p, v[8 * j + k]);
+              for (int i = 0; i < 8 * G; ++i) {
+                const float p = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                v[i] = fmaf(ws * __shfl_sync(0xFFFFFFFFu, h, i), p, v[i]);
               }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(s));
-            ++acc;
+            if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
           }
-        }
+          const int use = owner ? x_uses[1]++ : x_uses[0]++;
+          if (set != owner) {  // hand the sums over
+            if (!wait(x_empty(owner), (use & 1) ^ 1)) return;
+#pragma unroll
+            for (int i = 0; i < 8 * G; ++i) ex[i * kCols] = v[i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(handed(owner));
+            return;
+          }
+          if (!wait(handed(owner), use & 1)) return;
+#pragma unroll
+          for (int i = 0; i < 8 * G; ++i) v[i] += ex[i * kCols];
+#pragma unroll
+          for (int j = 0; j < G; ++j) emit(v + 8 * j, 8 * j);
+        };
+        if (n8 == 8) unit(std::integral_constant<int, 1>());
+        else if (n8 == 16) unit(std::integral_constant<int, 2>());
+        else if (n8 == 24) unit(std::integral_constant<int, 3>());
+        else unit(std::integral_constant<int, 4>());
         if (!ok) break;
-        const int use = owner ? x_uses[1]++ : x_uses[0]++;
-        if (set != owner) {  // hand the sums over
-          if (!wait(x_empty(owner), (use & 1) ^ 1)) break;
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i)
-            if (i < un.n) ex[i * kCols + col] = v[i];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(handed(owner));
-          continue;
-        }
-        if (!wait(handed(owner), use & 1)) break;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-          if (i < un.n) v[i] += ex[i * kCols + col];
-        if (un.kind == 0) {  // the tokens' scales
-          const float xs = lane < un.n
-                               ? a.x_scale[un.shared ? un.row0 + lane : tb.tok[un.row0 + lane]] : 0.f;
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i)
-            if (i < n8) v[i] *= __shfl_sync(0xFFFFFFFFu, xs, i);
-        }
+        if (set != owner) continue;
       }
       if (un.kind == 1) {
-        float* o = un.shared ? a.s_o + (int64_t)un.split * a.T * a.H
-                             : a.o + (int64_t)un.split * a.S * a.H;
-        const int c = un.tile * kCols + col;
-        if (c < a.H) {
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i)
-            if (i < un.n) o[(int64_t)(un.row0 + i) * a.H + c] = v[i];
-        }
         __syncwarp();
         if (lane == 0) {
           if (FP8) mbar_arrive(x_empty(owner));
@@ -947,23 +959,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       }
       // GEMM1: columns 0..63 are gate, 64..127 up of the same 64; the set's warps meet in shared
       // memory and take the rows in turn, two columns per lane
-      if (!FP8) {
-        const int use = owner ? x_uses[1]++ : x_uses[0]++;
-        if (!wait(x_empty(owner), (use & 1) ^ 1)) break;
-      }
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i)
-        if (i < un.n) ex[i * kCols + col] = v[i];
       __syncwarp();
       if (lane == 0) mbar_arrive(x_full(owner));
       if (!wait(x_full(owner), up_units & 1)) break;
       ++up_units;
       const int c = un.tile * 64 + 2 * lane;
+#pragma unroll 1
       for (int i = q; i < un.n; i += 4) {
         const int row = un.row0 + i;
         const float w = un.shared ? 1.f : tb.w[row];
-        const float2 g = *reinterpret_cast<const float2*>(ex + i * kCols + 2 * lane);
-        const float2 l = *reinterpret_cast<const float2*>(ex + i * kCols + 64 + 2 * lane);
+        const float* x = exchange + (owner * kChunk + i) * kCols + 2 * lane;
+        float2 g = *reinterpret_cast<const float2*>(x), l = *reinterpret_cast<const float2*>(x + 64);
+        if (FP8) {
+          const float xs = __ldcg(a.x_scale + (un.shared ? row : tb.tok[row]));
+          g.x *= xs, g.y *= xs, l.x *= xs, l.y *= xs;
+        }
         float h0 = w * (g.x * sigmoidf_(g.x) * l.x), h1 = w * (g.y * sigmoidf_(g.y) * l.y);
         if constexpr (FP8) {
           if (c >= I) h0 = h1 = 0.f;
@@ -997,7 +1007,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     }
     // ------------------------------------------------ sums of the partial rows
     const int target = 4 * (work.nc * work.split + work.ncs * work.splits);
-    const int routed = a.K * work.split, all = routed + (work.ncs > 0 ? work.splits : 0);
     for (int task = (warp - kFirstEpilogue) * (int)gridDim.x + (int)blockIdx.x;
          ok && task < a.T * work.nt2; task += 8 * (int)gridDim.x) {
       const int t = task / work.nt2, tile = task - t * work.nt2, c = tile * kCols + lane * 4;
@@ -1008,24 +1017,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         break;
       }
       if (c >= a.H) continue;
-      // rows in slot order, a slot's parts in order; 8 loads in flight
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < all; i0 += 8) {
-        float4 r8[8];
+      // part by part, a part's rows in slot order with 8 loads in flight; then the shared expert
+#pragma unroll 1
+      for (int p = 0; p < work.split; ++p) {
+        const float* o = a.o + (int64_t)p * a.S * a.H + c;
+#pragma unroll 1
+        for (int k0 = 0; k0 < a.K; k0 += 8) {
+          float4 r[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int j = i0 + r;
-          r8[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j >= all) continue;
-          const int k = j / work.split;
-          const float* p =
-              j < routed ? a.o + ((int64_t)(j - k * work.split) * a.S + tb.row[t * a.K + k]) * a.H
-                         : a.s_o + ((int64_t)(j - routed) * a.T + t) * a.H;
-          r8[r] = __ldcg(reinterpret_cast<const float4*>(p + c));
+          for (int i = 0; i < 8; ++i) {
+            r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + i < a.K)
+              r[i] = __ldcg(reinterpret_cast<const float4*>(
+                  o + (int64_t)tb.row[t * a.K + k0 + i] * a.H));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s.x += r[i].x, s.y += r[i].y, s.z += r[i].z, s.w += r[i].w;
         }
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          s.x += r8[r].x, s.y += r8[r].y, s.z += r8[r].z, s.w += r8[r].w;
+      }
+#pragma unroll 1
+      for (int p = 0; p < (work.ncs > 0 ? work.splits : 0); ++p) {
+        const float4 r = __ldcg(reinterpret_cast<const float4*>(a.s_o + ((int64_t)p * a.T + t) * a.H + c));
+        s.x += r.x, s.y += r.y, s.z += r.z, s.w += r.w;
       }
       *reinterpret_cast<uint2*>(a.y + (int64_t)t * a.H + c) =
           make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
@@ -1036,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   __syncthreads();
   if (warp == 3) {
     tc_fence_after();
-    tmem_dealloc(tmem, kSlots * 64);
+    tmem_dealloc(tmem, 512);
   }
 }
 
