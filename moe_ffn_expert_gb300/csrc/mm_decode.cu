@@ -66,6 +66,18 @@ struct Cfg {
   // a stage of e4m3 weights 64 (hi and lo parts of 32 rows), twice with the two scales of h
   static constexpr int SLOT_COLS = FP8 ? 128 : 64;
   static constexpr int RING = 512 / SLOT_COLS / 2;
+  // Scales of the last stages. Entry n is rewritten for stage n + SCALES, whose loads start when
+  // the products of stage n + SCALES - STAGES are done. Those had a free accumulator: of the two
+  // that a set has, and the sets take stages in turn but for one repetition where a unit follows
+  // another, so what either set has not read yet began at most 2 RING + 3 stages before them.
+  static constexpr int SCALES = 16;
+  static_assert(!FP8 || SCALES >= STAGES + 2 * RING + 4, "scale entries");
+};
+
+// What the e4m3 epilogue multiplies a stage's products with.
+struct Scales {
+  float h[2][kChunk];  // GEMM2: the rows' scales of h for the stage's two blocks of 64
+  float w[4];          // the columns' block of weights: gate or down; up (first and second block)
 };
 
 // int32 words at the start of the workspace (zeroed by k_logits)
@@ -84,8 +96,8 @@ struct DecodeArgs {
   int* hdr;
   int *ready1, *ready2;
   void *h, *s_h;           // bf16 [S, I], [T, Is]; e4m3: [2, S, I], [2, T, Is]
-  const float* x_scale;    // e4m3: [T], [S, ceil(I / 64)], [T, ceil(Is / 64)]
-  float *h_scale, *s_h_scale;
+  const float* x_scale;    // e4m3: [T]
+  float *h_scale, *s_h_scale;  // e4m3: [chunk][ceil(I / 64)][32]
   float *o, *s_o;          // [split][S, H], [split][T, H]
   int T, H, I, E, K, S, Is, score, normalize, route;
   float scale;
@@ -108,6 +120,7 @@ struct Building {
   int16_t id[kMaxSlots];       // expert of a slot
   uint8_t rank[kMaxSlots];     // slots of the same expert before it in its batch of 32
   uint32_t count[kMaxE];       // slots | chunks << 16, then the exclusive sums
+  uint32_t warp_sum[32];
   // then uint16_t [batches][E]: an expert's slots per batch, then those of the batches before; and
   // with a router fp32 [T][E] logits
 };
@@ -123,6 +136,21 @@ struct Unit {
 struct Work {
   int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, total;
 };
+
+// 4 bytes to shared memory, counted on `bar` when they are there.
+__device__ __forceinline__ void copy4_arrive(uint32_t dst, const float* src, uint32_t bar) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 
 // A value that all lanes share, in the form the compiler knows to be shared.
 __device__ __forceinline__ int uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
@@ -222,11 +250,12 @@ __device__ void split_row(const LogitArgs& a, int t, float* red) {
   }
 }
 
-// 4 experts x 4 tokens per block, H dealt to the 8 warps; the 16 sums of a warp's lanes are
-// reduced by halving exchanges, the warps' sums in order.
-template <typename RT>
+// N experts x N tokens per block, H dealt to the 8 warps; the N^2 sums of a warp's lanes are
+// reduced by halving exchanges, the warps' sums in order. N = 4 reads x and the router 4 times
+// less; N = 1 is a quarter of the code, which costs more than its reads when they are few.
+template <typename RT, int N>
 __global__ void __launch_bounds__(256) k_logits(LogitArgs a) {
-  __shared__ float part[8][16];
+  __shared__ float part[8][N * N < 8 ? 8 : N * N];
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -235,33 +264,34 @@ __global__ void __launch_bounds__(256) k_logits(LogitArgs a) {
     if (a.x8 != nullptr) split_row(a, (int)blockIdx.x - a.logit_blocks, &part[0][0]);
     return;
   }
-  const int eb = (a.E + 3) / 4;
-  const int e0 = (int)blockIdx.x % eb * 4, t0 = (int)blockIdx.x / eb * 4;
-  float acc[16];
+  const int eb = (a.E + N - 1) / N;
+  const int e0 = (int)blockIdx.x % eb * N, t0 = (int)blockIdx.x / eb * N;
+  float acc[N * N];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int i = 0; i < N * N; ++i) acc[i] = 0.f;
+#pragma unroll 1
   for (int c = tid * 8; c < a.H; c += 256 * 8) {
-    float w[4][8], x[4][8];
+    float w[N][8], x[N][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       load_vec<8>(static_cast<const RT*>(a.router) + (int64_t)min(e0 + i, a.E - 1) * a.H + c, w[i]);
       load_vec<8>(a.x + (int64_t)min(t0 + i, a.T - 1) * a.H + c, x[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[i * 4 + j] = fmaf(w[i][k], x[j][k], acc[i * 4 + j]);
+        for (int k = 0; k < 8; ++k) acc[i * N + j] = fmaf(w[i][k], x[j][k], acc[i * N + j]);
   }
-  const float s = warp_sum_many<16>(acc, lane);
-  if ((lane & 1) == 0) part[warp][lane >> 1] = s;
+  const float s = warp_sum_many<N * N>(acc, lane);
+  if (lane % (32 / (N * N)) == 0) part[warp][lane / (32 / (N * N))] = s;
   __syncthreads();
-  if (tid < 16) {
+  if (tid < N * N) {
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v += part[i][tid];
-    const int e = e0 + (tid >> 2), t = t0 + (tid & 3);
+    const int e = e0 + tid / N, t = t0 + tid % N;
     if (e < a.E && t < a.T) a.logits[(int64_t)t * a.E + e] = v;
   }
 }
@@ -396,7 +426,11 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
     }
   }
   __syncthreads();
-  for (int e = tid; e < a.E; e += kThreads) {
+  // slots (low half) and chunks (high half) of the experts before, summed over the block; a thread
+  // takes up to three consecutive experts
+  const int per = (a.E + kThreads - 1) / kThreads, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
+  uint32_t sum = 0;
+  for (int e = e0; e < e1; ++e) {
     uint32_t n = 0;
     for (int b = 0; b < batches; ++b) {
       const uint32_t here = before_batch[b * a.E + e];
@@ -404,34 +438,32 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
       n += here;
     }
     bd.count[e] = n | ((n + kChunk - 1) / kChunk) << 16;
+    sum += bd.count[e];
   }
-  __syncthreads();
-  if (warp == 0) {
-    // exclusive sums of slots (low half) and chunks (high half) over the experts; a lane takes
-    // consecutive experts
-    const int per = (a.E + 31) / 32, e0 = lane * per, e1 = min(a.E, e0 + per);
-    uint32_t sum = 0;
-    for (int e = e0; e < e1; ++e) sum += bd.count[e];
-    uint32_t before = sum;
+  uint32_t before = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, before, o);
-      if (lane >= o) before += v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) bd.warp_sum[warp] = before;
+  __syncthreads();
+  before -= sum;
+  const uint32_t others = lane < kThreads / 32 ? bd.warp_sum[lane] : 0u;
+  before += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? others : 0u);
+  const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, others);
+  if (tid == 0) tb.chunks = (int)(total >> 16);
+  for (int e = e0; e < e1; ++e) {
+    const uint32_t n = bd.count[e];
+    bd.count[e] = before;
+    const int first = (int)(before & 0xFFFFu), rows = (int)(n & 0xFFFFu);
+    for (int c = 0; c < (int)(n >> 16); ++c) {
+      const int at = (int)(before >> 16) + c;
+      tb.chunk_row[at] = (uint16_t)(first + c * kChunk);
+      tb.chunk_e[at] = (uint16_t)e;
+      tb.chunk_n[at] = (uint8_t)min(kChunk, rows - c * kChunk);
     }
-    if (lane == 31) tb.chunks = (int)(before >> 16);
-    before -= sum;
-    for (int e = e0; e < e1; ++e) {
-      const uint32_t n = bd.count[e];
-      bd.count[e] = before;
-      const int first = (int)(before & 0xFFFFu), rows = (int)(n & 0xFFFFu);
-      for (int c = 0; c < (int)(n >> 16); ++c) {
-        const int at = (int)(before >> 16) + c;
-        tb.chunk_row[at] = (uint16_t)(first + c * kChunk);
-        tb.chunk_e[at] = (uint16_t)e;
-        tb.chunk_n[at] = (uint8_t)min(kChunk, rows - c * kChunk);
-      }
-      before += n;
-    }
+    before += n;
   }
   __syncthreads();
   for (int s = tid; s < a.S; s += kThreads) {
@@ -520,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
   __shared__ Unit queue[kQueue];
-  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 4 * RING + 6 + 1];
+  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 4 * RING + 6 + 1 + (FP8 ? C::SCALES : 0)];
+  __shared__ alignas(128) Scales scales[FP8 ? C::SCALES : 1];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the stages' weights and rows (1024-byte aligned for the swizzle), then [row][128 columns] of
@@ -541,7 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   auto x_empty = [&](int s) { return bar0 + 8u * (X + 2 + s); };
   auto handed = [&](int s) { return bar0 + 8u * (X + 4 + s); };
   const uint32_t mma_done = bar0 + 8u * (X + 6);
+  auto scales_full = [&](int s) { return bar0 + 8u * (X + 7 + s); };
   if (tid == 0) {
+    if (FP8)
+      for (int s = 0; s < C::SCALES; ++s) mbar_init(scales_full(s), 1 + 3);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 2);  // the weights' and the rows' producers
       mbar_init(empty(s), 1);
@@ -679,6 +715,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       }
       const uint32_t bytes = (FP8 ? 2 : 1) * groups * (un.kind == 0 ? 512 : 1024);
       const uint32_t to = rows_at + (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
+      // e4m3: lanes 0..2 fetch the weights' scales of a stage, lane 0 the rows' scales of h. A
+      // unit's columns lie in one block of 128; its up columns, I further, may lie in two.
+      const float *sc = nullptr, *hs = nullptr;
+      int sc_stride = 0, nt64 = 0;
+      if (FP8) {
+        const int I = un.shared ? a.Is : a.I, rows = un.kind == 0 ? a.H : I;
+        const int cols = un.kind == 0 ? 2 * I : a.H;
+        const int c = un.kind == 1 ? un.tile * kCols : un.tile * 64 + (lane == 0 ? 0 : I + (lane - 1) * 63);
+        sc_stride = (cols + 127) / 128;
+        sc = un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
+                          : (un.shared ? a.s_down_scale : a.down_scale);
+        sc += (int64_t)un.e * ((rows + 127) / 128) * sc_stride + min(c / 128, sc_stride - 1);
+        nt64 = (I + 63) / 64;
+        hs = un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * kChunk
+                       : a.h_scale + (int64_t)un.ready * nt64 * kChunk;
+      }
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
         if (!ring.wait()) {
           if (lane == 0) give_up();
@@ -687,6 +739,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         ring.ask_next();
         if (lane == 0) mbar_arrive_expect_tx(full(ring.s), bytes);
+        if (FP8) {
+          Scales& to_scales = scales[it % C::SCALES];
+          const uint32_t bar = scales_full(it % C::SCALES);
+          if (lane < 3) copy4_arrive(smem_u32(&to_scales.w[lane]), sc + (int64_t)kb * sc_stride, bar);
+          if (lane == 0) {
+            const uint32_t n = un.kind == 0 ? 0u : min(2, nt64 - 2 * kb) * kChunk * 4u;
+            mbar_arrive_expect_tx(bar, n);
+            if (n) bulk_load(smem_u32(&to_scales.h), hs + 2 * kb * kChunk, n, bar);
+          }
+        }
         __syncwarp();
         if (loads) {
           const uint32_t dst = to + ring.s * C::B_BYTES;
@@ -701,6 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     }
     for (int j = max(0, it - STAGES); j < it; ++j)
       mbar_wait(full(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
+    if (FP8)
+      for (int j = max(0, it - C::SCALES); j < it; ++j)
+        mbar_wait(scales_full(j % C::SCALES), (j / C::SCALES) & 1, kTimeoutNs);
   } else if (warp == 2) {
     // ------------------------------------------------ issues the products
     // The warp stays in step, an elected lane issues, and what an issue takes is known to be the
@@ -791,6 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     int acc = 0;                    // accumulators taken from this set's ring
     int x_uses[2] = {0, 0};         // uses of each set's exchange buffer
     int up_units = 0;               // GEMM1 units that this set finished
+    int stages = 0;                 // e4m3: stages of the units before
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
       const Unit* const entry = take(qi);
@@ -806,6 +872,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       float* const ex = exchange + owner * kChunk * kCols + col;
       const int n8 = (un.n + 7) & ~7;
       const int I = un.shared ? a.Is : a.I, nt64 = (I + 63) / 64;
+      float x_scale = 1.f;  // of row `lane`
+      if (FP8 && un.kind == 0 && lane < un.n)
+        x_scale = __ldcg(a.x_scale + (un.shared ? un.row0 + lane : tb.tok[un.row0 + lane]));
       auto wait = [&](uint32_t bar, uint32_t phase) {
         if (mbar_wait(bar, phase, kTimeoutNs)) return true;
         if (lane == 0) give_up();
@@ -846,62 +915,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
         ++acc;
       } else {
-        // This warp's columns lie in one or two blocks of 128 (its first and last column's); lane
-        // i holds their scales of the i-th of 32 row blocks, so that the accumulators of a unit
-        // never wait for a scale from HBM. GEMM2: lane n holds row n's two scales of h.
-        const int q0 = un.kind == 0 ? (q < 2 ? un.tile * 64 + q * 32 : I + un.tile * 64 + q * 32 - 64)
-                                    : un.tile * kCols + q * 32;
-        const int cols = un.kind == 0 ? 2 * I : a.H, nb = (cols + 127) / 128;
-        const float* sc = un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
-                                       : (un.shared ? a.s_down_scale : a.down_scale);
-        const int row_blocks = ((un.kind == 0 ? a.H : I) + 127) / 128;
-        sc += (int64_t)un.e * row_blocks * nb;
-        const int b0 = min(q0 / 128, nb - 1), b1 = min((q0 + 31) / 128, nb - 1);
-        const bool second = (q0 + lane) / 128 > q0 / 128;  // this lane's column is in the latter
-        const int first = un.kb0 + (set ^ owner);          // this set's blocks: first, first + 2, ...
-        const float* hs = (un.shared ? a.s_h_scale : a.h_scale) +
-                          (int64_t)(un.row0 + min(lane, un.n - 1)) * nt64;
-        float sc0 = 0.f, sc1 = 0.f, hs0 = 1.f, hs1 = 1.f, hs0_next = 1.f, hs1_next = 1.f;
-        if (un.kind == 1) {  // the scales of h come with its rows
-          const int target = 4 * (un.shared ? work.nt1s : work.nt1);
-          int there = 1;
-          if (lane == 0) there = wait_counter(a.ready1 + un.ready, target, kTimeoutNs);
-          if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
-            if (lane == 0) give_up();
-            ok = false;
-            break;
-          }
-        }
-        auto load_hs = [&](int kb) {
-          if (un.kind == 0 || kb >= un.kb1) return;
-          hs0_next = __ldcg(hs + 2 * kb);
-          if (2 * kb + 1 < nt64) hs1_next = __ldcg(hs + 2 * kb + 1);
-        };
-        load_hs(first);
+        // which of a stage's weight scales is this column's
+        const int up = I + un.tile * 64;  // first up column
+        const int which = un.kind == 1 || q < 2 ? 0 : (up + col - 64) / 128 == up / 128 ? 1 : 2;
+        const int first = un.kb0 + (set ^ owner);  // this set's blocks: first, first + 2, ...
         // G groups of 8 rows
         auto unit = [&](auto groups) {
           constexpr int G = decltype(groups)::value;
           float v[8 * G];
 #pragma unroll
           for (int i = 0; i < 8 * G; ++i) v[i] = 0.f;
-          int loaded = -1;  // group of 32 row blocks whose scales the lanes hold
 #pragma unroll 1
           for (int kb = first; kb < un.kb1; kb += 2, ++acc) {
-            const int blk = kb - un.kb0;
-            if (blk >> 5 != loaded) {
-              loaded = blk >> 5;
-              const int at = un.kb0 + 32 * loaded + lane;
-              if (at < un.kb1) {
-                sc0 = __ldg(sc + (int64_t)at * nb + b0);
-                sc1 = __ldg(sc + (int64_t)at * nb + b1);
-              }
-            }
-            hs0 = hs0_next;
-            hs1 = hs1_next;
-            load_hs(kb + 2);
-            const float w0 = __shfl_sync(0xFFFFFFFFu, sc0, blk & 31);
-            const float w1 = __shfl_sync(0xFFFFFFFFu, sc1, blk & 31);
-            const float ws = second ? w1 : w0;
+            const int at = stages + kb - un.kb0;
+            if (!wait(scales_full(at % C::SCALES), (at / C::SCALES) & 1)) return;
+            const Scales& sc = scales[at % C::SCALES];
+            const float ws = sc.w[which];
             if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
             tc_fence_after();
             const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
@@ -916,11 +945,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                              *reinterpret_cast<uint32_t(*)[8]>(lo + 8 * j));
               }
               tmem_ld_wait();
-              const float h = half ? hs1 : hs0;
 #pragma unroll
               for (int i = 0; i < 8 * G; ++i) {
                 const float p = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-                v[i] = fmaf(ws * __shfl_sync(0xFFFFFFFFu, h, i), p, v[i]);
+                v[i] = fmaf(un.kind == 0 ? ws : ws * sc.h[half][i], p, v[i]);
               }
             }
             tc_fence_before();
@@ -946,6 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         else if (n8 == 16) unit(std::integral_constant<int, 2>());
         else if (n8 == 24) unit(std::integral_constant<int, 3>());
         else unit(std::integral_constant<int, 4>());
+        stages += un.kb1 - un.kb0;
         if (!ok) break;
         if (set != owner) continue;
       }
@@ -966,12 +995,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const int c = un.tile * 64 + 2 * lane;
 #pragma unroll 1
       for (int i = q; i < un.n; i += 4) {
+        const float xs = FP8 ? __shfl_sync(0xFFFFFFFFu, x_scale, i) : 1.f;
         const int row = un.row0 + i;
         const float w = un.shared ? 1.f : tb.w[row];
         const float* x = exchange + (owner * kChunk + i) * kCols + 2 * lane;
         float2 g = *reinterpret_cast<const float2*>(x), l = *reinterpret_cast<const float2*>(x + 64);
         if (FP8) {
-          const float xs = __ldcg(a.x_scale + (un.shared ? row : tb.tok[row]));
           g.x *= xs, g.y *= xs, l.x *= xs, l.y *= xs;
         }
         float h0 = w * (g.x * sigmoidf_(g.x) * l.x), h1 = w * (g.y * sigmoidf_(g.y) * l.y);
@@ -991,7 +1020,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                 (uint16_t)(lo0 | lo1 << 8);
           }
           if (lane == 0)
-            (un.shared ? a.s_h_scale : a.h_scale)[(int64_t)row * nt64 + un.tile] = inv;
+            (un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * kChunk
+                       : a.h_scale + (int64_t)un.ready * nt64 * kChunk)[un.tile * kChunk + i] = inv;
         } else {
           if (c < I)
             *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(un.shared ? a.s_h : a.h) +
@@ -1147,8 +1177,8 @@ Layout layout(const mm_decode_desc& d) {
   const bool fp8 = d.weight_type == MM_E4M3;
   l.off_x8 = take(fp8 ? (size_t)m.T * m.H * 2 : 0);
   l.off_xs = take(fp8 ? (size_t)m.T * 4 : 0);
-  l.off_hs = take(fp8 ? S * ((m.I + 63) / 64) * 4 : 0);
-  l.off_shs = take(fp8 ? (size_t)m.T * ((d.shared_I + 63) / 64) * 4 : 0);
+  l.off_hs = take(fp8 ? S * ((m.I + 63) / 64) * kChunk * 4 : 0);
+  l.off_shs = take(fp8 ? (size_t)(kMaxT / kChunk) * ((d.shared_I + 63) / 64) * kChunk * 4 : 0);
   l.off_h = take(S * m.I * 2);
   l.off_sh = take((size_t)m.T * d.shared_I * 2);
   l.off_o = take((size_t)kMaxSplit * S * m.H * 4);
@@ -1299,16 +1329,18 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   a.normalize = d->normalize;
   a.scale = d->scale;
   a.route = w->router != nullptr;
-  la.logit_blocks = a.route ? (a.E + 3) / 4 * ((a.T + 3) / 4) : 0;
+  const int tile = m.T * m.E * m.H <= ((int64_t)2 << 20) + 65536 ? 1 : 4;  // k_logits' N
+  la.logit_blocks = a.route ? (int)((m.E + tile - 1) / tile * ((m.T + tile - 1) / tile)) : 0;
   if (fp8) {
     la.x8 = reinterpret_cast<uint8_t*>(ws + l.off_x8);
     la.x_scale = reinterpret_cast<float*>(ws + l.off_xs);
   }
   const dim3 grid((unsigned)std::max(1, la.logit_blocks + (fp8 ? a.T : 0)));
-  if (d->router_type == MM_BF16)
-    MM_TRY(launch_pdl(k_logits<__nv_bfloat16>, grid, dim3(256), 0, st, la));
-  else
-    MM_TRY(launch_pdl(k_logits<float>, grid, dim3(256), 0, st, la));
+  auto* const logits = d->router_type == MM_BF16
+                           ? (tile == 1 ? k_logits<__nv_bfloat16, 1> : k_logits<__nv_bfloat16, 4>)
+                           : (tile == 1 ? k_logits<float, 1> : k_logits<float, 4>);
+  MM_TRY(launch_pdl(logits, grid, dim3(256), 0, st, la));
+  const int sms = std::max(1, device_sm_count());
   if (a.route && m.T > kMaxRouted) {
     int32_t* ids = topk_ids ? topk_ids : reinterpret_cast<int32_t*>(ws + l.off_ids);
     float* weights = topk_weights ? topk_weights : reinterpret_cast<float*>(ws + l.off_weights);
@@ -1319,7 +1351,6 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
     a.ids = ids;
     a.weights = weights;
   }
-  const int sms = std::max(1, device_sm_count());
   if (fp8)
     MM_TRY(launch_experts<true>(a, sms, st));
   else

@@ -46,12 +46,18 @@ __device__ __forceinline__ int select_topk(uint32_t (&key)[NV], int K, int lane)
     for (int j = NV - 2; j >= 0; --j) at = key[j] == best ? j : at;
   };
   scan();
+#pragma unroll 1
   for (int k = 0; k < K; ++k) {
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, best == top)) - 1;
+    const uint32_t holders = __ballot_sync(0xFFFFFFFFu, best == top);
+    const int owner = __ffs(holders) - 1;
     const int e = __shfl_sync(0xFFFFFFFFu, lane * NV + at, owner);
     if (lane == k) mine = e;
-    if (lane == owner) {
+    if constexpr (NV <= 8) {  // in every lane: shorter than a branch of one
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] = lane == owner && j == at ? 0u : key[j];
+      scan();
+    } else if (lane == owner) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (j == at) key[j] = 0;
