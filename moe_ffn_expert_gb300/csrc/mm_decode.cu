@@ -7,7 +7,7 @@
 //             and zeroed counters for the second kernel;
 //   k_experts one CTA per SM. Every CTA derives the same routing tables from the logits (or the
 //             caller's ids) in shared memory, then takes work units from one global counter:
-//     GEMM1   (chunk of up to 32 rows of one expert, 64 gate + 64 up columns): w * silu(g) * u
+//     GEMM1   (chunk of up to 32 (e4m3: 16) rows of one expert, 64 gate + 64 up columns): w * silu(g) * u
 //     GEMM2   (chunk, 128 output columns, part of I): fp32 partial rows
 //   and when they are out, sums the partial rows of (token, 128 columns) tasks in slot order, dealt
 //   evenly to the warps of the grid.
@@ -48,7 +48,6 @@ namespace {
 
 constexpr int kMaxT = 64, kMaxSlots = 1024, kMaxE = 1024;
 constexpr int kMaxRouted = 12;    // tokens whose selection every CTA repeats, one per warp
-constexpr int kChunk = 32;        // rows of one expert per unit
 constexpr int kCols = 128;        // weight columns per unit
 constexpr int kMaxSplit = 4;      // parts of I per GEMM2 column tile
 constexpr int kTileBytes = 16384; // one stage of weights: 64 x 128 bf16 or 128 x 128 e4m3
@@ -59,24 +58,27 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <bool FP8>
 struct Cfg {
+  // Rows of one expert per unit. e4m3: 16, so that four accumulators fit per epilogue set; with two
+  // the sets' work at the end of a unit stopped the products.
+  static constexpr int CHUNK = FP8 ? 16 : 32;
   static constexpr int KB = FP8 ? 128 : 64;                 // k per stage: 128 bytes of a row
-  static constexpr int B_BYTES = (FP8 ? 2 : 1) * kChunk * 128;
-  static constexpr int STAGES = FP8 ? 7 : 8;
+  static constexpr int B_BYTES = 32 * 128;                  // rows (e4m3: hi and lo parts)
+  static constexpr int STAGES = FP8 ? 9 : 8;
   // accumulators in tensor memory, half of them per epilogue set: 32 columns for a bf16 unit; for
-  // a stage of e4m3 weights 64 (hi and lo parts of 32 rows), twice with the two scales of h
-  static constexpr int SLOT_COLS = FP8 ? 128 : 64;
+  // a stage of e4m3 weights 32 (hi and lo parts of 16 rows), twice with the two scales of h
+  static constexpr int SLOT_COLS = 64;
   static constexpr int RING = 512 / SLOT_COLS / 2;
   // Scales of the last stages. Entry n is rewritten for stage n + SCALES, whose loads start when
-  // the products of stage n + SCALES - STAGES are done. Those had a free accumulator: of the two
+  // the products of stage n + SCALES - STAGES are done. Those had a free accumulator of the RING
   // that a set has, and the sets take stages in turn but for one repetition where a unit follows
   // another, so what either set has not read yet began at most 2 RING + 3 stages before them.
-  static constexpr int SCALES = 16;
+  static constexpr int SCALES = 32;
   static_assert(!FP8 || SCALES >= STAGES + 2 * RING + 4, "scale entries");
 };
 
 // What the e4m3 epilogue multiplies a stage's products with.
 struct Scales {
-  float h[2][kChunk];  // GEMM2: the rows' scales of h for the stage's two blocks of 64
+  float h[2][Cfg<true>::CHUNK];  // GEMM2: the rows' scales of h for the stage's two blocks of 64
   float w[4];          // the columns' block of weights: gate or down; up (first and second block)
 };
 
@@ -134,7 +136,7 @@ struct Unit {
 
 // Work units in claiming order.
 struct Work {
-  int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, total;
+  int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, total, chunk;
 };
 
 // 4 bytes to shared memory, counted on `bar` when they are there.
@@ -341,7 +343,7 @@ __device__ void select_row(const DecodeArgs& a, Building& bd, const float* row, 
 
 // Routing tables of the CTA: the slots sorted by expert (stable), cut into chunks. The same in
 // every CTA. False if a caller's id is out of range.
-__device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
+__device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int chunk) {
   Building& bd = *reinterpret_cast<Building*>(ring);
   uint16_t* before_batch = reinterpret_cast<uint16_t*>(ring + sizeof(Building));
   float* ls = reinterpret_cast<float*>(ring + sizeof(Building));  // (used before it)
@@ -377,7 +379,7 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
       return false;
     }
   }
-  if (a.S <= 32) {  // one warp, one slot per lane; experts in the order of their first slots
+  if (a.S <= chunk) {  // one warp, one slot per lane; experts in the order of their first slots
     if (warp == 0) {
       const int e = lane < a.S ? bd.id[lane] : -1 - lane;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
@@ -437,7 +439,7 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
       before_batch[b * a.E + e] = (uint16_t)n;
       n += here;
     }
-    bd.count[e] = n | ((n + kChunk - 1) / kChunk) << 16;
+    bd.count[e] = n | ((n + chunk - 1) / (uint32_t)chunk) << 16;
     sum += bd.count[e];
   }
   uint32_t before = sum;
@@ -459,9 +461,9 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring) {
     const int first = (int)(before & 0xFFFFu), rows = (int)(n & 0xFFFFu);
     for (int c = 0; c < (int)(n >> 16); ++c) {
       const int at = (int)(before >> 16) + c;
-      tb.chunk_row[at] = (uint16_t)(first + c * kChunk);
+      tb.chunk_row[at] = (uint16_t)(first + c * chunk);
       tb.chunk_e[at] = (uint16_t)e;
-      tb.chunk_n[at] = (uint8_t)min(kChunk, rows - c * kChunk);
+      tb.chunk_n[at] = (uint8_t)min(chunk, rows - c * chunk);
     }
     before += n;
   }
@@ -484,7 +486,9 @@ __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
   constexpr int KB = Cfg<FP8>::KB;
   Work w;
   w.nc = chunks;
-  w.ncs = a.Is > 0 ? (a.T + kChunk - 1) / kChunk : 0;
+  constexpr int CHUNK = Cfg<FP8>::CHUNK;
+  w.ncs = a.Is > 0 ? (a.T + CHUNK - 1) / CHUNK : 0;
+  w.chunk = CHUNK;
   w.nt1 = (a.I + 63) / 64;
   w.nt1s = (a.Is + 63) / 64;
   w.nt2 = (a.H + kCols - 1) / kCols;
@@ -503,6 +507,14 @@ __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
   return w;
 }
 
+// u / d for 0 <= u < 2^21: a reciprocal and a correction instead of the integer division's code.
+__device__ __forceinline__ int div_small(int u, int d) {
+  int q = (int)__fdividef((float)u + 0.5f, (float)d);
+  if (q * d > u) --q;
+  if ((q + 1) * d <= u) ++q;
+  return q;
+}
+
 __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, const Work& w,
                                         int u) {
   Unit r;
@@ -515,7 +527,7 @@ __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, c
     r.kind = 0;
     r.shared = u >= w.t1;
     const int v = r.shared ? u - w.t1 : u, nt = r.shared ? w.nt1s : w.nt1;
-    c = v / nt;
+    c = div_small(v, nt);
     r.tile = v - c * nt;
     r.kb0 = 0;
     r.kb1 = w.kb_h;
@@ -524,16 +536,16 @@ __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, c
     r.shared = u >= w.t2;
     const int v = u - (r.shared ? w.t2 : w.t1s), sp = r.shared ? w.splits : w.split;
     const int kb = r.shared ? w.kb_is : w.kb_i;
-    c = v / (w.nt2 * sp);
+    c = div_small(v, w.nt2 * sp);
     const int rest = v - c * w.nt2 * sp;
-    r.tile = rest / sp;
+    r.tile = sp == 1 ? rest : div_small(rest, sp);
     r.split = rest - r.tile * sp;
-    r.kb0 = kb * r.split / sp;
-    r.kb1 = kb * (r.split + 1) / sp;
+    r.kb0 = sp == 1 ? 0 : div_small(kb * r.split, sp);
+    r.kb1 = sp == 1 ? kb : div_small(kb * (r.split + 1), sp);
   }
   if (r.shared) {
-    r.row0 = c * kChunk;
-    r.n = min(kChunk, a.T - r.row0);
+    r.row0 = c * w.chunk;
+    r.n = min(w.chunk, a.T - r.row0);
     r.e = 0;
     r.ready = w.nc + c;
   } else {
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
   __shared__ Unit queue[kQueue];
-  __shared__ uint64_t bars[2 * STAGES + 2 * kQueue + 4 * RING + 6 + 1 + (FP8 ? C::SCALES : 0)];
+  __shared__ uint64_t bars[2 * STAGES + 3 * kQueue + 4 * RING + 6 + 1 + (FP8 ? C::SCALES : 0)];
   __shared__ alignas(128) Scales scales[FP8 ? C::SCALES : 1];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -563,11 +575,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   const uint32_t rows_at = base + STAGES * kTileBytes;
   float* const exchange = reinterpret_cast<float*>(aligned + STAGES * (kTileBytes + C::B_BYTES));
   const uint32_t bar0 = smem_u32(bars);
-  constexpr int Q = 2 * STAGES, ACC = Q + 2 * kQueue, X = ACC + 4 * RING;
+  constexpr int Q = 2 * STAGES, ACC = Q + 3 * kQueue, X = ACC + 4 * RING;
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto q_full = [&](int s) { return bar0 + 8u * (Q + s); };
   auto q_empty = [&](int s) { return bar0 + 8u * (Q + kQueue + s); };
+  auto stored = [&](int s) { return bar0 + 8u * (Q + 2 * kQueue + s); };
   auto acc_full = [&](int set, int s) { return bar0 + 8u * (ACC + set * RING + s); };
   auto acc_empty = [&](int set, int s) { return bar0 + 8u * (ACC + (2 + set) * RING + s); };
   auto x_full = [&](int s) { return bar0 + 8u * (X + s); };
@@ -584,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     }
     for (int s = 0; s < kQueue; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 2 + 8);  // row loads, MMA, epilogue warps
+      mbar_init(q_empty(s), 3 + 8);  // row loads, MMA, releases, epilogue warps
+      mbar_init(stored(s), 4);
     }
     for (int s = 0; s < 2 * RING; ++s) {
       mbar_init(acc_full(0, s), 1);
@@ -608,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   }
   tc_fence_before();
   pdl_wait();
-  const bool good = build_tables(a, tb, aligned);  // (its barriers publish the mbarriers and tmem_slot)
+  const bool good = build_tables(a, tb, aligned, C::CHUNK);  // (its barriers publish the mbarriers and tmem_slot)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const Work work = make_work<FP8>(a, tb.chunks);
@@ -702,8 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           r[i] = lo + (un.shared ? row : tb.tok[row]);
         }
       } else {
-        // the chunk's rows of h: every epilogue warp counts once per GEMM1 unit
-        const int target = 4 * (un.shared ? work.nt1s : work.nt1);
+        // the chunk's rows of h: one count per GEMM1 unit
+        const int target = un.shared ? work.nt1s : work.nt1;
         int there = 1;
         if (lane == 0) there = wait_counter(a.ready1 + un.ready, target, kTimeoutNs);
         if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
@@ -728,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                           : (un.shared ? a.s_down_scale : a.down_scale);
         sc += (int64_t)un.e * ((rows + 127) / 128) * sc_stride + min(c / 128, sc_stride - 1);
         nt64 = (I + 63) / 64;
-        hs = un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * kChunk
-                       : a.h_scale + (int64_t)un.ready * nt64 * kChunk;
+        hs = un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * C::CHUNK
+                       : a.h_scale + (int64_t)un.ready * nt64 * C::CHUNK;
       }
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
         if (!ring.wait()) {
@@ -744,9 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           const uint32_t bar = scales_full(it % C::SCALES);
           if (lane < 3) copy4_arrive(smem_u32(&to_scales.w[lane]), sc + (int64_t)kb * sc_stride, bar);
           if (lane == 0) {
-            const uint32_t n = un.kind == 0 ? 0u : min(2, nt64 - 2 * kb) * kChunk * 4u;
+            const uint32_t n = un.kind == 0 ? 0u : min(2, nt64 - 2 * kb) * C::CHUNK * 4u;
             mbar_arrive_expect_tx(bar, n);
-            if (n) bulk_load(smem_u32(&to_scales.h), hs + 2 * kb * kChunk, n, bar);
+            if (n) bulk_load(smem_u32(&to_scales.h), hs + 2 * kb * C::CHUNK, n, bar);
           }
         }
         __syncwarp();
@@ -826,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             if (ks == 2 && !upper) break;
             const uint64_t wk = wd + ks * (2048 / 16), bk = bd + ks * 2;
             if constexpr (FP8)
-              umma_e4m3(halves && ks >= 2 ? d + 64 : d, wk, bk, idesc,
+              umma_e4m3(halves && ks >= 2 ? d + C::SLOT_COLS / 2 : d, wk, bk, idesc,
                         ks == 0 || (halves && ks == 2) ? 0u : 1u);
             else
               umma_bf16(d, wk, bk, idesc, i == 0 && ks == 0 ? 0u : 1u);
@@ -846,6 +860,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     if (elect_one()) umma_commit(mma_done);
     __syncwarp();
     mbar_wait(mma_done, 0, kTimeoutNs);
+  } else if (warp == 3) {
+    // ------------------------------------------------ releases the units' results
+    // What the epilogue warps stored (ordered before this warp by their arrivals) is released to
+    // the other CTAs here: a release waits until the stores are through, some 1000 cycles that
+    // would otherwise stand between an epilogue warp's units.
+    if (lane == 0) {
+      for (int qi = 0;; ++qi) {
+        const Unit* const entry = take(qi);
+        if (entry == nullptr || entry->kind < 0) break;
+        int* const counter = entry->kind == 0 ? a.ready1 + entry->ready : a.ready2 + entry->tile;
+        if (!mbar_wait(stored(qi % kQueue), (qi / kQueue) & 1, kTimeoutNs)) {
+          give_up();
+          break;
+        }
+        fence_proxy_async_global();
+        red_add_release_gpu(counter, 1);
+        mbar_arrive(q_empty(qi % kQueue));
+      }
+    }
   } else if (warp >= kFirstEpilogue) {
     // ------------------------------------------------ accumulators to h, partial rows and y
     // Two sets of four warps. bf16: they take the units in turn. e4m3: both work on every unit,
@@ -869,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       if (un.kind < 0) break;
       const int owner = qi & 1;
       if (!FP8 && owner != set) continue;
-      float* const ex = exchange + owner * kChunk * kCols + col;
+      float* const ex = exchange + owner * C::CHUNK * kCols + col;
       const int n8 = (un.n + 7) & ~7;
       const int I = un.shared ? a.Is : a.I, nt64 = (I + 63) / 64;
       float x_scale = 1.f;  // of row `lane`
@@ -940,8 +973,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
               uint32_t hi[8 * G], lo[8 * G];
 #pragma unroll
               for (int j = 0; j < G; ++j) {
-                tmem_ld_32x8(d + half * 64 + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(hi + 8 * j));
-                tmem_ld_32x8(d + half * 64 + 8 * (G + j),
+                tmem_ld_32x8(d + half * (C::SLOT_COLS / 2) + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(hi + 8 * j));
+                tmem_ld_32x8(d + half * (C::SLOT_COLS / 2) + 8 * (G + j),
                              *reinterpret_cast<uint32_t(*)[8]>(lo + 8 * j));
               }
               tmem_ld_wait();
@@ -971,9 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           for (int j = 0; j < G; ++j) emit(v + 8 * j, 8 * j);
         };
         if (n8 == 8) unit(std::integral_constant<int, 1>());
-        else if (n8 == 16) unit(std::integral_constant<int, 2>());
-        else if (n8 == 24) unit(std::integral_constant<int, 3>());
-        else unit(std::integral_constant<int, 4>());
+        else unit(std::integral_constant<int, 2>());
         stages += un.kb1 - un.kb0;
         if (!ok) break;
         if (set != owner) continue;
@@ -982,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         __syncwarp();
         if (lane == 0) {
           if (FP8) mbar_arrive(x_empty(owner));
-          red_add_release_gpu(a.ready2 + un.tile, 1);
+          mbar_arrive(stored(qi % kQueue));
         }
         continue;
       }
@@ -998,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         const float xs = FP8 ? __shfl_sync(0xFFFFFFFFu, x_scale, i) : 1.f;
         const int row = un.row0 + i;
         const float w = un.shared ? 1.f : tb.w[row];
-        const float* x = exchange + (owner * kChunk + i) * kCols + 2 * lane;
+        const float* x = exchange + (owner * C::CHUNK + i) * kCols + 2 * lane;
         float2 g = *reinterpret_cast<const float2*>(x), l = *reinterpret_cast<const float2*>(x + 64);
         if (FP8) {
           g.x *= xs, g.y *= xs, l.x *= xs, l.y *= xs;
@@ -1020,8 +1051,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                 (uint16_t)(lo0 | lo1 << 8);
           }
           if (lane == 0)
-            (un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * kChunk
-                       : a.h_scale + (int64_t)un.ready * nt64 * kChunk)[un.tile * kChunk + i] = inv;
+            (un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * C::CHUNK
+                       : a.h_scale + (int64_t)un.ready * nt64 * C::CHUNK)[un.tile * C::CHUNK + i] = inv;
         } else {
           if (c < I)
             *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(un.shared ? a.s_h : a.h) +
@@ -1032,14 +1063,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(x_empty(owner));
-        red_add_release_gpu(a.ready1 + un.ready, 1);
+        mbar_arrive(stored(qi % kQueue));
       }
     }
     // ------------------------------------------------ sums of the partial rows
-    const int target = 4 * (work.nc * work.split + work.ncs * work.splits);
+    const int target = work.nc * work.split + work.ncs * work.splits;
     for (int task = (warp - kFirstEpilogue) * (int)gridDim.x + (int)blockIdx.x;
          ok && task < a.T * work.nt2; task += 8 * (int)gridDim.x) {
-      const int t = task / work.nt2, tile = task - t * work.nt2, c = tile * kCols + lane * 4;
+      const int t = div_small(task, work.nt2), tile = task - t * work.nt2, c = tile * kCols + lane * 4;
       int there = 1;
       if (lane == 0) there = wait_counter(a.ready2 + tile, target, kTimeoutNs);
       if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
@@ -1168,7 +1199,7 @@ Layout layout(const mm_decode_desc& d) {
     off = (off + bytes + 255) / 256 * 256;
     return o;
   };
-  take((W_READY1 + S + 2) * 4);  // header, GEMM1 counters: a chunk has a row at least
+  take((W_READY1 + S + kMaxT / Cfg<true>::CHUNK) * 4);  // header, GEMM1 counters: a chunk has a row
   l.off_ready2 = take((size_t)((m.H + kCols - 1) / kCols) * 4);
   l.zero_words = (int)(off / 4);
   l.off_logits = take((size_t)(m.T * m.E) * 4);
@@ -1177,8 +1208,9 @@ Layout layout(const mm_decode_desc& d) {
   const bool fp8 = d.weight_type == MM_E4M3;
   l.off_x8 = take(fp8 ? (size_t)m.T * m.H * 2 : 0);
   l.off_xs = take(fp8 ? (size_t)m.T * 4 : 0);
-  l.off_hs = take(fp8 ? S * ((m.I + 63) / 64) * kChunk * 4 : 0);
-  l.off_shs = take(fp8 ? (size_t)(kMaxT / kChunk) * ((d.shared_I + 63) / 64) * kChunk * 4 : 0);
+  constexpr int chunk = Cfg<true>::CHUNK;
+  l.off_hs = take(fp8 ? S * ((m.I + 63) / 64) * chunk * 4 : 0);
+  l.off_shs = take(fp8 ? (size_t)(kMaxT / chunk) * ((d.shared_I + 63) / 64) * chunk * 4 : 0);
   l.off_h = take(S * m.I * 2);
   l.off_sh = take((size_t)m.T * d.shared_I * 2);
   l.off_o = take((size_t)kMaxSplit * S * m.H * 4);
@@ -1211,7 +1243,7 @@ bool row_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, bool 
 
 template <bool FP8>
 constexpr size_t dynamic_smem() {
-  return 1024 + Cfg<FP8>::STAGES * (kTileBytes + Cfg<FP8>::B_BYTES) + 2 * kChunk * kCols * 4;
+  return 1024 + Cfg<FP8>::STAGES * (kTileBytes + Cfg<FP8>::B_BYTES) + 2 * Cfg<FP8>::CHUNK * kCols * 4;
 }
 
 template <bool FP8>
