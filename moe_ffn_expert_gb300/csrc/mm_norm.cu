@@ -11,11 +11,19 @@
 // <e d, f> needs d, which needs <w_pre v, r'>; written out,
 //   <e d, f> = <e f, u> + q <e f, w_pre v> - q^3 / H <w_pre v, r'> <e f, r'>,
 // so the six sums of a row come from one reduction. Everything is elementwise otherwise: the
-// kernels are bound by HBM. A block holds a row in registers, so each tensor moves once.
+// kernels are bound by HBM.
+//
+// Two forms. Rows of 16-byte words, many of them: persistent blocks, 16 columns per thread, whose
+// rows arrive by bulk copies into a ring in shared memory several rows ahead, so that HBM stays
+// busy through the reductions; weights and the backward's column sums stay in registers
+// (k_norm_fwd_rows, k_norm_bwd_rows). Few rows, odd widths and widths above 7680: a row in
+// registers straight from global memory (k_norm_fwd, k_norm_bwd).
 #include <cuda_runtime.h>
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "../../include/mm_ops.h"
 #include "mm_kernels.h"
@@ -25,6 +33,7 @@ namespace mm {
 namespace {
 
 constexpr int kMaxH = 16384;
+constexpr int kMaxRingH = 7680;  // 15 warps of 16 columns per thread, and the one that loads
 
 struct NormArgs {
   int64_t T, rows_per_gate;  // rows_per_gate: T / groups (0: no gate)
@@ -238,6 +247,411 @@ __global__ void __launch_bounds__(1024) k_norm_bwd(NormArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------------- row rings
+
+// A stage holds one row of each tensor in use; offsets in bytes, -1: not in use.
+struct RowRing {
+  int x, f, u, v, g;  // residual (forward: r, backward: r'), branch, the two gradients, gate
+  int bytes, depth, tail;  // tail: bytes behind the stages (the backward's sums of d_post)
+};
+
+template <typename T>
+__device__ __forceinline__ const T* row_at(const uint8_t* stage, int offset, int c) {
+  return reinterpret_cast<const T*>(stage + offset) + c;
+}
+
+// The rows of a block, piece after piece (see NormArgs).
+struct RowWalk {
+  int64_t piece, group, t, t1;
+  __device__ __forceinline__ void start(const NormArgs& a, int64_t p) {
+    piece = p;
+    if (p >= a.pieces) return;
+    group = a.pieces_per_group == 1 ? p : p / a.pieces_per_group;
+    const int64_t first = (p - group * a.pieces_per_group) * a.piece_rows;
+    t = group * a.group_rows + first;
+    t1 = group * a.group_rows + min(first + a.piece_rows, a.group_rows);
+  }
+  __device__ __forceinline__ bool more(const NormArgs& a) const { return piece < a.pieces; }
+  __device__ __forceinline__ void next(const NormArgs& a) {
+    if (++t == t1) start(a, piece + gridDim.x);
+  }
+};
+
+// One thread: the copies of row t into a stage.
+template <typename ST, typename BT, typename PT>
+__device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, uint32_t stage,
+                                         uint32_t bar, int64_t t, int64_t group) {
+  const uint32_t sb = a.H * sizeof(ST), bb = a.H * sizeof(BT), pb = a.H * sizeof(PT);
+  mbar_arrive_expect_tx(bar, (r.x >= 0 ? sb : 0) + (r.f >= 0 ? bb : 0) + (r.u >= 0 ? sb : 0) +
+                                 (r.v >= 0 ? bb : 0) + (r.g >= 0 ? pb : 0));
+  if (r.x >= 0) bulk_load(stage + r.x, static_cast<const ST*>(a.r) + t * a.H, sb, bar);
+  if (r.f >= 0) bulk_load(stage + r.f, static_cast<const BT*>(a.f) + t * a.H, bb, bar);
+  if (r.u >= 0) bulk_load(stage + r.u, static_cast<const ST*>(a.u) + t * a.H, sb, bar);
+  if (r.v >= 0) bulk_load(stage + r.v, static_cast<const BT*>(a.v) + t * a.H, bb, bar);
+  if (r.g >= 0) bulk_load(stage + r.g, static_cast<const PT*>(a.gate) + group * a.H, pb, bar);
+}
+
+// A row kernel's last warp issues the copies (a stage's cost hundreds of cycles, which in one of
+// the working warps every row would wait for); the others work on the rows and meet at a barrier
+// of their own.
+__device__ __forceinline__ void row_barrier(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+
+template <typename ST, typename BT, typename PT>
+__device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& ring, uint32_t smem,
+                                             uint32_t full, uint32_t empty);
+
+// Row loads are this library's own copies from memory that the launch was given: the wait for one
+// cannot run out unless the device has failed. It is bounded all the same (2 s), and then goes on.
+constexpr uint64_t kRowTimeoutNs = 2000000000ull;
+
+// Sum over the block: partial sums of the warps in `red` (32 floats, zero beyond the block's
+// warps), read back by every thread.
+__device__ __forceinline__ float block_sum_1(float v, float* red, int threads) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  row_barrier(threads);
+  const float4* r4 = reinterpret_cast<const float4*>(red);
+  float s = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < (threads + 127) / 128; ++i) {
+    const float4 p = r4[i];
+    s += (p.x + p.y) + (p.z + p.w);
+  }
+  return s;
+}
+
+template <typename ST, typename BT, typename PT>
+__device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& ring, uint32_t smem,
+                                             uint32_t full, uint32_t empty) {
+  if ((threadIdx.x & 31) != 0) return;
+  RowWalk row;
+  row.start(a, blockIdx.x);
+  int s = 0;
+  uint32_t ph = 1;
+  while (row.more(a)) {
+    mbar_wait(empty + 8u * s, ph, kRowTimeoutNs);
+    load_row<ST, BT, PT>(a, ring, smem + s * ring.bytes, full + 8u * s, row.t, row.group);
+    row.next(a);
+    if (++s == ring.depth) s = 0, ph ^= 1u;
+  }
+}
+
+// What a thread does per row is the same for 8 columns as for 16 but for the columns themselves:
+// with 8, and single floats, 52 instructions went into an element of the forward, and the issue
+// slots ran out at 3.6 TB/s. A thread has columns 8 tid .. and 8 (tid + threads) ..; the loop works
+// on pairs of floats.
+constexpr int kVecs = 2;
+
+template <typename ST, typename BT, typename PT>
+__global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float red[2][32];
+  __shared__ uint64_t bars[16];
+  const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32, step = threads * 8,
+            c0 = tid * 8;
+  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+  if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
+  if (tid == 0) {
+    for (int i = 0; i < ring.depth; ++i) {
+      mbar_init(smem_u32(&bars[i]), 1);
+      mbar_init(smem_u32(&bars[8 + i]), threads / 32);
+    }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  if (tid >= threads) {
+    produce_rows<ST, BT, PT>(a, ring, smem_u32(smem), smem_u32(bars), smem_u32(bars + 8));
+    return;
+  }
+  RowWalk row;
+  row.start(a, blockIdx.x);
+  // weights: of the branch (times the gate, where that is the same for many rows) and of the norm
+  f32x2 wb[kVecs][4], wn[kVecs][4];
+  auto branch_weights = [&](int64_t group) {
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = c0 + k * step;
+      f32x2 g[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wb[k][i] = both(1.f);
+      if (c >= H) continue;
+      if (post) load_pairs(static_cast<const PT*>(a.w_post) + c, wb[k]);
+      if (a.gate != nullptr && ring.g < 0) {
+        load_pairs(static_cast<const PT*>(a.gate) + group * H + c, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wb[k][i] = mul(wb[k][i], g[i]);
+      }
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wn[k][i] = both(1.f);
+    if (pre && c0 + k * step < H) load_pairs(static_cast<const PT*>(a.w_pre) + c0 + k * step, wn[k]);
+  }
+  if (row.more(a)) branch_weights(row.group);
+  int64_t group = row.group;
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  const float rh = 1.f / (float)H;
+  const f32x2 scale = both(a.scale);
+  while (row.more(a)) {
+    const uint8_t* stage = smem + s * ring.bytes;
+    if (a.gate != nullptr && ring.g < 0 && row.group != group) branch_weights(group = row.group);
+    mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
+    f32x2 x[kVecs][4], y[kVecs][4], acc = both(0.f);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = c0 + k * step;
+      if (c >= H) continue;
+      load_pairs(row_at<ST>(stage, ring.x, c), x[k]);
+      if (ring.f >= 0) {
+        load_pairs(row_at<BT>(stage, ring.f, c), y[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[k][i] = both(0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc = fma(y[k][i], y[k][i], acc);
+    }
+    f32x2 q = both(1.f);
+    if (post) q = both(rsqrtf(block_sum_1(sum_of(acc), red[0], threads) * rh + a.eps));
+    acc = both(0.f);
+    const int64_t at = row.t * H + c0;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = c0 + k * step;
+      if (c >= H) continue;
+      if (ring.g >= 0) {
+        f32x2 g[4];
+        load_pairs(row_at<PT>(stage, ring.g, c), g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[k][i] = mul(y[k][i], g[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[k][i] = fma(mul(q, y[k][i]), wb[k][i], mul(scale, x[k][i]));
+        acc = fma(x[k][i], x[k][i], acc);
+      }
+      if (a.out != nullptr) store_pairs(static_cast<ST*>(a.out) + at + k * step, x[k]);
+    }
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
+    float sum = 0.f;
+    if (pre)
+      sum = block_sum_1(sum_of(acc), red[post ? 1 : flip], threads);
+    if (pre) {
+      q = both(rsqrtf(sum * rh + a.eps));
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        if (c0 + k * step >= H) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[k][i] = mul(mul(q, x[k][i]), wn[k][i]);
+        store_pairs(static_cast<BT*>(a.n) + at + k * step, x[k]);
+      }
+    }
+    row.next(a);
+    flip ^= 1;
+    if (++s == ring.depth) s = 0, ph ^= 1u;
+  }
+}
+
+// Sums of 8 values over the block; red: [warps][8]. Every warp adds up the warps' sums itself.
+__device__ __forceinline__ void block_sum_8(float (&v)[8], float* red, int threads) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = threads >> 5;
+  const float mine = warp_sum_many<8>(v, lane);  // of value lane / 4
+  if ((lane & 3) == 0) red[warp * 8 + (lane >> 2)] = mine;
+  row_barrier(threads);
+  float s = 0.f;
+  for (int w = lane >> 3; w < warps; w += 4) s += red[w * 8 + (lane & 7)];
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, s, i);
+}
+
+// A row is read from its stage twice, before and after its sums: its values in registers over the
+// reduction would leave no room for the column sums of 16 columns.
+// The gate is the same over a piece, so sum d f s gives both its gradient (times w_post) and, times
+// the gate, the piece's share of d_post.
+template <typename ST, typename BT, typename PT>
+__global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2][16 * 8];
+  __shared__ uint64_t bars[16];
+  const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32, step = threads * 8,
+            c0 = tid * 8;
+  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr, gated = a.gate != nullptr;
+  if (tid == 0) {
+    for (int i = 0; i < ring.depth; ++i) {
+      mbar_init(smem_u32(&bars[i]), 1);
+      mbar_init(smem_u32(&bars[8 + i]), threads / 32);
+    }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  if (tid >= threads) {
+    produce_rows<ST, BT, PT>(a, ring, smem_u32(smem), smem_u32(bars), smem_u32(bars + 8));
+    return;
+  }
+  RowWalk row;
+  row.start(a, blockIdx.x);
+  // weights: w_post times the gate, w_pre; column sums: of d f s over a piece, of v r' q, of d_post
+  f32x2 wg[kVecs][4], wn[kVecs][4], raw[kVecs][4], d_pre[kVecs][4];
+  float* const d_post = reinterpret_cast<float*>(smem + ring.depth * ring.bytes);  // [H]
+  auto branch_weights = [&](int k, int64_t group, const uint8_t* stage, f32x2 (&g)[4],
+                            f32x2 (&w)[4]) {
+    const int c = c0 + k * step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = w[i] = both(1.f);
+    if (c >= H) return;
+    if (post) load_pairs(static_cast<const PT*>(a.w_post) + c, w);
+    if (gated)
+      load_pairs(ring.g >= 0 ? row_at<PT>(stage, ring.g, c)
+                             : static_cast<const PT*>(a.gate) + group * H + c, g);
+  };
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      wn[k][i] = both(1.f);
+      raw[k][i] = d_pre[k][i] = both(0.f);
+    }
+    if (post && c0 + k * step < H) store_pairs(d_post + c0 + k * step, raw[k]);
+    if (pre && c0 + k * step < H) load_pairs(static_cast<const PT*>(a.w_pre) + c0 + k * step, wn[k]);
+  }
+  bool fresh = true;  // a piece begins
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  const float rh = 1.f / (float)H;
+  while (row.more(a)) {
+    const uint8_t* stage = smem + s * ring.bytes;
+    mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
+    if (fresh) {
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        f32x2 g[4], w[4];
+        branch_weights(k, row.group, stage, g, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wg[k][i] = mul(w[i], g[i]);
+      }
+      fresh = false;
+    }
+    // a row's values: r', branch, the gradients of r' and of n
+    auto read = [&](int c, f32x2 (&x)[4], f32x2 (&f)[4], f32x2 (&u)[4], f32x2 (&v)[4]) {
+      auto none = [](f32x2 (&z)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = both(0.f);
+      };
+      if (pre) {
+        load_pairs(row_at<ST>(stage, ring.x, c), x);
+        load_pairs(row_at<BT>(stage, ring.v, c), v);
+      } else {
+        none(x);
+        none(v);
+      }
+      if (ring.f >= 0) load_pairs(row_at<BT>(stage, ring.f, c), f); else none(f);
+      if (ring.u >= 0) load_pairs(row_at<ST>(stage, ring.u, c), u); else none(u);
+    };
+    f32x2 acc[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) acc[i] = both(0.f);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      if (c0 + k * step >= H) continue;
+      f32x2 x[4], f[4], u[4], v[4];
+      read(c0 + k * step, x, f, u, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 wv = mul(wn[k][i], v[i]), ef = mul(wg[k][i], f[i]);
+        acc[0] = fma(x[i], x[i], acc[0]);
+        acc[1] = fma(wv, x[i], acc[1]);
+        acc[2] = fma(f[i], f[i], acc[2]);
+        acc[3] = fma(ef, u[i], acc[3]);
+        acc[4] = fma(ef, wv, acc[4]);
+        acc[5] = fma(ef, x[i], acc[5]);
+      }
+    }
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = i < 6 ? sum_of(acc[i < 6 ? i : 0]) : 0.f;
+    block_sum_8(sum, red[flip], threads);
+    const float q = pre ? rsqrtf(sum[0] * rh + a.eps) : 0.f;
+    const float cq = q * q * q * rh * sum[1];
+    const float sf = post ? rsqrtf(sum[2] * rh + a.eps) : 1.f;
+    const float cs =
+        post ? sf * sf * sf * rh * (pre ? sum[3] + q * sum[4] - cq * sum[5] : sum[3]) : 0.f;
+    const f32x2 q2 = both(q), ncq = both(-cq), sf2 = both(sf), ncs = both(-cs), scale = both(a.scale);
+    const int64_t at = row.t * H + c0;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      if (c0 + k * step >= H) continue;
+      f32x2 x[4], f[4], u[4], v[4], dr[4];
+      read(c0 + k * step, x, f, u, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x2 d = u[i];
+        if (pre) {
+          const f32x2 xq = mul(q2, x[i]);
+          d = fma(ncq, x[i], fma(q2, mul(wn[k][i], v[i]), d));
+          d_pre[k][i] = fma(v[i], xq, d_pre[k][i]);
+        }
+        raw[k][i] = fma(d, mul(sf2, f[i]), raw[k][i]);
+        dr[i] = mul(scale, d);
+        f[i] = fma(ncs, f[i], mul(sf2, mul(wg[k][i], d)));
+      }
+      store_pairs(static_cast<ST*>(a.dr) + at + k * step, dr);
+      if (a.df != nullptr) store_pairs(static_cast<BT*>(a.df) + at + k * step, f);
+    }
+    if (row.t + 1 == row.t1) {  // the piece ends
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const int c = c0 + k * step;
+        if (c >= H) continue;
+        f32x2 g[4], w[4], sum_post[4];
+        branch_weights(k, row.group, stage, g, w);
+        if (post) {
+          load_pairs(d_post + c, sum_post);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum_post[i] = fma(g[i], raw[k][i], sum_post[i]);
+          store_pairs(d_post + c, sum_post);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = mul(w[i], raw[k][i]);
+          raw[k][i] = both(0.f);
+        }
+        if (!gated) continue;
+        if (a.part_gate != nullptr)
+          store_pairs(a.part_gate + row.piece * H + c, w);
+        else
+          store_pairs(static_cast<PT*>(a.d_gate) + row.group * H + c, w);
+      }
+      fresh = true;
+    }
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
+    row.next(a);
+    flip ^= 1;
+    if (++s == ring.depth) s = 0, ph ^= 1u;
+  }
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    const int c = c0 + k * step;
+    if (c >= H) continue;
+    if (post) {
+      f32x2 sum_post[4];
+      load_pairs(d_post + c, sum_post);
+      store_pairs(a.part_post + (int64_t)blockIdx.x * H + c, sum_post);
+    }
+    if (pre) store_pairs(a.part_pre + (int64_t)blockIdx.x * H + c, d_pre[k]);
+  }
+}
+
 inline bool aligned_to(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
@@ -256,21 +670,36 @@ mm_status check_desc(const mm_norm_desc* d) {
   return MM_OK;
 }
 
-// How the backward's tokens are dealt to blocks.
-struct BwdPlan {
+// How tokens are dealt to blocks.
+struct RowPlan {
   int64_t group_rows, piece_rows, pieces_per_group, pieces, blocks;
-  size_t off_post, off_pre, off_gate, total;
 };
 
-BwdPlan plan_bwd(const mm_norm_desc& d, int sms) {
-  BwdPlan p{};
+RowPlan plan_rows(const mm_norm_desc& d, int64_t target) {
+  RowPlan p{};
   const int64_t groups = std::max<int64_t>(1, d.groups);
-  const int64_t target = (int64_t)sms * 2;
   p.group_rows = d.T / groups;
   p.piece_rows = std::max<int64_t>(1, std::min(p.group_rows, (d.T + target - 1) / target));
   p.pieces_per_group = (p.group_rows + p.piece_rows - 1) / p.piece_rows;
   p.pieces = groups * p.pieces_per_group;
   p.blocks = std::min(p.pieces, target);
+  return p;
+}
+
+struct BwdPlan : RowPlan {
+  size_t off_post, off_pre, off_gate, total;
+};
+
+// Working threads of a block, 16 columns each, and the blocks that share an SM: 512 threads (the
+// registers of the column sums).
+inline int row_threads(int64_t H) { return (int)((H + 511) / 512 * 32); }
+inline int64_t blocks_per_sm(int64_t H) {
+  return std::max<int64_t>(1, 512 / (row_threads(std::min<int64_t>(H, kMaxRingH)) + 32));
+}
+
+BwdPlan plan_bwd(const mm_norm_desc& d, int sms) {
+  BwdPlan p{};
+  static_cast<RowPlan&>(p) = plan_rows(d, sms * blocks_per_sm(d.H));
   const size_t slice = ((size_t)d.H * 4 + 255) / 256 * 256;
   p.off_post = 0;
   p.off_pre = slice * (size_t)p.blocks;
@@ -278,6 +707,31 @@ BwdPlan plan_bwd(const mm_norm_desc& d, int sms) {
   p.total = p.off_gate +
             (d.groups > 0 && p.pieces_per_group > 1 ? slice * (size_t)p.pieces : 0);
   return p;
+}
+
+// The row ring of a problem with at most `per_sm` blocks on an SM, fewer where rows are so long
+// that less than three stages would fit; depth < 2: it does not fit.
+RowRing plan_ring(const mm_norm_desc& d, const NormArgs& a, bool backward, int64_t& per_sm) {
+  const int sb = (int)(d.H * (d.stream_type == MM_BF16 ? 2 : 4));
+  const int bb = (int)(d.H * (d.block_type == MM_BF16 ? 2 : 4));
+  const int pb = (int)(d.H * (d.param_type == MM_BF16 ? 2 : 4));
+  RowRing r{-1, -1, -1, -1, -1, 0, 0, 0};
+  auto add = [&](int& at, bool used, int bytes) {
+    if (!used) return;
+    at = r.bytes;
+    r.bytes += (bytes + 127) / 128 * 128;
+  };
+  add(r.x, !backward || a.w_pre != nullptr, sb);
+  add(r.f, a.f != nullptr, bb);
+  add(r.u, backward && a.u != nullptr, sb);
+  add(r.v, backward && a.w_pre != nullptr, bb);
+  // a gate that changes every few rows travels with them
+  add(r.g, a.gate != nullptr && a.rows_per_gate < 8, pb);
+  r.tail = backward && a.w_post != nullptr ? (int)d.H * 4 : 0;
+  auto fit = [&](int64_t blocks) { return (216 * 1024 / blocks - r.tail) / std::max(1, r.bytes); };
+  while (per_sm > 1 && fit(per_sm) < 3) --per_sm;
+  r.depth = (int)std::min<int64_t>(8, fit(per_sm));
+  return r;
 }
 
 // Rows that can move as 16-byte words.
@@ -296,6 +750,38 @@ bool elements_aligned(size_t size, std::initializer_list<const void*> ptrs) {
 
 inline int threads_for(int64_t H, int per_thread) {
   return (int)std::min<int64_t>(1024, ((H + per_thread - 1) / per_thread + 31) / 32 * 32);
+}
+
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <auto* KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done_mask.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done_mask.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <auto* KERNEL>
+cudaError_t launch_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
+  const cudaError_t e = allow_smem<KERNEL>(216 * 1024);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3(row_threads(a.H) + 32),
+                    (size_t)r.bytes * r.depth + r.tail, st, a, r);
+}
+
+template <typename ST, typename BT, typename PT>
+cudaError_t launch_fwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
+  return launch_rows<&k_norm_fwd_rows<ST, BT, PT>>(a, r, blocks, st);
+}
+
+template <typename ST, typename BT, typename PT>
+cudaError_t launch_bwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
+  return launch_rows<&k_norm_bwd_rows<ST, BT, PT>>(a, r, blocks, st);
 }
 
 template <typename ST, typename BT>
@@ -318,6 +804,23 @@ cudaError_t launch_bwd(const NormArgs& a, int64_t blocks, bool w8, cudaStream_t 
   if (a.H <= 4096)
     return launch_pdl(k_norm_bwd<ST, BT, 1, 4>, grid, dim3(threads_for(a.H, 4)), 0, st, a);
   return launch_pdl(k_norm_bwd<ST, BT, 1, 16>, grid, dim3(threads_for(a.H, 16)), 0, st, a);
+}
+
+// Calls f with values of the stream, block and parameter types.
+template <typename F>
+cudaError_t with_types(const mm_norm_desc& d, F&& f) {
+  using B = __nv_bfloat16;
+  const bool p = d.param_type == MM_BF16;
+  if (d.stream_type == MM_BF16) return p ? f(B(), B(), B()) : f(B(), B(), 0.f);
+  if (d.block_type == MM_BF16) return p ? f(0.f, B(), B()) : f(0.f, B(), 0.f);
+  return p ? f(0.f, 0.f, B()) : f(0.f, 0.f, 0.f);
+}
+
+void deal_rows(NormArgs& a, const RowPlan& p) {
+  a.pieces = p.pieces;
+  a.pieces_per_group = p.pieces_per_group;
+  a.piece_rows = p.piece_rows;
+  a.group_rows = p.group_rows;
 }
 
 NormArgs norm_args(const mm_norm_desc& d) {
@@ -368,12 +871,21 @@ mm_status mm_residual_norm_forward(const mm_norm_desc* d, const void* residual, 
   const bool w8 =
       wide(*d, {residual, branch, post_weight, pre_weight, gate, residual_out, normed});
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (d->stream_type == MM_BF16)
-    MM_TRY((launch_fwd<__nv_bfloat16, __nv_bfloat16>(a, w8, st)));
-  else if (d->block_type == MM_BF16)
-    MM_TRY((launch_fwd<float, __nv_bfloat16>(a, w8, st)));
-  else
-    MM_TRY((launch_fwd<float, float>(a, w8, st)));
+  const int sms = std::max(1, device_sm_count());
+  int64_t per_sm = blocks_per_sm(d->H);
+  const RowRing ring = plan_ring(*d, a, false, per_sm);
+  // the ring pays from a few rows per block on
+  if (w8 && d->H <= kMaxRingH && d->T > 2 * sms * per_sm && ring.depth >= 2) {
+    const RowPlan p = plan_rows(*d, sms * per_sm);
+    deal_rows(a, p);
+    MM_TRY(with_types(*d, [&](auto s0, auto b0, auto p0) {
+      return launch_fwd_rows<decltype(s0), decltype(b0), decltype(p0)>(a, ring, p.blocks, st);
+    }));
+    return MM_OK;
+  }
+  MM_TRY(with_types(*d, [&](auto s0, auto b0, auto) {
+    return launch_fwd<decltype(s0), decltype(b0)>(a, w8, st);
+  }));
   return MM_OK;
 }
 
@@ -416,7 +928,8 @@ mm_status mm_residual_norm_backward(const mm_norm_desc* d, const void* residual_
       (d_residual_out == nullptr && d_normed == nullptr))
     return MM_ERR_INVALID_ARG;
   clear_error();
-  const BwdPlan p = plan_bwd(*d, std::max(1, device_sm_count()));
+  const int sms = std::max(1, device_sm_count());
+  BwdPlan p = plan_bwd(*d, sms);
   if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < p.total)
     return MM_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
@@ -433,20 +946,21 @@ mm_status mm_residual_norm_backward(const mm_norm_desc* d, const void* residual_
   a.d_gate = d_gate;
   a.part_post = reinterpret_cast<float*>(ws + p.off_post);
   a.part_pre = reinterpret_cast<float*>(ws + p.off_pre);
-  const bool gate_parts = gate != nullptr && p.pieces_per_group > 1;
-  a.part_gate = gate_parts ? reinterpret_cast<float*>(ws + p.off_gate) : nullptr;
-  a.pieces = p.pieces;
-  a.pieces_per_group = p.pieces_per_group;
-  a.piece_rows = p.piece_rows;
-  a.group_rows = p.group_rows;
   const bool w8 = wide(*d, {residual_out, branch, post_weight, pre_weight, gate, d_residual_out,
                             d_normed, d_residual, d_branch, d_gate});
-  if (d->stream_type == MM_BF16)
-    MM_TRY((launch_bwd<__nv_bfloat16, __nv_bfloat16>(a, p.blocks, w8, st)));
-  else if (d->block_type == MM_BF16)
-    MM_TRY((launch_bwd<float, __nv_bfloat16>(a, p.blocks, w8, st)));
-  else
-    MM_TRY((launch_bwd<float, float>(a, p.blocks, w8, st)));
+  int64_t per_sm = blocks_per_sm(d->H);  // (no more than the workspace is laid out for)
+  const RowRing ring = plan_ring(*d, a, true, per_sm);
+  static_cast<RowPlan&>(p) = plan_rows(*d, sms * per_sm);
+  deal_rows(a, p);
+  const bool gate_parts = gate != nullptr && p.pieces_per_group > 1;
+  a.part_gate = gate_parts ? reinterpret_cast<float*>(ws + p.off_gate) : nullptr;
+  const bool ringed = w8 && d->H <= kMaxRingH && ring.depth >= 2;
+  MM_TRY(with_types(*d, [&](auto s0, auto b0, auto p0) {
+    using ST = decltype(s0);
+    using BT = decltype(b0);
+    return ringed ? launch_bwd_rows<ST, BT, decltype(p0)>(a, ring, p.blocks, st)
+                : launch_bwd<ST, BT>(a, p.blocks, w8, st);
+  }));
   SumArgs sa{};
   sa.cols = (int)d->H;
   sa.type = d->param_type;

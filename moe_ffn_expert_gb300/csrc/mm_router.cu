@@ -220,9 +220,11 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
   }
 }
 
-// 32 columns per block, the parts dealt to 32 warps and added in a fixed order.
-__global__ void __launch_bounds__(1024) k_column_sums(SumArgs a) {
-  __shared__ float part[32][33];
+// 128 columns per block (4 per lane where the width allows 16-byte loads), the parts dealt to 16
+// warps with 8 loads in flight each; the warps' sums are added in order.
+template <int W>
+__global__ void __launch_bounds__(512) k_column_sums(SumArgs a) {
+  __shared__ float part[16][32 * W];
   pdl_wait();
   int k = 0;
 #pragma unroll
@@ -230,17 +232,31 @@ __global__ void __launch_bounds__(1024) k_column_sums(SumArgs a) {
     if (i < a.jobs && (int64_t)blockIdx.y >= a.job[i].first) k = i;
   const SumJob job = a.job[k];
   const int64_t y = (int64_t)blockIdx.y - job.first;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < a.cols)
-#pragma unroll 4
-    for (int64_t p = warp; p < job.parts; p += 32) s += job.src[(y * job.parts + p) * a.cols + c];
-  part[warp][lane] = s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = (blockIdx.x * 32 + lane) * W;
+  const float* src = job.src + y * job.parts * a.cols + c;
+  float s[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) s[i] = 0.f;
+  if (c < a.cols) {
+#pragma unroll 8
+    for (int64_t p = warp; p < job.parts; p += 16) {
+      const float* at = src + p * a.cols;
+      if constexpr (W == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(at));
+        s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+      } else {
+        s[0] += __ldcg(at);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) part[warp][lane * W + i] = s[i];
   __syncthreads();
-  s = warp_sum(part[lane][warp]);  // column `warp` of this block
-  const int col = blockIdx.x * 32 + warp;
-  if (lane == 0 && col < a.cols) {
-    const float v[1] = {s};
+  const int col = blockIdx.x * 32 * W + (int)threadIdx.x;
+  if (threadIdx.x < 32 * W && col < a.cols) {
+    float v[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[0] += part[i][threadIdx.x];
     store_any<1>(job.dst, a.type, y * a.cols + col, v);
   }
 }
@@ -306,8 +322,11 @@ cudaError_t launch_router(const mm_router_desc& d, const float* logits, const fl
 }
 
 cudaError_t launch_column_sums(const SumArgs& a, int64_t rows, cudaStream_t st) {
-  return launch_pdl(k_column_sums, dim3((unsigned)((a.cols + 31) / 32), (unsigned)rows),
-                    dim3(1024), 0, st, a);
+  if (a.cols % 4 == 0)
+    return launch_pdl(k_column_sums<4>, dim3((unsigned)((a.cols + 127) / 128), (unsigned)rows),
+                      dim3(512), 0, st, a);
+  return launch_pdl(k_column_sums<1>, dim3((unsigned)((a.cols + 31) / 32), (unsigned)rows),
+                    dim3(512), 0, st, a);
 }
 
 }  // namespace mm

@@ -99,4 +99,70 @@ __device__ __forceinline__ float warp_sum_many(float (&v)[N], int lane) {
   return s;
 }
 
+// Two 32-bit floats that one instruction works on (sm_100 and later).
+struct f32x2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(f32x2 p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ f32x2 mul(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float sum_of(f32x2 p) {
+  float a, b;
+  split(p, a, b);
+  return a + b;
+}
+
+// 8 elements at p (16-byte aligned) as four pairs, and back with one rounding.
+__device__ __forceinline__ void load_pairs(const __nv_bfloat16* p, f32x2 (&v)[4]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  v[0] = pair(bf16_lo(r.x), bf16_hi(r.x));
+  v[1] = pair(bf16_lo(r.y), bf16_hi(r.y));
+  v[2] = pair(bf16_lo(r.z), bf16_hi(r.z));
+  v[3] = pair(bf16_lo(r.w), bf16_hi(r.w));
+}
+__device__ __forceinline__ void load_pairs(const float* p, f32x2 (&v)[4]) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0];
+  const ulonglong2 b = reinterpret_cast<const ulonglong2*>(p)[1];
+  v[0].v = a.x, v[1].v = a.y, v[2].v = b.x, v[3].v = b.y;
+}
+__device__ __forceinline__ uint32_t pack_pair(f32x2 p) {
+  float a, b;
+  split(p, a, b);
+  return pack_bf16(a, b);
+}
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, const f32x2 (&v)[4]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_pair(v[0]), pack_pair(v[1]), pack_pair(v[2]), pack_pair(v[3]));
+}
+__device__ __forceinline__ void store_pairs(float* p, const f32x2 (&v)[4]) {
+  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(v[0].v, v[1].v);
+  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(v[2].v, v[3].v);
+}
+
+// Bytes (a multiple of 16, both addresses too) from global to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 }  // namespace mm
