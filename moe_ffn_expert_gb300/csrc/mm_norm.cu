@@ -255,11 +255,6 @@ struct RowRing {
   int bytes, depth, tail;  // tail: bytes behind the stages (the backward's sums of d_post)
 };
 
-template <typename T>
-__device__ __forceinline__ const T* row_at(const uint8_t* stage, int offset, int c) {
-  return reinterpret_cast<const T*>(stage + offset) + c;
-}
-
 // The rows of a block, piece after piece (see NormArgs).
 struct RowWalk {
   int64_t piece, group, t, t1;
@@ -280,7 +275,7 @@ struct RowWalk {
 // One thread: the copies of row t into a stage.
 template <typename ST, typename BT, typename PT>
 __device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, uint32_t stage,
-                                         uint32_t bar, int64_t t, int64_t group) {
+                                         uint32_t bar, int64_t t) {
   const uint32_t sb = a.H * sizeof(ST), bb = a.H * sizeof(BT), pb = a.H * sizeof(PT);
   mbar_arrive_expect_tx(bar, (r.x >= 0 ? sb : 0) + (r.f >= 0 ? bb : 0) + (r.u >= 0 ? sb : 0) +
                                  (r.v >= 0 ? bb : 0) + (r.g >= 0 ? pb : 0));
@@ -288,7 +283,7 @@ __device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, ui
   if (r.f >= 0) bulk_load(stage + r.f, static_cast<const BT*>(a.f) + t * a.H, bb, bar);
   if (r.u >= 0) bulk_load(stage + r.u, static_cast<const ST*>(a.u) + t * a.H, sb, bar);
   if (r.v >= 0) bulk_load(stage + r.v, static_cast<const BT*>(a.v) + t * a.H, bb, bar);
-  if (r.g >= 0) bulk_load(stage + r.g, static_cast<const PT*>(a.gate) + group * a.H, pb, bar);
+  if (r.g >= 0) bulk_load(stage + r.g, static_cast<const PT*>(a.gate) + t / a.rows_per_gate * a.H, pb, bar);
 }
 
 // A row kernel's last warp issues the copies (a stage's cost hundreds of cycles, which in one of
@@ -332,26 +327,29 @@ __device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& r
   uint32_t ph = 1;
   while (row.more(a)) {
     mbar_wait(empty + 8u * s, ph, kRowTimeoutNs);
-    load_row<ST, BT, PT>(a, ring, smem + s * ring.bytes, full + 8u * s, row.t, row.group);
+    load_row<ST, BT, PT>(a, ring, smem + s * ring.bytes, full + 8u * s, row.t);
     row.next(a);
     if (++s == ring.depth) s = 0, ph ^= 1u;
   }
 }
 
+// FULL: every part is there (branch, both norms, both upstream gradients; a gate, if any, the same
+// for several rows), which takes the tests for the parts out of the loop.
+//
 // What a thread does per row is the same for 8 columns as for 16 but for the columns themselves:
 // with 8, and single floats, 52 instructions went into an element of the forward, and the issue
 // slots ran out at 3.6 TB/s. A thread has columns 8 tid .. and 8 (tid + threads) ..; the loop works
 // on pairs of floats.
 constexpr int kVecs = 2;
 
-template <typename ST, typename BT, typename PT>
+template <typename ST, typename BT, typename PT, bool FULL>
 __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[2][32];
   __shared__ uint64_t bars[16];
   const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32, step = threads * 8,
             c0 = tid * 8;
-  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+  const bool post = FULL || a.w_post != nullptr, pre = FULL || a.w_pre != nullptr;
   if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
   if (tid == 0) {
     for (int i = 0; i < ring.depth; ++i) {
@@ -379,7 +377,7 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
       for (int i = 0; i < 4; ++i) wb[k][i] = both(1.f);
       if (c >= H) continue;
       if (post) load_pairs(static_cast<const PT*>(a.w_post) + c, wb[k]);
-      if (a.gate != nullptr && ring.g < 0) {
+      if (a.gate != nullptr && (FULL || ring.g < 0)) {
         load_pairs(static_cast<const PT*>(a.gate) + group * H + c, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) wb[k][i] = mul(wb[k][i], g[i]);
@@ -399,17 +397,17 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
   const float rh = 1.f / (float)H;
   const f32x2 scale = both(a.scale);
   while (row.more(a)) {
-    const uint8_t* stage = smem + s * ring.bytes;
-    if (a.gate != nullptr && ring.g < 0 && row.group != group) branch_weights(group = row.group);
+    const uint32_t stage = smem_u32(smem) + s * ring.bytes;
+    if (a.gate != nullptr && (FULL || ring.g < 0) && row.group != group) branch_weights(group = row.group);
     mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
     f32x2 x[kVecs][4], y[kVecs][4], acc = both(0.f);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       const int c = c0 + k * step;
       if (c >= H) continue;
-      load_pairs(row_at<ST>(stage, ring.x, c), x[k]);
-      if (ring.f >= 0) {
-        load_pairs(row_at<BT>(stage, ring.f, c), y[k]);
+      lds_pairs<ST>(stage + ring.x + c * (int)sizeof(ST), x[k]);
+      if (FULL || ring.f >= 0) {
+        lds_pairs<BT>(stage + ring.f + c * (int)sizeof(BT), y[k]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[k][i] = both(0.f);
@@ -425,9 +423,9 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
     for (int k = 0; k < kVecs; ++k) {
       const int c = c0 + k * step;
       if (c >= H) continue;
-      if (ring.g >= 0) {
+      if (!FULL && ring.g >= 0) {
         f32x2 g[4];
-        load_pairs(row_at<PT>(stage, ring.g, c), g);
+        lds_pairs<PT>(stage + ring.g + c * (int)sizeof(PT), g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[k][i] = mul(y[k][i], g[i]);
       }
@@ -436,7 +434,7 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
         x[k][i] = fma(mul(q, y[k][i]), wb[k][i], mul(scale, x[k][i]));
         acc = fma(x[k][i], x[k][i], acc);
       }
-      if (a.out != nullptr) store_pairs(static_cast<ST*>(a.out) + at + k * step, x[k]);
+      if (FULL || a.out != nullptr) store_pairs(static_cast<ST*>(a.out) + at + k * step, x[k]);
     }
     __syncwarp();
     if ((tid & 31) == 0) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
@@ -477,14 +475,14 @@ __device__ __forceinline__ void block_sum_8(float (&v)[8], float* red, int threa
 // reduction would leave no room for the column sums of 16 columns.
 // The gate is the same over a piece, so sum d f s gives both its gradient (times w_post) and, times
 // the gate, the piece's share of d_post.
-template <typename ST, typename BT, typename PT>
+template <typename ST, typename BT, typename PT, bool FULL>
 __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][16 * 8];
   __shared__ uint64_t bars[16];
   const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32, step = threads * 8,
             c0 = tid * 8;
-  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr, gated = a.gate != nullptr;
+  const bool post = FULL || a.w_post != nullptr, pre = FULL || a.w_pre != nullptr, gated = a.gate != nullptr;
   if (tid == 0) {
     for (int i = 0; i < ring.depth; ++i) {
       mbar_init(smem_u32(&bars[i]), 1);
@@ -503,16 +501,17 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
   // weights: w_post times the gate, w_pre; column sums: of d f s over a piece, of v r' q, of d_post
   f32x2 wg[kVecs][4], wn[kVecs][4], raw[kVecs][4], d_pre[kVecs][4];
   float* const d_post = reinterpret_cast<float*>(smem + ring.depth * ring.bytes);  // [H]
-  auto branch_weights = [&](int k, int64_t group, const uint8_t* stage, f32x2 (&g)[4],
-                            f32x2 (&w)[4]) {
+  auto branch_weights = [&](int k, int64_t group, uint32_t stage, f32x2 (&g)[4], f32x2 (&w)[4]) {
     const int c = c0 + k * step;
 #pragma unroll
     for (int i = 0; i < 4; ++i) g[i] = w[i] = both(1.f);
     if (c >= H) return;
     if (post) load_pairs(static_cast<const PT*>(a.w_post) + c, w);
-    if (gated)
-      load_pairs(ring.g >= 0 ? row_at<PT>(stage, ring.g, c)
-                             : static_cast<const PT*>(a.gate) + group * H + c, g);
+    if (!gated) return;
+    if (!FULL && ring.g >= 0)
+      lds_pairs<PT>(stage + ring.g + c * (int)sizeof(PT), g);
+    else
+      load_pairs(static_cast<const PT*>(a.gate) + group * H + c, g);
   };
 #pragma unroll
   for (int k = 0; k < kVecs; ++k) {
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
   uint32_t ph = 0;
   const float rh = 1.f / (float)H;
   while (row.more(a)) {
-    const uint8_t* stage = smem + s * ring.bytes;
+    const uint32_t stage = smem_u32(smem) + s * ring.bytes;
     mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
     if (fresh) {
 #pragma unroll
@@ -548,14 +547,14 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
         for (int i = 0; i < 4; ++i) z[i] = both(0.f);
       };
       if (pre) {
-        load_pairs(row_at<ST>(stage, ring.x, c), x);
-        load_pairs(row_at<BT>(stage, ring.v, c), v);
+        lds_pairs<ST>(stage + ring.x + c * (int)sizeof(ST), x);
+        lds_pairs<BT>(stage + ring.v + c * (int)sizeof(BT), v);
       } else {
         none(x);
         none(v);
       }
-      if (ring.f >= 0) load_pairs(row_at<BT>(stage, ring.f, c), f); else none(f);
-      if (ring.u >= 0) load_pairs(row_at<ST>(stage, ring.u, c), u); else none(u);
+      if (FULL || ring.f >= 0) lds_pairs<BT>(stage + ring.f + c * (int)sizeof(BT), f); else none(f);
+      if (FULL || ring.u >= 0) lds_pairs<ST>(stage + ring.u + c * (int)sizeof(ST), u); else none(u);
     };
     f32x2 acc[6];
 #pragma unroll
@@ -605,7 +604,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
         f[i] = fma(ncs, f[i], mul(sf2, mul(wg[k][i], d)));
       }
       store_pairs(static_cast<ST*>(a.dr) + at + k * step, dr);
-      if (a.df != nullptr) store_pairs(static_cast<BT*>(a.df) + at + k * step, f);
+      if (FULL || a.df != nullptr) store_pairs(static_cast<BT*>(a.df) + at + k * step, f);
     }
     if (row.t + 1 == row.t1) {  // the piece ends
 #pragma unroll
@@ -675,9 +674,10 @@ struct RowPlan {
   int64_t group_rows, piece_rows, pieces_per_group, pieces, blocks;
 };
 
-RowPlan plan_rows(const mm_norm_desc& d, int64_t target) {
+// by_group: a piece lies within one gate's rows.
+RowPlan plan_rows(const mm_norm_desc& d, int64_t target, bool by_group = true) {
   RowPlan p{};
-  const int64_t groups = std::max<int64_t>(1, d.groups);
+  const int64_t groups = by_group ? std::max<int64_t>(1, d.groups) : 1;
   p.group_rows = d.T / groups;
   p.piece_rows = std::max<int64_t>(1, std::min(p.group_rows, (d.T + target - 1) / target));
   p.pieces_per_group = (p.group_rows + p.piece_rows - 1) / p.piece_rows;
@@ -776,12 +776,16 @@ cudaError_t launch_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cud
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_fwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
-  return launch_rows<&k_norm_fwd_rows<ST, BT, PT>>(a, r, blocks, st);
+  const bool full = a.w_post && a.w_pre && a.out && r.g < 0;  // (a post weight has a branch)
+  return full ? launch_rows<&k_norm_fwd_rows<ST, BT, PT, true>>(a, r, blocks, st)
+              : launch_rows<&k_norm_fwd_rows<ST, BT, PT, false>>(a, r, blocks, st);
 }
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_bwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
-  return launch_rows<&k_norm_bwd_rows<ST, BT, PT>>(a, r, blocks, st);
+  const bool full = a.w_post && a.w_pre && a.u && r.g < 0;
+  return full ? launch_rows<&k_norm_bwd_rows<ST, BT, PT, true>>(a, r, blocks, st)
+              : launch_rows<&k_norm_bwd_rows<ST, BT, PT, false>>(a, r, blocks, st);
 }
 
 template <typename ST, typename BT>
@@ -876,7 +880,7 @@ mm_status mm_residual_norm_forward(const mm_norm_desc* d, const void* residual, 
   const RowRing ring = plan_ring(*d, a, false, per_sm);
   // the ring pays from a few rows per block on
   if (w8 && d->H <= kMaxRingH && d->T > 2 * sms * per_sm && ring.depth >= 2) {
-    const RowPlan p = plan_rows(*d, sms * per_sm);
+    const RowPlan p = plan_rows(*d, sms * per_sm, ring.g < 0);
     deal_rows(a, p);
     MM_TRY(with_types(*d, [&](auto s0, auto b0, auto p0) {
       return launch_fwd_rows<decltype(s0), decltype(b0), decltype(p0)>(a, ring, p.blocks, st);

@@ -141,6 +141,21 @@ __device__ __forceinline__ void load_pairs(const float* p, f32x2 (&v)[4]) {
   const ulonglong2 b = reinterpret_cast<const ulonglong2*>(p)[1];
   v[0].v = a.x, v[1].v = a.y, v[2].v = b.x, v[3].v = b.y;
 }
+// The same from shared memory (byte address).
+template <typename T>
+__device__ __forceinline__ void lds_pairs(uint32_t at, f32x2 (&v)[4]) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t r[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(bf16_lo(r[i]), bf16_hi(r[i]));
+  } else {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0].v), "=l"(v[1].v) : "r"(at));
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2].v), "=l"(v[3].v) : "r"(at + 16));
+  }
+}
 __device__ __forceinline__ uint32_t pack_pair(f32x2 p) {
   float a, b;
   split(p, a, b);
