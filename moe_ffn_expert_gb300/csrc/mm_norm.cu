@@ -13,11 +13,11 @@
 // so the six sums of a row come from one reduction. Everything is elementwise otherwise: the
 // kernels are bound by HBM.
 //
-// Two forms. Rows of 16-byte words, many of them: persistent blocks, 16 columns per thread, whose
+// Two forms. Many rows: persistent blocks, 16 columns per thread, whose
 // rows arrive by bulk copies into a ring in shared memory several rows ahead, so that HBM stays
 // busy through the reductions; weights and the backward's column sums stay in registers
-// (k_norm_fwd_rows, k_norm_bwd_rows). Few rows, odd widths and widths above 7680: a row in
-// registers straight from global memory (k_norm_fwd, k_norm_bwd).
+// (k_norm_fwd_rows, k_norm_bwd_rows). Few rows, widths above 7680 and tensors off 16-byte
+// boundaries: a row in registers straight from global memory (k_norm_fwd, k_norm_bwd).
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -33,7 +33,7 @@ namespace mm {
 namespace {
 
 constexpr int kMaxH = 16384;
-constexpr int kMaxRingH = 7680;  // 15 warps of 16 columns per thread, and the one that loads
+constexpr int kMaxRingH = 7680;  // 15 warps of 16 columns per thread (odd rows: 8)
 
 struct NormArgs {
   int64_t T, rows_per_gate;  // rows_per_gate: T / groups (0: no gate)
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(1024) k_norm_bwd(NormArgs a) {
 // A stage holds one row of each tensor in use; offsets in bytes, -1: not in use.
 struct RowRing {
   int x, f, u, v, g;  // residual (forward: r, backward: r'), branch, the two gradients, gate
-  int bytes, depth, tail;  // tail: bytes behind the stages (the backward's sums of d_post)
+  int bytes, depth, odd, tail;  // odd: single elements (see Columns); tail: bytes behind the stages (the backward's sums of d_post)
 };
 
 // The rows of a block, piece after piece (see NormArgs).
@@ -272,18 +272,132 @@ struct RowWalk {
   }
 };
 
+// ODD rows start off a 16-byte boundary: their copies run from the boundary before to the one
+// after (the last row's, to the last one within the tensor: what is left of it, under 16 bytes, the
+// loading warp copies itself), and a thread works on single elements, `threads` apart, instead of
+// 8 together. Both hold a thread's columns as kVecs x 4 pairs.
+struct Span {  // of a row's bytes that are copied
+  int64_t from;
+  uint32_t bytes;
+};
+template <bool ODD>
+__device__ __forceinline__ Span row_span(int64_t row, int64_t rows, uint32_t row_bytes) {
+  const int64_t start = row * row_bytes;
+  if (!ODD) return Span{start, row_bytes};
+  const int64_t end = min((start + row_bytes + 15) & ~15ll, rows * row_bytes & ~15ll);
+  return Span{start & ~15ll, (uint32_t)(end - (start & ~15ll))};
+}
+
+// Address of a row's first element in its stage.
+template <bool ODD>
+__device__ __forceinline__ uint32_t row_at(uint32_t stage, int offset, int64_t row,
+                                           uint32_t row_bytes) {
+  return stage + offset + (ODD ? (uint32_t)(row * row_bytes) & 15u : 0u);
+}
+
+template <bool ODD>
+struct Columns {
+  int H, threads;
+  __device__ __forceinline__ int first(int k) const {
+    return ODD ? (int)threadIdx.x + 8 * k * threads : ((int)threadIdx.x + k * threads) * 8;
+  }
+  __device__ __forceinline__ bool any(int k) const { return first(k) < H; }
+  // f(pair, half, column) for every column of group k (ODD)
+  template <typename F>
+  __device__ __forceinline__ void each(int k, F&& f) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = first(k) + i * threads;
+      f(i, c);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void gather(int k, f32x2 (&v)[4], F&& value) const {
+    float e[8];
+    each(k, [&](int i, int c) { e[i] = c < H ? value(c) : 0.f; });
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(e[2 * i], e[2 * i + 1]);
+  }
+  // from a row in its stage
+  template <typename T>
+  __device__ __forceinline__ void stage(uint32_t row, int k, f32x2 (&v)[4]) const {
+    if constexpr (ODD) {
+      gather(k, v, [&](int c) {
+        const uint32_t at = row + c * (uint32_t)sizeof(T);
+        if constexpr (sizeof(T) == 2) {
+          uint16_t w;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(at));
+          return __uint_as_float((uint32_t)w << 16);
+        } else {
+          float w;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(w) : "r"(at));
+          return w;
+        }
+      });
+    } else {
+      lds_pairs<T>(row + first(k) * (uint32_t)sizeof(T), v);
+    }
+  }
+  // from and to rows in global (or, as floats, shared) memory
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, int k, f32x2 (&v)[4]) const {
+    if constexpr (ODD)
+      gather(k, v, [&](int c) { return element(row[c]); });
+    else
+      load_pairs(row + first(k), v);
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int k, const f32x2 (&v)[4]) const {
+    if constexpr (ODD) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) split(v[i], e[2 * i], e[2 * i + 1]);
+      each(k, [&](int i, int c) {
+        if (c < H) put(row + c, e[i]);
+      });
+    } else {
+      store_pairs(row + first(k), v);
+    }
+  }
+  static __device__ __forceinline__ float element(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ float element(float v) { return v; }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+};
+
 // One thread: the copies of row t into a stage.
-template <typename ST, typename BT, typename PT>
+template <typename ST, typename BT, typename PT, bool ODD>
 __device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, uint32_t stage,
                                          uint32_t bar, int64_t t) {
-  const uint32_t sb = a.H * sizeof(ST), bb = a.H * sizeof(BT), pb = a.H * sizeof(PT);
-  mbar_arrive_expect_tx(bar, (r.x >= 0 ? sb : 0) + (r.f >= 0 ? bb : 0) + (r.u >= 0 ? sb : 0) +
-                                 (r.v >= 0 ? bb : 0) + (r.g >= 0 ? pb : 0));
-  if (r.x >= 0) bulk_load(stage + r.x, static_cast<const ST*>(a.r) + t * a.H, sb, bar);
-  if (r.f >= 0) bulk_load(stage + r.f, static_cast<const BT*>(a.f) + t * a.H, bb, bar);
-  if (r.u >= 0) bulk_load(stage + r.u, static_cast<const ST*>(a.u) + t * a.H, sb, bar);
-  if (r.v >= 0) bulk_load(stage + r.v, static_cast<const BT*>(a.v) + t * a.H, bb, bar);
-  if (r.g >= 0) bulk_load(stage + r.g, static_cast<const PT*>(a.gate) + t / a.rows_per_gate * a.H, pb, bar);
+  const Span ss = row_span<ODD>(t, a.T, a.H * sizeof(ST)), bs = row_span<ODD>(t, a.T, a.H * sizeof(BT));
+  Span ps{0, 0};
+  if (r.g >= 0)
+    ps = row_span<ODD>(t / a.rows_per_gate, a.T / a.rows_per_gate, a.H * sizeof(PT));
+  if (ODD && t + 1 == a.T) {  // what the copies leave out, before the arrival below
+    auto rest = [&](int offset, const void* base, const Span& span, int64_t total) {
+      const char* src = static_cast<const char*>(base) + span.from;
+      if (offset >= 0)
+        for (uint32_t i = span.bytes; (int64_t)i < total - span.from; i += 2)
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + offset + i),
+                       "h"(*reinterpret_cast<const uint16_t*>(src + i))
+                       : "memory");
+    };
+    rest(r.x, a.r, ss, a.T * a.H * sizeof(ST));
+    rest(r.f, a.f, bs, a.T * a.H * sizeof(BT));
+    rest(r.u, a.u, ss, a.T * a.H * sizeof(ST));
+    rest(r.v, a.v, bs, a.T * a.H * sizeof(BT));
+    rest(r.g, a.gate, ps, r.g >= 0 ? a.T / a.rows_per_gate * a.H * sizeof(PT) : 0);
+  }
+  mbar_arrive_expect_tx(bar, (r.x >= 0 ? ss.bytes : 0) + (r.f >= 0 ? bs.bytes : 0) +
+                                 (r.u >= 0 ? ss.bytes : 0) + (r.v >= 0 ? bs.bytes : 0) + ps.bytes);
+  auto copy = [&](int offset, const void* base, const Span& span) {
+    if (offset >= 0) bulk_load(stage + offset, static_cast<const char*>(base) + span.from, span.bytes, bar);
+  };
+  copy(r.x, a.r, ss);
+  copy(r.f, a.f, bs);
+  copy(r.u, a.u, ss);
+  copy(r.v, a.v, bs);
+  copy(r.g, a.gate, ps);
 }
 
 // A row kernel's last warp issues the copies (a stage's cost hundreds of cycles, which in one of
@@ -292,10 +406,6 @@ __device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, ui
 __device__ __forceinline__ void row_barrier(int threads) {
   asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 }
-
-template <typename ST, typename BT, typename PT>
-__device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& ring, uint32_t smem,
-                                             uint32_t full, uint32_t empty);
 
 // Row loads are this library's own copies from memory that the launch was given: the wait for one
 // cannot run out unless the device has failed. It is bounded all the same (2 s), and then goes on.
@@ -317,7 +427,7 @@ __device__ __forceinline__ float block_sum_1(float v, float* red, int threads) {
   return s;
 }
 
-template <typename ST, typename BT, typename PT>
+template <typename ST, typename BT, typename PT, bool ODD>
 __device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& ring, uint32_t smem,
                                              uint32_t full, uint32_t empty) {
   if ((threadIdx.x & 31) != 0) return;
@@ -327,7 +437,7 @@ __device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& r
   uint32_t ph = 1;
   while (row.more(a)) {
     mbar_wait(empty + 8u * s, ph, kRowTimeoutNs);
-    load_row<ST, BT, PT>(a, ring, smem + s * ring.bytes, full + 8u * s, row.t);
+    load_row<ST, BT, PT, ODD>(a, ring, smem + s * ring.bytes, full + 8u * s, row.t);
     row.next(a);
     if (++s == ring.depth) s = 0, ph ^= 1u;
   }
@@ -340,15 +450,21 @@ __device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& r
 // with 8, and single floats, 52 instructions went into an element of the forward, and the issue
 // slots ran out at 3.6 TB/s. A thread has columns 8 tid .. and 8 (tid + threads) ..; the loop works
 // on pairs of floats.
-constexpr int kVecs = 2;
+// ODD rows: 8 columns, whose addresses and masks are their own.
+constexpr int kRowThreads = 512;  // at most, the loading warp included
+template <bool ODD>
+struct Shape {
+  static constexpr int VECS = ODD ? 1 : 2;
+};
 
-template <typename ST, typename BT, typename PT, bool FULL>
-__global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring) {
+template <typename ST, typename BT, typename PT, bool FULL, bool ODD>
+__global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRing ring) {
+  constexpr int kVecs = Shape<ODD>::VECS;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[2][32];
   __shared__ uint64_t bars[16];
-  const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32, step = threads * 8,
-            c0 = tid * 8;
+  const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32;
+  const Columns<ODD> cols{H, threads};
   const bool post = FULL || a.w_post != nullptr, pre = FULL || a.w_pre != nullptr;
   if (tid < 64) red[tid >> 5][tid & 31] = 0.f;
   if (tid == 0) {
@@ -361,7 +477,7 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
   __syncthreads();
   pdl_wait();
   if (tid >= threads) {
-    produce_rows<ST, BT, PT>(a, ring, smem_u32(smem), smem_u32(bars), smem_u32(bars + 8));
+    produce_rows<ST, BT, PT, ODD>(a, ring, smem_u32(smem), smem_u32(bars), smem_u32(bars + 8));
     return;
   }
   RowWalk row;
@@ -371,14 +487,13 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
   auto branch_weights = [&](int64_t group) {
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      const int c = c0 + k * step;
       f32x2 g[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) wb[k][i] = both(1.f);
-      if (c >= H) continue;
-      if (post) load_pairs(static_cast<const PT*>(a.w_post) + c, wb[k]);
+      if (!cols.any(k)) continue;
+      if (post) cols.load(static_cast<const PT*>(a.w_post), k, wb[k]);
       if (a.gate != nullptr && (FULL || ring.g < 0)) {
-        load_pairs(static_cast<const PT*>(a.gate) + group * H + c, g);
+        cols.load(static_cast<const PT*>(a.gate) + group * H, k, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) wb[k][i] = mul(wb[k][i], g[i]);
       }
@@ -388,7 +503,7 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
   for (int k = 0; k < kVecs; ++k) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) wn[k][i] = both(1.f);
-    if (pre && c0 + k * step < H) load_pairs(static_cast<const PT*>(a.w_pre) + c0 + k * step, wn[k]);
+    if (pre && cols.any(k)) cols.load(static_cast<const PT*>(a.w_pre), k, wn[k]);
   }
   if (row.more(a)) branch_weights(row.group);
   int64_t group = row.group;
@@ -401,13 +516,14 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
     if (a.gate != nullptr && (FULL || ring.g < 0) && row.group != group) branch_weights(group = row.group);
     mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
     f32x2 x[kVecs][4], y[kVecs][4], acc = both(0.f);
+    const uint32_t xr = row_at<ODD>(stage, ring.x, row.t, H * sizeof(ST));
+    const uint32_t fr = row_at<ODD>(stage, ring.f, row.t, H * sizeof(BT));
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      const int c = c0 + k * step;
-      if (c >= H) continue;
-      lds_pairs<ST>(stage + ring.x + c * (int)sizeof(ST), x[k]);
+      if (!cols.any(k)) continue;
+      cols.template stage<ST>(xr, k, x[k]);
       if (FULL || ring.f >= 0) {
-        lds_pairs<BT>(stage + ring.f + c * (int)sizeof(BT), y[k]);
+        cols.template stage<BT>(fr, k, y[k]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[k][i] = both(0.f);
@@ -418,14 +534,14 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
     f32x2 q = both(1.f);
     if (post) q = both(rsqrtf(block_sum_1(sum_of(acc), red[0], threads) * rh + a.eps));
     acc = both(0.f);
-    const int64_t at = row.t * H + c0;
+    const int64_t at = row.t * H;
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      const int c = c0 + k * step;
-      if (c >= H) continue;
+      if (!cols.any(k)) continue;
       if (!FULL && ring.g >= 0) {
         f32x2 g[4];
-        lds_pairs<PT>(stage + ring.g + c * (int)sizeof(PT), g);
+        const int64_t gate_row = row.t / a.rows_per_gate;
+        cols.template stage<PT>(row_at<ODD>(stage, ring.g, gate_row, H * sizeof(PT)), k, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[k][i] = mul(y[k][i], g[i]);
       }
@@ -434,7 +550,7 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
         x[k][i] = fma(mul(q, y[k][i]), wb[k][i], mul(scale, x[k][i]));
         acc = fma(x[k][i], x[k][i], acc);
       }
-      if (FULL || a.out != nullptr) store_pairs(static_cast<ST*>(a.out) + at + k * step, x[k]);
+      if (FULL || a.out != nullptr) cols.store(static_cast<ST*>(a.out) + at, k, x[k]);
     }
     __syncwarp();
     if ((tid & 31) == 0) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
@@ -445,10 +561,10 @@ __global__ void __launch_bounds__(512) k_norm_fwd_rows(NormArgs a, RowRing ring)
       q = both(rsqrtf(sum * rh + a.eps));
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
-        if (c0 + k * step >= H) continue;
+        if (!cols.any(k)) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[k][i] = mul(mul(q, x[k][i]), wn[k][i]);
-        store_pairs(static_cast<BT*>(a.n) + at + k * step, x[k]);
+        cols.store(static_cast<BT*>(a.n) + at, k, x[k]);
       }
     }
     row.next(a);
@@ -473,15 +589,17 @@ __device__ __forceinline__ void block_sum_8(float (&v)[8], float* red, int threa
 
 // A row is read from its stage twice, before and after its sums: its values in registers over the
 // reduction would leave no room for the column sums of 16 columns.
-// The gate is the same over a piece, so sum d f s gives both its gradient (times w_post) and, times
-// the gate, the piece's share of d_post.
-template <typename ST, typename BT, typename PT, bool FULL>
-__global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring) {
+// Where the gate is the same over a piece, sum d f s gives both its gradient (times w_post) and,
+// times the gate, the piece's share of d_post; a gate per token (own_gate) has its gradient written
+// with the row, and the sum is of g d f s.
+template <typename ST, typename BT, typename PT, bool FULL, bool ODD>
+__global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRing ring) {
+  constexpr int kVecs = Shape<ODD>::VECS;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float red[2][16 * 8];
+  __shared__ float red[2][kRowThreads / 32 * 8];
   __shared__ uint64_t bars[16];
-  const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32, step = threads * 8,
-            c0 = tid * 8;
+  const int tid = threadIdx.x, H = a.H, threads = blockDim.x - 32;
+  const Columns<ODD> cols{H, threads};
   const bool post = FULL || a.w_post != nullptr, pre = FULL || a.w_pre != nullptr, gated = a.gate != nullptr;
   if (tid == 0) {
     for (int i = 0; i < ring.depth; ++i) {
@@ -493,25 +611,19 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
   __syncthreads();
   pdl_wait();
   if (tid >= threads) {
-    produce_rows<ST, BT, PT>(a, ring, smem_u32(smem), smem_u32(bars), smem_u32(bars + 8));
+    produce_rows<ST, BT, PT, ODD>(a, ring, smem_u32(smem), smem_u32(bars), smem_u32(bars + 8));
     return;
   }
   RowWalk row;
   row.start(a, blockIdx.x);
-  // weights: w_post times the gate, w_pre; column sums: of d f s over a piece, of v r' q, of d_post
+  // weights: w_post (times the piece's gate), w_pre; column sums: of d f s, of v r' q, of d_post
   f32x2 wg[kVecs][4], wn[kVecs][4], raw[kVecs][4], d_pre[kVecs][4];
   float* const d_post = reinterpret_cast<float*>(smem + ring.depth * ring.bytes);  // [H]
-  auto branch_weights = [&](int k, int64_t group, uint32_t stage, f32x2 (&g)[4], f32x2 (&w)[4]) {
-    const int c = c0 + k * step;
+  const bool own_gate = !FULL && ring.g >= 0, piece_gate = gated && !own_gate;
+  auto post_weights = [&](int k, f32x2 (&w)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = w[i] = both(1.f);
-    if (c >= H) return;
-    if (post) load_pairs(static_cast<const PT*>(a.w_post) + c, w);
-    if (!gated) return;
-    if (!FULL && ring.g >= 0)
-      lds_pairs<PT>(stage + ring.g + c * (int)sizeof(PT), g);
-    else
-      load_pairs(static_cast<const PT*>(a.gate) + group * H + c, g);
+    for (int i = 0; i < 4; ++i) w[i] = both(1.f);
+    if (post && cols.any(k)) cols.load(static_cast<const PT*>(a.w_post), k, w);
   };
 #pragma unroll
   for (int k = 0; k < kVecs; ++k) {
@@ -520,10 +632,11 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
       wn[k][i] = both(1.f);
       raw[k][i] = d_pre[k][i] = both(0.f);
     }
-    if (post && c0 + k * step < H) store_pairs(d_post + c0 + k * step, raw[k]);
-    if (pre && c0 + k * step < H) load_pairs(static_cast<const PT*>(a.w_pre) + c0 + k * step, wn[k]);
+    if (post && cols.any(k)) cols.store(d_post, k, raw[k]);
+    if (pre && cols.any(k)) cols.load(static_cast<const PT*>(a.w_pre), k, wn[k]);
+    post_weights(k, wg[k]);
   }
-  bool fresh = true;  // a piece begins
+  bool fresh = piece_gate;  // a piece with a gate of its own begins
   int s = 0, flip = 0;
   uint32_t ph = 0;
   const float rh = 1.f / (float)H;
@@ -533,40 +646,56 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
     if (fresh) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
-        f32x2 g[4], w[4];
-        branch_weights(k, row.group, stage, g, w);
+        if (!cols.any(k)) continue;
+        f32x2 g[4];
+        post_weights(k, wg[k]);
+        cols.load(static_cast<const PT*>(a.gate) + row.group * H, k, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wg[k][i] = mul(w[i], g[i]);
+        for (int i = 0; i < 4; ++i) wg[k][i] = mul(wg[k][i], g[i]);
       }
       fresh = false;
     }
+    const uint32_t xr = row_at<ODD>(stage, ring.x, row.t, H * sizeof(ST));
+    const uint32_t vr = row_at<ODD>(stage, ring.v, row.t, H * sizeof(BT));
+    const uint32_t fr = row_at<ODD>(stage, ring.f, row.t, H * sizeof(BT));
+    const uint32_t ur = row_at<ODD>(stage, ring.u, row.t, H * sizeof(ST));
     // a row's values: r', branch, the gradients of r' and of n
-    auto read = [&](int c, f32x2 (&x)[4], f32x2 (&f)[4], f32x2 (&u)[4], f32x2 (&v)[4]) {
+    auto read = [&](int k, f32x2 (&x)[4], f32x2 (&f)[4], f32x2 (&u)[4], f32x2 (&v)[4]) {
       auto none = [](f32x2 (&z)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = both(0.f);
       };
       if (pre) {
-        lds_pairs<ST>(stage + ring.x + c * (int)sizeof(ST), x);
-        lds_pairs<BT>(stage + ring.v + c * (int)sizeof(BT), v);
+        cols.template stage<ST>(xr, k, x);
+        cols.template stage<BT>(vr, k, v);
       } else {
         none(x);
         none(v);
       }
-      if (FULL || ring.f >= 0) lds_pairs<BT>(stage + ring.f + c * (int)sizeof(BT), f); else none(f);
-      if (FULL || ring.u >= 0) lds_pairs<ST>(stage + ring.u + c * (int)sizeof(ST), u); else none(u);
+      if (FULL || ring.f >= 0) cols.template stage<BT>(fr, k, f); else none(f);
+      if (FULL || ring.u >= 0) cols.template stage<ST>(ur, k, u); else none(u);
+    };
+    // the row's own gate, and w_post times it
+    auto gates = [&](int k, f32x2 (&g)[4], f32x2 (&w)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = wg[k][i];
+      if (!own_gate) return;
+      cols.template stage<PT>(row_at<ODD>(stage, ring.g, row.t, H * sizeof(PT)), k, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = mul(w[i], g[i]);
     };
     f32x2 acc[6];
 #pragma unroll
     for (int i = 0; i < 6; ++i) acc[i] = both(0.f);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      if (c0 + k * step >= H) continue;
-      f32x2 x[4], f[4], u[4], v[4];
-      read(c0 + k * step, x, f, u, v);
+      if (!cols.any(k)) continue;
+      f32x2 x[4], f[4], u[4], v[4], g[4], w[4];
+      read(k, x, f, u, v);
+      gates(k, g, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f32x2 wv = mul(wn[k][i], v[i]), ef = mul(wg[k][i], f[i]);
+        const f32x2 wv = mul(wn[k][i], v[i]), ef = mul(w[i], f[i]);
         acc[0] = fma(x[i], x[i], acc[0]);
         acc[1] = fma(wv, x[i], acc[1]);
         acc[2] = fma(f[i], f[i], acc[2]);
@@ -585,12 +714,13 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
     const float cs =
         post ? sf * sf * sf * rh * (pre ? sum[3] + q * sum[4] - cq * sum[5] : sum[3]) : 0.f;
     const f32x2 q2 = both(q), ncq = both(-cq), sf2 = both(sf), ncs = both(-cs), scale = both(a.scale);
-    const int64_t at = row.t * H + c0;
+    const int64_t at = row.t * H;
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
-      if (c0 + k * step >= H) continue;
-      f32x2 x[4], f[4], u[4], v[4], dr[4];
-      read(c0 + k * step, x, f, u, v);
+      if (!cols.any(k)) continue;
+      f32x2 x[4], f[4], u[4], v[4], g[4], w[4], dr[4];
+      read(k, x, f, u, v);
+      gates(k, g, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f32x2 d = u[i];
@@ -599,36 +729,43 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
           d = fma(ncq, x[i], fma(q2, mul(wn[k][i], v[i]), d));
           d_pre[k][i] = fma(v[i], xq, d_pre[k][i]);
         }
-        raw[k][i] = fma(d, mul(sf2, f[i]), raw[k][i]);
+        const f32x2 fs = mul(sf2, f[i]);
+        if (own_gate) {  // its gradient leaves with the row; the sum is of g d f s
+          const f32x2 own = mul(d, fs);
+          raw[k][i] = fma(g[i], own, raw[k][i]);
+          g[i] = mul(wg[k][i], own);
+        } else {
+          raw[k][i] = fma(d, fs, raw[k][i]);
+        }
         dr[i] = mul(scale, d);
-        f[i] = fma(ncs, f[i], mul(sf2, mul(wg[k][i], d)));
+        f[i] = fma(ncs, f[i], mul(sf2, mul(w[i], d)));
       }
-      store_pairs(static_cast<ST*>(a.dr) + at + k * step, dr);
-      if (FULL || a.df != nullptr) store_pairs(static_cast<BT*>(a.df) + at + k * step, f);
+      cols.store(static_cast<ST*>(a.dr) + at, k, dr);
+      if (FULL || a.df != nullptr) cols.store(static_cast<BT*>(a.df) + at, k, f);
+      if (own_gate) cols.store(static_cast<PT*>(a.d_gate) + at, k, g);
     }
-    if (row.t + 1 == row.t1) {  // the piece ends
+    if (piece_gate && row.t + 1 == row.t1) {  // the piece ends
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
-        const int c = c0 + k * step;
-        if (c >= H) continue;
+        if (!cols.any(k)) continue;
         f32x2 g[4], w[4], sum_post[4];
-        branch_weights(k, row.group, stage, g, w);
+        post_weights(k, w);
+        cols.load(static_cast<const PT*>(a.gate) + row.group * H, k, g);
         if (post) {
-          load_pairs(d_post + c, sum_post);
+          cols.load(d_post, k, sum_post);
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum_post[i] = fma(g[i], raw[k][i], sum_post[i]);
-          store_pairs(d_post + c, sum_post);
+          cols.store(d_post, k, sum_post);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           w[i] = mul(w[i], raw[k][i]);
           raw[k][i] = both(0.f);
         }
-        if (!gated) continue;
         if (a.part_gate != nullptr)
-          store_pairs(a.part_gate + row.piece * H + c, w);
+          cols.store(a.part_gate + row.piece * H, k, w);
         else
-          store_pairs(static_cast<PT*>(a.d_gate) + row.group * H + c, w);
+          cols.store(static_cast<PT*>(a.d_gate) + row.group * H, k, w);
       }
       fresh = true;
     }
@@ -640,14 +777,15 @@ __global__ void __launch_bounds__(512) k_norm_bwd_rows(NormArgs a, RowRing ring)
   }
 #pragma unroll
   for (int k = 0; k < kVecs; ++k) {
-    const int c = c0 + k * step;
-    if (c >= H) continue;
+    if (!cols.any(k)) continue;
     if (post) {
       f32x2 sum_post[4];
-      load_pairs(d_post + c, sum_post);
-      store_pairs(a.part_post + (int64_t)blockIdx.x * H + c, sum_post);
+      cols.load(d_post, k, sum_post);  // zero unless pieces have gates
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum_post[i] = fma(both(1.f), raw[k][i], sum_post[i]);
+      cols.store(a.part_post + (int64_t)blockIdx.x * H, k, sum_post);
     }
-    if (pre) store_pairs(a.part_pre + (int64_t)blockIdx.x * H + c, d_pre[k]);
+    if (pre) cols.store(a.part_pre + (int64_t)blockIdx.x * H, k, d_pre[k]);
   }
 }
 
@@ -690,16 +828,18 @@ struct BwdPlan : RowPlan {
   size_t off_post, off_pre, off_gate, total;
 };
 
-// Working threads of a block, 16 columns each, and the blocks that share an SM: 512 threads (the
-// registers of the column sums).
-inline int row_threads(int64_t H) { return (int)((H + 511) / 512 * 32); }
-inline int64_t blocks_per_sm(int64_t H) {
-  return std::max<int64_t>(1, 512 / (row_threads(std::min<int64_t>(H, kMaxRingH)) + 32));
+// Working threads of a block (see Shape), and the blocks that share an SM: all of its registers.
+inline int row_threads(int64_t H, bool odd) {
+  const int64_t h = std::min<int64_t>(H, kMaxRingH / (odd ? 2 : 1));
+  return (int)(odd ? (h + 255) / 256 * 32 : (h + 511) / 512 * 32);
+}
+inline int64_t blocks_per_sm(int64_t H, bool odd) {
+  return std::max<int64_t>(1, kRowThreads / (row_threads(H, odd) + 32));
 }
 
 BwdPlan plan_bwd(const mm_norm_desc& d, int sms) {
   BwdPlan p{};
-  static_cast<RowPlan&>(p) = plan_rows(d, sms * blocks_per_sm(d.H));
+  static_cast<RowPlan&>(p) = plan_rows(d, sms * std::max(blocks_per_sm(d.H, false), blocks_per_sm(d.H, true)));
   const size_t slice = ((size_t)d.H * 4 + 255) / 256 * 256;
   p.off_post = 0;
   p.off_pre = slice * (size_t)p.blocks;
@@ -711,23 +851,24 @@ BwdPlan plan_bwd(const mm_norm_desc& d, int sms) {
 
 // The row ring of a problem with at most `per_sm` blocks on an SM, fewer where rows are so long
 // that less than three stages would fit; depth < 2: it does not fit.
-RowRing plan_ring(const mm_norm_desc& d, const NormArgs& a, bool backward, int64_t& per_sm) {
+RowRing plan_ring(const mm_norm_desc& d, const NormArgs& a, bool backward, bool odd,
+                  int64_t& per_sm) {
   const int sb = (int)(d.H * (d.stream_type == MM_BF16 ? 2 : 4));
   const int bb = (int)(d.H * (d.block_type == MM_BF16 ? 2 : 4));
   const int pb = (int)(d.H * (d.param_type == MM_BF16 ? 2 : 4));
-  RowRing r{-1, -1, -1, -1, -1, 0, 0, 0};
+  RowRing r{-1, -1, -1, -1, -1, 0, 0, odd ? 1 : 0, 0};
   auto add = [&](int& at, bool used, int bytes) {
     if (!used) return;
     at = r.bytes;
-    r.bytes += (bytes + 127) / 128 * 128;
+    r.bytes += (bytes + (odd ? 30 : 0) + 127) / 128 * 128;
   };
   add(r.x, !backward || a.w_pre != nullptr, sb);
   add(r.f, a.f != nullptr, bb);
   add(r.u, backward && a.u != nullptr, sb);
   add(r.v, backward && a.w_pre != nullptr, bb);
-  // a gate that changes every few rows travels with them
-  add(r.g, a.gate != nullptr && a.rows_per_gate < 8, pb);
-  r.tail = backward && a.w_post != nullptr ? (int)d.H * 4 : 0;
+  // a gate that changes every few rows (backward: with every row) travels with them
+  add(r.g, a.gate != nullptr && a.rows_per_gate < (backward ? 2 : 8), pb);
+  r.tail = backward && a.w_post != nullptr ? (int)(d.H + 3) / 4 * 16 : 0;
   auto fit = [&](int64_t blocks) { return (216 * 1024 / blocks - r.tail) / std::max(1, r.bytes); };
   while (per_sm > 1 && fit(per_sm) < 3) --per_sm;
   r.depth = (int)std::min<int64_t>(8, fit(per_sm));
@@ -737,6 +878,15 @@ RowRing plan_ring(const mm_norm_desc& d, const NormArgs& a, bool backward, int64
 // Rows that can move as 16-byte words.
 bool wide(const mm_norm_desc& d, std::initializer_list<const void*> ptrs) {
   if (d.H % 8) return false;
+  for (const void* p : ptrs)
+    if (!aligned_to(p, 16)) return false;
+  return true;
+}
+
+// Rows off 16-byte boundaries that bulk copies can bring all the same: what is copied starts on one.
+bool odd_rows(const mm_norm_desc& d, std::initializer_list<const void*> ptrs) {
+  // (from 64 on no row but the last ends within 16 bytes of the tensor's end)
+  if (d.H < 64 || d.H > kMaxRingH / 2) return false;
   for (const void* p : ptrs)
     if (!aligned_to(p, 16)) return false;
   return true;
@@ -770,22 +920,24 @@ template <auto* KERNEL>
 cudaError_t launch_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
   const cudaError_t e = allow_smem<KERNEL>(216 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3(row_threads(a.H) + 32),
+  return launch_pdl(KERNEL, dim3((unsigned)blocks), dim3(row_threads(a.H, r.odd) + 32),
                     (size_t)r.bytes * r.depth + r.tail, st, a, r);
 }
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_fwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
   const bool full = a.w_post && a.w_pre && a.out && r.g < 0;  // (a post weight has a branch)
-  return full ? launch_rows<&k_norm_fwd_rows<ST, BT, PT, true>>(a, r, blocks, st)
-              : launch_rows<&k_norm_fwd_rows<ST, BT, PT, false>>(a, r, blocks, st);
+  if (r.odd) return launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, true>>(a, r, blocks, st);
+  return full ? launch_rows<&k_norm_fwd_rows<ST, BT, PT, true, false>>(a, r, blocks, st)
+              : launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, false>>(a, r, blocks, st);
 }
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_bwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
   const bool full = a.w_post && a.w_pre && a.u && r.g < 0;
-  return full ? launch_rows<&k_norm_bwd_rows<ST, BT, PT, true>>(a, r, blocks, st)
-              : launch_rows<&k_norm_bwd_rows<ST, BT, PT, false>>(a, r, blocks, st);
+  if (r.odd) return launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, true>>(a, r, blocks, st);
+  return full ? launch_rows<&k_norm_bwd_rows<ST, BT, PT, true, false>>(a, r, blocks, st)
+              : launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, false>>(a, r, blocks, st);
 }
 
 template <typename ST, typename BT>
@@ -876,10 +1028,11 @@ mm_status mm_residual_norm_forward(const mm_norm_desc* d, const void* residual, 
       wide(*d, {residual, branch, post_weight, pre_weight, gate, residual_out, normed});
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int sms = std::max(1, device_sm_count());
-  int64_t per_sm = blocks_per_sm(d->H);
-  const RowRing ring = plan_ring(*d, a, false, per_sm);
+  int64_t per_sm = blocks_per_sm(d->H, !w8);
+  const RowRing ring = plan_ring(*d, a, false, !w8, per_sm);
   // the ring pays from a few rows per block on
-  if (w8 && d->H <= kMaxRingH && d->T > 2 * sms * per_sm && ring.depth >= 2) {
+  if ((w8 || odd_rows(*d, {residual, branch, gate})) && d->H <= kMaxRingH &&
+      d->T > 2 * sms * per_sm && ring.depth >= 2) {
     const RowPlan p = plan_rows(*d, sms * per_sm, ring.g < 0);
     deal_rows(a, p);
     MM_TRY(with_types(*d, [&](auto s0, auto b0, auto p0) {
@@ -952,13 +1105,16 @@ mm_status mm_residual_norm_backward(const mm_norm_desc* d, const void* residual_
   a.part_pre = reinterpret_cast<float*>(ws + p.off_pre);
   const bool w8 = wide(*d, {residual_out, branch, post_weight, pre_weight, gate, d_residual_out,
                             d_normed, d_residual, d_branch, d_gate});
-  int64_t per_sm = blocks_per_sm(d->H);  // (no more than the workspace is laid out for)
-  const RowRing ring = plan_ring(*d, a, true, per_sm);
-  static_cast<RowPlan&>(p) = plan_rows(*d, sms * per_sm);
+  int64_t per_sm = blocks_per_sm(d->H, !w8);  // (no more than the workspace is laid out for)
+  const RowRing ring = plan_ring(*d, a, true, !w8, per_sm);
+  const bool ringed =
+      (w8 || odd_rows(*d, {residual_out, branch, gate, d_residual_out, d_normed})) &&
+      d->H <= kMaxRingH && ring.depth >= 2;
+  const bool own_gate = ringed && ring.g >= 0;
+  static_cast<RowPlan&>(p) = plan_rows(*d, sms * per_sm, !own_gate);
   deal_rows(a, p);
-  const bool gate_parts = gate != nullptr && p.pieces_per_group > 1;
+  const bool gate_parts = gate != nullptr && !own_gate && p.pieces_per_group > 1;
   a.part_gate = gate_parts ? reinterpret_cast<float*>(ws + p.off_gate) : nullptr;
-  const bool ringed = w8 && d->H <= kMaxRingH && ring.depth >= 2;
   MM_TRY(with_types(*d, [&](auto s0, auto b0, auto p0) {
     using ST = decltype(s0);
     using BT = decltype(b0);
