@@ -443,8 +443,8 @@ __device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& r
   }
 }
 
-// FULL: every part is there (branch, both norms, both upstream gradients; a gate, if any, the same
-// for several rows), which takes the tests for the parts out of the loop.
+// FULL: every part is there (branch, both norms, both upstream gradients; OWN: and a gate that comes
+// with its row), which takes the tests for the parts out of the loop.
 //
 // What a thread does per row is the same for 8 columns as for 16 but for the columns themselves:
 // with 8, and single floats, 52 instructions went into an element of the forward, and the issue
@@ -457,7 +457,7 @@ struct Shape {
   static constexpr int VECS = ODD ? 1 : 2;
 };
 
-template <typename ST, typename BT, typename PT, bool FULL, bool ODD>
+template <typename ST, typename BT, typename PT, bool FULL, bool ODD, bool OWN>
 __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRing ring) {
   constexpr int kVecs = Shape<ODD>::VECS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
     produce_rows<ST, BT, PT, ODD>(a, ring, smem_u32(smem), smem_u32(bars), smem_u32(bars + 8));
     return;
   }
+  const bool own_gate = FULL ? OWN : ring.g >= 0;  // the gate comes with the row
   RowWalk row;
   row.start(a, blockIdx.x);
   // weights: of the branch (times the gate, where that is the same for many rows) and of the norm
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
       for (int i = 0; i < 4; ++i) wb[k][i] = both(1.f);
       if (!cols.any(k)) continue;
       if (post) cols.load(static_cast<const PT*>(a.w_post), k, wb[k]);
-      if (a.gate != nullptr && (FULL || ring.g < 0)) {
+      if (a.gate != nullptr && !own_gate) {
         cols.load(static_cast<const PT*>(a.gate) + group * H, k, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) wb[k][i] = mul(wb[k][i], g[i]);
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
   const f32x2 scale = both(a.scale);
   while (row.more(a)) {
     const uint32_t stage = smem_u32(smem) + s * ring.bytes;
-    if (a.gate != nullptr && (FULL || ring.g < 0) && row.group != group) branch_weights(group = row.group);
+    if (a.gate != nullptr && !own_gate && row.group != group) branch_weights(group = row.group);
     mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
     f32x2 x[kVecs][4], y[kVecs][4], acc = both(0.f);
     const uint32_t xr = row_at<ODD>(stage, ring.x, row.t, H * sizeof(ST));
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       if (!cols.any(k)) continue;
-      if (!FULL && ring.g >= 0) {
+      if (own_gate) {
         f32x2 g[4];
         const int64_t gate_row = row.t / a.rows_per_gate;
         cols.template stage<PT>(row_at<ODD>(stage, ring.g, gate_row, H * sizeof(PT)), k, g);
@@ -592,7 +593,7 @@ __device__ __forceinline__ void block_sum_8(float (&v)[8], float* red, int threa
 // Where the gate is the same over a piece, sum d f s gives both its gradient (times w_post) and,
 // times the gate, the piece's share of d_post; a gate per token (own_gate) has its gradient written
 // with the row, and the sum is of g d f s.
-template <typename ST, typename BT, typename PT, bool FULL, bool ODD>
+template <typename ST, typename BT, typename PT, bool FULL, bool ODD, bool OWN>
 __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRing ring) {
   constexpr int kVecs = Shape<ODD>::VECS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
   // weights: w_post (times the piece's gate), w_pre; column sums: of d f s, of v r' q, of d_post
   f32x2 wg[kVecs][4], wn[kVecs][4], raw[kVecs][4], d_pre[kVecs][4];
   float* const d_post = reinterpret_cast<float*>(smem + ring.depth * ring.bytes);  // [H]
-  const bool own_gate = !FULL && ring.g >= 0, piece_gate = gated && !own_gate;
+  const bool own_gate = FULL ? OWN : ring.g >= 0, piece_gate = gated && !own_gate;
   auto post_weights = [&](int k, f32x2 (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = both(1.f);
@@ -926,18 +927,20 @@ cudaError_t launch_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cud
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_fwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
-  const bool full = a.w_post && a.w_pre && a.out && r.g < 0;  // (a post weight has a branch)
-  if (r.odd) return launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, true>>(a, r, blocks, st);
-  return full ? launch_rows<&k_norm_fwd_rows<ST, BT, PT, true, false>>(a, r, blocks, st)
-              : launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, false>>(a, r, blocks, st);
+  if (r.odd) return launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, true, false>>(a, r, blocks, st);
+  if (!(a.w_post && a.w_pre && a.out))  // (a post weight has a branch)
+    return launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, false, false>>(a, r, blocks, st);
+  return r.g < 0 ? launch_rows<&k_norm_fwd_rows<ST, BT, PT, true, false, false>>(a, r, blocks, st)
+                 : launch_rows<&k_norm_fwd_rows<ST, BT, PT, true, false, true>>(a, r, blocks, st);
 }
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_bwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
-  const bool full = a.w_post && a.w_pre && a.u && r.g < 0;
-  if (r.odd) return launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, true>>(a, r, blocks, st);
-  return full ? launch_rows<&k_norm_bwd_rows<ST, BT, PT, true, false>>(a, r, blocks, st)
-              : launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, false>>(a, r, blocks, st);
+  if (r.odd) return launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, true, false>>(a, r, blocks, st);
+  if (!(a.w_post && a.w_pre && a.u))  // (a post weight has a branch)
+    return launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, false, false>>(a, r, blocks, st);
+  return r.g < 0 ? launch_rows<&k_norm_bwd_rows<ST, BT, PT, true, false, false>>(a, r, blocks, st)
+                 : launch_rows<&k_norm_bwd_rows<ST, BT, PT, true, false, true>>(a, r, blocks, st);
 }
 
 template <typename ST, typename BT>
