@@ -20,7 +20,6 @@ tensors are copied to contiguous ones, and everything else runs in libmm.so on t
 from __future__ import annotations
 
 import ctypes
-from functools import lru_cache
 
 import torch
 
@@ -57,16 +56,30 @@ def _on_gpu(op, first, *others):
             raise ValueError(f"{op}: all tensors must be on {first.device}")
 
 
+class _Plans(dict):
+    """What a call of some signature (shapes, types, devices, options) needs: checked and described
+    once. Small calls cost less than their checks."""
+
+    def remember(self, key, plan):
+        if len(self) >= 1024:
+            self.clear()
+        self[key] = plan
+        return plan
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.dtype, t.get_device())
+
+
 # ------------------------------------------------------------------------------- residual_norm
 
-@lru_cache(maxsize=256)
-def _norm_plan(T, H, groups, stream, block, param, scale, eps):
-    """(descriptor, its address, backward workspace bytes) of one problem."""
-    d = _abi.mm_norm_desc(T, H, groups, stream, block, param, scale, eps)
-    return d, ctypes.addressof(d), int(_abi._lib().mm_residual_norm_workspace_size(ctypes.byref(d)))
+_norm_plans = _Plans()
 
 
-def _norm_inputs(residual, branch, post_weight, pre_weight, gate, residual_scale, eps):
+def _norm_plan(residual, branch, post_weight, pre_weight, gate, residual_scale, eps, block_type,
+               key):
+    """Checks the inputs; (address of the descriptor, backward workspace bytes, descriptor).
+    block_type: normed's type where there is no branch."""
     _on_gpu("residual_norm", residual, branch, post_weight, pre_weight, gate)
     if residual.dim() != 2:
         raise ValueError("expected residual[T,H]")
@@ -82,20 +95,24 @@ def _norm_inputs(residual, branch, post_weight, pre_weight, gate, residual_scale
             raise ValueError(f"expected {name}[H]")
     groups = 0
     if gate is not None:
-        if gate.dim() == 1:
-            gate = gate.unsqueeze(0)
-        if gate.dim() != 2 or gate.shape[1] != H or gate.shape[0] < 1 or T % gate.shape[0]:
+        groups = 1 if gate.dim() == 1 else gate.shape[0]
+        if gate.dim() not in (1, 2) or gate.shape[-1] != H or groups < 1 or T % groups:
             raise ValueError("expected gate[H] or gate[G,H] with T a multiple of G")
-        groups = gate.shape[0]
     if any(p.dtype != params[0].dtype for p in params):
         raise TypeError("post_weight, pre_weight and gate must have one dtype")
     stream = _type("residual", residual)
     block = _type("branch", branch) if branch is not None else stream
     if block > stream:
         raise TypeError("a bfloat16 residual needs a bfloat16 branch")
+    if branch is None and block_type is not None:
+        block = _TYPE.get(block_type, 2)
+        if block > stream:
+            raise TypeError("normed must be no wider than the residual")
     param = _type("parameters", params[0]) if params else stream
-    plan = _norm_plan(T, H, groups, stream, block, param, float(residual_scale), float(eps))
-    return plan, gate
+    d = _abi.mm_norm_desc(T, H, groups, stream, block, param, residual_scale, eps)
+    at = ctypes.addressof(d)
+    return _norm_plans.remember(
+        key, (at, int(_abi._lib().mm_residual_norm_workspace_size(at)), d))
 
 
 def residual_norm_forward(residual, branch=None, *, post_weight=None, pre_weight=None, gate=None,
@@ -104,22 +121,21 @@ def residual_norm_forward(residual, branch=None, *, post_weight=None, pre_weight
     rmsnorm(r', pre_weight) (None without a pre_weight). `gate` is [H] (per channel) or [G, H],
     row g for the g-th T / G tokens. normed has the branch's type; without a branch
     `normed_dtype` (the residual's if None)."""
-    plan, gate = _norm_inputs(residual, branch, post_weight, pre_weight, gate, residual_scale, eps)
-    ndt = residual.dtype if branch is None else branch.dtype
-    if branch is None and normed_dtype is not None and normed_dtype != ndt:
-        d = plan[0]
-        if _TYPE.get(normed_dtype, 2) > d.stream_type:
-            raise TypeError("normed_dtype must be no wider than the residual")
-        ndt = normed_dtype
-        plan = _norm_plan(d.T, d.H, d.groups, d.stream_type, _TYPE[ndt], d.param_type,
-                          float(residual_scale), float(eps))
+    key = (_sig(residual), _sig(branch), _sig(post_weight), _sig(pre_weight), _sig(gate),
+           residual_scale, eps, normed_dtype)
+    plan = _norm_plans.get(key) or _norm_plan(residual, branch, post_weight, pre_weight, gate,
+                                              residual_scale, eps, normed_dtype, key)
     residual, branch, gate = _contiguous(residual), _contiguous(branch), _contiguous(gate)
     post_weight, pre_weight = _contiguous(post_weight), _contiguous(pre_weight)
     out = torch.empty_like(residual)
-    normed = torch.empty(residual.shape, dtype=ndt, device=residual.device) \
-        if pre_weight is not None else None
+    normed = None
+    if pre_weight is not None:
+        if branch is not None:
+            normed = torch.empty_like(branch)
+        else:
+            normed = torch.empty_like(residual, dtype=normed_dtype or residual.dtype)
     _abi.check(_abi._lib().mm_residual_norm_forward(
-        plan[1], residual.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(pre_weight), _ptr(gate),
+        plan[0], residual.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(pre_weight), _ptr(gate),
         out.data_ptr(), _ptr(normed), _stream(residual)), "mm_residual_norm_forward")
     return out, normed
 
@@ -129,26 +145,27 @@ def residual_norm_backward(residual_out, branch, d_residual_out, d_normed, *, po
     """(d_residual, d_branch, d_post_weight, d_pre_weight, d_gate) at the forward's residual_out
     and branch; None in the place of what was not given. d_residual_out may be None (zero);
     d_normed is given exactly if pre_weight is."""
-    plan, g2 = _norm_inputs(residual_out, branch, post_weight, pre_weight, gate, residual_scale, eps)
-    if (d_normed is None) != (pre_weight is None):
-        raise ValueError("give d_normed exactly if pre_weight is given")
-    if d_residual_out is None and d_normed is None:
-        raise ValueError("give d_residual_out or d_normed")
-    d = plan[0]
-    if d_residual_out is not None and (d_residual_out.shape != residual_out.shape
-                                       or d_residual_out.dtype != residual_out.dtype):
-        raise ValueError("d_residual_out must have residual_out's shape and dtype")
-    if d_normed is not None:
-        if d_normed.shape != residual_out.shape:
-            raise ValueError("d_normed must have residual_out's shape")
-        block = _type("d_normed", d_normed)
-        if branch is None and block < d.stream_type:
-            plan = _norm_plan(d.T, d.H, d.groups, d.stream_type, block, d.param_type,
-                              float(residual_scale), float(eps))
-        elif block != d.block_type:
-            raise TypeError("d_normed must have the branch's dtype")
-    _on_gpu("residual_norm", residual_out, d_residual_out, d_normed)
-    residual_out, branch, g2 = _contiguous(residual_out), _contiguous(branch), _contiguous(g2)
+    key = (_sig(residual_out), _sig(branch), _sig(post_weight), _sig(pre_weight), _sig(gate),
+           residual_scale, eps, _sig(d_residual_out), _sig(d_normed))
+    plan = _norm_plans.get(key)
+    if plan is None:
+        if (d_normed is None) != (pre_weight is None):
+            raise ValueError("give d_normed exactly if pre_weight is given")
+        if d_residual_out is None and d_normed is None:
+            raise ValueError("give d_residual_out or d_normed")
+        _on_gpu("residual_norm", residual_out, d_residual_out, d_normed)
+        if d_residual_out is not None and (d_residual_out.shape != residual_out.shape
+                                           or d_residual_out.dtype != residual_out.dtype):
+            raise ValueError("d_residual_out must have residual_out's shape and dtype")
+        if d_normed is not None:
+            _type("d_normed", d_normed)
+            if d_normed.shape != residual_out.shape:
+                raise ValueError("d_normed must have residual_out's shape")
+            if branch is not None and d_normed.dtype != branch.dtype:
+                raise TypeError("d_normed must have the branch's dtype")
+        plan = _norm_plan(residual_out, branch, post_weight, pre_weight, gate, residual_scale, eps,
+                          None if d_normed is None else d_normed.dtype, key)
+    residual_out, branch, gate = _contiguous(residual_out), _contiguous(branch), _contiguous(gate)
     d_residual_out, d_normed = _contiguous(d_residual_out), _contiguous(d_normed)
     post_weight, pre_weight = _contiguous(post_weight), _contiguous(pre_weight)
     like = torch.empty_like
@@ -156,12 +173,12 @@ def residual_norm_backward(residual_out, branch, d_residual_out, d_normed, *, po
     df = None if branch is None else like(branch)
     dpost = None if post_weight is None else like(post_weight)
     dpre = None if pre_weight is None else like(pre_weight)
-    dg = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
-    ws = torch.empty(plan[2], dtype=torch.uint8, device=residual_out.device)
+    dg = None if gate is None else like(gate)
+    ws = torch.empty(plan[1], dtype=torch.uint8, device=residual_out.device)
     _abi.check(_abi._lib().mm_residual_norm_backward(
-        plan[1], residual_out.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(pre_weight),
-        _ptr(g2), _ptr(d_residual_out), _ptr(d_normed), dr.data_ptr(), _ptr(df), _ptr(dpost),
-        _ptr(dpre), _ptr(dg), ws.data_ptr(), plan[2], _stream(residual_out)),
+        plan[0], residual_out.data_ptr(), _ptr(branch), _ptr(post_weight), _ptr(pre_weight),
+        _ptr(gate), _ptr(d_residual_out), _ptr(d_normed), dr.data_ptr(), _ptr(df), _ptr(dpost),
+        _ptr(dpre), _ptr(dg), ws.data_ptr(), plan[1], _stream(residual_out)),
         "mm_residual_norm_backward")
     return dr, df, dpost, dpre, dg
 
@@ -200,15 +217,12 @@ def residual_norm(residual, branch=None, *, post_weight=None, pre_weight=None, g
 
 # ------------------------------------------------------------------------------- router
 
-@lru_cache(maxsize=256)
-def _router_plan(T, E, K, logits_type, score, normalize, scale):
-    d = _abi.mm_router_desc(T, E, K, logits_type, _SCORE[score], int(normalize), scale)
-    return d, ctypes.addressof(d), int(_abi._lib().mm_router_workspace_size(ctypes.byref(d)))
+_router_plans = _Plans()
 
 
-def _router_inputs(logits, k, score, normalize, scale):
-    if not logits.is_cuda:
-        raise ValueError("the router runs on a CUDA device only (no CPU path)")
+def _router_plan(logits, k, score, normalize, scale, bias, key):
+    """Checks the inputs; (address of the descriptor, workspace bytes, T, E, device, descriptor)."""
+    _on_gpu("the router", logits, bias)
     if logits.dim() != 2:
         raise ValueError("expected logits[T,E]")
     if score not in _SCORE:
@@ -216,7 +230,13 @@ def _router_inputs(logits, k, score, normalize, scale):
     T, E = logits.shape
     if not 1 <= k <= E:
         raise ValueError("expected 1 <= k <= E")
-    return _router_plan(T, E, int(k), _type("logits", logits), score, bool(normalize), float(scale))
+    if bias is not None and (bias.shape != (E,) or bias.dtype != torch.float32):
+        raise ValueError("expected bias[E] in float32")
+    d = _abi.mm_router_desc(T, E, int(k), _type("logits", logits), _SCORE[score], int(bool(normalize)),
+                            scale)
+    at = ctypes.addressof(d)
+    ws = int(_abi._lib().mm_router_workspace_size(at))
+    return _router_plans.remember(key, (at, ws, T, E, logits.device, d))
 
 
 def router_forward(logits, k, *, bias=None, score="softmax", normalize=True, scale=1.0,
@@ -224,47 +244,47 @@ def router_forward(logits, k, *, bias=None, score="softmax", normalize=True, sca
     """(topk_ids int32 [T,k], topk_weights fp32 [T,k], prob_sum fp32 [E], lse fp32 [T]); the last
     two are None without `stats`. See mm_ops.h for the definitions. `bias` fp32 [E] takes part in
     the selection only."""
-    plan = _router_inputs(logits, k, score, normalize, scale)
-    T, E = logits.shape
-    if bias is not None:
-        if bias.shape != (E,) or bias.dtype != torch.float32 or bias.device != logits.device:
-            raise ValueError("expected bias[E] in float32 on the logits' device")
-        bias = _contiguous(bias)
-    logits = _contiguous(logits)
-    dev = logits.device
+    key = (_sig(logits), k, score, normalize, scale, _sig(bias))
+    at, ws_bytes, T, E, dev, _ = _router_plans.get(key) or _router_plan(
+        logits, k, score, normalize, scale, bias, key)
+    logits, bias = _contiguous(logits), _contiguous(bias)
     ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
     prob_sum = lse = ws = None
     if stats:
         prob_sum = torch.empty(E, dtype=torch.float32, device=dev)
         lse = torch.empty(T, dtype=torch.float32, device=dev)
-        ws = torch.empty(plan[2], dtype=torch.uint8, device=dev)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     _abi.check(_abi._lib().mm_router_forward(
-        plan[1], logits.data_ptr(), _ptr(bias), ids.data_ptr(), weights.data_ptr(), _ptr(prob_sum),
-        _ptr(lse), _ptr(ws), plan[2] if stats else 0, _stream(logits)), "mm_router_forward")
+        at, logits.data_ptr(), _ptr(bias), ids.data_ptr(), weights.data_ptr(), _ptr(prob_sum),
+        _ptr(lse), _ptr(ws), ws_bytes if stats else 0, _stream(logits)), "mm_router_forward")
     return ids, weights, prob_sum, lse
 
 
 def router_backward(logits, topk_ids, d_weights, d_prob_sum=None, d_lse=None, *, score="softmax",
                     normalize=True, scale=1.0):
     """d_logits (the logits' type) from the gradients of topk_weights, prob_sum and lse."""
-    if topk_ids.dim() != 2 or topk_ids.dtype != torch.int32:
-        raise ValueError("expected topk_ids[T,k] in int32")
-    plan = _router_inputs(logits, topk_ids.shape[1], score, normalize, scale)
-    T, E = logits.shape
-    _on_gpu("the router", logits, topk_ids, d_weights, d_prob_sum, d_lse)
-    for name, t, shape in (("topk_ids", topk_ids, (T, topk_ids.shape[1])),
-                           ("d_weights", d_weights, tuple(topk_ids.shape)),
-                           ("d_prob_sum", d_prob_sum, (E,)), ("d_lse", d_lse, (T,))):
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"expected {name} of shape {shape}")
-        if t is not None and t is not topk_ids and t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32")
+    key = (_sig(logits), _sig(topk_ids), _sig(d_weights), _sig(d_prob_sum), _sig(d_lse), score,
+           normalize, scale)
+    plan = _router_plans.get(key)
+    if plan is None:
+        if topk_ids.dim() != 2 or topk_ids.dtype != torch.int32:
+            raise ValueError("expected topk_ids[T,k] in int32")
+        _on_gpu("the router", logits, topk_ids, d_weights, d_prob_sum, d_lse)
+        T, E = logits.shape if logits.dim() == 2 else (-1, -1)
+        for name, t, shape in (("topk_ids", topk_ids, (T, topk_ids.shape[1])),
+                               ("d_weights", d_weights, tuple(topk_ids.shape)),
+                               ("d_prob_sum", d_prob_sum, (E,)), ("d_lse", d_lse, (T,))):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"expected {name} of shape {shape}")
+            if t is not None and t is not topk_ids and t.dtype != torch.float32:
+                raise TypeError(f"{name} must be float32")
+        plan = _router_plan(logits, topk_ids.shape[1], score, normalize, scale, None, key)
     logits, topk_ids, d_weights = _contiguous(logits), _contiguous(topk_ids), _contiguous(d_weights)
     d_prob_sum, d_lse = _contiguous(d_prob_sum), _contiguous(d_lse)
     dz = torch.empty_like(logits)
     _abi.check(_abi._lib().mm_router_backward(
-        plan[1], logits.data_ptr(), topk_ids.data_ptr(), d_weights.data_ptr(), _ptr(d_prob_sum),
+        plan[0], logits.data_ptr(), topk_ids.data_ptr(), d_weights.data_ptr(), _ptr(d_prob_sum),
         _ptr(d_lse), dz.data_ptr(), _stream(logits)), "mm_router_backward")
     return dz
 

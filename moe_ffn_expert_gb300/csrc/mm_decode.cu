@@ -319,11 +319,10 @@ __device__ void select_row(const DecodeArgs& a, Building& bd, const float* row, 
       if (lane * NV + j < a.E) sum += expf(z[j] - m);
     sum = warp_sum(sum);
   }
-  const int id = select_topk<NV>(key, a.K, lane);
+  const int id = select_topk<NV>(key, a.K, lane, bd.id + t * a.K);
   const float zs = lane < a.K ? row[id] : 0.f;
   const float w = selected_weight(zs, lane < a.K, a.score, a.normalize, a.scale, m, sum);
   if (lane < a.K) {
-    bd.id[t * a.K + lane] = (int16_t)id;
     bd.slot_w[t * a.K + lane] = w;
     if (blockIdx.x == 0) {
       if (a.ids != nullptr) a.ids[t * a.K + lane] = id;

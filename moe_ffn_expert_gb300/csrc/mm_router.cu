@@ -22,7 +22,7 @@
 namespace mm {
 namespace {
 
-constexpr int kWarps = 8;  // rows in flight per block
+constexpr int kWarps = 16;  // rows in flight per block
 
 struct RouterArgs {
   int64_t T;
@@ -43,6 +43,44 @@ __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 
+// The lane's NV logits, of experts lane * NV on; zero past E. `words`: whole rows of aligned words.
+template <typename LT, int NV>
+__device__ __forceinline__ void load_logits(const LT* row, int E, int lane, bool words,
+                                            float (&z)[NV]) {
+  constexpr int BYTES = NV * sizeof(LT);
+  if constexpr (BYTES == 8 || BYTES % 16 == 0) {
+    if (words) {
+      const LT* at = row + lane * NV;
+      if constexpr (BYTES == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        if constexpr (sizeof(LT) == 2) {
+          z[0] = bf16_lo(v.x), z[1] = bf16_hi(v.x), z[2] = bf16_lo(v.y), z[3] = bf16_hi(v.y);
+        } else {
+          z[0] = __uint_as_float(v.x), z[1] = __uint_as_float(v.y);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < BYTES / 16; ++j) {
+          const uint4 v = reinterpret_cast<const uint4*>(at)[j];
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(LT) == 2) {
+              z[8 * j + 2 * i] = bf16_lo(u[i]);
+              z[8 * j + 2 * i + 1] = bf16_hi(u[i]);
+            } else {
+              z[4 * j + i] = __uint_as_float(u[i]);
+            }
+          }
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) z[j] = lane * NV + j < E ? load_logit(row + lane * NV + j) : 0.f;
+}
+
 template <int NV>
 __device__ __forceinline__ float row_max(const float (&z)[NV], int E, int lane) {
   float m = -INFINITY;
@@ -55,11 +93,14 @@ __device__ __forceinline__ float row_max(const float (&z)[NV], int E, int lane) 
 
 template <typename LT, int NV>
 __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
-  __shared__ float part[kWarps][32];
+  constexpr int SUMS = NV < 4 ? NV : 4;  // probabilities per lane summed over the warps at a time
+  __shared__ float part[kWarps][32 * SUMS];
+  __shared__ int slot[kWarps][16];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, K = a.K;
+  const bool words = E == 32 * NV && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
   const bool all = a.prob_part != nullptr || (a.score == MM_SCORE_SOFTMAX && !a.normalize);
   float acc[NV];
 #pragma unroll
@@ -68,11 +109,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
     const LT* row = static_cast<const LT*>(a.logits) + t * E;
     float z[NV];
     uint32_t key[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = lane * NV + j;
-      z[j] = e < E ? load_logit(row + e) : 0.f;
-    }
+    load_logits<LT, NV>(row, E, lane, words, z);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int e = lane * NV + j;
@@ -111,7 +148,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
       }
       if (lane == 0) a.lse[t] = m + logf(s);
     }
-    const int id = select_topk<NV>(key, K, lane);
+    const int id = select_topk<NV>(key, K, lane, &slot[warp][0]);
     const float zs = lane < K ? load_logit(row + id) : 0.f;
     const float w = selected_weight(zs, lane < K, a.score, a.normalize, a.scale, m, A);
     if (lane < K) {
@@ -121,14 +158,16 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
   }
   if (a.prob_part == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {  // the block's warps, in order
-    part[warp][lane] = acc[j];
+  for (int j = 0; j < NV; j += SUMS) {  // the block's warps, in order
+#pragma unroll
+    for (int i = 0; i < SUMS; ++i) part[warp][lane * SUMS + i] = acc[j + i];
     __syncthreads();
-    if (warp == 0 && lane * NV + j < E) {
+    const int e = (int)threadIdx.x / SUMS * NV + j + (int)threadIdx.x % SUMS;
+    if (threadIdx.x < 32 * SUMS && e < E) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) s += part[i][lane];
-      a.prob_part[(int64_t)blockIdx.x * E + lane * NV + j] = s;
+      for (int i = 0; i < kWarps; ++i) s += part[i][threadIdx.x];
+      a.prob_part[(int64_t)blockIdx.x * E + e] = s;
     }
     __syncthreads();
   }
@@ -139,17 +178,15 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = a.E, K = a.K;
+  const bool words = E == 32 * NV && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
   const bool soft = a.score == MM_SCORE_SOFTMAX;
   const bool all = a.dP != nullptr || (soft && !a.normalize);
   for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
     const LT* row = static_cast<const LT*>(a.logits) + t * E;
     float z[NV], dz[NV];
+    load_logits<LT, NV>(row, E, lane, words, z);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = lane * NV + j;
-      z[j] = e < E ? load_logit(row + e) : 0.f;
-      dz[j] = 0.f;
-    }
+    for (int j = 0; j < NV; ++j) dz[j] = 0.f;
     const int id_in = lane < K ? a.ids_in[t * K + lane] : -1;
     const bool has = id_in >= 0 && id_in < E;
     const float dw = has ? a.scale * a.dw[t * K + lane] : 0.f;
@@ -214,17 +251,25 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
       for (int j = 0; j < NV; ++j)
         if (e == lane * NV + j) dz[j] += v;
     }
+    LT* const out = static_cast<LT*>(a.dz) + t * E + lane * NV;
+    if (NV >= 8 && words && (reinterpret_cast<uintptr_t>(a.dz) & 15) == 0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (lane * NV + j < E) store_logit(static_cast<LT*>(a.dz) + t * E + lane * NV + j, dz[j]);
+      for (int j = 0; j + 8 <= NV; j += 8)
+        store_vec<8>(out + j, *reinterpret_cast<const float(*)[8]>(dz + (NV >= 8 ? j : 0)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (lane * NV + j < E) store_logit(out + j, dz[j]);
+    }
   }
 }
 
-// 128 columns per block (4 per lane where the width allows 16-byte loads), the parts dealt to 16
-// warps with 8 loads in flight each; the warps' sums are added in order.
-template <int W>
+// LANES x W columns per block, the parts dealt to 512 / LANES slices with 8 loads in flight each;
+// the slices' sums are added in order.
+template <int LANES, int W>
 __global__ void __launch_bounds__(512) k_column_sums(SumArgs a) {
-  __shared__ float part[16][32 * W];
+  constexpr int SLICES = 512 / LANES, COLS = LANES * W;
+  __shared__ float part[SLICES][COLS + 1];
   pdl_wait();
   int k = 0;
 #pragma unroll
@@ -232,31 +277,30 @@ __global__ void __launch_bounds__(512) k_column_sums(SumArgs a) {
     if (i < a.jobs && (int64_t)blockIdx.y >= a.job[i].first) k = i;
   const SumJob job = a.job[k];
   const int64_t y = (int64_t)blockIdx.y - job.first;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = (blockIdx.x * 32 + lane) * W;
+  const int slice = threadIdx.x / LANES, at = threadIdx.x % LANES * W, c = blockIdx.x * COLS + at;
   const float* src = job.src + y * job.parts * a.cols + c;
   float s[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) s[i] = 0.f;
   if (c < a.cols) {
 #pragma unroll 8
-    for (int64_t p = warp; p < job.parts; p += 16) {
-      const float* at = src + p * a.cols;
+    for (int64_t p = slice; p < job.parts; p += SLICES) {
       if constexpr (W == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(at));
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + p * a.cols));
         s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
       } else {
-        s[0] += __ldcg(at);
+        s[0] += __ldcg(src + p * a.cols);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < W; ++i) part[warp][lane * W + i] = s[i];
+  for (int i = 0; i < W; ++i) part[slice][at + i] = s[i];
   __syncthreads();
-  const int col = blockIdx.x * 32 * W + (int)threadIdx.x;
-  if (threadIdx.x < 32 * W && col < a.cols) {
+  const int col = blockIdx.x * COLS + (int)threadIdx.x;
+  if (threadIdx.x < COLS && col < a.cols) {
     float v[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[0] += part[i][threadIdx.x];
+#pragma unroll 16
+    for (int i = 0; i < SLICES; ++i) v[0] += part[i][threadIdx.x];
     store_any<1>(job.dst, a.type, y * a.cols + col, v);
   }
 }
@@ -322,11 +366,13 @@ cudaError_t launch_router(const mm_router_desc& d, const float* logits, const fl
 }
 
 cudaError_t launch_column_sums(const SumArgs& a, int64_t rows, cudaStream_t st) {
-  if (a.cols % 4 == 0)
-    return launch_pdl(k_column_sums<4>, dim3((unsigned)((a.cols + 127) / 128), (unsigned)rows),
-                      dim3(512), 0, st, a);
-  return launch_pdl(k_column_sums<1>, dim3((unsigned)((a.cols + 31) / 32), (unsigned)rows),
-                    dim3(512), 0, st, a);
+  auto grid = [&](int cols) { return dim3((unsigned)((a.cols + cols - 1) / cols), (unsigned)rows); };
+  if (a.cols % 4 != 0) return launch_pdl(k_column_sums<32, 1>, grid(32), dim3(512), 0, st, a);
+  // 128 columns per block read whole lines; 32 share the parts of few columns among more threads
+  // (16384 x 512 backward 45 us with 32 and 51 with 128, 64 x 7168 14 and 11)
+  if (a.cols >= 1024)
+    return launch_pdl(k_column_sums<32, 4>, grid(128), dim3(512), 0, st, a);
+  return launch_pdl(k_column_sums<8, 4>, grid(32), dim3(512), 0, st, a);
 }
 
 }  // namespace mm

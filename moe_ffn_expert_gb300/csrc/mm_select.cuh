@@ -28,42 +28,74 @@ __device__ __forceinline__ float sigmoid_accurate(float z) { return 1.0f / (1.0f
 
 // The K largest of the warp's row: key[j] of a lane belongs to expert lane * NV + j, so among
 // equal keys the lowest lane has the lowest expert. Returns the expert of rank `lane` (lanes
-// >= K: -1). Each lane keeps its own first largest key; a round is one maximum over the warp, a
-// ballot for its lowest holder, and a new largest key for that lane. (A lane's experts dealt out
-// 32 apart need a second reduction per round for the tie, and a rescan in the chain of rounds:
-// 24.4 us instead of 11 for 16384 rows of 128.)
-template <int NV>
-__device__ __forceinline__ int select_topk(uint32_t (&key)[NV], int K, int lane) {
-  int mine = -1;
+// >= K: -1); `slot`: shared memory for the K
+// experts, of the warp's own. Each lane keeps its largest key
+// at hand; a round is one maximum over the warp, a ballot for its lowest holder, which writes its
+// expert to the rank's slot and brings up its next key.
+//   NV <= 4: a lane's keys are sorted first (adjacent exchanges, so equal keys keep their order)
+//   and a round shifts them: 6 moves instead of a search of 13 steps.
+//   NV == 8: the search, in every lane (shorter than a branch of one; sorting 8 takes as long as
+//   nine rounds save). Above that: the search, in the one lane.
+template <int NV, typename ID>
+__device__ __forceinline__ int select_topk(uint32_t (&key)[NV], int K, int lane,
+                                           volatile ID* slot) {
+  const uint32_t lower = (1u << lane) - 1;
+  int at[NV <= 4 ? NV : 1];
   uint32_t best;
-  int at;
   auto scan = [&] {
     best = key[0];
 #pragma unroll
     for (int j = 1; j < NV; ++j) best = max(best, key[j]);
-    at = NV - 1;
+    at[0] = lane * NV + NV - 1;
 #pragma unroll
-    for (int j = NV - 2; j >= 0; --j) at = key[j] == best ? j : at;
+    for (int j = NV - 2; j >= 0; --j) at[0] = key[j] == best ? lane * NV + j : at[0];
   };
-  scan();
+  if constexpr (NV <= 4) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) at[j] = lane * NV + j;
+#pragma unroll
+    for (int pass = 0; pass < NV; ++pass)
+#pragma unroll
+      for (int j = pass & 1; j + 1 < NV; j += 2) {
+        const uint32_t x = key[j], y = key[j + 1];
+        const int ax = at[j], ay = at[j + 1];
+        const bool swap = y > x;
+        key[j] = swap ? y : x, key[j + 1] = swap ? x : y;
+        at[j] = swap ? ay : ax, at[j + 1] = swap ? ax : ay;
+      }
+    best = key[0];
+  } else {
+    scan();
+  }
 #pragma unroll 1
   for (int k = 0; k < K; ++k) {
     const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const uint32_t holders = __ballot_sync(0xFFFFFFFFu, best == top);
-    const int owner = __ffs(holders) - 1;
-    const int e = __shfl_sync(0xFFFFFFFFu, lane * NV + at, owner);
-    if (lane == k) mine = e;
-    if constexpr (NV <= 8) {  // in every lane: shorter than a branch of one
+    const bool holds = best == top;
+    const uint32_t holders = __ballot_sync(0xFFFFFFFFu, holds);
+    const bool owner = holds && (holders & lower) == 0;
+    if (owner) slot[k] = (ID)at[0];
+    if constexpr (NV <= 4) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) key[j] = lane == owner && j == at ? 0u : key[j];
-      scan();
-    } else if (lane == owner) {
+      for (int j = 0; j < NV; ++j) {
+        key[j] = owner ? (j + 1 < NV ? key[j + 1 < NV ? j + 1 : 0] : 0u) : key[j];
+        if (j + 1 < NV) at[j] = owner ? at[j + 1 < NV ? j + 1 : 0] : at[j];
+      }
+      best = key[0];
+    } else if constexpr (NV <= 8) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (j == at) key[j] = 0;
+        key[j] = owner && lane * NV + j == at[0] ? 0u : key[j];
+      scan();
+    } else if (owner) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (lane * NV + j == at[0]) key[j] = 0;
       scan();
     }
   }
+  __syncwarp();
+  const int mine = lane < K ? (int)slot[lane] : -1;
+  __syncwarp();  // the slots may be written again
   return mine;
 }
 
