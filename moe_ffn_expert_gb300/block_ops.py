@@ -121,6 +121,7 @@ def residual_norm_forward(residual, branch=None, *, post_weight=None, pre_weight
     rmsnorm(r', pre_weight) (None without a pre_weight). `gate` is [H] (per channel) or [G, H],
     row g for the g-th T / G tokens. normed has the branch's type; without a branch
     `normed_dtype` (the residual's if None)."""
+    residual_scale, eps = float(residual_scale), float(eps)
     key = (_sig(residual), _sig(branch), _sig(post_weight), _sig(pre_weight), _sig(gate),
            residual_scale, eps, normed_dtype)
     plan = _norm_plans.get(key) or _norm_plan(residual, branch, post_weight, pre_weight, gate,
@@ -145,6 +146,7 @@ def residual_norm_backward(residual_out, branch, d_residual_out, d_normed, *, po
     """(d_residual, d_branch, d_post_weight, d_pre_weight, d_gate) at the forward's residual_out
     and branch; None in the place of what was not given. d_residual_out may be None (zero);
     d_normed is given exactly if pre_weight is."""
+    residual_scale, eps = float(residual_scale), float(eps)
     key = (_sig(residual_out), _sig(branch), _sig(post_weight), _sig(pre_weight), _sig(gate),
            residual_scale, eps, _sig(d_residual_out), _sig(d_normed))
     plan = _norm_plans.get(key)
@@ -232,7 +234,7 @@ def _router_plan(logits, k, score, normalize, scale, bias, key):
         raise ValueError("expected 1 <= k <= E")
     if bias is not None and (bias.shape != (E,) or bias.dtype != torch.float32):
         raise ValueError("expected bias[E] in float32")
-    d = _abi.mm_router_desc(T, E, int(k), _type("logits", logits), _SCORE[score], int(bool(normalize)),
+    d = _abi.mm_router_desc(T, E, k, _type("logits", logits), _SCORE[score], int(normalize),
                             scale)
     at = ctypes.addressof(d)
     ws = int(_abi._lib().mm_router_workspace_size(at))
@@ -244,6 +246,7 @@ def router_forward(logits, k, *, bias=None, score="softmax", normalize=True, sca
     """(topk_ids int32 [T,k], topk_weights fp32 [T,k], prob_sum fp32 [E], lse fp32 [T]); the last
     two are None without `stats`. See mm_ops.h for the definitions. `bias` fp32 [E] takes part in
     the selection only."""
+    k, normalize, scale = int(k), bool(normalize), float(scale)
     key = (_sig(logits), k, score, normalize, scale, _sig(bias))
     at, ws_bytes, T, E, dev, _ = _router_plans.get(key) or _router_plan(
         logits, k, score, normalize, scale, bias, key)
@@ -264,6 +267,7 @@ def router_forward(logits, k, *, bias=None, score="softmax", normalize=True, sca
 def router_backward(logits, topk_ids, d_weights, d_prob_sum=None, d_lse=None, *, score="softmax",
                     normalize=True, scale=1.0):
     """d_logits (the logits' type) from the gradients of topk_weights, prob_sum and lse."""
+    normalize, scale = bool(normalize), float(scale)
     key = (_sig(logits), _sig(topk_ids), _sig(d_weights), _sig(d_prob_sum), _sig(d_lse), score,
            normalize, scale)
     plan = _router_plans.get(key)

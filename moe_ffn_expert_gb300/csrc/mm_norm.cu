@@ -365,7 +365,7 @@ struct Columns {
   static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 };
 
-// One thread: the copies of row t into a stage.
+// One warp: the copies of row t into a stage.
 template <typename ST, typename BT, typename PT, bool ODD>
 __device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, uint32_t stage,
                                          uint32_t bar, int64_t t) {
@@ -373,21 +373,23 @@ __device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, ui
   Span ps{0, 0};
   if (r.g >= 0)
     ps = row_span<ODD>(t / a.rows_per_gate, a.T / a.rows_per_gate, a.H * sizeof(PT));
-  if (ODD && t + 1 == a.T) {  // what the copies leave out, before the arrival below
-    auto rest = [&](int offset, const void* base, const Span& span, int64_t total) {
-      const char* src = static_cast<const char*>(base) + span.from;
-      if (offset >= 0)
-        for (uint32_t i = span.bytes; (int64_t)i < total - span.from; i += 2)
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + offset + i),
-                       "h"(*reinterpret_cast<const uint16_t*>(src + i))
-                       : "memory");
+  const int lane = threadIdx.x & 31;
+  if (ODD && t + 1 == a.T) {  // what the copies leave out, up to 7 words of each tensor
+    auto rest = [&](int at, int offset, const void* base, const Span& span, int64_t total) {
+      const int64_t i = span.from + span.bytes + 2 * (lane & 7);
+      if (offset >= 0 && (lane >> 3) == at && i < total)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + offset + (uint32_t)(i - span.from)),
+                     "h"(*reinterpret_cast<const uint16_t*>(static_cast<const char*>(base) + i))
+                     : "memory");
     };
-    rest(r.x, a.r, ss, a.T * a.H * sizeof(ST));
-    rest(r.f, a.f, bs, a.T * a.H * sizeof(BT));
-    rest(r.u, a.u, ss, a.T * a.H * sizeof(ST));
-    rest(r.v, a.v, bs, a.T * a.H * sizeof(BT));
-    rest(r.g, a.gate, ps, r.g >= 0 ? a.T / a.rows_per_gate * a.H * sizeof(PT) : 0);
+    rest(0, r.x, a.r, ss, a.T * a.H * sizeof(ST));
+    rest(1, r.f, a.f, bs, a.T * a.H * sizeof(BT));
+    rest(2, r.u, a.u, ss, a.T * a.H * sizeof(ST));
+    rest(3, r.v, a.v, bs, a.T * a.H * sizeof(BT));
+    rest(0, r.g, a.gate, ps, r.g >= 0 ? a.T / a.rows_per_gate * a.H * sizeof(PT) : 0);
+    __syncwarp();
   }
+  if (lane != 0) return;
   mbar_arrive_expect_tx(bar, (r.x >= 0 ? ss.bytes : 0) + (r.f >= 0 ? bs.bytes : 0) +
                                  (r.u >= 0 ? ss.bytes : 0) + (r.v >= 0 ? bs.bytes : 0) + ps.bytes);
   auto copy = [&](int offset, const void* base, const Span& span) {
@@ -430,7 +432,6 @@ __device__ __forceinline__ float block_sum_1(float v, float* red, int threads) {
 template <typename ST, typename BT, typename PT, bool ODD>
 __device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& ring, uint32_t smem,
                                              uint32_t full, uint32_t empty) {
-  if ((threadIdx.x & 31) != 0) return;
   RowWalk row;
   row.start(a, blockIdx.x);
   int s = 0;
@@ -927,8 +928,12 @@ cudaError_t launch_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cud
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_fwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
-  if (r.odd) return launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, true, false>>(a, r, blocks, st);
-  if (!(a.w_post && a.w_pre && a.out))  // (a post weight has a branch)
+  const bool full = a.w_post && a.w_pre && a.out;  // (a post weight has a branch)
+  if (r.odd)
+    return full && r.g < 0
+               ? launch_rows<&k_norm_fwd_rows<ST, BT, PT, true, true, false>>(a, r, blocks, st)
+               : launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, true, false>>(a, r, blocks, st);
+  if (!full)
     return launch_rows<&k_norm_fwd_rows<ST, BT, PT, false, false, false>>(a, r, blocks, st);
   return r.g < 0 ? launch_rows<&k_norm_fwd_rows<ST, BT, PT, true, false, false>>(a, r, blocks, st)
                  : launch_rows<&k_norm_fwd_rows<ST, BT, PT, true, false, true>>(a, r, blocks, st);
@@ -936,8 +941,12 @@ cudaError_t launch_fwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks,
 
 template <typename ST, typename BT, typename PT>
 cudaError_t launch_bwd_rows(const NormArgs& a, const RowRing& r, int64_t blocks, cudaStream_t st) {
-  if (r.odd) return launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, true, false>>(a, r, blocks, st);
-  if (!(a.w_post && a.w_pre && a.u))  // (a post weight has a branch)
+  const bool full = a.w_post && a.w_pre && a.u;  // (a post weight has a branch)
+  if (r.odd)
+    return full && r.g < 0
+               ? launch_rows<&k_norm_bwd_rows<ST, BT, PT, true, true, false>>(a, r, blocks, st)
+               : launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, true, false>>(a, r, blocks, st);
+  if (!full)
     return launch_rows<&k_norm_bwd_rows<ST, BT, PT, false, false, false>>(a, r, blocks, st);
   return r.g < 0 ? launch_rows<&k_norm_bwd_rows<ST, BT, PT, true, false, false>>(a, r, blocks, st)
                  : launch_rows<&k_norm_bwd_rows<ST, BT, PT, true, false, true>>(a, r, blocks, st);
