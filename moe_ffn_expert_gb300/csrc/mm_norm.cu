@@ -371,22 +371,27 @@ __device__ __forceinline__ void load_row(const NormArgs& a, const RowRing& r, ui
                                          uint32_t bar, int64_t t) {
   const Span ss = row_span<ODD>(t, a.T, a.H * sizeof(ST)), bs = row_span<ODD>(t, a.T, a.H * sizeof(BT));
   Span ps{0, 0};
-  if (r.g >= 0)
-    ps = row_span<ODD>(t / a.rows_per_gate, a.T / a.rows_per_gate, a.H * sizeof(PT));
+  const bool last = t + 1 == a.T;
+  bool last_gate = false;  // the gate's last row serves several
+  if (r.g >= 0) {
+    const int64_t gate = t / a.rows_per_gate, gates = a.T / a.rows_per_gate;
+    ps = row_span<ODD>(gate, gates, a.H * sizeof(PT));
+    last_gate = gate + 1 == gates;
+  }
   const int lane = threadIdx.x & 31;
-  if (ODD && t + 1 == a.T) {  // what the copies leave out, up to 7 words of each tensor
-    auto rest = [&](int at, int offset, const void* base, const Span& span, int64_t total) {
+  if (ODD && (last || last_gate)) {  // what the copies leave out, up to 7 words of each tensor
+    auto rest = [&](int at, bool use, int offset, const void* base, const Span& span, int64_t total) {
       const int64_t i = span.from + span.bytes + 2 * (lane & 7);
-      if (offset >= 0 && (lane >> 3) == at && i < total)
+      if (use && offset >= 0 && (lane >> 3) == at && i < total)
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + offset + (uint32_t)(i - span.from)),
                      "h"(*reinterpret_cast<const uint16_t*>(static_cast<const char*>(base) + i))
                      : "memory");
     };
-    rest(0, r.x, a.r, ss, a.T * a.H * sizeof(ST));
-    rest(1, r.f, a.f, bs, a.T * a.H * sizeof(BT));
-    rest(2, r.u, a.u, ss, a.T * a.H * sizeof(ST));
-    rest(3, r.v, a.v, bs, a.T * a.H * sizeof(BT));
-    rest(0, r.g, a.gate, ps, r.g >= 0 ? a.T / a.rows_per_gate * a.H * sizeof(PT) : 0);
+    rest(0, last, r.x, a.r, ss, a.T * a.H * sizeof(ST));
+    rest(1, last, r.f, a.f, bs, a.T * a.H * sizeof(BT));
+    rest(2, last, r.u, a.u, ss, a.T * a.H * sizeof(ST));
+    rest(3, last, r.v, a.v, bs, a.T * a.H * sizeof(BT));
+    rest(0, last_gate, r.g, a.gate, ps, r.g >= 0 ? a.T / a.rows_per_gate * a.H * sizeof(PT) : 0);
     __syncwarp();
   }
   if (lane != 0) return;

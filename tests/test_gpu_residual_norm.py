@@ -307,3 +307,96 @@ def test_refusals():
                      (lambda: block_ops.residual_norm_backward(r, f, r, None, pre_weight=i["pre_weight"]), ValueError)):
         with pytest.raises(err):
             bad()
+
+
+# Rows by bulk copies take over the forward above two waves of blocks (a few hundred to a few
+# thousand tokens, by width), and the backward wherever a few rows fit in shared memory.
+
+@pytest.mark.parametrize("T,H,groups", [
+    (1000, 2048, 1), (1000, 2048, 4), (999, 2048, 333), (1001, 2048, 1001), (310, 7168, 1),
+    (310, 7680, 2), (310, 7688, 1), (2500, 512, 2500), (2500, 512, 250), (2501, 200, 0), (3000, 64, 1),
+    # odd: rows start off 16-byte boundaries, the last one ends off one
+    (1000, 2047, 1), (999, 2047, 333), (310, 3839, 310), (620, 3839, 2), (310, 3841, 1),
+    (1601, 1023, 1601), (1100, 1999, 0), (2501, 77, 1), (2501, 65, 1), (2501, 63, 1)])
+@pytest.mark.parametrize("st,bt,pt", [(BF, BF, BF), (F32, BF, F32), (F32, F32, F32)])
+def test_many_rows(T, H, groups, st, bt, pt):
+    check(*make(T, H, st, bt, pt, groups))
+
+
+@pytest.mark.parametrize("post,pre,groups", [(False, True, 1), (True, False, 1), (False, False, 1), (True, True, 0),
+                                             (False, True, 0), (False, False, 1250), (True, False, 1250),
+                                             (False, True, 1250)])
+@pytest.mark.parametrize("H", [1024, 1021])
+def test_parts_left_out_of_many_rows(post, pre, groups, H):
+    check(*make(2500, H, post=post, pre=pre, groups=groups))
+
+
+@pytest.mark.parametrize("H", [1024, 1021])
+def test_many_rows_before_the_first_block(H):
+    check(*make(3300, H, F32, BF, F32, branch=False), scale=1.0)
+
+
+@pytest.mark.parametrize("H", [1024, 1021])
+def test_many_rows_in_place_through_the_c_abi(H):
+    import ctypes
+    T = 3300
+    i, up = make(T, H)
+    (out, n), g = run_both(i, up, scale=1.0)
+    d = _abi.mm_norm_desc(T, H, 1, 0, 0, 0, 1.0, 1e-6)
+    lib, at, st = _abi._lib(), ctypes.addressof(d), torch.cuda.current_stream().cuda_stream
+    r2, f2, dr = i["residual"].clone(), i["branch"].clone(), up["d_out"].clone()
+    w = [i[k].data_ptr() for k in ("post_weight", "pre_weight", "gate")]
+    assert lib.mm_residual_norm_forward(at, r2.data_ptr(), f2.data_ptr(), *w, r2.data_ptr(),
+                                        f2.data_ptr(), st) == 0
+    assert torch.equal(r2, out) and torch.equal(f2, n)
+    nbytes = lib.mm_residual_norm_workspace_size(at)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    sums = [torch.empty_like(i[k]) for k in ("post_weight", "pre_weight", "gate")]
+    df = torch.empty_like(f2)
+    assert lib.mm_residual_norm_backward(
+        at, i["residual"].data_ptr(), i["branch"].data_ptr(), *w, dr.data_ptr(), up["d_normed"].data_ptr(),
+        dr.data_ptr(), df.data_ptr(), *[s.data_ptr() for s in sums], ws.data_ptr(), nbytes, st) == 0
+    assert torch.equal(dr, g["residual"]) and torch.equal(df, g["branch"])
+    assert torch.equal(sums[0], g["post"]) and torch.equal(sums[2], g["gate"])
+
+
+def test_bad_rows_among_many_stay_in_their_rows():
+    i, up = make(2500, 1021, groups=0)
+    clean = run_both(i, up)
+    j = dict(i, residual=i["residual"].clone(), branch=i["branch"].clone())
+    j["residual"][1700, 1020] = float("nan")
+    j["branch"][2499, 0] = float("inf")
+    got = run_both(j, up)
+    rows = [t for t in range(2500) if t not in (1700, 2499)]
+    for a, b in zip((*got[0], got[1]["residual"], got[1]["branch"]),
+                    (*clean[0], clean[1]["residual"], clean[1]["branch"])):
+        assert torch.equal(a[rows], b[rows])
+
+
+@pytest.mark.parametrize("H", [7168, 2047])
+def test_more_than_2_31_elements(H):
+    """The last rows of a tensor whose offsets pass 32 bits, against the oracle for those rows."""
+    T = (2 ** 31 + 4096) // H + 8
+    small, up = make(16, H)
+    def tall(t):
+        return t.repeat((T + 15) // 16, 1)[:T].contiguous()
+    i = dict(small, residual=tall(small["residual"]), branch=tall(small["branch"]))
+    u = {k: tall(t) for k, t in up.items()}
+    (out, n), g = run_both(i, u)
+    at = [t % 16 for t in range(T - 5, T)]
+    part = dict(small, residual=small["residual"][at], branch=small["branch"][at])
+    ro, rn, mo, mn = oracle_forward(part, 0.75, 1e-6)
+    close("residual_out", out[-5:], ro, mo)
+    close("normed", n[-5:], rn, mn)
+    ref = oracle_backward(part, {k: t[at] for k, t in up.items()}, 0.75, 1e-6)
+    close("d_residual", g["residual"][-5:], *ref["residual"])
+    close("d_branch", g["branch"][-5:], *ref["branch"])
+
+
+def test_scale_as_a_tensor_is_read_at_every_call():
+    i, _ = make(4, 64)
+    s = torch.tensor(1.0)
+    a = block_ops.residual_norm_forward(i["residual"], None, residual_scale=s)[0]
+    s.fill_(2.0)
+    b = block_ops.residual_norm_forward(i["residual"], None, residual_scale=s)[0]
+    assert torch.equal(a * 2, b)
