@@ -447,6 +447,8 @@ class MoEDecoder:
             raise ValueError(f"expected topk_ids and topk_weights [T,{self.k}]")
         if topk_ids.dtype not in (torch.int32, torch.int64):
             raise TypeError("topk_ids must be int32 or int64")
+        if topk_ids.device != self.device or topk_weights.device != self.device:
+            raise ValueError(f"expected topk_ids and topk_weights on {self.device}")
         ids = _contiguous(topk_ids.to(torch.int32))
         return self._call(x, ids, _contiguous(topk_weights.to(torch.float32)))
 

@@ -341,3 +341,54 @@ def test_refusals():
                      (lambda: decoder(m, route=True)(m["x"], m["ids"], m["w"]), ValueError)):
         with pytest.raises(err):
             bad()
+
+
+@pytest.mark.parametrize("T", [15, 17, 18, 47, 49])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunks_of_rows_begin_and_end(T, fp8):
+    ids = torch.full((T, 1), 2, device="cuda")
+    check(make(T, 256, 192, 4, 1, fp8, shared=64, ids=ids))
+
+
+@pytest.mark.parametrize("T", [1, 11, 12, 13, 14, 31, 64])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("score,normalize", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_routing_at_every_number_of_tokens(T, fp8, score, normalize):
+    """Selected by the experts' kernel itself, or from 13 tokens on by a launch before it: what a
+    decoder does with its own selection is what one without a router does with the same."""
+    m = make(T, 272, 64, 48, 6, fp8, shared=32)
+    y, ids, w = decoder(m, route=True, score=score, normalize=normalize, max_tokens=64).with_routing(m["x"])
+    z = m["x"].float() @ m["router"].float().t()
+    ids2, w2, _, _ = block_ops.router_forward(z, 6, score=score, normalize=normalize)
+    assert torch.equal(ids, ids2) and torch.allclose(w, w2, rtol=1e-4)
+    assert torch.equal(y, decoder(m, max_tokens=64)(m["x"], ids, w))
+    close(y, reference(m, ids, w))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_experts_whose_offsets_pass_32_bits(fp8):
+    """Only the last experts hold numbers; the ones before are not read."""
+    T, H, I, E, K = 3, 4096, 1024, 300, 2
+    m = make(T, H, I, 2, K, fp8)
+    dt = m["up"].dtype
+    big = dict(m, up=torch.empty(E, H, 2 * I, dtype=dt, device="cuda"), down=torch.empty(E, I, H, dtype=dt, device="cuda"))
+    for k in ("up", "down"):
+        big[k][E - 2:] = m[k]
+    if fp8:
+        for k in ("us", "ds"):
+            big[k] = torch.full((E, *m[k].shape[1:]), float("nan"), device="cuda")
+            big[k][E - 2:] = m[k]
+    assert big["up"].numel() > 2 ** 31
+    y = decoder(m)(m["x"], m["ids"], m["w"])
+    got = decoder(big)(m["x"], m["ids"] + (E - 2), m["w"])
+    assert torch.equal(got, y)
+    close(y, reference(m))
+
+
+def test_ids_of_another_device_are_refused():
+    m = make(2, 64, 32, 4, 2)
+    d = decoder(m)
+    with pytest.raises(ValueError):
+        d(m["x"], m["ids"].cpu(), m["w"])
+    with pytest.raises(ValueError):
+        d(m["x"], m["ids"], m["w"].cpu())
