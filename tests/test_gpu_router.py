@@ -269,3 +269,53 @@ def test_refusals():
                      (lambda: block_ops.router_backward(z, torch.zeros(4, 2, device="cuda"), z[:, :2]), ValueError)):
         with pytest.raises(err):
             bad()
+
+
+@pytest.mark.parametrize("T,E,K", [(20000, 128, 8), (9000, 100, 6), (20000, 16, 2), (9801, 64, 16), (6000, 256, 8),
+                                   (6000, 512, 10), (5001, 1024, 16), (20000, 4, 1), (12345, 160, 8)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_many_rows(T, E, K, dt):
+    z = logits(T, E, dt, seed=E)
+    check_forward(z, K, "softmax", True)
+    check_forward(z, K, "softmax", False, bias=torch.randn(E, device="cuda"))
+    check_backward(z, K, "softmax", False, True)
+    check_backward(z, K, "sigmoid", True, True)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("E", [32, 64, 128, 256, 512, 1024])
+def test_logits_off_a_16_byte_boundary(dt, E):
+    z = logits(300, E, dt)
+    buf = torch.empty(z.numel() + 1, dtype=dt, device="cuda")
+    odd = buf[1:].view(z.shape).copy_(z)
+    K = 8
+    a = block_ops.router_forward(z, K, stats=True)
+    b = block_ops.router_forward(odd, K, stats=True)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    dw = torch.randn(300, K, device="cuda")
+    g = block_ops.router_backward(z, a[0], dw, normalize=False)
+    assert torch.equal(g, block_ops.router_backward(odd, a[0], dw, normalize=False))
+
+
+@pytest.mark.parametrize("E", [3, 64, 128, 200, 1024])
+def test_rows_of_equal_logits(E):
+    """Every key alike, in every lane: the experts come in order."""
+    K = min(E, 16)
+    for v in (0.0, -0.0, -math.inf):
+        ids, w, _, _ = block_ops.router_forward(torch.full((40, E), v, device="cuda"), K)
+        assert torch.equal(ids, torch.arange(K, device="cuda", dtype=torch.int32).expand(40, K))
+    z = torch.zeros(40, E, device="cuda", dtype=BF)
+    z[:, E // 2:] = 1.0  # two values only
+    assert torch.equal(block_ops.router_forward(z, K)[0].long(), choose(z.float(), K))
+
+
+def test_more_than_2_31_logits():
+    T, E = 2 ** 21 + 40, 1024
+    z = logits(64, E, BF).repeat(T // 64 + 1, 1)[:T].contiguous()
+    ids, w, ps, lse = block_ops.router_forward(z, 4, stats=True)
+    assert torch.equal(ids[-64:].long(), choose(z[-64:].float(), 4))
+    assert torch.allclose(lse[-64:].double(), torch.logsumexp(z[-64:].double(), 1), rtol=4e-6, atol=4e-6)
+    dz = block_ops.router_backward(z, ids, torch.ones_like(w), None, torch.ones_like(lse), normalize=False)
+    ref, mag = gradient(z[-64:], ids[-64:].long(), torch.ones(64, 4, device="cuda", dtype=torch.float64), None,
+                        torch.ones(64, device="cuda", dtype=torch.float64), "softmax", False, 1.0)
+    assert ((dz[-64:].double() - ref).abs() <= 1e-5 * mag + 2.0 ** -8 * ref.abs() + 1e-37).all()
