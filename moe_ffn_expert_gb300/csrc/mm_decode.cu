@@ -7,7 +7,8 @@
 //             and zeroed counters for the second kernel;
 //   k_experts one CTA per SM. Every CTA derives the same routing tables from the logits (or the
 //             caller's ids) in shared memory, then takes work units from one global counter:
-//     GEMM1   (chunk of up to 32 (e4m3: 16) rows of one expert, 64 gate + 64 up columns): w * silu(g) * u
+//     GEMM1   (chunk of up to 32 (e4m3: 16) rows of one expert, 64 (e4m3: 128) gate columns and the
+//             same of up): w * silu(g) * u
 //     GEMM2   (chunk, 128 output columns, part of I): fp32 partial rows
 //   and when they are out, sums the partial rows of (token, 128 columns) tasks in slot order, dealt
 //   evenly to the warps of the grid.
@@ -31,7 +32,7 @@
 // below that is rounded), so both halves of every row are columns of N and the accumulator's two
 // columns are added: twice the columns, no conversion of the weights, which outnumber the rows'
 // elements many times. The products of 128 x 128 blocks are scaled in 32 bits as they leave the
-// tensor memory. h is split the same way, with a scale per row and 64 columns.
+// tensor memory. h is split the same way, with a scale per row and 128 columns.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -58,15 +59,19 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <bool FP8>
 struct Cfg {
-  // Rows of one expert per unit. e4m3: 16, so that four accumulators fit per epilogue set; with two
-  // the sets' work at the end of a unit stopped the products.
+  // Rows of one expert per unit. e4m3: 16, so that eight accumulators fit per epilogue set; with
+  // two the sets' work at the end of a unit stopped the products.
   static constexpr int CHUNK = FP8 ? 16 : 32;
   static constexpr int KB = FP8 ? 128 : 64;                 // k per stage: 128 bytes of a row
   static constexpr int B_BYTES = 32 * 128;                  // rows (e4m3: hi and lo parts)
   static constexpr int STAGES = FP8 ? 9 : 8;
-  // accumulators in tensor memory, half of them per epilogue set: 32 columns for a bf16 unit; for
-  // a stage of e4m3 weights 32 (hi and lo parts of 16 rows), twice with the two scales of h
-  static constexpr int SLOT_COLS = 64;
+  // columns of h that a GEMM1 unit makes. bf16: 64, from stages of 64 gate + 64 up columns. e4m3:
+  // 128, from stages of gate columns and of up columns in turn, so that a stage is one box of whole
+  // 128-byte lines: two boxes of 64 bytes a row stream at 6.3 TB/s, one of 128 at 7.1.
+  static constexpr int H_COLS = FP8 ? 128 : 64;
+  // accumulators in tensor memory, half of them per epilogue set: of 32 columns for a bf16 unit
+  // (every second 32 unused); for a stage of e4m3 weights 32, hi and lo parts of 16 rows
+  static constexpr int SLOT_COLS = FP8 ? 32 : 64;
   static constexpr int RING = 512 / SLOT_COLS / 2;
   // Scales of the last stages. Entry n is rewritten for stage n + SCALES, whose loads start when
   // the products of stage n + SCALES - STAGES are done. Those had a free accumulator of the RING
@@ -78,15 +83,15 @@ struct Cfg {
 
 // What the e4m3 epilogue multiplies a stage's products with.
 struct Scales {
-  float h[2][Cfg<true>::CHUNK];  // GEMM2: the rows' scales of h for the stage's two blocks of 64
-  float w[4];          // the columns' block of weights: gate or down; up (first and second block)
+  float h[Cfg<true>::CHUNK];  // GEMM2: the rows' scales of the stage's 128 columns of h
+  float w[4];                 // of the blocks of weights of the first and of the last column
 };
 
 // int32 words at the start of the workspace (zeroed by k_logits)
 enum { W_STATUS = 0, W_NEXT = 1, W_READY1 = 64 };
 
 struct DecodeArgs {
-  CUtensorMap up, down, s_up, s_down;  // weights, boxes of 64 columns
+  CUtensorMap up, down, s_up, s_down;  // weights, boxes of 128 bytes x 64 (e4m3: 128) rows
   CUtensorMap x;                       // token rows (e4m3: hi rows, then lo rows), one per box
   CUtensorMap h_rows, s_h_rows;        // rows of h (the same), 8 per box
   const float *up_scale, *down_scale, *s_up_scale, *s_down_scale;
@@ -99,7 +104,7 @@ struct DecodeArgs {
   int *ready1, *ready2;
   void *h, *s_h;           // bf16 [S, I], [T, Is]; e4m3: [2, S, I], [2, T, Is]
   const float* x_scale;    // e4m3: [T]
-  float *h_scale, *s_h_scale;  // e4m3: [chunk][ceil(I / 64)][32]
+  float *h_scale, *s_h_scale;  // e4m3: [chunk][ceil(I / 128)][16]
   float *o, *s_o;          // [split][S, H], [split][T, H]
   int T, H, I, E, K, S, Is, score, normalize, route;
   float scale;
@@ -131,7 +136,7 @@ struct Building {
 // that runs once costs more to fetch than to execute).
 struct Unit {
   int kind;  // 0 GEMM1, 1 GEMM2, -1 no more units
-  int shared, row0, n, e, tile, kb0, kb1, split, ready;
+  int shared, row0, n, e, tile, kb0, kb1, split, ready;  // kb: stages (see stage_k)
 };
 
 // Work units in claiming order.
@@ -177,6 +182,10 @@ __device__ __forceinline__ void split_e4m3(float xs, uint8_t& hi, uint8_t& lo) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(hi, __NV_E4M3);
   const float back = __half2float(*reinterpret_cast<const __half*>(&h));
   lo = __nv_cvt_float_to_fp8((xs - back) * 16.f, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint8_t* b) {
+  return (uint32_t)b[0] | (uint32_t)b[1] << 8 | (uint32_t)b[2] << 16 | (uint32_t)b[3] << 24;
 }
 
 // The power of two that brings a largest magnitude into [128, 256) and its inverse. `amax` that is
@@ -235,11 +244,8 @@ __device__ void split_row(const LogitArgs& a, int t, float* red) {
     uint8_t h[8], l[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) split_e4m3(v[k] * s, h[k], l[k]);
-    auto word = [](const uint8_t* b) {
-      return (uint32_t)b[0] | (uint32_t)b[1] << 8 | (uint32_t)b[2] << 16 | (uint32_t)b[3] << 24;
-    };
-    *reinterpret_cast<uint2*>(hi + c) = make_uint2(word(h), word(h + 4));
-    *reinterpret_cast<uint2*>(lo + c) = make_uint2(word(l), word(l + 4));
+    *reinterpret_cast<uint2*>(hi + c) = make_uint2(word_of(h), word_of(h + 4));
+    *reinterpret_cast<uint2*>(lo + c) = make_uint2(word_of(l), word_of(l + 4));
   }
 }
 
@@ -471,6 +477,12 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int
   return true;
 }
 
+// The block of k that a unit's stage kb holds. e4m3 GEMM1: gate at even stages, up at odd ones.
+template <bool FP8>
+__device__ __forceinline__ int stage_k(int kind, int kb) {
+  return FP8 && kind == 0 ? kb >> 1 : kb;
+}
+
 template <bool FP8>
 __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
   constexpr int KB = Cfg<FP8>::KB;
@@ -479,10 +491,10 @@ __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
   constexpr int CHUNK = Cfg<FP8>::CHUNK;
   w.ncs = a.Is > 0 ? (a.T + CHUNK - 1) / CHUNK : 0;
   w.chunk = CHUNK;
-  w.nt1 = (a.I + 63) / 64;
-  w.nt1s = (a.Is + 63) / 64;
+  w.nt1 = (a.I + Cfg<FP8>::H_COLS - 1) / Cfg<FP8>::H_COLS;
+  w.nt1s = (a.Is + Cfg<FP8>::H_COLS - 1) / Cfg<FP8>::H_COLS;
   w.nt2 = (a.H + kCols - 1) / kCols;
-  w.kb_h = (a.H + KB - 1) / KB;
+  w.kb_h = (a.H + KB - 1) / KB * (FP8 ? 2 : 1);
   w.kb_i = (a.I + KB - 1) / KB;
   w.kb_is = (a.Is + KB - 1) / KB;
   // GEMM2 units too few for the SMs are cut along I
@@ -580,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   auto scales_full = [&](int s) { return bar0 + 8u * (X + 7 + s); };
   if (tid == 0) {
     if (FP8)
-      for (int s = 0; s < C::SCALES; ++s) mbar_init(scales_full(s), 1 + 3);
+      for (int s = 0; s < C::SCALES; ++s) mbar_init(scales_full(s), 1 + 2);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 2);  // the weights' and the rows' producers
       mbar_init(empty(s), 1);
@@ -652,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const CUtensorMap* map = un.kind == 0 ? (un.shared ? &a.s_up : &a.up)
                                             : (un.shared ? &a.s_down : &a.down);
       const int e = uniform(un.e), kb1 = uniform(un.kb1);
-      const int c0 = uniform(un.tile * (un.kind == 0 ? 64 : kCols));
-      const int c1 = uniform(un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + 64);
+      const int kind = uniform(un.kind), c0 = uniform(un.tile * (un.kind == 0 ? C::H_COLS : kCols));
+      const int c1 = uniform(un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + (FP8 ? 0 : 64));
       for (int kb = uniform(un.kb0); kb < kb1; ++kb, ++it) {
         if (!ring.wait()) {
           if (lane == 0) give_up();
@@ -664,8 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (elect_one()) {
           const uint32_t dst = base + ring.s * kTileBytes, bar = full(ring.s);
           mbar_arrive_expect_tx(bar, kTileBytes);
-          tma_load_3d(dst, map, bar, c0, kb * KB, e);
-          tma_load_3d(dst + kTileBytes / 2, map, bar, c1, kb * KB, e);
+          if (FP8) {
+            tma_load_3d(dst, map, bar, kb & 1 ? c1 : c0, stage_k<FP8>(kind, kb) * KB, e);
+          } else {
+            tma_load_3d(dst, map, bar, c0, kb * KB, e);
+            tma_load_3d(dst + kTileBytes / 2, map, bar, c1, kb * KB, e);
+          }
         }
         __syncwarp();
         ring.next();
@@ -719,21 +735,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       }
       const uint32_t bytes = (FP8 ? 2 : 1) * groups * (un.kind == 0 ? 512 : 1024);
       const uint32_t to = rows_at + (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
-      // e4m3: lanes 0..2 fetch the weights' scales of a stage, lane 0 the rows' scales of h. A
-      // unit's columns lie in one block of 128; its up columns, I further, may lie in two.
-      const float *sc = nullptr, *hs = nullptr;
-      int sc_stride = 0, nt64 = 0;
+      // e4m3: lanes 0 and 1 fetch the weights' scales of a stage (up columns may lie in two blocks
+      // of 128, the others lie in one), lane 0 the rows' scales of h
+      const float *sc0 = nullptr, *sc1 = nullptr, *hs = nullptr;
+      int sc_stride = 0;
       if (FP8) {
         const int I = un.shared ? a.Is : a.I, rows = un.kind == 0 ? a.H : I;
-        const int cols = un.kind == 0 ? 2 * I : a.H;
-        const int c = un.kind == 1 ? un.tile * kCols : un.tile * 64 + (lane == 0 ? 0 : I + (lane - 1) * 63);
+        const int cols = un.kind == 0 ? 2 * I : a.H, c = un.tile * kCols + (lane ? 127 : 0);
         sc_stride = (cols + 127) / 128;
-        sc = un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
-                          : (un.shared ? a.s_down_scale : a.down_scale);
-        sc += (int64_t)un.e * ((rows + 127) / 128) * sc_stride + min(c / 128, sc_stride - 1);
-        nt64 = (I + 63) / 64;
-        hs = un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * C::CHUNK
-                       : a.h_scale + (int64_t)un.ready * nt64 * C::CHUNK;
+        const float* const sc = (un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
+                                              : (un.shared ? a.s_down_scale : a.down_scale)) +
+                                (int64_t)un.e * ((rows + 127) / 128) * sc_stride;
+        sc0 = sc + min(c / 128, sc_stride - 1);
+        sc1 = un.kind == 0 ? sc + min((I + c) / 128, sc_stride - 1) : sc0;
+        const int nt = (I + 127) / 128;
+        hs = un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt * C::CHUNK
+                       : a.h_scale + (int64_t)un.ready * nt * C::CHUNK;
       }
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
         if (!ring.wait()) {
@@ -746,18 +763,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (FP8) {
           Scales& to_scales = scales[it % C::SCALES];
           const uint32_t bar = scales_full(it % C::SCALES);
-          if (lane < 3) copy4_arrive(smem_u32(&to_scales.w[lane]), sc + (int64_t)kb * sc_stride, bar);
+          if (lane < 2)
+            copy4_arrive(smem_u32(&to_scales.w[lane]),
+                         (kb & 1 ? sc1 : sc0) + (int64_t)stage_k<FP8>(un.kind, kb) * sc_stride, bar);
           if (lane == 0) {
-            const uint32_t n = un.kind == 0 ? 0u : min(2, nt64 - 2 * kb) * C::CHUNK * 4u;
+            const uint32_t n = un.kind == 0 ? 0u : C::CHUNK * 4u;
             mbar_arrive_expect_tx(bar, n);
-            if (n) bulk_load(smem_u32(&to_scales.h), hs + 2 * kb * C::CHUNK, n, bar);
+            if (n) bulk_load(smem_u32(&to_scales.h), hs + kb * C::CHUNK, n, bar);
           }
         }
         __syncwarp();
         if (loads) {
           const uint32_t dst = to + ring.s * C::B_BYTES;
           if (un.kind == 0)
-            tma_gather4(dst, map, full(ring.s), kb * KB, r[0], r[1], r[2], r[3]);
+            tma_gather4(dst, map, full(ring.s), stage_k<FP8>(0, kb) * KB, r[0], r[1], r[2], r[3]);
           else
             tma_load_2d(dst, map, full(ring.s), kb * KB, r[0]);
         }
@@ -776,8 +795,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     // same in all lanes: operands that are not pass through a move to a uniform register each, and
     // with descriptors built per product in a branch of one lane an issue took 165 cycles instead
     // of 41, longer than its weights take to arrive.
-    const uint64_t wdesc = FP8 ? sdesc_sw64(base, kTileBytes / 2, 512)
-                               : sdesc_sw128(base, kTileBytes / 2, 1024);
+    // (a stage of e4m3 weights is one block of 128 columns; of bf16, two of 64)
+    const uint64_t wdesc = sdesc_sw128(base, kTileBytes / 2, 1024);
     const uint64_t bdesc = sdesc_sw128(rows_at, 16, 1024);
     Walk<STAGES> ring(full(0), 0);
     Walk<RING> accs[2] = {Walk<RING>(acc_empty(0, 0), 1), Walk<RING>(acc_empty(1, 0), 1)};
@@ -786,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const Unit* const entry = take(qi);
       if (!__all_sync(0xFFFFFFFFu, entry != nullptr)) break;
       const int kind = uniform(entry->kind), blocks = uniform(entry->kb1 - entry->kb0);
-      const int rows = uniform(entry->n), kb0 = uniform(entry->kb0), shared = uniform(entry->shared);
+      const int rows = uniform(entry->n);
       taken(qi);
       if (kind < 0) break;
       // N: the chunk's rows (e4m3: their hi parts, then their lo parts)
@@ -819,19 +838,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         ring.ask_next();
         tc_fence_after();
-        // e4m3, GEMM2: 64 rows of weights per scale of h (the last block may have 64 rows only)
-        const bool halves = FP8 && kind == 1;
-        const bool upper = !halves || (kb0 + i) * 128 + 64 < (shared ? a.Is : a.I);
         if (elect_one()) {
           const uint64_t wd = wdesc + (uint32_t)ring.s * (kTileBytes / 16);
           const uint64_t bd = bdesc + (uint32_t)ring.s * (C::B_BYTES / 16);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {  // 16 (bf16) or 32 (e4m3) rows of weights
-            if (ks == 2 && !upper) break;
-            const uint64_t wk = wd + ks * (2048 / 16), bk = bd + ks * 2;
+            const uint64_t wk = wd + ks * ((FP8 ? 4096 : 2048) / 16), bk = bd + ks * 2;
             if constexpr (FP8)
-              umma_e4m3(halves && ks >= 2 ? d + C::SLOT_COLS / 2 : d, wk, bk, idesc,
-                        ks == 0 || (halves && ks == 2) ? 0u : 1u);
+              umma_e4m3(d, wk, bk, idesc, ks == 0 ? 0u : 1u);
             else
               umma_bf16(d, wk, bk, idesc, i == 0 && ks == 0 ? 0u : 1u);
           }
@@ -894,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       if (!FP8 && owner != set) continue;
       float* const ex = exchange + owner * C::CHUNK * kCols + col;
       const int n8 = (un.n + 7) & ~7;
-      const int I = un.shared ? a.Is : a.I, nt64 = (I + 63) / 64;
+      const int I = un.shared ? a.Is : a.I;
       float x_scale = 1.f;  // of row `lane`
       if (FP8 && un.kind == 0 && lane < un.n)
         x_scale = __ldcg(a.x_scale + (un.shared ? un.row0 + lane : tb.tok[un.row0 + lane]));
@@ -938,10 +952,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
         ++acc;
       } else {
-        // which of a stage's weight scales is this column's
-        const int up = I + un.tile * 64;  // first up column
-        const int which = un.kind == 1 || q < 2 ? 0 : (up + col - 64) / 128 == up / 128 ? 1 : 2;
-        const int first = un.kb0 + (set ^ owner);  // this set's blocks: first, first + 2, ...
+        // which of a stage's weight scales is this column's (the owner's stages are gate)
+        const int up = I + un.tile * kCols;  // first up column
+        const int which = un.kind == 0 && set != owner ? (up + col) / 128 - up / 128 : 0;
+        const int first = un.kb0 + (set ^ owner);  // this set's stages: first, first + 2, ...
         // G groups of 8 rows
         auto unit = [&](auto groups) {
           constexpr int G = decltype(groups)::value;
@@ -957,22 +971,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
             tc_fence_after();
             const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
-            const int halves = un.kind == 0 ? 1 : min(2, nt64 - 2 * kb);
-#pragma unroll 1
-            for (int half = 0; half < halves; ++half) {
-              uint32_t hi[8 * G], lo[8 * G];
+            uint32_t hi[8 * G], lo[8 * G];
 #pragma unroll
-              for (int j = 0; j < G; ++j) {
-                tmem_ld_32x8(d + half * (C::SLOT_COLS / 2) + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(hi + 8 * j));
-                tmem_ld_32x8(d + half * (C::SLOT_COLS / 2) + 8 * (G + j),
-                             *reinterpret_cast<uint32_t(*)[8]>(lo + 8 * j));
-              }
-              tmem_ld_wait();
+            for (int j = 0; j < G; ++j) {
+              tmem_ld_32x8(d + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(hi + 8 * j));
+              tmem_ld_32x8(d + 8 * (G + j), *reinterpret_cast<uint32_t(*)[8]>(lo + 8 * j));
+            }
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 8 * G; ++i) {
-                const float p = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-                v[i] = fmaf(un.kind == 0 ? ws : ws * sc.h[half][i], p, v[i]);
-              }
+            for (int i = 0; i < 8 * G; ++i) {
+              const float p = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+              v[i] = fmaf(un.kind == 0 ? ws : ws * sc.h[i], p, v[i]);
             }
             tc_fence_before();
             __syncwarp();
@@ -988,10 +997,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             return;
           }
           if (!wait(handed(owner), use & 1)) return;
+          if (un.kind == 1) {
 #pragma unroll
-          for (int i = 0; i < 8 * G; ++i) v[i] += ex[i * kCols];
+            for (int i = 0; i < 8 * G; ++i) v[i] += ex[i * kCols];
 #pragma unroll
-          for (int j = 0; j < G; ++j) emit(v + 8 * j, 8 * j);
+            for (int j = 0; j < G; ++j) emit(v + 8 * j, 8 * j);
+            return;
+          }
+#pragma unroll
+          for (int i = 0; i < 8 * G; ++i) {  // v: gate, handed over: up; h in the place of up
+            if (i >= un.n) continue;
+            const float xs = __shfl_sync(0xFFFFFFFFu, x_scale, i), g = v[i] * xs, u = ex[i * kCols] * xs;
+            const float w = un.shared ? 1.f : tb.w[un.row0 + i];
+            ex[i * kCols] = un.tile * kCols + col < I ? w * (g * sigmoidf_(g) * u) : 0.f;
+          }
         };
         if (n8 == 8) unit(std::integral_constant<int, 1>());
         else unit(std::integral_constant<int, 2>());
@@ -1007,46 +1026,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         continue;
       }
-      // GEMM1: columns 0..63 are gate, 64..127 up of the same 64; the set's warps meet in shared
-      // memory and take the rows in turn, two columns per lane
+      // GEMM1: the set's warps meet in shared memory and take the rows in turn
       __syncwarp();
       if (lane == 0) mbar_arrive(x_full(owner));
       if (!wait(x_full(owner), up_units & 1)) break;
       ++up_units;
-      const int c = un.tile * 64 + 2 * lane;
 #pragma unroll 1
       for (int i = q; i < un.n; i += 4) {
-        const float xs = FP8 ? __shfl_sync(0xFFFFFFFFu, x_scale, i) : 1.f;
         const int row = un.row0 + i;
-        const float w = un.shared ? 1.f : tb.w[row];
-        const float* x = exchange + (owner * C::CHUNK + i) * kCols + 2 * lane;
-        float2 g = *reinterpret_cast<const float2*>(x), l = *reinterpret_cast<const float2*>(x + 64);
-        if (FP8) {
-          g.x *= xs, g.y *= xs, l.x *= xs, l.y *= xs;
-        }
-        float h0 = w * (g.x * sigmoidf_(g.x) * l.x), h1 = w * (g.y * sigmoidf_(g.y) * l.y);
-        if constexpr (FP8) {
-          if (c >= I) h0 = h1 = 0.f;
-          float m = fmaxf(fabsf(h0), fabsf(h1));
-          if (h0 != h0 || h1 != h1) m = INFINITY;
+        const float* x = exchange + (owner * C::CHUNK + i) * kCols;
+        if constexpr (FP8) {  // 128 columns of h, 4 per lane
+          const int c = un.tile * kCols + 4 * lane;
+          const float4 h = *reinterpret_cast<const float4*>(x + 4 * lane);
+          float m = fmaxf(fmaxf(fabsf(h.x), fabsf(h.y)), fmaxf(fabsf(h.z), fabsf(h.w)));
+          if (h.x != h.x || h.y != h.y || h.z != h.z || h.w != h.w) m = INFINITY;
           float inv;
           const float s = split_scale(warp_max(m), &inv);
-          uint8_t hi0, lo0, hi1, lo1;
-          split_e4m3(h0 * s, hi0, lo0);
-          split_e4m3(h1 * s, hi1, lo1);
+          uint8_t hi[4], lo[4];
+          split_e4m3(h.x * s, hi[0], lo[0]);
+          split_e4m3(h.y * s, hi[1], lo[1]);
+          split_e4m3(h.z * s, hi[2], lo[2]);
+          split_e4m3(h.w * s, hi[3], lo[3]);
           uint8_t* dst = static_cast<uint8_t*>(un.shared ? a.s_h : a.h) + (int64_t)row * I + c;
           if (c < I) {
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)(hi0 | hi1 << 8);
-            *reinterpret_cast<uint16_t*>(dst + (int64_t)(un.shared ? a.T : a.S) * I) =
-                (uint16_t)(lo0 | lo1 << 8);
+            *reinterpret_cast<uint32_t*>(dst) = word_of(hi);
+            *reinterpret_cast<uint32_t*>(dst + (int64_t)(un.shared ? a.T : a.S) * I) = word_of(lo);
           }
+          const int nt = (I + 127) / 128;
           if (lane == 0)
-            (un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt64 * C::CHUNK
-                       : a.h_scale + (int64_t)un.ready * nt64 * C::CHUNK)[un.tile * C::CHUNK + i] = inv;
-        } else {
+            (un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt * C::CHUNK
+                       : a.h_scale + (int64_t)un.ready * nt * C::CHUNK)[un.tile * C::CHUNK + i] = inv;
+        } else {  // columns 0..63 are gate, 64..127 up of the same 64: two per lane
+          const int c = un.tile * 64 + 2 * lane;
+          const float w = un.shared ? 1.f : tb.w[row];
+          const float2 g = *reinterpret_cast<const float2*>(x + 2 * lane);
+          const float2 l = *reinterpret_cast<const float2*>(x + 64 + 2 * lane);
           if (c < I)
             *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(un.shared ? a.s_h : a.h) +
-                                         (int64_t)row * I + c) = pack_bf16(h0, h1);
+                                         (int64_t)row * I + c) =
+                pack_bf16(w * (g.x * sigmoidf_(g.x) * l.x), w * (g.y * sigmoidf_(g.y) * l.y));
         }
       }
       fence_proxy_async_global();
@@ -1199,8 +1217,8 @@ Layout layout(const mm_decode_desc& d) {
   l.off_x8 = take(fp8 ? (size_t)m.T * m.H * 2 : 0);
   l.off_xs = take(fp8 ? (size_t)m.T * 4 : 0);
   constexpr int chunk = Cfg<true>::CHUNK;
-  l.off_hs = take(fp8 ? S * ((m.I + 63) / 64) * chunk * 4 : 0);
-  l.off_shs = take(fp8 ? (size_t)(kMaxT / chunk) * ((d.shared_I + 63) / 64) * chunk * 4 : 0);
+  l.off_hs = take(fp8 ? S * ((m.I + 127) / 128) * chunk * 4 : 0);
+  l.off_shs = take(fp8 ? (size_t)(kMaxT / chunk) * ((d.shared_I + 127) / 128) * chunk * 4 : 0);
   l.off_h = take(S * m.I * 2);
   l.off_sh = take((size_t)m.T * d.shared_I * 2);
   l.off_o = take((size_t)kMaxSplit * S * m.H * 4);
@@ -1214,10 +1232,9 @@ bool weight_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, in
   const uint64_t es = fp8 ? 1 : 2;
   const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)n};
   const uint64_t strides[2] = {(uint64_t)cols * es, (uint64_t)cols * rows * es};
-  const uint32_t box[3] = {64, fp8 ? 128u : 64u, 1};
+  const uint32_t box[3] = {fp8 ? 128u : 64u, fp8 ? 128u : 64u, 1};
   return make_map(m, base, 3, dims, strides, box,
-                  fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                  fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                  fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
 // Rows of 128-byte boxes: bf16 or e4m3 [rows, cols].

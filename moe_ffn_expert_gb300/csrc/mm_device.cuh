@@ -480,12 +480,6 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
-// The same for a 64-byte-swizzled MN-major tile of 8-bit elements (64 MN-elements = 64 B per
-// k-row): lbo = stride between 64-wide MN blocks, sbo = 512 (8 k-rows). Layout type 4.
-__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (sdesc_sw128(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
-}
-
 // Instruction descriptor of tcgen05.mma kind::f16: bf16 A and B, fp32 D, dense.
 // Bits: D format [4,6) = 1 (f32); A format [7,10) = 1 (bf16); B format [10,13) = 1 (bf16);
 // A major [15] and B major [16] (0 = K-major, 1 = MN-major); N >> 3 in [17,23); M >> 4 in [24,29).
