@@ -73,18 +73,6 @@ struct Cfg {
   // (every second 32 unused); for a stage of e4m3 weights 32, hi and lo parts of 16 rows
   static constexpr int SLOT_COLS = FP8 ? 32 : 64;
   static constexpr int RING = 512 / SLOT_COLS / 2;
-  // Scales of the last stages. Entry n is rewritten for stage n + SCALES, whose loads start when
-  // the products of stage n + SCALES - STAGES are done. Those had a free accumulator of the RING
-  // that a set has, and the sets take stages in turn but for one repetition where a unit follows
-  // another, so what either set has not read yet began at most 2 RING + 3 stages before them.
-  static constexpr int SCALES = 32;
-  static_assert(!FP8 || SCALES >= STAGES + 2 * RING + 4, "scale entries");
-};
-
-// What the e4m3 epilogue multiplies a stage's products with.
-struct Scales {
-  float h[Cfg<true>::CHUNK];  // GEMM2: the rows' scales of the stage's 128 columns of h
-  float w[4];                 // of the blocks of weights of the first and of the last column
 };
 
 // int32 words at the start of the workspace (zeroed by k_logits)
@@ -92,8 +80,8 @@ enum { W_STATUS = 0, W_NEXT = 1, W_READY1 = 64 };
 
 struct DecodeArgs {
   CUtensorMap up, down, s_up, s_down;  // weights, boxes of 128 bytes x 64 (e4m3: 128) rows
-  CUtensorMap x;                       // token rows (e4m3: hi rows, then lo rows), one per box
-  CUtensorMap h_rows, s_h_rows;        // rows of h (the same), 8 per box
+  CUtensorMap x;                       // token rows (e4m3: hi and lo parts in turn), one per box
+  CUtensorMap h_rows, s_h_rows;        // rows of h (the same), 8 (16 parts) per box
   const float *up_scale, *down_scale, *s_up_scale, *s_down_scale;
   const float* logits;    // with a router
   const float* bias;
@@ -102,7 +90,7 @@ struct DecodeArgs {
   __nv_bfloat16* y;
   int* hdr;
   int *ready1, *ready2;
-  void *h, *s_h;           // bf16 [S, I], [T, Is]; e4m3: [2, S, I], [2, T, Is]
+  void *h, *s_h;           // bf16 [S, I], [T, Is]; e4m3: [S, 2, I], [T, 2, Is]
   const float* x_scale;    // e4m3: [T]
   float *h_scale, *s_h_scale;  // e4m3: [chunk][ceil(I / 128)][16]
   float *o, *s_o;          // [split][S, H], [split][T, H]
@@ -143,12 +131,6 @@ struct Unit {
 struct Work {
   int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, total, chunk;
 };
-
-// 4 bytes to shared memory, counted on `bar` when they are there.
-__device__ __forceinline__ void copy4_arrive(uint32_t dst, const float* src, uint32_t bar) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 // A value that all lanes share, in the form the compiler knows to be shared.
 __device__ __forceinline__ int uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
@@ -208,7 +190,7 @@ struct LogitArgs {
   int zero_n;
   int T, H, E;
   int logit_blocks;  // then, for e4m3 weights, one block per token
-  uint8_t* x8;       // [2, T, H]
+  uint8_t* x8;       // [T, 2, H]: hi and lo parts
   float* x_scale;    // [T]
 };
 
@@ -236,8 +218,8 @@ __device__ void split_row(const LogitArgs& a, int t, float* red) {
   float inv;
   const float s = split_scale(nan ? INFINITY : m, &inv);
   if (tid == 0) a.x_scale[t] = inv;
-  uint8_t* hi = a.x8 + (int64_t)t * a.H;
-  uint8_t* lo = a.x8 + (int64_t)(a.T + t) * a.H;
+  uint8_t* hi = a.x8 + (int64_t)t * 2 * a.H;
+  uint8_t* lo = hi + a.H;
   for (int c = tid * 8; c < a.H; c += 256 * 8) {
     float v[8];
     load_vec<8>(row + c, v);
@@ -566,8 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
   __shared__ Unit queue[kQueue];
-  __shared__ uint64_t bars[2 * STAGES + 3 * kQueue + 4 * RING + 6 + 1 + (FP8 ? C::SCALES : 0)];
-  __shared__ alignas(128) Scales scales[FP8 ? C::SCALES : 1];
+  __shared__ uint64_t bars[2 * STAGES + 3 * kQueue + 4 * RING + 6 + 1];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the stages' weights and rows (1024-byte aligned for the swizzle), then [row][128 columns] of
@@ -589,10 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   auto x_empty = [&](int s) { return bar0 + 8u * (X + 2 + s); };
   auto handed = [&](int s) { return bar0 + 8u * (X + 4 + s); };
   const uint32_t mma_done = bar0 + 8u * (X + 6);
-  auto scales_full = [&](int s) { return bar0 + 8u * (X + 7 + s); };
   if (tid == 0) {
-    if (FP8)
-      for (int s = 0; s < C::SCALES; ++s) mbar_init(scales_full(s), 1 + 2);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 2);  // the weights' and the rows' producers
       mbar_init(empty(s), 1);
@@ -708,18 +686,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       taken(qi);
       if (un.kind < 0) break;
       const CUtensorMap* map = un.kind == 0 ? &a.x : un.shared ? &a.s_h_rows : &a.h_rows;
-      // lanes of the first half load the rows (e4m3: their hi parts), those of the second the lo
-      // parts; x: 4 rows by number per lane, h: 8 consecutive rows
-      const int part = lane >> 4, j = lane & 15;
-      const int n8 = (un.n + 7) & ~7, groups = un.kind == 0 ? (un.n + 3) / 4 : n8 / 8;
-      const bool loads = (FP8 || part == 0) && j < groups;
-      const int lo = part * (un.kind == 0 || un.shared ? a.T : a.S);  // first row of the lo parts
+      // a lane loads 4 rows of x by number (e4m3: hi and lo parts of 2) or 8 consecutive rows of h
+      // (e4m3: 16, hi and lo in turn)
+      constexpr int PARTS = FP8 ? 2 : 1, X_ROWS = 4 / PARTS;
+      const int groups = un.kind == 0 ? (un.n + X_ROWS - 1) / X_ROWS : (un.n + 7) / 8;
       int r[4] = {0, 0, 0, 0};
       if (un.kind == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = un.row0 + min(4 * j + i, un.n - 1);
-          r[i] = lo + (un.shared ? row : tb.tok[row]);
+          const int row = un.row0 + min(lane * X_ROWS + i / PARTS, un.n - 1);
+          r[i] = (un.shared ? row : tb.tok[row]) * PARTS + i % PARTS;
         }
       } else {
         // the chunk's rows of h: one count per GEMM1 unit
@@ -731,27 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           break;
         }
         fence_proxy_async_global();
-        r[0] = lo + un.row0 + 8 * j;
+        r[0] = (un.row0 + 8 * lane) * PARTS;
       }
-      const uint32_t bytes = (FP8 ? 2 : 1) * groups * (un.kind == 0 ? 512 : 1024);
-      const uint32_t to = rows_at + (part * n8 + j * (un.kind == 0 ? 4 : 8)) * 128;
-      // e4m3: lanes 0 and 1 fetch the weights' scales of a stage (up columns may lie in two blocks
-      // of 128, the others lie in one), lane 0 the rows' scales of h
-      const float *sc0 = nullptr, *sc1 = nullptr, *hs = nullptr;
-      int sc_stride = 0;
-      if (FP8) {
-        const int I = un.shared ? a.Is : a.I, rows = un.kind == 0 ? a.H : I;
-        const int cols = un.kind == 0 ? 2 * I : a.H, c = un.tile * kCols + (lane ? 127 : 0);
-        sc_stride = (cols + 127) / 128;
-        const float* const sc = (un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
-                                              : (un.shared ? a.s_down_scale : a.down_scale)) +
-                                (int64_t)un.e * ((rows + 127) / 128) * sc_stride;
-        sc0 = sc + min(c / 128, sc_stride - 1);
-        sc1 = un.kind == 0 ? sc + min((I + c) / 128, sc_stride - 1) : sc0;
-        const int nt = (I + 127) / 128;
-        hs = un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt * C::CHUNK
-                       : a.h_scale + (int64_t)un.ready * nt * C::CHUNK;
-      }
+      const uint32_t lane_bytes = un.kind == 0 ? 512 : PARTS * 1024, bytes = groups * lane_bytes;
+      const uint32_t to = rows_at + lane * lane_bytes;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
         if (!ring.wait()) {
           if (lane == 0) give_up();
@@ -760,20 +719,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         ring.ask_next();
         if (lane == 0) mbar_arrive_expect_tx(full(ring.s), bytes);
-        if (FP8) {
-          Scales& to_scales = scales[it % C::SCALES];
-          const uint32_t bar = scales_full(it % C::SCALES);
-          if (lane < 2)
-            copy4_arrive(smem_u32(&to_scales.w[lane]),
-                         (kb & 1 ? sc1 : sc0) + (int64_t)stage_k<FP8>(un.kind, kb) * sc_stride, bar);
-          if (lane == 0) {
-            const uint32_t n = un.kind == 0 ? 0u : C::CHUNK * 4u;
-            mbar_arrive_expect_tx(bar, n);
-            if (n) bulk_load(smem_u32(&to_scales.h), hs + kb * C::CHUNK, n, bar);
-          }
-        }
         __syncwarp();
-        if (loads) {
+        if (lane < groups) {
           const uint32_t dst = to + ring.s * C::B_BYTES;
           if (un.kind == 0)
             tma_gather4(dst, map, full(ring.s), stage_k<FP8>(0, kb) * KB, r[0], r[1], r[2], r[3]);
@@ -786,9 +733,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     }
     for (int j = max(0, it - STAGES); j < it; ++j)
       mbar_wait(full(j % STAGES), (j / STAGES) & 1, kTimeoutNs);
-    if (FP8)
-      for (int j = max(0, it - C::SCALES); j < it; ++j)
-        mbar_wait(scales_full(j % C::SCALES), (j / C::SCALES) & 1, kTimeoutNs);
   } else if (warp == 2) {
     // ------------------------------------------------ issues the products
     // The warp stays in step, an elected lane issues, and what an issue takes is known to be the
@@ -808,8 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const int rows = uniform(entry->n);
       taken(qi);
       if (kind < 0) break;
-      // N: the chunk's rows (e4m3: their hi parts, then their lo parts)
-      const uint32_t n = FP8 ? 2 * ((rows + 7) & ~7) : (rows + 15) & ~15;
+      const uint32_t n = ((FP8 ? 2 * rows : rows) + 15) & ~15;  // the chunk's rows
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
       int set = qi & 1;
       uint32_t d = 0;
@@ -893,7 +836,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     int acc = 0;                    // accumulators taken from this set's ring
     int x_uses[2] = {0, 0};         // uses of each set's exchange buffer
     int up_units = 0;               // GEMM1 units that this set finished
-    int stages = 0;                 // e4m3: stages of the units before
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
       const Unit* const entry = take(qi);
@@ -952,9 +894,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
         ++acc;
       } else {
-        // which of a stage's weight scales is this column's (the owner's stages are gate)
-        const int up = I + un.tile * kCols;  // first up column
-        const int which = un.kind == 0 && set != owner ? (up + col) / 128 - up / 128 : 0;
+        // this column's scales of the weights (the owner's GEMM1 stages are gate), down its blocks,
+        // and of the rows of h: row `lane`, block by block. A stage's are fetched a stage ahead.
+        const int scale_cols = un.kind == 0 ? 2 * I : a.H, scale_rows = un.kind == 0 ? a.H : I;
+        const int stride = (scale_cols + 127) / 128, nt = (I + 127) / 128;
+        const int scale_col = un.tile * kCols + col + (un.kind == 0 && set != owner ? I : 0);
+        const float* const ws_at =
+            (un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
+                          : (un.shared ? a.s_down_scale : a.down_scale)) +
+            (int64_t)un.e * ((scale_rows + 127) / 128) * stride + min(scale_col / 128, stride - 1);
+        const float* const hs_at =
+            (un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt * C::CHUNK
+                       : a.h_scale + (int64_t)un.ready * nt * C::CHUNK) + lane % C::CHUNK;
         const int first = un.kb0 + (set ^ owner);  // this set's stages: first, first + 2, ...
         // G groups of 8 rows
         auto unit = [&](auto groups) {
@@ -962,27 +913,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           float v[8 * G];
 #pragma unroll
           for (int i = 0; i < 8 * G; ++i) v[i] = 0.f;
+          float ws = 0.f, hs = 1.f;
+          if (first < un.kb1) ws = __ldg(ws_at + (int64_t)stage_k<FP8>(un.kind, first) * stride);
 #pragma unroll 1
           for (int kb = first; kb < un.kb1; kb += 2, ++acc) {
-            const int at = stages + kb - un.kb0;
-            if (!wait(scales_full(at % C::SCALES), (at / C::SCALES) & 1)) return;
-            const Scales& sc = scales[at % C::SCALES];
-            const float ws = sc.w[which];
+            float next_ws = 0.f, next_hs = 1.f;
+            if (kb + 2 < un.kb1) next_ws = __ldg(ws_at + (int64_t)stage_k<FP8>(un.kind, kb + 2) * stride);
             if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
             tc_fence_after();
-            const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
-            uint32_t hi[8 * G], lo[8 * G];
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-              tmem_ld_32x8(d + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(hi + 8 * j));
-              tmem_ld_32x8(d + 8 * (G + j), *reinterpret_cast<uint32_t(*)[8]>(lo + 8 * j));
+            if (un.kind == 1) {  // (the products of h are there, so its scales are)
+              if (kb == first) hs = __ldcg(hs_at + kb * C::CHUNK);
+              if (kb + 2 < un.kb1) next_hs = __ldcg(hs_at + (kb + 2) * C::CHUNK);
             }
+            const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
+            uint32_t r[16 * G];  // hi and lo parts of the rows in turn
+#pragma unroll
+            for (int j = 0; j < 2 * G; ++j)
+              tmem_ld_32x8(d + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(r + 8 * j));
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 8 * G; ++i) {
-              const float p = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-              v[i] = fmaf(un.kind == 0 ? ws : ws * sc.h[i], p, v[i]);
+              const float p = fmaf(__uint_as_float(r[2 * i + 1]), 0.0625f, __uint_as_float(r[2 * i]));
+              v[i] = fmaf(un.kind == 0 ? ws : ws * __shfl_sync(0xFFFFFFFFu, hs, i), p, v[i]);
             }
+            ws = next_ws;
+            hs = next_hs;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
@@ -1014,7 +969,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         };
         if (n8 == 8) unit(std::integral_constant<int, 1>());
         else unit(std::integral_constant<int, 2>());
-        stages += un.kb1 - un.kb0;
         if (!ok) break;
         if (set != owner) continue;
       }
@@ -1047,10 +1001,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           split_e4m3(h.y * s, hi[1], lo[1]);
           split_e4m3(h.z * s, hi[2], lo[2]);
           split_e4m3(h.w * s, hi[3], lo[3]);
-          uint8_t* dst = static_cast<uint8_t*>(un.shared ? a.s_h : a.h) + (int64_t)row * I + c;
+          uint8_t* dst = static_cast<uint8_t*>(un.shared ? a.s_h : a.h) + (int64_t)row * 2 * I + c;
           if (c < I) {
             *reinterpret_cast<uint32_t*>(dst) = word_of(hi);
-            *reinterpret_cast<uint32_t*>(dst + (int64_t)(un.shared ? a.T : a.S) * I) = word_of(lo);
+            *reinterpret_cast<uint32_t*>(dst + I) = word_of(lo);
           }
           const int nt = (I + 127) / 128;
           if (lane == 0)
@@ -1332,11 +1286,11 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   bool maps = weight_map(&a.up, w->up, 2 * m.I, m.H, m.E, fp8) &&
               weight_map(&a.down, w->down, m.H, m.I, m.E, fp8) &&
               row_map(&a.x, x_rows, m.H, parts * m.T, fp8, 1) &&
-              row_map(&a.h_rows, ws + l.off_h, m.I, parts * m.T * m.K, fp8, 8);
+              row_map(&a.h_rows, ws + l.off_h, m.I, parts * m.T * m.K, fp8, 8 * parts);
   if (shared)
     maps = maps && weight_map(&a.s_up, w->shared_up, 2 * d->shared_I, m.H, 1, fp8) &&
            weight_map(&a.s_down, w->shared_down, m.H, d->shared_I, 1, fp8) &&
-           row_map(&a.s_h_rows, ws + l.off_sh, d->shared_I, parts * m.T, fp8, 8);
+           row_map(&a.s_h_rows, ws + l.off_sh, d->shared_I, parts * m.T, fp8, 8 * parts);
   if (!maps) return cuda_fail(cudaErrorInvalidValue, "decode tensor maps");
   a.up_scale = w->up_scale;
   a.down_scale = w->down_scale;
