@@ -644,7 +644,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const int e = uniform(un.e), kb1 = uniform(un.kb1);
       const int kind = uniform(un.kind), c0 = uniform(un.tile * (un.kind == 0 ? C::H_COLS : kCols));
       const int c1 = uniform(un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + (FP8 ? 0 : 64));
-      for (int kb = uniform(un.kb0); kb < kb1; ++kb, ++it) {
+      // The next unit is claimed with two stages of this one left, so that the claim's latency passes
+      // behind them. (Not earlier: a CTA stuck in front of a chunk that is not ready should not sit on
+      // units that others could take.)
+      const int kb0 = uniform(un.kb0), claim_at = max(kb0, kb1 - 2);
+      int next = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        if (kb == claim_at && lane == 0) next = atomicAdd(a.hdr + W_NEXT, 1);
         if (!ring.wait()) {
           if (lane == 0) give_up();
           ok = false;
@@ -664,11 +670,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         __syncwarp();
         ring.next();
       }
-      // The next unit is claimed only when this one's loads are issued: the ring still holds work
-      // for longer than the claim takes, and a CTA stuck in front of a chunk that is not ready
-      // does not sit on units that others could take.
-      int next = 0;
-      if (lane == 0) next = atomicAdd(a.hdr + W_NEXT, 1);
       u = gridDim.x + __shfl_sync(0xFFFFFFFFu, next, 0);
     }
     // no CTA leaves with a copy into its shared memory in flight
