@@ -51,7 +51,7 @@ constexpr int kMaxT = 64, kMaxSlots = 1024, kMaxE = 1024;
 constexpr int kMaxRouted = 12;    // tokens whose selection every CTA repeats, one per warp
 constexpr int kCols = 128;        // weight columns per unit
 constexpr int kMaxSplit = 4;      // parts of I per GEMM2 column tile
-constexpr int kTileBytes = 16384; // one stage of weights: 64 x 128 bf16 or 128 x 128 e4m3
+constexpr int kTileBytes = 16384; // one block of weights: 64 x 128 bf16 or 128 x 128 e4m3
 constexpr int kThreads = 384;     // weight loads, row loads, MMA, tensor memory; 2 x 4 epilogue
 constexpr int kFirstEpilogue = 4;
 constexpr int kQueue = 8;         // units claimed ahead
@@ -59,19 +59,26 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <bool FP8>
 struct Cfg {
-  // Rows of one expert per unit. e4m3: 16, so that eight accumulators fit per epilogue set; with
+  // Rows of one expert per unit. e4m3: 16, so that four accumulators fit per epilogue set; with
   // two the sets' work at the end of a unit stopped the products.
   static constexpr int CHUNK = FP8 ? 16 : 32;
-  static constexpr int KB = FP8 ? 128 : 64;                 // k per stage: 128 bytes of a row
-  static constexpr int B_BYTES = 32 * 128;                  // rows (e4m3: hi and lo parts)
-  static constexpr int STAGES = FP8 ? 9 : 8;
+  static constexpr int KB = FP8 ? 128 : 64;   // k of a block: 128 bytes of a row
+  // Blocks of weights per stage. e4m3: two, which a warp waits for, issues and commits together:
+  // with one the products' warp took some 540 cycles a block, and a block arrives every 690. GEMM1:
+  // gate and up columns of the same k; GEMM2: the next two k.
+  static constexpr int BLOCKS = FP8 ? 2 : 1;
+  static constexpr int KB2 = KB * BLOCKS;             // k per stage of GEMM2
+  static constexpr int A_BYTES = BLOCKS * kTileBytes;
+  static constexpr int B_BYTES = BLOCKS * 32 * 128;   // rows (e4m3: hi and lo parts)
+  static constexpr int STAGES = FP8 ? 4 : 8;
   // columns of h that a GEMM1 unit makes. bf16: 64, from stages of 64 gate + 64 up columns. e4m3:
-  // 128, from stages of gate columns and of up columns in turn, so that a stage is one box of whole
-  // 128-byte lines: two boxes of 64 bytes a row stream at 6.3 TB/s, one of 128 at 7.1.
+  // 128, so that a block is one box of whole 128-byte lines: two boxes of 64 bytes a row stream at
+  // 6.3 TB/s, one of 128 at 7.1.
   static constexpr int H_COLS = FP8 ? 128 : 64;
-  // accumulators in tensor memory, half of them per epilogue set: of 32 columns for a bf16 unit
-  // (every second 32 unused); for a stage of e4m3 weights 32, hi and lo parts of 16 rows
-  static constexpr int SLOT_COLS = FP8 ? 32 : 64;
+  // Accumulators in tensor memory, a ring per epilogue set. bf16: an accumulator per unit (of 32
+  // columns; the other 32 unused). e4m3: one per stage, 32 columns (hi and lo parts of 16 rows) per
+  // block.
+  static constexpr int SLOT_COLS = 64;
   static constexpr int RING = 512 / SLOT_COLS / 2;
 };
 
@@ -124,7 +131,7 @@ struct Building {
 // that runs once costs more to fetch than to execute).
 struct Unit {
   int kind;  // 0 GEMM1, 1 GEMM2, -1 no more units
-  int shared, row0, n, e, tile, kb0, kb1, split, ready;  // kb: stages (see stage_k)
+  int shared, row0, n, e, tile, kb0, kb1, split, ready;  // kb: stages
 };
 
 // Work units in claiming order.
@@ -459,15 +466,9 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int
   return true;
 }
 
-// The block of k that a unit's stage kb holds. e4m3 GEMM1: gate at even stages, up at odd ones.
-template <bool FP8>
-__device__ __forceinline__ int stage_k(int kind, int kb) {
-  return FP8 && kind == 0 ? kb >> 1 : kb;
-}
-
 template <bool FP8>
 __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
-  constexpr int KB = Cfg<FP8>::KB;
+  constexpr int KB = Cfg<FP8>::KB, KB2 = Cfg<FP8>::KB2;
   Work w;
   w.nc = chunks;
   constexpr int CHUNK = Cfg<FP8>::CHUNK;
@@ -476,9 +477,9 @@ __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
   w.nt1 = (a.I + Cfg<FP8>::H_COLS - 1) / Cfg<FP8>::H_COLS;
   w.nt1s = (a.Is + Cfg<FP8>::H_COLS - 1) / Cfg<FP8>::H_COLS;
   w.nt2 = (a.H + kCols - 1) / kCols;
-  w.kb_h = (a.H + KB - 1) / KB * (FP8 ? 2 : 1);
-  w.kb_i = (a.I + KB - 1) / KB;
-  w.kb_is = (a.Is + KB - 1) / KB;
+  w.kb_h = (a.H + KB - 1) / KB;
+  w.kb_i = (a.I + KB2 - 1) / KB2;
+  w.kb_is = (a.Is + KB2 - 1) / KB2;
   // GEMM2 units too few for the SMs are cut along I
   const int units = (w.nc + w.ncs) * w.nt2;
   const int want = max(1, min(kMaxSplit, (int)gridDim.x / max(1, units)));
@@ -548,15 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tables tb;
   __shared__ Unit queue[kQueue];
-  __shared__ uint64_t bars[2 * STAGES + 3 * kQueue + 4 * RING + 6 + 1];
+  __shared__ uint64_t bars[2 * STAGES + 3 * kQueue + 4 * RING + 4 + 1];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the stages' weights and rows (1024-byte aligned for the swizzle), then [row][128 columns] of
   // a unit for each epilogue set
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const aligned = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t rows_at = base + STAGES * kTileBytes;
-  float* const exchange = reinterpret_cast<float*>(aligned + STAGES * (kTileBytes + C::B_BYTES));
+  const uint32_t rows_at = base + STAGES * C::A_BYTES;
+  float* const exchange = reinterpret_cast<float*>(aligned + STAGES * (C::A_BYTES + C::B_BYTES));
   const uint32_t bar0 = smem_u32(bars);
   constexpr int Q = 2 * STAGES, ACC = Q + 3 * kQueue, X = ACC + 4 * RING;
   auto full = [&](int s) { return bar0 + 8u * s; };
@@ -568,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   auto acc_empty = [&](int set, int s) { return bar0 + 8u * (ACC + (2 + set) * RING + s); };
   auto x_full = [&](int s) { return bar0 + 8u * (X + s); };
   auto x_empty = [&](int s) { return bar0 + 8u * (X + 2 + s); };
-  auto handed = [&](int s) { return bar0 + 8u * (X + 4 + s); };
-  const uint32_t mma_done = bar0 + 8u * (X + 6);
+  const uint32_t mma_done = bar0 + 8u * (X + 4);
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full(s), 2);  // the weights' and the rows' producers
@@ -587,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     for (int s = 0; s < 2; ++s) {
       mbar_init(x_full(s), 4);
       mbar_init(x_empty(s), 4);
-      mbar_init(handed(s), 4);
     }
     mbar_init(mma_done, 1);
     mbar_fence_init();
@@ -642,8 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const CUtensorMap* map = un.kind == 0 ? (un.shared ? &a.s_up : &a.up)
                                             : (un.shared ? &a.s_down : &a.down);
       const int e = uniform(un.e), kb1 = uniform(un.kb1);
-      const int kind = uniform(un.kind), c0 = uniform(un.tile * (un.kind == 0 ? C::H_COLS : kCols));
+      const int c0 = uniform(un.tile * (un.kind == 0 ? C::H_COLS : kCols));
       const int c1 = uniform(un.kind == 0 ? (un.shared ? a.Is : a.I) + c0 : c0 + (FP8 ? 0 : 64));
+      // k of the first and from there to the second half (bf16: columns) of a stage
+      const int k_step = uniform(un.kind == 0 ? KB : C::KB2), k_half = uniform(FP8 && un.kind == 1 ? KB : 0);
       // The next unit is claimed with two stages of this one left, so that the claim's latency passes
       // behind them. (Not earlier: a CTA stuck in front of a chunk that is not ready should not sit on
       // units that others could take.)
@@ -658,14 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         ring.ask_next();
         if (elect_one()) {
-          const uint32_t dst = base + ring.s * kTileBytes, bar = full(ring.s);
-          mbar_arrive_expect_tx(bar, kTileBytes);
-          if (FP8) {
-            tma_load_3d(dst, map, bar, kb & 1 ? c1 : c0, stage_k<FP8>(kind, kb) * KB, e);
-          } else {
-            tma_load_3d(dst, map, bar, c0, kb * KB, e);
-            tma_load_3d(dst + kTileBytes / 2, map, bar, c1, kb * KB, e);
-          }
+          const uint32_t dst = base + ring.s * C::A_BYTES, bar = full(ring.s);
+          mbar_arrive_expect_tx(bar, C::A_BYTES);
+          tma_load_3d(dst, map, bar, c0, kb * k_step, e);
+          tma_load_3d(dst + C::A_BYTES / 2, map, bar, c1, kb * k_step + k_half, e);
         }
         __syncwarp();
         ring.next();
@@ -710,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         fence_proxy_async_global();
         r[0] = (un.row0 + 8 * lane) * PARTS;
       }
-      const uint32_t lane_bytes = un.kind == 0 ? 512 : PARTS * 1024, bytes = groups * lane_bytes;
+      const uint32_t lane_bytes = un.kind == 0 ? 512 : PARTS * 1024;
+      const uint32_t bytes = groups * lane_bytes * (un.kind == 0 ? 1 : C::BLOCKS);
       const uint32_t to = rows_at + lane * lane_bytes;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
         if (!ring.wait()) {
@@ -724,9 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane < groups) {
           const uint32_t dst = to + ring.s * C::B_BYTES;
           if (un.kind == 0)
-            tma_gather4(dst, map, full(ring.s), stage_k<FP8>(0, kb) * KB, r[0], r[1], r[2], r[3]);
+            tma_gather4(dst, map, full(ring.s), kb * KB, r[0], r[1], r[2], r[3]);
           else
-            tma_load_2d(dst, map, full(ring.s), kb * KB, r[0]);
+#pragma unroll
+            for (int p = 0; p < C::BLOCKS; ++p)
+              tma_load_2d(dst + p * (C::B_BYTES / C::BLOCKS), map, full(ring.s), kb * C::KB2 + p * KB, r[0]);
         }
         __syncwarp();
         ring.next();
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     // same in all lanes: operands that are not pass through a move to a uniform register each, and
     // with descriptors built per product in a branch of one lane an issue took 165 cycles instead
     // of 41, longer than its weights take to arrive.
-    // (a stage of e4m3 weights is one block of 128 columns; of bf16, two of 64)
+    // (a block of e4m3 weights is 128 columns of 128 bytes a row; of bf16, twice 64)
     const uint64_t wdesc = sdesc_sw128(base, kTileBytes / 2, 1024);
     const uint64_t bdesc = sdesc_sw128(rows_at, 16, 1024);
     Walk<STAGES> ring(full(0), 0);
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       if (kind < 0) break;
       const uint32_t n = ((FP8 ? 2 * rows : rows) + 15) & ~15;  // the chunk's rows
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
-      int set = qi & 1;
+      const int set = qi & 1;
       uint32_t d = 0;
       auto next_slot = [&] {  // the next accumulator of `set`, free
         Walk<RING>& w = set ? accs[1] : accs[0];
@@ -783,13 +783,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         ring.ask_next();
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t wd = wdesc + (uint32_t)ring.s * (kTileBytes / 16);
+          const uint64_t wd = wdesc + (uint32_t)ring.s * (C::A_BYTES / 16);
           const uint64_t bd = bdesc + (uint32_t)ring.s * (C::B_BYTES / 16);
+          const uint32_t b_half = kind == 0 ? 0u : C::B_BYTES / 2 / 16;  // e4m3 GEMM1: the same rows
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {  // 16 (bf16) or 32 (e4m3) rows of weights
-            const uint64_t wk = wd + ks * ((FP8 ? 4096 : 2048) / 16), bk = bd + ks * 2;
+          for (int i4 = 0; i4 < 4 * C::BLOCKS; ++i4) {  // 16 (bf16) or 32 (e4m3) rows of weights
+            const int p = i4 / 4, ks = i4 % 4;
+            const uint64_t wk = wd + i4 * ((FP8 ? 4096 : 2048) / 16), bk = bd + ks * 2 + p * b_half;
             if constexpr (FP8)
-              umma_e4m3(d, wk, bk, idesc, ks == 0 ? 0u : 1u);
+              umma_e4m3(d + p * (C::SLOT_COLS / 2), wk, bk, idesc, ks == 0 ? 0u : 1u);
             else
               umma_bf16(d, wk, bk, idesc, i == 0 && ks == 0 ? 0u : 1u);
           }
@@ -798,10 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         __syncwarp();
         ring.next();
-        if (FP8) {
-          slot_done();
-          set ^= 1;
-        }
+        if (FP8) slot_done();
       }
       if (!FP8 && ok) slot_done();
     }
@@ -829,13 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     }
   } else if (warp >= kFirstEpilogue) {
     // ------------------------------------------------ accumulators to h, partial rows and y
-    // Two sets of four warps. bf16: they take the units in turn. e4m3: both work on every unit,
-    // each on every second accumulator; the unit's owner (in turn) adds the other's sums.
+    // Two sets of four warps take the units in turn.
     const int set = (warp - kFirstEpilogue) >> 2, q = warp & 3;  // q: the warp's quarter of the lanes
     const int col = q * 32 + lane;  // of the unit's 128
     const uint32_t tmem_q = tmem + set * RING * C::SLOT_COLS + ((uint32_t)(q * 32) << 16);
-    int acc = 0;                    // accumulators taken from this set's ring
-    int x_uses[2] = {0, 0};         // uses of each set's exchange buffer
+    int acc = 0;                    // accumulators taken from the ring
     int up_units = 0;               // GEMM1 units that this set finished
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
@@ -847,9 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const Unit un = *entry;
       taken(qi);
       if (un.kind < 0) break;
-      const int owner = qi & 1;
-      if (!FP8 && owner != set) continue;
-      float* const ex = exchange + owner * C::CHUNK * kCols + col;
+      if ((qi & 1) != set) continue;
+      float* const ex = exchange + set * C::CHUNK * kCols + col;
       const int n8 = (un.n + 7) & ~7;
       const int I = un.shared ? a.Is : a.I;
       float x_scale = 1.f;  // of row `lane`
@@ -876,10 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
       };
       if constexpr (!FP8) {
-        if (un.kind == 0) {
-          const int use = owner ? x_uses[1]++ : x_uses[0]++;
-          if (!wait(x_empty(owner), (use & 1) ^ 1)) break;
-        }
+        if (un.kind == 0 && !wait(x_empty(set), (up_units & 1) ^ 1)) break;
         if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) break;
         tc_fence_after();
         const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
@@ -895,75 +888,95 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
         ++acc;
       } else {
-        // this column's scales of the weights (the owner's GEMM1 stages are gate), down its blocks,
-        // and of the rows of h: row `lane`, block by block. A stage's are fetched a stage ahead.
-        const int scale_cols = un.kind == 0 ? 2 * I : a.H, scale_rows = un.kind == 0 ? a.H : I;
-        const int stride = (scale_cols + 127) / 128, nt = (I + 127) / 128;
-        const int scale_col = un.tile * kCols + col + (un.kind == 0 && set != owner ? I : 0);
+        // The scales of a stage's two blocks of weights (GEMM1: gate and up, whose columns may lie in
+        // two blocks of scales; GEMM2: the next two k, a last one past the end with none and weights of
+        // zero): lane l holds those of stage kb0 + l, fetched 32 stages at a time, as HBM under load
+        // answers later than a few stages.
+        const bool up = un.kind == 0;
+        const int stride = up ? (2 * I + 127) / 128 : work.nt2, nt = (I + 127) / 128;
+        const int up_col = I + un.tile * kCols + q * 32;  // the warp's first up column
+        const int block0 = min(up_col / 128, stride - 1), block1 = min((up_col + 31) / 128, stride - 1);
+        const bool second = up && (up_col + lane) / 128 != up_col / 128;
         const float* const ws_at =
-            (un.kind == 0 ? (un.shared ? a.s_up_scale : a.up_scale)
-                          : (un.shared ? a.s_down_scale : a.down_scale)) +
-            (int64_t)un.e * ((scale_rows + 127) / 128) * stride + min(scale_col / 128, stride - 1);
+            (up ? (un.shared ? a.s_up_scale : a.up_scale)
+                : (un.shared ? a.s_down_scale : a.down_scale)) +
+            (int64_t)un.e * (up ? (a.H + 127) / 128 : nt) * stride;
+        auto fetch = [&](int kb) {
+          float3 w = make_float3(0.f, 0.f, 0.f);
+          if (kb >= un.kb1) return w;
+          const float* const at = ws_at + (int64_t)(up ? kb : 2 * kb) * stride;
+          w.x = __ldg(at + un.tile);
+          if (up)
+            w.y = __ldg(at + block0), w.z = __ldg(at + block1);
+          else if (2 * kb + 1 < nt)
+            w.y = __ldg(at + stride + un.tile);
+          return w;
+        };
+        // and those of the rows of h: lane l holds row l % 16 of block l / 16
         const float* const hs_at =
             (un.shared ? a.s_h_scale + (int64_t)(un.ready - work.nc) * nt * C::CHUNK
                        : a.h_scale + (int64_t)un.ready * nt * C::CHUNK) + lane % C::CHUNK;
-        const int first = un.kb0 + (set ^ owner);  // this set's stages: first, first + 2, ...
+        auto row_scale = [&](int kb) {
+          return __ldcg(hs_at + min(2 * kb + lane / C::CHUNK, nt - 1) * C::CHUNK);
+        };
         // G groups of 8 rows
         auto unit = [&](auto groups) {
           constexpr int G = decltype(groups)::value;
-          float v[8 * G];
+          float v[2][8 * G];
 #pragma unroll
-          for (int i = 0; i < 8 * G; ++i) v[i] = 0.f;
-          float ws = 0.f, hs = 1.f;
-          if (first < un.kb1) ws = __ldg(ws_at + (int64_t)stage_k<FP8>(un.kind, first) * stride);
+          for (int i = 0; i < 8 * G; ++i) v[0][i] = v[1][i] = 0.f;
+          float3 held = fetch(un.kb0 + lane), later = fetch(un.kb0 + lane + 32);
+          float hs = 1.f;
+          int at = 0;  // the lane that holds the stage's
 #pragma unroll 1
-          for (int kb = first; kb < un.kb1; kb += 2, ++acc) {
-            float next_ws = 0.f, next_hs = 1.f;
-            if (kb + 2 < un.kb1) next_ws = __ldg(ws_at + (int64_t)stage_k<FP8>(un.kind, kb + 2) * stride);
+          for (int kb = un.kb0; kb < un.kb1; ++kb, ++acc, ++at) {
+            if (at == 32) {
+              at = 0;
+              held = later;
+              later = fetch(kb + lane + 32);
+            }
+            float ws[2] = {__shfl_sync(0xFFFFFFFFu, held.x, at), __shfl_sync(0xFFFFFFFFu, held.y, at)};
+            const float w2 = __shfl_sync(0xFFFFFFFFu, held.z, at);
+            if (second) ws[1] = w2;
+            float next_hs = 1.f;
             if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
             tc_fence_after();
-            if (un.kind == 1) {  // (the products of h are there, so its scales are)
-              if (kb == first) hs = __ldcg(hs_at + kb * C::CHUNK);
-              if (kb + 2 < un.kb1) next_hs = __ldcg(hs_at + (kb + 2) * C::CHUNK);
+            if (!up) {  // (the products of h are there, so its scales are)
+              if (kb == un.kb0) hs = row_scale(kb);
+              if (kb + 1 < un.kb1) next_hs = row_scale(kb + 1);
             }
             const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
-            uint32_t r[16 * G];  // hi and lo parts of the rows in turn
 #pragma unroll
-            for (int j = 0; j < 2 * G; ++j)
-              tmem_ld_32x8(d + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(r + 8 * j));
-            tmem_ld_wait();
+            for (int half = 0; half < 2; ++half) {
+              uint32_t r[16 * G];  // hi and lo parts of the rows in turn
 #pragma unroll
-            for (int i = 0; i < 8 * G; ++i) {
-              const float p = fmaf(__uint_as_float(r[2 * i + 1]), 0.0625f, __uint_as_float(r[2 * i]));
-              v[i] = fmaf(un.kind == 0 ? ws : ws * __shfl_sync(0xFFFFFFFFu, hs, i), p, v[i]);
+              for (int j = 0; j < 2 * G; ++j)
+                tmem_ld_32x8(d + half * (C::SLOT_COLS / 2) + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(r + 8 * j));
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8 * G; ++i) {
+                const float p = fmaf(__uint_as_float(r[2 * i + 1]), 0.0625f, __uint_as_float(r[2 * i]));
+                const float rs = up ? 1.f : __shfl_sync(0xFFFFFFFFu, hs, half * C::CHUNK + i);
+                v[half][i] = fmaf(ws[half] * rs, p, v[half][i]);
+              }
             }
-            ws = next_ws;
             hs = next_hs;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
           }
-          const int use = owner ? x_uses[1]++ : x_uses[0]++;
-          if (set != owner) {  // hand the sums over
-            if (!wait(x_empty(owner), (use & 1) ^ 1)) return;
+          if (!up) {
 #pragma unroll
-            for (int i = 0; i < 8 * G; ++i) ex[i * kCols] = v[i];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(handed(owner));
+            for (int i = 0; i < 8 * G; ++i) v[0][i] += v[1][i];
+#pragma unroll
+            for (int j = 0; j < G; ++j) emit(v[0] + 8 * j, 8 * j);
             return;
           }
-          if (!wait(handed(owner), use & 1)) return;
-          if (un.kind == 1) {
+          if (!wait(x_empty(set), (up_units & 1) ^ 1)) return;
 #pragma unroll
-            for (int i = 0; i < 8 * G; ++i) v[i] += ex[i * kCols];
-#pragma unroll
-            for (int j = 0; j < G; ++j) emit(v + 8 * j, 8 * j);
-            return;
-          }
-#pragma unroll
-          for (int i = 0; i < 8 * G; ++i) {  // v: gate, handed over: up; h in the place of up
+          for (int i = 0; i < 8 * G; ++i) {
             if (i >= un.n) continue;
-            const float xs = __shfl_sync(0xFFFFFFFFu, x_scale, i), g = v[i] * xs, u = ex[i * kCols] * xs;
+            const float xs = __shfl_sync(0xFFFFFFFFu, x_scale, i), g = v[0][i] * xs, u = v[1][i] * xs;
             const float w = un.shared ? 1.f : tb.w[un.row0 + i];
             ex[i * kCols] = un.tile * kCols + col < I ? w * (g * sigmoidf_(g) * u) : 0.f;
           }
@@ -971,25 +984,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (n8 == 8) unit(std::integral_constant<int, 1>());
         else unit(std::integral_constant<int, 2>());
         if (!ok) break;
-        if (set != owner) continue;
       }
       if (un.kind == 1) {
         __syncwarp();
-        if (lane == 0) {
-          if (FP8) mbar_arrive(x_empty(owner));
-          mbar_arrive(stored(qi % kQueue));
-        }
+        if (lane == 0) mbar_arrive(stored(qi % kQueue));
         continue;
       }
       // GEMM1: the set's warps meet in shared memory and take the rows in turn
       __syncwarp();
-      if (lane == 0) mbar_arrive(x_full(owner));
-      if (!wait(x_full(owner), up_units & 1)) break;
+      if (lane == 0) mbar_arrive(x_full(set));
+      if (!wait(x_full(set), up_units & 1)) break;
       ++up_units;
 #pragma unroll 1
       for (int i = q; i < un.n; i += 4) {
         const int row = un.row0 + i;
-        const float* x = exchange + (owner * C::CHUNK + i) * kCols;
+        const float* x = exchange + (set * C::CHUNK + i) * kCols;
         if constexpr (FP8) {  // 128 columns of h, 4 per lane
           const int c = un.tile * kCols + 4 * lane;
           const float4 h = *reinterpret_cast<const float4*>(x + 4 * lane);
@@ -1025,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       fence_proxy_async_global();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(x_empty(owner));
+        mbar_arrive(x_empty(set));
         mbar_arrive(stored(qi % kQueue));
       }
     }
@@ -1205,7 +1214,7 @@ bool row_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, bool 
 
 template <bool FP8>
 constexpr size_t dynamic_smem() {
-  return 1024 + Cfg<FP8>::STAGES * (kTileBytes + Cfg<FP8>::B_BYTES) + 2 * Cfg<FP8>::CHUNK * kCols * 4;
+  return 1024 + Cfg<FP8>::STAGES * (Cfg<FP8>::A_BYTES + Cfg<FP8>::B_BYTES) + 2 * Cfg<FP8>::CHUNK * kCols * 4;
 }
 
 template <bool FP8>
