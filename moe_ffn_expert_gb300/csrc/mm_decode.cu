@@ -49,6 +49,7 @@ namespace {
 
 constexpr int kMaxT = 64, kMaxSlots = 1024, kMaxE = 1024;
 constexpr int kMaxRouted = 12;    // tokens whose selection every CTA repeats, one per warp
+constexpr int kRanked = 128;      // slots that are sorted by comparing each with all
 constexpr int kCols = 128;        // weight columns per unit
 constexpr int kMaxSplit = 4;      // parts of I per GEMM2 column tile
 constexpr int kTileBytes = 16384; // one block of weights: 64 x 128 bf16 or 128 x 128 e4m3
@@ -334,6 +335,7 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int
   float* ls = reinterpret_cast<float*>(ring + sizeof(Building));  // (used before it)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) tb.bad = 0;
+  if (tid < 8 && a.S + tid < kMaxSlots) bd.id[a.S + tid] = 0x7FFF;  // above every expert
   if (a.route) {
     // a row's selection starts from shared memory (kMaxRouted rows of at most 1024 fit)
     const int n = a.T * a.E;
@@ -392,6 +394,52 @@ __device__ bool build_tables(const DecodeArgs& a, Tables& tb, uint8_t* ring, int
       }
       if (lane == 0) tb.chunks = __popc(leaders);
     }
+    fence_proxy_async_smem();
+    __syncthreads();
+    return true;
+  }
+  if (a.S <= kRanked) {
+    // A slot's row is the number of slots of a lower expert or of its own and an earlier number, 8
+    // comparisons per load; a chunk's number is that of the chunks that begin in rows before. (The
+    // way below takes 2 us longer for 64 slots; this one 2 us longer for 198.)
+    int e = 0, row = 0, before = 0, same = 0;
+    if (tid < a.S) {
+      e = bd.id[tid];
+      for (int i = 0; i < a.S; i += 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(bd.id + i);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int x = (int)(u[j >> 1] >> (j & 1) * 16 & 0xFFFFu);
+          row += x < e;
+          same += x == e;
+          before += x == e && i + j < tid;
+        }
+      }
+      row += before;
+      tb.row[tid] = (int16_t)row;
+      tb.tok[row] = (int16_t)(tid / a.K);
+      tb.w[row] = bd.slot_w[tid];
+      bd.rank[row] = before % chunk == 0;  // a chunk begins
+    }
+    __syncthreads();
+    if (warp < kRanked / 32) {
+      const uint32_t begins = __ballot_sync(0xFFFFFFFFu, tid < a.S && bd.rank[tid]);
+      if (lane == 0) bd.warp_sum[warp] = begins;
+    }
+    __syncthreads();
+    int total = 0, c = 0;
+#pragma unroll
+    for (int i = 0; i < kRanked / 32; ++i) {
+      if (i == row >> 5) c = total + __popc(bd.warp_sum[i] & ((1u << (row & 31)) - 1u));
+      total += __popc(bd.warp_sum[i]);
+    }
+    if (tid < a.S && before % chunk == 0) {
+      tb.chunk_row[c] = (uint16_t)row;
+      tb.chunk_e[c] = (uint16_t)e;
+      tb.chunk_n[c] = (uint8_t)min(chunk, same - before);
+    }
+    if (tid == 0) tb.chunks = total;
     fence_proxy_async_smem();
     __syncthreads();
     return true;
