@@ -135,9 +135,10 @@ struct Unit {
   int shared, row0, n, e, tile, kb0, kb1, split, ready;  // kb: stages
 };
 
-// Work units in claiming order.
+// Work units in claiming order: of each product the shared expert's before the others, as they are
+// the longest when it is wider (33 tokens, 1536 beside 768: 53 us, 58 with them last).
 struct Work {
-  int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1, t1s, t2, total, chunk;
+  int nc, ncs, nt1, nt1s, nt2, split, splits, kb_h, kb_i, kb_is, t1s, t1, t2s, total, chunk;
 };
 
 // A value that all lanes share, in the form the compiler knows to be shared.
@@ -533,10 +534,10 @@ __device__ __forceinline__ Work make_work(const DecodeArgs& a, int chunks) {
   const int want = max(1, min(kMaxSplit, (int)gridDim.x / max(1, units)));
   w.split = min(want, w.kb_i);
   w.splits = min(want, max(1, w.kb_is));
-  w.t1 = w.nc * w.nt1;
-  w.t1s = w.t1 + w.ncs * w.nt1s;
-  w.t2 = w.t1s + w.nc * w.nt2 * w.split;
-  w.total = w.t2 + w.ncs * w.nt2 * w.splits;
+  w.t1s = w.ncs * w.nt1s;
+  w.t1 = w.t1s + w.nc * w.nt1;
+  w.t2s = w.t1 + w.ncs * w.nt2 * w.splits;
+  w.total = w.t2s + w.nc * w.nt2 * w.split;
   return w;
 }
 
@@ -556,18 +557,18 @@ __device__ __forceinline__ Unit unit_at(const DecodeArgs& a, const Tables& tb, c
   r.shared = 0;
   r.split = 0;
   int c;
-  if (u < w.t1s) {
+  if (u < w.t1) {
     r.kind = 0;
-    r.shared = u >= w.t1;
-    const int v = r.shared ? u - w.t1 : u, nt = r.shared ? w.nt1s : w.nt1;
+    r.shared = u < w.t1s;
+    const int v = r.shared ? u : u - w.t1s, nt = r.shared ? w.nt1s : w.nt1;
     c = div_small(v, nt);
     r.tile = v - c * nt;
     r.kb0 = 0;
     r.kb1 = w.kb_h;
   } else {
     r.kind = 1;
-    r.shared = u >= w.t2;
-    const int v = u - (r.shared ? w.t2 : w.t1s), sp = r.shared ? w.splits : w.split;
+    r.shared = u < w.t2s;
+    const int v = u - (r.shared ? w.t1 : w.t2s), sp = r.shared ? w.splits : w.split;
     const int kb = r.shared ? w.kb_is : w.kb_i;
     c = div_small(v, w.nt2 * sp);
     const int rest = v - c * w.nt2 * sp;
