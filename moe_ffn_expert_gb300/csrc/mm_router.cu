@@ -22,7 +22,12 @@
 namespace mm {
 namespace {
 
-constexpr int kWarps = 16;  // rows in flight per block
+// Rows in flight per block, at most. The forward's blocks leave partial sums, so it has fewer and
+// larger ones (16384 x 128 with them: 15.7 us, 16.7 in blocks of 8; 8192 x 256 backward: 10.8 us in
+// blocks of 8, 12.1 of 16).
+constexpr int kFwdWarps = 16, kBwdWarps = 8;
+// Few rows spread over more SMs (64 rows of 256: 2.7 us in blocks of 4, 3.5 in blocks of 16).
+inline int warps_per_block(int64_t T, int most) { return T <= 2048 ? 4 : most; }
 
 struct RouterArgs {
   int64_t T;
@@ -92,20 +97,20 @@ __device__ __forceinline__ float row_max(const float (&z)[NV], int E, int lane) 
 }
 
 template <typename LT, int NV>
-__global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
+__global__ void __launch_bounds__(32 * kFwdWarps) k_router_fwd(RouterArgs a) {
   constexpr int SUMS = NV < 4 ? NV : 4;  // probabilities per lane summed over the warps at a time
-  __shared__ float part[kWarps][32 * SUMS];
-  __shared__ int slot[kWarps][16];
+  __shared__ float part[kFwdWarps][32 * SUMS];
+  __shared__ int slot[kFwdWarps][16];
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int E = a.E, K = a.K;
   const bool words = E == 32 * NV && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
   const bool all = a.prob_part != nullptr || (a.score == MM_SCORE_SOFTMAX && !a.normalize);
   float acc[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) acc[j] = 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+  for (int64_t t = (int64_t)blockIdx.x * warps + warp; t < a.T; t += (int64_t)gridDim.x * warps) {
     const LT* row = static_cast<const LT*>(a.logits) + t * E;
     float z[NV];
     uint32_t key[NV];
@@ -165,8 +170,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
     const int e = (int)threadIdx.x / SUMS * NV + j + (int)threadIdx.x % SUMS;
     if (threadIdx.x < 32 * SUMS && e < E) {
       float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) s += part[i][threadIdx.x];
+#pragma unroll 4
+      for (int i = 0; i < warps; ++i) s += part[i][threadIdx.x];
       a.prob_part[(int64_t)blockIdx.x * E + e] = s;
     }
     __syncthreads();
@@ -174,14 +179,14 @@ __global__ void __launch_bounds__(32 * kWarps) k_router_fwd(RouterArgs a) {
 }
 
 template <typename LT, int NV>
-__global__ void __launch_bounds__(32 * kWarps) k_router_bwd(RouterArgs a) {
+__global__ void __launch_bounds__(32 * kBwdWarps) k_router_bwd(RouterArgs a) {
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int E = a.E, K = a.K;
   const bool words = E == 32 * NV && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
   const bool soft = a.score == MM_SCORE_SOFTMAX;
   const bool all = a.dP != nullptr || (soft && !a.normalize);
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+  for (int64_t t = (int64_t)blockIdx.x * warps + warp; t < a.T; t += (int64_t)gridDim.x * warps) {
     const LT* row = static_cast<const LT*>(a.logits) + t * E;
     float z[NV], dz[NV];
     load_logits<LT, NV>(row, E, lane, words, z);
@@ -317,8 +322,10 @@ mm_status check_desc(const mm_router_desc* d) {
   return MM_OK;
 }
 
-int64_t router_blocks(const mm_router_desc& d) {
-  return std::min<int64_t>((d.T + kWarps - 1) / kWarps, (int64_t)std::max(1, device_sm_count()) * 4);
+// The forward's or the backward's blocks: at most 64 warps per SM.
+int64_t router_blocks(const mm_router_desc& d, int most = kFwdWarps) {
+  const int warps = warps_per_block(d.T, most);
+  return std::min<int64_t>((d.T + warps - 1) / warps, (int64_t)std::max(1, device_sm_count()) * 64 / warps);
 }
 
 RouterArgs router_args(const mm_router_desc& d) {
@@ -344,7 +351,7 @@ cudaError_t for_width(int E, F&& f) {
 }
 
 cudaError_t launch_fwd(const mm_router_desc& d, const RouterArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)router_blocks(d)), block(32 * kWarps);
+  const dim3 grid((unsigned)router_blocks(d)), block(32 * warps_per_block(d.T, kFwdWarps));
   return for_width(d.E, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     return d.logits_type == MM_BF16
@@ -446,14 +453,12 @@ mm_status mm_router_backward(const mm_router_desc* d, const void* logits, const 
   a.dL = d_lse;
   a.dz = d_logits;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t blocks = router_blocks(*d);
+  const dim3 blocks((unsigned)router_blocks(*d, kBwdWarps)), threads(32 * warps_per_block(d->T, kBwdWarps));
   MM_TRY(for_width(d->E, [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     return d->logits_type == MM_BF16
-               ? launch_pdl(k_router_bwd<__nv_bfloat16, NV>, dim3((unsigned)blocks),
-                            dim3(32 * kWarps), 0, st, a)
-               : launch_pdl(k_router_bwd<float, NV>, dim3((unsigned)blocks), dim3(32 * kWarps), 0,
-                            st, a);
+               ? launch_pdl(k_router_bwd<__nv_bfloat16, NV>, blocks, threads, 0, st, a)
+               : launch_pdl(k_router_bwd<float, NV>, blocks, threads, 0, st, a);
   }));
   return MM_OK;
 }

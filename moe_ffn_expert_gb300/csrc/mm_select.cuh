@@ -33,7 +33,8 @@ __device__ __forceinline__ float sigmoid_accurate(float z) { return 1.0f / (1.0f
 // at hand; a round is one maximum over the warp, a ballot for its lowest holder, which writes its
 // expert to the rank's slot and brings up its next key.
 //   NV <= 4: a lane's keys are sorted first (adjacent exchanges, so equal keys keep their order)
-//   and a round shifts them: 6 moves instead of a search of 13 steps.
+//   and a round shifts them: 6 moves instead of a search of 13 steps (16384 rows of 128, K = 8:
+//   9.9 us, 11.4 with the search).
 //   NV == 8: the search, in every lane (shorter than a branch of one; sorting 8 takes as long as
 //   nine rounds save). Above that: the search, in the one lane.
 template <int NV, typename ID>
