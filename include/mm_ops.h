@@ -7,8 +7,8 @@
  *                        statistics, forward and backward: what mm_forward takes as topk_ids and
  *                        topk_weights;
  *   mm_decode            the whole MoE layer for a few tokens (inference): router product,
- *                        selection, experts and weighted sum in two launches, with bf16 expert
- *                        weights or e4m3 ones that carry a scale per 128 x 128 block;
+ *                        selection, experts and weighted sum in two or three launches, with bf16
+ *                        expert weights or e4m3 ones that carry a scale per 128 x 128 block;
  *   mm_quantize_blocks   bf16 weights to e4m3 and the scales of their blocks.
  *
  * The rules of mm.h hold here too: row-major contiguous device memory, every buffer (workspaces
@@ -45,8 +45,8 @@ int mm_ops_version(void);
  * bf16 or fp32. A gate has `groups` rows of H, each for T / groups consecutive tokens (1: one
  * gate per channel; T: one per token; 0: no gate).
  * Sizes: T >= 0 (T = 0 does nothing forward and writes zero parameter gradients backward),
- * 1 <= H <= 16384, T a multiple of groups. Rows whose length is a multiple of 16 bytes in every
- * type, at 16-byte aligned addresses, move as 16-byte words; others element by element. */
+ * 1 <= H <= 16384, T a multiple of groups. Fastest are H a multiple of 8 and 16-byte aligned
+ * tensors; aligned tensors of other widths up to 3840 come next. */
 typedef struct mm_norm_desc {
   int64_t T, H, groups;
   int32_t stream_type, block_type, param_type; /* mm_dtype */
@@ -124,11 +124,15 @@ mm_status mm_router_backward(const mm_router_desc* d, const void* logits, const 
 
 /* ---- decode -------------------------------------------------------------------------------
  *
- * The whole MoE layer for T <= 64 tokens with T * K <= 1024, inference only, in two launches:
+ * The whole MoE layer for T <= 64 tokens with T * K <= 1024, inference only, in two launches (three
+ * with a router from 13 tokens on):
  *   logits = x router^T (fp32), selection and weights as the router above (or the caller's ids
- *   and weights), y_t = sum_k w_tk o_tk + o_shared_t with o = (silu(x Wg) * (x Wu)) Wd, the
- *   products w * h rounded to bf16 once, everything else in 32 bits, y rounded once.
- * Every selected expert's weights are read once per 32 of its tokens.
+ *   and weights), y_t = sum_k w_tk o_tk + o_shared_t with o = (silu(x Wg) * (x Wu)) Wd. Products
+ *   and sums are in 32 bits, y is rounded once. Between the two products, w * h is rounded once to
+ *   bf16; with e4m3 weights x and w * h are each kept as a sum of two e4m3 numbers times a power of
+ *   two (of a row of x; of a row and 128 columns of h): 8 significant bits of every value down to
+ *   2^-14 of the row's largest, in steps of 2^-21 of the largest below that.
+ * Every selected expert's weights are read once per 32 (e4m3: 16) of its tokens.
  *
  * weight_type MM_BF16: up bf16 [E, H, 2I], down bf16 [E, I, H] as in mm.h; H, I, shared_I multiples
  * of 8. MM_E4M3: the same shapes in e4m3 with fp32 scales of their 128 x 128 blocks,

@@ -33,6 +33,12 @@
 // columns are added: twice the columns, no conversion of the weights, which outnumber the rows'
 // elements many times. The products of 128 x 128 blocks are scaled in 32 bits as they leave the
 // tensor memory. h is split the same way, with a scale per row and 128 columns.
+//
+// Measured (device time of a call; the floor is the hit experts' bytes at a plain copy's rate):
+// 128 experts of 2048 x 768, top-8, bf16: 64 tokens 182 us, 6.5 TB/s (floor 175); 8 tokens 76 (72);
+// one token 24.6 (11): logits 2, tables 2.6, the first weights 1.8, GEMM2 behind GEMM1, the sums 2.
+// e4m3: 8 tokens 50 us (36), 64 tokens 110 (88); 256 experts of 7168 x 2048, 16 tokens: 629 us, 7.1
+// TB/s (663: weights alone stream a little faster than a copy).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

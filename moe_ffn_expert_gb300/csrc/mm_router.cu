@@ -10,8 +10,11 @@
 //   prob_sum:            dz_e += p_e (dP_e - sum_i dP_i p_i)   [sigmoid: times (1 - a_e)]
 //   lse:                 dz_e += dL exp(z_e - lse)
 //
-// A row is a few hundred bytes: the kernels are bound by launch and row latency at serving sizes,
-// and by the K rounds of the selection over many rows.
+// A row is a few hundred bytes: the kernels are bound by launch and row latency at serving sizes
+// (64 rows of 256, K = 8: 2.7 us; one row: 2.7), and by instructions over many rows (16384 rows of
+// 128, K = 8: 10.0 us, of which 2.3 are the selection's last 7 rounds; 15.6 with the loss
+// statistics, whose partial sums take a second launch; backward of 8192 rows of 256: 10.6 us, 1.6
+// TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>

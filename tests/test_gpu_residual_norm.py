@@ -400,3 +400,8 @@ def test_scale_as_a_tensor_is_read_at_every_call():
     s.fill_(2.0)
     b = block_ops.residual_norm_forward(i["residual"], None, residual_scale=s)[0]
     assert torch.equal(a * 2, b)
+
+
+@pytest.mark.parametrize("T,H,groups", [(400, 7168, 1), (400, 7680, 4), (330, 6144, 330)])
+def test_rows_of_which_one_fits_in_shared_memory(T, H, groups):
+    check(*make(T, H, F32, F32, F32, groups))
