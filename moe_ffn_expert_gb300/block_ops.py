@@ -336,6 +336,12 @@ def quantize_expert_weights(w):
     return q, scale
 
 
+def _padded(t, rows, cols):
+    """A copy of a matrix or matrices with zero rows and columns added (1-byte types as bytes)."""
+    as_bytes = t.view(torch.uint8) if t.element_size() == 1 else t
+    return torch.nn.functional.pad(as_bytes, (0, cols, 0, rows)).view(t.dtype)
+
+
 class MoEDecoder:
     """The whole MoE layer for up to `max_tokens` (<= 64) tokens a call, inference only: keeps the
     weights, their description and a workspace between calls.
@@ -345,6 +351,9 @@ class MoEDecoder:
     tokens alone and selects k experts as moe_router does (router_bias fp32 [E], score, normalize,
     scale); without one it takes topk_ids and topk_weights [T,k]. `shared`: (up [H,2Is],
     down [Is,H]) of a shared expert, and their two scales for 8-bit weights (or None, None).
+
+    mm_decode takes H in multiples of 8 (8-bit weights: 16). For another H the decoder keeps copies of
+    the weights with zeros up to the next one, and pads x and cuts y in every call.
 
     Calls run on the current stream and use the one workspace: one decoder serves one stream."""
 
@@ -396,6 +405,12 @@ class MoEDecoder:
             raise ValueError("expected 1 <= k <= E")
         kept = [up, down, up_scale, down_scale, s_up, s_down, s_us, s_ds, router_weight, router_bias]
         _on_gpu("MoEDecoder", *kept)
+        self._pad = -H % (16 if fp8 else 8)
+        if self._pad:  # (the blocks of 128 that have scales stay the same)
+            for i, (rows, cols) in {0: (self._pad, 0), 1: (0, self._pad), 4: (self._pad, 0),
+                                    5: (0, self._pad), 8: (0, self._pad)}.items():
+                if kept[i] is not None:
+                    kept[i] = _padded(kept[i], rows, cols)
         kept = [_contiguous(t) for t in kept]
         self._kept = kept
         self._weights = _abi.mm_decode_weights(*[_ptr(t) for t in kept])
@@ -405,7 +420,7 @@ class MoEDecoder:
         rt = _type("router_weight", router_weight) if self.routes else _abi.MM_BF16
         self._fields = (Is, _abi.MM_E4M3 if fp8 else _abi.MM_BF16, rt, _SCORE[score], int(normalize),
                         float(scale))
-        self._dims = (H, I, E)
+        self._dims = (H + self._pad, I, E)
         self._descs = {}
         nbytes = self._desc(self.max_tokens)[1]
         if nbytes == 0:
@@ -428,12 +443,12 @@ class MoEDecoder:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens in a decoder for {self.max_tokens}")
-        x = _contiguous(x)
+        x = torch.nn.functional.pad(x, (0, self._pad)) if self._pad else _contiguous(x)
         y = torch.empty_like(x)
         _abi.check(_abi._lib().mm_decode(
             self._desc(T)[0], self._weights_at, x.data_ptr(), _ptr(ids), _ptr(weights), y.data_ptr(),
             self._ws.data_ptr(), self._ws.numel(), _stream(x)), "mm_decode")
-        return y
+        return y[:, :self.H].contiguous() if self._pad else y
 
     def __call__(self, x, topk_ids=None, topk_weights=None):
         """y [T,H] bf16 for x [T,H] bf16."""

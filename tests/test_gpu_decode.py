@@ -392,3 +392,14 @@ def test_ids_of_another_device_are_refused():
         d(m["x"], m["ids"].cpu(), m["w"])
     with pytest.raises(ValueError):
         d(m["x"], m["ids"], m["w"].cpu())
+
+
+@pytest.mark.parametrize("H,I,fp8", [(1016, 496, True), (1000, 32, True), (8, 16, True), (7160, 64, True), (120, 48, True),
+                                     (1001, 40, False), (3, 8, False), (515, 512, False)])
+@pytest.mark.parametrize("T,shared", [(1, 0), (21, 48)])
+def test_widths_that_are_padded(H, I, fp8, T, shared):
+    m = make(T, H, I, 16, 4, fp8, shared=shared)
+    y = check(m)
+    assert y.shape == (T, H) and y.is_contiguous()
+    y, ids, w = decoder(m, route=True).with_routing(m["x"])
+    close(y, reference(m, ids, w))

@@ -319,3 +319,14 @@ def test_more_than_2_31_logits():
     ref, mag = gradient(z[-64:], ids[-64:].long(), torch.ones(64, 4, device="cuda", dtype=torch.float64), None,
                         torch.ones(64, device="cuda", dtype=torch.float64), "softmax", False, 1.0)
     assert ((dz[-64:].double() - ref).abs() <= 1e-5 * mag + 2.0 ** -8 * ref.abs() + 1e-37).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_normalized_expert_has_a_constant_weight(score):
+    """K = 1, normalised: the weight is `scale` whatever the logits, so their gradient is zero, without
+    rounding noise (dw - dw w / w)."""
+    z = logits(400, 16, F32)
+    ids, w, _, _ = block_ops.router_forward(z, 1, score=score, scale=2.5)
+    assert (w == 2.5).all()
+    dw = torch.randn(400, 1, device="cuda")
+    assert not block_ops.router_backward(z, ids, dw, score=score, scale=2.5).any()
