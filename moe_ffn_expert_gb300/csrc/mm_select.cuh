@@ -118,7 +118,7 @@ __device__ __forceinline__ float selected_weight(float z, bool has, int score, i
     total = warp_sum(a);
   else if (score == MM_SCORE_SOFTMAX)
     total = row_sum;
-  return total == 0.f ? 0.f : scale * a / total;
+  return total == 0.f ? 0.f : scale * (a / total);
 }
 
 }  // namespace mm
