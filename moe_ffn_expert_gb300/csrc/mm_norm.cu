@@ -545,7 +545,10 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
       for (int i = 0; i < 4; ++i) acc = fma(y[k][i], y[k][i], acc);
     }
     f32x2 q = both(1.f);
-    if (post) q = both(rsqrtf(block_sum_1(sum_of(acc), red[0], threads) * rh + a.eps));
+    // Two sums a row take a buffer each, so that each one's barrier separates the other buffer's reads
+    // from its next use; a row's only sum takes them in turn, for the next row's barrier to do it.
+    if (post)
+      q = both(rsqrtf(block_sum_1(sum_of(acc), red[pre ? 0 : flip], threads) * rh + a.eps));
     acc = both(0.f);
     const int64_t at = row.t * H;
 #pragma unroll

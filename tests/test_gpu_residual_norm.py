@@ -405,3 +405,24 @@ def test_scale_as_a_tensor_is_read_at_every_call():
 @pytest.mark.parametrize("T,H,groups", [(400, 7168, 1), (400, 7680, 4), (330, 6144, 330)])
 def test_rows_of_which_one_fits_in_shared_memory(T, H, groups):
     check(*make(T, H, F32, F32, F32, groups))
+
+
+@pytest.mark.parametrize("T,H,groups", [
+    # rows of bulk copies in blocks of 2 to 15 working warps, and of 2 to 15 with odd rows
+    (3300, 1024, 0), (2500, 2048, 1), (1300, 5120, 1), (1300, 7680, 4), (2500, 1024, 2500),
+    (3300, 513, 1), (2501, 1021, 0), (1300, 2047, 1), (1300, 3839, 2)])
+def test_post_norm_alone_over_many_rows_repeats(T, H, groups):
+    """After the last block there is one sum per row, whose buffer the next row's sum must not
+    overwrite while a slower warp still reads it. An overwritten partial sum scales part of a row by
+    another row's norm: rows of very different sizes next to each other make that visible."""
+    i, up = make(T, H, pre=False, groups=groups)
+    i["branch"].mul_(torch.exp2(4.0 * (torch.arange(T, device="cuda") % 3))[:, None].to(BF))
+    kw = dict(post_weight=i["post_weight"], gate=i["gate"], residual_scale=0.75)
+    ref, _, mag, _ = oracle_forward(i, 0.75, 1e-6)
+    first, none = block_ops.residual_norm_forward(i["residual"], i["branch"], **kw)
+    assert none is None
+    close("residual_out", first, ref, mag)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        differ += (block_ops.residual_norm_forward(i["residual"], i["branch"], **kw)[0] != first).sum()
+    assert int(differ) == 0
