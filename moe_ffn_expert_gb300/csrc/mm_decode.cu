@@ -656,6 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   }
   tc_fence_before();
   pdl_wait();
+  // The first unit is claimed like the others, so that no unit belongs to a CTA that is not running;
+  // the claim's latency passes behind the tables.
+  int first_unit = 0;
+  if (tid == 0) first_unit = atomicAdd(a.hdr + W_NEXT, 1);
   const bool good = build_tables(a, tb, aligned, C::CHUNK);  // (its barriers publish the mbarriers and tmem_slot)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     // a caller's id is out of range: nothing to do
   } else if (warp == 0) {
     // ------------------------------------------------ claims units and loads their weights
-    int u = blockIdx.x, it = 0;
+    int u = __shfl_sync(0xFFFFFFFFu, first_unit, 0), it = 0;
     Walk<STAGES> ring(empty(0), 1);
     bool ok = true;
     for (int qi = 0; ok; ++qi) {
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         __syncwarp();
         ring.next();
       }
-      u = gridDim.x + __shfl_sync(0xFFFFFFFFu, next, 0);
+      u = __shfl_sync(0xFFFFFFFFu, next, 0);
     }
     // no CTA leaves with a copy into its shared memory in flight
     for (int j = max(0, it - STAGES); j < it; ++j)

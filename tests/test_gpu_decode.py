@@ -403,3 +403,22 @@ def test_widths_that_are_padded(H, I, fp8, T, shared):
     assert y.shape == (T, H) and y.is_contiguous()
     y, ids, w = decoder(m, route=True).with_routing(m["x"])
     close(y, reference(m, ids, w))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_decoders_on_streams_of_different_priority(fp8):
+    """A grid of higher priority takes SMs that free up while the other is partly dispatched: what a
+    running CTA waits for must never belong to one that has no SM yet."""
+    ms = [make(T, 1024, 512, 16, 4, fp8, seed=T) for T in (16, 40)]
+    ds = [decoder(m) for m in ms]
+    ref = [d(m["x"], m["ids"], m["w"]) for d, m in zip(ds, ms)]
+    streams = [torch.cuda.Stream(priority=0), torch.cuda.Stream(priority=-1)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(40):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(ds[i](ms[i]["x"], ms[i]["ids"], ms[i]["w"]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert ds[i].status() == _abi.MM_OK and all(torch.equal(o, ref[i]) for o in outs[i])
