@@ -763,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           if (lane == 0) give_up();
           break;
         }
+        __syncwarp();  // (a shuffle orders no memory: lane 0's acquire holds for all from here on)
         fence_proxy_async_global();
         r[0] = (un.row0 + 8 * lane) * PARTS;
       }
@@ -1108,6 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) give_up();
         break;
       }
+      __syncwarp();  // lane 0's acquire holds for all lanes' loads
       if (c >= a.H) continue;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       // part by part, a part's rows in slot order with 8 loads in flight; then the shared expert
