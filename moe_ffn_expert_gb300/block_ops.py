@@ -15,7 +15,8 @@ A few tokens at a time (inference):
 
 `residual_norm` and `moe_router` are differentiable; the `*_forward` / `*_backward` functions are
 the calls they make. Argument marshalling only: shapes and types are checked, non-contiguous
-tensors are copied to contiguous ones, and everything else runs in libmm.so on the current stream.
+tensors are copied to contiguous ones, and everything else runs in libmm.so on the current stream of
+the tensors' device, which becomes the current one for the call if it is not.
 """
 from __future__ import annotations
 
@@ -54,6 +55,12 @@ def _on_gpu(op, first, *others):
     for t in others:
         if t is not None and t.device != first.device:
             raise ValueError(f"{op}: all tensors must be on {first.device}")
+
+
+def _elsewhere(t):
+    """Whether t is on a GPU that is not the current one (the library launches on the current one)."""
+    device = t.get_device()
+    return device >= 0 and device != torch._C._cuda_getDevice()
 
 
 class _Plans(dict):
@@ -121,6 +128,11 @@ def residual_norm_forward(residual, branch=None, *, post_weight=None, pre_weight
     rmsnorm(r', pre_weight) (None without a pre_weight). `gate` is [H] (per channel) or [G, H],
     row g for the g-th T / G tokens. normed has the branch's type; without a branch
     `normed_dtype` (the residual's if None)."""
+    if _elsewhere(residual):
+        with torch.cuda.device(residual.device):
+            return residual_norm_forward(
+                residual, branch, post_weight=post_weight, pre_weight=pre_weight, gate=gate,
+                residual_scale=residual_scale, eps=eps, normed_dtype=normed_dtype)
     residual_scale, eps = float(residual_scale), float(eps)
     key = (_sig(residual), _sig(branch), _sig(post_weight), _sig(pre_weight), _sig(gate),
            residual_scale, eps, normed_dtype)
@@ -146,6 +158,11 @@ def residual_norm_backward(residual_out, branch, d_residual_out, d_normed, *, po
     """(d_residual, d_branch, d_post_weight, d_pre_weight, d_gate) at the forward's residual_out
     and branch; None in the place of what was not given. d_residual_out may be None (zero);
     d_normed is given exactly if pre_weight is."""
+    if _elsewhere(residual_out):
+        with torch.cuda.device(residual_out.device):
+            return residual_norm_backward(
+                residual_out, branch, d_residual_out, d_normed, post_weight=post_weight,
+                pre_weight=pre_weight, gate=gate, residual_scale=residual_scale, eps=eps)
     residual_scale, eps = float(residual_scale), float(eps)
     key = (_sig(residual_out), _sig(branch), _sig(post_weight), _sig(pre_weight), _sig(gate),
            residual_scale, eps, _sig(d_residual_out), _sig(d_normed))
@@ -246,6 +263,10 @@ def router_forward(logits, k, *, bias=None, score="softmax", normalize=True, sca
     """(topk_ids int32 [T,k], topk_weights fp32 [T,k], prob_sum fp32 [E], lse fp32 [T]); the last
     two are None without `stats`. See mm_ops.h for the definitions. `bias` fp32 [E] takes part in
     the selection only."""
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return router_forward(logits, k, bias=bias, score=score, normalize=normalize,
+                                  scale=scale, stats=stats)
     k, normalize, scale = int(k), bool(normalize), float(scale)
     key = (_sig(logits), k, score, normalize, scale, _sig(bias))
     at, ws_bytes, T, E, dev, _ = _router_plans.get(key) or _router_plan(
@@ -267,6 +288,10 @@ def router_forward(logits, k, *, bias=None, score="softmax", normalize=True, sca
 def router_backward(logits, topk_ids, d_weights, d_prob_sum=None, d_lse=None, *, score="softmax",
                     normalize=True, scale=1.0):
     """d_logits (the logits' type) from the gradients of topk_weights, prob_sum and lse."""
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return router_backward(logits, topk_ids, d_weights, d_prob_sum, d_lse, score=score,
+                                   normalize=normalize, scale=scale)
     normalize, scale = bool(normalize), float(scale)
     key = (_sig(logits), _sig(topk_ids), _sig(d_weights), _sig(d_prob_sum), _sig(d_lse), score,
            normalize, scale)
@@ -324,6 +349,9 @@ def moe_router(logits, k, *, bias=None, score="softmax", normalize=True, scale=1
 def quantize_expert_weights(w):
     """(q float8_e4m3fn of w's shape, scale fp32 [..., ceil(R/128), ceil(C/128)]) of bf16 matrices
     w [..., R, C]: one scale per 128 x 128 block (mm_quantize_blocks)."""
+    if _elsewhere(w):
+        with torch.cuda.device(w.device):
+            return quantize_expert_weights(w)
     if w.dim() < 2 or w.dtype != torch.bfloat16 or not w.is_cuda:
         raise ValueError("expected bfloat16 matrices [..., R, C] on a CUDA device")
     w = w.contiguous()
@@ -438,6 +466,9 @@ class MoEDecoder:
         return got
 
     def _call(self, x, ids, weights):
+        if _elsewhere(x):
+            with torch.cuda.device(x.device):
+                return self._call(x, ids, weights)
         if x.dim() != 2 or x.shape[1] != self.H or x.dtype != torch.bfloat16 or x.device != self.device:
             raise ValueError(f"expected x[T,{self.H}] in bfloat16 on {self.device}")
         T = x.shape[0]
@@ -478,4 +509,5 @@ class MoEDecoder:
     def status(self) -> int:
         """Waits for the current stream and returns the last call's status (MM_OK,
         MM_ERR_BAD_EXPERT_ID or MM_ERR_TIMEOUT)."""
-        return _abi.mm_get_status(self._ws.data_ptr(), _stream(self._ws))
+        with torch.cuda.device(self.device):
+            return _abi.mm_get_status(self._ws.data_ptr(), _stream(self._ws))
