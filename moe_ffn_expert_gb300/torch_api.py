@@ -81,12 +81,13 @@ def _options(shared=None, tokens_per_expert=None):
 
 def forward(ws: Workspace, x, topk_ids, topk_weights, up_proj_weight, down_proj_weight, y=None,
             flags: int = 0, shared=None, tokens_per_expert=None):
-    """One mm_forward(_ex) on the current stream; `shared` = (shared_up, shared_down)."""
+    """One mm_forward(_ex) on the current stream of x's device; `shared` = (shared_up, shared_down)."""
     if y is None:
         y = torch.empty_like(x)
-    st = _abi.mm_forward_ex(ws.dims, _options(shared, tokens_per_expert), _ptr(x), _ptr(topk_ids),
-                            _ptr(topk_weights), _ptr(up_proj_weight), _ptr(down_proj_weight), _ptr(y),
-                            ws.ptr, ws.nbytes, _stream(x.device), flags)
+    with torch.cuda.device(x.device):
+        st = _abi.mm_forward_ex(ws.dims, _options(shared, tokens_per_expert), _ptr(x), _ptr(topk_ids),
+                                _ptr(topk_weights), _ptr(up_proj_weight), _ptr(down_proj_weight), _ptr(y),
+                                ws.ptr, ws.nbytes, _stream(x.device), flags)
     _abi.check(st, "mm_forward")
     return y
 
@@ -103,10 +104,11 @@ def backward(ws: Workspace, dy, x, topk_ids, topk_weights, up_proj_weight, down_
     if shared is not None and d_shared is None:
         d_shared = tuple(torch.empty(t.shape, dtype=gdt, device=x.device) for t in shared)
     opt = _options((*shared, *d_shared) if shared is not None else None)
-    st = _abi.mm_backward_ex(ws.dims, opt, _ptr(dy), _ptr(x), _ptr(topk_ids), _ptr(topk_weights),
-                             _ptr(up_proj_weight), _ptr(down_proj_weight), ws.ptr, ws.nbytes,
-                             _ptr(dx), _ptr(d_topk), _ptr(d_up), _ptr(d_down), _stream(x.device),
-                             flags)
+    with torch.cuda.device(x.device):
+        st = _abi.mm_backward_ex(ws.dims, opt, _ptr(dy), _ptr(x), _ptr(topk_ids), _ptr(topk_weights),
+                                 _ptr(up_proj_weight), _ptr(down_proj_weight), ws.ptr, ws.nbytes,
+                                 _ptr(dx), _ptr(d_topk), _ptr(d_up), _ptr(d_down), _stream(x.device),
+                                 flags)
     _abi.check(st, "mm_backward")
     if shared is not None:
         return dx, d_topk, d_up, d_down, d_shared[0], d_shared[1]

@@ -3,7 +3,7 @@ Host logic only: the current device and the tensors are stand-ins, and nothing i
 import pytest
 import torch
 
-from moe_ffn_expert_gb300 import block_ops
+from moe_ffn_expert_gb300 import _abi, block_ops, torch_api
 
 
 class Reached(Exception):
@@ -63,3 +63,21 @@ def test_a_device_that_is_current_is_not_set_again(state, monkeypatch):
     with pytest.raises(Reached):
         block_ops.router_forward(Elsewhere(state), 2)
     assert not block_ops._elsewhere(torch.zeros(1))  # host tensors are refused by the checks
+
+
+def test_the_layer_makes_the_tensors_device_the_current_one(state, monkeypatch):
+    seen = []
+
+    def call(*_):
+        seen.append(state["current"])
+        return _abi.MM_OK
+
+    monkeypatch.setattr(_abi, "mm_forward_ex", call)
+    monkeypatch.setattr(_abi, "mm_backward_ex", call)
+    monkeypatch.setattr(torch_api, "_stream", lambda device: 0)
+    monkeypatch.setattr(torch_api, "_ptr", lambda t: 0)
+    ws = torch_api.Workspace.wrap(_abi.dims(1, 64, 64, 1, 1), torch.empty(0))
+    x = Elsewhere(state)
+    torch_api.forward(ws, x, x, x, x, x, y=x)
+    torch_api.backward(ws, x, x, x, x, x, x, dx=x, d_topk=x, d_up=x, d_down=x)
+    assert seen == [1, 1] and state["current"] == 0
