@@ -13,10 +13,11 @@ A few tokens at a time (inference):
     layer = MoEDecoder(up, down, k=8, router_weight=router_weight)   # once per layer
     f     = layer(n)                                                 # router, experts, sum
 
-`residual_norm` and `moe_router` are differentiable; the `*_forward` / `*_backward` functions are
-the calls they make. Argument marshalling only: shapes and types are checked, non-contiguous
-tensors are copied to contiguous ones, and everything else runs in libmm.so on the current stream of
-the tensors' device, which becomes the current one for the call if it is not.
+`residual_norm` and `moe_router` are differentiable once (a second derivative is refused); the
+`*_forward` / `*_backward` functions are the calls they make. Argument marshalling only: shapes and
+types are checked, non-contiguous tensors are copied to contiguous ones, and everything else runs in
+libmm.so on the current stream of the tensors' device, which becomes the current one for the call if
+it is not.
 """
 from __future__ import annotations
 
@@ -25,6 +26,7 @@ import ctypes
 import torch
 
 from . import _abi
+from ._first_order import first_order_only
 
 _TYPE = {torch.bfloat16: _abi.MM_BF16, torch.float32: _abi.MM_FP32}
 _SCORE = {"softmax": _abi.MM_SCORE_SOFTMAX, "sigmoid": _abi.MM_SCORE_SIGMOID}
@@ -224,7 +226,8 @@ class ResidualNormFunction(torch.autograd.Function):
         dr, df, dpost, dpre, dg = residual_norm_backward(
             out, branch, d_out, d_normed, post_weight=post_weight, pre_weight=pre_weight,
             gate=gate, residual_scale=ctx.scale, eps=ctx.eps)
-        return dr, df, dpost, dpre, dg, None, None, None
+        return (*first_order_only("residual_norm", (dr, df, dpost, dpre, dg),
+                                  (*ctx.saved_tensors, d_out, d_normed)), None, None, None)
 
 
 def residual_norm(residual, branch=None, *, post_weight=None, pre_weight=None, gate=None,
@@ -336,7 +339,9 @@ class RouterFunction(torch.autograd.Function):
             return (None,) * 7
         if d_weights is None:
             d_weights = torch.zeros(ids.shape, dtype=torch.float32, device=ids.device)
-        return (router_backward(logits, ids, d_weights, d_prob_sum, d_lse, **ctx.how),) + (None,) * 6
+        dz = router_backward(logits, ids, d_weights, d_prob_sum, d_lse, **ctx.how)
+        return (*first_order_only("moe_router", (dz,), (logits, d_weights, d_prob_sum, d_lse)),
+                *(None,) * 6)
 
 
 def moe_router(logits, k, *, bias=None, score="softmax", normalize=True, scale=1.0, stats=False):

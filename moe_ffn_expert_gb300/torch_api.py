@@ -12,6 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import _abi
+from ._first_order import first_order_only
 
 
 def _ptr(t: torch.Tensor) -> int:
@@ -167,7 +168,10 @@ class HyperMegaMoEFunction(torch.autograd.Function):
                        shared=tuple(shared) if ctx.has_shared else None)
         dx, d_topk, d_up, d_down = out[:4]
         ds_up, ds_down = out[4:] if ctx.has_shared else (None, None)
-        return dx, None, d_topk.to(ctx.wdtype), d_up, d_down, ds_up, ds_down, None
+        dx, d_topk, d_up, d_down, ds_up, ds_down = first_order_only(
+            "hyper_mega_moe", (dx, d_topk.to(ctx.wdtype), d_up, d_down, ds_up, ds_down),
+            (dy, *ctx.saved_tensors))
+        return dx, None, d_topk, d_up, d_down, ds_up, ds_down, None
 
 
 def hyper_mega_moe(x, topk_ids, topk_weights, up_proj_weight, down_proj_weight, *,
@@ -181,6 +185,14 @@ def hyper_mega_moe(x, topk_ids, topk_weights, up_proj_weight, down_proj_weight, 
     host wait) and raises MMError(MM_ERR_TOKENS_PER_EXPERT) if they differ."""
     if (shared_up_proj_weight is None) != (shared_down_proj_weight is None):
         raise ValueError("give both shared-expert weights or neither")
-    return HyperMegaMoEFunction.apply(x, topk_ids, topk_weights, up_proj_weight, down_proj_weight,
-                                      shared_up_proj_weight, shared_down_proj_weight,
-                                      tokens_per_expert)
+
+    # conversions are autograd's: what the backward keeps are then the function's own inputs
+    def converted(t):
+        return None if t is None else t.contiguous()
+
+    if topk_weights.is_floating_point():
+        topk_weights = topk_weights.to(torch.float32)
+    return HyperMegaMoEFunction.apply(converted(x), topk_ids, converted(topk_weights),
+                                      converted(up_proj_weight), converted(down_proj_weight),
+                                      converted(shared_up_proj_weight),
+                                      converted(shared_down_proj_weight), tokens_per_expert)
