@@ -754,7 +754,8 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
           raw[k][i] = fma(d, fs, raw[k][i]);
         }
         dr[i] = mul(scale, d);
-        f[i] = fma(ncs, f[i], mul(sf2, mul(w[i], d)));
+        // (without a norm the branch's value takes no part, not even an infinite one times zero)
+        f[i] = post ? fma(ncs, f[i], mul(sf2, mul(w[i], d))) : mul(w[i], d);
       }
       cols.store(static_cast<ST*>(a.dr) + at, k, dr);
       if (FULL || a.df != nullptr) cols.store(static_cast<BT*>(a.df) + at, k, f);

@@ -426,3 +426,19 @@ def test_post_norm_alone_over_many_rows_repeats(T, H, groups):
     for _ in range(300):
         differ += (block_ops.residual_norm_forward(i["residual"], i["branch"], **kw)[0] != first).sum()
     assert int(differ) == 0
+
+
+@pytest.mark.parametrize("H", [1024, 1021, 8192])
+@pytest.mark.parametrize("groups", [0, 1, 2500])
+@pytest.mark.parametrize("pre", [True, False])
+def test_without_a_post_weight_the_branch_value_is_not_used(H, groups, pre):
+    """d_branch = gate * d does not depend on the branch, not even on an infinite one, whether rows come
+    by bulk copies or straight from memory."""
+    T = 2500
+    i, up = make(T, H, post=False, pre=pre, groups=groups)
+    kw = dict(pre_weight=i["pre_weight"], gate=i["gate"])
+    clean = block_ops.residual_norm_backward(i["residual"], i["branch"], up["d_out"], up["d_normed"], **kw)
+    f = i["branch"].clone()
+    f[3], f[2000, 5], f[T - 1, H - 1] = float("inf"), float("-inf"), float("nan")
+    got = block_ops.residual_norm_backward(i["residual"], f, up["d_out"], up["d_normed"], **kw)
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
