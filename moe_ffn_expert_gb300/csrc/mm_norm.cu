@@ -139,6 +139,13 @@ __global__ void __launch_bounds__(1024) k_norm_fwd(NormArgs a) {
   }
 }
 
+// A norm's backward takes q^3 / H <.., r'> r' off a row, q = 1 / rms: here the factor of q r', which is
+// of unit size as q <.., r'> is of the other factor's. q^3 by itself leaves the range of 32 bits for
+// rows of 1e13 (or, with no eps, 1e-13).
+__device__ __forceinline__ float unit_factor(float q, float rh, float dot) {
+  return (q * rh) * (q * dot);
+}
+
 // A block walks its pieces row by row; the three parameter gradients of its columns stay in
 // registers until the block (weights) or the piece (gate) ends.
 template <typename ST, typename BT, int W, int NV>
@@ -203,9 +210,9 @@ __global__ void __launch_bounds__(1024) k_norm_bwd(NormArgs a) {
       if (pre || post) block_sum<6>(sum, red, flip);
       const float rh = 1.f / (float)H;
       const float q = pre ? rsqrtf(sum[0] * rh + a.eps) : 0.f;
-      const float cq = q * q * q * rh * sum[1];
+      const float cq = unit_factor(q, rh, sum[1]);
       const float s = post ? rsqrtf(sum[2] * rh + a.eps) : 1.f;
-      const float cs = s * s * s * rh * (pre ? sum[3] + q * sum[4] - cq * sum[5] : sum[3]);
+      const float cs = unit_factor(s, rh, pre ? sum[3] + q * sum[4] - cq * (q * sum[5]) : sum[3]);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * (int)blockDim.x + (int)threadIdx.x) * W;
@@ -217,13 +224,13 @@ __global__ void __launch_bounds__(1024) k_norm_bwd(NormArgs a) {
         if (pre) load_any<W>(a.w_pre, a.ptype, c, wq);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const float d = pre ? u[j][i] + q * (wq[i] * v[j][i]) - cq * x[j][i] : u[j][i];
-          const float sf = s * f[j][i];
+          const float xq = q * x[j][i], sf = s * f[j][i];
+          const float d = pre ? u[j][i] + q * (wq[i] * v[j][i]) - cq * xq : u[j][i];
           dr[i] = a.scale * d;
-          d_pre[j][i] += v[j][i] * x[j][i] * q;
+          d_pre[j][i] += v[j][i] * xq;
           d_gate[j][i] += d * (w[i] * sf);
           d_post[j][i] += g[j][i] * d * sf;
-          df[i] = post ? s * (e[j][i] * d) - cs * f[j][i] : g[j][i] * d;
+          df[i] = post ? s * (e[j][i] * d) - cs * sf : g[j][i] * d;
         }
         store_vec<W>(static_cast<ST*>(a.dr) + t * H + c, dr);
         if (a.df != nullptr) store_vec<W>(static_cast<BT*>(a.df) + t * H + c, df);
@@ -725,10 +732,9 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
     for (int i = 0; i < 8; ++i) sum[i] = i < 6 ? sum_of(acc[i < 6 ? i : 0]) : 0.f;
     block_sum_8(sum, red[flip], threads);
     const float q = pre ? rsqrtf(sum[0] * rh + a.eps) : 0.f;
-    const float cq = q * q * q * rh * sum[1];
+    const float cq = unit_factor(q, rh, sum[1]);
     const float sf = post ? rsqrtf(sum[2] * rh + a.eps) : 1.f;
-    const float cs =
-        post ? sf * sf * sf * rh * (pre ? sum[3] + q * sum[4] - cq * sum[5] : sum[3]) : 0.f;
+    const float cs = post ? unit_factor(sf, rh, pre ? sum[3] + q * sum[4] - cq * (q * sum[5]) : sum[3]) : 0.f;
     const f32x2 q2 = both(q), ncq = both(-cq), sf2 = both(sf), ncs = both(-cs), scale = both(a.scale);
     const int64_t at = row.t * H;
 #pragma unroll
@@ -742,7 +748,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
         f32x2 d = u[i];
         if (pre) {
           const f32x2 xq = mul(q2, x[i]);
-          d = fma(ncq, x[i], fma(q2, mul(wn[k][i], v[i]), d));
+          d = fma(ncq, xq, fma(q2, mul(wn[k][i], v[i]), d));
           d_pre[k][i] = fma(v[i], xq, d_pre[k][i]);
         }
         const f32x2 fs = mul(sf2, f[i]);
@@ -755,7 +761,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
         }
         dr[i] = mul(scale, d);
         // (without a norm the branch's value takes no part, not even an infinite one times zero)
-        f[i] = post ? fma(ncs, f[i], mul(sf2, mul(w[i], d))) : mul(w[i], d);
+        f[i] = post ? fma(ncs, fs, mul(sf2, mul(w[i], d))) : mul(w[i], d);
       }
       cols.store(static_cast<ST*>(a.dr) + at, k, dr);
       if (FULL || a.df != nullptr) cols.store(static_cast<BT*>(a.df) + at, k, f);

@@ -442,3 +442,20 @@ def test_without_a_post_weight_the_branch_value_is_not_used(H, groups, pre):
     f[3], f[2000, 5], f[T - 1, H - 1] = float("inf"), float("-inf"), float("nan")
     got = block_ops.residual_norm_backward(i["residual"], f, up["d_out"], up["d_normed"], **kw)
     assert torch.equal(got[0], clean[0]) and torch.equal(got[1], clean[1])
+
+
+@pytest.mark.parametrize("H", [512, 511, 8192])
+@pytest.mark.parametrize("stream,branch", [(2.0 ** 46, 1.0), (1.0, 2.0 ** 46), (2.0 ** 54, 2.0 ** 50),
+                                           (2.0 ** -46, 1.0), (2.0 ** -46, 2.0 ** -50)])
+def test_gradients_of_very_large_and_small_rows(H, stream, branch):
+    """Rows whose 1 / rms has a cube beyond 32 bits; without an eps, which would hide small ones. The
+    upstream gradient of r' is left out: it would cover what comes through the norm of a large row."""
+    i, up = make(700, H, F32, F32, F32)
+    i["residual"].mul_(stream)
+    i["branch"].mul_(branch)
+    kw = dict(post_weight=i["post_weight"], pre_weight=i["pre_weight"], gate=i["gate"], eps=0.0)
+    got = block_ops.residual_norm_backward(i["residual"], i["branch"], None, up["d_normed"], **kw)
+    ref = oracle_backward(i, dict(up, d_out=torch.zeros_like(up["d_out"])), 1.0, 0.0)
+    for g, k in zip(got, ("residual", "branch", "post", "pre", "gate")):
+        want, mag = ref[k]
+        assert ((g.double() - want).abs() <= 1e-5 * mag + 1e-37).all(), k
