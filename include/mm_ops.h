@@ -46,7 +46,9 @@ int mm_ops_version(void);
  * gate per channel; T: one per token; 0: no gate).
  * Sizes: T >= 0 (T = 0 does nothing forward and writes zero parameter gradients backward),
  * 1 <= H <= 16384, T a multiple of groups. Fastest are H a multiple of 8 and 16-byte aligned
- * tensors; aligned tensors of other widths up to 3840 come next. */
+ * tensors; aligned tensors of other widths up to 3840 come next.
+ * Device waits are bounded. One that runs out (a failing device) leaves NaN in the rows of its block
+ * that were still to come, and in the parameter gradients. */
 typedef struct mm_norm_desc {
   int64_t T, H, groups;
   int32_t stream_type, block_type, param_type; /* mm_dtype */
@@ -77,6 +79,10 @@ mm_status mm_residual_norm_backward(const mm_norm_desc* d, const void* residual_
                                     void* d_residual, void* d_branch, void* d_post_weight,
                                     void* d_pre_weight, void* d_gate, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/* Test hook: while on, residual_norm calls of this host thread let the loads of one block stop after
+ * its first row (in the kernels that load rows ahead) and limit device waits to 50 ms. */
+void mm_residual_norm_test_stall(int on);
 
 /* ---- router -------------------------------------------------------------------------------
  *

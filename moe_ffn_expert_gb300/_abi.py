@@ -137,6 +137,7 @@ def _lib():
         "mm_residual_norm_forward": (st, [_P] * 9),
         "mm_residual_norm_workspace_size": (ctypes.c_size_t, [_P]),
         "mm_residual_norm_backward": (st, [_P] * 14 + [ctypes.c_size_t, _P]),
+        "mm_residual_norm_test_stall": (None, [ctypes.c_int]),
         "mm_router_workspace_size": (ctypes.c_size_t, [_P]),
         "mm_router_forward": (st, [_P] * 8 + [ctypes.c_size_t, _P]),
         "mm_router_backward": (st, [_P] * 8),

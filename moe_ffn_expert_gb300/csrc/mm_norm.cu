@@ -53,6 +53,8 @@ struct NormArgs {
   // a piece: up to piece_rows consecutive tokens of one gate group; a block takes pieces
   // blockIdx.x, + gridDim.x, ...
   int64_t pieces, pieces_per_group, piece_rows, group_rows;
+  uint64_t timeout_ns;  // of a row's arrival (row rings)
+  int stall;            // test hook: block 0's loading warp stops after its first row
 };
 
 // Block sum of N values; red: 2 buffers of 32 * N floats, `flip` alternates between calls so that
@@ -428,8 +430,19 @@ __device__ __forceinline__ void row_barrier(int threads) {
 }
 
 // Row loads are this library's own copies from memory that the launch was given: the wait for one
-// cannot run out unless the device has failed. It is bounded all the same (2 s), and then goes on.
-constexpr uint64_t kRowTimeoutNs = 2000000000ull;
+// cannot run out unless the device has failed. It is bounded all the same, and then shows: a thread
+// whose wait ran out (kLost, beside the parity that it would wait for next) waits no more, hands no
+// stage back and puts NaN into the row's sums (or, without any, in the place of what it would have
+// read), so its block's remaining rows and column sums are NaN. A loading warp that gets no stage back
+// issues no further copy.
+constexpr uint64_t kRowTimeoutNs = 2000000000ull, kTestTimeoutNs = 50000000ull;
+constexpr uint32_t kLost = 2;
+
+__device__ __forceinline__ void await_row(uint32_t bar, uint32_t& ph, uint64_t limit_ns) {
+  if (ph < kLost && !mbar_wait(bar, ph, limit_ns)) ph |= kLost;
+}
+
+__device__ __forceinline__ f32x2 nan_pair() { return both(__int_as_float(0x7FC00000)); }
 
 // Sum over the block: partial sums of the warps in `red` (32 floats, zero beyond the block's
 // warps), read back by every thread.
@@ -454,12 +467,18 @@ __device__ __forceinline__ void produce_rows(const NormArgs& a, const RowRing& r
   row.start(a, blockIdx.x);
   int s = 0;
   uint32_t ph = 1;
+  bool stop = false;
   while (row.more(a)) {
-    mbar_wait(empty + 8u * s, ph, kRowTimeoutNs);
+    const bool free_stage = mbar_wait(empty + 8u * s, ph, a.timeout_ns);
+    if (!__all_sync(0xFFFFFFFFu, free_stage) || stop) break;
     load_row<ST, BT, PT, ODD>(a, ring, smem + s * ring.bytes, full + 8u * s, row.t);
     row.next(a);
+    stop = a.stall && blockIdx.x == 0;
     if (++s == ring.depth) s = 0, ph ^= 1u;
   }
+  // no block leaves with a copy into its shared memory in flight: the stages before s had their last
+  // one in this turn of the ring, the others (if any) in the turn before
+  for (int i = 0; i < ring.depth; ++i) mbar_wait(full + 8u * i, i < s ? ph ^ 1u : ph, a.timeout_ns);
 }
 
 // FULL: every part is there (branch, both norms, both upstream gradients; OWN: and a gate that comes
@@ -534,7 +553,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
   while (row.more(a)) {
     const uint32_t stage = smem_u32(smem) + s * ring.bytes;
     if (a.gate != nullptr && !own_gate && row.group != group) branch_weights(group = row.group);
-    mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
+    await_row(smem_u32(&bars[s]), ph, a.timeout_ns);
     f32x2 x[kVecs][4], y[kVecs][4], acc = both(0.f);
     const uint32_t xr = row_at<ODD>(stage, ring.x, row.t, H * sizeof(ST));
     const uint32_t fr = row_at<ODD>(stage, ring.f, row.t, H * sizeof(BT));
@@ -550,7 +569,12 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc = fma(y[k][i], y[k][i], acc);
+      if (!post && ph >= kLost) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[k][i] = nan_pair();
+      }
     }
+    if (post && ph >= kLost) acc = nan_pair();
     f32x2 q = both(1.f);
     // Two sums a row take a buffer each, so that each one's barrier separates the other buffer's reads
     // from its next use; a row's only sum takes them in turn, for the next row's barrier to do it.
@@ -576,7 +600,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_fwd_rows(NormArgs a, RowRi
       if (FULL || a.out != nullptr) cols.store(static_cast<ST*>(a.out) + at, k, x[k]);
     }
     __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
+    if ((tid & 31) == 0 && ph < kLost) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
     float sum = 0.f;
     if (pre)
       sum = block_sum_1(sum_of(acc), red[post ? 1 : flip], threads);
@@ -665,7 +689,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
   const float rh = 1.f / (float)H;
   while (row.more(a)) {
     const uint32_t stage = smem_u32(smem) + s * ring.bytes;
-    mbar_wait(smem_u32(&bars[s]), ph, kRowTimeoutNs);
+    await_row(smem_u32(&bars[s]), ph, a.timeout_ns);
     if (fresh) {
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
@@ -730,6 +754,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
     float sum[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = i < 6 ? sum_of(acc[i < 6 ? i : 0]) : 0.f;
+    if (ph >= kLost) sum[0] = sum[2] = __int_as_float(0x7FC00000);
     block_sum_8(sum, red[flip], threads);
     const float q = pre ? rsqrtf(sum[0] * rh + a.eps) : 0.f;
     const float cq = unit_factor(q, rh, sum[1]);
@@ -750,6 +775,8 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
           const f32x2 xq = mul(q2, x[i]);
           d = fma(ncq, xq, fma(q2, mul(wn[k][i], v[i]), d));
           d_pre[k][i] = fma(v[i], xq, d_pre[k][i]);
+        } else if (ph >= kLost) {
+          d = nan_pair();
         }
         const f32x2 fs = mul(sf2, f[i]);
         if (own_gate) {  // its gradient leaves with the row; the sum is of g d f s
@@ -793,7 +820,7 @@ __global__ void __launch_bounds__(kRowThreads) k_norm_bwd_rows(NormArgs a, RowRi
       fresh = true;
     }
     __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
+    if ((tid & 31) == 0 && ph < kLost) mbar_arrive(smem_u32(&bars[8 + s]));  // the stage is read
     row.next(a);
     flip ^= 1;
     if (++s == ring.depth) s = 0, ph ^= 1u;
@@ -1012,6 +1039,8 @@ void deal_rows(NormArgs& a, const RowPlan& p) {
   a.group_rows = p.group_rows;
 }
 
+thread_local int t_stall = 0;  // mm_residual_norm_test_stall
+
 NormArgs norm_args(const mm_norm_desc& d) {
   NormArgs a{};
   a.T = d.T;
@@ -1020,6 +1049,8 @@ NormArgs norm_args(const mm_norm_desc& d) {
   a.scale = d.residual_scale;
   a.eps = d.eps;
   a.rows_per_gate = d.groups > 0 ? d.T / d.groups : 0;
+  a.stall = t_stall;
+  a.timeout_ns = t_stall ? kTestTimeoutNs : kRowTimeoutNs;
   return a;
 }
 
@@ -1031,6 +1062,8 @@ using namespace mm;
 extern "C" {
 
 int mm_ops_version(void) { return 1; }
+
+void mm_residual_norm_test_stall(int on) { t_stall = on != 0; }
 
 mm_status mm_residual_norm_forward(const mm_norm_desc* d, const void* residual, const void* branch,
                                    const void* post_weight, const void* pre_weight,

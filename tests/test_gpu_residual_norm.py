@@ -459,3 +459,40 @@ def test_gradients_of_very_large_and_small_rows(H, stream, branch):
     for g, k in zip(got, ("residual", "branch", "post", "pre", "gate")):
         want, mag = ref[k]
         assert ((g.double() - want).abs() <= 1e-5 * mag + 1e-37).all(), k
+
+
+@pytest.mark.parametrize("T,H,groups", [(2500, 1024, 1), (2500, 1021, 0), (1300, 7168, 4), (2500, 1024, 2500)])
+@pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True), (False, False)])
+def test_rows_that_never_come_are_nan(T, H, groups, post, pre):
+    """One block's loads stop after its first row: its other rows and all parameter gradients that they
+    belong to are NaN, every other row is what it is otherwise, and the next call is as ever."""
+    i, up = make(T, H, groups=groups, post=post, pre=pre)
+    ref = run_both(i, up)
+    lib = _abi._lib()
+    lib.mm_residual_norm_test_stall(1)
+    try:
+        got = run_both(i, up)
+        torch.cuda.synchronize()
+    finally:
+        lib.mm_residual_norm_test_stall(0)
+
+    def rows(a, b):
+        lost = torch.isnan(a).all(1)
+        assert 1 <= int(lost.sum()) < T // 2
+        assert torch.equal(a[~lost], b[~lost])
+        return lost
+
+    lost = rows(got[0][0], ref[0][0])
+    if pre:
+        assert torch.equal(rows(got[0][1], ref[0][1]), lost)
+    lost = rows(got[1]["residual"], ref[1]["residual"])
+    assert torch.equal(rows(got[1]["branch"], ref[1]["branch"]), lost)
+    for k in ("post", "pre"):
+        assert got[1][k] is None or torch.isnan(got[1][k]).all()
+    if groups:
+        gates = torch.isnan(got[1]["gate"]).all(1)
+        assert gates.any() and torch.equal(gates, lost.view(groups, -1).any(1))
+        assert torch.equal(got[1]["gate"][~gates], ref[1]["gate"][~gates])
+    again = run_both(i, up)
+    assert all(torch.equal(again[1][k], ref[1][k]) for k in ref[1] if ref[1][k] is not None)
+    assert torch.equal(again[0][0], ref[0][0])
