@@ -99,6 +99,29 @@ __device__ __forceinline__ float row_max(const float (&z)[NV], int E, int lane) 
   return m == -INFINITY ? 0.f : m;  // a row of -inf: exp(z) is 0 without a shift
 }
 
+// The row's a (in 32 bits up to a common factor, which its uses divide out) and their sum. m: row_max.
+template <int NV>
+__device__ __forceinline__ float row_scores(const float (&z)[NV], float (&x)[NV], int E, int lane,
+                                            bool soft, float m) {
+  float A = 0.f;
+  if (!soft) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      x[j] = lane * NV + j >= E ? 0.f : sigmoid_accurate(z[j]);
+      A += x[j];
+    }
+    A = warp_sum(A);
+    if (!(A < kTinySigmoids)) return A;
+    A = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    x[j] = lane * NV + j >= E ? 0.f : expf(z[j] - m);
+    A += x[j];
+  }
+  return warp_sum(A);
+}
+
 template <typename LT, int NV>
 __global__ void __launch_bounds__(32 * kFwdWarps) k_router_fwd(RouterArgs a) {
   constexpr int SUMS = NV < 4 ? NV : 4;  // probabilities per lane summed over the warps at a time
@@ -132,13 +155,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps) k_router_fwd(RouterArgs a) {
     if (all || a.lse != nullptr) m = row_max<NV>(z, E, lane);
     if (all) {
       float x[NV];
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        x[j] = lane * NV + j >= E ? 0.f
-               : a.score == MM_SCORE_SIGMOID ? sigmoid_accurate(z[j]) : expf(z[j] - m);
-        A += x[j];
-      }
-      A = warp_sum(A);
+      A = row_scores<NV>(z, x, E, lane, a.score == MM_SCORE_SOFTMAX, m);
       if (a.prob_part != nullptr) {
         const float inv = A == 0.f ? 0.f : 1.f / A;
 #pragma unroll
@@ -203,12 +220,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_router_bwd(RouterArgs a) {
     if (all || a.dL != nullptr) m = row_max<NV>(z, E, lane);
     float p[NV];
     if (all) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        p[j] = lane * NV + j >= E ? 0.f : soft ? expf(z[j] - m) : sigmoid_accurate(z[j]);
-        A += p[j];
-      }
-      A = warp_sum(A);
+      A = row_scores<NV>(z, p, E, lane, soft, m);
       inv = A == 0.f ? 0.f : 1.f / A;
 #pragma unroll
       for (int j = 0; j < NV; ++j) p[j] *= inv;

@@ -100,6 +100,10 @@ __device__ __forceinline__ int select_topk(uint32_t (&key)[NV], int K, int lane,
   return mine;
 }
 
+// Sums of sigmoids below this: every logit is below -46, where sigmoid(z) is e^z to 32 bits. Ratios are
+// then taken of e^(z - largest z), as the sigmoids themselves leave the range of 32 bits from -88 on.
+constexpr float kTinySigmoids = 1e-20f;
+
 // The weight of the lane's selected expert with logit z (lane < K), as mm_ops.h defines it.
 // row_max, row_sum: max and sum of a over the whole row (used by softmax without `normalize`).
 __device__ __forceinline__ float selected_weight(float z, bool has, int score, int normalize,
@@ -114,9 +118,15 @@ __device__ __forceinline__ float selected_weight(float z, bool has, int score, i
     a = has ? expf(z - m) : 0.f;
   }
   float total = 1.f;
-  if (normalize)
+  if (normalize) {
     total = warp_sum(a);
-  else if (score == MM_SCORE_SOFTMAX)
+    if (score == MM_SCORE_SIGMOID && total < kTinySigmoids) {
+      float m = warp_max(has ? z : -INFINITY);
+      if (m == -INFINITY) m = 0.f;
+      a = has ? expf(z - m) : 0.f;
+      total = warp_sum(a);
+    }
+  } else if (score == MM_SCORE_SOFTMAX)
     total = row_sum;
   return total == 0.f ? 0.f : scale * (a / total);
 }

@@ -330,3 +330,18 @@ def test_one_normalized_expert_has_a_constant_weight(score):
     assert (w == 2.5).all()
     dw = torch.randn(400, 1, device="cuda")
     assert not block_ops.router_backward(z, ids, dw, score=score, scale=2.5).any()
+
+
+@pytest.mark.parametrize("shift", [60.0, 88.0, 100.0, 200.0, 600.0])
+@pytest.mark.parametrize("E,K", [(20, 3), (128, 8), (256, 8), (1000, 16)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_sigmoid_scores_far_below_zero(shift, E, K, dt):
+    """Scores whose sigmoids 32 bits cannot hold still have ratios: normalised weights, probabilities
+    and their gradients, as defined. Rows of ordinary logits stand between."""
+    z = logits(40, E, F32, seed=E)
+    z[::2] -= shift
+    z[5, 3:] = -math.inf
+    z[6, 3:] = -math.inf
+    z = z.to(dt)
+    check_forward(z, K, "sigmoid", True, scale=1.5)
+    check_backward(z[7:].contiguous(), K, "sigmoid", True, True, scale=1.5)
