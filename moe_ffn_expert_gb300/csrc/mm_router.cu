@@ -171,7 +171,15 @@ __global__ void __launch_bounds__(32 * kFwdWarps) k_router_fwd(RouterArgs a) {
           if (lane * NV + j < E) s += expf(z[j] - m);
         s = warp_sum(s);
       }
-      if (lane == 0) a.lse[t] = m + logf(s);
+      if (lane == 0) {
+        float lse = m + logf(s);
+        if (m == INFINITY) {  // infinity - infinity: s is NaN, whether a logit is or not
+          lse = INFINITY;
+#pragma unroll 1
+          for (int e = 0; e < E; ++e) lse += fabsf(load_logit(row + e));
+        }
+        a.lse[t] = lse;
+      }
     }
     const int id = select_topk<NV>(key, K, lane, &slot[warp][0]);
     const float zs = lane < K ? load_logit(row + id) : 0.f;

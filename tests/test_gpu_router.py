@@ -345,3 +345,15 @@ def test_sigmoid_scores_far_below_zero(shift, E, K, dt):
     z = z.to(dt)
     check_forward(z, K, "sigmoid", True, scale=1.5)
     check_backward(z[7:].contiguous(), K, "sigmoid", True, True, scale=1.5)
+
+
+def test_log_sum_of_infinite_logits():
+    """log sum exp of a row with +inf is +inf, unless a NaN stands beside it."""
+    z = logits(4, 40, F32)
+    z[0, 7] = math.inf
+    z[1, 7], z[1, 9] = math.inf, -math.inf
+    z[2, 7], z[2, 30] = math.inf, math.nan
+    for score in ("softmax", "sigmoid"):
+        lse = block_ops.router_forward(z, 4, score=score, stats=True)[3]
+        assert torch.equal(lse.isnan(), torch.logsumexp(z, 1).isnan()) and (lse[:2] == math.inf).all()
+        assert torch.isfinite(lse[3])
