@@ -500,6 +500,8 @@ class MoEDecoder:
             raise TypeError("topk_ids must be int32 or int64")
         if topk_ids.device != self.device or topk_weights.device != self.device:
             raise ValueError(f"expected topk_ids and topk_weights on {self.device}")
+        if topk_ids.dtype == torch.int64:  # (a number beyond 32 bits must not become another expert's)
+            topk_ids = topk_ids.clamp(-1, self._dims[2])
         ids = _contiguous(topk_ids.to(torch.int32))
         return self._call(x, ids, _contiguous(topk_weights.to(torch.float32)))
 

@@ -422,3 +422,17 @@ def test_two_decoders_on_streams_of_different_priority(fp8):
     torch.cuda.synchronize()
     for i in range(2):
         assert ds[i].status() == _abi.MM_OK and all(torch.equal(o, ref[i]) for o in outs[i])
+
+
+def test_64_bit_ids_out_of_range_are_reported():
+    """Also those whose low 32 bits are an expert's number."""
+    m = make(4, 128, 64, 8, 2)
+    d = decoder(m)
+    y = d(m["x"], m["ids"].long(), m["w"])
+    assert d.status() == _abi.MM_OK
+    for bad in (2 ** 32 + 3, -2 ** 32, 8, -1):
+        ids = m["ids"].long()
+        ids[2, 1] = bad
+        d(m["x"], ids, m["w"])
+        assert d.status() == _abi.MM_ERR_BAD_EXPERT_ID, bad
+    assert torch.equal(d(m["x"], m["ids"].long(), m["w"]), y)
