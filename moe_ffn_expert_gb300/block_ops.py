@@ -385,8 +385,12 @@ class MoEDecoder:
     scale); without one it takes topk_ids and topk_weights [T,k]. `shared`: (up [H,2Is],
     down [Is,H]) of a shared expert, and their two scales for 8-bit weights (or None, None).
 
-    mm_decode takes H in multiples of 8 (8-bit weights: 16). For another H the decoder keeps copies of
-    the weights with zeros up to the next one, and pads x and cuts y in every call.
+    The decoder reads the given tensors in every call, so that updates of the weights take effect in
+    the next one. Two kinds it has to copy: non-contiguous ones, and, as mm_decode takes H in multiples
+    of 8 (8-bit weights: 16), those of another H, with zeros up to the next multiple (x is padded and y
+    cut in every call). A call takes over the updates of copied tensors that autograd counts (in-place
+    operations, an optimizer's step); after others (through `.data` or a raw pointer, of inference
+    tensors, or before a captured graph's replay) call reload().
 
     Calls run on the current stream and use the one workspace: one decoder serves one stream."""
 
@@ -436,8 +440,9 @@ class MoEDecoder:
             raise ValueError("expected router_bias[E] in float32, with a router_weight")
         if not 1 <= k <= E:
             raise ValueError("expected 1 <= k <= E")
-        kept = [up, down, up_scale, down_scale, s_up, s_down, s_us, s_ds, router_weight, router_bias]
-        _on_gpu("MoEDecoder", *kept)
+        given = [up, down, up_scale, down_scale, s_up, s_down, s_us, s_ds, router_weight, router_bias]
+        _on_gpu("MoEDecoder", *given)
+        kept = list(given)
         self._pad = -H % (16 if fp8 else 8)
         if self._pad:  # (the blocks of 128 that have scales stay the same)
             for i, (rows, cols) in {0: (self._pad, 0), 1: (0, self._pad), 4: (self._pad, 0),
@@ -446,6 +451,8 @@ class MoEDecoder:
                     kept[i] = _padded(kept[i], rows, cols)
         kept = [_contiguous(t) for t in kept]
         self._kept = kept
+        self._copies = [(g, t) for g, t in zip(given, kept) if t is not g]
+        self._versions = self._count_updates()
         self._weights = _abi.mm_decode_weights(*[_ptr(t) for t in kept])
         self._weights_at = ctypes.addressof(self._weights)
         self.routes = router_weight is not None
@@ -459,6 +466,18 @@ class MoEDecoder:
         if nbytes == 0:
             raise ValueError(f"unsupported sizes max_tokens={max_tokens} H={H} I={I} E={E} k={k} Is={Is}")
         self._ws = torch.empty(nbytes, dtype=torch.uint8, device=up.device)
+
+    def _count_updates(self):
+        return [0 if g.is_inference() else g._version for g, _ in self._copies]
+
+    @torch.no_grad()
+    def reload(self):
+        """Takes over the present values of the given tensors that the decoder keeps copies of."""
+        self._versions = self._count_updates()
+        for given, copy in self._copies:
+            if given.element_size() == 1:  # 8-bit types have few operations of their own
+                given, copy = given.view(torch.uint8), copy.view(torch.uint8)
+            copy[tuple(slice(n) for n in given.shape)].copy_(given)
 
     def _desc(self, T):
         """(address of the descriptor of a call with T tokens, its workspace bytes)."""
@@ -479,6 +498,8 @@ class MoEDecoder:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens in a decoder for {self.max_tokens}")
+        if self._copies and self._count_updates() != self._versions:
+            self.reload()
         x = torch.nn.functional.pad(x, (0, self._pad)) if self._pad else _contiguous(x)
         y = torch.empty_like(x)
         _abi.check(_abi._lib().mm_decode(

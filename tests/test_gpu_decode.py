@@ -436,3 +436,55 @@ def test_64_bit_ids_out_of_range_are_reported():
         d(m["x"], ids, m["w"])
         assert d.status() == _abi.MM_ERR_BAD_EXPERT_ID, bad
     assert torch.equal(d(m["x"], m["ids"].long(), m["w"]), y)
+
+
+@pytest.mark.parametrize("H,fp8", [(1000, True), (515, False), (512, False), (512, True)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_updates_of_the_weights_take_effect(H, fp8, strided):
+    """Whether the decoder reads the given weights themselves or copies of them (an H that is padded,
+    non-contiguous tensors)."""
+    def spread(t):  # the same values, non-contiguous
+        raw = t.view(torch.uint8) if t.dtype == F8 else t
+        return torch.stack([raw, raw], -1)[..., 0].view(t.dtype) if t.dtype != F8 else \
+            raw.transpose(-1, -2).contiguous().transpose(-1, -2).view(t.dtype)
+
+    m = make(9, H, 64, 8, 2, fp8, shared=32)
+    new = make(9, H, 64, 8, 2, fp8, shared=32, seed=1)
+    new["x"] = m["x"]
+    if strided:
+        m.update({k: spread(m[k]) for k in ("up", "down", "router")})
+    d = decoder(m, route=True)
+    graph = torch.cuda.CUDAGraph()
+    before = d(m["x"])
+    with torch.cuda.graph(graph):
+        captured = d(m["x"])
+    for k in ("up", "down", "us", "ds", "router"):
+        if m[k] is not None:
+            raw = [t.view(torch.uint8) if t.dtype == F8 else t for t in (m[k], new[k])]
+            raw[0].copy_(raw[1])
+    for given, value in zip(m["shared"], new["shared"]):
+        if given is not None:
+            given.view(torch.uint8).copy_(value.view(torch.uint8))
+    want = decoder(new, route=True)(m["x"])
+    assert not torch.equal(before, want)
+    assert torch.equal(d(m["x"]), want)
+    graph.replay()  # (the call before it has renewed what there are copies of)
+    torch.cuda.synchronize()
+    assert torch.equal(captured, want)
+    for t in (m["down"], m["shared"][1]):
+        (t.data.view(torch.uint8) if fp8 else t.data).zero_()  # not counted by autograd
+    d.reload()
+    assert not d(m["x"]).any()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not captured.any()
+
+
+def test_inference_weights_are_reloaded():
+    with torch.inference_mode():
+        m = make(3, 515, 64, 4, 2)
+        d = decoder(m)
+        d(m["x"], m["ids"], m["w"])
+        m["down"].zero_()
+        d.reload()
+        assert not d(m["x"], m["ids"], m["w"]).any()
