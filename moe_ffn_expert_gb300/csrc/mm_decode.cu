@@ -1393,7 +1393,14 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   a.normalize = d->normalize;
   a.scale = d->scale;
   a.route = w->router != nullptr;
-  const int tile = m.T * m.E * m.H <= ((int64_t)2 << 20) + 65536 ? 1 : 4;  // k_logits' N
+  // k_logits' N. One output per block as long as that makes few blocks per SM, whatever H; from there on
+  // the 16 outputs of a block save more reads than they leave SMs idle. A call with 1 and with 4, bf16, H =
+  // 512 / 2048 / 7168, us: 512 outputs (8 tokens of 64 experts) 13.1, 19.3, 38.3 and 13.2, 19.5, 39.3;
+  // 768 (6 of 128) 13.8, 19.5, 38.8 and 13.9, 19.3, 39.2; 1024 (8 of 128) 14.6, 20.0, 39.6 and 14.4,
+  // 19.5, 39.8; 2048 (8 of 256) 15.9, 21.8, 43.0 and 14.8, 20.5, 41.4. One token has no four to read a
+  // router row for: of 1024 experts 19.5, 25.8, 43.8 and 20.1, 26.0, 44.9.
+  const int sms = std::max(1, device_sm_count());
+  const int tile = m.T == 1 || m.T * m.E <= 6 * sms ? 1 : 4;
   la.logit_blocks = a.route ? (int)((m.E + tile - 1) / tile * ((m.T + tile - 1) / tile)) : 0;
   if (fp8) {
     la.x8 = reinterpret_cast<uint8_t*>(ws + l.off_x8);
@@ -1404,7 +1411,6 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
                            ? (tile == 1 ? k_logits<__nv_bfloat16, 1> : k_logits<__nv_bfloat16, 4>)
                            : (tile == 1 ? k_logits<float, 1> : k_logits<float, 4>);
   MM_TRY(launch_pdl(logits, grid, dim3(256), 0, st, la));
-  const int sms = std::max(1, device_sm_count());
   if (a.route && m.T > kMaxRouted) {
     int32_t* ids = topk_ids ? topk_ids : reinterpret_cast<int32_t*>(ws + l.off_ids);
     float* weights = topk_weights ? topk_weights : reinterpret_cast<float*>(ws + l.off_weights);

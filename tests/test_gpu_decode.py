@@ -488,3 +488,14 @@ def test_inference_weights_are_reloaded():
         m["down"].zero_()
         d.reload()
         assert not d(m["x"], m["ids"], m["w"]).any()
+
+
+@pytest.mark.parametrize("H,E", [(136, 128), (2048, 128), (512, 500), (1024, 24)])
+def test_a_token_is_routed_alike_among_any_number(H, E):
+    """The router's product has a form for few outputs and one for many; both add in one order."""
+    m = make(64, H, 16, E, 4)
+    d = decoder(m, route=True)
+    _, ids, w = d.with_routing(m["x"])
+    for T in (1, 2, 7, 8, 12, 13, 33, 48):
+        _, ids_t, w_t = d.with_routing(m["x"][:T].contiguous())
+        assert torch.equal(ids_t, ids[:T]) and torch.equal(w_t, w[:T]), T
