@@ -757,13 +757,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       } else {
         // the chunk's rows of h: one count per GEMM1 unit
         const int target = un.shared ? work.nt1s : work.nt1;
-        int there = 1;
-        if (lane == 0) there = wait_counter(a.ready1 + un.ready, target, kTimeoutNs);
-        if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
+        // (every lane acquires what it will load: a shuffle of lane 0's answer would order no memory)
+        const bool there = wait_counter(a.ready1 + un.ready, target, kTimeoutNs);
+        if (!__all_sync(0xFFFFFFFFu, there)) {
           if (lane == 0) give_up();
           break;
         }
-        __syncwarp();  // (a shuffle orders no memory: lane 0's acquire holds for all from here on)
         fence_proxy_async_global();
         r[0] = (un.row0 + 8 * lane) * PARTS;
       }
@@ -1103,13 +1102,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     for (int task = (warp - kFirstEpilogue) * (int)gridDim.x + (int)blockIdx.x;
          ok && task < a.T * work.nt2; task += 8 * (int)gridDim.x) {
       const int t = div_small(task, work.nt2), tile = task - t * work.nt2, c = tile * kCols + lane * 4;
-      int there = 1;
-      if (lane == 0) there = wait_counter(a.ready2 + tile, target, kTimeoutNs);
-      if (!__shfl_sync(0xFFFFFFFFu, there, 0)) {
+      const bool there = wait_counter(a.ready2 + tile, target, kTimeoutNs);  // every lane, as above
+      if (!__all_sync(0xFFFFFFFFu, there)) {
         if (lane == 0) give_up();
         break;
       }
-      __syncwarp();  // lane 0's acquire holds for all lanes' loads
       if (c >= a.H) continue;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       // part by part, a part's rows in slot order with 8 loads in flight; then the shared expert
