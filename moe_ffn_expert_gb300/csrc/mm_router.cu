@@ -99,6 +99,15 @@ __device__ __forceinline__ float row_max(const float (&z)[NV], int E, int lane) 
   return m == -INFINITY ? 0.f : m;  // a row of -inf: exp(z) is 0 without a shift
 }
 
+// log sum exp of a row with an infinite logit: infinite, or NaN with a NaN beside it.
+template <typename LT>
+__device__ __noinline__ float infinite_sum(const LT* row, int E) {
+  float sum = INFINITY;
+#pragma unroll 1
+  for (int e = 0; e < E; ++e) sum += fabsf(load_logit(row + e));
+  return sum;
+}
+
 // The row's a (in 32 bits up to a common factor, which its uses divide out) and their sum. m: row_max.
 template <int NV>
 __device__ __forceinline__ float row_scores(const float (&z)[NV], float (&x)[NV], int E, int lane,
@@ -171,15 +180,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps) k_router_fwd(RouterArgs a) {
           if (lane * NV + j < E) s += expf(z[j] - m);
         s = warp_sum(s);
       }
-      if (lane == 0) {
-        float lse = m + logf(s);
-        if (m == INFINITY) {  // infinity - infinity: s is NaN, whether a logit is or not
-          lse = INFINITY;
-#pragma unroll 1
-          for (int e = 0; e < E; ++e) lse += fabsf(load_logit(row + e));
-        }
-        a.lse[t] = lse;
-      }
+      if (lane == 0) a.lse[t] = m < INFINITY ? m + logf(s) : infinite_sum(row, E);
     }
     const int id = select_topk<NV>(key, K, lane, &slot[warp][0]);
     const float zs = lane < K ? load_logit(row + id) : 0.f;
