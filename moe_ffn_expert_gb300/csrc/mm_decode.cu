@@ -26,6 +26,11 @@
 // row-major tiles that TMA brings (MN-major descriptors), and the chunk's rows as N: 16 or 32
 // columns of the accumulator instead of 128 rows of padding. No thread touches a weight.
 //
+// h goes from the first product to the second as the sum of two bf16 parts, each a column of N of its
+// own, so that y's rounding is the only one to 16 bits: y is off by 1.67e-3 in the mean square, as the
+// rounded exact y is (one part: 2.36e-3). The second product's N is up to 64 and a stage's rows take twice
+// the room, for one stage of weights fewer: 64 tokens of 128 experts 182.6 us, 181.0 with one part.
+//
 // e4m3 weights meet 16-bit activations: tensor cores take either both in 8 bits or both in 16.
 // A bf16 number is the exact sum of two e4m3 numbers, x s = hi + lo / 16 (4 significant bits
 // each, s a power of two per row that keeps the row's largest value below 256; what lies 2^-22
@@ -76,14 +81,15 @@ struct Cfg {
   static constexpr int BLOCKS = FP8 ? 2 : 1;
   static constexpr int KB2 = KB * BLOCKS;             // k per stage of GEMM2
   static constexpr int A_BYTES = BLOCKS * kTileBytes;
-  static constexpr int B_BYTES = BLOCKS * 32 * 128;   // rows (e4m3: hi and lo parts)
-  static constexpr int STAGES = FP8 ? 4 : 8;
+  // rows, GEMM2's and (e4m3) GEMM1's in two parts
+  static constexpr int B_BYTES = BLOCKS * 2 * CHUNK * 128;
+  static constexpr int STAGES = FP8 ? 4 : 7;
   // columns of h that a GEMM1 unit makes. bf16: 64, from stages of 64 gate + 64 up columns. e4m3:
   // 128, so that a block is one box of whole 128-byte lines: two boxes of 64 bytes a row stream at
   // 6.3 TB/s, one of 128 at 7.1.
   static constexpr int H_COLS = FP8 ? 128 : 64;
   // Accumulators in tensor memory, a ring per epilogue set. bf16: an accumulator per unit (of 32
-  // columns; the other 32 unused). e4m3: one per stage, 32 columns (hi and lo parts of 16 rows) per
+  // columns in GEMM1, 64 in GEMM2). e4m3: one per stage, 32 columns (hi and lo parts of 16 rows) per
   // block.
   static constexpr int SLOT_COLS = 64;
   static constexpr int RING = 512 / SLOT_COLS / 2;
@@ -95,7 +101,7 @@ enum { W_STATUS = 0, W_NEXT = 1, W_READY1 = 64 };
 struct DecodeArgs {
   CUtensorMap up, down, s_up, s_down;  // weights, boxes of 128 bytes x 64 (e4m3: 128) rows
   CUtensorMap x;                       // token rows (e4m3: hi and lo parts in turn), one per box
-  CUtensorMap h_rows, s_h_rows;        // rows of h (the same), 8 (16 parts) per box
+  CUtensorMap h_rows, s_h_rows;        // rows of h (hi and lo parts in turn), 8 (16 parts) per box
   const float *up_scale, *down_scale, *s_up_scale, *s_down_scale;
   const float* logits;    // with a router
   const float* bias;
@@ -104,7 +110,7 @@ struct DecodeArgs {
   __nv_bfloat16* y;
   int* hdr;
   int *ready1, *ready2;
-  void *h, *s_h;           // bf16 [S, I], [T, Is]; e4m3: [S, 2, I], [T, 2, Is]
+  void *h, *s_h;           // [S, 2, I], [T, 2, Is]: hi and lo parts
   const float* x_scale;    // e4m3: [T]
   float *h_scale, *s_h_scale;  // e4m3: [chunk][ceil(I / 128)][16]
   float *o, *s_o;          // [split][S, H], [split][T, H]
@@ -179,6 +185,11 @@ __device__ __forceinline__ void split_e4m3(float xs, uint8_t& hi, uint8_t& lo) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(hi, __NV_E4M3);
   const float back = __half2float(*reinterpret_cast<const __half*>(&h));
   lo = __nv_cvt_float_to_fp8((xs - back) * 16.f, __NV_SATFINITE, __NV_E4M3);
+}
+
+// What a rounded part leaves of a value: nothing of an infinity or a NaN.
+__device__ __forceinline__ float rest_of(float v, float part) {
+  return fabsf(part) <= 3.4e38f ? v - part : 0.f;
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint8_t* b) {
@@ -743,8 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       taken(qi);
       if (un.kind < 0) break;
       const CUtensorMap* map = un.kind == 0 ? &a.x : un.shared ? &a.s_h_rows : &a.h_rows;
-      // a lane loads 4 rows of x by number (e4m3: hi and lo parts of 2) or 8 consecutive rows of h
-      // (e4m3: 16, hi and lo in turn)
+      // a lane loads 4 rows of x by number (e4m3: hi and lo parts of 2) or the hi and lo parts, in
+      // turn, of 8 consecutive rows of h
       constexpr int PARTS = FP8 ? 2 : 1, X_ROWS = 4 / PARTS;
       const int groups = un.kind == 0 ? (un.n + X_ROWS - 1) / X_ROWS : (un.n + 7) / 8;
       int r[4] = {0, 0, 0, 0};
@@ -764,9 +775,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           break;
         }
         fence_proxy_async_global();
-        r[0] = (un.row0 + 8 * lane) * PARTS;
+        r[0] = (un.row0 + 8 * lane) * 2;
       }
-      const uint32_t lane_bytes = un.kind == 0 ? 512 : PARTS * 1024;
+      const uint32_t lane_bytes = un.kind == 0 ? 512 : 2048;
       const uint32_t bytes = groups * lane_bytes * (un.kind == 0 ? 1 : C::BLOCKS);
       const uint32_t to = rows_at + lane * lane_bytes;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
@@ -812,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const int rows = uniform(entry->n);
       taken(qi);
       if (kind < 0) break;
-      const uint32_t n = ((FP8 ? 2 * rows : rows) + 15) & ~15;  // the chunk's rows
+      const uint32_t n = ((FP8 || kind == 1 ? 2 * rows : rows) + 15) & ~15;  // the chunk's rows or their parts
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
       const int set = qi & 1;
       uint32_t d = 0;
@@ -937,10 +948,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
 #pragma unroll 1
         for (int j = 0; j < n8; j += 8) {
-          uint32_t r[8];
-          tmem_ld_32x8(d + j, r);
-          tmem_ld_wait();
-          emit(reinterpret_cast<const float*>(r), j);
+          float v[8];
+          if (un.kind == 0) {
+            uint32_t r[8];
+            tmem_ld_32x8(d + j, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+          } else {  // hi and lo parts of the rows in turn
+            uint32_t r[16];
+            tmem_ld_32x16(d + 2 * j, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[2 * i]) + __uint_as_float(r[2 * i + 1]);
+          }
+          emit(v, j);
         }
         tc_fence_before();
         __syncwarp();
@@ -1084,10 +1106,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           const float w = un.shared ? 1.f : tb.w[row];
           const float2 g = *reinterpret_cast<const float2*>(x + 2 * lane);
           const float2 l = *reinterpret_cast<const float2*>(x + 64 + 2 * lane);
-          if (c < I)
-            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(un.shared ? a.s_h : a.h) +
-                                         (int64_t)row * I + c) =
-                pack_bf16(w * (g.x * sigmoidf_(g.x) * l.x), w * (g.y * sigmoidf_(g.y) * l.y));
+          if (c < I) {
+            uint32_t* const dst = reinterpret_cast<uint32_t*>(
+                static_cast<__nv_bfloat16*>(un.shared ? a.s_h : a.h) + (int64_t)row * 2 * I + c);
+            const float h0 = w * (g.x * sigmoidf_(g.x) * l.x), h1 = w * (g.y * sigmoidf_(g.y) * l.y);
+            const uint32_t hi = pack_bf16(h0, h1);
+            dst[0] = hi;
+            dst[I / 2] = pack_bf16(rest_of(h0, bf16_lo(hi)), rest_of(h1, bf16_hi(hi)));
+          }
         }
       }
       fence_proxy_async_global();
@@ -1241,8 +1267,8 @@ Layout layout(const mm_decode_desc& d) {
   constexpr int chunk = Cfg<true>::CHUNK;
   l.off_hs = take(fp8 ? S * ((m.I + 127) / 128) * chunk * 4 : 0);
   l.off_shs = take(fp8 ? (size_t)(kMaxT / chunk) * ((d.shared_I + 127) / 128) * chunk * 4 : 0);
-  l.off_h = take(S * m.I * 2);
-  l.off_sh = take((size_t)m.T * d.shared_I * 2);
+  l.off_h = take(S * m.I * 2 * (fp8 ? 1 : 2));
+  l.off_sh = take((size_t)m.T * d.shared_I * 2 * (fp8 ? 1 : 2));
   l.off_o = take((size_t)kMaxSplit * S * m.H * 4);
   l.off_so = take(d.shared_I > 0 ? (size_t)kMaxSplit * m.T * m.H * 4 : 0);
   l.total = off;
@@ -1350,15 +1376,15 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   la.E = (int)m.E;
   DecodeArgs a{};
   char* const x_rows = fp8 ? ws + l.off_x8 : static_cast<char*>(const_cast<void*>(x));
-  const int64_t parts = fp8 ? 2 : 1;  // hi and lo
+  const int64_t parts = fp8 ? 2 : 1;  // of x
   bool maps = weight_map(&a.up, w->up, 2 * m.I, m.H, m.E, fp8) &&
               weight_map(&a.down, w->down, m.H, m.I, m.E, fp8) &&
               row_map(&a.x, x_rows, m.H, parts * m.T, fp8, 1) &&
-              row_map(&a.h_rows, ws + l.off_h, m.I, parts * m.T * m.K, fp8, 8 * parts);
+              row_map(&a.h_rows, ws + l.off_h, m.I, 2 * m.T * m.K, fp8, 16);
   if (shared)
     maps = maps && weight_map(&a.s_up, w->shared_up, 2 * d->shared_I, m.H, 1, fp8) &&
            weight_map(&a.s_down, w->shared_down, m.H, d->shared_I, 1, fp8) &&
-           row_map(&a.s_h_rows, ws + l.off_sh, d->shared_I, parts * m.T, fp8, 8 * parts);
+           row_map(&a.s_h_rows, ws + l.off_sh, d->shared_I, 2 * m.T, fp8, 16);
   if (!maps) return cuda_fail(cudaErrorInvalidValue, "decode tensor maps");
   a.up_scale = w->up_scale;
   a.down_scale = w->down_scale;

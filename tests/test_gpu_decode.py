@@ -499,3 +499,25 @@ def test_a_token_is_routed_alike_among_any_number(H, E):
     for T in (1, 2, 7, 8, 12, 13, 33, 48):
         _, ids_t, w_t = d.with_routing(m["x"][:T].contiguous())
         assert torch.equal(ids_t, ids[:T]) and torch.equal(w_t, w[:T]), T
+
+
+@pytest.mark.parametrize("T,H,I,E,K,shared", [(1, 512, 64, 4, 2, 0), (7, 264, 72, 6, 2, 40), (33, 256, 128, 2, 1, 64),
+                                              (64, 512, 128, 8, 2, 0), (64, 136, 64, 1, 1, 0)])
+def test_only_the_output_is_rounded_to_16_bits(T, H, I, E, K, shared):
+    """w h goes into the second product in two bf16 parts, 2^-18 of it left out. With the sums of both
+    products in 32 bits (below 1e-5 of their terms' magnitudes each), 3e-5 of the magnitudes and the
+    rounding of y bound the error. A single bf16 w h leaves 2^-9 / sqrt(3) of the root of the sum of
+    squares, some times that where y is small."""
+    m = make(T, H, I, E, K, shared=shared)
+    y = decoder(m)(m["x"], m["ids"], m["w"])
+    x, ids, w = m["x"].double(), m["ids"].long(), m["w"].double()
+    want, ab = torch.zeros_like(x), torch.zeros_like(x)
+    for e in range(E):
+        t, k = (ids == e).nonzero(as_tuple=True)
+        o, _, a = ffn(x[t], m["up"][e].double(), m["down"][e].double())
+        want.index_add_(0, t, w[t, k][:, None] * o)
+        ab.index_add_(0, t, w[t, k][:, None] * a)
+    if shared:
+        o, _, a = ffn(x, m["shared"][0].double(), m["shared"][1].double())
+        want, ab = want + o, ab + a
+    assert ((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + 3e-5 * ab).all()
