@@ -135,9 +135,10 @@ mm_status mm_router_backward(const mm_router_desc* d, const void* logits, const 
  *   logits = x router^T (fp32), selection and weights as the router above (or the caller's ids
  *   and weights), y_t = sum_k w_tk o_tk + o_shared_t with o = (silu(x Wg) * (x Wu)) Wd. Products
  *   and sums are in 32 bits, y is rounded once. Between the two products, w * h is kept as the sum
- *   of two bf16 numbers (16 significant bits); with e4m3 weights x and w * h as the sum of two e4m3
- *   numbers times a power of two (of a row of x; of a row and 128 columns of h): 8 significant bits
- *   of every value down to 2^-14 of the row's largest, in steps of 2^-21 of the largest below that.
+ *   of two bf16 numbers (16 significant bits). With e4m3 weights x is the sum of two e4m3 numbers
+ *   and w * h of three, times a power of two (of a row of x; of a row and 128 columns of h): 8 (12)
+ *   significant bits of every value down to 2^-13 of the row's (its 128 columns') largest, in steps
+ *   of at most 2^-20 (2^-24) of the largest below that.
  * Every selected expert's weights are read once per 32 (e4m3: 16) of its tokens.
  *
  * weight_type MM_BF16: up bf16 [E, H, 2I], down bf16 [E, I, H] as in mm.h; H, I, shared_I multiples

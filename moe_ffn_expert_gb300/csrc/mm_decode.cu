@@ -33,11 +33,13 @@
 //
 // e4m3 weights meet 16-bit activations: tensor cores take either both in 8 bits or both in 16.
 // A bf16 number is the exact sum of two e4m3 numbers, x s = hi + lo / 16 (4 significant bits
-// each, s a power of two per row that keeps the row's largest value below 256; what lies 2^-22
+// each, s a power of two per row that keeps the row's largest value below 256; what lies 2^-20
 // below that is rounded), so both halves of every row are columns of N and the accumulator's two
 // columns are added: twice the columns, no conversion of the weights, which outnumber the rows'
 // elements many times. The products of 128 x 128 blocks are scaled in 32 bits as they leave the
-// tensor memory. h is split the same way, with a scale per row and 128 columns.
+// tensor memory. h, which has more bits than a bf16 number, is split the same way into three parts
+// (2^-12 of a value is left out), with a scale per row and 128 columns: y is off by 1.66e-3, the rounding
+// of y, where two parts left 1.77e-3, in the same time.
 //
 // Measured (device time of a call; the floor is the hit experts' bytes at a plain copy's rate):
 // 128 experts of 2048 x 768, top-8, bf16: 64 tokens 182 us, 6.5 TB/s (floor 175); 8 tokens 76 (72);
@@ -81,16 +83,17 @@ struct Cfg {
   static constexpr int BLOCKS = FP8 ? 2 : 1;
   static constexpr int KB2 = KB * BLOCKS;             // k per stage of GEMM2
   static constexpr int A_BYTES = BLOCKS * kTileBytes;
-  // rows, GEMM2's and (e4m3) GEMM1's in two parts
-  static constexpr int B_BYTES = BLOCKS * 2 * CHUNK * 128;
+  // parts of a row of x and of h (see above), and the rows of a stage: the larger of the two
+  static constexpr int X_PARTS = FP8 ? 2 : 1, H_PARTS = FP8 ? 3 : 2;
+  static constexpr int B_BYTES = BLOCKS * H_PARTS * CHUNK * 128;
   static constexpr int STAGES = FP8 ? 4 : 7;
   // columns of h that a GEMM1 unit makes. bf16: 64, from stages of 64 gate + 64 up columns. e4m3:
   // 128, so that a block is one box of whole 128-byte lines: two boxes of 64 bytes a row stream at
   // 6.3 TB/s, one of 128 at 7.1.
   static constexpr int H_COLS = FP8 ? 128 : 64;
-  // Accumulators in tensor memory, a ring per epilogue set. bf16: an accumulator per unit (of 32
-  // columns in GEMM1, 64 in GEMM2). e4m3: one per stage, 32 columns (hi and lo parts of 16 rows) per
-  // block.
+  // Accumulators in tensor memory, a ring per epilogue set. bf16: a slot per unit (32 columns in GEMM1,
+  // 64 in GEMM2). e4m3: a slot per stage in GEMM1 (32 columns, the parts of 16 rows, for each block),
+  // one per block in GEMM2 (48 columns).
   static constexpr int SLOT_COLS = 64;
   static constexpr int RING = 512 / SLOT_COLS / 2;
 };
@@ -101,7 +104,7 @@ enum { W_STATUS = 0, W_NEXT = 1, W_READY1 = 64 };
 struct DecodeArgs {
   CUtensorMap up, down, s_up, s_down;  // weights, boxes of 128 bytes x 64 (e4m3: 128) rows
   CUtensorMap x;                       // token rows (e4m3: hi and lo parts in turn), one per box
-  CUtensorMap h_rows, s_h_rows;        // rows of h (hi and lo parts in turn), 8 (16 parts) per box
+  CUtensorMap h_rows, s_h_rows;        // rows of h (their parts in turn), 8 per box
   const float *up_scale, *down_scale, *s_up_scale, *s_down_scale;
   const float* logits;    // with a router
   const float* bias;
@@ -110,7 +113,7 @@ struct DecodeArgs {
   __nv_bfloat16* y;
   int* hdr;
   int *ready1, *ready2;
-  void *h, *s_h;           // [S, 2, I], [T, 2, Is]: hi and lo parts
+  void *h, *s_h;           // [S, parts, I], [T, parts, Is]
   const float* x_scale;    // e4m3: [T]
   float *h_scale, *s_h_scale;  // e4m3: [chunk][ceil(I / 128)][16]
   float *o, *s_o;          // [split][S, H], [split][T, H]
@@ -179,12 +182,18 @@ struct Walk {
   }
 };
 
-// x = (hi + lo / 16) / s for |x s| < 256.
-__device__ __forceinline__ void split_e4m3(float xs, uint8_t& hi, uint8_t& lo) {
-  hi = __nv_cvt_float_to_fp8(xs, __NV_SATFINITE, __NV_E4M3);
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(hi, __NV_E4M3);
-  const float back = __half2float(*reinterpret_cast<const __half*>(&h));
-  lo = __nv_cvt_float_to_fp8((xs - back) * 16.f, __NV_SATFINITE, __NV_E4M3);
+// The e4m3 part of a value below 256, which becomes 16 times what is left of it (below 256 again):
+// v = hi + lo / 16 (+ lo2 / 256).
+__device__ __forceinline__ uint8_t take_e4m3(float& v) {
+  const uint8_t part = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(part, __NV_E4M3);
+  v = (v - __half2float(*reinterpret_cast<const __half*>(&h))) * 16.f;
+  return part;
+}
+
+// hi + lo / 16 of two parts' products.
+__device__ __forceinline__ float whole(uint32_t hi, uint32_t lo) {
+  return fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi));
 }
 
 // What a rounded part leaves of a value: nothing of an infinity or a NaN.
@@ -251,7 +260,11 @@ __device__ void split_row(const LogitArgs& a, int t, float* red) {
     load_vec<8>(row + c, v);
     uint8_t h[8], l[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) split_e4m3(v[k] * s, h[k], l[k]);
+    for (int k = 0; k < 8; ++k) {
+      float rest = v[k] * s;
+      h[k] = take_e4m3(rest);
+      l[k] = take_e4m3(rest);
+    }
     *reinterpret_cast<uint2*>(hi + c) = make_uint2(word_of(h), word_of(h + 4));
     *reinterpret_cast<uint2*>(lo + c) = make_uint2(word_of(l), word_of(l + 4));
   }
@@ -754,9 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       taken(qi);
       if (un.kind < 0) break;
       const CUtensorMap* map = un.kind == 0 ? &a.x : un.shared ? &a.s_h_rows : &a.h_rows;
-      // a lane loads 4 rows of x by number (e4m3: hi and lo parts of 2) or the hi and lo parts, in
-      // turn, of 8 consecutive rows of h
-      constexpr int PARTS = FP8 ? 2 : 1, X_ROWS = 4 / PARTS;
+      // a lane loads 4 rows of x by number (e4m3: both parts of 2) or the parts of 8 consecutive rows
+      // of h
+      constexpr int PARTS = C::X_PARTS, X_ROWS = 4 / PARTS;
       const int groups = un.kind == 0 ? (un.n + X_ROWS - 1) / X_ROWS : (un.n + 7) / 8;
       int r[4] = {0, 0, 0, 0};
       if (un.kind == 0) {
@@ -775,9 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           break;
         }
         fence_proxy_async_global();
-        r[0] = (un.row0 + 8 * lane) * 2;
+        r[0] = (un.row0 + 8 * lane) * C::H_PARTS;
       }
-      const uint32_t lane_bytes = un.kind == 0 ? 512 : 2048;
+      const uint32_t lane_bytes = un.kind == 0 ? 512 : C::H_PARTS * 1024;
       const uint32_t bytes = groups * lane_bytes * (un.kind == 0 ? 1 : C::BLOCKS);
       const uint32_t to = rows_at + lane * lane_bytes;
       for (int kb = un.kb0; kb < un.kb1; ++kb, ++it) {
@@ -823,14 +836,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       const int rows = uniform(entry->n);
       taken(qi);
       if (kind < 0) break;
-      const uint32_t n = ((FP8 || kind == 1 ? 2 * rows : rows) + 15) & ~15;  // the chunk's rows or their parts
+      const uint32_t n = ((kind == 0 ? C::X_PARTS : C::H_PARTS) * rows + 15) & ~15;  // parts of the chunk's rows
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, n, 1, 0) : idesc_bf16_f32(128, n, 1, 0);
       const int set = qi & 1;
-      uint32_t d = 0;
-      auto next_slot = [&] {  // the next accumulator of `set`, free
+      uint32_t d[2] = {0, 0};  // of the two blocks
+      int slot[2] = {0, 0};
+      auto next_slot = [&](int p) {  // the next accumulator of `set`, free
         Walk<RING>& w = set ? accs[1] : accs[0];
         if (w.wait()) {
-          d = tmem + (set * RING + w.s) * C::SLOT_COLS;
+          slot[p] = w.s;
+          d[p] = tmem + (set * RING + w.s) * C::SLOT_COLS;
           tc_fence_after();
           return true;
         }
@@ -842,9 +857,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         w.ask_next();
         w.next();
       };
-      if (!FP8 && !next_slot()) break;
+      if (!FP8 && !next_slot(0)) break;
       for (int i = 0; i < blocks; ++i) {
-        if (FP8 && !next_slot()) break;
+        if (FP8) {
+          if (!next_slot(0)) break;
+          d[1] = d[0] + C::SLOT_COLS / 2;
+          if (kind == 1) {
+            slot_done();
+            if (!next_slot(1)) break;
+          }
+        }
         if (!ring.wait()) {
           if (lane == 0) give_up();
           ok = false;
@@ -861,12 +883,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             const int p = i4 / 4, ks = i4 % 4;
             const uint64_t wk = wd + i4 * ((FP8 ? 4096 : 2048) / 16), bk = bd + ks * 2 + p * b_half;
             if constexpr (FP8)
-              umma_e4m3(d + p * (C::SLOT_COLS / 2), wk, bk, idesc, ks == 0 ? 0u : 1u);
+              umma_e4m3(d[p], wk, bk, idesc, ks == 0 ? 0u : 1u);
             else
-              umma_bf16(d, wk, bk, idesc, i == 0 && ks == 0 ? 0u : 1u);
+              umma_bf16(d[0], wk, bk, idesc, i == 0 && ks == 0 ? 0u : 1u);
           }
           umma_commit(empty(ring.s));
-          if (FP8 || i + 1 == blocks) umma_commit(acc_full(set, (set ? accs[1] : accs[0]).s));
+          if (FP8 || i + 1 == blocks) umma_commit(acc_full(set, slot[0]));
+          if (FP8 && kind == 1) umma_commit(acc_full(set, slot[1]));
         }
         __syncwarp();
         ring.next();
@@ -1026,25 +1049,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
               if (kb == un.kb0) hs = row_scale(kb);
               if (kb + 1 < un.kb1) next_hs = row_scale(kb + 1);
             }
-            const uint32_t d = tmem_q + acc % RING * C::SLOT_COLS;
+            auto release = [&] {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
+            };
+            if (up) {  // both parts of the rows in turn, both blocks in one slot
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t r[16 * G];  // hi and lo parts of the rows in turn
+              for (int half = 0; half < 2; ++half) {
+                uint32_t r[16 * G];
 #pragma unroll
-              for (int j = 0; j < 2 * G; ++j)
-                tmem_ld_32x8(d + half * (C::SLOT_COLS / 2) + 8 * j, *reinterpret_cast<uint32_t(*)[8]>(r + 8 * j));
-              tmem_ld_wait();
+                for (int j = 0; j < 2 * G; ++j)
+                  tmem_ld_32x8(tmem_q + acc % RING * C::SLOT_COLS + half * (C::SLOT_COLS / 2) + 8 * j,
+                               *reinterpret_cast<uint32_t(*)[8]>(r + 8 * j));
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 8 * G; ++i) {
-                const float p = fmaf(__uint_as_float(r[2 * i + 1]), 0.0625f, __uint_as_float(r[2 * i]));
-                const float rs = up ? 1.f : __shfl_sync(0xFFFFFFFFu, hs, half * C::CHUNK + i);
-                v[half][i] = fmaf(ws[half] * rs, p, v[half][i]);
+                for (int i = 0; i < 8 * G; ++i)
+                  v[half][i] = fmaf(ws[half], whole(r[2 * i], r[2 * i + 1]), v[half][i]);
+              }
+            } else {  // three parts, a slot per block
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                if (half == 1) {
+                  release();
+                  ++acc;
+                  if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
+                  tc_fence_after();
+                }
+                uint32_t r[24 * G];
+#pragma unroll
+                for (int j = 0; j < 3 * G; ++j)
+                  tmem_ld_32x8(tmem_q + acc % RING * C::SLOT_COLS + 8 * j,
+                               *reinterpret_cast<uint32_t(*)[8]>(r + 8 * j));
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8 * G; ++i) {
+                  const float rest = whole(r[3 * i + 1], r[3 * i + 2]);
+                  const float rs = __shfl_sync(0xFFFFFFFFu, hs, half * C::CHUNK + i);
+                  v[half][i] = fmaf(ws[half] * rs, whole(r[3 * i], __float_as_uint(rest)), v[half][i]);
+                }
               }
             }
             hs = next_hs;
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
+            release();
           }
           if (!up) {
 #pragma unroll
@@ -1087,15 +1134,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
           if (h.x != h.x || h.y != h.y || h.z != h.z || h.w != h.w) m = INFINITY;
           float inv;
           const float s = split_scale(warp_max(m), &inv);
-          uint8_t hi[4], lo[4];
-          split_e4m3(h.x * s, hi[0], lo[0]);
-          split_e4m3(h.y * s, hi[1], lo[1]);
-          split_e4m3(h.z * s, hi[2], lo[2]);
-          split_e4m3(h.w * s, hi[3], lo[3]);
-          uint8_t* dst = static_cast<uint8_t*>(un.shared ? a.s_h : a.h) + (int64_t)row * 2 * I + c;
+          uint8_t part[C::H_PARTS][4];
+          const float hs[4] = {h.x * s, h.y * s, h.z * s, h.w * s};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float rest = hs[j];
+#pragma unroll
+            for (int k = 0; k < C::H_PARTS; ++k) part[k][j] = take_e4m3(rest);
+          }
+          uint8_t* dst = static_cast<uint8_t*>(un.shared ? a.s_h : a.h) + (int64_t)row * C::H_PARTS * I + c;
           if (c < I) {
-            *reinterpret_cast<uint32_t*>(dst) = word_of(hi);
-            *reinterpret_cast<uint32_t*>(dst + I) = word_of(lo);
+#pragma unroll
+            for (int k = 0; k < C::H_PARTS; ++k)
+              *reinterpret_cast<uint32_t*>(dst + (int64_t)k * I) = word_of(part[k]);
           }
           const int nt = (I + 127) / 128;
           if (lane == 0)
@@ -1267,8 +1318,9 @@ Layout layout(const mm_decode_desc& d) {
   constexpr int chunk = Cfg<true>::CHUNK;
   l.off_hs = take(fp8 ? S * ((m.I + 127) / 128) * chunk * 4 : 0);
   l.off_shs = take(fp8 ? (size_t)(kMaxT / chunk) * ((d.shared_I + 127) / 128) * chunk * 4 : 0);
-  l.off_h = take(S * m.I * 2 * (fp8 ? 1 : 2));
-  l.off_sh = take((size_t)m.T * d.shared_I * 2 * (fp8 ? 1 : 2));
+  const size_t h_bytes = fp8 ? Cfg<true>::H_PARTS : 2 * Cfg<false>::H_PARTS;
+  l.off_h = take(S * m.I * h_bytes);
+  l.off_sh = take((size_t)m.T * d.shared_I * h_bytes);
   l.off_o = take((size_t)kMaxSplit * S * m.H * 4);
   l.off_so = take(d.shared_I > 0 ? (size_t)kMaxSplit * m.T * m.H * 4 : 0);
   l.total = off;
@@ -1376,15 +1428,16 @@ mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const v
   la.E = (int)m.E;
   DecodeArgs a{};
   char* const x_rows = fp8 ? ws + l.off_x8 : static_cast<char*>(const_cast<void*>(x));
-  const int64_t parts = fp8 ? 2 : 1;  // of x
+  const int64_t parts = fp8 ? Cfg<true>::X_PARTS : Cfg<false>::X_PARTS;
+  const int64_t h_parts = fp8 ? Cfg<true>::H_PARTS : Cfg<false>::H_PARTS;
   bool maps = weight_map(&a.up, w->up, 2 * m.I, m.H, m.E, fp8) &&
               weight_map(&a.down, w->down, m.H, m.I, m.E, fp8) &&
               row_map(&a.x, x_rows, m.H, parts * m.T, fp8, 1) &&
-              row_map(&a.h_rows, ws + l.off_h, m.I, 2 * m.T * m.K, fp8, 16);
+              row_map(&a.h_rows, ws + l.off_h, m.I, h_parts * m.T * m.K, fp8, 8 * h_parts);
   if (shared)
     maps = maps && weight_map(&a.s_up, w->shared_up, 2 * d->shared_I, m.H, 1, fp8) &&
            weight_map(&a.s_down, w->shared_down, m.H, d->shared_I, 1, fp8) &&
-           row_map(&a.s_h_rows, ws + l.off_sh, d->shared_I, 2 * m.T, fp8, 16);
+           row_map(&a.s_h_rows, ws + l.off_sh, d->shared_I, h_parts * m.T, fp8, 8 * h_parts);
   if (!maps) return cuda_fail(cudaErrorInvalidValue, "decode tensor maps");
   a.up_scale = w->up_scale;
   a.down_scale = w->down_scale;

@@ -521,3 +521,38 @@ def test_only_the_output_is_rounded_to_16_bits(T, H, I, E, K, shared):
         o, _, a = ffn(x, m["shared"][0].double(), m["shared"][1].double())
         want, ab = want + o, ab + a
     assert ((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + 3e-5 * ab).all()
+
+
+@pytest.mark.parametrize("T,H,I,E,K,shared", [(1, 512, 64, 4, 2, 0), (7, 272, 80, 6, 2, 48), (33, 256, 128, 2, 1, 64),
+                                              (64, 512, 128, 8, 2, 0), (64, 144, 64, 1, 1, 0)])
+def test_e4m3_weights_meet_more_than_eight_bits_of_h(T, H, I, E, K, shared):
+    """w h goes into the second product in three e4m3 parts, each of which leaves at most 2^-4 of what it is
+    a part of: 2^-12 of a value. Independent errors of that size add up to 2^-12 / sqrt(3) of the root of
+    the terms' sum of squares, six times that is allowed; the sums and y's rounding as above."""
+    m = make(T, H, I, E, K, True, shared=shared)
+    y = decoder(m)(m["x"], m["ids"], m["w"])
+    want, _ = reference(m)
+    sq, ab = (torch.zeros_like(want) for _ in range(2))
+    x, ids, w = m["x"].double(), m["ids"].long(), m["w"].double()
+    for e in range(E):
+        t, k = (ids == e).nonzero(as_tuple=True)
+        _, s, a = ffn(x[t], values(m["up"][e:e + 1], m["us"][e:e + 1])[0], values(m["down"][e:e + 1], m["ds"][e:e + 1])[0])
+        sq.index_add_(0, t, w[t, k][:, None].square() * s)
+        ab.index_add_(0, t, w[t, k][:, None] * a)
+    if shared:
+        su, sd, sus, sds = m["shared"]
+        _, s, a = ffn(x, values(su[None], sus[None])[0], values(sd[None], sds[None])[0])
+        sq, ab = sq + s, ab + a
+    tol = 2.0 ** -8 * want.abs() + 3.5 * 2.0 ** -12 * sq.sqrt() + 3e-5 * ab
+    assert ((y.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T", [1, 16, 40])
+def test_rows_with_a_few_large_channels_and_e4m3_weights(T):
+    """Values of x down to 2^-13 of their row's largest keep their 8 bits, smaller ones are off by 2^-21 of
+    the largest at most, which the sums' 1e-5 of the magnitudes of the row's terms covers: the largest is
+    one of them. Channels of 2^10 and 2^18 times the others, whose weights are as large as any."""
+    for factor in (2.0 ** 10, 2.0 ** 18):
+        m = make(T, 512, 128, 8, 2, True, shared=64)
+        m["x"][:, 7::100] *= factor
+        check(m)
