@@ -44,6 +44,12 @@ def _contiguous(t):
     return t if t is None or t.is_contiguous() else t.contiguous()
 
 
+def _aligned(t):
+    """A contiguous tensor on a 16-byte boundary, as TMA wants it: `t` itself if it is one."""
+    t = _contiguous(t)
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _type(name, t):
     try:
         return _TYPE[t.dtype]
@@ -359,7 +365,7 @@ def quantize_expert_weights(w):
             return quantize_expert_weights(w)
     if w.dim() < 2 or w.dtype != torch.bfloat16 or not w.is_cuda:
         raise ValueError("expected bfloat16 matrices [..., R, C] on a CUDA device")
-    w = w.contiguous()
+    w = _aligned(w)
     *lead, R, C = w.shape
     n = w.numel() // (R * C) if R * C else 0
     q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
@@ -386,8 +392,8 @@ class MoEDecoder:
     down [Is,H]) of a shared expert, and their two scales for 8-bit weights (or None, None).
 
     The decoder reads the given tensors in every call, so that updates of the weights take effect in
-    the next one. Two kinds it has to copy: non-contiguous ones, and, as mm_decode takes H in multiples
-    of 8 (8-bit weights: 16), those of another H, with zeros up to the next multiple (x is padded and y
+    the next one. Two kinds it has to copy: tensors that are not contiguous (matrices: from a 16-byte
+    boundary on), and, as mm_decode takes H in multiples of 8 (8-bit weights: 16), those of another H, with zeros up to the next multiple (x is padded and y
     cut in every call). A call takes over the updates of copied tensors that autograd counts (in-place
     operations, an optimizer's step); after others (through `.data` or a raw pointer, of inference
     tensors, or before a captured graph's replay) call reload().
@@ -449,7 +455,7 @@ class MoEDecoder:
                                     5: (0, self._pad), 8: (0, self._pad)}.items():
                 if kept[i] is not None:
                     kept[i] = _padded(kept[i], rows, cols)
-        kept = [_contiguous(t) for t in kept]
+        kept = [_aligned(t) if i in (0, 1, 4, 5, 8) else _contiguous(t) for i, t in enumerate(kept)]
         self._kept = kept
         self._copies = [(g, t) for g, t in zip(given, kept) if t is not g]
         self._versions = self._count_updates()
@@ -500,7 +506,7 @@ class MoEDecoder:
             raise ValueError(f"{T} tokens in a decoder for {self.max_tokens}")
         if self._copies and self._count_updates() != self._versions:
             self.reload()
-        x = torch.nn.functional.pad(x, (0, self._pad)) if self._pad else _contiguous(x)
+        x = torch.nn.functional.pad(x, (0, self._pad)) if self._pad else _aligned(x)
         y = torch.empty_like(x)
         _abi.check(_abi._lib().mm_decode(
             self._desc(T)[0], self._weights_at, x.data_ptr(), _ptr(ids), _ptr(weights), y.data_ptr(),

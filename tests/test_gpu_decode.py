@@ -556,3 +556,23 @@ def test_rows_with_a_few_large_channels_and_e4m3_weights(T):
         m = make(T, 512, 128, 8, 2, True, shared=64)
         m["x"][:, 7::100] *= factor
         check(m)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tensors_off_a_16_byte_boundary(fp8):
+    def odd(t):
+        raw = t.view(torch.uint8) if t.dtype == F8 else t
+        buf = torch.empty(raw.numel() + 1, dtype=raw.dtype, device="cuda")
+        return buf[1:].view(raw.shape).copy_(raw).view(t.dtype)
+
+    m = make(5, 256, 64, 8, 2, fp8)
+    y = decoder(m)(m["x"], m["ids"], m["w"])
+    n = {k: odd(v) if isinstance(v, torch.Tensor) else v for k, v in m.items()}
+    assert n["x"].data_ptr() % 16 and n["up"].data_ptr() % 16
+    d = decoder(n)
+    assert torch.equal(d(n["x"], n["ids"], n["w"]), y)
+    (n["down"].view(torch.uint8) if fp8 else n["down"]).zero_()
+    assert not d(n["x"], n["ids"], n["w"]).any()
+    w = torch.randn(2, 256, 128, device="cuda").to(BF)
+    for a, b in zip(block_ops.quantize_expert_weights(odd(w)), block_ops.quantize_expert_weights(w)):
+        assert torch.equal(a.float(), b.float())
