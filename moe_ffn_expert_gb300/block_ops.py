@@ -123,6 +123,8 @@ def _norm_plan(residual, branch, post_weight, pre_weight, gate, residual_scale, 
         block = _TYPE.get(block_type, 2)
         if block > stream:
             raise TypeError("normed must be no wider than the residual")
+    elif pre_weight is not None and block_type is not None and _TYPE.get(block_type) != block:
+        raise TypeError("normed has the branch's dtype: normed_dtype is for calls without a branch")
     param = _type("parameters", params[0]) if params else stream
     d = _abi.mm_norm_desc(T, H, groups, stream, block, param, residual_scale, eps)
     at = ctypes.addressof(d)

@@ -496,3 +496,12 @@ def test_rows_that_never_come_are_nan(T, H, groups, post, pre):
     again = run_both(i, up)
     assert all(torch.equal(again[1][k], ref[1][k]) for k in ref[1] if ref[1][k] is not None)
     assert torch.equal(again[0][0], ref[0][0])
+
+
+def test_a_normed_dtype_that_is_not_the_branch_s_is_refused():
+    i, _ = make(8, 64, F32, BF, F32)
+    for op in (block_ops.residual_norm, block_ops.residual_norm_forward):
+        with pytest.raises(TypeError):
+            op(i["residual"], i["branch"], pre_weight=i["pre_weight"], normed_dtype=F32)
+        assert op(i["residual"], i["branch"], pre_weight=i["pre_weight"], normed_dtype=BF)[1].dtype == BF
+        assert op(i["residual"], None, pre_weight=i["pre_weight"], normed_dtype=F32)[1].dtype == F32
