@@ -1043,17 +1043,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             const float w2 = __shfl_sync(0xFFFFFFFFu, held.z, at);
             if (second) ws[1] = w2;
             float next_hs = 1.f;
-            if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
+            // (GEMM2: a slot per block, whose products are committed together)
+            const int last = up ? acc : acc + 1;
+            if (!wait(acc_full(set, last % RING), (last / RING) & 1)) return;
             tc_fence_after();
             if (!up) {  // (the products of h are there, so its scales are)
               if (kb == un.kb0) hs = row_scale(kb);
               if (kb + 1 < un.kb1) next_hs = row_scale(kb + 1);
             }
-            auto release = [&] {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(acc_empty(set, acc % RING));
-            };
             if (up) {  // both parts of the rows in turn, both blocks in one slot
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
@@ -1070,16 +1067,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             } else {  // three parts, a slot per block
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                if (half == 1) {
-                  release();
-                  ++acc;
-                  if (!wait(acc_full(set, acc % RING), (acc / RING) & 1)) return;
-                  tc_fence_after();
-                }
                 uint32_t r[24 * G];
 #pragma unroll
                 for (int j = 0; j < 3 * G; ++j)
-                  tmem_ld_32x8(tmem_q + acc % RING * C::SLOT_COLS + 8 * j,
+                  tmem_ld_32x8(tmem_q + (acc + half) % RING * C::SLOT_COLS + 8 * j,
                                *reinterpret_cast<uint32_t(*)[8]>(r + 8 * j));
                 tmem_ld_wait();
 #pragma unroll
@@ -1091,7 +1082,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
               }
             }
             hs = next_hs;
-            release();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(acc_empty(set, acc % RING));
+              if (!up) mbar_arrive(acc_empty(set, last % RING));
+            }
+            acc = last;
           }
           if (!up) {
 #pragma unroll
