@@ -42,10 +42,10 @@
 // of y, where two parts left 1.77e-3, in the same time.
 //
 // Measured (device time of a call; the floor is the hit experts' bytes at a plain copy's rate):
-// 128 experts of 2048 x 768, top-8, bf16: 64 tokens 182 us, 6.5 TB/s (floor 175); 8 tokens 76 (72);
-// one token 24.6 (11): logits 2, tables 2.6, the first weights 1.8, GEMM2 behind GEMM1, the sums 2.
-// e4m3: 8 tokens 50 us (36), 64 tokens 110 (88); 256 experts of 7168 x 2048, 16 tokens: 629 us, 7.1
-// TB/s (663: weights alone stream a little faster than a copy).
+// 128 experts of 2048 x 768, top-8, bf16: 64 tokens 182 us, 6.5 TB/s (floor 175); 8 tokens 77 (72);
+// one token 24.1 (11): logits 2, tables 2.6, the first weights 1.8, GEMM2 behind GEMM1, the sums 2.
+// e4m3: one token 24.7 us (5.6), 8 tokens 49 (36), 64 tokens 107 (88); 256 experts of 7168 x 2048, 16
+// tokens: 614-637 us, 7.1-7.3 TB/s (663: weights alone stream a little faster than a copy).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

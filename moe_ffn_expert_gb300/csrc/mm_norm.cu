@@ -19,11 +19,18 @@
 // (k_norm_fwd_rows, k_norm_bwd_rows). Few rows, widths above 7680 and tensors off 16-byte
 // boundaries: a row in registers straight from global memory (k_norm_fwd, k_norm_bwd).
 //
-// Measured, bf16, device time of a call: forward 4096 x 7168 40.4 us, 5.8 TB/s (82 us with a row per
-// block); 16384 x 2048 47.4 us, 5.7 TB/s; one row of 2048 2.7 us. Backward 16384 x 2048 73.2 us, 5.5
+// Measured, bf16, device time of a call: forward 4096 x 7168 40.5 us, 5.8 TB/s (82 us with a row per
+// block); 16384 x 2048 47.1 us, 5.7 TB/s; one row of 2048 2.6 us. Backward 16384 x 2048 73.5 us, 5.5
 // TB/s (318 us with a row per block and sums by columns): 66 us for the rows, the rest for the sums of
-// 456 blocks' columns; 4096 x 7168 69 us, 5.1 TB/s. fp32 1000 x 2047 26 us, 1.9 TB/s: 7 rows per SM,
-// so latencies and the sums' launch bound it.
+// 456 blocks' columns; 4096 x 7168 68 us, 5.2 TB/s. fp32 1000 x 2047 23.3 us, 2.1 TB/s: 20 us for the
+// rows of 144 blocks, seven each and one after another, 2.8 us a row of single-element loads; then the
+// sums' launch.
+//
+// What spills (ptxas): k_norm_bwd at widths above 7680 or tensors off 16-byte boundaries, 0.6 KB a thread
+// up to 8192 and 2.2 to 3.1 KB above in 8-column words (1024 threads leave 64 registers a thread and 32
+// column sums beside the row), 1.6 KB in single columns above 4096; it is the form for what the rows'
+// ring does not take (4096 x 8192 backward 278 us, floor 59). k_norm_bwd_rows with a part left out
+// spills 64 to 180 bytes for its tests (16384 x 2048 without post norm and gate 147 us).
 #include <cuda_runtime.h>
 #include <math.h>
 
