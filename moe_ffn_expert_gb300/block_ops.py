@@ -452,12 +452,13 @@ class MoEDecoder:
         _on_gpu("MoEDecoder", *given)
         kept = list(given)
         self._pad = -H % (16 if fp8 else 8)
-        if self._pad:  # (the blocks of 128 that have scales stay the same)
-            for i, (rows, cols) in {0: (self._pad, 0), 1: (0, self._pad), 4: (self._pad, 0),
-                                    5: (0, self._pad), 8: (0, self._pad)}.items():
-                if kept[i] is not None:
-                    kept[i] = _padded(kept[i], rows, cols)
-        kept = [_aligned(t) if i in (0, 1, 4, 5, 8) else _contiguous(t) for i, t in enumerate(kept)]
+        with torch.inference_mode(False), torch.no_grad():  # copies can be renewed from anywhere
+            if self._pad:  # (the blocks of 128 that have scales stay the same)
+                for i, (rows, cols) in {0: (self._pad, 0), 1: (0, self._pad), 4: (self._pad, 0),
+                                        5: (0, self._pad), 8: (0, self._pad)}.items():
+                    if kept[i] is not None:
+                        kept[i] = _padded(kept[i], rows, cols)
+            kept = [_aligned(t) if i in (0, 1, 4, 5, 8) else _contiguous(t) for i, t in enumerate(kept)]
         self._kept = kept
         self._copies = [(g, t) for g, t in zip(given, kept) if t is not g]
         self._versions = self._count_updates()

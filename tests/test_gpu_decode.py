@@ -576,3 +576,16 @@ def test_tensors_off_a_16_byte_boundary(fp8):
     w = torch.randn(2, 256, 128, device="cuda").to(BF)
     for a, b in zip(block_ops.quantize_expert_weights(odd(w)), block_ops.quantize_expert_weights(w)):
         assert torch.equal(a.float(), b.float())
+
+
+def test_copies_made_in_inference_mode_are_renewed_outside():
+    m = make(3, 515, 64, 4, 2)
+    m["down"] = torch.nn.Parameter(m["down"])
+    with torch.inference_mode():
+        d = decoder(m)
+        y = d(m["x"], m["ids"], m["w"])
+    with torch.no_grad():
+        m["down"].mul_(2)
+    assert torch.equal(d(m["x"], m["ids"], m["w"]), 2 * y)
+    assert not any(copy.requires_grad for _, copy in d._copies)
+    assert torch.equal(decoder(m)(m["x"], m["ids"], m["w"]), 2 * y)
