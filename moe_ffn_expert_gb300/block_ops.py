@@ -395,10 +395,11 @@ class MoEDecoder:
 
     The decoder reads the given tensors in every call, so that updates of the weights take effect in
     the next one. Two kinds it has to copy: tensors that are not contiguous (matrices: from a 16-byte
-    boundary on), and, as mm_decode takes H in multiples of 8 (8-bit weights: 16), those of another H, with zeros up to the next multiple (x is padded and y
-    cut in every call). A call takes over the updates of copied tensors that autograd counts (in-place
-    operations, an optimizer's step); after others (through `.data` or a raw pointer, of inference
-    tensors, or before a captured graph's replay) call reload().
+    boundary on), and, as mm_decode takes H in multiples of 8 (8-bit weights: 16), those of another H,
+    with zeros up to the next multiple (x is padded and y cut in every call). A call takes over the
+    updates of copied tensors that autograd counts (in-place operations, an optimizer's step); after
+    others (through `.data` or a raw pointer, of inference tensors, or before a captured graph's
+    replay) call reload().
 
     Calls run on the current stream and use the one workspace: one decoder serves one stream."""
 

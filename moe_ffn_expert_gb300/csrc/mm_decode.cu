@@ -39,7 +39,8 @@
 // elements many times. The products of 128 x 128 blocks are scaled in 32 bits as they leave the
 // tensor memory. h, which has more bits than a bf16 number, is split the same way into three parts
 // (2^-12 of a value is left out), with a scale per row and 128 columns: y is off by 1.66e-3, the rounding
-// of y, where two parts left 1.77e-3, in the same time.
+// of y, where two parts left 1.77e-3. 64 tokens of 128 experts take 107 us, 109 with two parts; 33 tokens
+// of 32 experts with a shared one 41.0, 39.7; one token 24.6, 23.7.
 //
 // Measured (device time of a call; the floor is the hit experts' bytes at a plain copy's rate):
 // 128 experts of 2048 x 768, top-8, bf16: 64 tokens 182 us, 6.5 TB/s (floor 175); 8 tokens 77 (72);
