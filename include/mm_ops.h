@@ -171,8 +171,9 @@ size_t mm_decode_workspace_size(const mm_decode_desc* d);
 
 /* x, y bf16 [T, H], 16-byte aligned. With a router, topk_ids and topk_weights are outputs (either
  * may be NULL: not wanted); without one they are inputs, int32 and fp32 [T, K]; an id outside
- * [0, E) records MM_ERR_BAD_EXPERT_ID in the workspace's status word (mm_get_status) and y is not
- * written. Device waits are bounded and record MM_ERR_TIMEOUT the same way. */
+ * [0, E) records MM_ERR_BAD_EXPERT_ID in the workspace's status word (mm_get_status) and y is NaN.
+ * Device waits are bounded; one that runs out records MM_ERR_TIMEOUT the same way, and what of y was
+ * not computed is NaN. */
 mm_status mm_decode(const mm_decode_desc* d, const mm_decode_weights* w, const void* x,
                     int32_t* topk_ids, float* topk_weights, void* y, void* workspace,
                     size_t workspace_bytes, void* stream);

@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
   const bool good = build_tables(a, tb, aligned, C::CHUNK);  // (its barriers publish the mbarriers and tmem_slot)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const Work work = make_work<FP8>(a, tb.chunks);
+  const Work work = make_work<FP8>(a, good ? tb.chunks : 0);
   // a wait that runs out ends its role; the roles that depend on it run out in turn
   auto give_up = [&] { set_status(a.hdr + W_STATUS, MM_ERR_TIMEOUT); };
   // entry qi of the queue (null: the wait ran out), every lane
@@ -703,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     if (lane == 0) mbar_arrive(q_empty(qi % kQueue));
   };
 
-  if (!good) {
-    // a caller's id is out of range: nothing to do
+  if (!good && warp < kFirstEpilogue) {
+    // a caller's id is out of range: nothing to do but y
   } else if (warp == 0) {
     // ------------------------------------------------ claims units and loads their weights
     int u = __shfl_sync(0xFFFFFFFFu, first_unit, 0), it = 0;
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     const uint32_t tmem_q = tmem + set * RING * C::SLOT_COLS + ((uint32_t)(q * 32) << 16);
     int acc = 0;                    // accumulators taken from the ring
     int up_units = 0;               // GEMM1 units that this set finished
-    bool ok = true;
+    bool ok = good;
     for (int qi = 0; ok; ++qi) {
       const Unit* const entry = take(qi);
       if (entry == nullptr) {
@@ -1173,16 +1173,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
       }
     }
     // ------------------------------------------------ sums of the partial rows
+    // (after an error NaN, so that what was not computed does not pass for a result)
+    ok = __all_sync(0xFFFFFFFFu, ok);
     const int target = work.nc * work.split + work.ncs * work.splits;
     for (int task = (warp - kFirstEpilogue) * (int)gridDim.x + (int)blockIdx.x;
-         ok && task < a.T * work.nt2; task += 8 * (int)gridDim.x) {
+         task < a.T * work.nt2; task += 8 * (int)gridDim.x) {
       const int t = div_small(task, work.nt2), tile = task - t * work.nt2, c = tile * kCols + lane * 4;
-      const bool there = wait_counter(a.ready2 + tile, target, kTimeoutNs);  // every lane, as above
-      if (!__all_sync(0xFFFFFFFFu, there)) {
-        if (lane == 0) give_up();
-        break;
+      if (ok) {
+        const bool there = wait_counter(a.ready2 + tile, target, kTimeoutNs);  // every lane, as above
+        ok = __all_sync(0xFFFFFFFFu, there);
+        if (!ok && lane == 0) give_up();
       }
       if (c >= a.H) continue;
+      if (!ok) {
+        *reinterpret_cast<uint2*>(a.y + (int64_t)t * a.H + c) = make_uint2(0x7FC07FC0u, 0x7FC07FC0u);
+        continue;
+      }
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       // part by part, a part's rows in slot order with 8 loads in flight; then the shared expert
 #pragma unroll 1

@@ -589,3 +589,17 @@ def test_copies_made_in_inference_mode_are_renewed_outside():
     assert torch.equal(d(m["x"], m["ids"], m["w"]), 2 * y)
     assert not any(copy.requires_grad for _, copy in d._copies)
     assert torch.equal(decoder(m)(m["x"], m["ids"], m["w"]), 2 * y)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 4, 40, 64])
+def test_bad_expert_ids_leave_no_result(T, fp8):
+    """All of y is NaN, whichever way the tables are built, and the next call is as ever."""
+    m = make(T, 528, 64, 20, 4, fp8, shared=32)
+    d = decoder(m)
+    y = d(m["x"], m["ids"], m["w"])
+    for at, bad in (((0, 0), 20), ((T - 1, 3), -1)):
+        ids = m["ids"].clone()
+        ids[at] = bad
+        assert torch.isnan(d(m["x"], ids, m["w"])).all() and d.status() == _abi.MM_ERR_BAD_EXPERT_ID
+    assert torch.equal(d(m["x"], m["ids"], m["w"]), y) and d.status() == _abi.MM_OK
