@@ -14,6 +14,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmm.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mm.h")
 OPS_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mm_ops.h")
+EXPERTS_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mm_experts.h")
 
 MM_OK = 0
 MM_ERR_INVALID_ARG = 1
@@ -38,6 +39,8 @@ MM_FP32 = 1
 MM_E4M3 = 2
 MM_SCORE_SOFTMAX = 0
 MM_SCORE_SIGMOID = 1
+MM_GROUPED_SINGLE_CTA = 0x1
+MM_GROUPED_CTA_PAIRS = 0x2
 MM_TRACE_CTA = 0
 MM_TRACE_MAINLOOP = 1
 MM_TRACE_EPILOGUE = 2
@@ -97,6 +100,12 @@ class mm_decode_weights(ctypes.Structure):
         "shared_down_scale", "router", "router_bias")]
 
 
+class mm_grouped_desc(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("E", ctypes.c_int32), ("transposed", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
 _P = ctypes.c_void_p
 _LIB = None
 
@@ -144,6 +153,11 @@ def _lib():
         "mm_decode_workspace_size": (ctypes.c_size_t, [_P]),
         "mm_decode": (st, [_P] * 7 + [ctypes.c_size_t, _P]),
         "mm_quantize_blocks": (st, [ctypes.c_int64] * 3 + [_P] * 4),
+        # include/mm_experts.h (descriptors are passed by address)
+        "mm_experts_version": (ctypes.c_int, []),
+        "mm_grouped_workspace_size": (ctypes.c_size_t, [_P]),
+        "mm_grouped_mm": (st, [_P] * 6 + [ctypes.c_size_t, _P]),
+        "mm_grouped_mm_weight_grad": (st, [_P] * 5 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -1,0 +1,287 @@
+"""Products grouped by expert against their definition in 64 bits.
+
+Tolerances: products of bf16 numbers are exact in 32 bits. An instruction of the tensor cores adds 16 of
+them to the accumulator; the sum of its 17 numbers is off by at most 2^-22 of the sum of magnitudes so
+far (each number is cut at the 24 bits of the largest). Over a sum of n terms that is
+(n / 16 + 1) 2^-22 of the magnitudes' sum, and the result's rounding is half a step of its type."""
+import pytest
+import torch
+
+from moe_ffn_expert_gb300 import _abi, expert_ops
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+SINGLE, PAIRS = _abi.MM_GROUPED_SINGLE_CTA, _abi.MM_GROUPED_CTA_PAIRS
+NAN = float("nan")
+
+
+def offsets_of(sizes, before=0):
+    at = [before]
+    for n in sizes:
+        at.append(at[-1] + n)
+    return torch.tensor(at, dtype=torch.int32, device="cuda")
+
+
+def inputs(sizes, K, N, transposed=False, before=0, behind=0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    R, E = before + sum(sizes) + behind, len(sizes)
+
+    def randn(*s):
+        return torch.randn(*s, generator=g, device="cuda").to(BF)
+
+    w = randn(E, N, K).transpose(1, 2) if transposed else randn(E, K, N)
+    return randn(R, K), w, offsets_of(sizes, before), randn(R, N)
+
+
+def spans(offsets):
+    at = offsets.tolist()
+    return list(enumerate(zip(at[:-1], at[1:])))
+
+
+def close(got, ref, mag, terms):
+    assert got.shape == ref.shape
+    tol = torch.finfo(got.dtype).eps / 2 * ref.abs() + (terms / 16 + 1) * 2.0 ** -22 * mag
+    bad = ~((got.double() - ref).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+def check_forward(rows, weight, offsets, **how):
+    got = expert_ops.grouped_mm_forward(rows, weight, offsets, **how)
+    ref = torch.zeros(got.shape, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(ref)
+    for e, (a, b) in spans(offsets):
+        x, w = rows[a:b].double(), weight[e].double()
+        ref[a:b], mag[a:b] = x @ w, x.abs() @ w.abs()
+    assert got.dtype == (how.get("out_dtype") or BF) and got.is_contiguous()
+    close(got, ref, mag, rows.shape[1])
+    return got
+
+
+def check_weight_grad(rows, d_out, offsets, weight, **how):
+    got = expert_ops.grouped_mm_weight_grad(rows, d_out, offsets, weight, **how)
+    ref = torch.zeros(weight.shape, dtype=torch.float64, device="cuda")
+    mag, terms = torch.zeros_like(ref), 0
+    for e, (a, b) in spans(offsets):
+        x, d = rows[a:b].double(), d_out[a:b].double()
+        ref[e], mag[e], terms = x.t() @ d, x.abs().t() @ d.abs(), max(terms, b - a)
+    assert got.dtype == (how.get("dtype") or BF)
+    close(got, ref, mag, terms)
+    return got
+
+
+SIZES = {"one": [1], "two": [1, 1], "ragged": [16, 17, 255, 256, 257, 0, 513, 3], "empty": [0, 0, 0],
+         "last": [0, 0, 31], "even": [64, 128], "many": [5] * 40, "wide": [1025, 700]}
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS, 0])
+@pytest.mark.parametrize("K,N", [(8, 8), (64, 128), (72, 136), (200, 520), (1024, 264)])
+@pytest.mark.parametrize("sizes", SIZES.values(), ids=SIZES)
+def test_forward(sizes, K, N, form):
+    for transposed in (False, True):
+        for out in (BF, F32):
+            x, w, at, _ = inputs(sizes, K, N, transposed)
+            check_forward(x, w, at, out_dtype=out, flags=form)
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS, 0])
+@pytest.mark.parametrize("K,N", [(8, 8), (64, 128), (72, 136), (520, 200), (264, 1024)])
+@pytest.mark.parametrize("sizes", SIZES.values(), ids=SIZES)
+def test_weight_grad(sizes, K, N, form):
+    for transposed in (False, True):
+        for out in (BF, F32):
+            x, w, at, d = inputs(sizes, K, N, transposed)
+            got = check_weight_grad(x, d, at, w, dtype=out, flags=form)
+            assert got.transpose(1, 2).is_contiguous() if transposed else got.is_contiguous()
+
+
+@pytest.mark.parametrize("K,N", [(33, 70), (7, 8), (64, 1), (1, 1), (130, 96)])
+def test_odd_widths(K, N):
+    x, w, at, d = inputs([3, 0, 40, 1], K, N, transposed=True, behind=2)
+    check_forward(x, w, at)
+    check_weight_grad(x, d, at, w, dtype=F32)
+    into = torch.ones(w.shape, device="cuda")
+    expert_ops.grouped_mm_weight_grad(x, d, at, w, into=into)
+    assert torch.allclose(into - 1, check_weight_grad(x, d, at, w, dtype=F32), atol=1e-5, rtol=1e-6)
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+def test_both_forms_give_the_same_bits(form):
+    x, w, at, d = inputs([300, 1, 0, 77, 900], 776, 392, behind=9)
+    assert torch.equal(expert_ops.grouped_mm_forward(x, w, at, flags=form), expert_ops.grouped_mm_forward(x, w, at))
+    assert torch.equal(expert_ops.grouped_mm_weight_grad(x, d, at, w, flags=form),
+                       expert_ops.grouped_mm_weight_grad(x, d, at, w))
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+@pytest.mark.parametrize("value", [NAN, float("inf")])
+def test_rows_of_others_have_no_part(form, value):
+    """An expert's results do not depend on what its neighbours' rows and the rows of nobody hold."""
+    sizes = [21, 5, 40, 0, 130, 1]
+    x, w, at, d = inputs(sizes, 136, 264, before=3, behind=50)
+    clean_out = check_forward(x, w, at, flags=form)
+    clean_dw = check_weight_grad(x, d, at, w, flags=form)
+    assert (clean_out[:3] == 0).all() and (clean_out[-50:] == 0).all()
+    for e, (a, b) in spans(at):
+        x2, d2 = torch.full_like(x, value), torch.full_like(d, value)
+        x2[a:b], d2[a:b] = x[a:b], d[a:b]
+        assert torch.equal(expert_ops.grouped_mm_forward(x2, w, at, flags=form)[a:b], clean_out[a:b])
+        assert torch.equal(expert_ops.grouped_mm_weight_grad(x2, d2, at, w, flags=form)[e], clean_dw[e])
+    w2 = torch.full_like(w, value)
+    w2[4] = w[4]
+    a, b = at[4].item(), at[5].item()
+    got = expert_ops.grouped_mm_forward(x, w2, at, flags=form)
+    assert torch.equal(got[a:b], clean_out[a:b]) and (got[:3] == 0).all() and (got[-50:] == 0).all()
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+@pytest.mark.parametrize("bad", [[-1, 5, 9], [0, 9, 5], [0, 5, 41], [0, 2 ** 31 - 1, 3], [7, 3, 40],
+                                 [-(2 ** 31), 0, 40]])
+def test_offsets_that_are_none(bad, form):
+    x, w, _, d = inputs([20, 20], 64, 72)
+    at = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    for out in (BF, F32):
+        assert expert_ops.grouped_mm_forward(x, w, at, out_dtype=out, flags=form).isnan().all()
+        assert expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=out, flags=form).isnan().all()
+    x, w, at, _ = inputs([20, 20], 64, 72)
+    check_forward(x, w, at, flags=form)  # the next call is none the worse
+    big = at.long().clone()
+    big[2] = 2 ** 32 + 40  # 40 in the low half
+    assert expert_ops.grouped_mm_forward(x, w, big).isnan().all()
+    assert torch.equal(expert_ops.grouped_mm_forward(x, w, at.long()), expert_ops.grouped_mm_forward(x, w, at))
+
+
+def test_many_experts_and_none_of_the_rows():
+    x, w, at, d = inputs([(7 * e) % 5 for e in range(1024)], 64, 40)
+    check_forward(x, w, at)
+    check_weight_grad(x, d, at, w)
+    x, w, at, d = inputs([0, 0], 64, 40)
+    assert expert_ops.grouped_mm_forward(x, w, at).shape == (0, 40)
+    assert (check_weight_grad(x, d, at, w) == 0).all()
+    x, w, at, d = inputs([0, 0], 64, 40, behind=7)
+    assert (check_forward(x, w, at) == 0).all() and (check_weight_grad(x, d, at, w) == 0).all()
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_sums_into_a_kept_gradient(form, transposed, dt):
+    x, w, at, d = inputs([70, 0, 9], 136, 72, transposed)
+    own = expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=F32)
+    into = torch.full((3, 72, 136) if transposed else (3, 136, 72), 0.5, dtype=dt, device="cuda")
+    into = into.transpose(1, 2) if transposed else into
+    before = into.clone()
+    got = expert_ops.grouped_mm_weight_grad(x, d, at, w, into=into, flags=form)
+    assert got.data_ptr() == into.data_ptr() and got.stride() == into.stride()
+    assert torch.equal(into, (before.float() + own).to(dt))
+    assert torch.equal(into[1], before[1])
+
+
+def test_strides_alignment_and_other_layouts():
+    x, w, at, d = inputs([30, 11], 64, 72)
+    ref, dw = expert_ops.grouped_mm_forward(x, w, at), expert_ops.grouped_mm_weight_grad(x, d, at, w)
+    wide = torch.zeros(41, 100, dtype=BF, device="cuda")
+    wide[:, 3:67] = x
+    for rows in (wide[:, 3:67], x.t().contiguous().t(), torch.cat([x.flatten()[:1], x.flatten()])[1:].view(41, 64)):
+        assert torch.equal(expert_ops.grouped_mm_forward(rows, w, at), ref)
+        assert torch.equal(expert_ops.grouped_mm_weight_grad(rows, d, at, w), dw)
+    for weight in (w.permute(1, 0, 2).contiguous().permute(1, 0, 2), torch.cat([w.flatten()[:1], w.flatten()])[1:].view(2, 64, 72),
+                   w.transpose(1, 2).contiguous().transpose(1, 2)):
+        assert torch.equal(expert_ops.grouped_mm_forward(x, weight, at), ref)
+        assert torch.equal(expert_ops.grouped_mm_weight_grad(x, d, at, weight), dw)
+    one = w[:1].expand(2, 64, 72)  # the experts share one matrix
+    assert torch.equal(expert_ops.grouped_mm_forward(x, one, at)[:30], ref[:30])
+
+
+def test_gradients_by_the_formula_and_by_differences():
+    x, w, at, d = inputs([50, 0, 33], 72, 136, transposed=True, behind=4)
+    x.requires_grad_(True)
+    w = w.detach().requires_grad_(True)
+    out = expert_ops.grouped_mm(x, w, at)
+    out.backward(d)
+    assert torch.equal(x.grad, check_forward(d, w.detach().transpose(1, 2), at))
+    assert torch.equal(w.grad, check_weight_grad(x.detach(), d, at, w.detach()))
+    assert (x.grad[-4:] == 0).all() and (w.grad[1] == 0).all()
+    # out is linear in each: the difference over a step of bf16 numbers, 32-bit results
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for t, other in ((x, lambda s: (s, w.detach())), (w, lambda s: (x.detach(), s))):
+        step = torch.randint(-2, 3, t.shape, generator=g, device="cuda").to(BF)
+        moved = expert_ops.grouped_mm_forward(*other(step), at, out_dtype=F32)
+        by_difference, by_gradient = (moved * d).double().sum(), (t.grad.double() * step.double()).sum()
+        # the gradient's rounding: 2^-8 of each element, random signs; 8 deviations of their sum
+        tol = 8 * 2.0 ** -8 * (t.grad.double() * step.double()).square().sum().sqrt() + 1e-5 * moved.abs().sum()
+        assert abs(by_difference - by_gradient) <= tol
+    out = expert_ops.grouped_mm(x, w, at, out_dtype=F32)
+    assert out.dtype == F32
+    x.grad = w.grad = None
+    out.sum().backward()  # an expanded gradient
+    ones = torch.ones_like(d)
+    assert torch.equal(x.grad, expert_ops.grouped_mm_forward(ones, w.detach().transpose(1, 2), at))
+    only = expert_ops.grouped_mm(x.detach(), w, at)
+    w.grad = None
+    only.backward(d)
+    assert w.grad is not None
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        (gx,) = torch.autograd.grad((expert_ops.grouped_mm(x, w, at) * d).sum(), x, create_graph=True)
+        gx.square().sum().backward()
+
+
+def test_a_captured_step_replays_with_other_sizes():
+    K, N, R = 136, 264, 400
+    x, w, at, d = inputs([100, 0, 200, 90], K, N, behind=10)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        expert_ops.grouped_mm_backward(d, x, w, at)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        out = expert_ops.grouped_mm_forward(x, w, at)
+        dx, dw = expert_ops.grouped_mm_backward(d, x, w, at)
+    for sizes in ([0, 0, 0, 400], [1, 2, 3, 4], [400, 0, 0, 0], [0, 0, 0, 0], [133, 133, 133, 1]):
+        x2, w2, at2, d2 = inputs(sizes, K, N, behind=R - sum(sizes), seed=3)
+        for t, v in ((x, x2), (w, w2), (at, at2), (d, d2)):
+            t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, expert_ops.grouped_mm_forward(x2, w2, at2))
+        want = expert_ops.grouped_mm_backward(d2, x2, w2, at2)
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+def test_calls_on_two_streams_at_once():
+    cases = [inputs([90, 300, 1], 200, 136, seed=s) for s in range(2)]
+    want = [expert_ops.grouped_mm_backward(d, x, w, at) for x, w, at, d in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, (x, w, at, d) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(expert_ops.grouped_mm_backward(d, x, w, at))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for pair in got[i] for a, b in zip(pair, want[i]))
+
+
+def test_refusals():
+    x, w, at, d = inputs([3, 4], 64, 72)
+    call = expert_ops.grouped_mm_forward
+    for args in ((x[:, :32], w, at), (x[0], w, at), (x, w[0], at), (x, w, at[:2]), (x, w, at.float()), (x.cpu(), w, at),
+                 (x, w, at.cpu())):
+        with pytest.raises(ValueError):
+            call(*args)
+    with pytest.raises(ValueError):
+        call(x, w, at, flags=3)
+    for args in ((x.float(), w, at), (x, w.float(), at)):
+        with pytest.raises(TypeError):
+            call(*args)
+    with pytest.raises(TypeError):
+        call(x, w, at, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        expert_ops.grouped_mm_weight_grad(x, d[:, :8], at, w)
+    with pytest.raises(ValueError):
+        expert_ops.grouped_mm_weight_grad(x, d, at, w, into=torch.zeros(2, 64, 80, device="cuda")[:, :, :72])
+    with pytest.raises(ValueError):
+        expert_ops.grouped_mm_weight_grad(x, d, at, w, into=torch.zeros(2, 72, 64, device="cuda"))
+    with pytest.raises(TypeError):
+        expert_ops.grouped_mm_weight_grad(x, d, at, w, into=torch.zeros(2, 64, 72, device="cuda"), dtype=BF)
