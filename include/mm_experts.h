@@ -8,7 +8,7 @@
  *   mm_grouped_mm_*      each expert's rows times its matrix, ragged sizes, and the gradients;
  *   mm_expert_combine_*  a token's weighted sum of its slots' rows, and its gradients;
  *   mm_grad_norm         the norm of many tensors together;
- *   mm_grad_scale        the tensors scaled down to a largest norm.
+ *   mm_grad_clip         the tensors scaled down to a largest norm.
  *
  * The rules of mm_ops.h hold here too: row-major contiguous device memory, every buffer (workspaces
  * included) belongs to the caller, nothing is allocated, all work is enqueued on `stream` and nothing
@@ -28,6 +28,46 @@ extern "C" {
 
 /* Version of this header's functions and structs. */
 int mm_experts_version(void);
+
+/* ---- the order of a selection -------------------------------------------------------------
+ *
+ * Slots s = t K + k of topk_ids int32 [T, K], sorted by expert, equal ones by s:
+ *   offsets[e]      int32 [E + 1]  slots with an id below e (of those with an expert)
+ *   row_of_slot[s]  int32 [T, K]   place of slot s in the order
+ *   slot_of_row[r]  int32 [T K]    slot at place r
+ * An id outside [0, E) is a slot without an expert: row_of_slot is -1 there, and as many places of
+ * slot_of_row behind offsets[E] are -1. These are mm_forward's tables without their padding.
+ * Sizes: T >= 0, 1 <= E <= 1024, 1 <= K <= 16, T K < 2^31 - 2^16, 1 <= H <= 2^20. */
+typedef struct mm_expert_desc {
+  int64_t T, H;
+  int32_t E, K;
+  int32_t type; /* MM_BF16 or MM_FP32: of x, rows, y and their gradients */
+} mm_expert_desc;
+
+/* Bytes of workspace of mm_expert_table (0: unsupported sizes). Needs no initialisation. H and type
+ * of the descriptor are not used by the two. */
+size_t mm_expert_table_workspace_size(const mm_expert_desc* d);
+
+mm_status mm_expert_table(const mm_expert_desc* d, const int32_t* topk_ids, int32_t* offsets,
+                          int32_t* row_of_slot, int32_t* slot_of_row, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* rows[r] = x[slot_of_row[r] / K] (x [T, H], rows [T K, H]); rows behind offsets[E] are zero. offsets
+ * and row_of_slot are mm_expert_table's; places outside [0, T K) are not written. */
+mm_status mm_expert_dispatch(const mm_expert_desc* d, const void* x, const int32_t* offsets,
+                             const int32_t* row_of_slot, void* rows, void* stream);
+
+/* y[t] = sum_k w[t,k] rows[row_of_slot[t,k]], k ascending, over the slots with an expert (a token
+ * without one gets zeros). w fp32 [T, K], or NULL: 1 (the gradient of mm_expert_dispatch). */
+mm_status mm_expert_combine(const mm_expert_desc* d, const void* rows, const int32_t* row_of_slot,
+                            const float* weights, void* y, void* stream);
+
+/* d_rows[r] = w[s] dy[t], zero behind offsets[E]; d_weights[t,k] = <dy[t], rows[r]> (fp32 [T, K], zero
+ * for a slot without an expert; NULL: not wanted, and rows may be NULL too). */
+mm_status mm_expert_combine_backward(const mm_expert_desc* d, const void* dy, const void* rows,
+                                     const int32_t* offsets, const int32_t* row_of_slot,
+                                     const float* weights, void* d_rows, float* d_weights,
+                                     void* stream);
 
 /* ---- grouped products ---------------------------------------------------------------------
  *
@@ -67,6 +107,32 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
 mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, const void* d_out,
                                     const int32_t* offsets, void* d_weight, int accumulate,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the norm of many tensors, and clipping -----------------------------------------------
+ *
+ *   norm = sqrt(sum over all tensors of the squares of their elements)
+ *   out  = min(1, max_norm / (norm + eps)) * data
+ * Squares are summed in 32 bits over at most 64 elements (in 64 bits where they would leave the range
+ * of 32), further in 64 bits: the norm is right for elements of any size. norm is fp32 (infinite where
+ * it is above that type). A NaN among the elements makes the norm and with it all of `out` NaN, an
+ * infinity makes the finite elements 0, as the formula has it. */
+typedef struct mm_tensor_ref {
+  const void* data;
+  void* out;         /* mm_grad_clip: where the scaled elements go; may be `data` itself */
+  int64_t count;     /* elements, contiguous; 0: data and out may be NULL */
+  int32_t type;      /* MM_BF16 or MM_FP32 */
+  int32_t out_type;  /* the same; of data and out that are one: equal to type */
+} mm_tensor_ref;
+
+/* Bytes of workspace for n tensors (0: unsupported). Needs no initialisation. */
+size_t mm_grad_workspace_size(int64_t n);
+
+/* `tensors`: n descriptions in host memory, read before the call returns. 0 <= n < 2^20. No tensor
+ * overlaps an `out` other than its own. */
+mm_status mm_grad_norm(int64_t n, const mm_tensor_ref* tensors, float* norm, void* workspace,
+                       size_t workspace_bytes, void* stream);
+mm_status mm_grad_clip(int64_t n, const mm_tensor_ref* tensors, double max_norm, double eps, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -94,10 +94,20 @@ class mm_decode_desc(ctypes.Structure):
                 ("normalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class mm_tensor_ref(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
 class mm_decode_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "up", "down", "up_scale", "down_scale", "shared_up", "shared_down", "shared_up_scale",
         "shared_down_scale", "router", "router_bias")]
+
+
+class mm_expert_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("E", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 class mm_grouped_desc(ctypes.Structure):
@@ -155,6 +165,15 @@ def _lib():
         "mm_quantize_blocks": (st, [ctypes.c_int64] * 3 + [_P] * 4),
         # include/mm_experts.h (descriptors are passed by address)
         "mm_experts_version": (ctypes.c_int, []),
+        "mm_expert_table_workspace_size": (ctypes.c_size_t, [_P]),
+        "mm_expert_table": (st, [_P] * 6 + [ctypes.c_size_t, _P]),
+        "mm_expert_dispatch": (st, [_P] * 6),
+        "mm_expert_combine": (st, [_P] * 6),
+        "mm_expert_combine_backward": (st, [_P] * 9),
+        "mm_grad_workspace_size": (ctypes.c_size_t, [ctypes.c_int64]),
+        "mm_grad_norm": (st, [ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P]),
+        "mm_grad_clip": (st, [ctypes.c_int64, _P, ctypes.c_double, ctypes.c_double, _P, _P,
+                              ctypes.c_size_t, _P]),
         "mm_grouped_workspace_size": (ctypes.c_size_t, [_P]),
         "mm_grouped_mm": (st, [_P] * 6 + [ctypes.c_size_t, _P]),
         "mm_grouped_mm_weight_grad": (st, [_P] * 5 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),

@@ -1,0 +1,464 @@
+// The order of a selection's slots by expert, the tokens' rows in that order, and a token's weighted
+// sum of its slots' rows with its gradients (definitions in mm_experts.h).
+//
+// Order: a stable counting sort. A block takes kSlots slots and counts them per expert (slots without
+// an expert are those of one more, the last); the blocks' counts before a block and the experts before
+// an expert give where its slots of that expert start, and within a block the warps' counts and the
+// lanes before a lane with the same expert the rest. Up to kSlots slots are one launch.
+//
+// Dispatch and combine move rows: a block has a token's row and its K slots' rows, so that each row is
+// read and written once.
+#include <algorithm>
+
+#include "../../include/mm_experts.h"
+#include "mm_kernels.h"
+#include "mm_rows.cuh"
+
+namespace mm {
+namespace {
+
+constexpr int kMaxE = 1024, kMaxK = 16;
+constexpr int kTableWarps = 16, kRounds = 4;  // a warp counts kRounds x 32 slots
+constexpr int kSlots = kTableWarps * kRounds * 32;
+// Blocks whose counts every block adds up by itself; more of them are added up by a launch between.
+constexpr int kFewBlocks = 128;
+
+struct TableArgs {
+  const int32_t* ids;
+  int32_t *offsets, *row_of_slot, *slot_of_row;
+  int32_t* counts;  // [blocks + 1][E + 1]; added up: the counts of the blocks before, the totals last
+  int S, E, blocks;
+};
+
+__device__ __forceinline__ int bucket_of(const TableArgs& a, int s) {
+  if (s >= a.S) return -1;
+  const int e = a.ids[s];
+  return e >= 0 && e < a.E ? e : a.E;
+}
+
+__global__ void __launch_bounds__(32 * kTableWarps) k_table_count(TableArgs a) {
+  __shared__ int count[kMaxE + 1];
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) count[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kSlots; i += blockDim.x) {
+    const int b = bucket_of(a, blockIdx.x * kSlots + i);
+    if (b >= 0) atomicAdd(&count[b], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x)
+    a.counts[(int64_t)blockIdx.x * (a.E + 1) + e] = count[e];
+}
+
+// 32 buckets a block, a warp for each of 32 runs of blocks: counts become the counts of the blocks
+// before, and the totals follow the last.
+__global__ void __launch_bounds__(1024) k_table_scan(TableArgs a) {
+  __shared__ int sums[32][33];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  const int64_t run = (a.blocks + 31) / 32, first = warp * run, end = min(first + run, (int64_t)a.blocks);
+  int sum = 0;
+  if (e <= a.E)
+    for (int64_t b = first; b < end; ++b) sum += a.counts[b * (a.E + 1) + e];
+  sums[warp][lane] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < warp; ++w) before += sums[w][lane];
+  if (e > a.E) return;
+  for (int64_t b = first; b < end; ++b) {
+    int32_t* at = a.counts + b * (a.E + 1) + e;
+    const int c = *at;
+    *at = before;
+    before += c;
+  }
+  if (warp == 31) a.counts[(int64_t)a.blocks * (a.E + 1) + e] = before;
+}
+
+__global__ void __launch_bounds__(32 * kTableWarps) k_table_rank(TableArgs a) {
+  constexpr int THREADS = 32 * kTableWarps, PER = (kMaxE + THREADS) / THREADS;
+  __shared__ __align__(4) uint16_t count[kTableWarps][kMaxE + 2];
+  __shared__ int base[kMaxE + 1];
+  __shared__ int sums[kTableWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, buckets = a.E + 1;
+  for (int i = threadIdx.x; i < kTableWarps * (kMaxE + 2) / 2; i += THREADS)
+    reinterpret_cast<uint32_t*>(&count[0][0])[i] = 0;
+  __syncthreads();
+  int b[kRounds];
+  unsigned same[kRounds];
+  const int s0 = (blockIdx.x * kTableWarps + warp) * kRounds * 32 + lane;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    b[r] = bucket_of(a, s0 + 32 * r);
+    same[r] = __match_any_sync(0xFFFFFFFFu, b[r]);
+    if (b[r] >= 0 && lane == __ffs(same[r]) - 1) count[warp][b[r]] += __popc(same[r]);
+    __syncwarp();
+  }
+  __syncthreads();
+  // a thread's PER buckets: their counts before this block, and in all blocks
+  int total[PER], before[PER], mine = 0;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int e = threadIdx.x * PER + p;
+    total[p] = before[p] = 0;
+    if (e < buckets) {
+      int run = 0;
+      for (int w = 0; w < kTableWarps; ++w) {
+        const int c = count[w][e];
+        count[w][e] = (uint16_t)run;
+        run += c;
+      }
+      if (a.blocks == 1) {
+        total[p] = run;
+      } else if (a.blocks <= kFewBlocks) {
+#pragma unroll 8
+        for (int k = 0; k < a.blocks; ++k) {
+          const int c = a.counts[k * buckets + e];
+          total[p] += c;
+          before[p] += k < (int)blockIdx.x ? c : 0;
+        }
+      } else {
+        total[p] = a.counts[(int64_t)a.blocks * buckets + e];
+        before[p] = a.counts[(int64_t)blockIdx.x * buckets + e];
+      }
+    }
+    mine += total[p];
+  }
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int at = upto - mine;
+  for (int w = 0; w < warp; ++w) at += sums[w];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int e = threadIdx.x * PER + p;
+    if (e < buckets) {
+      base[e] = at + before[p];
+      if (blockIdx.x == 0) a.offsets[e] = at;  // (slots without an expert are behind offsets[E])
+    }
+    at += total[p];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int s = s0 + 32 * r;
+    int row = 0;
+    if (b[r] >= 0) row = base[b[r]] + count[warp][b[r]] + __popc(same[r] & ((1u << lane) - 1u));
+    __syncwarp();
+    if (b[r] >= 0) {
+      if (lane == __ffs(same[r]) - 1) count[warp][b[r]] += __popc(same[r]);
+      const bool taken = b[r] < a.E;
+      a.row_of_slot[s] = taken ? row : -1;
+      a.slot_of_row[row] = taken ? s : -1;
+    }
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------------------------ rows
+
+struct RowArgs {
+  const void *x, *rows;  // the tokens' rows, the slots' rows
+  const int32_t *offsets, *row_of_slot;
+  const float* weights;
+  void *out_x, *out_rows;
+  float* d_weights;
+  int64_t T, S;
+  int H, E, K;
+  int words;  // of a row, in the words that the kernel moves
+};
+
+// Zero rows behind the last expert's, by all blocks of the launch together.
+template <typename V>
+__device__ __forceinline__ void zero_rows_behind(const RowArgs& a, V* rows) {
+  const int64_t first = max(0, a.offsets[a.E]);
+  for (int64_t r = first + blockIdx.x; r < a.S; r += gridDim.x)
+    for (int w = threadIdx.x; w < a.words; w += blockDim.x) rows[r * a.words + w] = V{};
+}
+
+template <typename V>
+__global__ void __launch_bounds__(256) k_dispatch(RowArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const V* x = static_cast<const V*>(a.x);
+  V* rows = static_cast<V*>(a.out_rows);
+  const int64_t t = blockIdx.x;
+  const int32_t* row = a.row_of_slot + t * a.K;
+  for (int w = threadIdx.x; w < a.words; w += blockDim.x) {
+    const V v = x[t * a.words + w];
+    for (int k = 0; k < a.K; ++k) {
+      const int64_t r = row[k];
+      if (r >= 0 && r < a.S) rows[r * a.words + w] = v;
+    }
+  }
+  zero_rows_behind(a, rows);
+}
+
+// W columns a thread. words: H / W.
+template <typename T, int W>
+__global__ void __launch_bounds__(256) k_combine(RowArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const T* rows = static_cast<const T*>(a.rows);
+  const int64_t t = blockIdx.x;
+  const int32_t* row = a.row_of_slot + t * a.K;
+  for (int w = threadIdx.x; w < a.words; w += blockDim.x) {
+    float y[W] = {};
+    for (int k0 = 0; k0 < a.K; k0 += 4) {  // four slots' loads in flight
+      float v[4][W];
+      float g[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t r = k0 + k < a.K ? row[k0 + k] : -1;
+        const bool there = r >= 0 && r < a.S;
+        g[k] = there ? (a.weights ? a.weights[t * a.K + k0 + k] : 1.f) : 0.f;
+        if (there) {
+          load_vec<W>(rows + r * a.H + (int64_t)w * W, v[k]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < W; ++i) v[k][i] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) y[i] = fmaf(g[k], v[k][i], y[i]);
+    }
+    store_vec<W>(static_cast<T*>(a.out_x) + t * a.H + (int64_t)w * W, y);
+  }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(256) k_combine_bwd(RowArgs a) {
+  __shared__ float part[8][8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const T* rows = static_cast<const T*>(a.rows);
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int k0 = 0; k0 < a.K; k0 += 8) {
+    float dot[8] = {};
+    int64_t row[8];
+    float g[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      row[k] = k0 + k < a.K ? a.row_of_slot[t * a.K + k0 + k] : -1;
+      if (row[k] >= a.S) row[k] = -1;
+      g[k] = row[k] >= 0 && a.weights ? a.weights[t * a.K + k0 + k] : 1.f;
+    }
+    for (int w = threadIdx.x; w < a.words; w += blockDim.x) {
+      float d[W];
+      load_vec<W>(static_cast<const T*>(a.x) + t * a.H + (int64_t)w * W, d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (row[k] < 0) continue;
+        const int64_t at = row[k] * a.H + (int64_t)w * W;
+        float v[W];
+        if (a.d_weights) {
+          load_vec<W>(rows + at, v);
+#pragma unroll
+          for (int i = 0; i < W; ++i) dot[k] = fmaf(d[i], v[i], dot[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = g[k] * d[i];
+        store_vec<W>(static_cast<T*>(a.out_rows) + at, v);
+      }
+    }
+    if (a.d_weights) {
+      const float sum = warp_sum_many<8>(dot, lane);
+      if ((lane & 3) == 0) part[warp][lane >> 2] = sum;
+      __syncthreads();
+      if (threadIdx.x < 8 && k0 + (int)threadIdx.x < a.K) {
+        float s = 0.f;
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) s += part[w][threadIdx.x];
+        a.d_weights[t * a.K + k0 + threadIdx.x] = s;
+      }
+      __syncthreads();
+    }
+  }
+  // (words of W elements)
+  const int64_t first = max(0, a.offsets[a.E]);
+  for (int64_t r = first + blockIdx.x; r < a.S; r += gridDim.x)
+    for (int w = threadIdx.x; w < a.words; w += blockDim.x) {
+      const float zero[W] = {};
+      store_vec<W>(static_cast<T*>(a.out_rows) + r * a.H + (int64_t)w * W, zero);
+    }
+}
+
+// ------------------------------------------------------------------------------------ host side
+
+inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+mm_status check_desc(const mm_expert_desc* d, bool rows) {
+  if (d == nullptr || d->T < 0 || d->E < 1 || d->K < 1) return MM_ERR_INVALID_ARG;
+  if (d->E > kMaxE || d->K > kMaxK || d->T > ((int64_t)1 << 31) ||
+      d->T * d->K >= ((int64_t)1 << 31) - ((int64_t)1 << 16))
+    return MM_ERR_UNSUPPORTED;
+  if (rows) {
+    if (d->H < 1 || (d->type != MM_BF16 && d->type != MM_FP32)) return MM_ERR_INVALID_ARG;
+    if (d->H > ((int64_t)1 << 20)) return MM_ERR_UNSUPPORTED;
+  }
+  return MM_OK;
+}
+
+int64_t table_blocks(const mm_expert_desc& d) { return (d.T * d.K + kSlots - 1) / kSlots; }
+
+RowArgs row_args(const mm_expert_desc& d) {
+  RowArgs a{};
+  a.T = d.T;
+  a.S = d.T * d.K;
+  a.H = (int)d.H;
+  a.E = d.E;
+  a.K = d.K;
+  return a;
+}
+
+inline unsigned threads_for(int words) { return (unsigned)std::min(256, (words + 31) / 32 * 32); }
+
+}  // namespace
+}  // namespace mm
+
+using namespace mm;
+
+extern "C" {
+
+size_t mm_expert_table_workspace_size(const mm_expert_desc* d) {
+  if (check_desc(d, false) != MM_OK) return 0;
+  const int64_t blocks = table_blocks(*d);
+  return blocks <= 1 ? 256 : std::max<size_t>(256, (size_t)(blocks + 1) * (d->E + 1) * 4);
+}
+
+mm_status mm_expert_table(const mm_expert_desc* d, const int32_t* topk_ids, int32_t* offsets,
+                          int32_t* row_of_slot, int32_t* slot_of_row, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  mm_status s = check_desc(d, false);
+  if (s != MM_OK) return s;
+  if (!offsets || !aligned_to(offsets, 4) || !aligned_to(topk_ids, 4) || !aligned_to(row_of_slot, 4) ||
+      !aligned_to(slot_of_row, 4))
+    return MM_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned_to(workspace, 256) ||
+      workspace_bytes < mm_expert_table_workspace_size(d))
+    return MM_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (d->T > 0 && (!topk_ids || !row_of_slot || !slot_of_row)) return MM_ERR_INVALID_ARG;
+  clear_error();
+  if (d->T == 0) {
+    MM_TRY(cudaMemsetAsync(offsets, 0, (size_t)(d->E + 1) * 4, st));
+    return MM_OK;
+  }
+  TableArgs a{topk_ids, offsets, row_of_slot, slot_of_row, static_cast<int32_t*>(workspace),
+              (int)(d->T * d->K), d->E, (int)table_blocks(*d)};
+  const dim3 grid((unsigned)a.blocks), threads(32 * kTableWarps);
+  if (a.blocks > 1) MM_TRY(launch_pdl(k_table_count, grid, threads, 0, st, a));
+  if (a.blocks > kFewBlocks)
+    MM_TRY(launch_pdl(k_table_scan, dim3((unsigned)(a.E + 32) / 32), dim3(1024), 0, st, a));
+  MM_TRY(launch_pdl(k_table_rank, grid, threads, 0, st, a));
+  return MM_OK;
+}
+
+mm_status mm_expert_dispatch(const mm_expert_desc* d, const void* x, const int32_t* offsets,
+                             const int32_t* row_of_slot, void* rows, void* stream) {
+  mm_status s = check_desc(d, true);
+  if (s != MM_OK) return s;
+  const size_t es = d->type == MM_BF16 ? 2 : 4;
+  if (!aligned_to(x, es) || !aligned_to(rows, es) || !aligned_to(offsets, 4) || !aligned_to(row_of_slot, 4))
+    return MM_ERR_INVALID_ARG;
+  if (d->T == 0) return MM_OK;
+  if (!x || !offsets || !row_of_slot || !rows) return MM_ERR_INVALID_ARG;
+  clear_error();
+  RowArgs a = row_args(*d);
+  a.x = x;
+  a.offsets = offsets;
+  a.row_of_slot = row_of_slot;
+  a.out_rows = rows;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // the widest words that rows consist of and start at
+  const uintptr_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rows) |
+                        (uintptr_t)(d->H * es);
+  const dim3 grid((unsigned)d->T);
+  auto go = [&](auto* kernel, int bytes) {
+    a.words = (int)(d->H * es / bytes);
+    return launch_pdl(kernel, grid, dim3(threads_for(a.words)), 0, st, a);
+  };
+  if (all % 16 == 0)
+    MM_TRY(go(k_dispatch<uint4>, 16));
+  else if (all % 8 == 0)
+    MM_TRY(go(k_dispatch<uint2>, 8));
+  else if (all % 4 == 0)
+    MM_TRY(go(k_dispatch<uint32_t>, 4));
+  else
+    MM_TRY(go(k_dispatch<uint16_t>, 2));
+  return MM_OK;
+}
+
+mm_status mm_expert_combine(const mm_expert_desc* d, const void* rows, const int32_t* row_of_slot,
+                            const float* weights, void* y, void* stream) {
+  mm_status s = check_desc(d, true);
+  if (s != MM_OK) return s;
+  const size_t es = d->type == MM_BF16 ? 2 : 4;
+  if (!aligned_to(rows, es) || !aligned_to(y, es) || !aligned_to(row_of_slot, 4) || !aligned_to(weights, 4))
+    return MM_ERR_INVALID_ARG;
+  if (d->T == 0) return MM_OK;
+  if (!rows || !row_of_slot || !y) return MM_ERR_INVALID_ARG;
+  clear_error();
+  RowArgs a = row_args(*d);
+  a.rows = rows;
+  a.row_of_slot = row_of_slot;
+  a.weights = weights;
+  a.out_x = y;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool wide = d->H % 8 == 0 && aligned_to(rows, 16) && aligned_to(y, 16);
+  a.words = (int)(wide ? d->H / 8 : d->H);
+  auto go = [&](auto* kernel) {
+    return launch_pdl(kernel, dim3((unsigned)d->T), dim3(threads_for(a.words)), 0, st, a);
+  };
+  if (d->type == MM_BF16)
+    MM_TRY(wide ? go(k_combine<__nv_bfloat16, 8>) : go(k_combine<__nv_bfloat16, 1>));
+  else
+    MM_TRY(wide ? go(k_combine<float, 8>) : go(k_combine<float, 1>));
+  return MM_OK;
+}
+
+mm_status mm_expert_combine_backward(const mm_expert_desc* d, const void* dy, const void* rows,
+                                     const int32_t* offsets, const int32_t* row_of_slot,
+                                     const float* weights, void* d_rows, float* d_weights,
+                                     void* stream) {
+  mm_status s = check_desc(d, true);
+  if (s != MM_OK) return s;
+  const size_t es = d->type == MM_BF16 ? 2 : 4;
+  if (!aligned_to(dy, es) || !aligned_to(rows, es) || !aligned_to(d_rows, es) || !aligned_to(offsets, 4) ||
+      !aligned_to(row_of_slot, 4) || !aligned_to(weights, 4) || !aligned_to(d_weights, 4))
+    return MM_ERR_INVALID_ARG;
+  if (d->T == 0) return MM_OK;
+  if (!dy || !offsets || !row_of_slot || !d_rows || (d_weights && !rows)) return MM_ERR_INVALID_ARG;
+  clear_error();
+  RowArgs a = row_args(*d);
+  a.x = dy;
+  a.rows = rows;
+  a.offsets = offsets;
+  a.row_of_slot = row_of_slot;
+  a.weights = weights;
+  a.out_rows = d_rows;
+  a.d_weights = d_weights;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool wide = d->H % 8 == 0 && aligned_to(dy, 16) && aligned_to(rows, 16) && aligned_to(d_rows, 16);
+  a.words = (int)(wide ? d->H / 8 : d->H);
+  auto go = [&](auto* kernel) {
+    return launch_pdl(kernel, dim3((unsigned)d->T), dim3(threads_for(a.words)), 0, st, a);
+  };
+  if (d->type == MM_BF16)
+    MM_TRY(wide ? go(k_combine_bwd<__nv_bfloat16, 8>) : go(k_combine_bwd<__nv_bfloat16, 1>));
+  else
+    MM_TRY(wide ? go(k_combine_bwd<float, 8>) : go(k_combine_bwd<float, 1>));
+  return MM_OK;
+}
+
+}  // extern "C"

@@ -1,20 +1,202 @@
 """PyTorch entry points of the operators for experts of a caller's own form (include/mm_experts.h).
 
-    out = grouped_mm(rows, weight, offsets)             # each expert's rows times its matrix
+The fused layer (torch_api) is one SwiGLU expert in bf16. Experts with another activation, a bias,
+adapters or results in 32 bits are built from its parts:
 
-`grouped_mm` is differentiable once (a second derivative is refused); the `*_forward` / `*_backward`
-functions are the calls it makes. As in block_ops: argument marshalling only, on the current stream of
-the tensors' device; non-contiguous tensors are copied to contiguous ones.
+    ids, weights, *_ = moe_router(logits, k)                     # block_ops
+    table = expert_table(ids, num_experts)                       # the slots' order by expert
+    rows  = expert_dispatch(x, table)                            # the tokens' rows in that order
+    h     = grouped_mm(rows, w1, table.offsets)                  # each expert's rows times its matrix
+    h     = torch.nn.functional.gelu(h)
+    o     = grouped_mm(h, w2, table.offsets)
+    y     = expert_combine(o, table, weights)                    # each token's weighted sum
+
+Any number of tokens, one included. `expert_dispatch`, `grouped_mm` and `expert_combine` are
+differentiable once (a second derivative is refused); the `*_forward` / `*_backward` functions are the
+calls they make. As in block_ops: argument marshalling only, on the current stream of the tensors'
+device; non-contiguous tensors are copied to contiguous ones.
 """
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
 from . import _abi
 from ._first_order import first_order_only
-from .block_ops import _aligned, _contiguous, _elsewhere, _on_gpu, _Plans, _sig, _stream, _type
+from .block_ops import _aligned, _contiguous, _elsewhere, _on_gpu, _Plans, _ptr, _sig, _stream, _type
+
+# ------------------------------------------------------------------------------- order and rows
+
+_table_plans, _row_plans = _Plans(), _Plans()
+
+
+class ExpertTable(NamedTuple):
+    """The order of a selection's slots s = t k + j by expert, equal ones by s."""
+    offsets: torch.Tensor      # int32 [E+1]: where each expert's rows start, and where the last one's end
+    row_of_slot: torch.Tensor  # int32 [T,k]: place of a slot, -1 for one without an expert
+    slot_of_row: torch.Tensor  # int32 [T k]: slot at a place, -1 behind offsets[E]
+    T: int
+    K: int
+    E: int
+
+
+def expert_table(topk_ids, num_experts):
+    """ExpertTable of topk_ids [T,k] (int32 or int64). A slot whose id is outside [0, num_experts) has no
+    expert: nobody computes it, and it adds nothing to its token."""
+    if _elsewhere(topk_ids):
+        with torch.cuda.device(topk_ids.device):
+            return expert_table(topk_ids, num_experts)
+    E = int(num_experts)
+    key = (_sig(topk_ids), E)
+    plan = _table_plans.get(key)
+    if plan is None:
+        _on_gpu("expert_table", topk_ids)
+        if topk_ids.dim() != 2 or topk_ids.dtype not in (torch.int32, torch.int64):
+            raise ValueError("expected topk_ids[T,k] in int32 or int64")
+        T, K = topk_ids.shape
+        d = _abi.mm_expert_desc(T, 0, E, K, 0)
+        at = ctypes.addressof(d)
+        nbytes = int(_abi._lib().mm_expert_table_workspace_size(at))
+        if nbytes == 0:
+            raise ValueError(f"unsupported sizes T={T} k={K} num_experts={E}")
+        plan = _table_plans.remember(key, (at, nbytes, T, K, d))
+    at, nbytes, T, K, _ = plan
+    if topk_ids.dtype == torch.int64:  # (a number beyond 32 bits must not become an expert's)
+        topk_ids = topk_ids.clamp(-1, E).to(torch.int32)
+    ids, dev = _contiguous(topk_ids), topk_ids.device
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    row = torch.empty((T, K), dtype=torch.int32, device=dev)
+    slot = torch.empty(T * K, dtype=torch.int32, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _abi.check(_abi._lib().mm_expert_table(
+        at, ids.data_ptr(), offsets.data_ptr(), row.data_ptr(), slot.data_ptr(), ws.data_ptr(), nbytes,
+        _stream(ids)), "mm_expert_table")
+    return ExpertTable(offsets, row, slot, T, K, E)
+
+
+def _row_plan(op, table, tokens, rows, weights, key):
+    """Checks the inputs; (address of the descriptor, descriptor). tokens [T,H], rows [T k,H], weights
+    [T,k]: those of them that the call has."""
+    first = tokens if tokens is not None else rows
+    _on_gpu(op, first, tokens, rows, weights, table.offsets, table.row_of_slot)
+    T, K, E = table.T, table.K, table.E
+    for name, t, shape in (("offsets", table.offsets, (E + 1,)), ("row_of_slot", table.row_of_slot, (T, K))):
+        if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"expected the table's {name} of shape {shape} in int32, contiguous")
+    if first.dim() != 2:
+        raise ValueError("expected rows of shape [n,H]")
+    H = first.shape[1]
+    for name, t, n in (("tokens", tokens, T), ("rows", rows, T * K)):
+        if t is not None and t.shape != (n, H):
+            raise ValueError(f"expected the {name}' rows of shape [{n},{H}]")
+        if t is not None and t.dtype != first.dtype:
+            raise TypeError(f"{op}: all rows must have one dtype")
+    if weights is not None and (weights.shape != (T, K) or weights.dtype != torch.float32):
+        raise ValueError("expected weights[T,k] in float32")
+    d = _abi.mm_expert_desc(T, H, E, K, _type("rows", first))
+    return _row_plans.remember(key, (ctypes.addressof(d), d))
+
+
+def dispatch_forward(x, table):
+    """rows [T k,H]: row r is x[t] for the token t of the slot at place r; zeros behind offsets[E]."""
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return dispatch_forward(x, table)
+    key = ("dispatch", _sig(x), _sig(table.offsets), _sig(table.row_of_slot), table[3:])
+    at, _ = _row_plans.get(key) or _row_plan("expert_dispatch", table, x, None, None, key)
+    x = _contiguous(x)
+    rows = torch.empty((table.T * table.K, x.shape[1]), dtype=x.dtype, device=x.device)
+    _abi.check(_abi._lib().mm_expert_dispatch(
+        at, x.data_ptr(), table.offsets.data_ptr(), table.row_of_slot.data_ptr(), rows.data_ptr(),
+        _stream(x)), "mm_expert_dispatch")
+    return rows
+
+
+def combine_forward(rows, table, weights=None):
+    """y [T,H]: y[t] = sum_j weights[t,j] rows[place of slot (t, j)], over the slots with an expert
+    (weights fp32 [T,k]; None: 1). rows bfloat16 or float32."""
+    if _elsewhere(rows):
+        with torch.cuda.device(rows.device):
+            return combine_forward(rows, table, weights)
+    key = ("combine", _sig(rows), _sig(weights), _sig(table.offsets), _sig(table.row_of_slot), table[3:])
+    at, _ = _row_plans.get(key) or _row_plan("expert_combine", table, None, rows, weights, key)
+    rows, weights = _contiguous(rows), _contiguous(weights)
+    y = torch.empty((table.T, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+    _abi.check(_abi._lib().mm_expert_combine(
+        at, rows.data_ptr(), table.row_of_slot.data_ptr(), _ptr(weights), y.data_ptr(), _stream(rows)),
+        "mm_expert_combine")
+    return y
+
+
+def combine_backward(dy, rows, table, weights=None, *, weight_grad=True):
+    """(d_rows [T k,H], d_weights fp32 [T,k]) for dy [T,H]: d_rows[place] = weight * dy[token] (zeros
+    behind offsets[E]), d_weights = <dy[token], rows[place]> (None without weight_grad: `rows` may be
+    None then)."""
+    if _elsewhere(dy):
+        with torch.cuda.device(dy.device):
+            return combine_backward(dy, rows, table, weights, weight_grad=weight_grad)
+    if not weight_grad:
+        rows = None
+    key = ("backward", _sig(dy), _sig(rows), _sig(weights), _sig(table.offsets), _sig(table.row_of_slot), table[3:])
+    plan = _row_plans.get(key)
+    if plan is None:
+        if weight_grad and rows is None:
+            raise ValueError("the weights' gradient needs the rows")
+        plan = _row_plan("expert_combine", table, dy, rows, weights, key)
+    dy, rows, weights = _contiguous(dy), _contiguous(rows), _contiguous(weights)
+    d_rows = torch.empty((table.T * table.K, dy.shape[1]), dtype=dy.dtype, device=dy.device)
+    d_weights = None
+    if weight_grad:
+        d_weights = torch.empty((table.T, table.K), dtype=torch.float32, device=dy.device)
+    _abi.check(_abi._lib().mm_expert_combine_backward(
+        plan[0], dy.data_ptr(), _ptr(rows), table.offsets.data_ptr(), table.row_of_slot.data_ptr(),
+        _ptr(weights), d_rows.data_ptr(), _ptr(d_weights), _stream(dy)), "mm_expert_combine_backward")
+    return d_rows, d_weights
+
+
+class DispatchFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, table):
+        ctx.save_for_backward(*table[:3])
+        ctx.sizes = table[3:]
+        return dispatch_forward(x, table)
+
+    @staticmethod
+    def backward(ctx, d_rows):
+        table = ExpertTable(*ctx.saved_tensors, *ctx.sizes)
+        return (*first_order_only("expert_dispatch", (combine_forward(d_rows, table),), (d_rows,)), None)
+
+
+def expert_dispatch(x, table):
+    """dispatch_forward with a gradient for x."""
+    return DispatchFunction.apply(x, table)
+
+
+class CombineFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weights, table):
+        ctx.save_for_backward(rows, weights, *table[:3])
+        ctx.sizes = table[3:]
+        return combine_forward(rows, table, weights)
+
+    @staticmethod
+    def backward(ctx, dy):
+        rows, weights, *order = ctx.saved_tensors
+        d_rows, d_weights = combine_backward(dy, rows, ExpertTable(*order, *ctx.sizes), weights,
+                                             weight_grad=ctx.needs_input_grad[1])
+        return (*first_order_only("expert_combine", (d_rows, d_weights), (rows, weights, dy)), None)
+
+
+def expert_combine(rows, table, weights=None):
+    """combine_forward with gradients for rows and weights (any floating type)."""
+    if weights is not None:
+        if not weights.is_floating_point():
+            raise TypeError("weights must be floating point")
+        weights = weights.to(torch.float32)
+    return CombineFunction.apply(rows, weights, table)
+
 
 # ------------------------------------------------------------------------------- grouped products
 
@@ -132,6 +314,7 @@ def grouped_mm_weight_grad(rows, d_out, offsets, weight, *, dtype=None, into=Non
         flags, key, d_out)
     rows, d_out, offsets = _aligned(rows), _aligned(d_out), _index32(offsets, rows.shape[0])
     if into is not None:
+        torch.autograd.graph.increment_version(into)
         out = into.transpose(1, 2) if transposed else into
     else:
         out = torch.empty((E, N, K) if transposed else (E, K, N), dtype=dtype, device=rows.device)

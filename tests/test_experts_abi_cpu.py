@@ -79,3 +79,83 @@ def test_grouped_host_checks():
                 assert call(grouped(), *full[:i], p, *full[i + 1:]) == BAD
     assert product(grouped(R=0), None, None, None, None) == _abi.MM_OK
     assert weight(grouped(R=0), None, None, None, 16) == BAD  # zeros have to go somewhere
+
+
+def test_expert_host_checks():
+    lib = _abi._lib()
+
+    def desc(T=8, H=64, E=4, K=2, type=0):
+        return _abi.mm_expert_desc(T, H, E, K, type)
+
+    def table(d, *p, w=256, size=1 << 30):
+        return lib.mm_expert_table(ref(d), *p, w, size, None)
+
+    def dispatch(d, *p):
+        return lib.mm_expert_dispatch(ref(d), *p, None)
+
+    def combine(d, *p):
+        return lib.mm_expert_combine(ref(d), *p, None)
+
+    def backward(d, *p):
+        return lib.mm_expert_combine_backward(ref(d), *p, None)
+
+    four, seven = (16,) * 4, (16,) * 7
+    assert lib.mm_expert_table(None, *four, 256, 1 << 30, None) == BAD
+    for d in (desc(T=-1), desc(E=0), desc(K=0)):
+        assert table(d, *four) == BAD and lib.mm_expert_table_workspace_size(ref(d)) == 0
+        assert dispatch(d, *four) == BAD and combine(d, *four) == BAD and backward(d, *seven) == BAD
+    for d in (desc(E=1025), desc(K=17), desc(T=2 ** 31 - 1), desc(T=2 ** 40)):
+        assert table(d, *four) == UNSUP and lib.mm_expert_table_workspace_size(ref(d)) == 0
+        assert dispatch(d, *four) == UNSUP and combine(d, *four) == UNSUP and backward(d, *seven) == UNSUP
+    for d in (desc(H=0), desc(type=2)):
+        assert dispatch(d, *four) == BAD and combine(d, *four) == BAD and backward(d, *seven) == BAD
+    big = desc(H=2 ** 20 + 1)
+    assert dispatch(big, *four) == UNSUP and combine(big, *four) == UNSUP and backward(big, *seven) == UNSUP
+    d, f = desc(), desc(type=1)
+    n = lib.mm_expert_table_workspace_size(ref(d))
+    assert n >= 256
+    assert table(d, *four, size=n - 1) == WS and table(d, *four, w=None) == WS and table(d, *four, w=64) == WS
+    for i in range(4):
+        for p in (None, 2):
+            assert table(d, *four[:i], p, *four[i + 1:]) == BAD
+        if i != 2:
+            assert combine(d, *four[:i], None, *four[i + 1:]) == (BAD if i != 2 else 0)
+        assert dispatch(f, *four[:i], 2, *four[i + 1:]) == BAD and combine(f, *four[:i], 2, *four[i + 1:]) == BAD
+        assert dispatch(d, *four[:i], None, *four[i + 1:]) == BAD
+    for i in range(7):
+        assert backward(f, *seven[:i], 2, *seven[i + 1:]) == BAD
+        if i not in (4, 6):  # no weights: 1; no d_weights: not wanted
+            assert backward(d, *seven[:i], None, *seven[i + 1:]) == BAD
+    empty = desc(T=0)
+    assert dispatch(empty, *[None] * 4) == combine(empty, *[None] * 4) == backward(empty, *[None] * 7) == _abi.MM_OK
+
+
+def test_grad_host_checks():
+    lib = _abi._lib()
+
+    def refs(*items):
+        return (_abi.mm_tensor_ref * len(items))(*[_abi.mm_tensor_ref(*i) for i in items])
+
+    def norm(t, n=None, out=16, w=256, size=1 << 30):
+        return lib.mm_grad_norm(len(t) if n is None else n, ctypes.addressof(t) if t else None, out, w, size, None)
+
+    def clip(t, max_norm=1.0, eps=1e-6, n=None, out=16, w=256, size=1 << 30):
+        return lib.mm_grad_clip(len(t) if n is None else n, ctypes.addressof(t) if t else None, max_norm, eps, out, w,
+                                size, None)
+
+    good = refs((32, 32, 5, 0, 0))
+    for call in (norm, clip):
+        assert call(good, n=-1) == BAD and call(good, n=2 ** 20) == UNSUP and call(None, n=1) == BAD
+        assert call(good, out=None) == BAD and call(good, out=2) == BAD
+        assert call(good, w=None) == WS and call(good, w=64) == WS
+        assert call(good, size=lib.mm_grad_workspace_size(1) - 1) == WS
+        for t in ((32, 32, -1, 0, 0), (32, 32, 5, 2, 0), (None, 32, 5, 0, 0), (33, 33, 5, 0, 0), (34, 34, 5, 1, 1)):
+            assert call(refs(t)) == BAD
+        assert call(refs((32, 32, 1 << 44, 0, 0))) == UNSUP
+    for t in ((32, None, 5, 0, 0), (32, 64, 5, 0, 2), (32, 66, 5, 0, 1), (32, 32, 5, 0, 1)):
+        assert clip(refs(t)) == BAD
+    for value in (-1.0, float("nan")):
+        assert clip(good, max_norm=value) == BAD and clip(good, eps=value) == BAD
+    assert clip(good, eps=float("inf")) == BAD
+    assert lib.mm_grad_workspace_size(-1) == lib.mm_grad_workspace_size(2 ** 20) == 0
+    assert lib.mm_grad_workspace_size(0) >= 256
