@@ -92,6 +92,36 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, kWaitNs));
 }
 
+// A value that all lanes share, in the form the compiler knows to be shared: what an issue of a copy or a
+// product takes is then in uniform registers, and no loop over the lanes' values stands around it.
+__device__ __forceinline__ int uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
+
+// A ring of barriers as one warp in step walks it. The next one is asked for before the present one's
+// work is issued, so that the answer's latency passes behind it.
+struct Ring {
+  uint32_t bar0, phase;  // first barrier; parity to wait for
+  int stages, s = 0;
+  bool ready = false;
+  __device__ __forceinline__ Ring(uint32_t bar, uint32_t first, int n) : bar0(bar), phase(first), stages(n) {}
+  __device__ __forceinline__ bool wait() {
+    if (__all_sync(0xFFFFFFFFu, ready)) return true;
+    return warp_wait(bar0 + 8u * s, phase);
+  }
+  __device__ __forceinline__ void ask_next() {
+    const bool wrap = s + 1 == stages;
+    ready = mbar_test_wait(bar0 + 8u * (wrap ? 0 : s + 1), wrap ? phase ^ 1u : phase);
+  }
+  __device__ __forceinline__ void next() {
+    if (++s == stages) s = 0, phase ^= 1u;
+  }
+  __device__ __forceinline__ void skip(int n) {  // n stages that another warp walks
+    ready = false;
+    s += n;
+    if (s / stages & 1) phase ^= 1u;
+    s %= stages;
+  }
+};
+
 // Where the experts' rows start (E + 1 numbers) and how many tiles of rows the experts before each
 // have, in shared memory. False if the offsets are no such table.
 template <bool WEIGHTS>
@@ -272,30 +302,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int units = !good ? 0 : WEIGHTS ? a.E * i_tiles * j_tiles : first_tile[a.E] * i_tiles;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int u = mine; u < units && ok; u += step) {
-        const Unit t = unit_at<WEIGHTS, PAIR>(a, start, first_tile, u, i_tiles, j_tiles, rank);
-        const int half = t.n16 / PAIR, blocks = (t.k + 63) / 64;
-        const uint32_t bytes = kABytes + (WEIGHTS ? (half + 63) / 64 * kBlock : half * 128u);
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
-          const uint32_t s = it % a.stages, ph = it / a.stages & 1u;
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, kWaitNs)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = sbase + s * a.stage_bytes, sb = sa + kABytes;
+    // ------------------------------------------------ loads
+    Ring ring(empty_bar(0), 1, a.stages);
+    int it = 0;
+    bool ok = true;
+    const bool kmajor = a.a_kmajor != 0;
+    for (int u = mine; u < units && ok; u += step) {
+      const Unit t = unit_at<WEIGHTS, PAIR>(a, start, first_tile, u, i_tiles, j_tiles, rank);
+      const int half = uniform(t.n16 / PAIR), blocks = uniform((t.k + 63) / 64);
+      const int e = uniform(t.e), i0 = uniform(t.i0), row0 = uniform(t.row0);
+      const int j0 = uniform(t.j0 + rank * (t.n16 / PAIR));
+      const bool mend = uniform(t.k & 15) != 0;
+      const uint32_t bytes = kABytes + (WEIGHTS ? (half + 63) / 64 * kBlock : half * 128u);
+      for (int kb = 0; kb < blocks; ++kb, ++it) {
+        if (!ring.wait()) {
+          ok = false;
+          break;
+        }
+        ring.ask_next();
+        if (elect_one()) {
+          const uint32_t sa = sbase + ring.s * a.stage_bytes, sb = sa + kABytes;
           const int k0 = kb * 64;
           // the two CTAs' bytes of a stage count on the even one's barrier, but those of a block that
           // is to be mended in place each on its own
-          const bool tail = WEIGHTS && PAIR == 2 && kb == blocks - 1 && (t.k & 15) != 0;
-          uint32_t bar = full_bar(s);
+          const bool tail = WEIGHTS && PAIR == 2 && kb == blocks - 1 && mend;
+          uint32_t bar = full_bar(ring.s);
           if (tail) {
-            if (rank == 1) bar = tail_bar(s);
+            if (rank == 1) bar = tail_bar(ring.s);
             mbar_arrive_expect_tx(bar, bytes);
-          } else {
-            if (rank == 0) mbar_arrive_expect_tx(bar, PAIR * bytes);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(bar, PAIR * bytes);
           }
           if constexpr (PAIR == 2) bar = mapa_shared(bar, tail ? rank : 0);
           auto load2 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
@@ -307,55 +343,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tma_load_3d(dst, map, bar, c0, c1, c2);
           };
           if constexpr (WEIGHTS) {
-            load2(sa, &m.a, t.i0, t.row0 + k0);
-            load2(sa + kBlock, &m.a, t.i0 + 64, t.row0 + k0);
-            for (int c = 0; c < half; c += 64)
-              load2(sb + c / 64 * kBlock, &m.b[0], t.j0 + rank * half + c, t.row0 + k0);
+            load2(sa, &m.a, i0, row0 + k0);
+            load2(sa + kBlock, &m.a, i0 + 64, row0 + k0);
+#pragma unroll
+            for (int c = 0; c < kMaxN / PAIR; c += 64)
+              if (c < half) load2(sb + c / 64 * kBlock, &m.b[0], j0 + c, row0 + k0);
           } else {
-            if (a.a_kmajor) {
-              load3(sa, &m.a, k0, t.i0, t.e);
+            if (kmajor) {
+              load3(sa, &m.a, k0, i0, e);
             } else {
-              load3(sa, &m.a, t.i0, k0, t.e);
-              load3(sa + kBlock, &m.a, t.i0 + 64, k0, t.e);
+              load3(sa, &m.a, i0, k0, e);
+              load3(sa + kBlock, &m.a, i0 + 64, k0, e);
             }
-            int r = 0;  // half = 128 + 64 + ... as its bits are
-            if (half == 256) {
-              load2(sb, &m.b[0], k0, t.j0);
-              load2(sb + 128 * 128, &m.b[0], k0, t.j0 + 128);
-              r = 256;
+            // boxes as half's bits are (256: 128 twice)
+            int r = 0;
+            if (PAIR == 1 && (half & 256)) {
+              load2(sb, &m.b[0], k0, j0);
+              load2(sb + 128 * 128, &m.b[0], k0, j0 + 128);
             }
 #pragma unroll
             for (int p = 0; p < 5; ++p) {
-              const int h = 128 >> p;
-              if (half - r >= h) {
-                load2(sb + r * 128, &m.b[p], k0, t.j0 + rank * half + r);
-                r += h;
+              if (half & (128 >> p)) {
+                load2(sb + r * 128, &m.b[p], k0, j0 + r);
+                r += 128 >> p;
               }
             }
           }
         }
-      }
-      // every stage's last release has landed before this CTA may leave
-      for (uint32_t s = 0; s < (uint32_t)a.stages && ok; ++s) {
-        if (it <= s) break;
-        ok = mbar_wait(empty_bar(s), (it - 1 - s) / a.stages & 1u, kWaitNs);
+        __syncwarp();
+        ring.next();
       }
     }
+    // every stage's last release has landed before this CTA may leave
+    for (int s = 0; s < a.stages && s < it && ok; ++s)
+      ok = warp_wait(empty_bar(s), (it - 1 - s) / a.stages & 1u);
   } else if (warp == 1) {
-    uint32_t it = 0, acc = 0, tails = 0;
+    // ------------------------------------------------ multiplies
+    // The warp stays in step and an elected lane issues from uniform registers.
+    Ring ring(full_bar(0), 0, a.stages);
+    const int a_mn = WEIGHTS || !a.a_kmajor, b_mn = WEIGHTS;
+    const uint64_t adesc = sdesc_sw128(sbase, a_mn ? kBlock : 16, 1024);
+    const uint64_t bdesc = sdesc_sw128(sbase + kABytes, b_mn ? kBlock : 16, 1024);
+    const uint32_t a_step = a_mn ? 2048 / 16 : 2, b_step = b_mn ? 2048 / 16 : 2;
+    uint32_t acc = 0, tails = 0;
     bool ok = true;
     for (int u = mine; u < units && ok; u += step) {
       const Unit t = unit_at<WEIGHTS, PAIR>(a, start, first_tile, u, i_tiles, j_tiles, rank);
-      if (t.k == 0) continue;
-      const int blocks = (t.k + 63) / 64, half = t.n16 / PAIR;
+      const int blocks = uniform((t.k + 63) / 64), n16 = uniform(t.n16);
+      if (blocks == 0) continue;
+      const int last = uniform(t.k) - (blocks - 1) * 64;  // terms in the last block
+      const bool mend = WEIGHTS && (last & 15) != 0;
       const uint32_t buf = acc & 1u;
       const uint32_t d = tmem + buf * kMaxN;
-      const int last = t.k - (blocks - 1) * 64;  // terms in the last block
-      const bool mend = WEIGHTS && (last & 15) != 0;
       // sets the rows of the next expert to zero in this CTA's part of stage s
       auto zero_rows = [&](uint32_t s) {
         const uint32_t sa = sbase + s * a.stage_bytes;
-        const int parts = 2 + (half + 63) / 64, end = ((last + 15) & ~15) * 128;
+        const int parts = 2 + (n16 / PAIR + 63) / 64, end = ((last + 15) & ~15) * 128;
         for (int p = 0; p < parts; ++p)
           for (int at = last * 128 + lane * 16; at < end; at += 512)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
@@ -366,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       if (PAIR == 2 && rank == 1) {  // the even CTA issues; this one mends its part
-        it += blocks;
+        ring.skip(blocks - 1);
         if (mend) {
-          const uint32_t s = (it - 1) % a.stages;
+          const uint32_t s = ring.s;
           if (!warp_wait(tail_bar(s), tails >> s & 1u)) {
             ok = false;
             break;
@@ -377,20 +420,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           zero_rows(s);
           if (lane == 0) mbar_arrive_remote(mapa_shared(fixed_bar(s), 0));
         }
+        ring.next();
         continue;
       }
       if (!warp_wait(acce_bar(buf), (acc >> 1 & 1u) ^ 1u)) break;
       tc_fence_after();
-      const int a_mn = WEIGHTS || !a.a_kmajor, b_mn = WEIGHTS;
-      const uint32_t idesc = idesc_bf16_f32(kTile * PAIR, t.n16, a_mn, b_mn);
-      for (int kb = 0; kb < blocks; ++kb, ++it) {
-        const uint32_t s = it % a.stages;
-        if (!warp_wait(full_bar(s), it / a.stages & 1u)) {
+      const uint32_t idesc = idesc_bf16_f32(kTile * PAIR, n16, a_mn, b_mn);
+      for (int kb = 0; kb < blocks; ++kb) {
+        if (!ring.wait()) {
           ok = false;
           break;
         }
+        const uint32_t s = ring.s;
+        ring.ask_next();
         int steps = 4;
-        if (kb == blocks - 1) {
+        if (WEIGHTS && kb == blocks - 1) {
           steps = (last + 15) / 16;
           if (mend) {
             zero_rows(s);
@@ -404,25 +448,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t sa = sbase + s * a.stage_bytes, sb = sa + kABytes;
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint64_t ad = sdesc_sw128(sa + kk * (a_mn ? 2048 : 32), a_mn ? kBlock : 16, 1024);
-            const uint64_t bd = sdesc_sw128(sb + kk * (b_mn ? 2048 : 32), b_mn ? kBlock : 16, 1024);
-            if constexpr (PAIR == 2) umma_bf16_pair(d, ad, bd, idesc, (kb | kk) != 0);
-            else umma_bf16(d, ad, bd, idesc, (kb | kk) != 0);
+        if (elect_one()) {
+          const uint64_t ad = adesc + s * (a.stage_bytes / 16), bd = bdesc + s * (a.stage_bytes / 16);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (WEIGHTS && kk >= steps) continue;
+            if constexpr (PAIR == 2) umma_bf16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb | kk) != 0);
+            else umma_bf16(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb | kk) != 0);
           }
           if constexpr (PAIR == 2) umma_commit_pair_mc(empty_bar(s), 0x3);
           else umma_commit(empty_bar(s));
+          if (kb == blocks - 1) {
+            if constexpr (PAIR == 2) umma_commit_pair_mc(accf_bar(buf), 0x3);
+            else umma_commit(accf_bar(buf));
+          }
         }
         __syncwarp();
+        ring.next();
       }
-      if (!ok) break;
-      if (lane == 0) {
-        if constexpr (PAIR == 2) umma_commit_pair_mc(accf_bar(buf), 0x3);
-        else umma_commit(accf_bar(buf));
-      }
-      __syncwarp();
       ++acc;
     }
   } else {
@@ -590,7 +633,13 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
     return MM_ERR_WORKSPACE;
   clear_error();
   MM_TRY(bind_context());
-  const int pair = d->flags & MM_GROUPED_CTA_PAIRS ? 2 : 1;
+  // Pairs read half as much of their operands per product. Where a launch has no more tiles of one CTA
+  // than SMs, these spread the matrices' columns over twice as many. (us a call, one CTA a tile and pairs:
+  // 8 rows of 8 of 128 experts, 2048 -> 1536, 13.1 and 13.8; 512 rows of 128, 768 -> 2048, 73.5 and 66.0;
+  // 131072 rows of 128, 2048 -> 1536, 592 and 528.)
+  const int64_t chunks = d->R / kMaxN + std::min<int64_t>(d->E, d->R);  // at most
+  const bool few = chunks * ((d->N + kTile - 1) / kTile) <= device_sm_count();
+  const int pair = d->flags & MM_GROUPED_CTA_PAIRS || (d->flags == 0 && !few) ? 2 : 1;
   Maps m;
   Args a{};
   a.offsets = offsets;
@@ -610,7 +659,6 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   for (int p = 0; p < 5; ++p) ok = ok && map2(&m.b[p], rows, d->K, d->R, 128u >> p);
   if (!ok) return cuda_fail(cudaErrorInvalidValue, "grouped product tensor maps");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t chunks = d->R / a.chunk + std::min<int64_t>(d->E, d->R);  // at most
   const int64_t units = chunks * ((d->N + kTile * pair - 1) / (kTile * pair));
   if (pair == 2)
     MM_TRY((launch<2, false>(m, a, units, st)));
@@ -637,7 +685,7 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
       MM_TRY(cudaMemsetAsync(d_weight, 0, (size_t)d->E * d->K * d->N * (d->out_type == MM_FP32 ? 4 : 2), st));
     return MM_OK;
   }
-  const int pair = d->flags & MM_GROUPED_CTA_PAIRS ? 2 : 1;
+  const int pair = d->flags & MM_GROUPED_SINGLE_CTA ? 1 : 2;
   Maps m;
   Args a{};
   a.offsets = offsets;
