@@ -209,38 +209,60 @@ __device__ __forceinline__ void fill(void* p, int64_t words, uint32_t v, int thr
   for (int64_t i = thread; i < words; i += threads) w[i] = make_uint4(v, v, v, v);
 }
 
-// Up to 32 columns of the accumulator (this lane: one i) to rows j of the output.
-__device__ __forceinline__ void store_columns(const Args& a, float (&v)[32], int64_t row, int i, int n,
-                                              int lane) {
-  if (a.f32) {
-    float* p = static_cast<float*>(a.out) + row * a.I + i;
+// Up to 32 columns of the accumulator (this lane: one i) to rows row .. of the output; n: how many there
+// are. The address of a row is that of the one before plus the pitch, as 64-bit products per element were
+// most of an epilogue's instructions.
+template <bool F32, bool ADD, bool FULL>
+__device__ __forceinline__ void store_rows(const Args& a, const float (&v)[32], int64_t row, int i, int n,
+                                           int lane) {
+  if constexpr (F32) {
     if (i >= a.I) return;
-    if (a.accumulate) {
+    float* p = static_cast<float*>(a.out) + row * a.I + i;
+    float old[32];
+    if constexpr (ADD) {
+      const float* at = p;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) v[j] += p[(int64_t)j * a.I];
+      for (int j = 0; j < 32; ++j, at += a.I) old[j] = FULL || j < n ? *at : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) p[(int64_t)j * a.I] = v[j];
-    return;
-  }
-  // two neighbouring lanes exchange, so that each has a pair of neighbouring columns of one row
-  const bool odd = lane & 1;
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + (row + odd) * a.I + (i & ~1);
+    for (int j = 0; j < 32; ++j, p += a.I)
+      if (FULL || j < n) *p = ADD ? v[j] + old[j] : v[j];
+  } else {
+    // Two neighbouring lanes exchange, so that each has a pair of neighbouring columns of one row: the
+    // even lane of row j, the odd one of row j + 1.
+    const int odd = lane & 1;
+    const bool there = i < a.I;
+    const uint32_t halves = odd ? 0x3276 : 0x5410;
+    uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row + odd) * a.I + (i & ~1));
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
-    float lo = odd ? other : v[j], hi = odd ? v[j + 1] : other;
-    if (j + odd < n && i < a.I) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(p + (int64_t)j * a.I);
-      if (a.accumulate) {
-        const uint32_t old = *at;
-        lo += bf16_lo(old);
-        hi += bf16_hi(old);
+    for (int j = 0; j < 32; j += 2, p += a.I) {
+      if constexpr (ADD) {  // (the sum is rounded, not its addend)
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+        if (there && (FULL || j + odd < n)) {
+          const uint32_t old = *p;
+          *p = pack_bf16((odd ? other : v[j]) + bf16_lo(old), (odd ? v[j + 1] : other) + bf16_hi(old));
+        }
+      } else {
+        const uint32_t mine = pack_bf16(v[j], v[j + 1]);
+        const uint32_t both = __byte_perm(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1), halves);
+        if (there && (FULL || j + odd < n)) *p = both;
       }
-      *at = pack_bf16(lo, hi);
     }
+  }
+}
+
+__device__ __forceinline__ void store_columns(const Args& a, const float (&v)[32], int64_t row, int i, int n,
+                                              int lane) {
+  const bool full = n >= 32;
+  if (a.accumulate) {
+    if (a.f32) store_rows<true, true, false>(a, v, row, i, n, lane);
+    else store_rows<false, true, false>(a, v, row, i, n, lane);
+  } else if (a.f32) {
+    if (full) store_rows<true, false, true>(a, v, row, i, n, lane);
+    else store_rows<true, false, false>(a, v, row, i, n, lane);
+  } else {
+    if (full) store_rows<false, false, true>(a, v, row, i, n, lane);
+    else store_rows<false, false, false>(a, v, row, i, n, lane);
   }
 }
 
