@@ -86,6 +86,9 @@ mm_status mm_expert_combine_backward(const mm_expert_desc* d, const void* dy, co
 #define MM_GROUPED_SINGLE_CTA 0x1u /* flags: one CTA per tile */
 #define MM_GROUPED_CTA_PAIRS 0x2u  /* flags: tiles shared by two CTAs. Without either flag the form goes
                                       by the sizes; results are the same bit for bit. */
+/* flags, a test hook for the failure path: the first CTA withholds its first sum, and device waits are
+ * bounded by 50 ms instead of 2 s. The call ends with NaN where results are missing. */
+#define MM_GROUPED_TEST_STALL 0x80000000u
 typedef struct mm_grouped_desc {
   int64_t R, K, N;
   int32_t E;
@@ -94,13 +97,12 @@ typedef struct mm_grouped_desc {
   uint32_t flags;
 } mm_grouped_desc;
 
-/* Bytes of workspace that mm_grouped_mm and mm_grouped_mm_weight_grad need (0: unsupported sizes).
- * Needs no initialisation; one call at a time may use it. */
-size_t mm_grouped_workspace_size(const mm_grouped_desc* d);
-
 mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* weight,
-                        const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
-                        void* stream);
+                        const int32_t* offsets, void* out, void* stream);
+
+/* Bytes of workspace that mm_grouped_mm_weight_grad needs (0: unsupported sizes). Needs no
+ * initialisation; one call at a time may use it. */
+size_t mm_grouped_workspace_size(const mm_grouped_desc* d);
 
 /* accumulate: the sums are added to what d_weight holds (in 32 bits, one rounding); experts without
  * rows keep theirs. d_weight has W's layout. */

@@ -41,6 +41,7 @@ MM_SCORE_SOFTMAX = 0
 MM_SCORE_SIGMOID = 1
 MM_GROUPED_SINGLE_CTA = 0x1
 MM_GROUPED_CTA_PAIRS = 0x2
+MM_GROUPED_TEST_STALL = 0x80000000
 MM_TRACE_CTA = 0
 MM_TRACE_MAINLOOP = 1
 MM_TRACE_EPILOGUE = 2
@@ -175,7 +176,7 @@ def _lib():
         "mm_grad_clip": (st, [ctypes.c_int64, _P, ctypes.c_double, ctypes.c_double, _P, _P,
                               ctypes.c_size_t, _P]),
         "mm_grouped_workspace_size": (ctypes.c_size_t, [_P]),
-        "mm_grouped_mm": (st, [_P] * 6 + [ctypes.c_size_t, _P]),
+        "mm_grouped_mm": (st, [_P] * 6),
         "mm_grouped_mm_weight_grad": (st, [_P] * 5 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
     }
     for name, (res, args) in sig.items():

@@ -11,11 +11,20 @@
 // rows that a chunk's box reaches into are columns of the accumulator that nobody stores.
 //
 // A CTA: a warp that loads (TMA, a ring of stages of 64 k), a warp that issues the products into two
-// accumulators of 256 columns in turn, eight warps that store. PAIR: two CTAs share one M = 256 product
-// (.cta_group::2); each holds its 128 columns of the matrix and half of the rows.
+// accumulators of 256 columns in turn, eight warps that store, and one that deals out the tiles. PAIR: two
+// CTAs share one M = 256 product (.cta_group::2); each holds its 128 columns of the matrix and half of
+// the rows.
 //
-// With k = rows (weights) the last 16 rows of an expert's sum may reach into the next expert's; those
-// rows are set to zero in shared memory, in both operands (0 times an infinity would not be 0).
+// With k = rows (weights) the last 16 rows of an expert's sum may reach into the next expert's, whose
+// infinities would not vanish by a zero in the other operand. A launch before copies every expert's last
+// rows % 16 rows of both operands to panels of 16 rows filled up with zeros, from where the last step's
+// operands are loaded. (Zeros written over the loaded rows in shared memory stood in the way of every
+// tile's last block: 65536 rows of 128 experts, 2048 x 1536, 384 us, of which 80 were theirs; boxes of
+// exactly the rows there are took 444 for their number.)
+//
+// The dealing warp of the even CTA tells all others the tiles through a queue, ahead of their use. Rows'
+// tiles are much alike: every CTA has every step-th. Weights' tiles go by the experts' rows: they are
+// claimed from a counter, largest sums first.
 #include <algorithm>
 #include <atomic>
 
@@ -26,8 +35,9 @@
 namespace mm {
 namespace {
 
-constexpr int kThreads = 320;      // a warp that loads, one that multiplies, eight that store
-constexpr int kStoreWarps = 8;
+constexpr int kThreads = 352;      // warps that load, multiply and deal out tiles, eight that store
+constexpr int kStoreWarps = 8, kFirstStore = 3;
+constexpr int kQueue = 8;          // tiles told and not yet taken by all
 constexpr int kMaxE = 1024;
 constexpr int kTile = 128;         // columns of the M operand per CTA
 constexpr int kMaxN = 256;         // rows (or columns of the other dimension) per tile
@@ -35,13 +45,15 @@ constexpr int kMaxStages = 12;
 constexpr uint32_t kABytes = kTile * 64 * 2;
 constexpr uint32_t kBlock = 64 * 64 * 2;  // 64 elements of a MN-major operand over 64 k
 constexpr uint32_t kBarBytes = 512;
-constexpr uint32_t kTableBytes = 2 * 4 * (kMaxE + 1) + 8;
+constexpr uint32_t kTableBytes = 2 * 4 * (kMaxE + 1) + 8 + 2 * kMaxE;
+constexpr uint32_t kOutBytes = 32 * 64;   // a storing warp's 32 rows of 32 columns
 constexpr uint32_t kMostSmem = 227 * 1024;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull, kTestWaitNs = 50000000ull;
 
 struct Maps {
   CUtensorMap a;     // rows: a box of 128 columns of the matrix (K-major) or 64 (MN-major); weights: 64 x 64
   CUtensorMap b[5];  // rows: boxes of 128, 64, 32, 16, 8 rows; weights: b[0], 64 x 64
+  CUtensorMap a_part[3], b_part[3];  // weights: boxes of 64 columns and 32 and 16 rows, and 16 of the panels
 };
 
 struct Args {
@@ -55,14 +67,21 @@ struct Args {
   int stages;
   uint32_t stage_bytes;
   int f32, accumulate;
+  int* next;      // counter of claimed tiles, or null: every step-th
+  uint64_t wait_ns;
+  int stall;      // test hook: CTA 0 withholds its first accumulator
 };
 
-struct Unit {
-  int e, i0, j0;   // i0: first column of this CTA; j0: rows: first row of the chunk in all rows
-  int n, n16;      // columns of the accumulator that are stored and computed
+// A tile. 32 bytes, as the queue holds it.
+struct __align__(16) Unit {
+  int e, i0, j0;   // i0: first column of the (even) CTA; j0: rows: first row of the chunk in all rows
+  int n;           // columns of the accumulator that are stored; < 0: no more tiles
   int row0, k;     // weights: the expert's first row; terms of a sum
+  int unused[2];
+  __device__ __forceinline__ int n16() const { return (n + 15) & ~15; }
 };
 
+// mbar_wait for what the other CTA's threads wrote before they arrived.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
@@ -87,9 +106,18 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
-// A wait by all lanes of a warp, with one answer for them.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, kWaitNs));
+// Waits by all lanes of a warp, with one answer for them.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity, limit_ns));
+}
+
+__device__ __forceinline__ void st_shared_cluster(uint32_t cluster_addr, int4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
 }
 
 // A value that all lanes share, in the form the compiler knows to be shared: what an issue of a copy or a
@@ -102,10 +130,12 @@ struct Ring {
   uint32_t bar0, phase;  // first barrier; parity to wait for
   int stages, s = 0;
   bool ready = false;
-  __device__ __forceinline__ Ring(uint32_t bar, uint32_t first, int n) : bar0(bar), phase(first), stages(n) {}
+  uint64_t limit_ns;
+  __device__ __forceinline__ Ring(uint32_t bar, uint32_t first, int n, uint64_t limit)
+      : bar0(bar), phase(first), stages(n), limit_ns(limit) {}
   __device__ __forceinline__ bool wait() {
     if (__all_sync(0xFFFFFFFFu, ready)) return true;
-    return warp_wait(bar0 + 8u * s, phase);
+    return warp_wait(bar0 + 8u * s, phase, limit_ns);
   }
   __device__ __forceinline__ void ask_next() {
     const bool wrap = s + 1 == stages;
@@ -114,18 +144,13 @@ struct Ring {
   __device__ __forceinline__ void next() {
     if (++s == stages) s = 0, phase ^= 1u;
   }
-  __device__ __forceinline__ void skip(int n) {  // n stages that another warp walks
-    ready = false;
-    s += n;
-    if (s / stages & 1) phase ^= 1u;
-    s %= stages;
-  }
 };
 
-// Where the experts' rows start (E + 1 numbers) and how many tiles of rows the experts before each
-// have, in shared memory. False if the offsets are no such table.
+// Where the experts' rows start (E + 1 numbers), how many chunks of rows the experts before each have,
+// and (weights) the experts by falling numbers of rows, in shared memory. False if the offsets are no
+// such table.
 template <bool WEIGHTS>
-__device__ __forceinline__ bool build_table(const Args& a, int* start, int* first) {
+__device__ __forceinline__ bool build_table(const Args& a, int* start, int* first, uint16_t* order) {
   __shared__ int sums[kThreads / 32];
   constexpr int PER = (kMaxE + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -162,20 +187,32 @@ __device__ __forceinline__ bool build_table(const Args& a, int* start, int* firs
     base += tiles[p];
     if (e == a.E - 1) first[a.E] = base;
   }
+  if constexpr (WEIGHTS) {  // the rank of an expert: how many have more rows, or as many and come first
+    for (int e = tid; e < a.E; e += kThreads) {
+      const int rows = start[e + 1] - start[e];
+      int rank = 0;
+#pragma unroll 4
+      for (int o = 0; o < a.E; ++o) {
+        const int other = start[o + 1] - start[o];
+        rank += other > rows || (other == rows && o < e);
+      }
+      order[rank] = (uint16_t)e;
+    }
+  }
   __syncthreads();
   return true;
 }
 
-// Unit u of the launch; i_tiles: tiles of the output's columns.
+// Tile u of the launch; i_tiles, j_tiles: tiles of an output's columns and (weights) rows.
 template <bool WEIGHTS, int PAIR>
-__device__ __forceinline__ Unit unit_at(const Args& a, const int* start, const int* first, int u,
-                                        int i_tiles, int j_tiles, int rank) {
-  Unit t;
+__device__ __forceinline__ Unit unit_at(const Args& a, const int* start, const int* first,
+                                        const uint16_t* order, int u, int i_tiles, int j_tiles) {
+  Unit t{};
   if constexpr (WEIGHTS) {
-    const int per = i_tiles * j_tiles;
-    t.e = u / per;
-    const int in = u - t.e * per, jt = in / i_tiles;
-    t.i0 = (in - jt * i_tiles) * kTile * PAIR + rank * kTile;
+    const int per = i_tiles * j_tiles, at = u / per;
+    t.e = order[at];
+    const int in = u - at * per, jt = in / i_tiles;
+    t.i0 = (in - jt * i_tiles) * kTile * PAIR;
     t.j0 = jt * a.chunk;
     t.n = min(a.chunk, a.J - t.j0);
     t.row0 = start[t.e];
@@ -193,13 +230,11 @@ __device__ __forceinline__ Unit unit_at(const Args& a, const int* start, const i
     const int rows = start[lo + 1] - start[lo];
     // equal chunks; as none is above a.chunk the last one has a row at least
     const int per = ((rows + chunks - 1) / chunks + 15) & ~15;
-    t.i0 = it * kTile * PAIR + rank * kTile;
+    t.i0 = it * kTile * PAIR;
     t.j0 = start[lo] + c * per;
     t.n = min(per, rows - c * per);
-    t.row0 = 0;
     t.k = a.K;
   }
-  t.n16 = (t.n + 15) & ~15;
   return t;
 }
 
@@ -253,16 +288,67 @@ __device__ __forceinline__ void store_rows(const Args& a, const float (&v)[32], 
 
 __device__ __forceinline__ void store_columns(const Args& a, const float (&v)[32], int64_t row, int i, int n,
                                               int lane) {
-  const bool full = n >= 32;
   if (a.accumulate) {
     if (a.f32) store_rows<true, true, false>(a, v, row, i, n, lane);
     else store_rows<false, true, false>(a, v, row, i, n, lane);
   } else if (a.f32) {
-    if (full) store_rows<true, false, true>(a, v, row, i, n, lane);
+    if (n >= 32) store_rows<true, false, true>(a, v, row, i, n, lane);
     else store_rows<true, false, false>(a, v, row, i, n, lane);
   } else {
-    if (full) store_rows<false, false, true>(a, v, row, i, n, lane);
-    else store_rows<false, false, false>(a, v, row, i, n, lane);
+    store_rows<false, false, false>(a, v, row, i, n, lane);
+  }
+}
+
+// 16 lanes x 32 columns of the accumulator: lane l has, of each 8 columns c, elements (l / 4, 2 (l % 4))
+// and the one right of it in r[4c], r[4c + 1], and those 8 lanes further down in r[4c + 2], r[4c + 3].
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// The same as bf16 by way of shared memory (`stage`, this warp's 32 rows of 64 bytes): 8 x 8 blocks are
+// stored transposed, and rows leave in words of 16 bytes. A third of the instructions of the exchange
+// between lanes. A row's 16-byte words are turned by half its number, so that eight rows' words of one
+// block lie in different banks. i: the warp's first column.
+__device__ __forceinline__ void store_staged(const Args& a, uint32_t taddr, uint32_t stage, int64_t row, int i,
+                                             int n, int lane) {
+  uint32_t lo[16], hi[16];
+  tmem_ld_16x32(taddr, lo);
+  tmem_ld_16x32(taddr + (16u << 16), hi);
+  tmem_ld_wait();
+  __syncwarp();  // the lanes have read what was here
+  const uint32_t to = stage + (lane & 7) * 64 + (((lane >> 3) ^ (lane >> 1 & 3)) << 4);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t p[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const uint32_t* r = (m < 2 ? lo : hi) + 4 * c + 2 * (m & 1);
+      p[m] = pack_bf16(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to + c * 512),
+                 "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                 : "memory");
+  }
+  __syncwarp();
+  const int j = lane >> 2, w = lane & 3;
+  const uint32_t from = stage + j * 64 + ((w ^ (j >> 1 & 3)) << 4);
+  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + (row + j) * a.I + i + 8 * w;
+  const bool there = i + 8 * w < a.I;
+#pragma unroll
+  for (int c = 0; c < 4; ++c, p += 8 * a.I) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(from + c * 512)
+                 : "memory");
+    if (there && j + 8 * c < n) *reinterpret_cast<uint4*>(p) = v;
   }
 }
 
@@ -271,33 +357,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_grouped(const __grid_constant__ Maps m, const Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t tmem_holder;
+  __shared__ Unit queue[kQueue];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
-  const uint32_t bars = sbase + a.stages * a.stage_bytes;
+  const uint32_t out_stage = sbase + a.stages * a.stage_bytes;
+  const uint32_t bars = out_stage + kStoreWarps * kOutBytes;
   int* const start = reinterpret_cast<int*>(smem_raw + (bars + kBarBytes - raw));
-  int* const first_tile = start + kMaxE + 1;
+  int* const first_chunk = start + kMaxE + 1;
+  uint16_t* const order = reinterpret_cast<uint16_t*>(first_chunk + kMaxE + 1);
   auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
   auto empty_bar = [&](uint32_t s) { return bars + 8u * (kMaxStages + s); };
-  // weights, pairs: the odd CTA's part of an expert's last block, loaded and set to zero
-  auto tail_bar = [&](uint32_t s) { return bars + 8u * (2 * kMaxStages + s); };
-  auto fixed_bar = [&](uint32_t s) { return bars + 8u * (3 * kMaxStages + s); };
-  auto accf_bar = [&](uint32_t b) { return bars + 8u * (4 * kMaxStages + b); };
-  auto acce_bar = [&](uint32_t b) { return bars + 8u * (4 * kMaxStages + 2 + b); };
-  static_assert(8 * (4 * kMaxStages + 4) <= kBarBytes, "barrier area");
+  auto accf_bar = [&](uint32_t b) { return bars + 8u * (2 * kMaxStages + b); };
+  auto acce_bar = [&](uint32_t b) { return bars + 8u * (2 * kMaxStages + 2 + b); };
+  auto told_bar = [&](uint32_t s) { return bars + 8u * (2 * kMaxStages + 4 + s); };
+  auto taken_bar = [&](uint32_t s) { return bars + 8u * (2 * kMaxStages + 4 + kQueue + s); };
+  static_assert(8 * (2 * kMaxStages + 4 + 2 * kQueue) <= kBarBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR == 2 ? (int)cluster_ctarank() : 0;
   const int step = (int)gridDim.x / PAIR, mine = (int)blockIdx.x / PAIR;
+  const uint64_t limit = a.wait_ns;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
-      mbar_init(tail_bar(s), 1);
-      mbar_init(fixed_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
       mbar_init(acce_bar(b), PAIR * kStoreWarps);
+    }
+    for (int q = 0; q < kQueue; ++q) {
+      mbar_init(told_bar(q), 1);
+      // those who take a tile: the storing and loading warps, the even CTA's multiplying one
+      mbar_init(taken_bar(q), PAIR * (kStoreWarps + 1) + 1);
     }
     mbar_fence_init();
     tma_prefetch_desc(&m.a);
@@ -314,28 +406,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   pdl_wait();
-  const bool good = build_table<WEIGHTS>(a, start, first_tile);  // (a barrier for the block)
+  const bool good = build_table<WEIGHTS>(a, start, first_chunk, order);  // (a barrier for the block)
   tc_fence_after();
   if constexpr (PAIR == 2) cluster_sync();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&tmem_holder);
 
   const int i_tiles = (a.I + kTile * PAIR - 1) / (kTile * PAIR);
   const int j_tiles = WEIGHTS ? (a.J + a.chunk - 1) / a.chunk : 1;
-  const int units = !good ? 0 : WEIGHTS ? a.E * i_tiles * j_tiles : first_tile[a.E] * i_tiles;
+  const int units = !good ? 0 : WEIGHTS ? a.E * i_tiles * j_tiles : first_chunk[a.E] * i_tiles;
+
+  // Entry number q of the queue, once it is there; false if the wait ran out. A lane reads a word, so
+  // that what frees the slot needs all words to have arrived: the odd CTA's arrival is then one without
+  // a release, which would wait for a storing warp's rows to reach memory.
+  auto take = [&](int q, Unit& t) {
+    const uint32_t slot = q % kQueue, bar = told_bar(slot), phase = q / kQueue & 1u;
+    if (!(PAIR == 2 && rank == 1 ? warp_wait_cluster(bar, phase, limit) : warp_wait(bar, phase, limit)))
+      return false;
+    const int word = static_cast<volatile const int*>(&queue[slot].e)[lane & 7];
+    t.e = __shfl_sync(0xFFFFFFFFu, word, 0);
+    t.i0 = __shfl_sync(0xFFFFFFFFu, word, 1);
+    t.j0 = __shfl_sync(0xFFFFFFFFu, word, 2);
+    t.n = __shfl_sync(0xFFFFFFFFu, word, 3);
+    t.row0 = __shfl_sync(0xFFFFFFFFu, word, 4);
+    t.k = __shfl_sync(0xFFFFFFFFu, word, 5);
+    if (lane == 0) {
+      if (PAIR == 2 && rank == 1) mbar_arrive_remote_relaxed(mapa_shared(taken_bar(slot), 0));
+      else mbar_arrive(taken_bar(slot));
+    }
+    return true;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------ loads
-    Ring ring(empty_bar(0), 1, a.stages);
+    Ring ring(empty_bar(0), 1, a.stages, limit);
     int it = 0;
     bool ok = true;
     const bool kmajor = a.a_kmajor != 0;
-    for (int u = mine; u < units && ok; u += step) {
-      const Unit t = unit_at<WEIGHTS, PAIR>(a, start, first_tile, u, i_tiles, j_tiles, rank);
-      const int half = uniform(t.n16 / PAIR), blocks = uniform((t.k + 63) / 64);
-      const int e = uniform(t.e), i0 = uniform(t.i0), row0 = uniform(t.row0);
-      const int j0 = uniform(t.j0 + rank * (t.n16 / PAIR));
-      const bool mend = uniform(t.k & 15) != 0;
-      const uint32_t bytes = kABytes + (WEIGHTS ? (half + 63) / 64 * kBlock : half * 128u);
+    for (int q = 0; ok; ++q) {
+      Unit t;
+      if (!take(q, t) || t.n < 0) break;
+      const int half = uniform(t.n16() / PAIR), blocks = uniform((t.k + 63) / 64);
+      const int e = uniform(t.e), i0 = uniform(t.i0) + rank * kTile, row0 = uniform(t.row0);
+      const int j0 = uniform(t.j0) + rank * half;
+      const int last = WEIGHTS ? uniform(t.k) - (blocks - 1) * 64 : 64;  // rows of the last block
       for (int kb = 0; kb < blocks; ++kb, ++it) {
         if (!ring.wait()) {
           ok = false;
@@ -345,17 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           const uint32_t sa = sbase + ring.s * a.stage_bytes, sb = sa + kABytes;
           const int k0 = kb * 64;
-          // the two CTAs' bytes of a stage count on the even one's barrier, but those of a block that
-          // is to be mended in place each on its own
-          const bool tail = WEIGHTS && PAIR == 2 && kb == blocks - 1 && mend;
+          const bool part = WEIGHTS && kb == blocks - 1 && last < 64;
+          const uint32_t bytes = WEIGHTS ? (2 + (half + 63) / 64) * (part ? (last + 15) & ~15 : 64) * 128u
+                                         : kABytes + half * 128u;
+          // the two CTAs' bytes of a stage count on the even one's barrier
           uint32_t bar = full_bar(ring.s);
-          if (tail) {
-            if (rank == 1) bar = tail_bar(ring.s);
-            mbar_arrive_expect_tx(bar, bytes);
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(bar, PAIR * bytes);
-          }
-          if constexpr (PAIR == 2) bar = mapa_shared(bar, tail ? rank : 0);
+          if (rank == 0) mbar_arrive_expect_tx(bar, PAIR * bytes);
+          if constexpr (PAIR == 2) bar = mapa_shared(bar, 0);
           auto load2 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
             if constexpr (PAIR == 2) tma_load_2d_pair(dst, map, bar, c0, c1);
             else tma_load_2d(dst, map, bar, c0, c1);
@@ -365,11 +474,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tma_load_3d(dst, map, bar, c0, c1, c2);
           };
           if constexpr (WEIGHTS) {
-            load2(sa, &m.a, i0, row0 + k0);
-            load2(sa + kBlock, &m.a, i0 + 64, row0 + k0);
+            // k-rows r .. of the stage from rows `from` of the operands
+            auto boxes = [&](const CUtensorMap* ma, const CUtensorMap* mb, int r, int from) {
+              load2(sa + r * 128, ma, i0, from);
+              load2(sa + kBlock + r * 128, ma, i0 + 64, from);
 #pragma unroll
-            for (int c = 0; c < kMaxN / PAIR; c += 64)
-              if (c < half) load2(sb + c / 64 * kBlock, &m.b[0], j0 + c, row0 + k0);
+              for (int c = 0; c < kMaxN / PAIR; c += 64)
+                if (c < half) load2(sb + c / 64 * kBlock + r * 128, mb, j0 + c, from);
+            };
+            if (!part) {
+              boxes(&m.a, &m.b[0], 0, row0 + k0);
+            } else {
+              if (last & 32) boxes(&m.a_part[0], &m.b_part[0], 0, row0 + k0);
+              if (last & 16) boxes(&m.a_part[1], &m.b_part[1], last & 32, row0 + k0 + (last & 32));
+              if (last & 15) boxes(&m.a_part[2], &m.b_part[2], last & 48, e * 16);
+            }
           } else {
             if (kmajor) {
               load3(sa, &m.a, k0, i0, e);
@@ -398,54 +517,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every stage's last release has landed before this CTA may leave
     for (int s = 0; s < a.stages && s < it && ok; ++s)
-      ok = warp_wait(empty_bar(s), (it - 1 - s) / a.stages & 1u);
+      ok = warp_wait(empty_bar(s), (it - 1 - s) / a.stages & 1u, limit);
   } else if (warp == 1) {
     // ------------------------------------------------ multiplies
-    // The warp stays in step and an elected lane issues from uniform registers.
-    Ring ring(full_bar(0), 0, a.stages);
+    // The warp stays in step and an elected lane of the even CTA issues, from uniform registers (by one
+    // lane's branch with operands of its own an issue took 300 cycles: 131072 rows of 128 experts, 2048
+    // -> 1536, 1015 us, 528 this way).
+    Ring ring(full_bar(0), 0, a.stages, limit);
     const int a_mn = WEIGHTS || !a.a_kmajor, b_mn = WEIGHTS;
     const uint64_t adesc = sdesc_sw128(sbase, a_mn ? kBlock : 16, 1024);
     const uint64_t bdesc = sdesc_sw128(sbase + kABytes, b_mn ? kBlock : 16, 1024);
     const uint32_t a_step = a_mn ? 2048 / 16 : 2, b_step = b_mn ? 2048 / 16 : 2;
-    uint32_t acc = 0, tails = 0;
-    bool ok = true;
-    for (int u = mine; u < units && ok; u += step) {
-      const Unit t = unit_at<WEIGHTS, PAIR>(a, start, first_tile, u, i_tiles, j_tiles, rank);
-      const int blocks = uniform((t.k + 63) / 64), n16 = uniform(t.n16);
+    uint32_t acc = 0;
+    bool ok = rank == 0;
+    for (int q = 0; ok; ++q) {
+      Unit t;
+      if (!take(q, t) || t.n < 0) break;
+      const int blocks = uniform((t.k + 63) / 64), n16 = uniform(t.n16());
       if (blocks == 0) continue;
       const int last = uniform(t.k) - (blocks - 1) * 64;  // terms in the last block
-      const bool mend = WEIGHTS && (last & 15) != 0;
       const uint32_t buf = acc & 1u;
       const uint32_t d = tmem + buf * kMaxN;
-      // sets the rows of the next expert to zero in this CTA's part of stage s
-      auto zero_rows = [&](uint32_t s) {
-        const uint32_t sa = sbase + s * a.stage_bytes;
-        const int parts = 2 + (n16 / PAIR + 63) / 64, end = ((last + 15) & ~15) * 128;
-        for (int p = 0; p < parts; ++p)
-          for (int at = last * 128 + lane * 16; at < end; at += 512)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             sa + (p < 2 ? p * kBlock : kABytes + (p - 2) * kBlock) + at),
-                         "r"(0)
-                         : "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-      };
-      if (PAIR == 2 && rank == 1) {  // the even CTA issues; this one mends its part
-        ring.skip(blocks - 1);
-        if (mend) {
-          const uint32_t s = ring.s;
-          if (!warp_wait(tail_bar(s), tails >> s & 1u)) {
-            ok = false;
-            break;
-          }
-          tails ^= 1u << s;
-          zero_rows(s);
-          if (lane == 0) mbar_arrive_remote(mapa_shared(fixed_bar(s), 0));
-        }
-        ring.next();
-        continue;
-      }
-      if (!warp_wait(acce_bar(buf), (acc >> 1 & 1u) ^ 1u)) break;
+      if (!warp_wait(acce_bar(buf), (acc >> 1 & 1u) ^ 1u, limit)) break;
       tc_fence_after();
       const uint32_t idesc = idesc_bf16_f32(kTile * PAIR, n16, a_mn, b_mn);
       for (int kb = 0; kb < blocks; ++kb) {
@@ -455,20 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t s = ring.s;
         ring.ask_next();
-        int steps = 4;
-        if (WEIGHTS && kb == blocks - 1) {
-          steps = (last + 15) / 16;
-          if (mend) {
-            zero_rows(s);
-            if constexpr (PAIR == 2) {
-              if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(fixed_bar(s), tails >> s & 1u, kWaitNs))) {
-                ok = false;
-                break;
-              }
-              tails ^= 1u << s;
-            }
-          }
-        }
+        const int steps = WEIGHTS && kb == blocks - 1 ? (last + 15) / 16 : 4;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t ad = adesc + s * (a.stage_bytes / 16), bd = bdesc + s * (a.stage_bytes / 16);
@@ -480,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if constexpr (PAIR == 2) umma_commit_pair_mc(empty_bar(s), 0x3);
           else umma_commit(empty_bar(s));
-          if (kb == blocks - 1) {
+          if (kb == blocks - 1 && !(a.stall && blockIdx.x == 0 && acc == 0)) {
             if constexpr (PAIR == 2) umma_commit_pair_mc(accf_bar(buf), 0x3);
             else umma_commit(accf_bar(buf));
           }
@@ -490,52 +570,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++acc;
     }
-  } else {
-    const int q = warp & 3, set = (warp - 2) >> 2;
-    const int64_t es = a.f32 ? 4 : 2;
-    {
-      const int thread = (int)blockIdx.x * (32 * kStoreWarps) + (int)threadIdx.x - 64;
-      const int threads = (int)gridDim.x * (32 * kStoreWarps);
-      char* out = static_cast<char*>(a.out);
-      if (!good) {
-        const int64_t rows = WEIGHTS ? (int64_t)a.E * a.J : a.R;
-        fill(out, rows * a.I * es / 16, a.f32 ? 0x7FC00000u : 0x7FC07FC0u, thread, threads);
-      } else if (!WEIGHTS) {
-        fill(out, start[0] * (a.I * es / 16), 0, thread, threads);
-        fill(out + start[a.E] * (a.I * es), (a.R - start[a.E]) * (a.I * es / 16), 0, thread, threads);
+  } else if (warp == 2) {
+    // ------------------------------------------------ deals out tiles
+    // Two claims are on their way at a time.
+    int u = mine, ahead = mine + step;
+    for (int q = 0; rank == 0; ++q) {
+      int next = ahead + step;
+      if (a.next != nullptr && lane == 0) next = 2 * step + atomicAdd(a.next, 1);
+      Unit t{};
+      if (u < units) t = unit_at<WEIGHTS, PAIR>(a, start, first_chunk, order, u, i_tiles, j_tiles);
+      else t.n = -1;
+      const uint32_t slot = q % kQueue;
+      if (!warp_wait(taken_bar(slot), (q / kQueue & 1u) ^ 1u, limit)) break;
+      if (lane == 0) {
+        queue[slot] = t;
+        mbar_arrive(told_bar(slot));
+        if constexpr (PAIR == 2) {
+          const uint32_t to = mapa_shared(smem_u32(&queue[slot]), 1);
+          st_shared_cluster(to, make_int4(t.e, t.i0, t.j0, t.n));
+          st_shared_cluster(to + 16, make_int4(t.row0, t.k, 0, 0));
+          mbar_arrive_remote(mapa_shared(told_bar(slot), 1));
+        }
       }
+      __syncwarp();
+      if (t.n < 0) break;
+      u = ahead;
+      ahead = __shfl_sync(0xFFFFFFFFu, next, 0);
     }
+  } else {
+    // ------------------------------------------------ stores
+    const int set = (warp - kFirstStore) >> 2, quarter = warp & 3;  // (of the accumulator's lanes)
+    const int64_t es = a.f32 ? 4 : 2;
+    const int64_t out_rows = WEIGHTS ? (int64_t)a.E * a.J : a.R;
+    const uint32_t nan = a.f32 ? 0x7FC00000u : 0x7FC07FC0u;
+    char* const out = static_cast<char*>(a.out);
+    const int thread = (int)blockIdx.x * (32 * kStoreWarps) + (int)threadIdx.x - 32 * kFirstStore;
+    const int threads = (int)gridDim.x * (32 * kStoreWarps);
+    if (!good) {
+      fill(out, out_rows * a.I * es / 16, nan, thread, threads);
+    } else if (!WEIGHTS) {
+      fill(out, start[0] * (a.I * es / 16), 0, thread, threads);
+      fill(out + start[a.E] * (a.I * es), (a.R - start[a.E]) * (a.I * es / 16), 0, thread, threads);
+    }
+    const uint32_t stage = out_stage + (warp - kFirstStore) * kOutBytes;
     uint32_t acc = 0;
-    bool ok = true;
-    for (int u = mine; u < units; u += step) {
-      const Unit t = unit_at<WEIGHTS, PAIR>(a, start, first_tile, u, i_tiles, j_tiles, rank);
-      if (t.k == 0 && a.accumulate) continue;  // adding zero changes nothing
+    for (int q = 0;; ++q) {
+      Unit t;
+      bool ok = take(q, t);
+      if (ok && t.n < 0) break;
+      if (ok && t.k == 0 && a.accumulate) continue;  // adding zero changes nothing
       const uint32_t buf = acc & 1u;
-      if (t.k > 0 && ok) {
-        ok = warp_wait(accf_bar(buf), acc >> 1 & 1u);
+      if (ok && t.k > 0) ok = warp_wait(accf_bar(buf), acc >> 1 & 1u, limit);
+      if (!ok) {  // the tiles that this CTA has or would have had are nobody's: NaN, if not others' results
+        fill(out, out_rows * a.I * es / 16, nan, (int)threadIdx.x - 32 * kFirstStore, 32 * kStoreWarps);
+        break;
       }
       tc_fence_after();
       const int64_t row0 = WEIGHTS ? (int64_t)t.e * a.J + t.j0 : t.j0;
-      const int i = t.i0 + q * 32 + lane;
+      const int i = t.i0 + rank * kTile + quarter * 32;
+      const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kMaxN;
       for (int c = set * 32; c < t.n; c += 64) {
-        float v[32];
-        if (t.k > 0 && ok) {
-          uint32_t r[32];
-          tmem_ld_32x32(tmem + ((uint32_t)(q * 32) << 16) + buf * kMaxN + c, r);
-          tmem_ld_wait();
+        if (t.k > 0 && !a.f32 && !a.accumulate) {
+          store_staged(a, from + c, stage, row0 + c, i, t.n - c, lane);
+        } else {
+          uint32_t r[32] = {};
+          if (t.k > 0) {
+            tmem_ld_32x32(from + c, r);
+            tmem_ld_wait();
+          }
+          float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        } else {
-          const float none = t.k > 0 ? __int_as_float(0x7FC00000) : 0.f;  // NaN after an error
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = none;
+          store_columns(a, v, row0 + c, i + lane, t.n - c, lane);
         }
-        store_columns(a, v, row0 + c, i, t.n - c, lane);
       }
       if (t.k > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) {
+        if (lane == 0) {
           if (PAIR == 2 && rank != 0) mbar_arrive_remote_relaxed(mapa_shared(acce_bar(buf), 0));
           else mbar_arrive(acce_bar(buf));
         }
@@ -555,6 +667,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+struct TailArgs {
+  const int32_t* offsets;
+  const uint4* from[2];  // the operands, rows of `words` words of 8 elements
+  uint4* panel[2];       // [E][16] rows
+  int words[2];
+  int R;
+  int* next;
+};
+
+// Block (e, y): the panels of expert e, part y of gridDim.y. And the counter of claimed tiles.
+__global__ void __launch_bounds__(256) k_tails(TailArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.next = 0;
+  const int e = blockIdx.x, s = a.offsets[e], t = a.offsets[e + 1];
+  if (s < 0 || t < s || t > a.R) return;  // (no table: the products' launch says so)
+  const int n = (t - s) & 15;
+  if (n == 0) return;
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int words = a.words[o];
+    const uint4* from = a.from[o] + (int64_t)(t - n) * words;
+    uint4* to = a.panel[o] + (int64_t)e * 16 * words;
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < 16 * words; i += gridDim.y * 256)
+      to[i] = i < n * words ? from[i] : make_uint4(0, 0, 0, 0);
+  }
+}
+
 // ------------------------------------------------------------------------------------ host side
 
 inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -562,12 +702,17 @@ inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintpt
 mm_status check_desc(const mm_grouped_desc* d) {
   if (d == nullptr || d->R < 0 || d->K < 1 || d->N < 1 || d->E < 1) return MM_ERR_INVALID_ARG;
   if (d->out_type != MM_BF16 && d->out_type != MM_FP32) return MM_ERR_INVALID_ARG;
-  if (d->flags > 2) return MM_ERR_INVALID_ARG;  // unknown flags, or both forms
+  const uint32_t forms = d->flags & ~MM_GROUPED_TEST_STALL;
+  if (forms > 2) return MM_ERR_INVALID_ARG;  // unknown flags, or both forms
   if (d->K % 8 || d->N % 8 || d->K > 65536 || d->N > 65536 || d->E > kMaxE ||
       d->R >= (int64_t)1 << 31)
     return MM_ERR_UNSUPPORTED;
   return MM_OK;
 }
+
+// Workspace: the counter, then the panels of both operands of weight gradients.
+constexpr size_t kHeaderBytes = 256;
+size_t panel_bytes(int64_t E, int64_t cols) { return ((size_t)E * 16 * cols * 2 + 255) / 256 * 256; }
 
 bool map2(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, uint32_t box_rows) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
@@ -576,10 +721,13 @@ bool map2(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, uint32_t
   return make_map(m, base, 2, dims, strides, box);
 }
 
+// units: tiles, at most.
 template <int PAIR, bool WEIGHTS>
-cudaError_t launch(const Maps& m, Args a, int64_t units, cudaStream_t st) {
+cudaError_t launch(const Maps& m, Args a, int64_t units, uint32_t flags, cudaStream_t st) {
+  a.stall = (flags & MM_GROUPED_TEST_STALL) != 0;
+  a.wait_ns = a.stall ? kTestWaitNs : kWaitNs;
   a.stage_bytes = kABytes + (WEIGHTS ? (a.chunk / PAIR + 63) / 64 * kBlock : a.chunk / PAIR * 128u);
-  const uint32_t fixed = 1024 + kBarBytes + kTableBytes;
+  const uint32_t fixed = 1024 + kStoreWarps * kOutBytes + kBarBytes + kTableBytes;
   a.stages = (int)std::min<uint32_t>(kMaxStages, (kMostSmem - 1024 - fixed) / a.stage_bytes);
   const size_t smem = fixed + (size_t)a.stages * a.stage_bytes;
   static std::atomic<uint64_t> ready{0};
@@ -639,20 +787,17 @@ extern "C" {
 int mm_experts_version(void) { return 1; }
 
 size_t mm_grouped_workspace_size(const mm_grouped_desc* d) {
-  return check_desc(d) == MM_OK ? 256 : 0;
+  return check_desc(d) == MM_OK ? kHeaderBytes + panel_bytes(d->E, d->K) + panel_bytes(d->E, d->N) : 0;
 }
 
 mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* weight,
-                        const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
-                        void* stream) {
+                        const int32_t* offsets, void* out, void* stream) {
   mm_status s = check_desc(d);
   if (s != MM_OK) return s;
   if (!aligned_to(rows, 16) || !aligned_to(weight, 16) || !aligned_to(out, 16) || !aligned_to(offsets, 4))
     return MM_ERR_INVALID_ARG;
   if (d->R == 0) return MM_OK;
   if (!rows || !weight || !out || !offsets) return MM_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < mm_grouped_workspace_size(d))
-    return MM_ERR_WORKSPACE;
   clear_error();
   MM_TRY(bind_context());
   // Pairs read half as much of their operands per product. Where a launch has no more tiles of one CTA
@@ -661,7 +806,7 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   // 131072 rows of 128, 2048 -> 1536, 592 and 528.)
   const int64_t chunks = d->R / kMaxN + std::min<int64_t>(d->E, d->R);  // at most
   const bool few = chunks * ((d->N + kTile - 1) / kTile) <= device_sm_count();
-  const int pair = d->flags & MM_GROUPED_CTA_PAIRS || (d->flags == 0 && !few) ? 2 : 1;
+  const int pair = d->flags & MM_GROUPED_CTA_PAIRS || (!(d->flags & MM_GROUPED_SINGLE_CTA) && !few) ? 2 : 1;
   Maps m;
   Args a{};
   a.offsets = offsets;
@@ -683,9 +828,9 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t units = chunks * ((d->N + kTile * pair - 1) / (kTile * pair));
   if (pair == 2)
-    MM_TRY((launch<2, false>(m, a, units, st)));
+    MM_TRY((launch<2, false>(m, a, units, d->flags, st)));
   else
-    MM_TRY((launch<1, false>(m, a, units, st)));
+    MM_TRY((launch<1, false>(m, a, units, d->flags, st)));
   return MM_OK;
 }
 
@@ -719,15 +864,30 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
   a.f32 = d->out_type == MM_FP32;
   a.accumulate = accumulate != 0;
   a.chunk = std::min(kMaxN, (a.J + 15) / 16 * 16);
-  const bool ok = map2(&m.a, d->transposed ? rows : d_out, a.I, d->R, 64) &&
-                  map2(&m.b[0], d->transposed ? d_out : rows, a.J, d->R, 64);
+  const void *by_i = d->transposed ? rows : d_out, *by_j = d->transposed ? d_out : rows;
+  char* const ws = static_cast<char*>(workspace);
+  char *const panel_i = ws + kHeaderBytes, *const panel_j = panel_i + panel_bytes(d->E, a.I);
+  bool ok = map2(&m.a, by_i, a.I, d->R, 64) && map2(&m.b[0], by_j, a.J, d->R, 64);
+  for (int p = 0; p < 2; ++p)
+    ok = ok && map2(&m.a_part[p], by_i, a.I, d->R, 32u >> p) && map2(&m.b_part[p], by_j, a.J, d->R, 32u >> p);
+  ok = ok && map2(&m.a_part[2], panel_i, a.I, 16 * (int64_t)d->E, 16) &&
+       map2(&m.b_part[2], panel_j, a.J, 16 * (int64_t)d->E, 16);
   if (!ok) return cuda_fail(cudaErrorInvalidValue, "grouped product tensor maps");
   const int64_t units = (int64_t)d->E * ((a.I + kTile * pair - 1) / (kTile * pair)) *
                         ((a.J + a.chunk - 1) / a.chunk);
+  TailArgs ta{offsets,
+              {static_cast<const uint4*>(by_i), static_cast<const uint4*>(by_j)},
+              {reinterpret_cast<uint4*>(panel_i), reinterpret_cast<uint4*>(panel_j)},
+              {a.I / 8, a.J / 8},
+              a.R,
+              reinterpret_cast<int*>(ws)};
+  a.next = ta.next;
+  const int words = 16 * std::max(ta.words[0], ta.words[1]);  // (a few to a thread)
+  MM_TRY(launch_pdl(k_tails, dim3((unsigned)d->E, (unsigned)((words + 2047) / 2048)), dim3(256), 0, st, ta));
   if (pair == 2)
-    MM_TRY((launch<2, true>(m, a, units, st)));
+    MM_TRY((launch<2, true>(m, a, units, d->flags, st)));
   else
-    MM_TRY((launch<1, true>(m, a, units, st)));
+    MM_TRY((launch<1, true>(m, a, units, d->flags, st)));
   return MM_OK;
 }
 

@@ -263,14 +263,13 @@ def grouped_mm_forward(rows, weight, offsets, *, out_dtype=None, flags=0):
     transposed, kept = _layout(weight) if weight.dim() == 3 else (False, weight)
     out_dtype = out_dtype or torch.bfloat16
     key = (_sig(rows), _sig(weight), _sig(offsets), out_dtype, transposed, flags)
-    at, nbytes, _ = _grouped_plans.get(key) or _grouped_plan(
+    at, _, _ = _grouped_plans.get(key) or _grouped_plan(
         rows, weight, offsets, _type("out", torch.empty(0, dtype=out_dtype)), transposed, flags, key)
     rows, offsets = _aligned(rows), _index32(offsets, rows.shape[0])
     out = torch.empty((rows.shape[0], weight.shape[2]), dtype=out_dtype, device=rows.device)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=rows.device)
     _abi.check(_abi._lib().mm_grouped_mm(
-        at, rows.data_ptr(), kept.data_ptr(), offsets.data_ptr(), out.data_ptr(), ws.data_ptr(), nbytes,
-        _stream(rows)), "mm_grouped_mm")
+        at, rows.data_ptr(), kept.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream(rows)),
+        "mm_grouped_mm")
     return out
 
 

@@ -32,7 +32,7 @@ def test_exports_every_header_symbol():
 
 
 def test_constants_match_the_header():
-    found = re.findall(r"#define\s+(MM_\w+)\s+(0x\d+|\d+)u?\b", open(_abi.EXPERTS_HEADER_PATH).read())
+    found = re.findall(r"#define\s+(MM_\w+)\s+(0x[0-9A-Fa-f]+|\d+)u?\b", open(_abi.EXPERTS_HEADER_PATH).read())
     assert len(found) >= 2
     for name, value in found:
         assert getattr(_abi, name) == int(value, 0), name
@@ -53,14 +53,14 @@ def grouped(R=8, K=64, N=72, E=4, transposed=0, out=0, flags=0):
 def test_grouped_host_checks():
     lib = _abi._lib()
 
-    def product(d, *p, w=256, size=1 << 30):
-        return lib.mm_grouped_mm(ref(d), *p, w, size, None)
+    def product(d, *p):
+        return lib.mm_grouped_mm(ref(d), *p, None)
 
-    def weight(d, *p, w=256, size=1 << 30):
+    def weight(d, *p, w=256, size=1 << 40):
         return lib.mm_grouped_mm_weight_grad(ref(d), *p, 0, w, size, None)
 
     full = (16, 16, 16, 16)
-    assert lib.mm_grouped_mm(None, *full, 256, 1 << 30, None) == BAD
+    assert lib.mm_grouped_mm(None, *full, None) == BAD
     assert lib.mm_grouped_workspace_size(None) == 0
     for call in (product, weight):
         for d in (grouped(R=-1), grouped(K=0), grouped(N=0), grouped(E=0), grouped(out=2), grouped(flags=3),
@@ -69,14 +69,13 @@ def test_grouped_host_checks():
         for d in (grouped(K=60), grouped(N=4), grouped(K=65544), grouped(N=65544), grouped(E=1025),
                   grouped(R=2 ** 31)):
             assert call(d, *full) == UNSUP and lib.mm_grouped_workspace_size(ref(d)) == 0
-        d = grouped()
-        n = lib.mm_grouped_workspace_size(ref(d))
-        assert n >= 256
-        assert call(grouped(), *full, w=None) == WS and call(grouped(), *full, w=128) == WS
-        assert call(grouped(), *full, size=n - 1) == WS
         for i in range(4):
             for p in (None, 2 if i == 2 else 8):
                 assert call(grouped(), *full[:i], p, *full[i + 1:]) == BAD
+    d = grouped()
+    n = lib.mm_grouped_workspace_size(ref(d))
+    assert n >= 256
+    assert weight(d, *full, w=None) == WS and weight(d, *full, w=128) == WS and weight(d, *full, size=n - 1) == WS
     assert product(grouped(R=0), None, None, None, None) == _abi.MM_OK
     assert weight(grouped(R=0), None, None, None, 16) == BAD  # zeros have to go somewhere
 

@@ -285,3 +285,17 @@ def test_refusals():
         expert_ops.grouped_mm_weight_grad(x, d, at, w, into=torch.zeros(2, 72, 64, device="cuda"))
     with pytest.raises(TypeError):
         expert_ops.grouped_mm_weight_grad(x, d, at, w, into=torch.zeros(2, 64, 72, device="cuda"), dtype=BF)
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+def test_a_sum_that_never_arrives_is_nan(form):
+    """The failure path: the first CTA withholds its first accumulator, and its waits run out."""
+    x, w, at, d = inputs([300, 5, 70], 136, 264)
+    got = expert_ops.grouped_mm_forward(x, w, at, flags=form | _abi.MM_GROUPED_TEST_STALL)
+    assert got[:128, :128].isnan().all()
+    good = expert_ops.grouped_mm_forward(x, w, at, flags=form)
+    assert torch.equal(torch.where(got.isnan(), good, got), good)
+    got = expert_ops.grouped_mm_weight_grad(x, d, at, w, flags=form | _abi.MM_GROUPED_TEST_STALL)
+    assert got[0, :128, :128].isnan().all()  # (the largest expert's is the first)
+    check_forward(x, w, at, flags=form)
+    check_weight_grad(x, d, at, w, flags=form)
