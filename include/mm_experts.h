@@ -44,8 +44,8 @@ typedef struct mm_expert_desc {
   int32_t type; /* MM_BF16 or MM_FP32: of x, rows, y and their gradients */
 } mm_expert_desc;
 
-/* Bytes of workspace of mm_expert_table (0: unsupported sizes). Needs no initialisation. H and type
- * of the descriptor are not used by the two. */
+/* Bytes of workspace of mm_expert_table (0: unsupported sizes). Needs no initialisation; up to 2048
+ * slots use none (NULL). H and type of the descriptor are not used by the two. */
 size_t mm_expert_table_workspace_size(const mm_expert_desc* d);
 
 mm_status mm_expert_table(const mm_expert_desc* d, const int32_t* topk_ids, int32_t* offsets,

@@ -76,55 +76,66 @@ __global__ void __launch_bounds__(1024) k_table_scan(TableArgs a) {
   if (warp == 31) a.counts[(int64_t)a.blocks * (a.E + 1) + e] = before;
 }
 
+// FEW: no launch between, the blocks' counts are added up here.
+template <bool FEW>
 __global__ void __launch_bounds__(32 * kTableWarps) k_table_rank(TableArgs a) {
   constexpr int THREADS = 32 * kTableWarps, PER = (kMaxE + THREADS) / THREADS;
   __shared__ __align__(4) uint16_t count[kTableWarps][kMaxE + 2];
-  __shared__ int base[kMaxE + 1];
+  __shared__ int base[kMaxE + 1];    // where a bucket starts, then where this block's slots of it do
+  __shared__ int before[kMaxE + 1];  // slots of a bucket in the blocks before
   __shared__ int sums[kTableWarps];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, buckets = a.E + 1;
   for (int i = threadIdx.x; i < kTableWarps * (kMaxE + 2) / 2; i += THREADS)
     reinterpret_cast<uint32_t*>(&count[0][0])[i] = 0;
-  __syncthreads();
+  for (int e = threadIdx.x; e < buckets; e += THREADS) {
+    base[e] = FEW ? 0 : a.counts[(int64_t)a.blocks * buckets + e];
+    before[e] = FEW ? 0 : a.counts[(int64_t)blockIdx.x * buckets + e];
+  }
   int b[kRounds];
   unsigned same[kRounds];
   const int s0 = (blockIdx.x * kTableWarps + warp) * kRounds * 32 + lane;
 #pragma unroll
+  for (int r = 0; r < kRounds; ++r) b[r] = bucket_of(a, s0 + 32 * r);
+  __syncthreads();
+  if (FEW && a.blocks > 1) {  // a warp adds up every kTableWarps-th block's counts
+    for (int e = lane; e < buckets; e += 32) {
+      int all = 0, mine = 0;
+#pragma unroll 8
+      for (int k = warp; k < a.blocks; k += kTableWarps) {
+        const int c = a.counts[k * buckets + e];
+        all += c;
+        mine += k < (int)blockIdx.x ? c : 0;
+      }
+      if (all != 0) atomicAdd(&base[e], all);
+      if (mine != 0) atomicAdd(&before[e], mine);
+    }
+  }
+#pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    b[r] = bucket_of(a, s0 + 32 * r);
     same[r] = __match_any_sync(0xFFFFFFFFu, b[r]);
     if (b[r] >= 0 && lane == __ffs(same[r]) - 1) count[warp][b[r]] += __popc(same[r]);
     __syncwarp();
   }
   __syncthreads();
-  // a thread's PER buckets: their counts before this block, and in all blocks
-  int total[PER], before[PER], mine = 0;
+  for (int e = threadIdx.x; e < buckets; e += THREADS) {
+    int run = 0;
+#pragma unroll
+    for (int w = 0; w < kTableWarps; ++w) {
+      const int c = count[w][e];
+      count[w][e] = (uint16_t)run;
+      run += c;
+    }
+    if (FEW && a.blocks == 1) base[e] = run;
+  }
+  __syncthreads();
+  // the buckets' totals to where they start
+  int total[PER], mine = 0;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     const int e = threadIdx.x * PER + p;
-    total[p] = before[p] = 0;
-    if (e < buckets) {
-      int run = 0;
-      for (int w = 0; w < kTableWarps; ++w) {
-        const int c = count[w][e];
-        count[w][e] = (uint16_t)run;
-        run += c;
-      }
-      if (a.blocks == 1) {
-        total[p] = run;
-      } else if (a.blocks <= kFewBlocks) {
-#pragma unroll 8
-        for (int k = 0; k < a.blocks; ++k) {
-          const int c = a.counts[k * buckets + e];
-          total[p] += c;
-          before[p] += k < (int)blockIdx.x ? c : 0;
-        }
-      } else {
-        total[p] = a.counts[(int64_t)a.blocks * buckets + e];
-        before[p] = a.counts[(int64_t)blockIdx.x * buckets + e];
-      }
-    }
+    total[p] = e < buckets ? base[e] : 0;
     mine += total[p];
   }
   int upto = mine;
@@ -141,7 +152,7 @@ __global__ void __launch_bounds__(32 * kTableWarps) k_table_rank(TableArgs a) {
   for (int p = 0; p < PER; ++p) {
     const int e = threadIdx.x * PER + p;
     if (e < buckets) {
-      base[e] = at + before[p];
+      base[e] = at + before[e];
       if (blockIdx.x == 0) a.offsets[e] = at;  // (slots without an expert are behind offsets[E])
     }
     at += total[p];
@@ -202,42 +213,59 @@ __global__ void __launch_bounds__(256) k_dispatch(RowArgs a) {
   zero_rows_behind(a, rows);
 }
 
-// W columns a thread. words: H / W.
+// Words of W columns that a thread has under way at a time: single columns (rows off 16-byte boundaries)
+// need more of them (1001 x 6 fp32 rows of 2047 backward: 38 us one at a time).
+template <int W>
+constexpr int kAtOnce = W == 1 ? 4 : 1;
+
+// words: H / W.
 template <typename T, int W>
 __global__ void __launch_bounds__(256) k_combine(RowArgs a) {
+  constexpr int U = kAtOnce<W>;
   pdl_wait();
   pdl_launch_dependents();
   const T* rows = static_cast<const T*>(a.rows);
   const int64_t t = blockIdx.x;
   const int32_t* row = a.row_of_slot + t * a.K;
-  for (int w = threadIdx.x; w < a.words; w += blockDim.x) {
-    float y[W] = {};
+  for (int w0 = threadIdx.x; w0 < a.words; w0 += blockDim.x * U) {
+    float y[U][W] = {};
     for (int k0 = 0; k0 < a.K; k0 += 4) {  // four slots' loads in flight
-      float v[4][W];
+      float v[4][U][W];
       float g[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int64_t r = k0 + k < a.K ? row[k0 + k] : -1;
         const bool there = r >= 0 && r < a.S;
         g[k] = there ? (a.weights ? a.weights[t * a.K + k0 + k] : 1.f) : 0.f;
-        if (there) {
-          load_vec<W>(rows + r * a.H + (int64_t)w * W, v[k]);
-        } else {
 #pragma unroll
-          for (int i = 0; i < W; ++i) v[k][i] = 0.f;
+        for (int u = 0; u < U; ++u) {
+          const int w = w0 + u * (int)blockDim.x;
+          if (there && w < a.words) {
+            load_vec<W>(rows + r * a.H + (int64_t)w * W, v[k][u]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[k][u][i] = 0.f;
+          }
         }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < W; ++i) y[i] = fmaf(g[k], v[k][i], y[i]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < W; ++i) y[u][i] = fmaf(g[k], v[k][u][i], y[u][i]);
     }
-    store_vec<W>(static_cast<T*>(a.out_x) + t * a.H + (int64_t)w * W, y);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = w0 + u * (int)blockDim.x;
+      if (w < a.words) store_vec<W>(static_cast<T*>(a.out_x) + t * a.H + (int64_t)w * W, y[u]);
+    }
   }
 }
 
 template <typename T, int W>
 __global__ void __launch_bounds__(256) k_combine_bwd(RowArgs a) {
+  constexpr int U = kAtOnce<W>;
   __shared__ float part[8][8];
   pdl_wait();
   pdl_launch_dependents();
@@ -254,22 +282,46 @@ __global__ void __launch_bounds__(256) k_combine_bwd(RowArgs a) {
       if (row[k] >= a.S) row[k] = -1;
       g[k] = row[k] >= 0 && a.weights ? a.weights[t * a.K + k0 + k] : 1.f;
     }
-    for (int w = threadIdx.x; w < a.words; w += blockDim.x) {
-      float d[W];
-      load_vec<W>(static_cast<const T*>(a.x) + t * a.H + (int64_t)w * W, d);
+    for (int w0 = threadIdx.x; w0 < a.words; w0 += blockDim.x * U) {
+      float d[U][W];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (row[k] < 0) continue;
-        const int64_t at = row[k] * a.H + (int64_t)w * W;
-        float v[W];
+      for (int u = 0; u < U; ++u) {
+        const int w = w0 + u * (int)blockDim.x;
+#pragma unroll
+        for (int i = 0; i < W; ++i) d[u][i] = 0.f;
+        if (w < a.words) load_vec<W>(static_cast<const T*>(a.x) + t * a.H + (int64_t)w * W, d[u]);
+      }
+#pragma unroll
+      for (int k4 = 0; k4 < 8; k4 += 4) {  // four slots' loads in flight
+        float v[4][U][W];
         if (a.d_weights) {
-          load_vec<W>(rows + at, v);
 #pragma unroll
-          for (int i = 0; i < W; ++i) dot[k] = fmaf(d[i], v[i], dot[k]);
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int w = w0 + u * (int)blockDim.x;
+#pragma unroll
+              for (int i = 0; i < W; ++i) v[k][u][i] = 0.f;
+              if (row[k4 + k] >= 0 && w < a.words)
+                load_vec<W>(rows + row[k4 + k] * a.H + (int64_t)w * W, v[k][u]);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = g[k] * d[i];
-        store_vec<W>(static_cast<T*>(a.out_rows) + at, v);
+        for (int k = 0; k < 4; ++k) {
+          if (row[k4 + k] < 0) continue;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int w = w0 + u * (int)blockDim.x;
+            if (w >= a.words) continue;
+            float o[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+              if (a.d_weights) dot[k4 + k] = fmaf(d[u][i], v[k][u][i], dot[k4 + k]);
+              o[i] = g[k4 + k] * d[u][i];
+            }
+            store_vec<W>(static_cast<T*>(a.out_rows) + row[k4 + k] * a.H + (int64_t)w * W, o);
+          }
+        }
       }
     }
     if (a.d_weights) {
@@ -344,8 +396,8 @@ mm_status mm_expert_table(const mm_expert_desc* d, const int32_t* topk_ids, int3
   if (!offsets || !aligned_to(offsets, 4) || !aligned_to(topk_ids, 4) || !aligned_to(row_of_slot, 4) ||
       !aligned_to(slot_of_row, 4))
     return MM_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned_to(workspace, 256) ||
-      workspace_bytes < mm_expert_table_workspace_size(d))
+  if (d->T * d->K > kSlots && (workspace == nullptr || !aligned_to(workspace, 256) ||
+                               workspace_bytes < mm_expert_table_workspace_size(d)))
     return MM_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (d->T > 0 && (!topk_ids || !row_of_slot || !slot_of_row)) return MM_ERR_INVALID_ARG;
@@ -360,7 +412,7 @@ mm_status mm_expert_table(const mm_expert_desc* d, const int32_t* topk_ids, int3
   if (a.blocks > 1) MM_TRY(launch_pdl(k_table_count, grid, threads, 0, st, a));
   if (a.blocks > kFewBlocks)
     MM_TRY(launch_pdl(k_table_scan, dim3((unsigned)(a.E + 32) / 32), dim3(1024), 0, st, a));
-  MM_TRY(launch_pdl(k_table_rank, grid, threads, 0, st, a));
+  MM_TRY(launch_pdl(a.blocks > kFewBlocks ? k_table_rank<false> : k_table_rank<true>, grid, threads, 0, st, a));
   return MM_OK;
 }
 

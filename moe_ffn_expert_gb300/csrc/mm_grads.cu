@@ -7,9 +7,10 @@
 // The tensors' addresses travel as the kernels' argument, kRefs at a time, so that a captured call
 // holds them by itself.
 //
-// A chunk is kChunk elements of one tensor. A thread's squares are summed in 32 bits over 64 elements,
-// then in 64 bits. Where those 32 bits would overflow or lose what is small (a sum of 2^126 or more, or
-// below 2^-80 but not of zeros alone) the 64 squares are summed in 64 bits instead.
+// A chunk is 32 KB of one tensor; a block has a run of chunks, and the second launch walks the
+// runs backwards, from what the first has read last and L2 still holds. A thread's squares are summed in
+// 32 bits over 64 elements (bf16; fp32: 32), then in 64 bits. Where those 32 bits would overflow or lose what is small (a
+// sum of 2^126 or more, or below 2^-80 but not of zeros alone) the squares are summed in 64 bits instead.
 #include <algorithm>
 
 #include "../../include/mm_experts.h"
@@ -21,9 +22,13 @@ namespace {
 
 constexpr int kRefs = 1000;    // tensors per launch, at most (32 KB of arguments)
 constexpr int kThreads = 256;
-constexpr int kSteps = 8;      // vectors of 8 elements per thread and chunk
-constexpr int kChunk = kThreads * 8 * kSteps;
-constexpr int kBlocks = 8;     // per SM
+constexpr int kBlocks = 4;     // per SM
+// Vectors of 8 elements per thread and chunk: eight 16-byte loads in flight of either type.
+template <typename T>
+constexpr int kSteps = 16 / sizeof(T);
+template <typename T>
+constexpr int kChunk = kThreads * 8 * kSteps<T>;
+inline int64_t chunk_of(int type) { return type == MM_BF16 ? kChunk<__nv_bfloat16> : kChunk<float>; }
 
 struct Ref {
   const void* data;
@@ -55,46 +60,77 @@ __device__ __forceinline__ int ref_of(const GradArgs<N>& a, int chunk) {
 
 inline __host__ __device__ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Elements at `at` .. at + 8 of a tensor, zeros past its end.
+// 8 elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t at, int64_t count, bool vec, float (&v)[8]) {
-  if (vec && at + 8 <= count) {
-    load_vec<8>(p + at, v);
-  } else {
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+};
+
+// A thread's vectors of a chunk: elements base + 8 (256 s + thread) on, zeros past the end.
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* p, int64_t base, int64_t count, bool vec, Raw<T> (&r)[kSteps<T>]) {
+  if (vec && base + kChunk<T> <= count) {
+    const uint4* at = reinterpret_cast<const uint4*>(p + base) + threadIdx.x * (sizeof(T) / 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float one[1] = {0.f};
-      if (at + i < count) load_vec<1>(p + at + i, one);
-      v[i] = one[0];
+    for (int s = 0; s < kSteps<T>; ++s)
+#pragma unroll
+      for (int w = 0; w < (int)sizeof(T) / 2; ++w) r[s].w[w] = __ldcs(at + s * kThreads * (sizeof(T) / 2) + w);
+    return;
+  }
+#pragma unroll
+  for (int s = 0; s < kSteps<T>; ++s) {
+    const int64_t at = base + (int64_t)(s * kThreads + threadIdx.x) * 8;
+    if (vec && at + 8 <= count) {
+#pragma unroll
+      for (int w = 0; w < (int)sizeof(T) / 2; ++w) r[s].w[w] = reinterpret_cast<const uint4*>(p + at)[w];
+    } else {
+      r[s] = Raw<T>{};
+      if (at >= count) continue;
+      T one[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) one[i] = at + i < count ? p[at + i] : T(0.f);
+      r[s] = *reinterpret_cast<const Raw<T>*>(one);
     }
   }
 }
 
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& r, float (&v)[8]) {
+  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
+}
+__device__ __forceinline__ void widen(const Raw<float>& r, float (&v)[8]) {
+  const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+}
+
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T* p, int64_t base, int64_t count) {
-  const bool vec = on16(p);
-  float v[kSteps][8];
-#pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-    load8(p, base + (int64_t)(s * kThreads + threadIdx.x) * 8, count, vec, v[s]);
+  Raw<T> r[kSteps<T>];
+  load_chunk(p, base, count, on16(p), r);
   float sum[4] = {};
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
+  for (int s = 0; s < kSteps<T>; ++s) {
+    float v[8];
+    widen(r[s], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i & 3] = fmaf(v[s][i], v[s][i], sum[i & 3]);
+    for (int i = 0; i < 8; ++i) sum[i & 3] = fmaf(v[i], v[i], sum[i & 3]);
+  }
   const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-  if (total >= 8.2718061e-25f && total < 8.5070592e37f) return total;  // 2^-80, 2^126
+  if (total >= 0x1p-80f && total < 0x1p126f) return total;
   double wide = 0.0;
-  bool any = false;
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
+  for (int s = 0; s < kSteps<T>; ++s) {
+    float v[8];
+    widen(r[s], v);
+    bool any = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) any |= v[s][i] != 0.f;
-  if (!any) return 0.0;
+    for (int i = 0; i < 8; ++i) any |= v[i] != 0.f;
+    if (!any) continue;
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wide += (double)v[s][i] * (double)v[s][i];
+    for (int i = 0; i < 8; ++i) wide += (double)v[i] * (double)v[i];
+  }
   return wide;
 }
 
@@ -110,53 +146,81 @@ __device__ __forceinline__ double block_sum(double v) {
   return s;
 }
 
+// The block's run of chunks: first .. end.
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_squares(const __grid_constant__ GradArgs<N> a) {
+__device__ __forceinline__ void run_of(const GradArgs<N>& a, int& first, int& end) {
+  first = (int)((int64_t)a.chunks * blockIdx.x / gridDim.x);
+  end = (int)((int64_t)a.chunks * (blockIdx.x + 1) / gridDim.x);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_squares(const __grid_constant__ GradArgs<N> a) {
   pdl_wait();
   pdl_launch_dependents();
+  int c, end;
+  run_of(a, c, end);
   double sum = 0.0;
-  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    const Ref& r = a.ref[ref_of(a, c)];
-    const int64_t base = (int64_t)(c - r.first) * kChunk;
-    sum += r.type == MM_BF16 ? chunk_squares(static_cast<const __nv_bfloat16*>(r.data), base, r.count)
-                             : chunk_squares(static_cast<const float*>(r.data), base, r.count);
+  if (c < end) {
+    for (int i = ref_of(a, c); c < end; ++i) {
+      const int stop = min(end, i + 1 < a.n ? a.ref[i + 1].first : a.chunks), first = a.ref[i].first;
+      const int64_t count = a.ref[i].count;
+      const void* data = a.ref[i].data;
+      if (a.ref[i].type == MM_BF16) {
+        for (; c < stop; ++c)
+          sum += chunk_squares(static_cast<const __nv_bfloat16*>(data), (int64_t)(c - first) * kChunk<__nv_bfloat16>, count);
+      } else {
+        for (; c < stop; ++c)
+          sum += chunk_squares(static_cast<const float*>(data), (int64_t)(c - first) * kChunk<float>, count);
+      }
+    }
   }
   sum = block_sum(sum);
   if (threadIdx.x == 0) a.parts[blockIdx.x] = sum;
 }
 
+// Chunks end - 1 .. c of a tensor whose chunks start with `first`.
 template <typename T, typename O>
-__device__ __forceinline__ void scale_chunk(const Ref& r, int64_t base, float before, float scale) {
-  const T* p = static_cast<const T*>(r.data);
-  O* out = static_cast<O*>(r.out);
+__device__ __forceinline__ void scale_chunks(const Ref& ref, int first, int c, int end, float before, float scale) {
+  const T* p = static_cast<const T*>(ref.data);
+  O* out = static_cast<O*>(ref.out);
+  const int64_t count = ref.count;
   const bool vec = on16(p) && on16(out);
-  float v[kSteps][8];
+  for (int k = end - 1; k >= c; --k) {
+    const int64_t base = (int64_t)(k - first) * kChunk<T>;
+    Raw<T> r[kSteps<T>];
+    load_chunk(p, base, count, vec, r);
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s)
-    load8(p, base + (int64_t)(s * kThreads + threadIdx.x) * 8, r.count, vec, v[s]);
+    for (int s = 0; s < kSteps<T>; ++s) {
+      const int64_t at = base + (int64_t)(s * kThreads + threadIdx.x) * 8;
+      float v[8];
+      widen(r[s], v);
+      if (before != 1.f) {
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t at = base + (int64_t)(s * kThreads + threadIdx.x) * 8;
-    if (before != 1.f) {
+        for (int i = 0; i < 8; ++i) v[i] *= before;
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[s][i] *= before;
-    }
+      for (int i = 0; i < 8; ++i) v[i] *= scale;
+      if (vec && at + 8 <= count) {
+        if constexpr (sizeof(O) == 2) {
+          __stcs(reinterpret_cast<uint4*>(out + at), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                                pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])));
+        } else {
+          __stcs(reinterpret_cast<float4*>(out + at), make_float4(v[0], v[1], v[2], v[3]));
+          __stcs(reinterpret_cast<float4*>(out + at) + 1, make_float4(v[4], v[5], v[6], v[7]));
+        }
+      } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[s][i] *= scale;
-    if (vec && at + 8 <= r.count) {
-      store_vec<8>(out + at, v[s]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float one[1] = {v[s][i]};
-        if (at + i < r.count) store_vec<1>(out + at + i, one);
+        for (int i = 0; i < 8; ++i) {
+          const float one[1] = {v[i]};
+          if (at + i < count) store_vec<1>(out + at + i, one);
+        }
       }
     }
   }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_scale(const __grid_constant__ GradArgs<N> a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) k_scale(const __grid_constant__ GradArgs<N> a) {
   pdl_wait();
   pdl_launch_dependents();
   double sum = 0.0;
@@ -168,17 +232,22 @@ __global__ void __launch_bounds__(kThreads) k_scale(const __grid_constant__ Grad
   // elements whose results are not below 2^-149 anyway.
   const float before = !(share < 0x1p-100) ? 1.f : share < 0x1p-160 ? 0x1p-120f : 0x1p-64f;
   const float scale = share >= 1.0 ? 1.f : (float)(share / before);  // (NaN stays NaN)
-  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    const Ref& r = a.ref[ref_of(a, c)];
-    if (scale == 1.f && r.data == r.out) continue;  // nothing changes
-    const int64_t base = (int64_t)(c - r.first) * kChunk;
-    if (r.type == MM_BF16) {
-      if (r.out_type == MM_BF16) scale_chunk<__nv_bfloat16, __nv_bfloat16>(r, base, before, scale);
-      else scale_chunk<__nv_bfloat16, float>(r, base, before, scale);
-    } else {
-      if (r.out_type == MM_BF16) scale_chunk<float, __nv_bfloat16>(r, base, before, scale);
-      else scale_chunk<float, float>(r, base, before, scale);
+  int c, end;
+  run_of(a, c, end);
+  if (c >= end) return;
+  for (int i = ref_of(a, end - 1); c < end; --i) {
+    const Ref& r = a.ref[i];
+    const int first = r.first, from = max(c, first);
+    if (!(scale == 1.f && r.data == r.out)) {  // (nothing changes)
+      if (r.type == MM_BF16) {
+        if (r.out_type == MM_BF16) scale_chunks<__nv_bfloat16, __nv_bfloat16>(r, first, from, end, before, scale);
+        else scale_chunks<__nv_bfloat16, float>(r, first, from, end, before, scale);
+      } else {
+        if (r.out_type == MM_BF16) scale_chunks<float, __nv_bfloat16>(r, first, from, end, before, scale);
+        else scale_chunks<float, float>(r, first, from, end, before, scale);
+      }
     }
+    end = from;
   }
 }
 
@@ -198,7 +267,7 @@ cudaError_t launch_refs(const mm_tensor_ref* t, int count, bool scale, GradArgs<
     if (t[i].count == 0) continue;
     a.ref[a.n++] = Ref{t[i].data, t[i].out, t[i].count, (int32_t)chunks, (int16_t)t[i].type,
                        (int16_t)t[i].out_type};
-    chunks += (t[i].count + kChunk - 1) / kChunk;
+    chunks += (t[i].count + chunk_of(t[i].type) - 1) / chunk_of(t[i].type);
   }
   if (chunks >= (int64_t)1 << 31) return cudaErrorInvalidValue;
   a.chunks = (int)chunks;

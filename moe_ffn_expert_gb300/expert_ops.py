@@ -69,9 +69,9 @@ def expert_table(topk_ids, num_experts):
     offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
     row = torch.empty((T, K), dtype=torch.int32, device=dev)
     slot = torch.empty(T * K, dtype=torch.int32, device=dev)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if T * K > 2048 else None
     _abi.check(_abi._lib().mm_expert_table(
-        at, ids.data_ptr(), offsets.data_ptr(), row.data_ptr(), slot.data_ptr(), ws.data_ptr(), nbytes,
+        at, ids.data_ptr(), offsets.data_ptr(), row.data_ptr(), slot.data_ptr(), _ptr(ws), nbytes,
         _stream(ids)), "mm_expert_table")
     return ExpertTable(offsets, row, slot, T, K, E)
 

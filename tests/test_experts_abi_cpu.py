@@ -113,7 +113,9 @@ def test_expert_host_checks():
     d, f = desc(), desc(type=1)
     n = lib.mm_expert_table_workspace_size(ref(d))
     assert n >= 256
-    assert table(d, *four, size=n - 1) == WS and table(d, *four, w=None) == WS and table(d, *four, w=64) == WS
+    many = desc(T=2049)  # (up to 2048 slots need no workspace)
+    n = lib.mm_expert_table_workspace_size(ref(many))
+    assert table(many, *four, size=n - 1) == WS and table(many, *four, w=None) == WS and table(many, *four, w=64) == WS
     for i in range(4):
         for p in (None, 2):
             assert table(d, *four[:i], p, *four[i + 1:]) == BAD
