@@ -97,12 +97,14 @@ typedef struct mm_grouped_desc {
   uint32_t flags;
 } mm_grouped_desc;
 
-mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* weight,
-                        const int32_t* offsets, void* out, void* stream);
+/* Bytes of workspace (0: unsupported sizes). Need no initialisation; one call at a time may use them.
+ * They depend on the current device's number of SMs. Where mm_grouped_mm's is 256, it uses none (NULL). */
+size_t mm_grouped_mm_workspace_size(const mm_grouped_desc* d);
+size_t mm_grouped_weight_grad_workspace_size(const mm_grouped_desc* d);
 
-/* Bytes of workspace that mm_grouped_mm_weight_grad needs (0: unsupported sizes). Needs no
- * initialisation; one call at a time may use it. */
-size_t mm_grouped_workspace_size(const mm_grouped_desc* d);
+mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* weight,
+                        const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream);
 
 /* accumulate: the sums are added to what d_weight holds (in 32 bits, one rounding); experts without
  * rows keep theirs. d_weight has W's layout. */

@@ -175,8 +175,9 @@ def _lib():
         "mm_grad_norm": (st, [ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P]),
         "mm_grad_clip": (st, [ctypes.c_int64, _P, ctypes.c_double, ctypes.c_double, _P, _P,
                               ctypes.c_size_t, _P]),
-        "mm_grouped_workspace_size": (ctypes.c_size_t, [_P]),
-        "mm_grouped_mm": (st, [_P] * 6),
+        "mm_grouped_mm_workspace_size": (ctypes.c_size_t, [_P]),
+        "mm_grouped_weight_grad_workspace_size": (ctypes.c_size_t, [_P]),
+        "mm_grouped_mm": (st, [_P] * 6 + [ctypes.c_size_t, _P]),
         "mm_grouped_mm_weight_grad": (st, [_P] * 5 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
     }
     for name, (res, args) in sig.items():

@@ -25,6 +25,13 @@
 // The dealing warp of the even CTA tells all others the tiles through a queue, ahead of their use. Rows'
 // tiles are much alike: every CTA has every step-th. Weights' tiles go by the experts' rows: they are
 // claimed from a counter, largest sums first.
+//
+// The tensor cores' sums lose about 2^-30 of their value with every term, always towards zero. Where the
+// result has 32 bits a sum is therefore cut into runs of at most kRun blocks, which the storing warps add
+// up in registers (8192 rows by 7168 x 2048: 5.6e-6 of the result's norm off without, below 1e-6 with).
+//
+// Few tiles, or one expert with most rows, would leave SMs idle: then sums are cut over k, the parts go to
+// slices of 32-bit numbers in the workspace, and a launch behind adds the slices in their order.
 #include <algorithm>
 #include <atomic>
 
@@ -35,8 +42,13 @@
 namespace mm {
 namespace {
 
-constexpr int kThreads = 352;      // warps that load, multiply and deal out tiles, eight that store
-constexpr int kStoreWarps = 8, kFirstStore = 3;
+constexpr int kThreads = 384;      // warps that load, multiply and deal out tiles (and none), eight that store
+constexpr int kStoreWarps = 8, kFirstStore = 4;
+// Registers of a thread: the block is launched with 168 x 384, and the storing warps, which hold a tile's
+// 128 sums per thread, take over what the first four warps do not need (56 x 128 + 224 x 256 of them).
+constexpr int kFewRegs = 56, kManyRegs = 224;
+static_assert(kFewRegs * 32 * kFirstStore + kManyRegs * 32 * kStoreWarps <= 168 * kThreads, "register shares");
+constexpr int kRun = 8;            // blocks of 64 terms
 constexpr int kQueue = 8;          // tiles told and not yet taken by all
 constexpr int kMaxE = 1024;
 constexpr int kTile = 128;         // columns of the M operand per CTA
@@ -67,6 +79,11 @@ struct Args {
   int stages;
   uint32_t stage_bytes;
   int f32, accumulate;
+  float* slices;  // sums of parts, rows of I
+  int64_t slice_rows;  // as many as there are
+  int parts;      // rows: parts of every sum, of part_blocks blocks (1: no parts, no slices)
+  int part_blocks;
+  int part_rows;  // weights: experts with more rows than this have parts of at most as many
   int* next;      // counter of claimed tiles, or null: every step-th
   uint64_t wait_ns;
   int stall;      // test hook: CTA 0 withholds its first accumulator
@@ -74,11 +91,18 @@ struct Args {
 
 // A tile. 32 bytes, as the queue holds it.
 struct __align__(16) Unit {
-  int e, i0, j0;   // i0: first column of the (even) CTA; j0: rows: first row of the chunk in all rows
+  int e, i0, j0;   // i0: first column of the (even) CTA; j0: first row of B (rows) or column of B (weights)
   int n;           // columns of the accumulator that are stored; < 0: no more tiles
-  int row0, k;     // weights: the expert's first row; terms of a sum
-  int unused[2];
+  int k0, k;       // first term of the sum (weights: a row) and their number
+  int row;         // row of the output, or of the slices, of the first column
+  int slice;       // whether it goes to the slices
   __device__ __forceinline__ int n16() const { return (n + 15) & ~15; }
+  __device__ __forceinline__ int blocks() const { return (k + 63) / 64; }
+  // Blocks of a run: all, or (wide results) at most kRun of as many equal runs as it takes.
+  __device__ __forceinline__ int run(bool wide) const {
+    const int b = blocks(), runs = (b + kRun - 1) / kRun;
+    return !wide || runs <= 1 ? b : (b + runs - 1) / runs;
+  }
 };
 
 // mbar_wait for what the other CTA's threads wrote before they arrived.
@@ -147,8 +171,8 @@ struct Ring {
 };
 
 // Where the experts' rows start (E + 1 numbers), how many chunks of rows the experts before each have,
-// and (weights) the experts by falling numbers of rows, in shared memory. False if the offsets are no
-// such table.
+// and (weights) the experts by falling numbers of rows, in which order the chunks are counted then, in
+// shared memory. False if the offsets are no such table.
 template <bool WEIGHTS>
 __device__ __forceinline__ bool build_table(const Args& a, int* start, int* first, uint16_t* order) {
   __shared__ int sums[kThreads / 32];
@@ -165,7 +189,8 @@ __device__ __forceinline__ bool build_table(const Args& a, int* start, int* firs
       bad |= s < 0 || t < s || t > a.R;
       start[e] = s;
       if (e == a.E - 1) start[a.E] = t;
-      tiles[p] = WEIGHTS ? 1 : (t - s + a.chunk - 1) / a.chunk;
+      // (weights: an expert without rows has a tile too, of zeros)
+      tiles[p] = WEIGHTS ? max(1, (t - s + a.part_rows - 1) / a.part_rows) : (t - s + a.chunk - 1) / a.chunk;
     }
     mine += tiles[p];
   }
@@ -187,16 +212,37 @@ __device__ __forceinline__ bool build_table(const Args& a, int* start, int* firs
     base += tiles[p];
     if (e == a.E - 1) first[a.E] = base;
   }
-  if constexpr (WEIGHTS) {  // the rank of an expert: how many have more rows, or as many and come first
+  if constexpr (WEIGHTS) {
+    // experts by falling numbers of rows (those with parts as if they had part_rows, so first): the rank
+    // of an expert is how many have more, or as many and come first
+    __syncthreads();
     for (int e = tid; e < a.E; e += kThreads) {
-      const int rows = start[e + 1] - start[e];
+      const int rows = min(a.part_rows, start[e + 1] - start[e]);
       int rank = 0;
 #pragma unroll 4
       for (int o = 0; o < a.E; ++o) {
-        const int other = start[o + 1] - start[o];
+        const int other = min(a.part_rows, start[o + 1] - start[o]);
         rank += other > rows || (other == rows && o < e);
       }
       order[rank] = (uint16_t)e;
+    }
+    __syncthreads();
+    // first: chunks of the experts before in this order (slices are numbered by it)
+    if (tid < 32) {
+      int base = 0;
+      for (int r0 = 0; r0 < a.E; r0 += 32) {
+        const int r = r0 + lane, e = r < a.E ? order[r] : 0;
+        const int c = r < a.E ? max(1, (start[e + 1] - start[e] + a.part_rows - 1) / a.part_rows) : 0;
+        int upto = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+          if (lane >= d) upto += v;
+        }
+        if (r < a.E) first[r] = base + upto - c;
+        base += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      }
+      if (lane == 0) first[a.E] = base;
     }
   }
   __syncthreads();
@@ -208,32 +254,39 @@ template <bool WEIGHTS, int PAIR>
 __device__ __forceinline__ Unit unit_at(const Args& a, const int* start, const int* first,
                                         const uint16_t* order, int u, int i_tiles, int j_tiles) {
   Unit t{};
+  const int per = WEIGHTS ? i_tiles * j_tiles : i_tiles * a.parts;
+  const int q = u / per;
+  int lo = 0, hi = a.E;  // first[lo] <= q < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= q) lo = mid; else hi = mid;
+  }
+  const int chunks = first[lo + 1] - first[lo];
+  t.e = WEIGHTS ? order[lo] : lo;
+  const int rows = start[t.e + 1] - start[t.e];
   if constexpr (WEIGHTS) {
-    const int per = i_tiles * j_tiles, at = u / per;
-    t.e = order[at];
-    const int in = u - at * per, jt = in / i_tiles;
+    const int in = u - q * per, jt = in / i_tiles, c = q - first[lo];
     t.i0 = (in - jt * i_tiles) * kTile * PAIR;
     t.j0 = jt * a.chunk;
     t.n = min(a.chunk, a.J - t.j0);
-    t.row0 = start[t.e];
-    t.k = start[t.e + 1] - t.row0;
+    // equal parts of whole blocks
+    const int part = chunks == 1 ? rows : ((rows + chunks - 1) / chunks + 63) & ~63;
+    t.k0 = start[t.e] + c * part;
+    t.k = min(part, rows - c * part);
+    t.slice = chunks > 1;
+    t.row = (t.slice ? q : t.e) * a.J + t.j0;
   } else {
-    const int q = u / i_tiles;
-    int lo = 0, hi = a.E;  // first[lo] <= q < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= q) lo = mid; else hi = mid;
-    }
-    t.e = lo;
-    const int chunks = first[lo + 1] - first[lo], in = u - first[lo] * i_tiles;
-    const int it = in / chunks, c = in - it * chunks;
-    const int rows = start[lo + 1] - start[lo];
+    const int in = u - first[lo] * per, it = in / (chunks * a.parts);
+    const int rest = in - it * chunks * a.parts, c = rest / a.parts, p = rest - c * a.parts;
     // equal chunks; as none is above a.chunk the last one has a row at least
-    const int per = ((rows + chunks - 1) / chunks + 15) & ~15;
+    const int size = ((rows + chunks - 1) / chunks + 15) & ~15;
     t.i0 = it * kTile * PAIR;
-    t.j0 = start[lo] + c * per;
-    t.n = min(per, rows - c * per);
-    t.k = a.K;
+    t.j0 = start[t.e] + c * size;
+    t.n = min(size, rows - c * size);
+    t.k0 = p * a.part_blocks * 64;
+    t.k = min(a.part_blocks * 64, a.K - t.k0);
+    t.slice = a.parts > 1;
+    t.row = p * a.R + t.j0;
   }
   return t;
 }
@@ -244,58 +297,44 @@ __device__ __forceinline__ void fill(void* p, int64_t words, uint32_t v, int thr
   for (int64_t i = thread; i < words; i += threads) w[i] = make_uint4(v, v, v, v);
 }
 
-// Up to 32 columns of the accumulator (this lane: one i) to rows row .. of the output; n: how many there
-// are. The address of a row is that of the one before plus the pitch, as 64-bit products per element were
-// most of an epilogue's instructions.
-template <bool F32, bool ADD, bool FULL>
-__device__ __forceinline__ void store_rows(const Args& a, const float (&v)[32], int64_t row, int i, int n,
-                                           int lane) {
-  if constexpr (F32) {
-    if (i >= a.I) return;
-    float* p = static_cast<float*>(a.out) + row * a.I + i;
-    float old[32];
+// Up to 32 sums of this lane's column i, to rows row .. of `out`; n: how many there are. The address of a
+// row is that of the one before plus the pitch, as 64-bit products per element were most of an epilogue's
+// instructions.
+template <bool ADD>
+__device__ __forceinline__ void store_fp32(const Args& a, float* out, const float (&v)[32], int64_t row, int i,
+                                           int n) {
+  if (i >= a.I) return;
+  float* p = out + row * a.I + i;
+  if (!ADD && n >= 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j, p += a.I) *p = v[j];
+    return;
+  }
+#pragma unroll
+  for (int j0 = 0; j0 < 32; j0 += 8, p += 8 * (int64_t)a.I) {
+    float old[8];
     if constexpr (ADD) {
-      const float* at = p;
 #pragma unroll
-      for (int j = 0; j < 32; ++j, at += a.I) old[j] = FULL || j < n ? *at : 0.f;
+      for (int j = 0; j < 8; ++j) old[j] = j0 + j < n ? p[j * (int64_t)a.I] : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j, p += a.I)
-      if (FULL || j < n) *p = ADD ? v[j] + old[j] : v[j];
-  } else {
-    // Two neighbouring lanes exchange, so that each has a pair of neighbouring columns of one row: the
-    // even lane of row j, the odd one of row j + 1.
-    const int odd = lane & 1;
-    const bool there = i < a.I;
-    const uint32_t halves = odd ? 0x3276 : 0x5410;
-    uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row + odd) * a.I + (i & ~1));
-#pragma unroll
-    for (int j = 0; j < 32; j += 2, p += a.I) {
-      if constexpr (ADD) {  // (the sum is rounded, not its addend)
-        const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
-        if (there && (FULL || j + odd < n)) {
-          const uint32_t old = *p;
-          *p = pack_bf16((odd ? other : v[j]) + bf16_lo(old), (odd ? v[j + 1] : other) + bf16_hi(old));
-        }
-      } else {
-        const uint32_t mine = pack_bf16(v[j], v[j + 1]);
-        const uint32_t both = __byte_perm(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1), halves);
-        if (there && (FULL || j + odd < n)) *p = both;
-      }
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < n) p[j * (int64_t)a.I] = ADD ? v[j0 + j] + old[j] : v[j0 + j];
   }
 }
 
-__device__ __forceinline__ void store_columns(const Args& a, const float (&v)[32], int64_t row, int i, int n,
-                                              int lane) {
-  if (a.accumulate) {
-    if (a.f32) store_rows<true, true, false>(a, v, row, i, n, lane);
-    else store_rows<false, true, false>(a, v, row, i, n, lane);
-  } else if (a.f32) {
-    if (n >= 32) store_rows<true, false, true>(a, v, row, i, n, lane);
-    else store_rows<true, false, false>(a, v, row, i, n, lane);
-  } else {
-    store_rows<false, false, false>(a, v, row, i, n, lane);
+// The same added to bf16 numbers. Two neighbouring lanes exchange, so that each has a pair of neighbouring
+// columns of one row: the even lane of row j, the odd one of row j + 1.
+__device__ __forceinline__ void add_bf16(const Args& a, const float (&v)[32], int64_t row, int i, int n, int lane) {
+  const int odd = lane & 1;
+  uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (row + odd) * a.I + (i & ~1));
+#pragma unroll
+  for (int j = 0; j < 32; j += 2, p += a.I) {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+    if (i < a.I && j + odd < n) {
+      const uint32_t old = *p;
+      *p = pack_bf16((odd ? other : v[j]) + bf16_lo(old), (odd ? v[j + 1] : other) + bf16_hi(old));
+    }
   }
 }
 
@@ -312,43 +351,48 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16])
       : "memory");
 }
 
-// The same as bf16 by way of shared memory (`stage`, this warp's 32 rows of 64 bytes): 8 x 8 blocks are
-// stored transposed, and rows leave in words of 16 bytes. A third of the instructions of the exchange
-// between lanes. A row's 16-byte words are turned by half its number, so that eight rows' words of one
-// block lie in different banks. i: the warp's first column.
-__device__ __forceinline__ void store_staged(const Args& a, uint32_t taddr, uint32_t stage, int64_t row, int i,
-                                             int n, int lane) {
+// 32 lanes x 32 columns of the accumulator as bf16: p[4c + m] is what stmatrix stores as block m of the
+// 8 columns c.
+__device__ __forceinline__ void load_bf16(uint32_t taddr, uint32_t (&p)[16]) {
   uint32_t lo[16], hi[16];
   tmem_ld_16x32(taddr, lo);
   tmem_ld_16x32(taddr + (16u << 16), hi);
   tmem_ld_wait();
-  __syncwarp();  // the lanes have read what was here
-  const uint32_t to = stage + (lane & 7) * 64 + (((lane >> 3) ^ (lane >> 1 & 3)) << 4);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t p[4];
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const uint32_t* r = (m < 2 ? lo : hi) + 4 * c + 2 * (m & 1);
-      p[m] = pack_bf16(__uint_as_float(r[0]), __uint_as_float(r[1]));
+      p[4 * c + m] = pack_bf16(__uint_as_float(r[0]), __uint_as_float(r[1]));
     }
+}
+
+// Those to rows row .. of the output by way of shared memory (`stage`, this warp's 32 rows of 64 bytes):
+// 8 x 8 blocks are stored transposed, and rows leave in words of 16 bytes; a third of the instructions
+// that an exchange between lanes takes. A row's 16-byte words are turned by half its number, so that
+// eight rows' words of one block lie in different banks. i: the warp's first column.
+__device__ __forceinline__ void store_bf16(const Args& a, const uint32_t (&p)[16], uint32_t stage, int64_t row,
+                                           int i, int n, int lane) {
+  __syncwarp();  // the lanes have read what was here
+  const uint32_t to = stage + (lane & 7) * 64 + (((lane >> 3) ^ (lane >> 1 & 3)) << 4);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to + c * 512),
-                 "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                 "r"(p[4 * c]), "r"(p[4 * c + 1]), "r"(p[4 * c + 2]), "r"(p[4 * c + 3])
                  : "memory");
-  }
   __syncwarp();
   const int j = lane >> 2, w = lane & 3;
   const uint32_t from = stage + j * 64 + ((w ^ (j >> 1 & 3)) << 4);
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + (row + j) * a.I + i + 8 * w;
+  __nv_bfloat16* at = static_cast<__nv_bfloat16*>(a.out) + (row + j) * a.I + i + 8 * w;
   const bool there = i + 8 * w < a.I;
 #pragma unroll
-  for (int c = 0; c < 4; ++c, p += 8 * a.I) {
+  for (int c = 0; c < 4; ++c, at += 8 * (int64_t)a.I) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(from + c * 512)
                  : "memory");
-    if (there && j + 8 * c < n) *reinterpret_cast<uint4*>(p) = v;
+    if (there && j + 8 * c < n) *reinterpret_cast<uint4*>(at) = v;
   }
 }
 
@@ -413,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int i_tiles = (a.I + kTile * PAIR - 1) / (kTile * PAIR);
   const int j_tiles = WEIGHTS ? (a.J + a.chunk - 1) / a.chunk : 1;
-  const int units = !good ? 0 : WEIGHTS ? a.E * i_tiles * j_tiles : first_chunk[a.E] * i_tiles;
+  const int units = !good ? 0 : first_chunk[a.E] * i_tiles * (WEIGHTS ? j_tiles : a.parts);
 
   // Entry number q of the queue, once it is there; false if the wait ran out. A lane reads a word, so
   // that what frees the slot needs all words to have arrived: the odd CTA's arrival is then one without
@@ -427,8 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.i0 = __shfl_sync(0xFFFFFFFFu, word, 1);
     t.j0 = __shfl_sync(0xFFFFFFFFu, word, 2);
     t.n = __shfl_sync(0xFFFFFFFFu, word, 3);
-    t.row0 = __shfl_sync(0xFFFFFFFFu, word, 4);
+    t.k0 = __shfl_sync(0xFFFFFFFFu, word, 4);
     t.k = __shfl_sync(0xFFFFFFFFu, word, 5);
+    t.row = __shfl_sync(0xFFFFFFFFu, word, 6);
+    t.slice = __shfl_sync(0xFFFFFFFFu, word, 7);
     if (lane == 0) {
       if (PAIR == 2 && rank == 1) mbar_arrive_remote_relaxed(mapa_shared(taken_bar(slot), 0));
       else mbar_arrive(taken_bar(slot));
@@ -436,222 +482,285 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------ loads
-    Ring ring(empty_bar(0), 1, a.stages, limit);
-    int it = 0;
-    bool ok = true;
-    const bool kmajor = a.a_kmajor != 0;
-    for (int q = 0; ok; ++q) {
-      Unit t;
-      if (!take(q, t) || t.n < 0) break;
-      const int half = uniform(t.n16() / PAIR), blocks = uniform((t.k + 63) / 64);
-      const int e = uniform(t.e), i0 = uniform(t.i0) + rank * kTile, row0 = uniform(t.row0);
-      const int j0 = uniform(t.j0) + rank * half;
-      const int last = WEIGHTS ? uniform(t.k) - (blocks - 1) * 64 : 64;  // rows of the last block
-      for (int kb = 0; kb < blocks; ++kb, ++it) {
-        if (!ring.wait()) {
-          ok = false;
-          break;
-        }
-        ring.ask_next();
-        if (elect_one()) {
-          const uint32_t sa = sbase + ring.s * a.stage_bytes, sb = sa + kABytes;
-          const int k0 = kb * 64;
-          const bool part = WEIGHTS && kb == blocks - 1 && last < 64;
-          const uint32_t bytes = WEIGHTS ? (2 + (half + 63) / 64) * (part ? (last + 15) & ~15 : 64) * 128u
-                                         : kABytes + half * 128u;
-          // the two CTAs' bytes of a stage count on the even one's barrier
-          uint32_t bar = full_bar(ring.s);
-          if (rank == 0) mbar_arrive_expect_tx(bar, PAIR * bytes);
-          if constexpr (PAIR == 2) bar = mapa_shared(bar, 0);
-          auto load2 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
-            if constexpr (PAIR == 2) tma_load_2d_pair(dst, map, bar, c0, c1);
-            else tma_load_2d(dst, map, bar, c0, c1);
-          };
-          auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
-            if constexpr (PAIR == 2) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
-            else tma_load_3d(dst, map, bar, c0, c1, c2);
-          };
-          if constexpr (WEIGHTS) {
-            // k-rows r .. of the stage from rows `from` of the operands
-            auto boxes = [&](const CUtensorMap* ma, const CUtensorMap* mb, int r, int from) {
-              load2(sa + r * 128, ma, i0, from);
-              load2(sa + kBlock + r * 128, ma, i0 + 64, from);
-#pragma unroll
-              for (int c = 0; c < kMaxN / PAIR; c += 64)
-                if (c < half) load2(sb + c / 64 * kBlock + r * 128, mb, j0 + c, from);
+  if (warp < kFirstStore) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (warp == 0) {
+      // ------------------------------------------------ loads
+      Ring ring(empty_bar(0), 1, a.stages, limit);
+      int it = 0;
+      bool ok = true;
+      const bool kmajor = a.a_kmajor != 0;
+      for (int q = 0; ok; ++q) {
+        Unit t;
+        if (!take(q, t) || t.n < 0) break;
+        const int half = uniform(t.n16() / PAIR), blocks = uniform(t.blocks());
+        const int e = uniform(t.e), i0 = uniform(t.i0) + rank * kTile, first_k = uniform(t.k0);
+        const int j0 = uniform(t.j0) + rank * half;
+        const int last = WEIGHTS ? uniform(t.k) - (blocks - 1) * 64 : 64;  // rows of the last block
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
+          if (!ring.wait()) {
+            ok = false;
+            break;
+          }
+          ring.ask_next();
+          if (elect_one()) {
+            const uint32_t sa = sbase + ring.s * a.stage_bytes, sb = sa + kABytes;
+            const int k0 = first_k + kb * 64;
+            const bool part = WEIGHTS && kb == blocks - 1 && last < 64;
+            const uint32_t bytes = WEIGHTS ? (2 + (half + 63) / 64) * (part ? (last + 15) & ~15 : 64) * 128u
+                                           : kABytes + half * 128u;
+            // the two CTAs' bytes of a stage count on the even one's barrier
+            uint32_t bar = full_bar(ring.s);
+            if (rank == 0) mbar_arrive_expect_tx(bar, PAIR * bytes);
+            if constexpr (PAIR == 2) bar = mapa_shared(bar, 0);
+            auto load2 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1) {
+              if constexpr (PAIR == 2) tma_load_2d_pair(dst, map, bar, c0, c1);
+              else tma_load_2d(dst, map, bar, c0, c1);
             };
-            if (!part) {
-              boxes(&m.a, &m.b[0], 0, row0 + k0);
-            } else {
-              if (last & 32) boxes(&m.a_part[0], &m.b_part[0], 0, row0 + k0);
-              if (last & 16) boxes(&m.a_part[1], &m.b_part[1], last & 32, row0 + k0 + (last & 32));
-              if (last & 15) boxes(&m.a_part[2], &m.b_part[2], last & 48, e * 16);
-            }
-          } else {
-            if (kmajor) {
-              load3(sa, &m.a, k0, i0, e);
-            } else {
-              load3(sa, &m.a, i0, k0, e);
-              load3(sa + kBlock, &m.a, i0 + 64, k0, e);
-            }
-            // boxes as half's bits are (256: 128 twice)
-            int r = 0;
-            if (PAIR == 1 && (half & 256)) {
-              load2(sb, &m.b[0], k0, j0);
-              load2(sb + 128 * 128, &m.b[0], k0, j0 + 128);
-            }
+            auto load3 = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
+              if constexpr (PAIR == 2) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
+              else tma_load_3d(dst, map, bar, c0, c1, c2);
+            };
+            if constexpr (WEIGHTS) {
+              // k-rows r .. of the stage from rows `from` of the operands
+              auto boxes = [&](const CUtensorMap* ma, const CUtensorMap* mb, int r, int from) {
+                load2(sa + r * 128, ma, i0, from);
+                load2(sa + kBlock + r * 128, ma, i0 + 64, from);
 #pragma unroll
-            for (int p = 0; p < 5; ++p) {
-              if (half & (128 >> p)) {
-                load2(sb + r * 128, &m.b[p], k0, j0 + r);
-                r += 128 >> p;
+                for (int c = 0; c < kMaxN / PAIR; c += 64)
+                  if (c < half) load2(sb + c / 64 * kBlock + r * 128, mb, j0 + c, from);
+              };
+              if (!part) {
+                boxes(&m.a, &m.b[0], 0, k0);
+              } else {
+                if (last & 32) boxes(&m.a_part[0], &m.b_part[0], 0, k0);
+                if (last & 16) boxes(&m.a_part[1], &m.b_part[1], last & 32, k0 + (last & 32));
+                if (last & 15) boxes(&m.a_part[2], &m.b_part[2], last & 48, e * 16);
+              }
+            } else {
+              if (kmajor) {
+                load3(sa, &m.a, k0, i0, e);
+              } else {
+                load3(sa, &m.a, i0, k0, e);
+                load3(sa + kBlock, &m.a, i0 + 64, k0, e);
+              }
+              // boxes as half's bits are (256: 128 twice)
+              int r = 0;
+              if (PAIR == 1 && (half & 256)) {
+                load2(sb, &m.b[0], k0, j0);
+                load2(sb + 128 * 128, &m.b[0], k0, j0 + 128);
+              }
+#pragma unroll
+              for (int p = 0; p < 5; ++p) {
+                if (half & (128 >> p)) {
+                  load2(sb + r * 128, &m.b[p], k0, j0 + r);
+                  r += 128 >> p;
+                }
               }
             }
           }
+          __syncwarp();
+          ring.next();
         }
-        __syncwarp();
-        ring.next();
       }
-    }
-    // every stage's last release has landed before this CTA may leave
-    for (int s = 0; s < a.stages && s < it && ok; ++s)
-      ok = warp_wait(empty_bar(s), (it - 1 - s) / a.stages & 1u, limit);
-  } else if (warp == 1) {
-    // ------------------------------------------------ multiplies
-    // The warp stays in step and an elected lane of the even CTA issues, from uniform registers (by one
-    // lane's branch with operands of its own an issue took 300 cycles: 131072 rows of 128 experts, 2048
-    // -> 1536, 1015 us, 528 this way).
-    Ring ring(full_bar(0), 0, a.stages, limit);
-    const int a_mn = WEIGHTS || !a.a_kmajor, b_mn = WEIGHTS;
-    const uint64_t adesc = sdesc_sw128(sbase, a_mn ? kBlock : 16, 1024);
-    const uint64_t bdesc = sdesc_sw128(sbase + kABytes, b_mn ? kBlock : 16, 1024);
-    const uint32_t a_step = a_mn ? 2048 / 16 : 2, b_step = b_mn ? 2048 / 16 : 2;
-    uint32_t acc = 0;
-    bool ok = rank == 0;
-    for (int q = 0; ok; ++q) {
-      Unit t;
-      if (!take(q, t) || t.n < 0) break;
-      const int blocks = uniform((t.k + 63) / 64), n16 = uniform(t.n16());
-      if (blocks == 0) continue;
-      const int last = uniform(t.k) - (blocks - 1) * 64;  // terms in the last block
-      const uint32_t buf = acc & 1u;
-      const uint32_t d = tmem + buf * kMaxN;
-      if (!warp_wait(acce_bar(buf), (acc >> 1 & 1u) ^ 1u, limit)) break;
-      tc_fence_after();
-      const uint32_t idesc = idesc_bf16_f32(kTile * PAIR, n16, a_mn, b_mn);
-      for (int kb = 0; kb < blocks; ++kb) {
-        if (!ring.wait()) {
-          ok = false;
-          break;
-        }
-        const uint32_t s = ring.s;
-        ring.ask_next();
-        const int steps = WEIGHTS && kb == blocks - 1 ? (last + 15) / 16 : 4;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t ad = adesc + s * (a.stage_bytes / 16), bd = bdesc + s * (a.stage_bytes / 16);
+      // every stage's last release has landed before this CTA may leave
+      for (int s = 0; s < a.stages && s < it && ok; ++s)
+        ok = warp_wait(empty_bar(s), (it - 1 - s) / a.stages & 1u, limit);
+    } else if (warp == 1) {
+      // ------------------------------------------------ multiplies
+      // The warp stays in step and an elected lane of the even CTA issues, from uniform registers (by one
+      // lane's branch with operands of its own an issue took 300 cycles: 131072 rows of 128 experts, 2048
+      // -> 1536, 1015 us, 528 this way).
+      Ring ring(full_bar(0), 0, a.stages, limit);
+      const int a_mn = WEIGHTS || !a.a_kmajor, b_mn = WEIGHTS;
+      const uint64_t adesc = sdesc_sw128(sbase, a_mn ? kBlock : 16, 1024);
+      const uint64_t bdesc = sdesc_sw128(sbase + kABytes, b_mn ? kBlock : 16, 1024);
+      const uint32_t a_step = a_mn ? 2048 / 16 : 2, b_step = b_mn ? 2048 / 16 : 2;
+      uint32_t acc = 0;
+      bool ok = rank == 0;
+      for (int q = 0; ok; ++q) {
+        Unit t;
+        if (!take(q, t) || t.n < 0) break;
+        const int blocks = uniform(t.blocks()), n16 = uniform(t.n16());
+        const int run = uniform(t.run(a.f32 || a.accumulate || t.slice));
+        const int last = uniform(t.k) - (blocks - 1) * 64;  // terms in the last block
+        const uint32_t idesc = idesc_bf16_f32(kTile * PAIR, n16, a_mn, b_mn);
+        uint32_t buf = 0, d = 0;
+        for (int kb = 0, left = 0; kb < blocks; ++kb) {
+          const bool opens = left == 0;  // a run, in the other accumulator
+          if (opens) {
+            left = min(run, blocks - kb);
+            buf = acc & 1u;
+            d = tmem + buf * kMaxN;
+            if (!warp_wait(acce_bar(buf), (acc >> 1 & 1u) ^ 1u, limit)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (!ring.wait()) {
+            ok = false;
+            break;
+          }
+          const uint32_t s = ring.s;
+          ring.ask_next();
+          const int steps = WEIGHTS && kb == blocks - 1 ? (last + 15) / 16 : 4;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ad = adesc + s * (a.stage_bytes / 16), bd = bdesc + s * (a.stage_bytes / 16);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (WEIGHTS && kk >= steps) continue;
-            if constexpr (PAIR == 2) umma_bf16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb | kk) != 0);
-            else umma_bf16(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb | kk) != 0);
+            for (int kk = 0; kk < 4; ++kk) {
+              if (WEIGHTS && kk >= steps) continue;
+              if constexpr (PAIR == 2) umma_bf16_pair(d, ad + kk * a_step, bd + kk * b_step, idesc, !opens || kk != 0);
+              else umma_bf16(d, ad + kk * a_step, bd + kk * b_step, idesc, !opens || kk != 0);
+            }
+            if constexpr (PAIR == 2) umma_commit_pair_mc(empty_bar(s), 0x3);
+            else umma_commit(empty_bar(s));
+            if (left == 1 && !(a.stall && blockIdx.x == 0 && acc == 0)) {
+              if constexpr (PAIR == 2) umma_commit_pair_mc(accf_bar(buf), 0x3);
+              else umma_commit(accf_bar(buf));
+            }
           }
-          if constexpr (PAIR == 2) umma_commit_pair_mc(empty_bar(s), 0x3);
-          else umma_commit(empty_bar(s));
-          if (kb == blocks - 1 && !(a.stall && blockIdx.x == 0 && acc == 0)) {
-            if constexpr (PAIR == 2) umma_commit_pair_mc(accf_bar(buf), 0x3);
-            else umma_commit(accf_bar(buf));
+          __syncwarp();
+          ring.next();
+          if (--left == 0) ++acc;
+        }
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------ deals out tiles
+      // Two claims are on their way at a time.
+      int u = mine, ahead = mine + step;
+      for (int q = 0; rank == 0; ++q) {
+        int next = ahead + step;
+        if (a.next != nullptr && lane == 0) next = 2 * step + atomicAdd(a.next, 1);
+        Unit t{};
+        if (u < units) t = unit_at<WEIGHTS, PAIR>(a, start, first_chunk, order, u, i_tiles, j_tiles);
+        else t.n = -1;
+        const uint32_t slot = q % kQueue;
+        if (!warp_wait(taken_bar(slot), (q / kQueue & 1u) ^ 1u, limit)) break;
+        if (lane == 0) {
+          queue[slot] = t;
+          mbar_arrive(told_bar(slot));
+          if constexpr (PAIR == 2) {
+            const uint32_t to = mapa_shared(smem_u32(&queue[slot]), 1);
+            st_shared_cluster(to, make_int4(t.e, t.i0, t.j0, t.n));
+            st_shared_cluster(to + 16, make_int4(t.k0, t.k, t.row, t.slice));
+            mbar_arrive_remote(mapa_shared(told_bar(slot), 1));
           }
         }
         __syncwarp();
-        ring.next();
+        if (t.n < 0) break;
+        u = ahead;
+        ahead = __shfl_sync(0xFFFFFFFFu, next, 0);
       }
-      ++acc;
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------ deals out tiles
-    // Two claims are on their way at a time.
-    int u = mine, ahead = mine + step;
-    for (int q = 0; rank == 0; ++q) {
-      int next = ahead + step;
-      if (a.next != nullptr && lane == 0) next = 2 * step + atomicAdd(a.next, 1);
-      Unit t{};
-      if (u < units) t = unit_at<WEIGHTS, PAIR>(a, start, first_chunk, order, u, i_tiles, j_tiles);
-      else t.n = -1;
-      const uint32_t slot = q % kQueue;
-      if (!warp_wait(taken_bar(slot), (q / kQueue & 1u) ^ 1u, limit)) break;
-      if (lane == 0) {
-        queue[slot] = t;
-        mbar_arrive(told_bar(slot));
-        if constexpr (PAIR == 2) {
-          const uint32_t to = mapa_shared(smem_u32(&queue[slot]), 1);
-          st_shared_cluster(to, make_int4(t.e, t.i0, t.j0, t.n));
-          st_shared_cluster(to + 16, make_int4(t.row0, t.k, 0, 0));
-          mbar_arrive_remote(mapa_shared(told_bar(slot), 1));
-        }
-      }
-      __syncwarp();
-      if (t.n < 0) break;
-      u = ahead;
-      ahead = __shfl_sync(0xFFFFFFFFu, next, 0);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     // ------------------------------------------------ stores
     const int set = (warp - kFirstStore) >> 2, quarter = warp & 3;  // (of the accumulator's lanes)
-    const int64_t es = a.f32 ? 4 : 2;
-    const int64_t out_rows = WEIGHTS ? (int64_t)a.E * a.J : a.R;
+    const bool to_slices = !WEIGHTS && a.parts > 1;
+    const int64_t row_words = a.I * (a.f32 ? 4 : 2) / 16;
+    const int64_t all_words = (WEIGHTS ? (int64_t)a.E * a.J : a.R) * row_words;
     const uint32_t nan = a.f32 ? 0x7FC00000u : 0x7FC07FC0u;
-    char* const out = static_cast<char*>(a.out);
+    uint4* const out = static_cast<uint4*>(a.out);
     const int thread = (int)blockIdx.x * (32 * kStoreWarps) + (int)threadIdx.x - 32 * kFirstStore;
     const int threads = (int)gridDim.x * (32 * kStoreWarps);
-    if (!good) {
-      fill(out, out_rows * a.I * es / 16, nan, thread, threads);
+    if (to_slices) {
+      // (the launch behind writes the output)
+    } else if (!good) {
+      fill(out, all_words, nan, thread, threads);
     } else if (!WEIGHTS) {
-      fill(out, start[0] * (a.I * es / 16), 0, thread, threads);
-      fill(out + start[a.E] * (a.I * es), (a.R - start[a.E]) * (a.I * es / 16), 0, thread, threads);
+      fill(out, start[0] * row_words, 0, thread, threads);
+      fill(out + start[a.E] * row_words, (a.R - start[a.E]) * row_words, 0, thread, threads);
     }
     const uint32_t stage = out_stage + (warp - kFirstStore) * kOutBytes;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t acc = 0;
+    // The accumulator of the next run, or false; and its hand-back, when it is in registers.
+    auto arrived = [&]() {
+      const bool ok = warp_wait(accf_bar(acc & 1u), acc >> 1 & 1u, limit);
+      tc_fence_after();
+      return ok;
+    };
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR == 2 && rank != 0) mbar_arrive_remote_relaxed(mapa_shared(acce_bar(acc & 1u), 0));
+        else mbar_arrive(acce_bar(acc & 1u));
+      }
+      ++acc;
+    };
     for (int q = 0;; ++q) {
       Unit t;
       bool ok = take(q, t);
       if (ok && t.n < 0) break;
       if (ok && t.k == 0 && a.accumulate) continue;  // adding zero changes nothing
-      const uint32_t buf = acc & 1u;
-      if (ok && t.k > 0) ok = warp_wait(accf_bar(buf), acc >> 1 & 1u, limit);
-      if (!ok) {  // the tiles that this CTA has or would have had are nobody's: NaN, if not others' results
-        fill(out, out_rows * a.I * es / 16, nan, (int)threadIdx.x - 32 * kFirstStore, 32 * kStoreWarps);
-        break;
-      }
-      tc_fence_after();
-      const int64_t row0 = WEIGHTS ? (int64_t)t.e * a.J + t.j0 : t.j0;
       const int i = t.i0 + rank * kTile + quarter * 32;
-      const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kMaxN;
-      for (int c = set * 32; c < t.n; c += 64) {
-        if (t.k > 0 && !a.f32 && !a.accumulate) {
-          store_staged(a, from + c, stage, row0 + c, i, t.n - c, lane);
-        } else {
-          uint32_t r[32] = {};
-          if (t.k > 0) {
-            tmem_ld_32x32(from + c, r);
-            tmem_ld_wait();
-          }
-          float v[32];
+      const int blocks = t.blocks();
+      if (a.f32 || a.accumulate || t.slice) {
+        float sum[kMaxN / 64][32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          store_columns(a, v, row0 + c, i + lane, t.n - c, lane);
+        for (int g = 0; g < kMaxN / 64; ++g)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[g][j] = 0.f;
+        const int run = t.run(true);
+        for (int kb = 0; kb < blocks && ok; kb += run) {
+          ok = arrived();
+          if (!ok) break;
+#pragma unroll
+          for (int g = 0; g < kMaxN / 64; ++g) {
+            const int c = set * 32 + 64 * g;
+            if (c >= t.n) continue;
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              uint32_t r[16];
+              tmem_ld_32x16(lanes + (acc & 1u) * kMaxN + c + h, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[g][h + j] += __uint_as_float(r[j]);
+            }
+          }
+          release();
+        }
+        if (ok) {
+#pragma unroll
+          for (int g = 0; g < kMaxN / 64; ++g) {
+            const int c = set * 32 + 64 * g;
+            if (c >= t.n) continue;
+            if (t.slice) store_fp32<false>(a, a.slices, sum[g], (int64_t)t.row + c, i + lane, t.n - c);
+            else if (!a.accumulate) store_fp32<false>(a, static_cast<float*>(a.out), sum[g], (int64_t)t.row + c, i + lane, t.n - c);
+            else if (a.f32) store_fp32<true>(a, static_cast<float*>(a.out), sum[g], (int64_t)t.row + c, i + lane, t.n - c);
+            else add_bf16(a, sum[g], (int64_t)t.row + c, i + lane, t.n - c, lane);
+          }
+        }
+      } else {
+        uint32_t p[kMaxN / 64][16];
+        if (ok && blocks > 0) ok = arrived();
+        if (ok) {
+#pragma unroll
+          for (int g = 0; g < kMaxN / 64; ++g) {
+            if (blocks == 0) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) p[g][j] = 0;
+            } else if (set * 32 + 64 * g < t.n) {
+              load_bf16(lanes + (acc & 1u) * kMaxN + set * 32 + 64 * g, p[g]);
+            }
+          }
+          if (blocks > 0) release();
+#pragma unroll
+          for (int g = 0; g < kMaxN / 64; ++g) {
+            const int c = set * 32 + 64 * g;
+            if (c < t.n) store_bf16(a, p[g], stage, (int64_t)t.row + c, i, t.n - c, lane);
+          }
         }
       }
-      if (t.k > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR == 2 && rank != 0) mbar_arrive_remote_relaxed(mapa_shared(acce_bar(buf), 0));
-          else mbar_arrive(acce_bar(buf));
-        }
-        ++acc;
+      if (!ok) {  // the tiles that this CTA has or would have had are nobody's: NaN, if not others' results
+        fill(out, all_words, nan, (int)threadIdx.x - 32 * kFirstStore, 32 * kStoreWarps);
+        if (a.slices != nullptr)
+          fill(a.slices, a.slice_rows * a.I / 4, 0x7FC00000u, (int)threadIdx.x - 32 * kFirstStore,
+               32 * kStoreWarps);
+        break;
       }
     }
   }
@@ -695,6 +804,121 @@ __global__ void __launch_bounds__(256) k_tails(TailArgs a) {
   }
 }
 
+struct JoinArgs {
+  const int32_t* offsets;
+  const float* slices;
+  void* out;
+  int R, E, I, J;
+  int parts;      // rows
+  int part_rows;  // weights
+  int f32, accumulate;
+};
+
+// Four sums of parts `first`, first + stride, ... in their order, to elements 4 w .. of the output.
+__device__ __forceinline__ void join_words(const JoinArgs& a, const float4* slice, int parts, int64_t stride,
+                                           int64_t w) {
+  float4 s = slice[0];
+#pragma unroll 4
+  for (int p = 1; p < parts; ++p) {
+    const float4 v = slice[p * stride];
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  if (a.f32) {
+    float4* at = static_cast<float4*>(a.out) + w;
+    if (a.accumulate) {
+      const float4 v = *at;
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    *at = s;
+  } else {
+    uint2* at = static_cast<uint2*>(a.out) + w;
+    if (a.accumulate) {
+      const uint2 v = *at;
+      s.x += bf16_lo(v.x), s.y += bf16_hi(v.x), s.z += bf16_lo(v.y), s.w += bf16_hi(v.y);
+    }
+    *at = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+  }
+}
+
+// Rows: the sums of the parts; zeros in no expert's rows, NaN for offsets that are no table.
+__global__ void __launch_bounds__(256) k_join_rows(JoinArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  int bad = 0;
+  for (int e = threadIdx.x; e < a.E; e += 256) {
+    const int s = a.offsets[e], t = a.offsets[e + 1];
+    bad |= s < 0 || t < s || t > a.R;
+  }
+  bad = __syncthreads_or(bad);
+  const int words = a.I / 4;
+  const int64_t all = (int64_t)a.R * words;
+  const int begin = a.offsets[0], end = a.offsets[a.E];
+  for (int64_t w = blockIdx.x * 256 + threadIdx.x; w < all; w += (int64_t)gridDim.x * 256) {
+    const int64_t r = w / words;
+    if (bad || r < begin || r >= end) {
+      const uint32_t v = !bad ? 0u : a.f32 ? 0x7FC00000u : 0x7FC07FC0u;
+      if (a.f32) static_cast<uint4*>(a.out)[w] = make_uint4(v, v, v, v);
+      else static_cast<uint2*>(a.out)[w] = make_uint2(v, v);
+    } else {
+      join_words(a, reinterpret_cast<const float4*>(a.slices) + w, a.parts, all, w);
+    }
+  }
+}
+
+// Weights: the sums of the parts of the experts that have some.
+__global__ void __launch_bounds__(256) k_join_weights(JoinArgs a) {
+  constexpr int PER = kMaxE / 256;
+  __shared__ int sums[8];
+  __shared__ int expert[kMaxE], first[kMaxE];  // those with parts, and their first slices
+  __shared__ int count;
+  pdl_wait();
+  pdl_launch_dependents();
+  // Slices are numbered as in build_table: by the experts with part_rows rows or more, in their order.
+  // (Offsets that are no table have left NaN in the output, and no parts.)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int chunks[PER], mine = 0, bad = 0;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int e = tid * PER + p;
+    chunks[p] = 0;
+    if (e < a.E) {
+      const int s = a.offsets[e], t = a.offsets[e + 1];
+      bad |= s < 0 || t < s || t > a.R;
+      if (t - s >= a.part_rows) chunks[p] = (t - s + a.part_rows - 1) / a.part_rows;
+    }
+    mine += chunks[p];
+  }
+  if (tid == 0) count = 0;
+  if (__syncthreads_or(bad)) return;
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int base = upto - mine;
+  for (int w = 0; w < warp; ++w) base += sums[w];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    if (chunks[p] > 1) {
+      const int at = atomicAdd(&count, 1);  // (in any order)
+      expert[at] = tid * PER + p | chunks[p] << 10;
+      first[at] = base;
+    }
+    base += chunks[p];
+  }
+  __syncthreads();
+  const int64_t words = (int64_t)a.J * a.I / 4;
+  for (int x = 0; x < count; ++x) {
+    const int e = expert[x] & 1023, parts = expert[x] >> 10;
+    const float4* slices = reinterpret_cast<const float4*>(a.slices) + first[x] * words;
+    for (int64_t w = (int64_t)blockIdx.x * 256 + tid; w < words; w += (int64_t)gridDim.x * 256)
+      join_words(a, slices + w, parts, words, e * words + w);
+  }
+}
+
 // ------------------------------------------------------------------------------------ host side
 
 inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -710,7 +934,37 @@ mm_status check_desc(const mm_grouped_desc* d) {
   return MM_OK;
 }
 
-// Workspace: the counter, then the panels of both operands of weight gradients.
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Parts of the sums of mm_grouped_mm: as many as bring a launch of few tiles to a tile of one CTA per SM,
+// of 4 blocks at least. (1 row by a matrix 7168 x 2048, 16 tiles: 31 us whole.)
+struct RowParts {
+  int parts, blocks;  // blocks of a part
+};
+RowParts row_parts(const mm_grouped_desc& d) {
+  const int64_t blocks = div_up(d.K, 64);
+  const int64_t tiles = (d.R / kMaxN + std::min<int64_t>(d.E, d.R)) * div_up(d.N, kTile);  // at most
+  const int64_t want = std::min<int64_t>(device_sm_count() / std::max<int64_t>(1, tiles), blocks / 4);
+  if (want < 2) return {1, (int)blocks};
+  const int64_t part = div_up(blocks, want);
+  return {(int)div_up(blocks, part), (int)part};
+}
+
+// Rows of an expert from which on its weight gradient has parts: half of what each pair of SMs gets on
+// average, so that no expert's tiles outlast the others' by more; and the slices of the experts above it,
+// at most (each has fewer than twice its rows / part_rows).
+struct WeightParts {
+  int64_t rows, slices;
+};
+WeightParts weight_parts(const mm_grouped_desc& d) {
+  const int64_t I = d.transposed ? d.K : d.N, J = d.transposed ? d.N : d.K;
+  const int64_t tiles = div_up(I, 2 * kTile) * div_up(J, kMaxN);
+  const int64_t rows = std::max<int64_t>(512, div_up(div_up(d.R * tiles, std::max(2, device_sm_count())), 64) * 64);
+  if (d.R <= rows) return {d.R + 1, 0};
+  return {rows, 2 * d.R / rows};
+}
+
+// Workspace of weight gradients: the counter, the panels of both operands, the slices.
 constexpr size_t kHeaderBytes = 256;
 size_t panel_bytes(int64_t E, int64_t cols) { return ((size_t)E * 16 * cols * 2 + 255) / 256 * 256; }
 
@@ -786,26 +1040,39 @@ extern "C" {
 
 int mm_experts_version(void) { return 1; }
 
-size_t mm_grouped_workspace_size(const mm_grouped_desc* d) {
-  return check_desc(d) == MM_OK ? kHeaderBytes + panel_bytes(d->E, d->K) + panel_bytes(d->E, d->N) : 0;
+size_t mm_grouped_mm_workspace_size(const mm_grouped_desc* d) {
+  if (check_desc(d) != MM_OK) return 0;
+  const RowParts p = row_parts(*d);
+  return p.parts == 1 ? 256 : std::max<size_t>(256, (size_t)p.parts * d->R * d->N * 4);
+}
+
+size_t mm_grouped_weight_grad_workspace_size(const mm_grouped_desc* d) {
+  if (check_desc(d) != MM_OK) return 0;
+  return kHeaderBytes + panel_bytes(d->E, d->K) + panel_bytes(d->E, d->N) +
+         (size_t)weight_parts(*d).slices * d->K * d->N * 4;
 }
 
 mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* weight,
-                        const int32_t* offsets, void* out, void* stream) {
+                        const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream) {
   mm_status s = check_desc(d);
   if (s != MM_OK) return s;
   if (!aligned_to(rows, 16) || !aligned_to(weight, 16) || !aligned_to(out, 16) || !aligned_to(offsets, 4))
     return MM_ERR_INVALID_ARG;
   if (d->R == 0) return MM_OK;
   if (!rows || !weight || !out || !offsets) return MM_ERR_INVALID_ARG;
+  const RowParts parts = row_parts(*d);
+  if (parts.parts > 1 && (workspace == nullptr || !aligned_to(workspace, 256) ||
+                          workspace_bytes < mm_grouped_mm_workspace_size(d)))
+    return MM_ERR_WORKSPACE;
   clear_error();
   MM_TRY(bind_context());
   // Pairs read half as much of their operands per product. Where a launch has no more tiles of one CTA
   // than SMs, these spread the matrices' columns over twice as many. (us a call, one CTA a tile and pairs:
-  // 8 rows of 8 of 128 experts, 2048 -> 1536, 13.1 and 13.8; 512 rows of 128, 768 -> 2048, 73.5 and 66.0;
-  // 131072 rows of 128, 2048 -> 1536, 592 and 528.)
+  // 8 rows of 8 of 128 experts, 2048 -> 1536, 13.1 and 14.1; 512 rows of 128, 768 -> 2048, 71.1 and 66.5;
+  // 131072 rows of 128, 2048 -> 1536, 590 and 543.)
   const int64_t chunks = d->R / kMaxN + std::min<int64_t>(d->E, d->R);  // at most
-  const bool few = chunks * ((d->N + kTile - 1) / kTile) <= device_sm_count();
+  const bool few = chunks * div_up(d->N, kTile) <= device_sm_count();
   const int pair = d->flags & MM_GROUPED_CTA_PAIRS || (!(d->flags & MM_GROUPED_SINGLE_CTA) && !few) ? 2 : 1;
   Maps m;
   Args a{};
@@ -818,6 +1085,12 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   a.a_kmajor = d->transposed != 0;
   a.f32 = d->out_type == MM_FP32;
   a.chunk = (int)std::min<int64_t>(kMaxN, (d->R + 15) / 16 * 16);
+  a.parts = parts.parts;
+  a.part_blocks = parts.blocks;
+  if (a.parts > 1) {
+    a.slices = static_cast<float*>(workspace);
+    a.slice_rows = a.parts * a.R;
+  }
   const int64_t inner = d->transposed ? d->K : d->N, outer = d->transposed ? d->N : d->K;
   const uint64_t dims[3] = {(uint64_t)inner, (uint64_t)outer, (uint64_t)d->E};
   const uint64_t strides[2] = {(uint64_t)inner * 2, (uint64_t)inner * outer * 2};
@@ -826,11 +1099,16 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   for (int p = 0; p < 5; ++p) ok = ok && map2(&m.b[p], rows, d->K, d->R, 128u >> p);
   if (!ok) return cuda_fail(cudaErrorInvalidValue, "grouped product tensor maps");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t units = chunks * ((d->N + kTile * pair - 1) / (kTile * pair));
+  const int64_t units = chunks * div_up(d->N, kTile * pair) * a.parts;
   if (pair == 2)
     MM_TRY((launch<2, false>(m, a, units, d->flags, st)));
   else
     MM_TRY((launch<1, false>(m, a, units, d->flags, st)));
+  if (a.parts > 1) {
+    const JoinArgs j{offsets, a.slices, out, a.R, a.E, a.I, 0, a.parts, 0, a.f32, 0};
+    const int64_t blocks = div_up((int64_t)a.R * a.I / 4, 256);
+    MM_TRY(launch_pdl(k_join_rows, dim3((unsigned)std::min<int64_t>(blocks, 1024)), dim3(256), 0, st, j));
+  }
   return MM_OK;
 }
 
@@ -842,7 +1120,8 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
   if (!aligned_to(rows, 16) || !aligned_to(d_out, 16) || !aligned_to(d_weight, 16) || !aligned_to(offsets, 4))
     return MM_ERR_INVALID_ARG;
   if (!d_weight || !offsets || (d->R > 0 && (!rows || !d_out))) return MM_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < mm_grouped_workspace_size(d))
+  if (workspace == nullptr || !aligned_to(workspace, 256) ||
+      workspace_bytes < mm_grouped_weight_grad_workspace_size(d))
     return MM_ERR_WORKSPACE;
   clear_error();
   MM_TRY(bind_context());
@@ -852,7 +1131,12 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
       MM_TRY(cudaMemsetAsync(d_weight, 0, (size_t)d->E * d->K * d->N * (d->out_type == MM_FP32 ? 4 : 2), st));
     return MM_OK;
   }
-  const int pair = d->flags & MM_GROUPED_SINGLE_CTA ? 1 : 2;
+  // Pairs, unless the experts have few rows: a tile is then little more than its result's way out, which
+  // the two CTAs of a pair wait for together. (us, one CTA a tile and pairs: 512 rows of 128 experts,
+  // 768 x 2048, 88 and 105; 65536 of 128, 2048 x 1536, 359 and 319.)
+  const bool few = d->R < 64 * (int64_t)d->E;
+  const int pair = d->flags & MM_GROUPED_SINGLE_CTA || (!(d->flags & MM_GROUPED_CTA_PAIRS) && few) ? 1 : 2;
+  const WeightParts parts = weight_parts(*d);
   Maps m;
   Args a{};
   a.offsets = offsets;
@@ -864,17 +1148,21 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
   a.f32 = d->out_type == MM_FP32;
   a.accumulate = accumulate != 0;
   a.chunk = std::min(kMaxN, (a.J + 15) / 16 * 16);
+  a.parts = 1;
+  a.part_rows = (int)std::min<int64_t>(parts.rows, INT32_MAX / 2);
   const void *by_i = d->transposed ? rows : d_out, *by_j = d->transposed ? d_out : rows;
   char* const ws = static_cast<char*>(workspace);
   char *const panel_i = ws + kHeaderBytes, *const panel_j = panel_i + panel_bytes(d->E, a.I);
+  if (parts.slices > 0) {
+    a.slices = reinterpret_cast<float*>(panel_j + panel_bytes(d->E, a.J));
+    a.slice_rows = parts.slices * a.J;
+  }
   bool ok = map2(&m.a, by_i, a.I, d->R, 64) && map2(&m.b[0], by_j, a.J, d->R, 64);
   for (int p = 0; p < 2; ++p)
     ok = ok && map2(&m.a_part[p], by_i, a.I, d->R, 32u >> p) && map2(&m.b_part[p], by_j, a.J, d->R, 32u >> p);
   ok = ok && map2(&m.a_part[2], panel_i, a.I, 16 * (int64_t)d->E, 16) &&
        map2(&m.b_part[2], panel_j, a.J, 16 * (int64_t)d->E, 16);
   if (!ok) return cuda_fail(cudaErrorInvalidValue, "grouped product tensor maps");
-  const int64_t units = (int64_t)d->E * ((a.I + kTile * pair - 1) / (kTile * pair)) *
-                        ((a.J + a.chunk - 1) / a.chunk);
   TailArgs ta{offsets,
               {static_cast<const uint4*>(by_i), static_cast<const uint4*>(by_j)},
               {reinterpret_cast<uint4*>(panel_i), reinterpret_cast<uint4*>(panel_j)},
@@ -884,10 +1172,16 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
   a.next = ta.next;
   const int words = 16 * std::max(ta.words[0], ta.words[1]);  // (a few to a thread)
   MM_TRY(launch_pdl(k_tails, dim3((unsigned)d->E, (unsigned)((words + 2047) / 2048)), dim3(256), 0, st, ta));
+  const int64_t units = (d->E + parts.slices) * div_up(a.I, kTile * pair) * div_up(a.J, a.chunk);
   if (pair == 2)
     MM_TRY((launch<2, true>(m, a, units, d->flags, st)));
   else
     MM_TRY((launch<1, true>(m, a, units, d->flags, st)));
+  if (parts.slices > 0) {
+    const JoinArgs j{offsets, a.slices, d_weight, a.R, a.E, a.I, a.J, 0, a.part_rows, a.f32, a.accumulate};
+    const int64_t blocks = std::min<int64_t>(div_up((int64_t)a.I * a.J / 4, 256), 8 * device_sm_count());
+    MM_TRY(launch_pdl(k_join_weights, dim3((unsigned)std::max<int64_t>(1, blocks)), dim3(256), 0, st, j));
+  }
   return MM_OK;
 }
 

@@ -232,7 +232,8 @@ def _grouped_plan(rows, weight, offsets, out_type, transposed, flags, key, d_out
         raise ValueError("expected d_out[R,N]")
     d = _abi.mm_grouped_desc(R, K, N, E, transposed, out_type, flags)
     at = ctypes.addressof(d)
-    ws = int(_abi._lib().mm_grouped_workspace_size(at))
+    lib = _abi._lib()
+    ws = int((lib.mm_grouped_mm_workspace_size if d_out is None else lib.mm_grouped_weight_grad_workspace_size)(at))
     if ws == 0:
         raise ValueError(f"unsupported sizes R={R} K={K} N={N} E={E}")
     return _grouped_plans.remember(key, (at, ws, d))
@@ -263,13 +264,14 @@ def grouped_mm_forward(rows, weight, offsets, *, out_dtype=None, flags=0):
     transposed, kept = _layout(weight) if weight.dim() == 3 else (False, weight)
     out_dtype = out_dtype or torch.bfloat16
     key = (_sig(rows), _sig(weight), _sig(offsets), out_dtype, transposed, flags)
-    at, _, _ = _grouped_plans.get(key) or _grouped_plan(
+    at, nbytes, _ = _grouped_plans.get(key) or _grouped_plan(
         rows, weight, offsets, _type("out", torch.empty(0, dtype=out_dtype)), transposed, flags, key)
     rows, offsets = _aligned(rows), _index32(offsets, rows.shape[0])
     out = torch.empty((rows.shape[0], weight.shape[2]), dtype=out_dtype, device=rows.device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=rows.device) if nbytes > 256 else None
     _abi.check(_abi._lib().mm_grouped_mm(
-        at, rows.data_ptr(), kept.data_ptr(), offsets.data_ptr(), out.data_ptr(), _stream(rows)),
-        "mm_grouped_mm")
+        at, rows.data_ptr(), kept.data_ptr(), offsets.data_ptr(), out.data_ptr(), _ptr(ws), nbytes,
+        _stream(rows)), "mm_grouped_mm")
     return out
 
 

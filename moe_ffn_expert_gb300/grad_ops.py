@@ -20,8 +20,9 @@ from .block_ops import _elsewhere, _stream
 
 _T = torch.Tensor
 _TYPE = {torch.bfloat16: _abi.MM_BF16, torch.float32: _abi.MM_FP32}
-# the last 8 bytes of mm_tensor_ref: both types
+# the last 8 bytes of mm_tensor_ref: both types, one of them
 _TYPES = {(s, d): _TYPE[s] | _TYPE[d] << 32 for s in _TYPE for d in _TYPE}
+_ONE_TYPE = {s: _TYPES[s, s] for s in _TYPE}
 
 
 def _dense(t):
@@ -55,8 +56,12 @@ def _call(src, dst, clip, device):
     if clip is not None and not _apart(froms, tos):
         raise ValueError("a tensor is given twice")
     types = [t.dtype for t in src]
+    to_types = types if same else [t.dtype for t in dst]
     try:
-        refs[3::4] = map(_TYPES.__getitem__, zip(types, types if same else [t.dtype for t in dst]))
+        if types == to_types:
+            refs[3::4] = map(_ONE_TYPE.__getitem__, types)
+        else:
+            refs[3::4] = map(_TYPES.__getitem__, zip(types, to_types))
     except KeyError:
         raise TypeError("gradients must be bfloat16 or float32") from None
     refs = array("q", refs)
@@ -76,6 +81,9 @@ def _list(tensors):
     return [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
 
 
+_NONE = type(None)
+
+
 def _device(op, first):
     if not first.is_cuda:
         raise ValueError(f"{op} runs on a CUDA device only (no CPU path)")
@@ -85,7 +93,9 @@ def _device(op, first):
 def grad_norm(tensors):
     """The root of the sum of the squares of all elements of all tensors (None entries are left out), a
     float32 scalar. Summed in 64 bits: right for elements of any size."""
-    tensors = [t for t in _list(tensors) if t is not None]
+    tensors = _list(tensors)
+    if _NONE in map(type, tensors):
+        tensors = [t for t in tensors if t is not None]
     if not tensors:
         return torch.zeros((), device="cuda")
     if _elsewhere(tensors[0]):
@@ -107,11 +117,11 @@ def clip_grad_norm(tensors, max_norm, *, eps=1e-6, out=None):
     dst = src if out is None else _list(out)
     if len(dst) != len(src):
         raise ValueError("expected as many tensors in `out`")
-    if any(t is None for t in src):
+    if _NONE in map(type, src):
         pairs = [(s, d) for s, d in zip(src, dst) if s is not None]
         src = [s for s, _ in pairs]
         dst = src if out is None else [d for _, d in pairs]
-    if out is not None and any(t is None for t in dst):
+    if out is not None and _NONE in map(type, dst):
         raise ValueError("`out` lacks a tensor")
     max_norm, eps = float(max_norm), float(eps)
     if not max_norm >= 0.0 or not 0.0 <= eps <= 3e38:

@@ -54,27 +54,28 @@ def test_grouped_host_checks():
     lib = _abi._lib()
 
     def product(d, *p):
-        return lib.mm_grouped_mm(ref(d), *p, None)
+        return lib.mm_grouped_mm(ref(d), *p, 256, 1 << 40, None)
 
     def weight(d, *p, w=256, size=1 << 40):
         return lib.mm_grouped_mm_weight_grad(ref(d), *p, 0, w, size, None)
 
     full = (16, 16, 16, 16)
-    assert lib.mm_grouped_mm(None, *full, None) == BAD
-    assert lib.mm_grouped_workspace_size(None) == 0
+    assert lib.mm_grouped_mm(None, *full, 256, 1 << 40, None) == BAD
+    sizes = (lib.mm_grouped_mm_workspace_size, lib.mm_grouped_weight_grad_workspace_size)
+    assert [f(None) for f in sizes] == [0, 0]
     for call in (product, weight):
         for d in (grouped(R=-1), grouped(K=0), grouped(N=0), grouped(E=0), grouped(out=2), grouped(flags=3),
                   grouped(flags=4)):
-            assert call(d, *full) == BAD and lib.mm_grouped_workspace_size(ref(d)) == 0
+            assert call(d, *full) == BAD and [f(ref(d)) for f in sizes] == [0, 0]
         for d in (grouped(K=60), grouped(N=4), grouped(K=65544), grouped(N=65544), grouped(E=1025),
                   grouped(R=2 ** 31)):
-            assert call(d, *full) == UNSUP and lib.mm_grouped_workspace_size(ref(d)) == 0
+            assert call(d, *full) == UNSUP and [f(ref(d)) for f in sizes] == [0, 0]
         for i in range(4):
             for p in (None, 2 if i == 2 else 8):
                 assert call(grouped(), *full[:i], p, *full[i + 1:]) == BAD
     d = grouped()
-    n = lib.mm_grouped_workspace_size(ref(d))
-    assert n >= 256
+    n = sizes[1](ref(d))
+    assert n >= 256 and sizes[0](ref(d)) >= 256
     assert weight(d, *full, w=None) == WS and weight(d, *full, w=128) == WS and weight(d, *full, size=n - 1) == WS
     assert product(grouped(R=0), None, None, None, None) == _abi.MM_OK
     assert weight(grouped(R=0), None, None, None, 16) == BAD  # zeros have to go somewhere

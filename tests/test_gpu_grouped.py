@@ -299,3 +299,57 @@ def test_a_sum_that_never_arrives_is_nan(form):
     assert got[0, :128, :128].isnan().all()  # (the largest expert's is the first)
     check_forward(x, w, at, flags=form)
     check_weight_grad(x, d, at, w, flags=form)
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+@pytest.mark.parametrize("sizes,K,N", [([1], 7168, 128), ([3], 2056, 264), ([0, 2, 0], 4096, 72), ([2], 4104, 1000)])
+def test_few_tiles_of_long_sums(sizes, K, N, form):
+    """Sums cut over k, with slices that a launch behind adds up."""
+    for transposed in (False, True):
+        for out in (BF, F32):
+            x, w, at, _ = inputs(sizes, K, N, transposed, before=2, behind=3)
+            got = check_forward(x, w, at, out_dtype=out, flags=form)
+            assert (got[:2] == 0).all() and (got[-3:] == 0).all()
+            assert torch.equal(got, expert_ops.grouped_mm_forward(x, w, at, out_dtype=out))
+            at2 = at.clone()
+            at2[-1] = x.shape[0] + 1
+            assert expert_ops.grouped_mm_forward(x, w, at2, out_dtype=out, flags=form).isnan().all()
+    stalled = expert_ops.grouped_mm_forward(x, w, at, flags=form | _abi.MM_GROUPED_TEST_STALL)
+    assert stalled.isnan().any() and torch.equal(torch.where(stalled.isnan(), got.to(BF), stalled), got.to(BF))
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+@pytest.mark.parametrize("sizes,K,N", [([9000], 136, 72), ([0, 5000, 33, 0, 4000, 1, 700], 264, 40), ([3001, 64, 2999], 64, 520),
+                                       ([513] * 5 + [20000], 24, 24), ([1024, 1024, 1025], 72, 64)])
+def test_experts_with_most_rows(sizes, K, N, form):
+    """Sums over rows cut into parts, for the experts that have many."""
+    for transposed in (False, True):
+        x, w, at, d = inputs(sizes, K, N, transposed, before=1, behind=5)
+        for out in (BF, F32):
+            got = check_weight_grad(x, d, at, w, dtype=out, flags=form)
+            assert torch.equal(got, expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=out))
+            shape = (len(sizes), N, K) if transposed else (len(sizes), K, N)
+            into = torch.full(shape, 0.5, dtype=out, device="cuda")
+            into = into.transpose(1, 2) if transposed else into
+            expert_ops.grouped_mm_weight_grad(x, d, at, w, into=into, flags=form)
+            own = expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=F32)
+            assert torch.equal(into, (0.5 + own).to(out))
+        bad = at.clone()
+        bad[-1] = x.shape[0] + 1
+        assert expert_ops.grouped_mm_weight_grad(x, d, bad, w, flags=form).isnan().all()
+    stalled = expert_ops.grouped_mm_weight_grad(x, d, at, w, flags=form | _abi.MM_GROUPED_TEST_STALL)
+    assert stalled.isnan().any()
+
+
+def test_long_sums_of_32_bits_keep_their_bits():
+    """Runs of 512 terms, added up in 32 bits: 32 additions of a run each lose at most 2^-23 of the sum so
+    far, always towards zero, so below 32 / 2 2^-23 = 2e-6 of a result that grows evenly, and the runs'
+    sum next to nothing. All terms of one sign, where this bias shows most."""
+    x, w, at, d = (t.abs() if t.is_floating_point() else t for t in inputs([9000, 70], 7168, 136))
+    for form in (SINGLE, PAIRS):
+        got = expert_ops.grouped_mm_forward(x, w, at, out_dtype=F32, flags=form).double()
+        ref = torch.cat([x[a:b].double() @ w[e].double() for e, (a, b) in spans(at)])
+        assert ((got - ref).norm() / ref.norm()) <= 2e-6
+        got = expert_ops.grouped_mm_weight_grad(x[:, :264], d, at, w[:, :264], dtype=F32, flags=form).double()
+        ref = torch.stack([x[a:b, :264].double().t() @ d[a:b].double() for _, (a, b) in spans(at)])
+        assert ((got - ref).norm() / ref.norm()) <= 2e-6
