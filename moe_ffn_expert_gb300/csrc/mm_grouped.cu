@@ -396,7 +396,8 @@ __device__ __forceinline__ void store_bf16(const Args& a, const uint32_t (&p)[16
   }
 }
 
-template <int PAIR, bool WEIGHTS>
+// WIDE: 32-bit or accumulated results, from runs that are added in registers.
+template <int PAIR, bool WEIGHTS, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grouped(const __grid_constant__ Maps m, const Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kFirstStore) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if constexpr (WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 0) {
       // ------------------------------------------------ loads
       Ring ring(empty_bar(0), 1, a.stages, limit);
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit t;
         if (!take(q, t) || t.n < 0) break;
         const int blocks = uniform(t.blocks()), n16 = uniform(t.n16());
-        const int run = uniform(t.run(a.f32 || a.accumulate || t.slice));
+        const int run = uniform(t.run(WIDE));
         const int last = uniform(t.k) - (blocks - 1) * 64;  // terms in the last block
         const uint32_t idesc = idesc_bf16_f32(kTile * PAIR, n16, a_mn, b_mn);
         uint32_t buf = 0, d = 0;
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    if constexpr (WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     // ------------------------------------------------ stores
     const int set = (warp - kFirstStore) >> 2, quarter = warp & 3;  // (of the accumulator's lanes)
     const bool to_slices = !WEIGHTS && a.parts > 1;
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && t.k == 0 && a.accumulate) continue;  // adding zero changes nothing
       const int i = t.i0 + rank * kTile + quarter * 32;
       const int blocks = t.blocks();
-      if (a.f32 || a.accumulate || t.slice) {
+      if constexpr (WIDE) {
         float sum[kMaxN / 64][32];
 #pragma unroll
         for (int g = 0; g < kMaxN / 64; ++g)
@@ -724,35 +725,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           release();
         }
         if (ok) {
+          float* const to = t.slice ? a.slices : static_cast<float*>(a.out);
+          const bool add = a.accumulate && !t.slice;
 #pragma unroll
           for (int g = 0; g < kMaxN / 64; ++g) {
             const int c = set * 32 + 64 * g;
             if (c >= t.n) continue;
-            if (t.slice) store_fp32<false>(a, a.slices, sum[g], (int64_t)t.row + c, i + lane, t.n - c);
-            else if (!a.accumulate) store_fp32<false>(a, static_cast<float*>(a.out), sum[g], (int64_t)t.row + c, i + lane, t.n - c);
-            else if (a.f32) store_fp32<true>(a, static_cast<float*>(a.out), sum[g], (int64_t)t.row + c, i + lane, t.n - c);
+            if (!add) store_fp32<false>(a, to, sum[g], (int64_t)t.row + c, i + lane, t.n - c);
+            else if (a.f32) store_fp32<true>(a, to, sum[g], (int64_t)t.row + c, i + lane, t.n - c);
             else add_bf16(a, sum[g], (int64_t)t.row + c, i + lane, t.n - c, lane);
           }
         }
       } else {
-        uint32_t p[kMaxN / 64][16];
         if (ok && blocks > 0) ok = arrived();
         if (ok) {
+          for (int c = set * 32; c < t.n; c += 64) {
+            if (t.slice) {
+              uint32_t r[32];
+              tmem_ld_32x32(lanes + (acc & 1u) * kMaxN + c, r);
+              tmem_ld_wait();
+              float v[32];
 #pragma unroll
-          for (int g = 0; g < kMaxN / 64; ++g) {
-            if (blocks == 0) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) p[g][j] = 0;
-            } else if (set * 32 + 64 * g < t.n) {
-              load_bf16(lanes + (acc & 1u) * kMaxN + set * 32 + 64 * g, p[g]);
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+              store_fp32<false>(a, a.slices, v, (int64_t)t.row + c, i + lane, t.n - c);
+            } else {
+              uint32_t p[16] = {};
+              if (blocks > 0) load_bf16(lanes + (acc & 1u) * kMaxN + c, p);
+              store_bf16(a, p, stage, (int64_t)t.row + c, i, t.n - c, lane);
             }
           }
           if (blocks > 0) release();
-#pragma unroll
-          for (int g = 0; g < kMaxN / 64; ++g) {
-            const int c = set * 32 + 64 * g;
-            if (c < t.n) store_bf16(a, p[g], stage, (int64_t)t.row + c, i, t.n - c, lane);
-          }
         }
       }
       if (!ok) {  // the tiles that this CTA has or would have had are nobody's: NaN, if not others' results
@@ -976,8 +978,8 @@ bool map2(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, uint32_t
 }
 
 // units: tiles, at most.
-template <int PAIR, bool WEIGHTS>
-cudaError_t launch(const Maps& m, Args a, int64_t units, uint32_t flags, cudaStream_t st) {
+template <int PAIR, bool WEIGHTS, bool WIDE>
+cudaError_t launch_form(const Maps& m, Args a, int64_t units, uint32_t flags, cudaStream_t st) {
   a.stall = (flags & MM_GROUPED_TEST_STALL) != 0;
   a.wait_ns = a.stall ? kTestWaitNs : kWaitNs;
   a.stage_bytes = kABytes + (WEIGHTS ? (a.chunk / PAIR + 63) / 64 * kBlock : a.chunk / PAIR * 128u);
@@ -991,14 +993,14 @@ cudaError_t launch(const Maps& m, Args a, int64_t units, uint32_t flags, cudaStr
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_grouped<PAIR, WEIGHTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_grouped<PAIR, WEIGHTS, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kMostSmem - 1024));
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   int fit = std::max(1, device_sm_count());
   if constexpr (PAIR == 1) {
-    return launch_pdl(k_grouped<PAIR, WEIGHTS>, dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(fit, units))),
+    return launch_pdl(k_grouped<PAIR, WEIGHTS, WIDE>, dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(fit, units))),
                       dim3(kThreads), smem, st, m, a);
   } else {
     cudaLaunchConfig_t cfg = {};
@@ -1019,7 +1021,7 @@ cudaError_t launch(const Maps& m, Args a, int64_t units, uint32_t flags, cudaStr
     fit = most_clusters[dev].load(std::memory_order_relaxed);
     if (fit == 0) {
       cfg.dynamicSmemBytes = kMostSmem - 1024;
-      e = cudaOccupancyMaxActiveClusters(&fit, k_grouped<PAIR, WEIGHTS>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&fit, k_grouped<PAIR, WEIGHTS, WIDE>, &cfg);
       if (e != cudaSuccess) return e;
       if (fit < 1) return cudaErrorInvalidConfiguration;
       most_clusters[dev].store(fit, std::memory_order_relaxed);
@@ -1027,8 +1029,18 @@ cudaError_t launch(const Maps& m, Args a, int64_t units, uint32_t flags, cudaStr
     }
     cfg.gridDim = dim3((unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(fit, units))));
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_grouped<PAIR, WEIGHTS>, m, a);
+    return cudaLaunchKernelEx(&cfg, k_grouped<PAIR, WEIGHTS, WIDE>, m, a);
   }
+}
+
+template <bool WEIGHTS>
+cudaError_t launch(int pair, const Maps& m, const Args& a, int64_t units, uint32_t flags, cudaStream_t st) {
+  const bool wide = a.f32 || a.accumulate;
+  if (pair == 2)
+    return wide ? launch_form<2, WEIGHTS, true>(m, a, units, flags, st)
+                : launch_form<2, WEIGHTS, false>(m, a, units, flags, st);
+  return wide ? launch_form<1, WEIGHTS, true>(m, a, units, flags, st)
+              : launch_form<1, WEIGHTS, false>(m, a, units, flags, st);
 }
 
 }  // namespace
@@ -1100,10 +1112,7 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   if (!ok) return cuda_fail(cudaErrorInvalidValue, "grouped product tensor maps");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t units = chunks * div_up(d->N, kTile * pair) * a.parts;
-  if (pair == 2)
-    MM_TRY((launch<2, false>(m, a, units, d->flags, st)));
-  else
-    MM_TRY((launch<1, false>(m, a, units, d->flags, st)));
+  MM_TRY(launch<false>(pair, m, a, units, d->flags, st));
   if (a.parts > 1) {
     const JoinArgs j{offsets, a.slices, out, a.R, a.E, a.I, 0, a.parts, 0, a.f32, 0};
     const int64_t blocks = div_up((int64_t)a.R * a.I / 4, 256);
@@ -1173,10 +1182,7 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
   const int words = 16 * std::max(ta.words[0], ta.words[1]);  // (a few to a thread)
   MM_TRY(launch_pdl(k_tails, dim3((unsigned)d->E, (unsigned)((words + 2047) / 2048)), dim3(256), 0, st, ta));
   const int64_t units = (d->E + parts.slices) * div_up(a.I, kTile * pair) * div_up(a.J, a.chunk);
-  if (pair == 2)
-    MM_TRY((launch<2, true>(m, a, units, d->flags, st)));
-  else
-    MM_TRY((launch<1, true>(m, a, units, d->flags, st)));
+  MM_TRY(launch<true>(pair, m, a, units, d->flags, st));
   if (parts.slices > 0) {
     const JoinArgs j{offsets, a.slices, d_weight, a.R, a.E, a.I, a.J, 0, a.part_rows, a.f32, a.accumulate};
     const int64_t blocks = std::min<int64_t>(div_up((int64_t)a.I * a.J / 4, 256), 8 * device_sm_count());
