@@ -58,7 +58,7 @@ constexpr uint32_t kABytes = kTile * 64 * 2;
 constexpr uint32_t kBlock = 64 * 64 * 2;  // 64 elements of a MN-major operand over 64 k
 constexpr uint32_t kBarBytes = 512;
 constexpr uint32_t kTableBytes = 2 * 4 * (kMaxE + 1) + 8 + 2 * kMaxE;
-constexpr uint32_t kOutBytes = 32 * 64;   // a storing warp's 32 rows of 32 columns
+constexpr uint32_t kOutBytes = 32 * 64;   // a storing warp's share of its set's 32 rows of 128 columns
 constexpr uint32_t kMostSmem = 227 * 1024;
 constexpr uint64_t kWaitNs = 2000000000ull, kTestWaitNs = 50000000ull;
 
@@ -105,43 +105,24 @@ struct __align__(16) Unit {
   }
 };
 
-// mbar_wait for what the other CTA's threads wrote before they arrived.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-      uint32_t ok;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(bar), "r"(parity)
-          : "memory");
-      if (ok) return true;
-    }
-    if (globaltimer_ns() - t0 > limit_ns) return false;
-  }
-}
-
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
-
 // Waits by all lanes of a warp, with one answer for them.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns));
 }
-__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity, limit_ns));
-}
 
-__device__ __forceinline__ void st_shared_cluster(uint32_t cluster_addr, int4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y),
-               "r"(v.z), "r"(v.w)
-               : "memory");
+// 32 bytes to the other CTA's shared memory, where their arrival completes a phase of the barrier. Without a
+// release, which would wait for this thread's accesses to global memory.
+__device__ __forceinline__ void send_cluster(uint32_t to, uint32_t bar, int4 lo, int4 hi) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 32;" ::"r"(bar) : "memory");
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+      "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(bar)
+      : "memory");
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+          to + 16),
+      "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w), "r"(bar)
+      : "memory");
 }
 
 // A value that all lanes share, in the form the compiler knows to be shared: what an issue of a copy or a
@@ -367,32 +348,49 @@ __device__ __forceinline__ void load_bf16(uint32_t taddr, uint32_t (&p)[16]) {
     }
 }
 
-// Those to rows row .. of the output by way of shared memory (`stage`, this warp's 32 rows of 64 bytes):
-// 8 x 8 blocks are stored transposed, and rows leave in words of 16 bytes; a third of the instructions
-// that an exchange between lanes takes. A row's 16-byte words are turned by half its number, so that
-// eight rows' words of one block lie in different banks. i: the warp's first column.
-__device__ __forceinline__ void store_bf16(const Args& a, const uint32_t (&p)[16], uint32_t stage, int64_t row,
-                                           int i, int n, int lane) {
-  __syncwarp();  // the lanes have read what was here
-  const uint32_t to = stage + (lane & 7) * 64 + (((lane >> 3) ^ (lane >> 1 & 3)) << 4);
+// Whether all four warps of a set say so.
+__device__ __forceinline__ bool agreed(bool ok, int set) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "r"(1 + set)
+      : "memory");
+  return all != 0;
+}
+
+// Those of a set's four warps (the CTA's 128 columns, one of `n` rows row .. at a time) to the output by way
+// of shared memory (`stage`, 32 rows of 256 bytes): 8 x 8 blocks are stored transposed, and rows leave in
+// words of 16 bytes, 256 bytes of a row at a time; a third of the instructions that an exchange between
+// lanes takes, and whole lines (rows of 64 bytes, each warp its own, reached 4.2 TB/s of writes where rows
+// of 128 reach 5.7). A row's words are turned by its number, so that eight rows' words of one block lie in
+// different banks. i: the CTA's first column.
+__device__ __forceinline__ void store_bf16(const Args& a, const uint32_t (&p)[16], uint32_t stage, int set,
+                                           int quarter, int64_t row, int i, int n, int lane) {
+  const auto sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory"); };
+  sync();  // all have read what was here
+  const int jw = lane & 7;
+  const uint32_t to = stage + jw * 256 + (((quarter * 4 + (lane >> 3)) ^ jw) << 4);
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to + c * 512),
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to + c * 2048),
                  "r"(p[4 * c]), "r"(p[4 * c + 1]), "r"(p[4 * c + 2]), "r"(p[4 * c + 3])
                  : "memory");
-  __syncwarp();
-  const int j = lane >> 2, w = lane & 3;
-  const uint32_t from = stage + j * 64 + ((w ^ (j >> 1 & 3)) << 4);
+  sync();
+  const int j = quarter * 8 + (lane >> 4), w = lane & 15;  // this warp's 8 rows, two at a time
   __nv_bfloat16* at = static_cast<__nv_bfloat16*>(a.out) + (row + j) * a.I + i + 8 * w;
   const bool there = i + 8 * w < a.I;
 #pragma unroll
-  for (int c = 0; c < 4; ++c, at += 8 * (int64_t)a.I) {
+  for (int c = 0; c < 4; ++c, at += 2 * (int64_t)a.I) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(from + c * 512)
+                 : "r"(stage + (j + 2 * c) * 256 + ((w ^ ((j + 2 * c) & 7)) << 4))
                  : "memory");
-    if (there && j + 8 * c < n) *reinterpret_cast<uint4*>(at) = v;
+    if (there && j + 2 * c < n) *reinterpret_cast<uint4*>(at) = v;
   }
 }
 
@@ -465,8 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a release, which would wait for a storing warp's rows to reach memory.
   auto take = [&](int q, Unit& t) {
     const uint32_t slot = q % kQueue, bar = told_bar(slot), phase = q / kQueue & 1u;
-    if (!(PAIR == 2 && rank == 1 ? warp_wait_cluster(bar, phase, limit) : warp_wait(bar, phase, limit)))
-      return false;
+    if (!warp_wait(bar, phase, limit)) return false;
     const int word = static_cast<volatile const int*>(&queue[slot].e)[lane & 7];
     t.e = __shfl_sync(0xFFFFFFFFu, word, 0);
     t.i0 = __shfl_sync(0xFFFFFFFFu, word, 1);
@@ -629,11 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 2) {
       // ------------------------------------------------ deals out tiles
-      // Two claims are on their way at a time.
-      int u = mine, ahead = mine + step;
+      // A claim is made three tiles ahead, so that its answer is there when it is looked at. (Two ahead a
+      // tile took 1.1 us at least, and with a release to the other CTA 2.7: 512 rows of 128 experts,
+      // 768 x 2048, 110 us in pairs, 88 now.)
+      int u = mine, ahead = mine + step, claimed = mine + 2 * step;
       for (int q = 0; rank == 0; ++q) {
-        int next = ahead + step;
-        if (a.next != nullptr && lane == 0) next = 2 * step + atomicAdd(a.next, 1);
+        int next = claimed + step;
+        if (a.next != nullptr && lane == 0) next = 3 * step + atomicAdd(a.next, 1);
         Unit t{};
         if (u < units) t = unit_at<WEIGHTS, PAIR>(a, start, first_chunk, order, u, i_tiles, j_tiles);
         else t.n = -1;
@@ -642,17 +641,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           queue[slot] = t;
           mbar_arrive(told_bar(slot));
-          if constexpr (PAIR == 2) {
-            const uint32_t to = mapa_shared(smem_u32(&queue[slot]), 1);
-            st_shared_cluster(to, make_int4(t.e, t.i0, t.j0, t.n));
-            st_shared_cluster(to + 16, make_int4(t.k0, t.k, t.row, t.slice));
-            mbar_arrive_remote(mapa_shared(told_bar(slot), 1));
-          }
+          if constexpr (PAIR == 2)
+            send_cluster(mapa_shared(smem_u32(&queue[slot]), 1), mapa_shared(told_bar(slot), 1),
+                         make_int4(t.e, t.i0, t.j0, t.n), make_int4(t.k0, t.k, t.row, t.slice));
         }
         __syncwarp();
         if (t.n < 0) break;
         u = ahead;
-        ahead = __shfl_sync(0xFFFFFFFFu, next, 0);
+        ahead = __shfl_sync(0xFFFFFFFFu, claimed, 0);
+        claimed = next;
       }
     }
   } else {
@@ -674,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fill(out, start[0] * row_words, 0, thread, threads);
       fill(out + start[a.E] * row_words, (a.R - start[a.E]) * row_words, 0, thread, threads);
     }
-    const uint32_t stage = out_stage + (warp - kFirstStore) * kOutBytes;
+    const uint32_t stage = out_stage + set * 4 * kOutBytes;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t acc = 0;
     // The accumulator of the next run, or false; and its hand-back, when it is in registers.
@@ -693,8 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++acc;
     };
     for (int q = 0;; ++q) {
-      Unit t;
+      Unit t{};
       bool ok = take(q, t);
+      if (!WIDE) ok = agreed(ok, set);
       if (ok && t.n < 0) break;
       if (ok && t.k == 0 && a.accumulate) continue;  // adding zero changes nothing
       const int i = t.i0 + rank * kTile + quarter * 32;
@@ -738,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         if (ok && blocks > 0) ok = arrived();
+        ok = agreed(ok, set);  // (the warps of a set meet at barriers)
         if (ok) {
           for (int c = set * 32; c < t.n; c += 64) {
             if (t.slice) {
@@ -751,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               uint32_t p[16] = {};
               if (blocks > 0) load_bf16(lanes + (acc & 1u) * kMaxN + c, p);
-              store_bf16(a, p, stage, (int64_t)t.row + c, i, t.n - c, lane);
+              store_bf16(a, p, stage, set, quarter, (int64_t)t.row + c, t.i0 + rank * kTile, t.n - c, lane);
             }
           }
           if (blocks > 0) release();
@@ -1140,11 +1139,7 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
       MM_TRY(cudaMemsetAsync(d_weight, 0, (size_t)d->E * d->K * d->N * (d->out_type == MM_FP32 ? 4 : 2), st));
     return MM_OK;
   }
-  // Pairs, unless the experts have few rows: a tile is then little more than its result's way out, which
-  // the two CTAs of a pair wait for together. (us, one CTA a tile and pairs: 512 rows of 128 experts,
-  // 768 x 2048, 88 and 105; 65536 of 128, 2048 x 1536, 359 and 319.)
-  const bool few = d->R < 64 * (int64_t)d->E;
-  const int pair = d->flags & MM_GROUPED_SINGLE_CTA || (!(d->flags & MM_GROUPED_CTA_PAIRS) && few) ? 1 : 2;
+  const int pair = d->flags & MM_GROUPED_SINGLE_CTA ? 1 : 2;
   const WeightParts parts = weight_parts(*d);
   Maps m;
   Args a{};
