@@ -4,7 +4,7 @@
 // Both are one shape of product: out[j][i] = sum_k A[i][k] B[j][k] with i contiguous in the output.
 //   rows:    i = output column, j = row of the expert; A = the expert's matrix, B = its rows.
 //   weights: i = the matrix's contiguous dimension, j = the other; k = the expert's rows; A and B are
-//            d_out and rows (or the other way round, for transposed matrices).
+//            d_out and rows (the other way round for transposed matrices).
 // The matrix is the M operand (128 columns a CTA) and the rows are N: a tile's N is the number of rows
 // of its chunk, rounded up to 16, so that ragged experts cost what they have and not a multiple of
 // 128, and one row costs 16. An expert of more than `chunk` rows is cut into equal chunks. Neighbours'
@@ -930,7 +930,7 @@ mm_status check_desc(const mm_grouped_desc* d) {
   const uint32_t forms = d->flags & ~MM_GROUPED_TEST_STALL;
   if (forms > 2) return MM_ERR_INVALID_ARG;  // unknown flags, or both forms
   if (d->K % 8 || d->N % 8 || d->K > 65536 || d->N > 65536 || d->E > kMaxE ||
-      d->R >= (int64_t)1 << 31)
+      d->R >= (int64_t)1 << 30)
     return MM_ERR_UNSUPPORTED;
   return MM_OK;
 }
@@ -1153,7 +1153,7 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
   a.accumulate = accumulate != 0;
   a.chunk = std::min(kMaxN, (a.J + 15) / 16 * 16);
   a.parts = 1;
-  a.part_rows = (int)std::min<int64_t>(parts.rows, INT32_MAX / 2);
+  a.part_rows = (int)parts.rows;
   const void *by_i = d->transposed ? rows : d_out, *by_j = d->transposed ? d_out : rows;
   char* const ws = static_cast<char*>(workspace);
   char *const panel_i = ws + kHeaderBytes, *const panel_j = panel_i + panel_bytes(d->E, a.I);

@@ -68,7 +68,7 @@ def test_grouped_host_checks():
                   grouped(flags=4)):
             assert call(d, *full) == BAD and [f(ref(d)) for f in sizes] == [0, 0]
         for d in (grouped(K=60), grouped(N=4), grouped(K=65544), grouped(N=65544), grouped(E=1025),
-                  grouped(R=2 ** 31)):
+                  grouped(R=2 ** 30)):
             assert call(d, *full) == UNSUP and [f(ref(d)) for f in sizes] == [0, 0]
         for i in range(4):
             for p in (None, 2 if i == 2 else 8):
