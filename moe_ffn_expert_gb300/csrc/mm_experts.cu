@@ -9,6 +9,7 @@
 // Dispatch and combine move rows: a block has a token's row and its K slots' rows, so that each row is
 // read and written once.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/mm_experts.h"
 #include "mm_kernels.h"
@@ -99,17 +100,23 @@ __global__ void __launch_bounds__(32 * kTableWarps) k_table_rank(TableArgs a) {
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) b[r] = bucket_of(a, s0 + 32 * r);
   __syncthreads();
-  if (FEW && a.blocks > 1) {  // a warp adds up every kTableWarps-th block's counts
-    for (int e = lane; e < buckets; e += 32) {
-      int all = 0, mine = 0;
-#pragma unroll 8
-      for (int k = warp; k < a.blocks; k += kTableWarps) {
-        const int c = a.counts[k * buckets + e];
-        all += c;
-        mine += k < (int)blockIdx.x ? c : 0;
+  if (FEW && a.blocks > 1) {
+    // all blocks' counts, 32 buckets of one block at a time, eight loads of a warp in flight
+    const int groups = (buckets + 31) / 32, loads = a.blocks * groups;
+    for (int i0 = warp; i0 < loads; i0 += 8 * kTableWarps) {
+      int c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kTableWarps, k = i / groups, e = (i - k * groups) * 32 + lane;
+        c[u] = i < loads && e < buckets ? a.counts[k * buckets + e] : 0;
       }
-      if (all != 0) atomicAdd(&base[e], all);
-      if (mine != 0) atomicAdd(&before[e], mine);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kTableWarps, k = i / groups, e = (i - k * groups) * 32 + lane;
+        if (c[u] == 0) continue;
+        atomicAdd(&base[e], c[u]);
+        if (k < (int)blockIdx.x) atomicAdd(&before[e], c[u]);
+      }
     }
   }
 #pragma unroll
@@ -213,15 +220,49 @@ __global__ void __launch_bounds__(256) k_dispatch(RowArgs a) {
   zero_rows_behind(a, rows);
 }
 
-// Words of W columns that a thread has under way at a time: single columns (rows off 16-byte boundaries)
-// need more of them (1001 x 6 fp32 rows of 2047 backward: 38 us one at a time).
+// Words of W columns of one row that a thread has under way at a time: single columns (rows off 16-byte
+// boundaries) need more of them. (1001 x 6 rows of 2047 columns, us, one, two and four at a time: fp32
+// backward 38, 20 and 24, bf16 forward 19, 14 and 11.)
 template <int W>
 constexpr int kAtOnce = W == 1 ? 4 : 1;
+template <int W>
+constexpr int kAtOnceBwd = W == 1 ? 2 : 1;
+
+// W columns as they lie in memory: half the registers of bf16 numbers that wait for their turn.
+template <typename T, int W>
+struct Word {
+  static_assert(W == 8, "widths 8 and 1");
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void widen(float (&v)[W]) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2) v[2 * k] = bf16_lo(u[k]), v[2 * k + 1] = bf16_hi(u[k]);
+        else v[4 * i + k] = __uint_as_float(u[k]);
+      }
+    }
+  }
+};
+template <typename T>
+struct Word<T, 1> {
+  T w{};
+  __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void widen(float (&v)[1]) const {
+    if constexpr (sizeof(T) == 2) v[0] = __bfloat162float(w);
+    else v[0] = w;
+  }
+};
 
 // words: H / W.
 template <typename T, int W>
 __global__ void __launch_bounds__(256) k_combine(RowArgs a) {
-  constexpr int U = kAtOnce<W>;
+  constexpr int U = kAtOnce<W>, N = 4;  // slots whose loads are in flight
   pdl_wait();
   pdl_launch_dependents();
   const T* rows = static_cast<const T*>(a.rows);
@@ -229,31 +270,32 @@ __global__ void __launch_bounds__(256) k_combine(RowArgs a) {
   const int32_t* row = a.row_of_slot + t * a.K;
   for (int w0 = threadIdx.x; w0 < a.words; w0 += blockDim.x * U) {
     float y[U][W] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 4) {  // four slots' loads in flight
-      float v[4][U][W];
-      float g[4];
+    for (int k0 = 0; k0 < a.K; k0 += N) {
+      Word<T, W> v[N][U];
+      bool there[N];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < N; ++k) {
         const int64_t r = k0 + k < a.K ? row[k0 + k] : -1;
-        const bool there = r >= 0 && r < a.S;
-        g[k] = there ? (a.weights ? a.weights[t * a.K + k0 + k] : 1.f) : 0.f;
+        there[k] = r >= 0 && r < a.S;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int w = w0 + u * (int)blockDim.x;
-          if (there && w < a.words) {
-            load_vec<W>(rows + r * a.H + (int64_t)w * W, v[k][u]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[k][u][i] = 0.f;
-          }
+          v[k][u] = Word<T, W>{};
+          if (there[k] && w < a.words) v[k][u].load(rows + r * a.H + (int64_t)w * W);
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < N; ++k) {
+        if (!there[k]) continue;
+        const float g = a.weights ? a.weights[t * a.K + k0 + k] : 1.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+          float x[W];
+          v[k][u].widen(x);
 #pragma unroll
-          for (int i = 0; i < W; ++i) y[u][i] = fmaf(g[k], v[k][u][i], y[u][i]);
+          for (int i = 0; i < W; ++i) y[u][i] = fmaf(g, x[i], y[u][i]);
+        }
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -263,72 +305,78 @@ __global__ void __launch_bounds__(256) k_combine(RowArgs a) {
   }
 }
 
-template <typename T, int W>
-__global__ void __launch_bounds__(256) k_combine_bwd(RowArgs a) {
-  constexpr int U = kAtOnce<W>;
-  __shared__ float part[8][8];
+// S slots at a time, of which N loads are in flight (fp32 words: what 32 registers hold). Tokens of one or
+// two slots have a kernel of fewer registers, as only more blocks bring more loads there (16384 tokens of
+// one slot, 1024 columns: 55 us with S = 8).
+template <typename T, int W, int S>
+__global__ void __launch_bounds__(256, S == 8 ? 3 : 1) k_combine_bwd(RowArgs a) {
+  constexpr int U = kAtOnceBwd<W>, N = S == 8 && W == 8 && sizeof(T) == 4 ? 4 : S;
+  __shared__ float part[8][S];
   pdl_wait();
   pdl_launch_dependents();
   const T* rows = static_cast<const T*>(a.rows);
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int k0 = 0; k0 < a.K; k0 += 8) {
-    float dot[8] = {};
-    int64_t row[8];
-    float g[8];
+  for (int k0 = 0; k0 < a.K; k0 += S) {
+    float dot[S] = {};
+    int row[S];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < S; ++k) {
       row[k] = k0 + k < a.K ? a.row_of_slot[t * a.K + k0 + k] : -1;
       if (row[k] >= a.S) row[k] = -1;
-      g[k] = row[k] >= 0 && a.weights ? a.weights[t * a.K + k0 + k] : 1.f;
     }
     for (int w0 = threadIdx.x; w0 < a.words; w0 += blockDim.x * U) {
-      float d[U][W];
+      Word<T, W> d[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int w = w0 + u * (int)blockDim.x;
-#pragma unroll
-        for (int i = 0; i < W; ++i) d[u][i] = 0.f;
-        if (w < a.words) load_vec<W>(static_cast<const T*>(a.x) + t * a.H + (int64_t)w * W, d[u]);
+        d[u] = Word<T, W>{};
+        if (w < a.words) d[u].load(static_cast<const T*>(a.x) + t * a.H + (int64_t)w * W);
       }
 #pragma unroll
-      for (int k4 = 0; k4 < 8; k4 += 4) {  // four slots' loads in flight
-        float v[4][U][W];
+      for (int kn = 0; kn < S; kn += N) {
+        Word<T, W> v[N][U];
         if (a.d_weights) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < N; ++k) {
+            const int r = row[kn + k];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int w = w0 + u * (int)blockDim.x;
-#pragma unroll
-              for (int i = 0; i < W; ++i) v[k][u][i] = 0.f;
-              if (row[k4 + k] >= 0 && w < a.words)
-                load_vec<W>(rows + row[k4 + k] * a.H + (int64_t)w * W, v[k][u]);
+              v[k][u] = Word<T, W>{};
+              if (r >= 0 && w < a.words) v[k][u].load(rows + (int64_t)r * a.H + w * W);
             }
+          }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (row[k4 + k] < 0) continue;
+        for (int k = 0; k < N; ++k) {
+          const int64_t r = row[kn + k];
+          if (r < 0) continue;
+          const float g = a.weights ? a.weights[t * a.K + k0 + kn + k] : 1.f;
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const int w = w0 + u * (int)blockDim.x;
             if (w >= a.words) continue;
-            float o[W];
+            float x[W], y[W];
+            d[u].widen(x);
+            if (a.d_weights) {
+              v[k][u].widen(y);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-              if (a.d_weights) dot[k4 + k] = fmaf(d[u][i], v[k][u][i], dot[k4 + k]);
-              o[i] = g[k4 + k] * d[u][i];
+              for (int i = 0; i < W; ++i) dot[kn + k] = fmaf(x[i], y[i], dot[kn + k]);
             }
-            store_vec<W>(static_cast<T*>(a.out_rows) + row[k4 + k] * a.H + (int64_t)w * W, o);
+#pragma unroll
+            for (int i = 0; i < W; ++i) y[i] = g * x[i];
+            store_vec<W>(static_cast<T*>(a.out_rows) + r * a.H + w * W, y);
           }
         }
       }
     }
     if (a.d_weights) {
-      const float sum = warp_sum_many<8>(dot, lane);
-      if ((lane & 3) == 0) part[warp][lane >> 2] = sum;
+      constexpr int LANES = 32 / S;
+      const float sum = warp_sum_many<S>(dot, lane);
+      if (lane % LANES == 0) part[warp][lane / LANES] = sum;
       __syncthreads();
-      if (threadIdx.x < 8 && k0 + (int)threadIdx.x < a.K) {
+      if (threadIdx.x < S && k0 + (int)threadIdx.x < a.K) {
         float s = 0.f;
         for (int w = 0; w < (int)blockDim.x / 32; ++w) s += part[w][threadIdx.x];
         a.d_weights[t * a.K + k0 + threadIdx.x] = s;
@@ -506,10 +554,17 @@ mm_status mm_expert_combine_backward(const mm_expert_desc* d, const void* dy, co
   auto go = [&](auto* kernel) {
     return launch_pdl(kernel, dim3((unsigned)d->T), dim3(threads_for(a.words)), 0, st, a);
   };
+  auto by_slots = [&](auto type, auto width) {
+    using T = decltype(type);
+    constexpr int W = decltype(width)::value;
+    return d->K <= 2 ? go(k_combine_bwd<T, W, 2>) : go(k_combine_bwd<T, W, 8>);
+  };
+  using Eight = std::integral_constant<int, 8>;
+  using One = std::integral_constant<int, 1>;
   if (d->type == MM_BF16)
-    MM_TRY(wide ? go(k_combine_bwd<__nv_bfloat16, 8>) : go(k_combine_bwd<__nv_bfloat16, 1>));
+    MM_TRY(wide ? by_slots(__nv_bfloat16{}, Eight{}) : by_slots(__nv_bfloat16{}, One{}));
   else
-    MM_TRY(wide ? go(k_combine_bwd<float, 8>) : go(k_combine_bwd<float, 1>));
+    MM_TRY(wide ? by_slots(float{}, Eight{}) : by_slots(float{}, One{}));
   return MM_OK;
 }
 
