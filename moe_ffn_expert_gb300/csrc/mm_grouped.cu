@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_fence_init();
     tma_prefetch_desc(&m.a);
-    tma_prefetch_desc(&m.b[0]);
+    if (WEIGHTS || a.chunk / PAIR > 64) tma_prefetch_desc(&m.b[0]);
   }
   if (warp == 1) {
     if constexpr (PAIR == 2) {
@@ -936,7 +936,8 @@ mm_status check_desc(const mm_grouped_desc* d) {
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Parts of the sums of mm_grouped_mm: as many as bring a launch of few tiles to a tile of one CTA per SM,
-// of 4 blocks at least. (1 row by a matrix 7168 x 2048, 16 tiles: 31 us whole.)
+// of 4 blocks at least. (1 row by a matrix 7168 x 2048, 16 tiles of 112 blocks: 11 us, 31 whole, 0.25 us a
+// block. Sums below 32 blocks do not gain the 3 us that the joining launch takes, and 5 of the host.)
 struct RowParts {
   int parts, blocks;  // blocks of a part
 };
@@ -944,7 +945,7 @@ RowParts row_parts(const mm_grouped_desc& d) {
   const int64_t blocks = div_up(d.K, 64);
   const int64_t tiles = (d.R / kMaxN + std::min<int64_t>(d.E, d.R)) * div_up(d.N, kTile);  // at most
   const int64_t want = std::min<int64_t>(device_sm_count() / std::max<int64_t>(1, tiles), blocks / 4);
-  if (want < 2) return {1, (int)blocks};
+  if (want < 2 || blocks < 32) return {1, (int)blocks};
   const int64_t part = div_up(blocks, want);
   return {(int)div_up(blocks, part), (int)part};
 }
@@ -1083,7 +1084,7 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   const int64_t chunks = d->R / kMaxN + std::min<int64_t>(d->E, d->R);  // at most
   const bool few = chunks * div_up(d->N, kTile) <= device_sm_count();
   const int pair = d->flags & MM_GROUPED_CTA_PAIRS || (!(d->flags & MM_GROUPED_SINGLE_CTA) && !few) ? 2 : 1;
-  Maps m;
+  Maps m{};
   Args a{};
   a.offsets = offsets;
   a.out = out;
@@ -1105,7 +1106,8 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   const uint64_t strides[2] = {(uint64_t)inner * 2, (uint64_t)inner * outer * 2};
   const uint32_t box[3] = {64, d->transposed ? 128u : 64u, 1};
   bool ok = make_map(&m.a, weight, 3, dims, strides, box);
-  for (int p = 0; p < 5; ++p) ok = ok && map2(&m.b[p], rows, d->K, d->R, 128u >> p);
+  for (int p = 0; p < 5; ++p)  // (larger boxes than a chunk's are not used)
+    if (128u >> p <= box_rows(a.chunk / pair)) ok = ok && map2(&m.b[p], rows, d->K, d->R, 128u >> p);
   if (!ok) return cuda_fail(cudaErrorInvalidValue, "grouped product tensor maps");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t units = chunks * div_up(d->N, kTile * pair) * a.parts;

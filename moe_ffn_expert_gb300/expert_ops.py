@@ -210,15 +210,14 @@ def _index32(t, most):
     return _contiguous(t)
 
 
-def _layout(weight):
-    """(whether [E,K,N] is kept as [E,N,K], the contiguous and aligned tensor)."""
-    if not weight.is_contiguous() and weight.transpose(1, 2).is_contiguous():
-        return True, _aligned(weight.transpose(1, 2))
-    return False, _aligned(weight)
+def _transposed(weight):
+    """Whether [E,K,N] is kept as contiguous [E,N,K]."""
+    return not weight.is_contiguous() and weight.dim() == 3 and weight.transpose(1, 2).is_contiguous()
 
 
 def _grouped_plan(rows, weight, offsets, out_type, transposed, flags, key, d_out=None):
-    """Checks the inputs; (address of the descriptor, workspace bytes, descriptor)."""
+    """Checks the inputs; (address of the descriptor, workspace bytes, zeros that bring K and N to
+    multiples of 8, descriptor). With such zeros there is no descriptor."""
     _on_gpu("grouped_mm", rows, weight, offsets, d_out)
     if weight.dim() != 3 or rows.dim() != 2 or rows.shape[1] != weight.shape[1]:
         raise ValueError("expected rows[R,K] and weight[E,K,N]")
@@ -230,18 +229,16 @@ def _grouped_plan(rows, weight, offsets, out_type, transposed, flags, key, d_out
         raise ValueError("expected offsets[E+1] in int32 or int64")
     if d_out is not None and d_out.shape != (R, N):
         raise ValueError("expected d_out[R,N]")
+    pad = (-K % 8, -N % 8)
+    if any(pad) and K and N:
+        return _grouped_plans.remember(key, (0, 0, pad, None))
     d = _abi.mm_grouped_desc(R, K, N, E, transposed, out_type, flags)
     at = ctypes.addressof(d)
     lib = _abi._lib()
     ws = int((lib.mm_grouped_mm_workspace_size if d_out is None else lib.mm_grouped_weight_grad_workspace_size)(at))
     if ws == 0:
         raise ValueError(f"unsupported sizes R={R} K={K} N={N} E={E}")
-    return _grouped_plans.remember(key, (at, ws, d))
-
-
-def _odd(weight):
-    """Zeros that bring K and N to multiples of 8."""
-    return (-weight.shape[1] % 8, -weight.shape[2] % 8) if weight.dim() == 3 else (0, 0)
+    return _grouped_plans.remember(key, (at, ws, None, d))
 
 
 def _widened(t, *pad):
@@ -256,18 +253,20 @@ def grouped_mm_forward(rows, weight, offsets, *, out_dtype=None, flags=0):
     if _elsewhere(rows):
         with torch.cuda.device(rows.device):
             return grouped_mm_forward(rows, weight, offsets, out_dtype=out_dtype, flags=flags)
-    pk, pn = _odd(weight)
-    if (pk or pn) and rows.dim() == 2 and rows.shape[1] == weight.shape[1]:
-        out = grouped_mm_forward(_widened(rows, 0, pk), _widened(weight, 0, pn, 0, pk), offsets,
+    transposed = _transposed(weight)
+    key = (_sig(rows), _sig(weight), _sig(offsets), out_dtype, transposed, flags)
+    plan = _grouped_plans.get(key)
+    if plan is None:
+        out_type = _type("out", torch.empty(0, dtype=out_dtype or torch.bfloat16))
+        plan = _grouped_plan(rows, weight, offsets, out_type, transposed, flags, key)
+    at, nbytes, pad, _ = plan
+    if pad is not None:
+        out = grouped_mm_forward(_widened(rows, 0, pad[0]), _widened(weight, 0, pad[1], 0, pad[0]), offsets,
                                  out_dtype=out_dtype, flags=flags)
         return out[:, :weight.shape[2]].contiguous()
-    transposed, kept = _layout(weight) if weight.dim() == 3 else (False, weight)
-    out_dtype = out_dtype or torch.bfloat16
-    key = (_sig(rows), _sig(weight), _sig(offsets), out_dtype, transposed, flags)
-    at, nbytes, _ = _grouped_plans.get(key) or _grouped_plan(
-        rows, weight, offsets, _type("out", torch.empty(0, dtype=out_dtype)), transposed, flags, key)
     rows, offsets = _aligned(rows), _index32(offsets, rows.shape[0])
-    out = torch.empty((rows.shape[0], weight.shape[2]), dtype=out_dtype, device=rows.device)
+    kept = _aligned(weight.transpose(1, 2) if transposed else weight)
+    out = torch.empty((rows.shape[0], weight.shape[2]), dtype=out_dtype or torch.bfloat16, device=rows.device)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=rows.device) if nbytes > 256 else None
     _abi.check(_abi._lib().mm_grouped_mm(
         at, rows.data_ptr(), kept.data_ptr(), offsets.data_ptr(), out.data_ptr(), _ptr(ws), nbytes,
@@ -288,31 +287,27 @@ def grouped_mm_weight_grad(rows, d_out, offsets, weight, *, dtype=None, into=Non
         if dtype is not None and dtype != into.dtype:
             raise TypeError("dtype is for results of their own: sums have the dtype of `into`")
         dtype = into.dtype
+        if not (into.is_contiguous() or _transposed(into)):
+            raise ValueError("`into` must be contiguous, or a transposed view of a contiguous tensor")
     dtype = dtype or torch.bfloat16
-    pk, pn = _odd(weight)
-    if (pk or pn) and rows.dim() == 2 and d_out.dim() == 2 and rows.shape[1] == weight.shape[1] \
-            and d_out.shape[1] == weight.shape[2]:
-        E, K, N = weight.shape
-        wide = weight.new_empty(1).expand(E, K + pk, N + pn)  # (its shape is all that counts)
-        got = grouped_mm_weight_grad(_widened(rows, 0, pk), _widened(d_out, 0, pn), offsets, wide,
+    transposed = _transposed(weight if into is None else into)
+    key = ("weight", _sig(rows), _sig(d_out), (weight.shape, weight.dtype), _sig(offsets), dtype, transposed, flags)
+    plan = _grouped_plans.get(key)
+    if plan is None:
+        out_type = _type("the weight gradient", torch.empty(0, dtype=dtype))
+        plan = _grouped_plan(rows, weight, offsets, out_type, transposed, flags, key, d_out)
+    at, nbytes, pad, _ = plan
+    E, K, N = weight.shape
+    if pad is not None:
+        wide = weight.new_empty(1).expand(E, K + pad[0], N + pad[1])  # (its shape is all that counts)
+        got = grouped_mm_weight_grad(_widened(rows, 0, pad[0]), _widened(d_out, 0, pad[1]), offsets, wide,
                                      dtype=torch.float32 if into is not None else dtype, flags=flags)
         got = got[:, :K, :N]
         if into is not None:
             return into.add_(got)
-        return got.contiguous()
-    if weight.dim() != 3:
-        raise ValueError("expected weight[E,K,N]")
-    E, K, N = weight.shape
-    like = weight if into is None else into
-    transposed = not like.is_contiguous() and like.transpose(1, 2).is_contiguous()
-    if into is not None and not (transposed or into.is_contiguous()):
-        raise ValueError("`into` must be contiguous, or a transposed view of a contiguous tensor")
+        return got.transpose(1, 2).contiguous().transpose(1, 2) if transposed else got.contiguous()
     if into is not None and into.data_ptr() % 16:
         raise ValueError("`into` must start on a 16-byte boundary")
-    key = ("weight", _sig(rows), _sig(d_out), (weight.shape, weight.dtype), _sig(offsets), dtype, transposed, flags)
-    at, nbytes, _ = _grouped_plans.get(key) or _grouped_plan(
-        rows, weight, offsets, _type("the weight gradient", torch.empty(0, dtype=dtype)), transposed,
-        flags, key, d_out)
     rows, d_out, offsets = _aligned(rows), _aligned(d_out), _index32(offsets, rows.shape[0])
     if into is not None:
         torch.autograd.graph.increment_version(into)

@@ -98,7 +98,8 @@ def test_weight_grad(sizes, K, N, form):
 def test_odd_widths(K, N):
     x, w, at, d = inputs([3, 0, 40, 1], K, N, transposed=True, behind=2)
     check_forward(x, w, at)
-    check_weight_grad(x, d, at, w, dtype=F32)
+    got = check_weight_grad(x, d, at, w, dtype=F32)
+    assert got.transpose(1, 2).is_contiguous()
     into = torch.ones(w.shape, device="cuda")
     expert_ops.grouped_mm_weight_grad(x, d, at, w, into=into)
     assert torch.allclose(into - 1, check_weight_grad(x, d, at, w, dtype=F32), atol=1e-5, rtol=1e-6)
