@@ -1078,11 +1078,12 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   clear_error();
   MM_TRY(bind_context());
   // Pairs read half as much of their operands per product. Where a launch has no more tiles of one CTA
-  // than SMs, these spread the matrices' columns over twice as many. (us a call, one CTA a tile and pairs:
-  // 8 rows of 8 of 128 experts, 2048 -> 1536, 13.1 and 14.1; 512 rows of 128, 768 -> 2048, 71.1 and 66.5;
-  // 131072 rows of 128, 2048 -> 1536, 590 and 543.)
+  // than SMs, these spread the matrices' columns over twice as many, and up to 128 columns leave a pair's
+  // second CTA nothing. (us a call, one CTA a tile and pairs: 8 rows of 8 of 128 experts, 2048 -> 1536, 13.1
+  // and 14.1; 512 rows of 128, 768 -> 2048, 71.1 and 66.5; 131072 rows of 128, 2048 -> 1536, 590 and 543;
+  // 27494 rows of 8, 2016 -> 128, 26.8 and 31.1, -> 264, 47.7 and 38.5.)
   const int64_t chunks = d->R / kMaxN + std::min<int64_t>(d->E, d->R);  // at most
-  const bool few = chunks * div_up(d->N, kTile) <= device_sm_count();
+  const bool few = d->N <= kTile || chunks * div_up(d->N, kTile) <= device_sm_count();
   const int pair = d->flags & MM_GROUPED_CTA_PAIRS || (!(d->flags & MM_GROUPED_SINGLE_CTA) && !few) ? 2 : 1;
   Maps m{};
   Args a{};

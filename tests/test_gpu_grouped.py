@@ -4,6 +4,8 @@ Tolerances: products of bf16 numbers are exact in 32 bits. An instruction of the
 them to the accumulator; the sum of its 17 numbers is off by at most 2^-22 of the sum of magnitudes so
 far (each number is cut at the 24 bits of the largest). Over a sum of n terms that is
 (n / 16 + 1) 2^-22 of the magnitudes' sum, and the result's rounding is half a step of its type."""
+import random
+
 import pytest
 import torch
 
@@ -354,3 +356,46 @@ def test_long_sums_of_32_bits_keep_their_bits():
         got = expert_ops.grouped_mm_weight_grad(x[:, :264], d, at, w[:, :264], dtype=F32, flags=form).double()
         ref = torch.stack([x[a:b, :264].double().t() @ d[a:b].double() for _, (a, b) in spans(at)])
         assert ((got - ref).norm() / ref.norm()) <= 2e-6
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sizes(seed):
+    rng = random.Random(seed)
+    E = rng.choice([1, 2, 3, 7, 16, 40, 200])
+    K, N = (8 * rng.randint(1, rng.choice([8, 40, 150])) for _ in range(2))
+    most = rng.choice([3, 40, 300, 1500]) if E < 40 else rng.choice([3, 40, 300])
+    sizes = [0 if rng.random() < 0.2 else rng.randint(0, most) for _ in range(E)]
+    if rng.random() < 0.3:
+        sizes[rng.randrange(E)] += 4000
+    before, behind = rng.choice([0, 0, 5]), rng.choice([0, 0, 1, 300])
+    if before + sum(sizes) + behind == 0:
+        behind = 1
+    x, w, at, d = inputs(sizes, K, N, rng.random() < 0.5, before, behind, seed)
+    form = rng.choice([SINGLE, PAIRS, 0])
+    for out in (BF, F32):
+        got = check_forward(x, w, at, out_dtype=out, flags=form)
+        assert (got[:before] == 0).all() and (got[before + sum(sizes):] == 0).all()
+        assert torch.equal(got, expert_ops.grouped_mm_forward(x, w, at, out_dtype=out))
+        got = check_weight_grad(x, d, at, w, dtype=out, flags=form)
+        assert torch.equal(got, expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=out))
+
+
+def test_offsets_past_32_bits():
+    """Results of more than 2^31 elements, and rows behind as many elements of inputs."""
+    R, K, N = 300_001, 8, 7200
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(R, K, generator=g, device="cuda").to(BF)
+    w = torch.randn(2, K, N, generator=g, device="cuda").to(BF)
+    at = torch.tensor([0, 5, R], dtype=torch.int32, device="cuda")
+    out = expert_ops.grouped_mm_forward(x, w, at)
+    pick = torch.tensor([0, 4, 5, 150_000, 298_262, 298_263, R - 2, R - 1], device="cuda")
+    ref = torch.stack([x[r].double() @ w[int(r >= 5)].double() for r in pick])
+    close(out[pick], ref, torch.full_like(ref, 8 * 16.0), K)
+    dx = expert_ops.grouped_mm_forward(out, w.transpose(1, 2), at)  # reads them again
+    ref = torch.stack([out[r].double() @ w[int(r >= 5)].double().t() for r in pick])
+    mag = torch.stack([out[r].double().abs() @ w[int(r >= 5)].double().abs().t() for r in pick])
+    close(dx[pick], ref, mag, N)
+    one = torch.zeros_like(x)
+    one[R - 1] = 1.0  # the last row alone
+    dw = expert_ops.grouped_mm_weight_grad(one, out, at, w)
+    assert torch.equal(dw[1], out[R - 1].expand(K, N)) and (dw[0] == 0).all()
