@@ -6,8 +6,13 @@
 // an expert give where its slots of that expert start, and within a block the warps' counts and the
 // lanes before a lane with the same expert the rest. Up to kSlots slots are one launch.
 //
-// Dispatch and combine move rows: a block has a token's row and its K slots' rows, so that each row is
-// read and written once.
+// The order is bound by latency: 512 slots of 128 experts 3.6 us, 131072 in two launches 10.5 us (a 2 MB
+// read and written).
+//
+// Dispatch and combine move rows and are bound by HBM: a block has a token's row and its K slots' rows, so
+// that each row is read and written once. 16384 x 8 rows of 2048 bf16 dispatched 91 us (6.6 TB/s), 4096 x 8
+// of 7168 combined 81 us (6.5 TB/s), the gradients of 8192 x 8 of 2048 88 us (6.5 TB/s). Rows off 16-byte
+// boundaries move element by element: the gradients of 1001 x 6 fp32 rows of 2047 20 us (4.9 TB/s).
 #include <algorithm>
 #include <type_traits>
 
