@@ -76,9 +76,9 @@ mm_status mm_expert_combine_backward(const mm_expert_desc* d, const void* dy, co
  *
  * rows bf16 [R, K], W bf16 [E, K, N] or, `transposed`, [E, N, K] (as a linear layer keeps it), offsets
  * int32 [E + 1]: rising, from 0 on, at most R. Rows in no expert's range (before the first, behind the
- * last) are not read; they are zero in `out`. The gradient of `rows` is mm_grouped_mm of d_out with K
- * and N exchanged and `transposed` negated. Offsets that fall, start below 0 or end above R make every
- * element of the output NaN; no row outside [0, R) is touched.
+ * last) have no part, whatever they hold; they are zero in `out`. The gradient of `rows` is
+ * mm_grouped_mm of d_out with K and N exchanged and `transposed` negated. Offsets that fall, start below
+ * 0 or end above R make every element of the output NaN; no row outside [0, R) is touched.
  * Sizes: 0 <= R < 2^30, 1 <= E <= 1024, K and N multiples of 8 up to 65536. rows, W, out, d_out and
  * d_weight 16-byte aligned. out_type (MM_BF16 or MM_FP32): of `out`, or of d_weight.
  * Device waits are bounded; what a wait that runs out (a failing device) leaves without a result is
