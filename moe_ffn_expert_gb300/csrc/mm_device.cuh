@@ -180,8 +180,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 }
 
 // Every thread of both CTAs of the cluster (release/acquire: shared-memory state, such as
-// initialised mbarriers, is visible to the peer afterwards).
+// initialised mbarriers, is visible to the peer afterwards). The lanes of a warp arrive together,
+// as the aligned form wants them, also where a branch of one lane stands before.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }

@@ -51,9 +51,10 @@ namespace {
 constexpr int kThreads = 384;      // warps that load, multiply and deal out tiles (and none), eight that store
 constexpr int kStoreWarps = 8, kFirstStore = 4;
 // Registers of a thread: the block is launched with 168 x 384, and the storing warps, which hold a tile's
-// 128 sums per thread, take over what the first four warps do not need (56 x 128 + 224 x 256 of them).
-constexpr int kFewRegs = 56, kManyRegs = 224;
-static_assert(kFewRegs * 32 * kFirstStore + kManyRegs * 32 * kStoreWarps <= 168 * kThreads, "register shares");
+// 128 sums per thread, take over what the first four warps do not need (56 x 128 + 224 x 256 of them). A
+// block launched with fewer would wait for them for ever, so the launch asks what the kernel was built with.
+constexpr int kLaunchRegs = 168, kFewRegs = 56, kManyRegs = 224;
+static_assert(kFewRegs * 32 * kFirstStore + kManyRegs * 32 * kStoreWarps <= kLaunchRegs * kThreads, "register shares");
 constexpr int kRun = 8;            // blocks of 64 terms
 constexpr int kQueue = 8;          // tiles told and not yet taken by all
 constexpr int kMaxE = 1024;
@@ -449,6 +450,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&m.a);
     if (WEIGHTS || a.chunk / PAIR > 64) tma_prefetch_desc(&m.b[0]);
   }
+  // Tensor memory is asked for, a wait without a limit, when nothing that it needs can be missing any more:
+  // the stream's kernels before have ended, so that none of them holds columns on this SM, and both CTAs
+  // of a pair, whose warps allocate together, have started.
+  pdl_wait();
+  if constexpr (PAIR == 2) cluster_sync();
   if (warp == 1) {
     if constexpr (PAIR == 2) {
       tmem_alloc_pair(smem_u32(&tmem_holder), 512);
@@ -459,7 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  pdl_wait();
   const bool good = build_table<WEIGHTS>(a, start, first_chunk, order);  // (a barrier for the block)
   tc_fence_after();
   if constexpr (PAIR == 2) cluster_sync();
@@ -999,6 +1004,12 @@ cudaError_t launch_form(const Maps& m, Args a, int64_t units, uint32_t flags, cu
     e = cudaFuncSetAttribute(k_grouped<PAIR, WEIGHTS, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kMostSmem - 1024));
     if (e != cudaSuccess) return e;
+    if constexpr (WIDE) {
+      cudaFuncAttributes built;
+      e = cudaFuncGetAttributes(&built, k_grouped<PAIR, WEIGHTS, WIDE>);
+      if (e != cudaSuccess) return e;
+      if (built.numRegs < kLaunchRegs) return cudaErrorLaunchOutOfResources;
+    }
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   int fit = std::max(1, device_sm_count());

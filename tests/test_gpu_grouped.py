@@ -399,3 +399,19 @@ def test_offsets_past_32_bits():
     one[R - 1] = 1.0  # the last row alone
     dw = expert_ops.grouped_mm_weight_grad(one, out, at, w)
     assert torch.equal(dw[1], out[R - 1].expand(K, N)) and (dw[0] == 0).all()
+
+
+def test_forms_and_types_in_turn_without_a_pause():
+    """Launches of one and of two CTAs a tile, of bf16 and 32-bit results, each of which takes tensor memory
+    that the one before has held: the same bits every time."""
+    x, w, at, d = inputs([300, 0, 65, 513], 264, 392, behind=3)
+    calls = [lambda how=how: (expert_ops.grouped_mm_forward(x, w, at, **how),
+                              expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=how["out_dtype"], flags=how["flags"]))
+             for how in (dict(out_dtype=dt, flags=form) for dt in (BF, F32) for form in (PAIRS, SINGLE, 0))]
+    want = [call() for call in calls]
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(120):
+        c = (5 * i + i // 6) % len(calls)
+        for got, ref in zip(calls[c](), want[c]):
+            wrong += (got != ref).sum()
+    assert int(wrong) == 0
