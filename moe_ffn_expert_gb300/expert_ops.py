@@ -83,8 +83,8 @@ def _row_plan(op, table, tokens, rows, weights, key):
     _on_gpu(op, first, tokens, rows, weights, table.offsets, table.row_of_slot)
     T, K, E = table.T, table.K, table.E
     for name, t, shape in (("offsets", table.offsets, (E + 1,)), ("row_of_slot", table.row_of_slot, (T, K))):
-        if t.shape != shape or t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"expected the table's {name} of shape {shape} in int32, contiguous")
+        if t.shape != shape or t.dtype != torch.int32:
+            raise ValueError(f"expected the table's {name} of shape {shape} in int32")
     if first.dim() != 2:
         raise ValueError("expected rows of shape [n,H]")
     H = first.shape[1]
@@ -106,11 +106,11 @@ def dispatch_forward(x, table):
             return dispatch_forward(x, table)
     key = ("dispatch", _sig(x), _sig(table.offsets), _sig(table.row_of_slot), table[3:])
     at, _ = _row_plans.get(key) or _row_plan("expert_dispatch", table, x, None, None, key)
-    x = _contiguous(x)
+    x, offsets, row_of_slot = _contiguous(x), _contiguous(table.offsets), _contiguous(table.row_of_slot)
     rows = torch.empty((table.T * table.K, x.shape[1]), dtype=x.dtype, device=x.device)
     _abi.check(_abi._lib().mm_expert_dispatch(
-        at, x.data_ptr(), table.offsets.data_ptr(), table.row_of_slot.data_ptr(), rows.data_ptr(),
-        _stream(x)), "mm_expert_dispatch")
+        at, x.data_ptr(), offsets.data_ptr(), row_of_slot.data_ptr(), rows.data_ptr(), _stream(x)),
+        "mm_expert_dispatch")
     return rows
 
 
@@ -122,10 +122,10 @@ def combine_forward(rows, table, weights=None):
             return combine_forward(rows, table, weights)
     key = ("combine", _sig(rows), _sig(weights), _sig(table.offsets), _sig(table.row_of_slot), table[3:])
     at, _ = _row_plans.get(key) or _row_plan("expert_combine", table, None, rows, weights, key)
-    rows, weights = _contiguous(rows), _contiguous(weights)
+    rows, weights, row_of_slot = _contiguous(rows), _contiguous(weights), _contiguous(table.row_of_slot)
     y = torch.empty((table.T, rows.shape[1]), dtype=rows.dtype, device=rows.device)
     _abi.check(_abi._lib().mm_expert_combine(
-        at, rows.data_ptr(), table.row_of_slot.data_ptr(), _ptr(weights), y.data_ptr(), _stream(rows)),
+        at, rows.data_ptr(), row_of_slot.data_ptr(), _ptr(weights), y.data_ptr(), _stream(rows)),
         "mm_expert_combine")
     return y
 
@@ -146,13 +146,14 @@ def combine_backward(dy, rows, table, weights=None, *, weight_grad=True):
             raise ValueError("the weights' gradient needs the rows")
         plan = _row_plan("expert_combine", table, dy, rows, weights, key)
     dy, rows, weights = _contiguous(dy), _contiguous(rows), _contiguous(weights)
+    offsets, row_of_slot = _contiguous(table.offsets), _contiguous(table.row_of_slot)
     d_rows = torch.empty((table.T * table.K, dy.shape[1]), dtype=dy.dtype, device=dy.device)
     d_weights = None
     if weight_grad:
         d_weights = torch.empty((table.T, table.K), dtype=torch.float32, device=dy.device)
     _abi.check(_abi._lib().mm_expert_combine_backward(
-        plan[0], dy.data_ptr(), _ptr(rows), table.offsets.data_ptr(), table.row_of_slot.data_ptr(),
-        _ptr(weights), d_rows.data_ptr(), _ptr(d_weights), _stream(dy)), "mm_expert_combine_backward")
+        plan[0], dy.data_ptr(), _ptr(rows), offsets.data_ptr(), row_of_slot.data_ptr(), _ptr(weights),
+        d_rows.data_ptr(), _ptr(d_weights), _stream(dy)), "mm_expert_combine_backward")
     return d_rows, d_weights
 
 

@@ -317,3 +317,25 @@ def test_refusals():
                  lambda: expert_ops.expert_combine(rows, table, table.row_of_slot)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_tables_of_any_strides():
+    """After a call with a contiguous table of the same shapes: strided and transposed copies of it give
+    the same results, an expanded one those of the numbers that it shows."""
+    T, K, H = 40, 4, 32
+    table, x, rows, w = rows_case(T, K, 8, H, BF)
+
+    def calls(t):
+        return (expert_ops.dispatch_forward(x, t), expert_ops.combine_forward(rows, t, w),
+                *expert_ops.combine_backward(x, rows, t, w))
+
+    want = calls(table)
+    two = lambda t: torch.stack([t, t + 1000], -1).flatten(-2)[..., ::2]
+    for other in (table._replace(row_of_slot=two(table.row_of_slot), offsets=two(table.offsets)),
+                  table._replace(row_of_slot=table.row_of_slot.t().contiguous().t())):
+        assert not other.row_of_slot.is_contiguous() and torch.equal(other.row_of_slot, table.row_of_slot)
+        for got, ref in zip(calls(other), want):
+            assert torch.equal(got, ref)
+    shown = table._replace(row_of_slot=table.row_of_slot[:1].expand(T, K))
+    assert torch.equal(expert_ops.combine_forward(rows, shown, w),
+                       expert_ops.combine_forward(rows, shown._replace(row_of_slot=shown.row_of_slot.contiguous()), w))
