@@ -98,7 +98,8 @@ typedef struct mm_grouped_desc {
 } mm_grouped_desc;
 
 /* Bytes of workspace (0: unsupported sizes). Need no initialisation; one call at a time may use them.
- * They depend on the current device's number of SMs. Where mm_grouped_mm's is 256, it uses none (NULL). */
+ * They depend on the current device's number of SMs. Where mm_grouped_mm's is 256, it uses none
+ * (NULL); where it uses some, it is more. */
 size_t mm_grouped_mm_workspace_size(const mm_grouped_desc* d);
 size_t mm_grouped_weight_grad_workspace_size(const mm_grouped_desc* d);
 

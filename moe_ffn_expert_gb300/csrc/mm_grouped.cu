@@ -1068,8 +1068,8 @@ int mm_experts_version(void) { return 1; }
 
 size_t mm_grouped_mm_workspace_size(const mm_grouped_desc* d) {
   if (check_desc(d) != MM_OK) return 0;
-  const RowParts p = row_parts(*d);
-  return p.parts == 1 ? 256 : std::max<size_t>(256, (size_t)p.parts * d->R * d->N * 4);
+  const RowParts p = row_parts(*d);  // (256 says that there are no slices)
+  return p.parts == 1 ? 256 : std::max<size_t>(512, (size_t)p.parts * d->R * d->N * 4);
 }
 
 size_t mm_grouped_weight_grad_workspace_size(const mm_grouped_desc* d) {

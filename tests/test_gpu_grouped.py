@@ -415,3 +415,33 @@ def test_forms_and_types_in_turn_without_a_pause():
         for got, ref in zip(calls[c](), want[c]):
             wrong += (got != ref).sum()
     assert int(wrong) == 0
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS, 0])
+@pytest.mark.parametrize("R,K,N", [(1, 2048, 8), (1, 2400, 8), (1, 2048, 1), (1, 7168, 8), (2, 4096, 8), (1, 2304, 16)])
+def test_sums_in_parts_of_few_results(R, K, N, form):
+    """Slices that are smaller than the smallest workspace there is otherwise (a token through an adapter of
+    rank 8), also as the gradient of the rows of an N -> K product."""
+    for transposed in (False, True):
+        for out in (BF, F32):
+            x, w, at, d = inputs([R], K, N, transposed)
+            check_forward(x, w, at, out_dtype=out, flags=form)
+    x, w, at, d = inputs([R], N, K)
+    dx, _ = expert_ops.grouped_mm_backward(d, x, w, at, flags=form)
+    assert torch.equal(dx, check_forward(d, w.transpose(1, 2), at, flags=form))
+
+
+def test_a_workspace_of_256_bytes_means_none():
+    """As the header says: for the library's own sizes, called as a C program calls it."""
+    import ctypes
+    lib = _abi._lib()
+    for R, K, N in ((1, 2048, 8), (1, 2400, 8), (1, 64, 8), (1, 4096, 72), (3, 2056, 264)):
+        x, w, at, _ = inputs([R], K, N)
+        d = _abi.mm_grouped_desc(R, K, N, 1, 0, 0, 0)
+        n = lib.mm_grouped_mm_workspace_size(ctypes.addressof(d))
+        ws = None if n == 256 else torch.empty(n, dtype=torch.uint8, device="cuda")
+        out = torch.empty(R, N, dtype=BF, device="cuda")
+        _abi.check(lib.mm_grouped_mm(ctypes.addressof(d), x.data_ptr(), w.data_ptr(), at.data_ptr(), out.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), n if ws is not None else 0,
+                                     torch.cuda.current_stream().cuda_stream), "mm_grouped_mm")
+        assert torch.equal(out, expert_ops.grouped_mm_forward(x, w, at))
