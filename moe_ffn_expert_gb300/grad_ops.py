@@ -136,6 +136,9 @@ def clip_grad_norm(tensors, max_norm, *, eps=1e-6, out=None):
         raise ValueError("`out` must have the tensors' shapes")
     given, late = dst, []
     if not all(map(_T.is_contiguous, src)) or (out is not None and not all(map(_T.is_contiguous, dst))):
+        froms = list(map(_T.data_ptr, src))  # (stand-ins have addresses of their own)
+        if not _apart(froms, froms if out is None else list(map(_T.data_ptr, dst))):
+            raise ValueError("a tensor is given twice")
         src, dst, late = _in_order(src, dst, out is None)
     norm = _call(src, dst, (max_norm, eps), device)
     if late:
