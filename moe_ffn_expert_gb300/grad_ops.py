@@ -33,6 +33,11 @@ def _dense(t):
     return t.permute(order).is_contiguous()
 
 
+def _repeats(t):
+    """Whether t is an expanded tensor, which cannot be written to."""
+    return t.numel() > 0 and any(n > 1 and step == 0 for n, step in zip(t.shape, t.stride()))
+
+
 def _apart(froms, tos):
     """No address twice among `tos`, and none of them another's of `froms` (empty tensors have none)."""
     once = set(tos)
@@ -111,7 +116,7 @@ def clip_grad_norm(tensors, max_norm, *, eps=1e-6, out=None):
     """Multiplies all tensors by min(1, max_norm / (norm + eps)), norm being grad_norm(tensors), which is
     returned. In place, or into the tensors `out` (of the same shapes, bfloat16 or float32, not
     overlapping `tensors`): for gradients that are accumulated in 32 bits and handed on in 16, or kept.
-    None entries are left out. A NaN in one tensor makes all of them NaN, an infinity makes finite
+    Expanded tensors cannot be scaled and are refused. None entries are left out. A NaN in one tensor makes all of them NaN, an infinity makes finite
     elements 0."""
     src = _list(tensors)
     dst = src if out is None else _list(out)
@@ -139,6 +144,8 @@ def clip_grad_norm(tensors, max_norm, *, eps=1e-6, out=None):
         froms = list(map(_T.data_ptr, src))  # (stand-ins have addresses of their own)
         if not _apart(froms, froms if out is None else list(map(_T.data_ptr, dst))):
             raise ValueError("a tensor is given twice")
+        if any(map(_repeats, dst)):
+            raise ValueError("a tensor to write shows one element at several places")
         src, dst, late = _in_order(src, dst, out is None)
     norm = _call(src, dst, (max_norm, eps), device)
     if late:

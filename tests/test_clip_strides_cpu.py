@@ -51,3 +51,16 @@ def test_a_tensor_given_twice(calls):
         with pytest.raises(ValueError, match="twice"):
             grad_ops.clip_grad_norm(src, 1.0, out=out)
     assert not calls
+
+
+def test_an_expanded_tensor_is_not_written_to(calls):
+    """Refused before the others are scaled."""
+    a, one = torch.ones(4, 5), torch.ones(5)
+    for src, out in (([a, one.expand(4, 5)], None), ([a, torch.ones(()).expand(7)], None), ([a], [one.expand(4, 5)]),
+                     ([a, torch.ones(4, 1).expand(4, 5)[:, 1:]], None)):
+        with pytest.raises(ValueError, match="several places"):
+            grad_ops.clip_grad_norm(src, 1.0, out=out)
+    assert not calls
+    grad_ops.clip_grad_norm([one.expand(4, 5)], 1.0, out=[a])  # read, it is a tensor as any other
+    grad_ops.clip_grad_norm([one[:0].expand(4, 0)], 1.0)
+    assert len(calls) == 2
