@@ -86,7 +86,7 @@ __device__ __forceinline__ void load_chunk(const T* p, int64_t base, int64_t cou
     } else {
       r[s] = Raw<T>{};
       if (at >= count) continue;
-      T one[8];
+      alignas(16) T one[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) one[i] = at + i < count ? p[at + i] : T(0.f);
       r[s] = *reinterpret_cast<const Raw<T>*>(one);
