@@ -82,7 +82,7 @@ mm_status mm_expert_combine_backward(const mm_expert_desc* d, const void* dy, co
  * Sizes: 0 <= R < 2^30, 1 <= E <= 1024, K and N multiples of 8 up to 65536. rows, W, out, d_out and
  * d_weight 16-byte aligned. out_type (MM_BF16 or MM_FP32): of `out`, or of d_weight.
  * Device waits are bounded; what a wait that runs out (a failing device) leaves without a result is
- * NaN. */
+ * NaN, and the caller's status word, if there is one, says so. */
 #define MM_GROUPED_SINGLE_CTA 0x1u /* flags: one CTA per tile */
 #define MM_GROUPED_CTA_PAIRS 0x2u  /* flags: tiles shared by two CTAs. Without either flag the form goes
                                       by the sizes; results are the same bit for bit. */
@@ -112,6 +112,19 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
 mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, const void* d_out,
                                     const int32_t* offsets, void* d_weight, int accumulate,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with a status: int32 [2] in device memory, zero before its first call and the caller's to read
+ * and to set back; any number of calls may share it (NULL: none). The first wait that runs out sets
+ * status[0] to MM_ERR_TIMEOUT and status[1] to what was awaited (1: a free stage for operands, 2: a free
+ * accumulator, 3: operands, 4: the next tile, 5: a free place for one, 6: a sum), plus 256 times the
+ * number of the CTA; later ones leave both. It costs nothing where no wait runs out. */
+mm_status mm_grouped_mm_ex(const mm_grouped_desc* d, const void* rows, const void* weight,
+                           const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* status, void* stream);
+mm_status mm_grouped_mm_weight_grad_ex(const mm_grouped_desc* d, const void* rows, const void* d_out,
+                                       const int32_t* offsets, void* d_weight, int accumulate,
+                                       void* workspace, size_t workspace_bytes, int32_t* status,
+                                       void* stream);
 
 /* ---- the norm of many tensors, and clipping -----------------------------------------------
  *

@@ -179,6 +179,8 @@ def _lib():
         "mm_grouped_weight_grad_workspace_size": (ctypes.c_size_t, [_P]),
         "mm_grouped_mm": (st, [_P] * 6 + [ctypes.c_size_t, _P]),
         "mm_grouped_mm_weight_grad": (st, [_P] * 5 + [ctypes.c_int, _P, ctypes.c_size_t, _P]),
+        "mm_grouped_mm_ex": (st, [_P] * 6 + [ctypes.c_size_t, _P, _P]),
+        "mm_grouped_mm_weight_grad_ex": (st, [_P] * 5 + [ctypes.c_int, _P, ctypes.c_size_t, _P, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -93,8 +93,12 @@ struct Args {
   int part_rows;  // weights: experts with more rows than this have parts of at most as many
   int* next;      // counter of claimed tiles, or null: every step-th
   uint64_t wait_ns;
+  int32_t* status;  // the caller's [2], or null
   int stall;      // test hook: CTA 0 withholds its first accumulator
 };
+
+// What a wait that ran out was for (numbers of mm_experts.h).
+enum Awaited { kFreeStage = 1, kFreeSum, kOperands, kTold, kTaken, kSum };
 
 // Rows that are loaded for n of a chunk: the next power of two from 8 on.
 __host__ __device__ constexpr uint32_t box_rows(int n) {
@@ -474,12 +478,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int j_tiles = WEIGHTS ? (a.J + a.chunk - 1) / a.chunk : 1;
   const int units = !good ? 0 : first_chunk[a.E] * i_tiles * (WEIGHTS ? j_tiles : a.parts);
 
+  // Records a wait that ran out, if it is the first. By a whole warp.
+  auto give_up = [&](Awaited what) {
+    if (a.status != nullptr && lane == 0 && atomicCAS(a.status, 0, MM_ERR_TIMEOUT) == 0)
+      a.status[1] = what | (int)blockIdx.x << 8;
+  };
+
   // Entry number q of the queue, once it is there; false if the wait ran out. A lane reads a word, so
   // that what frees the slot needs all words to have arrived: the odd CTA's arrival is then one without
   // a release, which would wait for a storing warp's rows to reach memory.
   auto take = [&](int q, Unit& t) {
     const uint32_t slot = q % kQueue, bar = told_bar(slot), phase = q / kQueue & 1u;
-    if (!warp_wait(bar, phase, limit)) return false;
+    if (!warp_wait(bar, phase, limit)) {
+      give_up(kTold);
+      return false;
+    }
     const int word = static_cast<volatile const int*>(&queue[slot].e)[lane & 7];
     t.e = __shfl_sync(0xFFFFFFFFu, word, 0);
     t.i0 = __shfl_sync(0xFFFFFFFFu, word, 1);
@@ -513,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = WEIGHTS ? uniform(t.k) - (blocks - 1) * 64 : 64;  // rows of the last block
         for (int kb = 0; kb < blocks; ++kb, ++it) {
           if (!ring.wait()) {
+            give_up(kFreeStage);
             ok = false;
             break;
           }
@@ -570,8 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // every stage's last release has landed before this CTA may leave
-      for (int s = 0; s < a.stages && s < it && ok; ++s)
+      for (int s = 0; s < a.stages && s < it && ok; ++s) {
         ok = warp_wait(empty_bar(s), (it - 1 - s) / a.stages & 1u, limit);
+        if (!ok) give_up(kFreeStage);
+      }
     } else if (warp == 1) {
       // ------------------------------------------------ multiplies
       // The warp stays in step and an elected lane of the even CTA issues, from uniform registers (by one
@@ -599,12 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             buf = acc & 1u;
             d = tmem + buf * kMaxN;
             if (!warp_wait(acce_bar(buf), (acc >> 1 & 1u) ^ 1u, limit)) {
+              give_up(kFreeSum);
               ok = false;
               break;
             }
             tc_fence_after();
           }
           if (!ring.wait()) {
+            give_up(kOperands);
             ok = false;
             break;
           }
@@ -645,7 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < units) t = unit_at<WEIGHTS, PAIR>(a, start, first_chunk, order, u, i_tiles, j_tiles);
         else t.n = -1;
         const uint32_t slot = q % kQueue;
-        if (!warp_wait(taken_bar(slot), (q / kQueue & 1u) ^ 1u, limit)) break;
+        if (!warp_wait(taken_bar(slot), (q / kQueue & 1u) ^ 1u, limit)) {
+          give_up(kTaken);
+          break;
+        }
         if (lane == 0) {
           queue[slot] = t;
           mbar_arrive(told_bar(slot));
@@ -685,6 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The accumulator of the next run, or false; and its hand-back, when it is in registers.
     auto arrived = [&]() {
       const bool ok = warp_wait(accf_bar(acc & 1u), acc >> 1 & 1u, limit);
+      if (!ok) give_up(kSum);
       tc_fence_after();
       return ok;
     };
@@ -1081,9 +1103,16 @@ size_t mm_grouped_weight_grad_workspace_size(const mm_grouped_desc* d) {
 mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* weight,
                         const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
                         void* stream) {
+  return mm_grouped_mm_ex(d, rows, weight, offsets, out, workspace, workspace_bytes, nullptr, stream);
+}
+
+mm_status mm_grouped_mm_ex(const mm_grouped_desc* d, const void* rows, const void* weight,
+                           const int32_t* offsets, void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* status, void* stream) {
   mm_status s = check_desc(d);
   if (s != MM_OK) return s;
-  if (!aligned_to(rows, 16) || !aligned_to(weight, 16) || !aligned_to(out, 16) || !aligned_to(offsets, 4))
+  if (!aligned_to(rows, 16) || !aligned_to(weight, 16) || !aligned_to(out, 16) || !aligned_to(offsets, 4) ||
+      !aligned_to(status, 4))
     return MM_ERR_INVALID_ARG;
   if (d->R == 0) return MM_OK;
   if (!rows || !weight || !out || !offsets) return MM_ERR_INVALID_ARG;
@@ -1104,6 +1133,7 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
   Maps m{};
   Args a{};
   a.offsets = offsets;
+  a.status = status;
   a.out = out;
   a.R = (int)d->R;
   a.E = d->E;
@@ -1140,9 +1170,18 @@ mm_status mm_grouped_mm(const mm_grouped_desc* d, const void* rows, const void* 
 mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, const void* d_out,
                                     const int32_t* offsets, void* d_weight, int accumulate,
                                     void* workspace, size_t workspace_bytes, void* stream) {
+  return mm_grouped_mm_weight_grad_ex(d, rows, d_out, offsets, d_weight, accumulate, workspace, workspace_bytes,
+                                      nullptr, stream);
+}
+
+mm_status mm_grouped_mm_weight_grad_ex(const mm_grouped_desc* d, const void* rows, const void* d_out,
+                                       const int32_t* offsets, void* d_weight, int accumulate,
+                                       void* workspace, size_t workspace_bytes, int32_t* status,
+                                       void* stream) {
   mm_status s = check_desc(d);
   if (s != MM_OK) return s;
-  if (!aligned_to(rows, 16) || !aligned_to(d_out, 16) || !aligned_to(d_weight, 16) || !aligned_to(offsets, 4))
+  if (!aligned_to(rows, 16) || !aligned_to(d_out, 16) || !aligned_to(d_weight, 16) || !aligned_to(offsets, 4) ||
+      !aligned_to(status, 4))
     return MM_ERR_INVALID_ARG;
   if (!d_weight || !offsets || (d->R > 0 && (!rows || !d_out))) return MM_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned_to(workspace, 256) ||
@@ -1161,6 +1200,7 @@ mm_status mm_grouped_mm_weight_grad(const mm_grouped_desc* d, const void* rows, 
   Maps m;
   Args a{};
   a.offsets = offsets;
+  a.status = status;
   a.out = d_weight;
   a.R = (int)d->R;
   a.E = d->E;

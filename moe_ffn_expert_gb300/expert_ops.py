@@ -242,18 +242,44 @@ def _grouped_plan(rows, weight, offsets, out_type, transposed, flags, key, d_out
     return _grouped_plans.remember(key, (at, ws, None, d))
 
 
+def grouped_status(device="cuda"):
+    """A status for the calls of grouped_mm, which may share it: what check_grouped_status looks at."""
+    return torch.zeros(2, dtype=torch.int32, device=device)
+
+
+#: what a wait that ran out was for
+_AWAITED = {1: "a free stage for operands", 2: "a free accumulator", 3: "operands", 4: "the next tile",
+            5: "a free place for a tile", 6: "a sum"}
+
+
+def check_grouped_status(status):
+    """Waits for the calls that were given `status`, and raises MMError (MM_ERR_TIMEOUT) if a wait in one of
+    them ran out: that call's result is NaN where it is missing, and the device is not to be trusted."""
+    code, where = status.tolist()
+    _abi.check(code, f"grouped_mm, CTA {where >> 8} awaiting {_AWAITED.get(where & 255, where & 255)}")
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    if status.shape != (2,) or status.dtype != torch.int32 or not status.is_contiguous() or status.device != device:
+        raise ValueError(f"expected status[2] in int32 on {device}, contiguous")
+    return status.data_ptr()
+
+
 def _widened(t, *pad):
     return torch.nn.functional.pad(t, pad) if any(pad) else t
 
 
-def grouped_mm_forward(rows, weight, offsets, *, out_dtype=None, flags=0):
+def grouped_mm_forward(rows, weight, offsets, *, out_dtype=None, flags=0, status=None):
     """out [R,N]: out[r] = rows[r] @ weight[e] for offsets[e] <= r < offsets[e+1], zero rows elsewhere.
     rows [R,K] and weight [E,K,N] bf16 (a transposed view of contiguous [E,N,K] is read as it is),
     offsets [E+1] rising from 0 on; offsets that do not rise or end above R make `out` NaN. out_dtype:
-    bfloat16 (None) or float32. K and N in multiples of 8 are read in place; others cost padded copies."""
+    bfloat16 (None) or float32. K and N in multiples of 8 are read in place; others cost padded copies.
+    status: a grouped_status, which a wait that runs out on the device sets (its results are NaN)."""
     if _elsewhere(rows):
         with torch.cuda.device(rows.device):
-            return grouped_mm_forward(rows, weight, offsets, out_dtype=out_dtype, flags=flags)
+            return grouped_mm_forward(rows, weight, offsets, out_dtype=out_dtype, flags=flags, status=status)
     transposed = _transposed(weight)
     key = (_sig(rows), _sig(weight), _sig(offsets), out_dtype, transposed, flags)
     plan = _grouped_plans.get(key)
@@ -263,25 +289,26 @@ def grouped_mm_forward(rows, weight, offsets, *, out_dtype=None, flags=0):
     at, nbytes, pad, _ = plan
     if pad is not None:
         out = grouped_mm_forward(_widened(rows, 0, pad[0]), _widened(weight, 0, pad[1], 0, pad[0]), offsets,
-                                 out_dtype=out_dtype, flags=flags)
+                                 out_dtype=out_dtype, flags=flags, status=status)
         return out[:, :weight.shape[2]].contiguous()
     rows, offsets = _aligned(rows), _index32(offsets, rows.shape[0])
     kept = _aligned(weight.transpose(1, 2) if transposed else weight)
     out = torch.empty((rows.shape[0], weight.shape[2]), dtype=out_dtype or torch.bfloat16, device=rows.device)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=rows.device) if nbytes > 256 else None
-    _abi.check(_abi._lib().mm_grouped_mm(
+    _abi.check(_abi._lib().mm_grouped_mm_ex(
         at, rows.data_ptr(), kept.data_ptr(), offsets.data_ptr(), out.data_ptr(), _ptr(ws), nbytes,
-        _stream(rows)), "mm_grouped_mm")
+        _status_ptr(status, rows.device), _stream(rows)), "mm_grouped_mm")
     return out
 
 
-def grouped_mm_weight_grad(rows, d_out, offsets, weight, *, dtype=None, into=None, flags=0):
+def grouped_mm_weight_grad(rows, d_out, offsets, weight, *, dtype=None, into=None, flags=0, status=None):
     """d_weight [E,K,N], d_weight[e] = rows_e^T d_out_e, laid out as `weight` (of which only shape and
     layout count), bfloat16 (None) or float32. `into`: such a tensor that the sums are added to instead
-    (gradients accumulated over micro-batches)."""
+    (gradients accumulated over micro-batches). status: as in grouped_mm_forward."""
     if _elsewhere(rows):
         with torch.cuda.device(rows.device):
-            return grouped_mm_weight_grad(rows, d_out, offsets, weight, dtype=dtype, into=into, flags=flags)
+            return grouped_mm_weight_grad(rows, d_out, offsets, weight, dtype=dtype, into=into, flags=flags,
+                                          status=status)
     if into is not None:
         if into.shape != weight.shape or into.device != rows.device:
             raise ValueError("expected `into` of the weight's shape on its device")
@@ -302,13 +329,14 @@ def grouped_mm_weight_grad(rows, d_out, offsets, weight, *, dtype=None, into=Non
     if pad is not None:
         wide = weight.new_empty(1).expand(E, K + pad[0], N + pad[1])  # (its shape is all that counts)
         got = grouped_mm_weight_grad(_widened(rows, 0, pad[0]), _widened(d_out, 0, pad[1]), offsets, wide,
-                                     dtype=torch.float32 if into is not None else dtype, flags=flags)
+                                     dtype=torch.float32 if into is not None else dtype, flags=flags, status=status)
         got = got[:, :K, :N]
         if into is not None:
             return into.add_(got)
         return got.transpose(1, 2).contiguous().transpose(1, 2) if transposed else got.contiguous()
     if into is not None and into.data_ptr() % 16:
         raise ValueError("`into` must start on a 16-byte boundary")
+    sign = _status_ptr(status, rows.device)
     rows, d_out, offsets = _aligned(rows), _aligned(d_out), _index32(offsets, rows.shape[0])
     if into is not None:
         torch.autograd.graph.increment_version(into)
@@ -316,25 +344,27 @@ def grouped_mm_weight_grad(rows, d_out, offsets, weight, *, dtype=None, into=Non
     else:
         out = torch.empty((E, N, K) if transposed else (E, K, N), dtype=dtype, device=rows.device)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=rows.device)
-    _abi.check(_abi._lib().mm_grouped_mm_weight_grad(
+    _abi.check(_abi._lib().mm_grouped_mm_weight_grad_ex(
         at, rows.data_ptr(), d_out.data_ptr(), offsets.data_ptr(), out.data_ptr(), into is not None,
-        ws.data_ptr(), nbytes, _stream(rows)), "mm_grouped_mm_weight_grad")
+        ws.data_ptr(), nbytes, sign, _stream(rows)), "mm_grouped_mm_weight_grad")
     return out.transpose(1, 2) if transposed else out
 
 
-def grouped_mm_backward(d_out, rows, weight, offsets, *, weight_grad_dtype=None, weight_grad=None, flags=0):
+def grouped_mm_backward(d_out, rows, weight, offsets, *, weight_grad_dtype=None, weight_grad=None, flags=0,
+                        status=None):
     """(d_rows bf16 [R,K], d_weight [E,K,N]) for d_out bf16 [R,N]. weight_grad_dtype: bfloat16 (None) or
     float32; weight_grad: a tensor that the weight's gradient is added to instead."""
-    d_rows = grouped_mm_forward(d_out, weight.transpose(1, 2), offsets, flags=flags)
+    d_rows = grouped_mm_forward(d_out, weight.transpose(1, 2), offsets, flags=flags, status=status)
     return d_rows, grouped_mm_weight_grad(rows, d_out, offsets, weight, dtype=weight_grad_dtype,
-                                          into=weight_grad, flags=flags)
+                                          into=weight_grad, flags=flags, status=status)
 
 
 class GroupedMMFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rows, weight, offsets, out_dtype):
+    def forward(ctx, rows, weight, offsets, out_dtype, status=None):
         ctx.save_for_backward(rows, weight, offsets)
-        return grouped_mm_forward(rows, weight, offsets, out_dtype=out_dtype)
+        ctx.status = status
+        return grouped_mm_forward(rows, weight, offsets, out_dtype=out_dtype, status=status)
 
     @staticmethod
     def backward(ctx, d_out):
@@ -342,13 +372,13 @@ class GroupedMMFunction(torch.autograd.Function):
         d = d_out.to(torch.bfloat16)
         d_rows = d_weight = None
         if ctx.needs_input_grad[0]:
-            d_rows = grouped_mm_forward(d, weight.transpose(1, 2), offsets)
+            d_rows = grouped_mm_forward(d, weight.transpose(1, 2), offsets, status=ctx.status)
         if ctx.needs_input_grad[1]:
-            d_weight = grouped_mm_weight_grad(rows, d, offsets, weight)
-        return (*first_order_only("grouped_mm", (d_rows, d_weight), (rows, weight, d_out)), None, None)
+            d_weight = grouped_mm_weight_grad(rows, d, offsets, weight, status=ctx.status)
+        return (*first_order_only("grouped_mm", (d_rows, d_weight), (rows, weight, d_out)), None, None, None)
 
 
-def grouped_mm(rows, weight, offsets, *, out_dtype=None):
+def grouped_mm(rows, weight, offsets, *, out_dtype=None, status=None):
     """grouped_mm_forward with gradients for rows and weight (of a float32 result rounded to bfloat16
-    first: the products take no wider ones)."""
-    return GroupedMMFunction.apply(rows, weight, offsets, out_dtype)
+    first: the products take no wider ones). status: of both directions."""
+    return GroupedMMFunction.apply(rows, weight, offsets, out_dtype, status)

@@ -161,3 +161,13 @@ def test_grad_host_checks():
     assert clip(good, eps=float("inf")) == BAD
     assert lib.mm_grad_workspace_size(-1) == lib.mm_grad_workspace_size(2 ** 20) == 0
     assert lib.mm_grad_workspace_size(0) >= 256
+
+
+def test_grouped_status_host_checks():
+    lib = _abi._lib()
+    d, full = grouped(), (16, 16, 16, 16)
+    for status in (2, 18):
+        assert lib.mm_grouped_mm_ex(ref(d), *full, 256, 1 << 40, status, None) == BAD
+        assert lib.mm_grouped_mm_weight_grad_ex(ref(d), *full, 0, 256, 1 << 40, status, None) == BAD
+    assert lib.mm_grouped_mm_ex(ref(grouped(R=0)), *[None] * 4, None, 0, 64, None) == _abi.MM_OK
+    assert lib.mm_grouped_mm_weight_grad_ex(ref(d), *full, 0, None, 1 << 40, 64, None) == WS

@@ -445,3 +445,67 @@ def test_a_workspace_of_256_bytes_means_none():
                                      None if ws is None else ws.data_ptr(), n if ws is not None else 0,
                                      torch.cuda.current_stream().cuda_stream), "mm_grouped_mm")
         assert torch.equal(out, expert_ops.grouped_mm_forward(x, w, at))
+
+
+STALL = _abi.MM_GROUPED_TEST_STALL
+
+
+def stalled_calls():
+    x, w, at, d = inputs([300, 5, 70], 136, 264)
+    long = inputs([2], 4104, 264)
+    into = lambda dt: torch.zeros(w.shape, dtype=dt, device="cuda")
+    return {"rows": lambda dt, **how: expert_ops.grouped_mm_forward(x, w, at, out_dtype=dt, **how),
+            "parts": lambda dt, **how: expert_ops.grouped_mm_forward(*long[:3], out_dtype=dt, **how),
+            "weights": lambda dt, **how: expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=dt, **how),
+            "into": lambda dt, **how: expert_ops.grouped_mm_weight_grad(x, d, at, w, into=into(dt), **how)}
+
+
+@pytest.mark.parametrize("form", [SINGLE, PAIRS])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("name", ["rows", "parts", "weights", "into"])
+def test_a_wait_that_runs_out_is_told(name, dt, form):
+    call = stalled_calls()[name]
+    status = expert_ops.grouped_status()
+    good = call(dt, flags=form, status=status)
+    expert_ops.check_grouped_status(status)
+    got = call(dt, flags=form | STALL, status=status)
+    with pytest.raises(_abi.MMError, match="MM_ERR_TIMEOUT") as error:
+        expert_ops.check_grouped_status(status)
+    assert error.value.status == _abi.MM_ERR_TIMEOUT
+    code, where = status.tolist()
+    assert where >> 8 in (0, 1) and 1 <= where & 255 <= 6  # (the first CTA's, or its pair's other one)
+    assert got.isnan().any() and torch.equal(torch.where(got.isnan(), good, got), good)
+    assert torch.equal(call(dt, flags=form, status=status), good)  # the next call is none the worse,
+    assert status.tolist() == [code, where]                       # and what happened stays told
+    status.zero_()
+    call(dt, flags=form, status=status)
+    expert_ops.check_grouped_status(status)
+
+
+def test_a_loop_ends_at_the_first_wait_that_ran_out():
+    call, status, done = stalled_calls()["weights"], expert_ops.grouped_status(), 0
+    with pytest.raises(_abi.MMError):
+        for i in range(10):
+            call(F32, flags=STALL if i == 3 else 0, status=status)
+            expert_ops.check_grouped_status(status)
+            done += 1
+    assert done == 3
+
+
+def test_a_status_of_all_calls_together():
+    x, w, at, d = inputs([50, 0, 33], 72, 136, transposed=True, behind=4)
+    status = expert_ops.grouped_status()
+    want = expert_ops.grouped_mm_backward(d, x, w, at)
+    x.requires_grad_(True)
+    w = w.detach().requires_grad_(True)
+    expert_ops.grouped_mm(x, w, at, status=status).backward(d)
+    assert torch.equal(x.grad, want[0]) and torch.equal(w.grad, want[1])
+    x, w, at, d = inputs([3, 0, 40, 1], 33, 70)  # padded
+    for a, b in zip(expert_ops.grouped_mm_backward(d, x, w, at, status=status), expert_ops.grouped_mm_backward(d, x, w, at)):
+        assert torch.equal(a, b)
+    expert_ops.check_grouped_status(status)
+    for bad in (status[:1], status.long(), status.cpu(), torch.zeros(4, dtype=torch.int32, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="status"):
+            expert_ops.grouped_mm_forward(x, w, at, status=bad)
+        with pytest.raises(ValueError, match="status"):
+            expert_ops.grouped_mm_weight_grad(x, d, at, w, status=bad)
