@@ -334,8 +334,9 @@ def grouped_mm_weight_grad(rows, d_out, offsets, weight, *, dtype=None, into=Non
         if into is not None:
             return into.add_(got)
         return got.transpose(1, 2).contiguous().transpose(1, 2) if transposed else got.contiguous()
-    if into is not None and into.data_ptr() % 16:
-        raise ValueError("`into` must start on a 16-byte boundary")
+    if into is not None and into.data_ptr() % 16:  # TMA and 16-byte stores want other memory
+        return into.add_(grouped_mm_weight_grad(rows, d_out, offsets, weight, dtype=torch.float32, flags=flags,
+                                                status=status))
     sign = _status_ptr(status, rows.device)
     rows, d_out, offsets = _aligned(rows), _aligned(d_out), _index32(offsets, rows.shape[0])
     if into is not None:

@@ -509,3 +509,20 @@ def test_a_status_of_all_calls_together():
             expert_ops.grouped_mm_forward(x, w, at, status=bad)
         with pytest.raises(ValueError, match="status"):
             expert_ops.grouped_mm_weight_grad(x, d, at, w, status=bad)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("K,N", [(136, 72), (33, 70)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_sums_into_a_kept_gradient_off_a_16_byte_boundary(transposed, K, N, dt):
+    """Of any widths; what lies around it stays as it was."""
+    x, w, at, d = inputs([70, 0, 9], K, N, transposed)
+    own = expert_ops.grouped_mm_weight_grad(x, d, at, w, dtype=F32)
+    for start in (1, 3):
+        flat = torch.full((start + w.numel() + 5,), 0.5, dtype=dt, device="cuda")
+        into = flat[start:start + w.numel()].view(3, *((N, K) if transposed else (K, N)))
+        into = into.transpose(1, 2) if transposed else into
+        got = expert_ops.grouped_mm_weight_grad(x, d, at, w, into=into)
+        assert into.data_ptr() % 16 and got.data_ptr() == into.data_ptr()
+        assert torch.equal(into, (0.5 + own).to(dt))
+        assert (flat[:start] == 0.5).all() and (flat[-5:] == 0.5).all()
