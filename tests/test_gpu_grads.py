@@ -183,3 +183,25 @@ def test_refusals():
         with pytest.raises(TypeError):
             call()
     assert torch.equal(a, torch.ones(10, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("to", [None, BF, F32])
+def test_what_lies_around_the_tensors_stays_as_it_was(dt, to):
+    """Views of one buffer at any place, elements between them and behind the last."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    flat = torch.randn(60000, generator=g, device="cuda").to(dt)
+    given, at, inside = flat.clone(), 1, torch.zeros(60000, dtype=torch.bool, device="cuda")
+    places = []
+    for i, n in enumerate([1, 2, 7, 8, 9, 1003, 16383, 16385, 3, 20000, 5]):
+        places.append((at, at + n))
+        inside[at:at + n] = True
+        at += n + 1 + i % 3
+    target = flat if to is None else torch.full((60000,), 7.0, dtype=to, device="cuda")
+    rest = target[~inside].clone()
+    cut = lambda t: [t[a:b] for a, b in places]
+    norm = norm64(cut(given))
+    grad_ops.clip_grad_norm(cut(flat), 0.5 * norm, out=None if to is None else cut(target))
+    check_scaled(cut(target), cut(given), norm, 0.5 * norm)
+    assert torch.equal(target[~inside], rest)
+    assert to is None or torch.equal(flat, given)
