@@ -12,7 +12,8 @@
 // Dispatch and combine move rows and are bound by HBM: a block has a token's row and its K slots' rows, so
 // that each row is read and written once. 16384 x 8 rows of 2048 bf16 dispatched 91 us (6.6 TB/s), 4096 x 8
 // of 7168 combined 81 us (6.5 TB/s), the gradients of 8192 x 8 of 2048 88 us (6.5 TB/s). Rows off 16-byte
-// boundaries move element by element: the gradients of 1001 x 6 fp32 rows of 2047 20 us (4.9 TB/s).
+// boundaries are loaded and stored element by element: the gradients of 1001 x 6 fp32 rows of 2047 20 us (4.9
+// TB/s), of bf16 rows 18 us (2.9). Aligned words shifted by a row's offset are not built.
 #include <algorithm>
 #include <type_traits>
 

@@ -8,7 +8,9 @@
 // holds them by itself.
 //
 // A chunk is 32 KB of one tensor; a block has a run of chunks, and the second launch walks the
-// runs backwards, from what the first has read last and L2 still holds. A thread's squares are summed in
+// runs backwards, from what the first has read last. (L2 gives nothing back all the same: the first pass
+// reads with streaming loads, and the second runs at the rate of a copy.) k_squares has 64 registers, for
+// four blocks per SM, and spills 36 bytes for it. A thread's squares are summed in
 // 32 bits over 64 elements (bf16; fp32: 32), then in 64 bits. Where those 32 bits would overflow or lose what is small (a
 // sum of 2^126 or more, or below 2^-80 but not of zeros alone) the squares are summed in 64 bits instead.
 #include <algorithm>
