@@ -374,9 +374,11 @@ __device__ __forceinline__ void load_bf16(uint32_t taddr, uint32_t (&p)[16]) {
     }
 }
 
-// Whether all four warps of a set say so.
+// Whether all four warps of a set say so. (Barriers, tensor-memory loads and setmaxnreg in their aligned forms
+// want the lanes of a warp together: each stands behind a __syncwarp or a vote.)
 __device__ __forceinline__ bool agreed(bool ok, int set) {
   uint32_t all;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -396,7 +398,10 @@ __device__ __forceinline__ bool agreed(bool ok, int set) {
 // different banks. i: the CTA's first column.
 __device__ __forceinline__ void store_bf16(const Args& a, const uint32_t (&p)[16], uint32_t stage, int set,
                                            int quarter, int64_t row, int i, int n, int lane) {
-  const auto sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory"); };
+  const auto sync = [&] {
+    __syncwarp();
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory");
+  };
   sync();  // all have read what was here
   const int jw = lane & 7;
   const uint32_t to = stage + jw * 256 + (((quarter * 4 + (lane >> 3)) ^ jw) << 4);
@@ -519,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  __syncwarp();
   if (warp < kFirstStore) {
     if constexpr (WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 0) {
@@ -779,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = agreed(ok, set);  // (the warps of a set meet at barriers)
         if (ok) {
           for (int c = set * 32; c < t.n; c += 64) {
+            __syncwarp();
             if (t.slice) {
               uint32_t r[32];
               tmem_ld_32x32(lanes + (acc & 1u) * kMaxN + c, r);

@@ -253,8 +253,8 @@ _AWAITED = {1: "a free stage for operands", 2: "a free accumulator", 3: "operand
 
 
 def check_grouped_status(status):
-    """Waits for the calls that were given `status`, and raises MMError (MM_ERR_TIMEOUT) if a wait in one of
-    them ran out: that call's result is NaN where it is missing, and the device is not to be trusted."""
+    """Waits for the current stream, and raises MMError (MM_ERR_TIMEOUT) if a wait in a call that was given
+    `status` ran out: that call's result is NaN where it is missing, and the device is not to be trusted."""
     code, where = status.tolist()
     _abi.check(code, f"grouped_mm, CTA {where >> 8} awaiting {_AWAITED.get(where & 255, where & 255)}")
 

@@ -35,3 +35,20 @@ def test_tensor_memory_of_a_pair_is_allocated_behind_what_it_waits_for(name, bod
     before = body[:body.index("tmem_alloc_pair(")]
     assert "pdl_wait();" in before and "cluster_sync();" in before
     assert before.index("pdl_wait();") < before.rindex("cluster_sync();")
+
+
+ALIGNED = r"bar\.sync|bar\.red|barrier\.cluster|setmaxnreg"
+TOGETHER = r"__syncwarp\(\)|__syncthreads\w*\(|_sync\(0x"
+
+
+def test_aligned_barriers_of_the_grouped_products_find_their_warps_together():
+    """A barrier in its aligned form counts a warp whose lanes come apart twice: in front of each stands, in
+    the same few lines, what brings them together."""
+    for name in ("mm_grouped.cu", "mm_device.cuh"):
+        lines = re.sub(r"//[^\n]*", "", open(os.path.join(mm_build.CSRC, name)).read()).split("\n")
+        found = [i for i, line in enumerate(lines) if re.search(ALIGNED, line)]
+        assert found
+        for i in found:
+            if "setmaxnreg.inc" in lines[i]:  # the other branch of the same decision
+                continue
+            assert re.search(TOGETHER, "\n".join(lines[max(0, i - 6):i])), (name, lines[i])
